@@ -2,7 +2,9 @@
  * sel.h -- C ABI of the GB300 (sm_103a) decode-step token-selection library.
  *
  * Four operations over batched fp32 logits rows of a vocabulary of V entries:
- * argmax, exact top-k, filtered sampling and speculative acceptance. Every
+ * argmax, exact top-k, filtered sampling and speculative acceptance; and the
+ * operators around them (4-bit output head, sampling of 16-bit rows with a
+ * policy per row, embedding of the drawn ids), declared at the end. Every
  * entry point takes device pointers, sizes, the policy parameters, a
  * caller-owned workspace and a cudaStream_t, validates its arguments on the
  * host, enqueues its kernels on that stream and returns. It never allocates,
@@ -655,6 +657,106 @@ sel_status spec_shard_draw(const float *d_target, const float *d_draft,
                            const spec_shard_plan *d_plan,
                            const double *d_masses, uint32_t *d_emitted,
                            void *d_ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * Around selection: the 4-bit output head that makes the logits rows, sampling
+ * of 16-bit rows with a policy for each row, and the embedding of the drawn
+ * ids. Together they carry a decode step from hidden states to the next
+ * step's input vectors on one stream. These calls need no workspace, so
+ * calls on different streams, and captured graphs, share nothing. Their
+ * inputs and outputs must not overlap.
+ */
+
+/* Element types. */
+typedef enum sel_dtype { SEL_F32 = 0, SEL_F16 = 1, SEL_BF16 = 2 } sel_dtype;
+
+#define SEL_MAX_H (1u << 20)          /* widest hidden state */
+#define SEL_MAX_LD (1ull << 40)       /* largest row stride, in elements */
+#define SEL_SAMPLE16_MAX_V 524208u    /* widest row of sel_sample16 */
+
+/*
+ * 4-bit matrices. Row v of a [V][H] matrix is H / 2 bytes: byte i holds column
+ * 2 i in its low nibble and column 2 i + 1 in its high one. Every `group`
+ * (32, 64 or 128; H a multiple of it) columns of a row share a scale s, of
+ * the hidden states' type, and a zero point z, a byte (any value; 8 for
+ * every group when the array is NULL). The entry is s * (q - z).
+ *
+ * sel_head_w4 -- logits[r][v] = sum over columns k of
+ * hidden[r][k] * s[v][k / group] * (q[v][k] - z[v][k / group]).
+ * Products are exact, a group is summed in fp32, its scale is applied in
+ * fp32 and each logit is rounded once to its type (f32 for the fp32 calls of
+ * this library, f16 or bf16 for sel_sample16). A nonfinite hidden state or
+ * scale gives nonfinite logits, which the selection calls fail closed.
+ *
+ *   d_hidden     [rows][H] of `dtype`, 16-byte aligned
+ *   d_q          [V][H / 2] bytes, 16-byte aligned
+ *   d_scales     [V][H / group] of `dtype`
+ *   d_zeros      [V][H / group] bytes, or NULL
+ *   dtype        SEL_F16 or SEL_BF16
+ *   d_logits     [rows] rows of V of `logits_dtype`, row r at r * ld
+ *   ld           elements between rows of d_logits, >= V; what lies between
+ *                the rows is left as it was
+ * The whole matrix is read once for every 64 rows.
+ */
+sel_status sel_head_w4(const void *d_hidden, uint32_t rows, const uint8_t *d_q,
+                       const void *d_scales, const uint8_t *d_zeros,
+                       uint32_t group, int dtype, uint32_t V, uint32_t H,
+                       void *d_logits, int logits_dtype, uint64_t ld,
+                       cudaStream_t stream);
+
+/*
+ * sel_sample16 -- sel_sample's chain (temperature, top-k, top-p, min-p, then
+ * the inverse-CDF draw) on f16 or bf16 rows, with a policy of its own for
+ * every row. Ids are ordered by (logit desc, id asc), -0 equal to +0; top-k
+ * keeps the first top_k, top-p the shortest prefix whose mass reaches
+ * top_p of the kept mass (the crossing token included), min-p the ids whose
+ * weight exp((x - max) / T) is at least min_p; the draw is the first
+ * survivor in that order whose cumulative mass exceeds u times the
+ * survivors' mass. This is sel_sample's order for top_k > 0; a row with
+ * top_k == 0 is walked in the same order here (sel_sample walks it by
+ * ascending id). Ranks are counted exactly; masses are sums in 64 bits.
+ * A logit of -Inf is a masked id: it is never drawn and does not count.
+ *
+ *   d_logits       rows of V of `dtype` (SEL_F16 or SEL_BF16), row r at
+ *                  r * ld; 2-byte aligned, any ld >= V. V at most
+ *                  SEL_SAMPLE16_MAX_V (SEL_EUNSUPPORTED beyond)
+ *   d_temperature  [rows] f32, >= 0 and finite; 0 is greedy (the lowest id of
+ *                  the maximum, probability 1); NULL: 1 for every row
+ *   d_top_k        [rows] u32, 0 or >= V keeps every id; NULL: 0
+ *   d_top_p        [rows] f32 in (0, 1], 1 disables it; NULL: 1
+ *   d_min_p        [rows] f32 in [0, 1), 0 disables it; NULL: 0
+ *   d_uniforms     [rows] f32 in [0, 1)
+ *   d_out_ids      [rows] u32: the drawn id or SEL_INVALID_ID
+ *   d_out_probs    [rows] f32: its probability among the survivors, or NaN
+ * A row is invalid when it holds a NaN or a +Inf, when every id is masked, or
+ * when a parameter or the uniform of the row is out of its range.
+ */
+sel_status sel_sample16(const void *d_logits, int dtype, uint32_t rows,
+                        uint32_t V, uint64_t ld, const float *d_temperature,
+                        const uint32_t *d_top_k, const float *d_top_p,
+                        const float *d_min_p, const float *d_uniforms,
+                        uint32_t *d_out_ids, float *d_out_probs,
+                        cudaStream_t stream);
+
+/*
+ * sel_embed -- out[i] = scale * table[ids[i]], formed in fp32 and rounded once;
+ * an id >= V (SEL_INVALID_ID: a failed row, the places behind a sequence's
+ * last emitted token) gives a row of zeros.
+ * sel_embed_w4 -- the same from a 4-bit matrix (as for sel_head_w4, so that
+ * tied weights serve both): out[i][k] = scale * s * (q - z).
+ *
+ *   d_ids    [n] u32, any order, repeats allowed
+ *   d_table  [V][H] of `dtype` (any sel_dtype), aligned to its elements;
+ *            d_q (16-byte aligned), d_scales, d_zeros, group as above
+ *   d_out    [n][H] of `dtype`; sel_embed_w4: 16-byte aligned
+ */
+sel_status sel_embed(const uint32_t *d_ids, uint32_t n, const void *d_table,
+                     int dtype, uint32_t V, uint32_t H, float scale,
+                     void *d_out, cudaStream_t stream);
+sel_status sel_embed_w4(const uint32_t *d_ids, uint32_t n, const uint8_t *d_q,
+                        const void *d_scales, const uint8_t *d_zeros,
+                        uint32_t group, int dtype, uint32_t V, uint32_t H,
+                        float scale, void *d_out, cudaStream_t stream);
 
 /* Static description of a status code. */
 const char *sel_status_string(sel_status status);

@@ -31,7 +31,10 @@ EXPORTED = ("sel_workspace_bytes", "sel_workspace_init", "sel_argmax", "sel_topk
             "sel_merge_shards", "sel_sample_shards", "sel_argmax_excluding",
             "spec_accept_sampler", "spec_diagnostics", "sel_topk_stats", "sel_shard_draw_mass",
             "sel_shard_draw", "spec_shard_stats", "spec_accept_shards", "spec_shard_draw_mass",
-            "spec_shard_draw")
+            "spec_shard_draw", "sel_head_w4", "sel_sample16", "sel_embed", "sel_embed_w4")
+SEL_F32, SEL_F16, SEL_BF16 = range(3)
+SEL_MAX_H = 1 << 20
+SEL_SAMPLE16_MAX_V = 524_208
 SEL_NOALLOC_SCRATCH_BYTES = 1 << 20
 SEL_MAX_SHARDS = 64
 SEL_MAX_EXCLUDED = 256
@@ -65,6 +68,7 @@ class SpecParams(ctypes.Structure):
 
 _vp = ctypes.c_void_p
 _u32 = ctypes.c_uint32
+_u64 = ctypes.c_uint64
 _sz = ctypes.c_size_t
 _lib: ctypes.CDLL | None = None
 
@@ -128,6 +132,15 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.spec_shard_draw.argtypes = [_vp, _vp, _u32, _u32, _u32, _u32, _u32, _u32, _vp, _vp, _vp, _vp, _sz, _vp]
     lib.spec_shard_draw.restype = ctypes.c_int
     lib.sel_sample_shards.restype = ctypes.c_int
+    _i, _f = ctypes.c_int, ctypes.c_float
+    lib.sel_head_w4.argtypes = [_vp, _u32, _vp, _vp, _vp, _u32, _i, _u32, _u32, _vp, _i, _u64, _vp]
+    lib.sel_head_w4.restype = _i
+    lib.sel_sample16.argtypes = [_vp, _i, _u32, _u32, _u64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
+    lib.sel_sample16.restype = _i
+    lib.sel_embed.argtypes = [_vp, _u32, _vp, _i, _u32, _u32, _f, _vp, _vp]
+    lib.sel_embed.restype = _i
+    lib.sel_embed_w4.argtypes = [_vp, _u32, _vp, _vp, _vp, _u32, _i, _u32, _u32, _f, _vp, _vp]
+    lib.sel_embed_w4.restype = _i
     lib.sel_status_string.argtypes = [ctypes.c_int]
     lib.sel_status_string.restype = ctypes.c_char_p
     if path is None:
@@ -421,6 +434,126 @@ def spec_shard_draw(target, draft, offset: int, g: int, G: int, plan, masses, em
     _check(load().spec_shard_draw(_ptr(target), _ptr(draft), S, K, V, int(offset), int(g), int(G), _ptr(plan),
                                   _ptr(masses), _ptr(emitted), _ptr(ws), _nbytes(ws), _stream(stream)),
            "spec_shard_draw")
+
+
+# ---------------------------------------------------------------------------
+# around selection: 4-bit output head, 16-bit sampling, embedding
+# ---------------------------------------------------------------------------
+
+_DTYPES = {torch.float32: SEL_F32, torch.float16: SEL_F16, torch.bfloat16: SEL_BF16}
+_IDS = (torch.int32, torch.uint32)
+
+
+def _device(first, *others) -> None:
+    """Every tensor on the one current CUDA device (the stream's)."""
+    dev = first.device
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        raise ValueError("tensors passed to the selection library must be on the current CUDA device")
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError("tensors of one call must be on one device")
+
+
+def _rows_2d(t, name) -> tuple[int, int, int]:
+    """(rows, columns, row stride) of a matrix whose rows are contiguous."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    ld = t.stride(0) if rows > 1 else cols
+    if ld < cols:
+        raise ValueError(f"the rows of {name} must not overlap")
+    return rows, cols, ld
+
+
+def _vector(t, n: int, dtypes, name) -> int | None:
+    if t is None:
+        return None
+    if t.dtype not in dtypes or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous vector of {n} entries of {' or '.join(map(str, dtypes))}")
+    return t.data_ptr()
+
+
+def _w4(q, scales, zeros, group: int, dtype) -> tuple[int, int]:
+    """(V, H) of a 4-bit matrix: q [V, H / 2] uint8, scales [V, H / group] of
+    `dtype`, zeros [V, H / group] uint8 or None."""
+    if q.dtype != torch.uint8 or q.dim() != 2 or not q.is_contiguous():
+        raise ValueError("q must be a contiguous uint8 matrix [V, H / 2]")
+    V, H = q.shape[0], 2 * q.shape[1]
+    if group <= 0 or H % group:
+        raise ValueError("H must be a multiple of group")
+    if scales.dtype != dtype or tuple(scales.shape) != (V, H // group) or not scales.is_contiguous():
+        raise ValueError(f"scales must be contiguous [V, H / group] of {dtype}")
+    if zeros is not None and (zeros.dtype != torch.uint8 or zeros.shape != scales.shape or not zeros.is_contiguous()):
+        raise ValueError("zeros must be contiguous uint8 [V, H / group]")
+    return V, H
+
+
+def sel_head_w4(hidden, q, scales, zeros, group: int, logits, stream=None) -> None:
+    """hidden [rows, H] f16/bf16 through the 4-bit matrix (q [V, H / 2] uint8,
+    scales [V, H / group] of hidden's type, zeros [V, H / group] uint8 or
+    None) into logits [rows, V] (f32, f16 or bf16; its rows may be padded)."""
+    _device(hidden, q, scales, zeros, logits)
+    V, H = _w4(q, scales, zeros, group, hidden.dtype)
+    rows, cols, ld = _rows_2d(logits, "logits")
+    if tuple(hidden.shape) != (rows, H) or not hidden.is_contiguous():
+        raise ValueError("hidden must be contiguous [rows, H]")
+    if cols != V or logits.dtype not in _DTYPES or hidden.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("logits must be [rows, V] of f32, f16 or bf16, hidden of f16 or bf16")
+    _check(load().sel_head_w4(hidden.data_ptr(), rows, q.data_ptr(), scales.data_ptr(),
+                              None if zeros is None else zeros.data_ptr(), group, _DTYPES[hidden.dtype], V, H,
+                              logits.data_ptr(), _DTYPES[logits.dtype], ld, _stream(stream)), "sel_head_w4")
+
+
+def sel_sample16(logits, temperature, top_k, top_p, min_p, uniforms, out_ids, out_probs, stream=None) -> None:
+    """logits [rows, V] f16/bf16 (rows may be padded); temperature, top_p,
+    min_p f32 [rows] and top_k int32/uint32 [rows], each or None (1, off, off,
+    off); uniforms, out_probs f32 [rows], out_ids int32/uint32 [rows]."""
+    _device(logits, temperature, top_k, top_p, min_p, uniforms, out_ids, out_probs)
+    rows, V, ld = _rows_2d(logits, "logits")
+    if logits.dtype not in _DTYPES:
+        raise ValueError("logits must be f16 or bf16")
+    f32 = (torch.float32,)
+    _check(load().sel_sample16(logits.data_ptr(), _DTYPES[logits.dtype], rows, V, ld,
+                               _vector(temperature, rows, f32, "temperature"), _vector(top_k, rows, _IDS, "top_k"),
+                               _vector(top_p, rows, f32, "top_p"), _vector(min_p, rows, f32, "min_p"),
+                               _vector(uniforms, rows, f32, "uniforms"), _vector(out_ids, rows, _IDS, "out_ids"),
+                               _vector(out_probs, rows, f32, "out_probs"), _stream(stream)), "sel_sample16")
+
+
+def _embed_out(ids, out, H: int, dtype) -> int:
+    if ids.dtype not in _IDS or not ids.is_contiguous():
+        raise ValueError("ids must be contiguous int32 or uint32")
+    n = ids.numel()
+    if out.dtype != dtype or out.numel() != n * H or out.shape[-1] != H or not out.is_contiguous():
+        raise ValueError(f"out must be contiguous [ids, H] of {dtype}")
+    return n
+
+
+def sel_embed(ids, table, scale: float, out, stream=None) -> None:
+    """out[i] = scale * table[ids[i]] (zeros for ids >= V); table [V, H] f32,
+    f16 or bf16, ids of any shape, out that shape plus [H]."""
+    _device(ids, table, out)
+    if table.dtype not in _DTYPES or table.dim() != 2 or not table.is_contiguous():
+        raise ValueError("table must be a contiguous matrix [V, H] of f32, f16 or bf16")
+    V, H = table.shape
+    n = _embed_out(ids, out, H, table.dtype)
+    _check(load().sel_embed(ids.data_ptr(), n, table.data_ptr(), _DTYPES[table.dtype], V, H, scale, out.data_ptr(),
+                            _stream(stream)), "sel_embed")
+
+
+def sel_embed_w4(ids, q, scales, zeros, group: int, scale: float, out, stream=None) -> None:
+    """sel_embed from a 4-bit matrix (as for sel_head_w4); out of the scales'
+    type."""
+    _device(ids, q, scales, zeros, out)
+    if scales.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("scales must be f16 or bf16")
+    V, H = _w4(q, scales, zeros, group, scales.dtype)
+    n = _embed_out(ids, out, H, scales.dtype)
+    _check(load().sel_embed_w4(ids.data_ptr(), n, q.data_ptr(), scales.data_ptr(),
+                               None if zeros is None else zeros.data_ptr(), group, _DTYPES[scales.dtype], V, H, scale,
+                               out.data_ptr(), _stream(stream)), "sel_embed_w4")
 
 
 # ---------------------------------------------------------------------------

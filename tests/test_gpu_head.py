@@ -1,0 +1,120 @@
+"""sel_head_w4 on the GPU against the 64-bit product."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import decode as D
+from sampling_row_fp32_gb300 import binding as B
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+def make(seed, rows, V, H, group, zeros, dtype):
+    rng = np.random.default_rng(seed)
+    q = rng.integers(0, 256, size=(V, H // 2), dtype=np.uint8)
+    s = torch.from_numpy(rng.uniform(-0.02, 0.04, size=(V, H // group))).to(DT[dtype])
+    z = torch.from_numpy(rng.integers(0, 256 if zeros == "any" else 16, size=(V, H // group), dtype=np.uint8)) if zeros else None
+    x = torch.from_numpy(rng.normal(0, 1, size=(rows, H))).to(DT[dtype])
+    return x, torch.from_numpy(q), s, z
+
+
+def tolerance(mag, want, group, H, out):
+    """Products are exact in fp32. A logit is a sum of `group` products a
+    group, scaled, over H / group groups: at most group + H / group + 2
+    roundings lie on a term's way, each at most a whole fp32 step (2^-23, as a
+    truncating accumulator gives) of a sum no larger than the terms'
+    magnitudes; then one rounding to the output type."""
+    acc = (group + H // group + 2) * 2.0 ** -23 * mag
+    eps = torch.finfo(DT[out]).eps / 2
+    return acc + eps * (np.abs(want) + acc) + torch.finfo(DT[out]).smallest_normal * eps
+
+
+def check(x, q, s, z, group, out="f32", ld=None):
+    rows, V, H = x.shape[0], q.shape[0], x.shape[1]
+    ld = ld or V
+    buf = torch.full((max(rows, 1), ld), -77.0, dtype=DT[out], device="cuda")
+    logits = buf[:rows, :V]
+    B.sel_head_w4(x.cuda(), q.cuda(), s.cuda(), None if z is None else z.cuda(), group, logits)
+    want, mag = D.head_w4(x.double().numpy(), q.numpy(), s.double().numpy(), None if z is None else z.numpy(), group)
+    got = logits.double().cpu().numpy()
+    tol = tolerance(mag, want, group, H, out)
+    assert (np.abs(got - want) <= tol).all(), np.max(np.abs(got - want) / tol)
+    assert (buf[:, V:] == -77.0).all()  # what lies between the rows is left as it was
+    return logits
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("rows,V,groups_per_row,zeros", [
+    (1, 1, 1, None), (1, 300, 5, None), (2, 129, 3, "any"), (8, 128, 8, "nibble"), (9, 257, 7, None),
+    (16, 1000, 2, "nibble"), (17, 513, 9, "any"), (33, 640, 4, None), (49, 1031, 11, "nibble"), (64, 256, 16, None),
+    (65, 300, 3, "any"), (130, 77, 6, None)])
+def test_shapes(dtype, group, rows, V, groups_per_row, zeros):
+    check(*make(rows + V, rows, V, groups_per_row * group, group, zeros, dtype), group)
+
+
+@pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("ld", [None, 1035, 1040])
+def test_output_types_and_strides(out, ld):
+    check(*make(3, 5, 1031, 512, 64, "nibble", "bf16"), 64, out, ld)
+
+
+@pytest.mark.parametrize("rows,V,H,group", [(1, 20_011, 4096, 128), (49, 20_011, 4096, 64), (64, 9_999, 8192, 32), (7, 40_000, 2880, 32)])
+def test_model_widths(rows, V, H, group):
+    check(*make(rows, rows, V, H, group, None, "bf16"), group)
+
+
+def test_every_nibble_at_every_place():
+    """Weights one column at a time: column k's nibble of row v alone gets through."""
+    H, V = 256, 512
+    q = np.zeros((V, H // 2), dtype=np.uint8)
+    for v in range(V):
+        k = v % H
+        q[v, k // 2] = (v % 16) << (4 * (k % 2))
+    x = torch.arange(1, H + 1).to(torch.float16)[None]  # whole numbers up to 256: exact everywhere
+    z = torch.zeros(V, H // 64, dtype=torch.uint8)
+    s = torch.ones(V, H // 64, dtype=torch.float16)
+    logits = check(x, torch.from_numpy(q), s, z, 64)
+    want = torch.tensor([(v % 16) * (v % H + 1) for v in range(V)], dtype=torch.float32)
+    assert torch.equal(logits[0].cpu(), want)
+
+
+def test_no_rows():
+    x, q, s, z = make(0, 0, 10, 64, 64, None, "bf16")
+    B.sel_head_w4(x.cuda(), q.cuda(), s.cuda(), None, 64, torch.empty(0, 10, device="cuda"))
+
+
+def test_nonfinite_inputs_fail_closed():
+    """A NaN hidden state or scale reaches its row's or column's logits and no others."""
+    x, q, s, z = make(1, 3, 200, 256, 64, None, "bf16")
+    x[1, 130] = float("nan")
+    s[77, 2] = float("inf")
+    logits = torch.empty(3, 200, device="cuda")
+    B.sel_head_w4(x.cuda(), q.cuda(), s.cuda(), None, 64, logits)
+    finite = torch.isfinite(logits).cpu()
+    want = torch.ones(3, 200, dtype=torch.bool)
+    want[1] = False
+    want[:, 77] = False
+    assert torch.equal(finite, want)
+
+
+def test_offsets_past_32_bits():
+    """A packed matrix of more than 2^32 bytes: its last rows are its own."""
+    V, H = 1_060_000, 8192
+    x, q, s, z = make(2, 2, 300, H, 128, None, "bf16")
+    big_q = torch.zeros(V, H // 2, dtype=torch.uint8, device="cuda")
+    big_s = torch.zeros(V, H // 128, dtype=torch.bfloat16, device="cuda")
+    big_q[-300:], big_s[-300:] = q.cuda(), s.cuda()
+    logits = torch.full((2, V), 5.0, device="cuda")
+    B.sel_head_w4(x.cuda(), big_q, big_s, None, 128, logits)
+    want, mag = D.head_w4(x.double().numpy(), q.numpy(), s.double().numpy(), None, 128)
+    assert (np.abs(logits[:, -300:].double().cpu().numpy() - want) <= tolerance(mag, want, 128, H, "f32")).all()
+    assert not logits[:, :-300].any()
