@@ -678,8 +678,8 @@ typedef enum sel_dtype { SEL_F32 = 0, SEL_F16 = 1, SEL_BF16 = 2 } sel_dtype;
  * 4-bit matrices. Row v of a [V][H] matrix is H / 2 bytes: byte i holds column
  * 2 i in its low nibble and column 2 i + 1 in its high one. Every `group`
  * (32, 64 or 128; H a multiple of it) columns of a row share a scale s, of
- * the hidden states' type, and a zero point z, a byte (any value; 8 for
- * every group when the array is NULL). The entry is s * (q - z).
+ * the hidden states' type, and a zero point z in 0..15 (the low four bits of
+ * a byte; 8 for every group when the array is NULL). The entry is s * (q - z).
  *
  * sel_head_w4 -- logits[r][v] = sum over columns k of
  * hidden[r][k] * s[v][k / group] * (q[v][k] - z[v][k / group]).

@@ -14,12 +14,12 @@ INVALID = 0xFFFFFFFF
 
 def dequantise(q, scales, zeros, group):
     """[V, H] float64 entries s * (q - z): byte i of a row holds column 2 i in
-    its low nibble and 2 i + 1 in its high one."""
+    its low nibble and 2 i + 1 in its high one; z is a byte's low four bits."""
     V, half = q.shape
     w = np.empty((V, 2 * half))
     w[:, 0::2] = q & 15
     w[:, 1::2] = q >> 4
-    z = np.full(scales.shape, 8.0) if zeros is None else zeros.astype(np.float64)
+    z = np.full(scales.shape, 8.0) if zeros is None else (zeros & 15).astype(np.float64)
     return (w - np.repeat(z, group, axis=1)) * np.repeat(scales, group, axis=1)
 
 

@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kNT) embed_w4_kernel(EmbedArgs a) {
         const uint32_t w = static_cast<const uint32_t*>(a.table)[static_cast<size_t>(id) * a.per_row + c];
         const size_t g = static_cast<size_t>(id) * (a.H / a.group) + (c * 8u) / a.group;
         const float s = to_f32(static_cast<const T*>(a.scales)[g]);
-        const int z = a.zeros ? a.zeros[g] : 8;
+        const int z = a.zeros ? a.zeros[g] & 15 : 8;
         T* e = reinterpret_cast<T*>(&v);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
