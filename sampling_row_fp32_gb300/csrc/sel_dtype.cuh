@@ -15,6 +15,14 @@ __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 
+// The value of a 16-bit pattern of T.
+template <typename T>
+__device__ __forceinline__ float bits_f32(uint16_t b);
+template <>
+__device__ __forceinline__ float bits_f32<__half>(uint16_t b) { return __half2float(__ushort_as_half(b)); }
+template <>
+__device__ __forceinline__ float bits_f32<__nv_bfloat16>(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
+
 // One rounding to nearest even.
 template <typename T>
 __device__ __forceinline__ T from_f32(float x);

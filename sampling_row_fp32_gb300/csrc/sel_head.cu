@@ -12,13 +12,14 @@
 // 256 (two subtiles of 128 TMEM lanes), each over all columns. Warp roles:
 //   warp 0        copies packed weights and hidden states into a ring of
 //                 shared-memory stages of 128 columns (TMA, swizzled)
-//   warps 4-11    unpack 64 columns of a row each: two 16-byte loads, nibbles
+//   warps 4-19    unpack 64 columns of a row each: two 16-byte loads, nibbles
 //                 to the type by placing them in the mantissa of 128 (bf16) or
 //                 1024 (f16) and subtracting 128 + z (1024 + z), both exact;
 //                 the tile goes to TMEM as the product's A operand
-//   warp 1        issues the products (A from TMEM, B = hidden states from
-//                 shared memory, D in TMEM, double-buffered by group)
-//   warps 12-19   read each group's D, add s * D to fp32 registers, and
+//   warps 1, 2    issue the products of a subtile each (A from TMEM, B =
+//                 hidden states from shared memory, D in TMEM,
+//                 double-buffered by group)
+//   warps 20-27   read each group's D, add s * D to fp32 registers, and
 //                 write the logits after the last group
 // Every wait is bounded; one that runs out makes the CTA's logits NaN.
 #include <cuda.h>
@@ -35,16 +36,21 @@
 namespace sel {
 namespace {
 
-constexpr int kNT = 640;
 constexpr uint32_t kTileV = 256;     // matrix rows a tile
 constexpr uint32_t kSubV = 128;      // rows a subtile: TMEM lanes
 constexpr uint32_t kBoxV = 64;       // rows a weight copy
 constexpr uint32_t kStageK = 128;    // columns a stage
-constexpr uint32_t kTileK = 64;      // columns an A buffer
+constexpr uint32_t kTileK = 64;      // columns of a 128-byte row of hidden states
 constexpr uint32_t kWBytes = kTileV * kStageK / 2;
-constexpr uint32_t kABufs = 4, kDBufs = 2;
-constexpr uint32_t kACols = kTileK / 2;  // TMEM columns of an A buffer
-constexpr uint32_t kMaxStages = 10;
+constexpr uint32_t kABufs = 2;
+constexpr uint32_t kACols = kStageK / 2;  // TMEM columns of an A buffer
+constexpr uint32_t kMaxStages = 10, kMaxDBufs = 4;
+
+// Warps: four of control, sixteen that unpack, eight of the epilogue; the
+// registers of a launch (896 x 72) are split 40 / 56 / 120 between them.
+constexpr int kUnpackWarp = 4, kEpilogueWarp = 20, kNT = 32 * 28;
+constexpr int kLaunchRegs = 72, kControlRegs = 40, kUnpackRegs = 56, kEpilogueRegs = 120;
+static_assert(4 * kControlRegs + 16 * kUnpackRegs + 8 * kEpilogueRegs <= 28 * kLaunchRegs);
 
 template <int N>
 struct Config {
@@ -52,6 +58,7 @@ struct Config {
     static constexpr uint32_t kStageBytes = kWBytes + 2 * kXAtom;
     static constexpr uint32_t kStages = 212 * 1024 / kStageBytes < kMaxStages ? 212 * 1024 / kStageBytes : kMaxStages;
     static constexpr uint32_t kSmem = kStages * kStageBytes + 1024;
+    static constexpr uint32_t kDBufs = N > 32 ? 2 : kMaxDBufs;
     static constexpr uint32_t kACol = 2 * kDBufs * N;  // A buffers lie behind the D buffers
     static_assert(kACol + 2 * kABufs * kACols <= 512);
 };
@@ -61,7 +68,7 @@ struct HeadArgs {
     const uint8_t* zeros;
     void* out;
     uint64_t ld;
-    uint32_t rows, V, H, group;
+    uint32_t rows, V, H, group_log2;
     uint32_t range;  // matrix rows a CTA
 };
 
@@ -109,22 +116,22 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
+// 16 or 32 columns of each lane, once they have arrived.
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(addr));
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
 }
-// Waits for the loads before it; the registers pass through, so that no use of
-// theirs moves ahead of the wait.
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 :
-                 : "memory");
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr)
+        : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -158,57 +165,318 @@ struct Unpack<__half> {
     }
 };
 
-// Eight nibbles to four pairs (columns 2 i, 2 i + 1) of q - z.
+// Eight nibbles to four pairs (columns 2 i, 2 i + 1) of q - z: byte i of the
+// word and of the word shifted by a nibble into the pair's halves, the low
+// nibble of each placed in the magic number, one subtraction.
 template <typename T>
 __device__ __forceinline__ void unpack8(uint32_t w, uint32_t zc, uint32_t* r) {
     const uint32_t u = w >> 4;
+    // (in assembly: left to itself the compiler spends twice the instructions)
+    asm("prmt.b32 %0, %1, %2, 0x4400;" : "=r"(r[0]) : "r"(w), "r"(u));
+    asm("prmt.b32 %0, %1, %2, 0x5511;" : "=r"(r[1]) : "r"(w), "r"(u));
+    asm("prmt.b32 %0, %1, %2, 0x6622;" : "=r"(r[2]) : "r"(w), "r"(u));
+    asm("prmt.b32 %0, %1, %2, 0x7733;" : "=r"(r[3]) : "r"(w), "r"(u));
 #pragma unroll
     for (uint32_t i = 0; i < 4; ++i) {
-        const uint32_t p = __byte_perm(w, u, i | (i << 4) | ((4 + i) << 8) | ((4 + i) << 12));
-        r[i] = Unpack<T>::sub((p & 0x000F000Fu) | Unpack<T>::kMagic, zc);
+        asm("lop3.b32 %0, %0, 0x000F000F, %1, 0xEA;" : "+r"(r[i]) : "r"(Unpack<T>::kMagic));
+        r[i] = Unpack<T>::sub(r[i], zc);
     }
 }
 
-__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t s) {
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(d), "l"(s));
+// A slot of a ring of barriers and the parity of the round it is in.
+template <uint32_t kN>
+struct Ring {
+    uint32_t i = 0, phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++i == kN) {
+            i = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
 }
+
+// Waits for a barrier's phase. A wait that runs out raises `err`, and with
+// `err` raised every other one returns at once: the roles then run to their
+// ends on whatever the buffers hold (in bounds as ever) and the CTA's logits
+// become NaN.
+__device__ __forceinline__ void wait_slow(uint64_t* bar, uint32_t phase, volatile uint32_t* err) {
+    for (uint32_t i = 0; i < kWaitPolls; ++i) {
+        if (mbar_try_wait(bar, phase) || *err) return;
+    }
+    *err = 1;
+}
+__device__ __forceinline__ void wait(uint64_t* bar, uint32_t phase, uint32_t* err) {
+    if (!mbar_try_wait(bar, phase)) wait_slow(bar, phase, err);
+    __syncwarp();
+}
+
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
+template <int kRegs>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 
 struct Ctx {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t a_full[2][kABufs], a_empty[2][kABufs];
-    uint64_t d_full[2][kDBufs], d_empty[2][kDBufs];
-    uint64_t drain;
+    uint64_t d_full[2][kMaxDBufs], d_empty[2][kMaxDBufs];
+    uint64_t drain[2];
     uint32_t tmem;
     uint32_t err;
 };
 
+// Issues one subtile's products. The group is a template parameter so that a
+// whole stage is straight-line code: this warp's instruction latencies, not
+// the tensor cores, bound it otherwise.
+template <typename T, int N>
+struct MmaRole {
+    using C = Config<N>;
+    Ctx* c;
+    unsigned char* ring;
+    uint32_t s, a0, d0;
+    bool leader;
+
+    template <int kGroupLog2>
+    __device__ __forceinline__ void run(uint32_t v_begin, uint32_t v_end, uint32_t blocks, uint32_t H) const {
+        constexpr uint32_t kIdesc = (1u << 4) | (Unpack<T>::kType << 7) | (Unpack<T>::kType << 10) |
+                                    (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(kSubV >> 4) << 24);
+        constexpr uint32_t kHalves = (1u << kGroupLog2) / 32;  // pieces of 32 columns a group
+        Ring<C::kStages> st;
+        Ring<kABufs> ar;
+        Ring<C::kDBufs> dr;
+        for (uint32_t vt = v_begin; vt < v_end; vt += kTileV) {
+            const bool active = s == 0 || v_end - vt > kSubV;
+            for (uint32_t blk = 0; blk < blocks; ++blk) {
+                for (uint32_t k = 0; k < H; k += kStageK) {
+                    // a subtile without rows waits for the stage like its other
+                    // readers, so that no arrival runs ahead into the slot's next use
+                    wait(&c->full[st.i], st.phase, &c->err);
+                    if (active) {
+                        wait(&c->a_full[s][ar.i], ar.phase, &c->err);
+                        tc_fence_after();
+                        const uint64_t b = smem_desc(smem_u32(ring + st.i * C::kStageBytes + kWBytes));
+                        const uint32_t at = a0 + ar.i * kACols;
+                        const uint32_t left = H - k;
+#pragma unroll
+                        for (uint32_t h = 0; h < kStageK / 32; ++h) {
+                            if (h > 0 && h * 32 >= left) break;  // whole groups only
+                            if (h % kHalves == 0) {
+                                wait(&c->d_empty[s][dr.i], dr.phase ^ 1, &c->err);
+                                tc_fence_after();
+                            }
+                            // 32 columns: two products; 64 columns of hidden states are an atom
+                            const uint64_t bh = b + (h / 2) * (C::kXAtom >> 4) + (h % 2) * 4;
+                            if (leader) {
+                                tc_mma(d0 + dr.i * N, at + h * 16, bh, kIdesc, h % kHalves != 0);
+                                tc_mma(d0 + dr.i * N, at + h * 16 + 8, bh + 2, kIdesc, true);
+                                if (h % kHalves == kHalves - 1) tc_commit(&c->d_full[s][dr.i]);
+                            }
+                            if (h % kHalves == kHalves - 1) dr.next();
+                        }
+                        if (leader) {
+                            tc_commit(&c->a_empty[s][ar.i]);
+                            tc_commit(&c->empty[st.i]);
+                        }
+                        ar.next();
+                    } else if (leader) {
+                        arrive(&c->empty[st.i]);
+                    }
+                    st.next();
+                }
+            }
+        }
+    }
+};
+
+// Entries kPer * stage .. + kPer - 1 of a row's group array (scales or zero
+// points), as raw bits in the low bytes; entries past the row's end are not
+// read. kPer entries of a stage are one load where they are aligned, which
+// the caller knows (`vec`).
+template <typename E, uint32_t kPer>
+__device__ __forceinline__ uint64_t group_entries(const E* row, uint32_t stage, uint32_t groups, bool vec) {
+    constexpr uint32_t kBytes = kPer * sizeof(E);
+    const E* p = row + stage * kPer;
+    if (vec) {
+        if constexpr (kBytes == 8) return *reinterpret_cast<const uint64_t*>(p);
+        else if constexpr (kBytes == 4) return *reinterpret_cast<const uint32_t*>(p);
+        else if constexpr (kBytes == 2) return *reinterpret_cast<const uint16_t*>(p);
+        else return *reinterpret_cast<const uint8_t*>(p);
+    }
+    uint64_t v = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < kPer; ++i)
+        if (stage * kPer + i < groups) v |= static_cast<uint64_t>(p[i]) << (8 * sizeof(E) * i);
+    return v;
+}
+
+// Unpacks half (64 columns) of every stage for one subtile's 32 lanes.
+template <typename T, int N>
+struct UnpackRole {
+    using C = Config<N>;
+    Ctx* c;
+    const unsigned char* ring;
+    const uint8_t* zeros;
+    uint32_t s, half, row, a0;  // row: within the tile
+
+    template <bool kZeros, int kGroupLog2>
+    __device__ __forceinline__ void run(uint32_t v_begin, uint32_t v_end, uint32_t V, uint32_t blocks, uint32_t H) const {
+        constexpr uint32_t kPer = kStageK >> kGroupLog2;  // groups a stage
+        const uint32_t lane = threadIdx.x & 31;
+        const uint32_t stages = (H + kStageK - 1) / kStageK, groups = H >> kGroupLog2;
+        // 16-byte chunk ch of a 64-byte row lies at ch ^ ((row >> 1) & 3)
+        const uint32_t sw = (row >> 1) & 3;
+        const unsigned char* src0 = ring + row * 64 + (((2 * half) ^ sw) << 4);
+        const unsigned char* src1 = ring + row * 64 + (((2 * half + 1) ^ sw) << 4);
+        const bool vec = kZeros && H % kStageK == 0 && reinterpret_cast<uintptr_t>(zeros) % kPer == 0;
+        Ring<C::kStages> st;
+        Ring<kABufs> ar;
+        for (uint32_t vt = v_begin; vt < v_end; vt += kTileV) {
+            const bool active = s == 0 || v_end - vt > kSubV;
+            const uint8_t* z = kZeros ? zeros + static_cast<uint64_t>(min(vt + row, V - 1)) * groups : nullptr;
+            for (uint32_t blk = 0; blk < blocks; ++blk) {
+                uint32_t z_next = 0;
+                if (kZeros) z_next = static_cast<uint32_t>(group_entries<uint8_t, kPer>(z, 0, groups, vec));
+                for (uint32_t i = 0; i < stages; ++i) {
+                    uint32_t zc0 = Unpack<T>::kMagic | 0x00080008u, zc1 = zc0;
+                    if (kZeros) {
+                        // this stage's zero points, and the next one's on their way
+                        const uint32_t zs = z_next >> (kPer == 4 ? 16 * half : kPer == 2 ? 8 * half : 0);
+                        zc0 = Unpack<T>::kMagic | (zs & 15) * 0x00010001u;
+                        zc1 = kPer == 4 ? Unpack<T>::kMagic | ((zs >> 8) & 15) * 0x00010001u : zc0;
+                        if (i + 1 < stages) z_next = static_cast<uint32_t>(group_entries<uint8_t, kPer>(z, i + 1, groups, vec));
+                    }
+                    wait(&c->full[st.i], st.phase, &c->err);
+                    if (active) {
+                        const uint4 q0 = *reinterpret_cast<const uint4*>(src0 + st.i * C::kStageBytes);
+                        const uint4 q1 = *reinterpret_cast<const uint4*>(src1 + st.i * C::kStageBytes);
+                        uint32_t r[32];
+                        unpack8<T>(q0.x, zc0, r);
+                        unpack8<T>(q0.y, zc0, r + 4);
+                        unpack8<T>(q0.z, zc0, r + 8);
+                        unpack8<T>(q0.w, zc0, r + 12);
+                        unpack8<T>(q1.x, zc1, r + 16);
+                        unpack8<T>(q1.y, zc1, r + 20);
+                        unpack8<T>(q1.z, zc1, r + 24);
+                        unpack8<T>(q1.w, zc1, r + 28);
+                        wait(&c->a_empty[s][ar.i], ar.phase ^ 1, &c->err);
+                        tc_fence_after();
+                        tmem_st32(a0 + ar.i * kACols, r);
+                        tmem_wait_st();
+                        tc_fence_before();
+                    }
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (active) arrive(&c->a_full[s][ar.i]);
+                        arrive(&c->empty[st.i]);
+                    }
+                    if (active) ar.next();
+                    st.next();
+                }
+            }
+        }
+    }
+};
+
+// Adds one subtile's scaled group products for 32 matrix rows and writes them.
+template <typename T, typename O, int N>
+struct EpilogueRole {
+    using C = Config<N>;
+    Ctx* c;
+    const T* scales;
+    O* out;
+    uint64_t ld;
+    uint32_t rows, s, row, d0;
+
+    template <int kGroupLog2>
+    __device__ __forceinline__ void run(uint32_t v_begin, uint32_t v_end, uint32_t V, uint32_t blocks, uint32_t H) const {
+        constexpr uint32_t kPer = kStageK >> kGroupLog2;
+        constexpr uint32_t kLd = N < 32 ? N : 32;  // columns of D a load
+        const uint32_t lane = threadIdx.x & 31;
+        const uint32_t stages = (H + kStageK - 1) / kStageK, groups = H >> kGroupLog2;
+        const bool vec = H % kStageK == 0 && reinterpret_cast<uintptr_t>(scales) % (2 * kPer) == 0;
+        Ring<C::kDBufs> dr;
+        for (uint32_t vt = v_begin; vt < v_end; vt += kTileV) {
+            if (s == 1 && v_end - vt <= kSubV) continue;
+            const uint16_t* sc =
+                reinterpret_cast<const uint16_t*>(scales) + static_cast<uint64_t>(min(vt + row, V - 1)) * groups;
+            for (uint32_t blk = 0; blk < blocks; ++blk) {
+                float acc[N];
+#pragma unroll
+                for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+                uint64_t s_next = group_entries<uint16_t, kPer>(sc, 0, groups, vec);
+                for (uint32_t st = 0; st < stages; ++st) {
+                    const uint64_t s_now = s_next;
+                    if (st + 1 < stages) s_next = group_entries<uint16_t, kPer>(sc, st + 1, groups, vec);
+#pragma unroll
+                    for (uint32_t g = 0; g < kPer; ++g) {
+                        if (g > 0 && st * kPer + g >= groups) break;
+                        const float sf = bits_f32<T>(static_cast<uint16_t>(s_now >> (16 * g)));
+                        wait(&c->d_full[s][dr.i], dr.phase, &c->err);
+                        tc_fence_after();
+#pragma unroll
+                        for (uint32_t h = 0; h < N / kLd; ++h) {
+                            uint32_t d[kLd];
+                            tmem_ld(d0 + dr.i * N + h * kLd, d);
+                            if (h == N / kLd - 1) {  // the buffer is read
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) arrive(&c->d_empty[s][dr.i]);
+                            }
+#pragma unroll
+                            for (uint32_t i = 0; i < kLd; ++i)
+                                acc[h * kLd + i] = fmaf(sf, __uint_as_float(d[i]), acc[h * kLd + i]);
+                        }
+                        dr.next();
+                    }
+                }
+                if (vt + row < v_end) {
+                    O* o = out + static_cast<uint64_t>(blk) * N * ld + vt + row;
+                    const uint32_t n = rows - blk * N;
+#pragma unroll
+                    for (uint32_t i = 0; i < N; ++i)
+                        if (i < n) o[i * ld] = from_f32<O>(acc[i]);
+                }
+            }
+        }
+    }
+};
+
 template <typename T, typename O, int N>
 __global__ void __launch_bounds__(kNT, 1)
-    head_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, HeadArgs a) {
+    head_kernel(const __grid_constant__ CUtensorMap map_tile, const __grid_constant__ CUtensorMap map_box,
+                const __grid_constant__ CUtensorMap map_x, HeadArgs a) {
     using C = Config<N>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     __shared__ Ctx c;
-    const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // (broadcasts: the compiler then keeps what follows from them in uniform registers)
+    const uint32_t tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFull, tid >> 5, 0);
 
     if (tid == 0) {
         for (uint32_t i = 0; i < C::kStages; ++i) {
             mbar_init(&c.full[i], 1);
-            mbar_init(&c.empty[i], 8 + 1);  // the unpacking warps and the products
+            mbar_init(&c.empty[i], 16 + 2);  // the unpacking warps and the products
         }
         for (uint32_t s = 0; s < 2; ++s) {
+            mbar_init(&c.drain[s], 1);
             for (uint32_t i = 0; i < kABufs; ++i) {
-                mbar_init(&c.a_full[s][i], 4);
+                mbar_init(&c.a_full[s][i], 8);
                 mbar_init(&c.a_empty[s][i], 1);
             }
-            for (uint32_t i = 0; i < kDBufs; ++i) {
+            for (uint32_t i = 0; i < C::kDBufs; ++i) {
                 mbar_init(&c.d_full[s][i], 1);
                 mbar_init(&c.d_empty[s][i], 4);
             }
         }
-        mbar_init(&c.drain, 1);
         c.err = 0;
     }
     if (warp == 1) {
@@ -219,205 +487,86 @@ __global__ void __launch_bounds__(kNT, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = c.tmem;
+    const uint32_t tmem = __shfl_sync(kFull, c.tmem, 0);
     pdl_wait();
     pdl_trigger();
 
     const uint32_t v_begin = blockIdx.x * a.range, v_end = min(a.V, v_begin + a.range);
     const uint32_t blocks = (a.rows + N - 1) / N;  // blocks of hidden rows
-    const uint32_t stages = (a.H + kStageK - 1) / kStageK;
-    const uint32_t ktiles = (a.H + kTileK - 1) / kTileK;
-    const uint32_t groups = a.H / a.group;
-    bool ok = true;
+    const uint32_t quarter = warp & 3;
 
-    if (warp == 0) {
-        if (lane == 0) {
-            uint32_t it = 0;
+    if (warp < kUnpackWarp) {
+        regs_dec<kControlRegs>();
+        // The control warps stay together, so that addresses and descriptors live
+        // in uniform registers; one elected lane issues. (Issued by a lane on its
+        // own, a stage's copies took 1.3k clocks, its products 1.7k, against the
+        // 750 that the weights' bytes take at the copy rate.)
+        const bool leader = elect_one();
+        if (warp == 0) {
+            const uint32_t stages = (a.H + kStageK - 1) / kStageK;
+            Ring<C::kStages> st;
+            uint32_t issued = 0;
+            bool ok = true;
             for (uint32_t vt = v_begin; vt < v_end && ok; vt += kTileV) {
                 const uint32_t boxes = (min(kTileV, v_end - vt) + kBoxV - 1) / kBoxV;
                 for (uint32_t blk = 0; blk < blocks && ok; ++blk) {
-                    for (uint32_t st = 0; st < stages; ++st, ++it) {
-                        const uint32_t slot = it % C::kStages;
-                        ok = mbar_wait(&c.empty[slot], ((it / C::kStages) & 1) ^ 1);
+                    for (uint32_t i = 0; i < stages; ++i) {
+                        ok = __all_sync(kFull, mbar_wait(&c.empty[st.i], st.phase ^ 1));
                         if (!ok) break;
-                        unsigned char* dst = ring + slot * C::kStageBytes;
-                        const uint32_t atoms = st * kStageK + kTileK < a.H ? 2 : 1;
-                        expect_tx(&c.full[slot], boxes * kBoxV * (kStageK / 2) + atoms * C::kXAtom);
-                        for (uint32_t b = 0; b < boxes; ++b)
-                            tma_2d(dst + b * kBoxV * (kStageK / 2), &map_w, st * (kStageK / 2), vt + b * kBoxV,
-                                   &c.full[slot]);
-                        for (uint32_t at = 0; at < atoms; ++at)
-                            tma_2d(dst + kWBytes + at * C::kXAtom, &map_x, st * kStageK + at * kTileK, blk * N,
-                                   &c.full[slot]);
-                    }
-                }
-            }
-            // every copy has landed before the CTA may end (on the normal path
-            // each wait succeeds at once or as the consumers' did)
-            for (uint32_t i = it > C::kStages ? it - C::kStages : 0; i < it; ++i)
-                if (!mbar_wait(&c.full[i % C::kStages], (i / C::kStages) & 1)) ok = false;
-            if (!ok) c.err = 1;
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = (1u << 4) | (Unpack<T>::kType << 7) | (Unpack<T>::kType << 10) |
-                                   (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(kSubV >> 4) << 24);
-            uint32_t it = 0, ac[2] = {0, 0}, dc[2] = {0, 0};
-            for (uint32_t vt = v_begin; vt < v_end && ok; vt += kTileV) {
-                const uint32_t subs = v_end - vt > kSubV ? 2 : 1;
-                for (uint32_t blk = 0; blk < blocks && ok; ++blk) {
-                    for (uint32_t kt = 0; kt < ktiles && ok; ++kt) {
-                        const uint32_t slot = it % C::kStages;
-                        if ((kt & 1) == 0) ok = mbar_wait(&c.full[slot], (it / C::kStages) & 1);
-                        const uint32_t steps = min(4u, (a.H - kt * kTileK) / 16);
-                        const uint64_t b0 =
-                            smem_desc(smem_u32(ring + slot * C::kStageBytes + kWBytes + (kt & 1) * C::kXAtom));
-#pragma unroll
-                        for (uint32_t s = 0; s < 2; ++s) {
-                            if (s >= subs || !ok) continue;
-                            const uint32_t buf = ac[s] % kABufs;
-                            ok = mbar_wait(&c.a_full[s][buf], (ac[s] / kABufs) & 1);
-                            if (!ok) continue;
-                            tc_fence_after();
-                            const uint32_t a0 = tmem + C::kACol + (s * kABufs + buf) * kACols;
-                            for (uint32_t j = 0; j < steps; ++j) {
-                                const uint32_t k = kt * kTileK + j * 16;
-                                const bool first = k % a.group == 0;
-                                const uint32_t db = dc[s] % kDBufs;
-                                if (first) {
-                                    ok = mbar_wait(&c.d_empty[s][db], ((dc[s] / kDBufs) & 1) ^ 1);
-                                    if (!ok) break;
-                                    tc_fence_after();
-                                }
-                                tc_mma(tmem + (s * kDBufs + db) * N, a0 + j * 8, b0 + j * 2, idesc, !first);
-                                if ((k + 16) % a.group == 0) {
-                                    tc_commit(&c.d_full[s][db]);
-                                    ++dc[s];
-                                }
+                        unsigned char* dst = ring + st.i * C::kStageBytes;
+                        uint64_t* full = &c.full[st.i];
+                        const bool two = i * kStageK + kTileK < a.H;
+                        if (leader) {
+                            expect_tx(full, boxes * kBoxV * (kStageK / 2) + (two ? 2 : 1) * C::kXAtom);
+                            if (boxes == kTileV / kBoxV) {
+                                tma_2d(dst, &map_tile, i * (kStageK / 2), vt, full);
+                            } else {
+                                for (uint32_t b = 0; b < boxes; ++b)
+                                    tma_2d(dst + b * kBoxV * (kStageK / 2), &map_box, i * (kStageK / 2), vt + b * kBoxV,
+                                           full);
                             }
-                            tc_commit(&c.a_empty[s][buf]);
-                            ++ac[s];
+                            tma_2d(dst + kWBytes, &map_x, i * kStageK, blk * N, full);
+                            if (two) tma_2d(dst + kWBytes + C::kXAtom, &map_x, i * kStageK + kTileK, blk * N, full);
                         }
-                        if ((kt & 1) || kt + 1 == ktiles) {
-                            tc_commit(&c.empty[slot]);
-                            ++it;
-                        }
+                        ++issued;
+                        st.next();
                     }
                 }
             }
+            // every copy has landed before the CTA may end
+            if (leader) {
+                for (uint32_t i = issued > C::kStages ? issued - C::kStages : 0; i < issued; ++i)
+                    if (!mbar_wait(&c.full[i % C::kStages], (i / C::kStages) & 1)) ok = false;
+                if (!ok) c.err = 1;
+            }
+        } else if (warp == 1 || warp == 2) {
+            const uint32_t s = warp - 1;
+            const MmaRole<T, N> role{&c, ring, s, tmem + C::kACol + s * kABufs * kACols, tmem + s * C::kDBufs * N, leader};
+            if (a.group_log2 == 7) role.template run<7>(v_begin, v_end, blocks, a.H);
+            else if (a.group_log2 == 6) role.template run<6>(v_begin, v_end, blocks, a.H);
+            else role.template run<5>(v_begin, v_end, blocks, a.H);
             // no product is in flight when the tensor memory is given back
-            tc_commit(&c.drain);
-            if (!mbar_wait(&c.drain, 0)) ok = false;
-            if (!ok) c.err = 1;
+            if (leader) tc_commit(&c.drain[s]);
+            if (!mbar_wait(&c.drain[s], 0)) c.err = 1;
         }
         __syncwarp();
-    } else if (warp >= 4 && warp < 12) {
-        const uint32_t s = (warp - 4) / 4, quarter = warp & 3;
-        const uint32_t row = s * kSubV + quarter * 32 + lane;
-        const uint32_t a0 = tmem + (quarter << 21) + C::kACol + s * kABufs * kACols;
-        // 16-byte chunk ch of a 64-byte row lies at ch ^ ((row >> 1) & 3)
-        const uint32_t w0 = row * 64, sw = (row >> 1) & 3;
-        uint32_t it = 0, ac = 0;
-        for (uint32_t vt = v_begin; vt < v_end && ok; vt += kTileV) {
-            const bool active = s == 0 || v_end - vt > kSubV;
-            const uint8_t* z = a.zeros ? a.zeros + static_cast<uint64_t>(min(vt + row, a.V - 1)) * groups : nullptr;
-            for (uint32_t blk = 0; blk < blocks && ok; ++blk) {
-                for (uint32_t kt = 0; kt < ktiles; ++kt) {
-                    const uint32_t slot = it % C::kStages;
-                    if ((kt & 1) == 0) ok = __all_sync(kFull, mbar_wait(&c.full[slot], (it / C::kStages) & 1));
-                    if (!ok) break;
-                    const bool last = (kt & 1) || kt + 1 == ktiles;
-                    if (active) {
-                        const uint32_t buf = ac % kABufs;
-                        const unsigned char* src = ring + slot * C::kStageBytes + w0;
-                        const uint32_t ch = (kt & 1) * 2;
-                        const uint4 q0 = *reinterpret_cast<const uint4*>(src + ((ch ^ sw) << 4));
-                        const uint4 q1 = *reinterpret_cast<const uint4*>(src + (((ch + 1) ^ sw) << 4));
-                        uint32_t z0 = 8, z1 = 8;
-                        if (z) {
-                            const uint32_t g = kt * kTileK / a.group;
-                            z0 = z[g] & 15;
-                            z1 = a.group == 32 && g + 1 < groups ? z[g + 1] & 15 : z0;
-                        }
-                        const uint32_t zc0 = Unpack<T>::kMagic | z0 | (z0 << 16), zc1 = Unpack<T>::kMagic | z1 | (z1 << 16);
-                        uint32_t r[32];
-                        unpack8<T>(q0.x, zc0, r);
-                        unpack8<T>(q0.y, zc0, r + 4);
-                        unpack8<T>(q0.z, zc0, r + 8);
-                        unpack8<T>(q0.w, zc0, r + 12);
-                        unpack8<T>(q1.x, zc1, r + 16);
-                        unpack8<T>(q1.y, zc1, r + 20);
-                        unpack8<T>(q1.z, zc1, r + 24);
-                        unpack8<T>(q1.w, zc1, r + 28);
-                        ok = __all_sync(kFull, mbar_wait(&c.a_empty[s][buf], ((ac / kABufs) & 1) ^ 1));
-                        if (!ok) break;
-                        tc_fence_after();
-                        tmem_st32(a0 + buf * kACols, r);
-                        tmem_wait_st();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) arrive(&c.a_full[s][buf]);
-                        ++ac;
-                    }
-                    if (last) {
-                        __syncwarp();
-                        if (lane == 0) arrive(&c.empty[slot]);
-                        ++it;
-                    }
-                }
-            }
-        }
-        if (!ok) c.err = 1;
-    } else if (warp >= 12) {
-        const uint32_t s = (warp - 12) / 4, quarter = warp & 3;
-        const uint32_t row = s * kSubV + quarter * 32 + lane;
-        const uint32_t d0 = tmem + (quarter << 21) + s * kDBufs * N;
-        uint32_t dc = 0;
-        for (uint32_t vt = v_begin; vt < v_end && ok; vt += kTileV) {
-            if (s == 1 && v_end - vt <= kSubV) continue;
-            const T* sc = static_cast<const T*>(a.scales) + static_cast<uint64_t>(min(vt + row, a.V - 1)) * groups;
-            for (uint32_t blk = 0; blk < blocks && ok; ++blk) {
-                uint64_t acc[N / 2];
-#pragma unroll
-                for (int i = 0; i < N / 2; ++i) acc[i] = 0;
-                T next = sc[0];
-                for (uint32_t g = 0; g < groups; ++g, ++dc) {
-                    const uint32_t sf = __float_as_uint(to_f32(next));
-                    if (g + 1 < groups) next = sc[g + 1];
-                    uint64_t s2;
-                    asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "r"(sf));
-                    const uint32_t db = dc % kDBufs;
-                    ok = __all_sync(kFull, mbar_wait(&c.d_full[s][db], (dc / kDBufs) & 1));
-                    if (!ok) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int h = 0; h < N / 16; ++h) {
-                        uint32_t d[16];
-                        tmem_ld16(d0 + db * N + h * 16, d);
-                        tmem_wait_ld(d);
-                        if (h == N / 16 - 1) {  // the buffer is read
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) arrive(&c.d_empty[s][db]);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) fma2(acc[h * 8 + i], d[2 * i], d[2 * i + 1], s2);
-                    }
-                }
-                if (!ok) break;
-                if (vt + row < v_end) {
-                    O* out = static_cast<O*>(a.out) + static_cast<uint64_t>(blk) * N * a.ld + vt + row;
-                    const uint32_t n = min(static_cast<uint32_t>(N), a.rows - blk * N);
-#pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        const uint32_t bits = static_cast<uint32_t>(acc[i / 2] >> (32 * (i & 1)));
-                        if (static_cast<uint32_t>(i) < n) out[static_cast<uint64_t>(i) * a.ld] = from_f32<O>(__uint_as_float(bits));
-                    }
-                }
-            }
-        }
-        if (!ok) c.err = 1;
+    } else if (warp < kEpilogueWarp) {
+        regs_dec<kUnpackRegs>();
+        const uint32_t wg = (warp - kUnpackWarp) / 4, s = wg & 1, half = wg >> 1;
+        const UnpackRole<T, N> role{&c, ring, a.zeros, s, half, s * kSubV + quarter * 32 + lane,
+                                    tmem + (quarter << 21) + C::kACol + s * kABufs * kACols + half * (kACols / 2)};
+        if (!a.zeros) role.template run<false, 7>(v_begin, v_end, a.V, blocks, a.H);
+        else if (a.group_log2 == 7) role.template run<true, 7>(v_begin, v_end, a.V, blocks, a.H);
+        else if (a.group_log2 == 6) role.template run<true, 6>(v_begin, v_end, a.V, blocks, a.H);
+        else role.template run<true, 5>(v_begin, v_end, a.V, blocks, a.H);
+    } else {
+        regs_inc<kEpilogueRegs>();
+        const uint32_t s = (warp - kEpilogueWarp) / 4;
+        const EpilogueRole<T, O, N> role{&c, static_cast<const T*>(a.scales), static_cast<O*>(a.out), a.ld, a.rows, s,
+                                         s * kSubV + quarter * 32 + lane, tmem + (quarter << 21) + s * C::kDBufs * N};
+        if (a.group_log2 == 7) role.template run<7>(v_begin, v_end, a.V, blocks, a.H);
+        else if (a.group_log2 == 6) role.template run<6>(v_begin, v_end, a.V, blocks, a.H);
+        else role.template run<5>(v_begin, v_end, a.V, blocks, a.H);
     }
     tc_fence_before();
     __syncthreads();
@@ -475,14 +624,21 @@ sel_status launch(const HeadIn& in, const HeadArgs& args, cudaStream_t stream) {
     HeadArgs a = args;
     // every SM a run of whole weight copies, as even as 64 rows allow
     a.range = ceil_div(ceil_div(a.V, static_cast<uint64_t>(sms)), kBoxV) * kBoxV;
-    CUtensorMap mw, mx;
-    if (!make_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, in.q, a.H / 2, a.V, kStageK / 2, kBoxV,
+    CUtensorMap mt, mb, mx;
+    if (!make_map(&mt, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, in.q, a.H / 2, a.V, kStageK / 2, kTileV,
+                  CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !make_map(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, in.q, a.H / 2, a.V, kStageK / 2, kBoxV,
                   CU_TENSOR_MAP_SWIZZLE_64B) ||
         !make_map(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, in.x, a.H, a.rows, kTileK, N, CU_TENSOR_MAP_SWIZZLE_128B))
         return SEL_ECUDA;
-    if (!set_dynamic_smem(head_kernel<T, O, N>, Config<N>::kSmem)) return SEL_ECUDA;
+    // the split of the registers counts on what the launch has
+    static const bool regs_ok = [] {
+        cudaFuncAttributes f{};
+        return cudaFuncGetAttributes(&f, head_kernel<T, O, N>) == cudaSuccess && f.numRegs == kLaunchRegs;
+    }();
+    if (!regs_ok || !set_dynamic_smem(head_kernel<T, O, N>, Config<N>::kSmem)) return SEL_ECUDA;
     const cudaError_t e = launch_pdl(head_kernel<T, O, N>, dim3(ceil_div(a.V, a.range)), dim3(kNT), Config<N>::kSmem,
-                                     stream, mw, mx, a);
+                                     stream, mt, mb, mx, a);
     return e == cudaSuccess ? SEL_OK : SEL_ECUDA;
 }
 
@@ -526,7 +682,7 @@ extern "C" sel_status sel_head_w4(const void* d_hidden, uint32_t rows, const uin
     a.rows = rows;
     a.V = V;
     a.H = H;
-    a.group = group;
+    a.group_log2 = group == 32 ? 5 : group == 64 ? 6 : 7;
     const HeadIn in{d_hidden, d_q};
     return dtype == SEL_F16 ? launch_out<__half>(logits_dtype, in, a, stream)
                             : launch_out<__nv_bfloat16>(logits_dtype, in, a, stream);
