@@ -11,8 +11,8 @@
 // A persistent CTA per SM owns a run of matrix rows and walks it in tiles of
 // 256 (two subtiles of 128 TMEM lanes), each over all columns. Warp roles:
 //   warp 0        copies packed weights and hidden states into a ring of
-//                 shared-memory stages of 128 columns (TMA, swizzled)
-//   warps 4-19    unpack 64 columns of a row each: two 16-byte loads, nibbles
+//                 shared-memory stages of 256 columns (TMA, swizzled)
+//   warps 4-19    unpack 128 columns of a row each: four 16-byte loads, nibbles
 //                 to the type by placing them in the mantissa of 128 (bf16) or
 //                 1024 (f16) and subtracting 128 + z (1024 + z), both exact;
 //                 the tile goes to TMEM as the product's A operand
@@ -39,11 +39,12 @@ namespace {
 constexpr uint32_t kTileV = 256;     // matrix rows a tile
 constexpr uint32_t kSubV = 128;      // rows a subtile: TMEM lanes
 constexpr uint32_t kBoxV = 64;       // rows a weight copy
-constexpr uint32_t kStageK = 128;    // columns a stage
-constexpr uint32_t kTileK = 64;      // columns of a 128-byte row of hidden states
+constexpr uint32_t kStageK = 256;    // columns a stage
+constexpr uint32_t kUnitK = 128;     // columns an A buffer
+constexpr uint32_t kAtomK = 64;      // columns of a 128-byte row of hidden states
 constexpr uint32_t kWBytes = kTileV * kStageK / 2;
-constexpr uint32_t kABufs = 2;
-constexpr uint32_t kACols = kStageK / 2;  // TMEM columns of an A buffer
+constexpr uint32_t kABufs = kStageK / kUnitK;
+constexpr uint32_t kACols = kUnitK / 2;  // TMEM columns of an A buffer
 constexpr uint32_t kMaxStages = 10, kMaxDBufs = 4;
 
 // Warps: four of control, sixteen that unpack, eight of the epilogue; the
@@ -55,7 +56,7 @@ static_assert(4 * kControlRegs + 16 * kUnpackRegs + 8 * kEpilogueRegs <= 28 * kL
 template <int N>
 struct Config {
     static constexpr uint32_t kXAtom = N * 128;  // 64 columns of N hidden rows
-    static constexpr uint32_t kStageBytes = kWBytes + 2 * kXAtom;
+    static constexpr uint32_t kStageBytes = kWBytes + kStageK / kAtomK * kXAtom;
     static constexpr uint32_t kStages = 212 * 1024 / kStageBytes < kMaxStages ? 212 * 1024 / kStageBytes : kMaxStages;
     static constexpr uint32_t kSmem = kStages * kStageBytes + 1024;
     static constexpr uint32_t kDBufs = N > 32 ? 2 : kMaxDBufs;
@@ -251,8 +252,8 @@ struct MmaRole {
                                     (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(kSubV >> 4) << 24);
         constexpr uint32_t kHalves = (1u << kGroupLog2) / 32;  // pieces of 32 columns a group
         Ring<C::kStages> st;
-        Ring<kABufs> ar;
         Ring<C::kDBufs> dr;
+        uint32_t a_phase[kABufs] = {};
         for (uint32_t vt = v_begin; vt < v_end; vt += kTileV) {
             const bool active = s == 0 || v_end - vt > kSubV;
             for (uint32_t blk = 0; blk < blocks; ++blk) {
@@ -261,32 +262,35 @@ struct MmaRole {
                     // readers, so that no arrival runs ahead into the slot's next use
                     wait(&c->full[st.i], st.phase, &c->err);
                     if (active) {
-                        wait(&c->a_full[s][ar.i], ar.phase, &c->err);
-                        tc_fence_after();
                         const uint64_t b = smem_desc(smem_u32(ring + st.i * C::kStageBytes + kWBytes));
-                        const uint32_t at = a0 + ar.i * kACols;
                         const uint32_t left = H - k;
 #pragma unroll
-                        for (uint32_t h = 0; h < kStageK / 32; ++h) {
-                            if (h > 0 && h * 32 >= left) break;  // whole groups only
-                            if (h % kHalves == 0) {
-                                wait(&c->d_empty[s][dr.i], dr.phase ^ 1, &c->err);
-                                tc_fence_after();
+                        for (uint32_t u = 0; u < kABufs; ++u) {
+                            if (u > 0 && u * kUnitK >= left) break;
+                            wait(&c->a_full[s][u], a_phase[u], &c->err);
+                            a_phase[u] ^= 1;
+                            tc_fence_after();
+#pragma unroll
+                            for (uint32_t h = 0; h < kUnitK / 32; ++h) {
+                                const uint32_t col = u * kUnitK + h * 32;
+                                if (h > 0 && col >= left) break;  // whole groups only
+                                if (h % kHalves == 0) {
+                                    wait(&c->d_empty[s][dr.i], dr.phase ^ 1, &c->err);
+                                    tc_fence_after();
+                                }
+                                // 32 columns: two products
+                                const uint64_t bh = b + (col / kAtomK) * (C::kXAtom >> 4) + (col % kAtomK) / 8;
+                                const uint32_t at = a0 + u * kACols + h * 16;
+                                if (leader) {
+                                    tc_mma(d0 + dr.i * N, at, bh, kIdesc, h % kHalves != 0);
+                                    tc_mma(d0 + dr.i * N, at + 8, bh + 2, kIdesc, true);
+                                    if (h % kHalves == kHalves - 1) tc_commit(&c->d_full[s][dr.i]);
+                                }
+                                if (h % kHalves == kHalves - 1) dr.next();
                             }
-                            // 32 columns: two products; 64 columns of hidden states are an atom
-                            const uint64_t bh = b + (h / 2) * (C::kXAtom >> 4) + (h % 2) * 4;
-                            if (leader) {
-                                tc_mma(d0 + dr.i * N, at + h * 16, bh, kIdesc, h % kHalves != 0);
-                                tc_mma(d0 + dr.i * N, at + h * 16 + 8, bh + 2, kIdesc, true);
-                                if (h % kHalves == kHalves - 1) tc_commit(&c->d_full[s][dr.i]);
-                            }
-                            if (h % kHalves == kHalves - 1) dr.next();
+                            if (leader) tc_commit(&c->a_empty[s][u]);
                         }
-                        if (leader) {
-                            tc_commit(&c->a_empty[s][ar.i]);
-                            tc_commit(&c->empty[st.i]);
-                        }
-                        ar.next();
+                        if (leader) tc_commit(&c->empty[st.i]);
                     } else if (leader) {
                         arrive(&c->empty[st.i]);
                     }
@@ -297,14 +301,14 @@ struct MmaRole {
     }
 };
 
-// Entries kPer * stage .. + kPer - 1 of a row's group array (scales or zero
+// Entries kPer * unit .. + kPer - 1 of a row's group array (scales or zero
 // points), as raw bits in the low bytes; entries past the row's end are not
-// read. kPer entries of a stage are one load where they are aligned, which
+// read. The kPer entries of a unit are one load where they are aligned, which
 // the caller knows (`vec`).
 template <typename E, uint32_t kPer>
-__device__ __forceinline__ uint64_t group_entries(const E* row, uint32_t stage, uint32_t groups, bool vec) {
+__device__ __forceinline__ uint64_t group_entries(const E* row, uint32_t unit, uint32_t groups, bool vec) {
     constexpr uint32_t kBytes = kPer * sizeof(E);
-    const E* p = row + stage * kPer;
+    const E* p = row + unit * kPer;
     if (vec) {
         if constexpr (kBytes == 8) return *reinterpret_cast<const uint64_t*>(p);
         else if constexpr (kBytes == 4) return *reinterpret_cast<const uint32_t*>(p);
@@ -314,71 +318,76 @@ __device__ __forceinline__ uint64_t group_entries(const E* row, uint32_t stage, 
     uint64_t v = 0;
 #pragma unroll
     for (uint32_t i = 0; i < kPer; ++i)
-        if (stage * kPer + i < groups) v |= static_cast<uint64_t>(p[i]) << (8 * sizeof(E) * i);
+        if (unit * kPer + i < groups) v |= static_cast<uint64_t>(p[i]) << (8 * sizeof(E) * i);
     return v;
 }
 
-// Unpacks half (64 columns) of every stage for one subtile's 32 lanes.
+// Unpacks one unit of every stage for 32 lanes of a subtile, into the A buffer
+// of that unit.
 template <typename T, int N>
 struct UnpackRole {
     using C = Config<N>;
     Ctx* c;
     const unsigned char* ring;
     const uint8_t* zeros;
-    uint32_t s, half, row, a0;  // row: within the tile
+    uint32_t s, unit, row, a0;  // row: within the tile
 
     template <bool kZeros, int kGroupLog2>
     __device__ __forceinline__ void run(uint32_t v_begin, uint32_t v_end, uint32_t V, uint32_t blocks, uint32_t H) const {
-        constexpr uint32_t kPer = kStageK >> kGroupLog2;  // groups a stage
+        constexpr uint32_t kPer = kUnitK >> kGroupLog2;  // groups a unit
         const uint32_t lane = threadIdx.x & 31;
-        const uint32_t stages = (H + kStageK - 1) / kStageK, groups = H >> kGroupLog2;
-        // 16-byte chunk ch of a 64-byte row lies at ch ^ ((row >> 1) & 3)
-        const uint32_t sw = (row >> 1) & 3;
-        const unsigned char* src0 = ring + row * 64 + (((2 * half) ^ sw) << 4);
-        const unsigned char* src1 = ring + row * 64 + (((2 * half + 1) ^ sw) << 4);
-        const bool vec = kZeros && H % kStageK == 0 && reinterpret_cast<uintptr_t>(zeros) % kPer == 0;
+        const uint32_t units = (H + kUnitK - 1) / kUnitK, groups = H >> kGroupLog2;
+        // 16-byte chunk ch of a 128-byte row lies at ch ^ (row & 7)
+        const unsigned char* src = ring + row * (kStageK / 2);
+        const uint32_t ch = unit * 4, sw = row & 7;
+        const bool vec = kZeros && H % kUnitK == 0 && reinterpret_cast<uintptr_t>(zeros) % kPer == 0;
         Ring<C::kStages> st;
-        Ring<kABufs> ar;
+        uint32_t phase = 0;  // of this unit's A buffer
         for (uint32_t vt = v_begin; vt < v_end; vt += kTileV) {
             const bool active = s == 0 || v_end - vt > kSubV;
             const uint8_t* z = kZeros ? zeros + static_cast<uint64_t>(min(vt + row, V - 1)) * groups : nullptr;
             for (uint32_t blk = 0; blk < blocks; ++blk) {
                 uint32_t z_next = 0;
-                if (kZeros) z_next = static_cast<uint32_t>(group_entries<uint8_t, kPer>(z, 0, groups, vec));
-                for (uint32_t i = 0; i < stages; ++i) {
-                    uint32_t zc0 = Unpack<T>::kMagic | 0x00080008u, zc1 = zc0;
-                    if (kZeros) {
-                        // this stage's zero points, and the next one's on their way
-                        const uint32_t zs = z_next >> (kPer == 4 ? 16 * half : kPer == 2 ? 8 * half : 0);
-                        zc0 = Unpack<T>::kMagic | (zs & 15) * 0x00010001u;
-                        zc1 = kPer == 4 ? Unpack<T>::kMagic | ((zs >> 8) & 15) * 0x00010001u : zc0;
-                        if (i + 1 < stages) z_next = static_cast<uint32_t>(group_entries<uint8_t, kPer>(z, i + 1, groups, vec));
-                    }
+                if (kZeros) z_next = static_cast<uint32_t>(group_entries<uint8_t, kPer>(z, unit, groups, vec));
+                for (uint32_t i = unit; i < kABufs * ((units + kABufs - 1) / kABufs); i += kABufs) {
+                    const uint32_t zs = z_next;  // this unit's zero points, and the next one's on their way
+                    if (kZeros && i + kABufs < units)
+                        z_next = static_cast<uint32_t>(group_entries<uint8_t, kPer>(z, i + kABufs, groups, vec));
                     wait(&c->full[st.i], st.phase, &c->err);
-                    if (active) {
-                        const uint4 q0 = *reinterpret_cast<const uint4*>(src0 + st.i * C::kStageBytes);
-                        const uint4 q1 = *reinterpret_cast<const uint4*>(src1 + st.i * C::kStageBytes);
-                        uint32_t r[32];
-                        unpack8<T>(q0.x, zc0, r);
-                        unpack8<T>(q0.y, zc0, r + 4);
-                        unpack8<T>(q0.z, zc0, r + 8);
-                        unpack8<T>(q0.w, zc0, r + 12);
-                        unpack8<T>(q1.x, zc1, r + 16);
-                        unpack8<T>(q1.y, zc1, r + 20);
-                        unpack8<T>(q1.z, zc1, r + 24);
-                        unpack8<T>(q1.w, zc1, r + 28);
-                        wait(&c->a_empty[s][ar.i], ar.phase ^ 1, &c->err);
-                        tc_fence_after();
-                        tmem_st32(a0 + ar.i * kACols, r);
+                    const bool mine = active && i < units;  // the last stage may end before its second unit
+                    if (mine) {
+                        const unsigned char* p = src + st.i * C::kStageBytes;
+                        uint4 q[4];
+#pragma unroll
+                        for (uint32_t j = 0; j < 4; ++j) q[j] = *reinterpret_cast<const uint4*>(p + (((ch + j) ^ sw) << 4));
+#pragma unroll
+                        for (uint32_t h = 0; h < 2; ++h) {
+                            uint32_t r[32];
+#pragma unroll
+                            for (uint32_t j = 0; j < 2; ++j) {
+                                const uint32_t z1 = kZeros ? (zs >> (8 * ((2 * h + j) * 32 >> kGroupLog2))) & 15 : 8;
+                                const uint32_t zc = Unpack<T>::kMagic | z1 * 0x00010001u;
+                                const uint4 v = q[2 * h + j];
+                                unpack8<T>(v.x, zc, r + 16 * j);
+                                unpack8<T>(v.y, zc, r + 16 * j + 4);
+                                unpack8<T>(v.z, zc, r + 16 * j + 8);
+                                unpack8<T>(v.w, zc, r + 16 * j + 12);
+                            }
+                            if (h == 0) {
+                                wait(&c->a_empty[s][unit], phase ^ 1, &c->err);
+                                tc_fence_after();
+                            }
+                            tmem_st32(a0 + h * 32, r);
+                        }
                         tmem_wait_st();
                         tc_fence_before();
                     }
                     __syncwarp();
                     if (lane == 0) {
-                        if (active) arrive(&c->a_full[s][ar.i]);
+                        if (mine) arrive(&c->a_full[s][unit]);
                         arrive(&c->empty[st.i]);
                     }
-                    if (active) ar.next();
+                    if (mine) phase ^= 1;
                     st.next();
                 }
             }
@@ -398,11 +407,11 @@ struct EpilogueRole {
 
     template <int kGroupLog2>
     __device__ __forceinline__ void run(uint32_t v_begin, uint32_t v_end, uint32_t V, uint32_t blocks, uint32_t H) const {
-        constexpr uint32_t kPer = kStageK >> kGroupLog2;
+        constexpr uint32_t kPer = kUnitK >> kGroupLog2;
         constexpr uint32_t kLd = N < 32 ? N : 32;  // columns of D a load
         const uint32_t lane = threadIdx.x & 31;
-        const uint32_t stages = (H + kStageK - 1) / kStageK, groups = H >> kGroupLog2;
-        const bool vec = H % kStageK == 0 && reinterpret_cast<uintptr_t>(scales) % (2 * kPer) == 0;
+        const uint32_t units = (H + kUnitK - 1) / kUnitK, groups = H >> kGroupLog2;
+        const bool vec = H % kUnitK == 0 && reinterpret_cast<uintptr_t>(scales) % (2 * kPer) == 0;
         Ring<C::kDBufs> dr;
         for (uint32_t vt = v_begin; vt < v_end; vt += kTileV) {
             if (s == 1 && v_end - vt <= kSubV) continue;
@@ -413,9 +422,9 @@ struct EpilogueRole {
 #pragma unroll
                 for (int i = 0; i < N; ++i) acc[i] = 0.0f;
                 uint64_t s_next = group_entries<uint16_t, kPer>(sc, 0, groups, vec);
-                for (uint32_t st = 0; st < stages; ++st) {
+                for (uint32_t st = 0; st < units; ++st) {
                     const uint64_t s_now = s_next;
-                    if (st + 1 < stages) s_next = group_entries<uint16_t, kPer>(sc, st + 1, groups, vec);
+                    if (st + 1 < units) s_next = group_entries<uint16_t, kPer>(sc, st + 1, groups, vec);
 #pragma unroll
                     for (uint32_t g = 0; g < kPer; ++g) {
                         if (g > 0 && st * kPer + g >= groups) break;
@@ -469,7 +478,7 @@ __global__ void __launch_bounds__(kNT, 1)
         for (uint32_t s = 0; s < 2; ++s) {
             mbar_init(&c.drain[s], 1);
             for (uint32_t i = 0; i < kABufs; ++i) {
-                mbar_init(&c.a_full[s][i], 8);
+                mbar_init(&c.a_full[s][i], 4);
                 mbar_init(&c.a_empty[s][i], 1);
             }
             for (uint32_t i = 0; i < C::kDBufs; ++i) {
@@ -515,9 +524,9 @@ __global__ void __launch_bounds__(kNT, 1)
                         if (!ok) break;
                         unsigned char* dst = ring + st.i * C::kStageBytes;
                         uint64_t* full = &c.full[st.i];
-                        const bool two = i * kStageK + kTileK < a.H;
+                        const uint32_t atoms = min(kStageK / kAtomK, (a.H - i * kStageK + kAtomK - 1) / kAtomK);
                         if (leader) {
-                            expect_tx(full, boxes * kBoxV * (kStageK / 2) + (two ? 2 : 1) * C::kXAtom);
+                            expect_tx(full, boxes * kBoxV * (kStageK / 2) + atoms * C::kXAtom);
                             if (boxes == kTileV / kBoxV) {
                                 tma_2d(dst, &map_tile, i * (kStageK / 2), vt, full);
                             } else {
@@ -525,8 +534,8 @@ __global__ void __launch_bounds__(kNT, 1)
                                     tma_2d(dst + b * kBoxV * (kStageK / 2), &map_box, i * (kStageK / 2), vt + b * kBoxV,
                                            full);
                             }
-                            tma_2d(dst + kWBytes, &map_x, i * kStageK, blk * N, full);
-                            if (two) tma_2d(dst + kWBytes + C::kXAtom, &map_x, i * kStageK + kTileK, blk * N, full);
+                            for (uint32_t at = 0; at < atoms; ++at)
+                                tma_2d(dst + kWBytes + at * C::kXAtom, &map_x, i * kStageK + at * kAtomK, blk * N, full);
                         }
                         ++issued;
                         st.next();
@@ -552,9 +561,9 @@ __global__ void __launch_bounds__(kNT, 1)
         __syncwarp();
     } else if (warp < kEpilogueWarp) {
         regs_dec<kUnpackRegs>();
-        const uint32_t wg = (warp - kUnpackWarp) / 4, s = wg & 1, half = wg >> 1;
-        const UnpackRole<T, N> role{&c, ring, a.zeros, s, half, s * kSubV + quarter * 32 + lane,
-                                    tmem + (quarter << 21) + C::kACol + s * kABufs * kACols + half * (kACols / 2)};
+        const uint32_t wg = (warp - kUnpackWarp) / 4, s = wg & 1, unit = wg >> 1;
+        const UnpackRole<T, N> role{&c, ring, a.zeros, s, unit, s * kSubV + quarter * 32 + lane,
+                                    tmem + (quarter << 21) + C::kACol + (s * kABufs + unit) * kACols};
         if (!a.zeros) role.template run<false, 7>(v_begin, v_end, a.V, blocks, a.H);
         else if (a.group_log2 == 7) role.template run<true, 7>(v_begin, v_end, a.V, blocks, a.H);
         else if (a.group_log2 == 6) role.template run<true, 6>(v_begin, v_end, a.V, blocks, a.H);
@@ -626,10 +635,10 @@ sel_status launch(const HeadIn& in, const HeadArgs& args, cudaStream_t stream) {
     a.range = ceil_div(ceil_div(a.V, static_cast<uint64_t>(sms)), kBoxV) * kBoxV;
     CUtensorMap mt, mb, mx;
     if (!make_map(&mt, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, in.q, a.H / 2, a.V, kStageK / 2, kTileV,
-                  CU_TENSOR_MAP_SWIZZLE_64B) ||
+                  CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_map(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, in.q, a.H / 2, a.V, kStageK / 2, kBoxV,
-                  CU_TENSOR_MAP_SWIZZLE_64B) ||
-        !make_map(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, in.x, a.H, a.rows, kTileK, N, CU_TENSOR_MAP_SWIZZLE_128B))
+                  CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, in.x, a.H, a.rows, kAtomK, N, CU_TENSOR_MAP_SWIZZLE_128B))
         return SEL_ECUDA;
     // the split of the registers counts on what the launch has
     static const bool regs_ok = [] {
