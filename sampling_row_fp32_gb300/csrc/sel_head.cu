@@ -16,80 +16,52 @@
 //                 to the type by placing them in the mantissa of 128 (bf16) or
 //                 1024 (f16) and subtracting 128 + z (1024 + z), both exact;
 //                 the tile goes to TMEM as the product's A operand
+//   warp 3        brings the rows' scales and zero points (a ring of its own)
 //   warps 1, 2    issue the products of a subtile each (A from TMEM, B =
 //                 hidden states from shared memory, D in TMEM,
 //                 double-buffered by group)
 //   warps 20-27   read each group's D, add s * D to fp32 registers, and
 //                 write the logits after the last group
 // Every wait is bounded; one that runs out makes the CTA's logits NaN.
-#include <cuda.h>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_runtime.h>
+#include <type_traits>
 
-#include "sel.h"
-#include "sel_common.cuh"
-#include "sel_dtype.cuh"
-#include "sel_plan.h"
-#include "sel_units.cuh"
+#include "sel_head.cuh"
 
 namespace sel {
 namespace {
 
-constexpr uint32_t kTileV = 256;     // matrix rows a tile
 constexpr uint32_t kSubV = 128;      // rows a subtile: TMEM lanes
-constexpr uint32_t kBoxV = 64;       // rows a weight copy
-constexpr uint32_t kStageK = 256;    // columns a stage
-constexpr uint32_t kUnitK = 128;     // columns an A buffer
 constexpr uint32_t kAtomK = 64;      // columns of a 128-byte row of hidden states
-constexpr uint32_t kWBytes = kTileV * kStageK / 2;
 constexpr uint32_t kABufs = kStageK / kUnitK;
 constexpr uint32_t kACols = kUnitK / 2;  // TMEM columns of an A buffer
 constexpr uint32_t kMaxStages = 10, kMaxDBufs = 4;
 
 // Warps: four of control, sixteen that unpack, eight of the epilogue; the
-// registers of a launch (896 x 72) are split 40 / 56 / 120 between them.
+// registers of a launch (896 x 72) are split 56 / 56 / 112 between them.
 constexpr int kUnpackWarp = 4, kEpilogueWarp = 20, kNT = 32 * 28;
-constexpr int kLaunchRegs = 72, kControlRegs = 40, kUnpackRegs = 56, kEpilogueRegs = 120;
+constexpr int kLaunchRegs = 72, kControlRegs = 56, kUnpackRegs = 56, kEpilogueRegs = 112;
 static_assert(4 * kControlRegs + 16 * kUnpackRegs + 8 * kEpilogueRegs <= 28 * kLaunchRegs);
+
+// Group entries have a ring of their own: the epilogue reads a stage's scales
+// well after its weights' slot is free again.
+constexpr uint32_t kEntrySlots = 5, kEntryBytes = kTileV * (EntryBytes<5>::kScales + EntryBytes<5>::kZeros);
 
 template <int N>
 struct Config {
     static constexpr uint32_t kXAtom = N * 128;  // 64 columns of N hidden rows
     static constexpr uint32_t kStageBytes = kWBytes + kStageK / kAtomK * kXAtom;
-    static constexpr uint32_t kStages = 212 * 1024 / kStageBytes < kMaxStages ? 212 * 1024 / kStageBytes : kMaxStages;
-    static constexpr uint32_t kSmem = kStages * kStageBytes + 1024;
+    static constexpr uint32_t kStages = 196 * 1024 / kStageBytes < kMaxStages ? 196 * 1024 / kStageBytes : kMaxStages;
+    static constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + kEntrySlots * kEntryBytes;
+    static_assert(kSmem + 1024 <= 227 * 1024);
     static constexpr uint32_t kDBufs = N > 32 ? 2 : kMaxDBufs;
     static constexpr uint32_t kACol = 2 * kDBufs * N;  // A buffers lie behind the D buffers
     static_assert(kACol + 2 * kABufs * kACols <= 512);
-};
-
-struct HeadArgs {
-    const void* scales;
-    const uint8_t* zeros;
-    void* out;
-    uint64_t ld;
-    uint32_t rows, V, H, group_log2;
-    uint32_t range;  // matrix rows a CTA
 };
 
 // ---------------------------------------------------------------------------
 // tensor memory and tensor core primitives
 // ---------------------------------------------------------------------------
 
-__device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-            smem_u32(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
-        : "memory");
-}
-__device__ __forceinline__ void expect_tx(uint64_t* bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void arrive(uint64_t* bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 // The barrier completes once every product issued before by this thread has.
@@ -143,29 +115,6 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t addr) {
            (1ull << 46) | (2ull << 61);
 }
 
-template <typename T>
-struct Unpack;
-template <>
-struct Unpack<__nv_bfloat16> {
-    static constexpr uint32_t kMagic = 0x43004300u;  // 128: the mantissa's last bit is 1
-    static constexpr uint32_t kType = 1;
-    static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
-        uint32_t r;
-        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-        return r;
-    }
-};
-template <>
-struct Unpack<__half> {
-    static constexpr uint32_t kMagic = 0x64006400u;  // 1024
-    static constexpr uint32_t kType = 0;
-    static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
-        uint32_t r;
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-        return r;
-    }
-};
-
 // Eight nibbles to four pairs (columns 2 i, 2 i + 1) of q - z: byte i of the
 // word and of the word shifted by a nibble into the pair's halves, the low
 // nibble of each placed in the magic number, one subtraction.
@@ -184,42 +133,8 @@ __device__ __forceinline__ void unpack8(uint32_t w, uint32_t zc, uint32_t* r) {
     }
 }
 
-// A slot of a ring of barriers and the parity of the round it is in.
-template <uint32_t kN>
-struct Ring {
-    uint32_t i = 0, phase = 0;
-    __device__ __forceinline__ void next() {
-        if (++i == kN) {
-            i = 0;
-            phase ^= 1;
-        }
-    }
-};
-
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xFFFFFFFF;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(p));
-    return p != 0;
-}
-
-// Waits for a barrier's phase. A wait that runs out raises `err`, and with
-// `err` raised every other one returns at once: the roles then run to their
-// ends on whatever the buffers hold (in bounds as ever) and the CTA's logits
-// become NaN.
-__device__ __forceinline__ void wait_slow(uint64_t* bar, uint32_t phase, volatile uint32_t* err) {
-    for (uint32_t i = 0; i < kWaitPolls; ++i) {
-        if (mbar_try_wait(bar, phase) || *err) return;
-    }
-    *err = 1;
-}
-__device__ __forceinline__ void wait(uint64_t* bar, uint32_t phase, uint32_t* err) {
-    if (!mbar_try_wait(bar, phase)) wait_slow(bar, phase, err);
-    __syncwarp();
-}
+template <int k>
+using Log2 = std::integral_constant<int, k>;
 
 template <int kRegs>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
@@ -230,6 +145,7 @@ struct Ctx {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t a_full[2][kABufs], a_empty[2][kABufs];
     uint64_t d_full[2][kMaxDBufs], d_empty[2][kMaxDBufs];
+    uint64_t e_full[kEntrySlots], e_empty[kEntrySlots];
     uint64_t drain[2];
     uint32_t tmem;
     uint32_t err;
@@ -301,27 +217,6 @@ struct MmaRole {
     }
 };
 
-// Entries kPer * unit .. + kPer - 1 of a row's group array (scales or zero
-// points), as raw bits in the low bytes; entries past the row's end are not
-// read. The kPer entries of a unit are one load where they are aligned, which
-// the caller knows (`vec`).
-template <typename E, uint32_t kPer>
-__device__ __forceinline__ uint64_t group_entries(const E* row, uint32_t unit, uint32_t groups, bool vec) {
-    constexpr uint32_t kBytes = kPer * sizeof(E);
-    const E* p = row + unit * kPer;
-    if (vec) {
-        if constexpr (kBytes == 8) return *reinterpret_cast<const uint64_t*>(p);
-        else if constexpr (kBytes == 4) return *reinterpret_cast<const uint32_t*>(p);
-        else if constexpr (kBytes == 2) return *reinterpret_cast<const uint16_t*>(p);
-        else return *reinterpret_cast<const uint8_t*>(p);
-    }
-    uint64_t v = 0;
-#pragma unroll
-    for (uint32_t i = 0; i < kPer; ++i)
-        if (unit * kPer + i < groups) v |= static_cast<uint64_t>(p[i]) << (8 * sizeof(E) * i);
-    return v;
-}
-
 // Unpacks one unit of every stage for 32 lanes of a subtile, into the A buffer
 // of that unit.
 template <typename T, int N>
@@ -329,32 +224,34 @@ struct UnpackRole {
     using C = Config<N>;
     Ctx* c;
     const unsigned char* ring;
-    const uint8_t* zeros;
+    uint32_t entries;  // shared memory address
     uint32_t s, unit, row, a0;  // row: within the tile
 
     template <bool kZeros, int kGroupLog2>
-    __device__ __forceinline__ void run(uint32_t v_begin, uint32_t v_end, uint32_t V, uint32_t blocks, uint32_t H) const {
-        constexpr uint32_t kPer = kUnitK >> kGroupLog2;  // groups a unit
+    __device__ __forceinline__ void run(uint32_t v_begin, uint32_t v_end, uint32_t blocks, uint32_t H) const {
+        using B = EntryBytes<kGroupLog2>;
         const uint32_t lane = threadIdx.x & 31;
-        const uint32_t units = (H + kUnitK - 1) / kUnitK, groups = H >> kGroupLog2;
-        // 16-byte chunk ch of a 128-byte row lies at ch ^ (row & 7)
+        // 16-byte chunk ch of a row lies at ch ^ (row & 7)
         const unsigned char* src = ring + row * (kStageK / 2);
         const uint32_t ch = unit * 4, sw = row & 7;
-        const bool vec = kZeros && H % kUnitK == 0 && reinterpret_cast<uintptr_t>(zeros) % kPer == 0;
+        const uint32_t ez = entries + kTileV * B::kScales + row * B::kZeros;
         Ring<C::kStages> st;
+        Ring<kEntrySlots> er;
         uint32_t phase = 0;  // of this unit's A buffer
         for (uint32_t vt = v_begin; vt < v_end; vt += kTileV) {
             const bool active = s == 0 || v_end - vt > kSubV;
-            const uint8_t* z = kZeros ? zeros + static_cast<uint64_t>(min(vt + row, V - 1)) * groups : nullptr;
             for (uint32_t blk = 0; blk < blocks; ++blk) {
-                uint32_t z_next = 0;
-                if (kZeros) z_next = static_cast<uint32_t>(group_entries<uint8_t, kPer>(z, unit, groups, vec));
-                for (uint32_t i = unit; i < kABufs * ((units + kABufs - 1) / kABufs); i += kABufs) {
-                    const uint32_t zs = z_next;  // this unit's zero points, and the next one's on their way
-                    if (kZeros && i + kABufs < units)
-                        z_next = static_cast<uint32_t>(group_entries<uint8_t, kPer>(z, i + kABufs, groups, vec));
+                for (uint32_t k = 0; k < H; k += kStageK) {
+                    uint32_t zs = 0;  // the unit's zero points
+                    if (kZeros) {
+                        uint32_t v[(B::kZeros + 3) / 4];
+                        wait(&c->e_full[er.i], er.phase, &c->err);
+                        read_entries<B::kZeros>(ez + er.i * kEntryBytes, v);
+                        if constexpr (kGroupLog2 == 5) zs = unit ? v[1] : v[0];
+                        else zs = v[0] >> (unit * (B::kZeros / 2) * 8);
+                    }
                     wait(&c->full[st.i], st.phase, &c->err);
-                    const bool mine = active && i < units;  // the last stage may end before its second unit
+                    const bool mine = active && k + unit * kUnitK < H;  // the last stage may end before its second unit
                     if (mine) {
                         const unsigned char* p = src + st.i * C::kStageBytes;
                         uint4 q[4];
@@ -386,9 +283,11 @@ struct UnpackRole {
                     if (lane == 0) {
                         if (mine) arrive(&c->a_full[s][unit]);
                         arrive(&c->empty[st.i]);
+                        if (kZeros) arrive(&c->e_empty[er.i]);
                     }
                     if (mine) phase ^= 1;
                     st.next();
+                    er.next();
                 }
             }
         }
@@ -400,35 +299,37 @@ template <typename T, typename O, int N>
 struct EpilogueRole {
     using C = Config<N>;
     Ctx* c;
-    const T* scales;
+    uint32_t entries;  // shared memory address
     O* out;
     uint64_t ld;
     uint32_t rows, s, row, d0;
 
     template <int kGroupLog2>
-    __device__ __forceinline__ void run(uint32_t v_begin, uint32_t v_end, uint32_t V, uint32_t blocks, uint32_t H) const {
-        constexpr uint32_t kPer = kUnitK >> kGroupLog2;
+    __device__ __forceinline__ void run(uint32_t v_begin, uint32_t v_end, uint32_t blocks, uint32_t H) const {
+        using B = EntryBytes<kGroupLog2>;
         constexpr uint32_t kLd = N < 32 ? N : 32;  // columns of D a load
         const uint32_t lane = threadIdx.x & 31;
-        const uint32_t units = (H + kUnitK - 1) / kUnitK, groups = H >> kGroupLog2;
-        const bool vec = H % kUnitK == 0 && reinterpret_cast<uintptr_t>(scales) % (2 * kPer) == 0;
+        const uint32_t es = entries + row * B::kScales;
         Ring<C::kDBufs> dr;
+        Ring<kEntrySlots> er;
         for (uint32_t vt = v_begin; vt < v_end; vt += kTileV) {
-            if (s == 1 && v_end - vt <= kSubV) continue;
-            const uint16_t* sc =
-                reinterpret_cast<const uint16_t*>(scales) + static_cast<uint64_t>(min(vt + row, V - 1)) * groups;
+            const bool active = s == 0 || v_end - vt > kSubV;
             for (uint32_t blk = 0; blk < blocks; ++blk) {
                 float acc[N];
 #pragma unroll
                 for (int i = 0; i < N; ++i) acc[i] = 0.0f;
-                uint64_t s_next = group_entries<uint16_t, kPer>(sc, 0, groups, vec);
-                for (uint32_t st = 0; st < units; ++st) {
-                    const uint64_t s_now = s_next;
-                    if (st + 1 < units) s_next = group_entries<uint16_t, kPer>(sc, st + 1, groups, vec);
+                for (uint32_t k = 0; k < H; k += kStageK) {
+                    uint32_t sc[B::kScales / 4];
+                    wait(&c->e_full[er.i], er.phase, &c->err);
+                    read_entries<B::kScales>(es + er.i * kEntryBytes, sc);
+                    __syncwarp();
+                    if (lane == 0) arrive(&c->e_empty[er.i]);
+                    er.next();
+                    if (!active) continue;
 #pragma unroll
-                    for (uint32_t g = 0; g < kPer; ++g) {
-                        if (g > 0 && st * kPer + g >= groups) break;
-                        const float sf = bits_f32<T>(static_cast<uint16_t>(s_now >> (16 * g)));
+                    for (uint32_t g = 0; g < B::kGroups; ++g) {
+                        if (g > 0 && k + (g << kGroupLog2) >= H) break;
+                        const float sf = bits_f32<T>(entry16(sc, g));
                         wait(&c->d_full[s][dr.i], dr.phase, &c->err);
                         tc_fence_after();
 #pragma unroll
@@ -447,7 +348,7 @@ struct EpilogueRole {
                         dr.next();
                     }
                 }
-                if (vt + row < v_end) {
+                if (active && vt + row < v_end) {
                     O* o = out + static_cast<uint64_t>(blk) * N * ld + vt + row;
                     const uint32_t n = rows - blk * N;
 #pragma unroll
@@ -466,6 +367,7 @@ __global__ void __launch_bounds__(kNT, 1)
     using C = Config<N>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    unsigned char* entries = ring + C::kStages * C::kStageBytes;
     __shared__ Ctx c;
     // (broadcasts: the compiler then keeps what follows from them in uniform registers)
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFull, tid >> 5, 0);
@@ -485,6 +387,10 @@ __global__ void __launch_bounds__(kNT, 1)
                 mbar_init(&c.d_full[s][i], 1);
                 mbar_init(&c.d_empty[s][i], 4);
             }
+        }
+        for (uint32_t i = 0; i < kEntrySlots; ++i) {
+            mbar_init(&c.e_full[i], 1);
+            mbar_init(&c.e_empty[i], 8 + (a.zeros ? 16 : 0));  // the epilogue's warps, and the unpacking ones
         }
         c.err = 0;
     }
@@ -557,25 +463,39 @@ __global__ void __launch_bounds__(kNT, 1)
             // no product is in flight when the tensor memory is given back
             if (leader) tc_commit(&c.drain[s]);
             if (!mbar_wait(&c.drain[s], 0)) c.err = 1;
+        } else {
+            auto copy = [&](auto log2, auto zeros) {
+                copy_entries<decltype(log2)::value, decltype(zeros)::value, kTileV / 32>(
+                    a, entries, kEntryBytes, kTileV, kEntrySlots, blocks, 0, 1, v_begin, v_end,
+                    [&](uint32_t slot, uint32_t phase) { wait(&c.e_empty[slot], phase ^ 1, &c.err); },
+                    [&](uint32_t slot) {
+                        if (lane == 0) arrive(&c.e_full[slot]);
+                    });
+            };
+            using Yes = std::true_type;
+            using No = std::false_type;
+            if (a.group_log2 == 7) a.zeros ? copy(Log2<7>{}, Yes{}) : copy(Log2<7>{}, No{});
+            else if (a.group_log2 == 6) a.zeros ? copy(Log2<6>{}, Yes{}) : copy(Log2<6>{}, No{});
+            else a.zeros ? copy(Log2<5>{}, Yes{}) : copy(Log2<5>{}, No{});
         }
         __syncwarp();
     } else if (warp < kEpilogueWarp) {
         regs_dec<kUnpackRegs>();
         const uint32_t wg = (warp - kUnpackWarp) / 4, s = wg & 1, unit = wg >> 1;
-        const UnpackRole<T, N> role{&c, ring, a.zeros, s, unit, s * kSubV + quarter * 32 + lane,
+        const UnpackRole<T, N> role{&c, ring, smem_u32(entries), s, unit, s * kSubV + quarter * 32 + lane,
                                     tmem + (quarter << 21) + C::kACol + (s * kABufs + unit) * kACols};
-        if (!a.zeros) role.template run<false, 7>(v_begin, v_end, a.V, blocks, a.H);
-        else if (a.group_log2 == 7) role.template run<true, 7>(v_begin, v_end, a.V, blocks, a.H);
-        else if (a.group_log2 == 6) role.template run<true, 6>(v_begin, v_end, a.V, blocks, a.H);
-        else role.template run<true, 5>(v_begin, v_end, a.V, blocks, a.H);
+        if (!a.zeros) role.template run<false, 7>(v_begin, v_end, blocks, a.H);
+        else if (a.group_log2 == 7) role.template run<true, 7>(v_begin, v_end, blocks, a.H);
+        else if (a.group_log2 == 6) role.template run<true, 6>(v_begin, v_end, blocks, a.H);
+        else role.template run<true, 5>(v_begin, v_end, blocks, a.H);
     } else {
         regs_inc<kEpilogueRegs>();
         const uint32_t s = (warp - kEpilogueWarp) / 4;
-        const EpilogueRole<T, O, N> role{&c, static_cast<const T*>(a.scales), static_cast<O*>(a.out), a.ld, a.rows, s,
+        const EpilogueRole<T, O, N> role{&c, smem_u32(entries), static_cast<O*>(a.out), a.ld, a.rows, s,
                                          s * kSubV + quarter * 32 + lane, tmem + (quarter << 21) + s * C::kDBufs * N};
-        if (a.group_log2 == 7) role.template run<7>(v_begin, v_end, a.V, blocks, a.H);
-        else if (a.group_log2 == 6) role.template run<6>(v_begin, v_end, a.V, blocks, a.H);
-        else role.template run<5>(v_begin, v_end, a.V, blocks, a.H);
+        if (a.group_log2 == 7) role.template run<7>(v_begin, v_end, blocks, a.H);
+        else if (a.group_log2 == 6) role.template run<6>(v_begin, v_end, blocks, a.H);
+        else role.template run<5>(v_begin, v_end, blocks, a.H);
     }
     tc_fence_before();
     __syncthreads();
@@ -592,52 +512,14 @@ __global__ void __launch_bounds__(kNT, 1)
 // host side
 // ---------------------------------------------------------------------------
 
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled() {
-    static const EncodeTiled f = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult r{};
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-            r != cudaDriverEntryPointSuccess) {
-            (void)cudaGetLastError();
-            p = nullptr;
-        }
-        return reinterpret_cast<EncodeTiled>(p);
-    }();
-    return f;
-}
-
-// A row-major matrix [rows][cols] read in boxes of box_cols x box_rows.
-bool make_map(CUtensorMap* map, CUtensorMapDataType type, uint32_t elem, const void* base, uint64_t cols, uint64_t rows,
-              uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle swizzle) {
-    const EncodeTiled f = encode_tiled();
-    if (!f) return false;
-    const cuuint64_t dims[2] = {cols, rows}, strides[1] = {cols * elem};
-    const cuuint32_t box[2] = {box_cols, box_rows}, step[2] = {1, 1};
-    return f(map, type, 2, const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-struct HeadIn {
-    const void* x;
-    const void* q;
-};
-
 template <typename T, typename O, int N>
 sel_status launch(const HeadIn& in, const HeadArgs& args, cudaStream_t stream) {
     const int sms = device_sms();
     if (sms <= 0) return SEL_ECUDA;
     HeadArgs a = args;
-    // every SM a run of whole weight copies, as even as 64 rows allow
-    a.range = ceil_div(ceil_div(a.V, static_cast<uint64_t>(sms)), kBoxV) * kBoxV;
+    a.range = head_range(a.V, sms);
     CUtensorMap mt, mb, mx;
-    if (!make_map(&mt, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, in.q, a.H / 2, a.V, kStageK / 2, kTileV,
-                  CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_map(&mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, in.q, a.H / 2, a.V, kStageK / 2, kBoxV,
-                  CU_TENSOR_MAP_SWIZZLE_128B) ||
+    if (!make_weight_map(&mt, in.q, a.V, a.H, kTileV) || !make_weight_map(&mb, in.q, a.V, a.H, kBoxV) ||
         !make_map(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, in.x, a.H, a.rows, kAtomK, N, CU_TENSOR_MAP_SWIZZLE_128B))
         return SEL_ECUDA;
     // the split of the registers counts on what the launch has
@@ -693,6 +575,7 @@ extern "C" sel_status sel_head_w4(const void* d_hidden, uint32_t rows, const uin
     a.H = H;
     a.group_log2 = group == 32 ? 5 : group == 64 ? 6 : 7;
     const HeadIn in{d_hidden, d_q};
+    if (head_few_fits(rows, H)) return head_few(dtype, logits_dtype, in, a, stream);
     return dtype == SEL_F16 ? launch_out<__half>(logits_dtype, in, a, stream)
                             : launch_out<__nv_bfloat16>(logits_dtype, in, a, stream);
 }

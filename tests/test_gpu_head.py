@@ -32,7 +32,7 @@ def tolerance(mag, want, group, H, out):
     roundings lie on a term's way, each at most a whole fp32 step (2^-23, as a
     truncating accumulator gives) of a sum no larger than the terms'
     magnitudes; then one rounding to the output type."""
-    acc = (group + H // group + 2) * 2.0 ** -23 * mag
+    acc = (group + H // group + 2) * 2.0 ** -23 * mag + 2.0 ** -126  # (fp32's smallest normal)
     eps = torch.finfo(DT[out]).eps / 2
     return acc + eps * (np.abs(want) + acc) + torch.finfo(DT[out]).smallest_normal * eps
 
@@ -67,7 +67,8 @@ def test_output_types_and_strides(out, ld):
     check(*make(3, 5, 1031, 512, 64, "nibble", "bf16"), 64, out, ld)
 
 
-@pytest.mark.parametrize("rows,V,H,group", [(1, 20_011, 4096, 128), (49, 20_011, 4096, 64), (64, 9_999, 8192, 32), (7, 40_000, 2880, 32)])
+@pytest.mark.parametrize("rows,V,H,group", [(8, 30_011, 8192, 64), (16, 30_011, 4096, 32), (13, 20_011, 4096, 128),
+                                            (1, 20_011, 4096, 128), (49, 20_011, 4096, 64), (64, 9_999, 8192, 32), (7, 40_000, 2880, 32)])
 def test_model_widths(rows, V, H, group):
     check(*make(rows, rows, V, H, group, None, "bf16"), group)
 
@@ -85,6 +86,29 @@ def test_every_nibble_at_every_place():
     logits = check(x, torch.from_numpy(q), s, z, 64)
     want = torch.tensor([(v % 16) * (v % H + 1) for v in range(V)], dtype=torch.float32)
     assert torch.equal(logits[0].cpu(), want)
+
+
+@pytest.mark.parametrize("rows", [1, 5, 12])
+@pytest.mark.parametrize("low", [1e-3, 1e-9, 1e-30, 1e-40])
+def test_hidden_states_of_a_wide_range(rows, low):
+    """Values from `low` to 1e30 in one row, most of the weights of the large
+    ones zero, so that the small ones decide: nothing of them may get lost."""
+    x, q, s, z = make(rows, rows, 700, 512, 64, None, "bf16")
+    rng = np.random.default_rng(1)
+    big = torch.from_numpy(rng.random(x.shape) < 0.05)
+    x = torch.where(big, x.float() * 1e30, x.float() * low).bfloat16()
+    cols = big.any(0).numpy().nonzero()[0]
+    qn = q.numpy()
+    for k in cols:  # nibble 8: weight 0
+        qn[:600, k // 2] = (qn[:600, k // 2] & (0xF0 if k % 2 == 0 else 0x0F)) | (8 << (4 * (k % 2)))
+    check(x, q, s, z, 64)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -130, 2.0 ** -100, 2.0 ** 100, 2.0 ** 122])
+def test_hidden_states_at_the_ends_of_bf16(scale):
+    x, q, s, z = make(2, 3, 300, 256, 128, "nibble", "bf16")
+    x[1] = 0
+    check((x.double() * scale).bfloat16(), q, s, z, 128)
 
 
 def test_no_rows():
