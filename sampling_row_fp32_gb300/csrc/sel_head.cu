@@ -34,7 +34,7 @@ constexpr uint32_t kSubV = 128;      // rows a subtile: TMEM lanes
 constexpr uint32_t kAtomK = 64;      // columns of a 128-byte row of hidden states
 constexpr uint32_t kABufs = kStageK / kUnitK;
 constexpr uint32_t kACols = kUnitK / 2;  // TMEM columns of an A buffer
-constexpr uint32_t kMaxStages = 10, kMaxDBufs = 4;
+constexpr uint32_t kMaxStages = 10, kDBufs = 2;
 
 // Warps: four of control, sixteen that unpack, eight of the epilogue; the
 // registers of a launch (896 x 72) are split 56 / 56 / 112 between them.
@@ -53,8 +53,9 @@ struct Config {
     static constexpr uint32_t kStages = 196 * 1024 / kStageBytes < kMaxStages ? 196 * 1024 / kStageBytes : kMaxStages;
     static constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + kEntrySlots * kEntryBytes;
     static_assert(kSmem + 1024 <= 227 * 1024);
-    static constexpr uint32_t kDBufs = N > 32 ? 2 : kMaxDBufs;
-    static constexpr uint32_t kACol = 2 * kDBufs * N;  // A buffers lie behind the D buffers
+    // A D buffer's 64 columns hold up to 64 / N groups, handed over together.
+    static constexpr uint32_t kBatch = 64 / N;
+    static constexpr uint32_t kACol = 2 * kDBufs * 64;  // A buffers lie behind the D buffers
     static_assert(kACol + 2 * kABufs * kACols <= 512);
 };
 
@@ -144,7 +145,7 @@ __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.a
 struct Ctx {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t a_full[2][kABufs], a_empty[2][kABufs];
-    uint64_t d_full[2][kMaxDBufs], d_empty[2][kMaxDBufs];
+    uint64_t d_full[2][kDBufs], d_empty[2][kDBufs];
     uint64_t e_full[kEntrySlots], e_empty[kEntrySlots];
     uint64_t drain[2];
     uint32_t tmem;
@@ -166,9 +167,11 @@ struct MmaRole {
     __device__ __forceinline__ void run(uint32_t v_begin, uint32_t v_end, uint32_t blocks, uint32_t H) const {
         constexpr uint32_t kIdesc = (1u << 4) | (Unpack<T>::kType << 7) | (Unpack<T>::kType << 10) |
                                     (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(kSubV >> 4) << 24);
-        constexpr uint32_t kHalves = (1u << kGroupLog2) / 32;  // pieces of 32 columns a group
+        constexpr uint32_t kPieces = (1u << kGroupLog2) / 32;  // pieces of 32 columns a group
+        constexpr uint32_t kGroups = kUnitK >> kGroupLog2;     // groups a unit
+        constexpr uint32_t kBatch = (C::kBatch < kGroups ? C::kBatch : kGroups) * kPieces;  // pieces a D buffer
         Ring<C::kStages> st;
-        Ring<C::kDBufs> dr;
+        Ring<kDBufs> dr;
         uint32_t a_phase[kABufs] = {};
         for (uint32_t vt = v_begin; vt < v_end; vt += kTileV) {
             const bool active = s == 0 || v_end - vt > kSubV;
@@ -190,19 +193,22 @@ struct MmaRole {
                             for (uint32_t h = 0; h < kUnitK / 32; ++h) {
                                 const uint32_t col = u * kUnitK + h * 32;
                                 if (h > 0 && col >= left) break;  // whole groups only
-                                if (h % kHalves == 0) {
+                                if (h % kBatch == 0) {
                                     wait(&c->d_empty[s][dr.i], dr.phase ^ 1, &c->err);
                                     tc_fence_after();
                                 }
                                 // 32 columns: two products
                                 const uint64_t bh = b + (col / kAtomK) * (C::kXAtom >> 4) + (col % kAtomK) / 8;
                                 const uint32_t at = a0 + u * kACols + h * 16;
+                                const uint32_t d = d0 + dr.i * 64 + h % kBatch / kPieces * N;
                                 if (leader) {
-                                    tc_mma(d0 + dr.i * N, at, bh, kIdesc, h % kHalves != 0);
-                                    tc_mma(d0 + dr.i * N, at + 8, bh + 2, kIdesc, true);
-                                    if (h % kHalves == kHalves - 1) tc_commit(&c->d_full[s][dr.i]);
+                                    tc_mma(d, at, bh, kIdesc, h % kPieces != 0);
+                                    tc_mma(d, at + 8, bh + 2, kIdesc, true);
                                 }
-                                if (h % kHalves == kHalves - 1) dr.next();
+                                if (h % kBatch == kBatch - 1 || col + 32 >= left) {
+                                    if (leader) tc_commit(&c->d_full[s][dr.i]);
+                                    dr.next();
+                                }
                             }
                             if (leader) tc_commit(&c->a_empty[s][u]);
                         }
@@ -308,9 +314,11 @@ struct EpilogueRole {
     __device__ __forceinline__ void run(uint32_t v_begin, uint32_t v_end, uint32_t blocks, uint32_t H) const {
         using B = EntryBytes<kGroupLog2>;
         constexpr uint32_t kLd = N < 32 ? N : 32;  // columns of D a load
+        constexpr uint32_t kPer = kUnitK >> kGroupLog2;
+        constexpr uint32_t kBatch = C::kBatch < kPer ? C::kBatch : kPer;  // groups a D buffer
         const uint32_t lane = threadIdx.x & 31;
         const uint32_t es = entries + row * B::kScales;
-        Ring<C::kDBufs> dr;
+        Ring<kDBufs> dr;
         Ring<kEntrySlots> er;
         for (uint32_t vt = v_begin; vt < v_end; vt += kTileV) {
             const bool active = s == 0 || v_end - vt > kSubV;
@@ -327,23 +335,26 @@ struct EpilogueRole {
                     er.next();
                     if (!active) continue;
 #pragma unroll
-                    for (uint32_t g = 0; g < B::kGroups; ++g) {
-                        if (g > 0 && k + (g << kGroupLog2) >= H) break;
-                        const float sf = bits_f32<T>(entry16(sc, g));
+                    for (uint32_t g0 = 0; g0 < B::kGroups; g0 += kBatch) {
+                        if (g0 > 0 && k + (g0 << kGroupLog2) >= H) break;
                         wait(&c->d_full[s][dr.i], dr.phase, &c->err);
                         tc_fence_after();
 #pragma unroll
-                        for (uint32_t h = 0; h < N / kLd; ++h) {
+                        for (uint32_t h = 0; h < kBatch * N / kLd; ++h) {
+                            // columns h kLd .. of the buffer: of group g, from hidden row r
+                            const uint32_t g = g0 + h * kLd / N, r = h * kLd % N;
+                            const float sf = bits_f32<T>(entry16(sc, g));
                             uint32_t d[kLd];
-                            tmem_ld(d0 + dr.i * N + h * kLd, d);
-                            if (h == N / kLd - 1) {  // the buffer is read
+                            tmem_ld(d0 + dr.i * 64 + h * kLd, d);
+                            if (h == kBatch * N / kLd - 1) {  // the buffer is read
                                 tc_fence_before();
                                 __syncwarp();
                                 if (lane == 0) arrive(&c->d_empty[s][dr.i]);
                             }
+                            if (g == 0 || k + (g << kGroupLog2) < H) {  // (the last batch may be short)
 #pragma unroll
-                            for (uint32_t i = 0; i < kLd; ++i)
-                                acc[h * kLd + i] = fmaf(sf, __uint_as_float(d[i]), acc[h * kLd + i]);
+                                for (uint32_t i = 0; i < kLd; ++i) acc[r + i] = fmaf(sf, __uint_as_float(d[i]), acc[r + i]);
+                            }
                         }
                         dr.next();
                     }
@@ -383,7 +394,7 @@ __global__ void __launch_bounds__(kNT, 1)
                 mbar_init(&c.a_full[s][i], 4);
                 mbar_init(&c.a_empty[s][i], 1);
             }
-            for (uint32_t i = 0; i < C::kDBufs; ++i) {
+            for (uint32_t i = 0; i < kDBufs; ++i) {
                 mbar_init(&c.d_full[s][i], 1);
                 mbar_init(&c.d_empty[s][i], 4);
             }
@@ -456,7 +467,7 @@ __global__ void __launch_bounds__(kNT, 1)
             }
         } else if (warp == 1 || warp == 2) {
             const uint32_t s = warp - 1;
-            const MmaRole<T, N> role{&c, ring, s, tmem + C::kACol + s * kABufs * kACols, tmem + s * C::kDBufs * N, leader};
+            const MmaRole<T, N> role{&c, ring, s, tmem + C::kACol + s * kABufs * kACols, tmem + s * kDBufs * 64, leader};
             if (a.group_log2 == 7) role.template run<7>(v_begin, v_end, blocks, a.H);
             else if (a.group_log2 == 6) role.template run<6>(v_begin, v_end, blocks, a.H);
             else role.template run<5>(v_begin, v_end, blocks, a.H);
@@ -492,7 +503,7 @@ __global__ void __launch_bounds__(kNT, 1)
         regs_inc<kEpilogueRegs>();
         const uint32_t s = (warp - kEpilogueWarp) / 4;
         const EpilogueRole<T, O, N> role{&c, smem_u32(entries), static_cast<O*>(a.out), a.ld, a.rows, s,
-                                         s * kSubV + quarter * 32 + lane, tmem + (quarter << 21) + s * C::kDBufs * N};
+                                         s * kSubV + quarter * 32 + lane, tmem + (quarter << 21) + s * kDBufs * 64};
         if (a.group_log2 == 7) role.template run<7>(v_begin, v_end, blocks, a.H);
         else if (a.group_log2 == 6) role.template run<6>(v_begin, v_end, blocks, a.H);
         else role.template run<5>(v_begin, v_end, blocks, a.H);
