@@ -16,7 +16,7 @@
 //                 to the type by placing them in the mantissa of 128 (bf16) or
 //                 1024 (f16) and subtracting 128 + z (1024 + z), both exact;
 //                 the tile goes to TMEM as the product's A operand
-//   warp 3        brings the rows' scales and zero points (a ring of its own)
+//   warp 3        brings the rows' scales and zero points
 //   warps 1, 2    issue the products of a subtile each (A from TMEM, B =
 //                 hidden states from shared memory, D in TMEM,
 //                 double-buffered by group)
@@ -42,16 +42,17 @@ constexpr int kUnpackWarp = 4, kEpilogueWarp = 20, kNT = 32 * 28;
 constexpr int kLaunchRegs = 72, kControlRegs = 56, kUnpackRegs = 56, kEpilogueRegs = 112;
 static_assert(4 * kControlRegs + 16 * kUnpackRegs + 8 * kEpilogueRegs <= 28 * kLaunchRegs);
 
-// Group entries have a ring of their own: the epilogue reads a stage's scales
-// well after its weights' slot is free again.
-constexpr uint32_t kEntrySlots = 5, kEntryBytes = kTileV * (EntryBytes<5>::kScales + EntryBytes<5>::kZeros);
+// Zero points lie in their stage's slot. Scales have a ring of their own: the
+// epilogue reads them well after the slot of their stage is free again.
+constexpr uint32_t kZeroBytes = kTileV * EntryBytes<5>::kZeros;
+constexpr uint32_t kScaleSlots = 5, kScaleBytes = kTileV * EntryBytes<5>::kScales;
 
 template <int N>
 struct Config {
     static constexpr uint32_t kXAtom = N * 128;  // 64 columns of N hidden rows
-    static constexpr uint32_t kStageBytes = kWBytes + kStageK / kAtomK * kXAtom;
-    static constexpr uint32_t kStages = 196 * 1024 / kStageBytes < kMaxStages ? 196 * 1024 / kStageBytes : kMaxStages;
-    static constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + kEntrySlots * kEntryBytes;
+    static constexpr uint32_t kStageBytes = kWBytes + kStageK / kAtomK * kXAtom + kZeroBytes;
+    static constexpr uint32_t kStages = 204 * 1024 / kStageBytes < kMaxStages ? 204 * 1024 / kStageBytes : kMaxStages;
+    static constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + kScaleSlots * kScaleBytes;
     static_assert(kSmem + 1024 <= 227 * 1024);
     // A D buffer's 64 columns hold up to 64 / N groups, handed over together.
     static constexpr uint32_t kBatch = 64 / N;
@@ -146,7 +147,7 @@ struct Ctx {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t a_full[2][kABufs], a_empty[2][kABufs];
     uint64_t d_full[2][kDBufs], d_empty[2][kDBufs];
-    uint64_t e_full[kEntrySlots], e_empty[kEntrySlots];
+    uint64_t e_full[kScaleSlots], e_empty[kScaleSlots];
     uint64_t drain[2];
     uint32_t tmem;
     uint32_t err;
@@ -223,6 +224,68 @@ struct MmaRole {
     }
 };
 
+// Brings the zero points of each stage into its slot and its scales into their
+// ring. Loads go out before the waits for the slots.
+template <int N>
+struct EntryRole {
+    using C = Config<N>;
+    Ctx* c;
+    unsigned char* ring;
+    unsigned char* scales;
+
+    template <int kGroupLog2, bool kZeros>
+    __device__ __forceinline__ void run(const HeadArgs& a, uint32_t v_begin, uint32_t v_end, uint32_t blocks) const {
+        using B = EntryBytes<kGroupLog2>;
+        constexpr uint32_t kBatch = kGroupLog2 == 5 ? 4 : 8;  // rows a lane holds at a time
+        const uint32_t lane = threadIdx.x & 31;
+        const uint32_t groups = a.H >> kGroupLog2, stages = (a.H + kStageK - 1) / kStageK;
+        const auto* s_base = static_cast<const unsigned char*>(a.scales);
+        const uint32_t ws = entry_width(s_base, 2 * groups), wz = kZeros ? entry_width(a.zeros, groups) : 16;
+        const bool wide = ws >= B::kScales && wz >= B::kZeros;
+        Ring<C::kStages> st;
+        Ring<kScaleSlots> er;
+        for (uint32_t vt = v_begin; vt < v_end; vt += kTileV) {
+            const uint32_t rows = min(kTileV, v_end - vt);
+            const unsigned char* s_src = s_base + 2 * static_cast<uint64_t>(vt) * groups;
+            const unsigned char* z_src = a.zeros + static_cast<uint64_t>(vt) * groups;
+            for (uint32_t blk = 0; blk < blocks; ++blk) {
+                for (uint32_t i = 0; i < stages; ++i) {
+                    unsigned char* s_dst = scales + er.i * kScaleBytes;
+                    unsigned char* z_dst = ring + (st.i + 1) * C::kStageBytes - kZeroBytes;
+                    if (wide) {
+#pragma unroll
+                        for (uint32_t u = 0; u < kTileV / 32; u += kBatch) {
+                            typename Word<B::kScales>::Type s[kBatch];
+                            typename Word<B::kZeros>::Type z[kBatch];
+                            const uint32_t u0 = u * 32 + lane;
+                            if (kZeros) load_words<B::kZeros, B::kZeros, kBatch>(z, z_src, i * B::kZeros, groups, rows, u0);
+                            load_words<B::kScales, B::kScales, kBatch>(s, s_src, i * B::kScales, 2 * groups, rows, u0);
+                            if (u == 0) {
+                                if (kZeros) wait(&c->empty[st.i], st.phase ^ 1, &c->err);
+                                wait(&c->e_empty[er.i], er.phase ^ 1, &c->err);
+                            }
+                            if (kZeros) store_words<B::kZeros, B::kZeros, kBatch>(z_dst, z, rows, u0);
+                            store_words<B::kScales, B::kScales, kBatch>(s_dst, s, rows, u0);
+                        }
+                    } else {
+                        if (kZeros) wait(&c->empty[st.i], st.phase ^ 1, &c->err);
+                        wait(&c->e_empty[er.i], er.phase ^ 1, &c->err);
+                        if (kZeros) copy_rows<B::kZeros, 8>(z_dst, z_src, i * B::kZeros, groups, rows, wz);
+                        copy_rows<B::kScales, 8>(s_dst, s_src, i * B::kScales, 2 * groups, rows, ws);
+                    }
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (kZeros) arrive(&c->full[st.i]);
+                        arrive(&c->e_full[er.i]);
+                    }
+                    st.next();
+                    er.next();
+                }
+            }
+        }
+    }
+};
+
 // Unpacks one unit of every stage for 32 lanes of a subtile, into the A buffer
 // of that unit.
 template <typename T, int N>
@@ -230,7 +293,6 @@ struct UnpackRole {
     using C = Config<N>;
     Ctx* c;
     const unsigned char* ring;
-    uint32_t entries;  // shared memory address
     uint32_t s, unit, row, a0;  // row: within the tile
 
     template <bool kZeros, int kGroupLog2>
@@ -240,23 +302,21 @@ struct UnpackRole {
         // 16-byte chunk ch of a row lies at ch ^ (row & 7)
         const unsigned char* src = ring + row * (kStageK / 2);
         const uint32_t ch = unit * 4, sw = row & 7;
-        const uint32_t ez = entries + kTileV * B::kScales + row * B::kZeros;
+        const uint32_t ez = smem_u32(ring) + C::kStageBytes - kZeroBytes + row * B::kZeros;
         Ring<C::kStages> st;
-        Ring<kEntrySlots> er;
         uint32_t phase = 0;  // of this unit's A buffer
         for (uint32_t vt = v_begin; vt < v_end; vt += kTileV) {
             const bool active = s == 0 || v_end - vt > kSubV;
             for (uint32_t blk = 0; blk < blocks; ++blk) {
                 for (uint32_t k = 0; k < H; k += kStageK) {
+                    wait(&c->full[st.i], st.phase, &c->err);
                     uint32_t zs = 0;  // the unit's zero points
                     if (kZeros) {
                         uint32_t v[(B::kZeros + 3) / 4];
-                        wait(&c->e_full[er.i], er.phase, &c->err);
-                        read_entries<B::kZeros>(ez + er.i * kEntryBytes, v);
+                        read_entries<B::kZeros>(ez + st.i * C::kStageBytes, v);
                         if constexpr (kGroupLog2 == 5) zs = unit ? v[1] : v[0];
                         else zs = v[0] >> (unit * (B::kZeros / 2) * 8);
                     }
-                    wait(&c->full[st.i], st.phase, &c->err);
                     const bool mine = active && k + unit * kUnitK < H;  // the last stage may end before its second unit
                     if (mine) {
                         const unsigned char* p = src + st.i * C::kStageBytes;
@@ -289,11 +349,9 @@ struct UnpackRole {
                     if (lane == 0) {
                         if (mine) arrive(&c->a_full[s][unit]);
                         arrive(&c->empty[st.i]);
-                        if (kZeros) arrive(&c->e_empty[er.i]);
                     }
                     if (mine) phase ^= 1;
                     st.next();
-                    er.next();
                 }
             }
         }
@@ -305,7 +363,7 @@ template <typename T, typename O, int N>
 struct EpilogueRole {
     using C = Config<N>;
     Ctx* c;
-    uint32_t entries;  // shared memory address
+    uint32_t scales;  // shared memory address of their ring
     O* out;
     uint64_t ld;
     uint32_t rows, s, row, d0;
@@ -317,9 +375,9 @@ struct EpilogueRole {
         constexpr uint32_t kPer = kUnitK >> kGroupLog2;
         constexpr uint32_t kBatch = C::kBatch < kPer ? C::kBatch : kPer;  // groups a D buffer
         const uint32_t lane = threadIdx.x & 31;
-        const uint32_t es = entries + row * B::kScales;
+        const uint32_t es = scales + row * B::kScales;
         Ring<kDBufs> dr;
-        Ring<kEntrySlots> er;
+        Ring<kScaleSlots> er;
         for (uint32_t vt = v_begin; vt < v_end; vt += kTileV) {
             const bool active = s == 0 || v_end - vt > kSubV;
             for (uint32_t blk = 0; blk < blocks; ++blk) {
@@ -329,7 +387,7 @@ struct EpilogueRole {
                 for (uint32_t k = 0; k < H; k += kStageK) {
                     uint32_t sc[B::kScales / 4];
                     wait(&c->e_full[er.i], er.phase, &c->err);
-                    read_entries<B::kScales>(es + er.i * kEntryBytes, sc);
+                    read_entries<B::kScales>(es + er.i * kScaleBytes, sc);
                     __syncwarp();
                     if (lane == 0) arrive(&c->e_empty[er.i]);
                     er.next();
@@ -378,14 +436,14 @@ __global__ void __launch_bounds__(kNT, 1)
     using C = Config<N>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    unsigned char* entries = ring + C::kStages * C::kStageBytes;
+    unsigned char* scales = ring + C::kStages * C::kStageBytes;
     __shared__ Ctx c;
     // (broadcasts: the compiler then keeps what follows from them in uniform registers)
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFull, tid >> 5, 0);
 
     if (tid == 0) {
         for (uint32_t i = 0; i < C::kStages; ++i) {
-            mbar_init(&c.full[i], 1);
+            mbar_init(&c.full[i], a.zeros ? 2 : 1);  // the copies, and the helper's zero points
             mbar_init(&c.empty[i], 16 + 2);  // the unpacking warps and the products
         }
         for (uint32_t s = 0; s < 2; ++s) {
@@ -399,9 +457,9 @@ __global__ void __launch_bounds__(kNT, 1)
                 mbar_init(&c.d_empty[s][i], 4);
             }
         }
-        for (uint32_t i = 0; i < kEntrySlots; ++i) {
+        for (uint32_t i = 0; i < kScaleSlots; ++i) {
             mbar_init(&c.e_full[i], 1);
-            mbar_init(&c.e_empty[i], 8 + (a.zeros ? 16 : 0));  // the epilogue's warps, and the unpacking ones
+            mbar_init(&c.e_empty[i], 8);
         }
         c.err = 0;
     }
@@ -475,13 +533,9 @@ __global__ void __launch_bounds__(kNT, 1)
             if (leader) tc_commit(&c.drain[s]);
             if (!mbar_wait(&c.drain[s], 0)) c.err = 1;
         } else {
+            const EntryRole<N> role{&c, ring, scales};
             auto copy = [&](auto log2, auto zeros) {
-                copy_entries<decltype(log2)::value, decltype(zeros)::value, kTileV / 32>(
-                    a, entries, kEntryBytes, kTileV, kEntrySlots, blocks, 0, 1, v_begin, v_end,
-                    [&](uint32_t slot, uint32_t phase) { wait(&c.e_empty[slot], phase ^ 1, &c.err); },
-                    [&](uint32_t slot) {
-                        if (lane == 0) arrive(&c.e_full[slot]);
-                    });
+                role.template run<decltype(log2)::value, decltype(zeros)::value>(a, v_begin, v_end, blocks);
             };
             using Yes = std::true_type;
             using No = std::false_type;
@@ -493,7 +547,7 @@ __global__ void __launch_bounds__(kNT, 1)
     } else if (warp < kEpilogueWarp) {
         regs_dec<kUnpackRegs>();
         const uint32_t wg = (warp - kUnpackWarp) / 4, s = wg & 1, unit = wg >> 1;
-        const UnpackRole<T, N> role{&c, ring, smem_u32(entries), s, unit, s * kSubV + quarter * 32 + lane,
+        const UnpackRole<T, N> role{&c, ring, s, unit, s * kSubV + quarter * 32 + lane,
                                     tmem + (quarter << 21) + C::kACol + (s * kABufs + unit) * kACols};
         if (!a.zeros) role.template run<false, 7>(v_begin, v_end, blocks, a.H);
         else if (a.group_log2 == 7) role.template run<true, 7>(v_begin, v_end, blocks, a.H);
@@ -502,7 +556,7 @@ __global__ void __launch_bounds__(kNT, 1)
     } else {
         regs_inc<kEpilogueRegs>();
         const uint32_t s = (warp - kEpilogueWarp) / 4;
-        const EpilogueRole<T, O, N> role{&c, smem_u32(entries), static_cast<O*>(a.out), a.ld, a.rows, s,
+        const EpilogueRole<T, O, N> role{&c, smem_u32(scales), static_cast<O*>(a.out), a.ld, a.rows, s,
                                          s * kSubV + quarter * 32 + lane, tmem + (quarter << 21) + s * kDBufs * 64};
         if (a.group_log2 == 7) role.template run<7>(v_begin, v_end, blocks, a.H);
         else if (a.group_log2 == 6) role.template run<6>(v_begin, v_end, blocks, a.H);

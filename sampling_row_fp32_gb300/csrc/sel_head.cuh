@@ -144,27 +144,36 @@ struct Word<1> { using Type = uint8_t; };
 // A warp copies kBytes bytes at byte `at` of each of `rows` rows of row_bytes
 // bytes, zeros past a row's end, as words of kW bytes (which divide the rows'
 // addresses and length, so that a word is all in a row or all past its end).
-// Neighbouring lanes take neighbouring words.
+// Neighbouring lanes take neighbouring words; u0 is the lane's first.
+template <uint32_t kBytes, uint32_t kW, uint32_t kBatch>
+__device__ __forceinline__ void load_words(typename Word<kW>::Type (&v)[kBatch], const unsigned char* src, uint32_t at,
+                                           uint32_t row_bytes, uint32_t rows, uint32_t u0) {
+    using W = typename Word<kW>::Type;
+    constexpr uint32_t kPerRow = kBytes / kW;
+#pragma unroll
+    for (uint32_t j = 0; j < kBatch; ++j) {
+        const uint32_t u = u0 + 32 * j, off = at + u % kPerRow * kW;
+        v[j] = W{};
+        if (u < rows * kPerRow && off < row_bytes)
+            v[j] = *reinterpret_cast<const W*>(src + static_cast<uint64_t>(u / kPerRow) * row_bytes + off);
+    }
+}
+template <uint32_t kBytes, uint32_t kW, uint32_t kBatch>
+__device__ __forceinline__ void store_words(unsigned char* dst, const typename Word<kW>::Type (&v)[kBatch], uint32_t rows,
+                                            uint32_t u0) {
+#pragma unroll
+    for (uint32_t j = 0; j < kBatch; ++j) {
+        const uint32_t u = u0 + 32 * j;
+        if (u < rows * (kBytes / kW)) *reinterpret_cast<typename Word<kW>::Type*>(dst + u * kW) = v[j];
+    }
+}
 template <uint32_t kBytes, uint32_t kW, uint32_t kBatch>
 __device__ __forceinline__ void copy_words(unsigned char* dst, const unsigned char* src, uint32_t at, uint32_t row_bytes,
                                            uint32_t rows) {
-    using W = typename Word<kW>::Type;
-    constexpr uint32_t kPerRow = kBytes / kW;
-    const uint32_t lane = threadIdx.x & 31, total = rows * kPerRow;
-    for (uint32_t u0 = lane; u0 < total; u0 += 32 * kBatch) {
-        W v[kBatch];
-#pragma unroll
-        for (uint32_t j = 0; j < kBatch; ++j) {
-            const uint32_t u = u0 + 32 * j, off = at + u % kPerRow * kW;
-            v[j] = W{};
-            if (u < total && off < row_bytes)
-                v[j] = *reinterpret_cast<const W*>(src + static_cast<uint64_t>(u / kPerRow) * row_bytes + off);
-        }
-#pragma unroll
-        for (uint32_t j = 0; j < kBatch; ++j) {
-            const uint32_t u = u0 + 32 * j;
-            if (u < total) *reinterpret_cast<W*>(dst + u * kW) = v[j];
-        }
+    for (uint32_t u0 = threadIdx.x & 31; u0 < rows * (kBytes / kW); u0 += 32 * kBatch) {
+        typename Word<kW>::Type v[kBatch];
+        load_words<kBytes, kW, kBatch>(v, src, at, row_bytes, rows, u0);
+        store_words<kBytes, kW, kBatch>(dst, v, rows, u0);
     }
 }
 template <uint32_t kBytes, uint32_t kBatch>
