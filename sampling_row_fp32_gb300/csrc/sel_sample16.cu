@@ -13,9 +13,10 @@
 // One cluster of C CTAs per row. Each CTA reads its share of the row once,
 // into registers, and counts it into a histogram of 65,536 16-bit counters in
 // its shared memory (a share holds fewer than 65,536 ids, so no counter
-// overflows). After one cluster barrier every CTA walks the row's non-empty
-// bins through distributed shared memory, decides the cut and the draw (all
-// CTAs decide the same), and the CTA that holds the drawn rank finds its id
+// overflows). After a cluster barrier the CTAs share the row's non-empty bins
+// between them, sum their counts through distributed shared memory, and
+// exchange the totals; each border (of top-k, top-p, the draw) is then found
+// by the CTA whose bins hold it. The CTA whose share holds the drawn id finds it
 // in its registers.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -66,12 +67,82 @@ struct Kind<__half> {
 };
 
 template <typename T>
-__device__ __forceinline__ double bin_value(uint32_t bin) {
+__device__ __forceinline__ float bin_value(uint32_t bin) {
     const uint32_t u = bin < 0x8000u ? 0x7FFFu - bin : bin;
-    if constexpr (sizeof(T) == 2 && Kind<T>::kInf == 0x7F80) return static_cast<double>(__uint_as_float(u << 16));
-    return static_cast<double>(__half2float(__ushort_as_half(static_cast<unsigned short>(u))));
+    return bits_f32<T>(static_cast<uint16_t>(u));
 }
 
+// ---------------------------------------------------------------------------
+// weights: exp((x - max) / T) to about 45 bits without FP64, whose units would
+// take 25 us over the distinct values of one f16 row
+// ---------------------------------------------------------------------------
+// With r = log2(e) / T as a sum of two floats, 2^y for y = (x - max) r, also
+// kept as two floats: y = k / 256 + g with |g| <= 1/512, and
+// 2^g = 1 + z + z^2/2 + z^3/6 + z^4/24 with z = g ln 2 <= 0.0014, whose next
+// term is below 2^-56. Only z itself needs its second float; the higher terms
+// are below 2^-20 and good to 2^-44 in one. 2^(j/256) comes from a table of
+// float pairs, summed from its series at compile time.
+
+constexpr int kTable = 256;
+struct ExpTable {
+    float2 v[kTable];
+    constexpr ExpTable() : v{} {
+        for (int j = 0; j < kTable; ++j) {
+            const double z = j * 0.693147180559945309417232121458 / kTable;
+            double term = 1.0, sum = 1.0;
+            for (int k = 1; k < 24; ++k) {
+                term *= z / k;
+                sum += term;
+            }
+            const float hi = static_cast<float>(sum);
+            v[j].x = hi;
+            v[j].y = static_cast<float>(sum - static_cast<double>(hi));
+        }
+    }
+};
+__constant__ const ExpTable kExpTable;
+
+struct Weights {
+    float top;            // the row's largest logit, times `pre`
+    float pre, post;      // powers of two, their product about 1 / T: r stays near 1
+    FF r;                 // log2(e) / (T pre post)
+    const float2* table;  // in shared memory
+
+    __device__ __forceinline__ Weights(float row_max, float T, const float2* tab) : table(tab) {
+        const int e = min(max(static_cast<int>(__float_as_uint(T) >> 23) - 127, -126), 126);  // T is about 2^e
+        pre = exp2i(e > 0 ? -e : 0);
+        post = exp2i(e > 0 ? 0 : -e);
+        top = row_max * pre;
+        r = ff_from_double(1.4426950408889634 / (static_cast<double>(T) * pre * post));
+    }
+    static __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
+
+    // 0 below 2^-100, the whole tail of a row weighing less than 2^-80 then
+    __device__ __forceinline__ FF operator()(float logit) const {
+        constexpr float kLn2 = 0.693147182464599609375f, kLn2Lo = -1.904654299957767e-9f;
+        const float x = logit * pre;
+        const float ds = x - top;  // and the subtraction's rounding error
+        const float v = ds - x;
+        const float dl = ((x - (ds - v)) - (top + v)) * post;
+        const float dh = ds * post;
+        const float yh = dh * r.hi;
+        if (!(yh > -100.0f)) return FF{0.0f, 0.0f};
+        const float yl = __fmaf_rn(dh, r.hi, -yh) + __fmaf_rn(dl, r.hi, dh * r.lo);
+        const float magic = __fmaf_rn(yh, static_cast<float>(kTable), 12582912.0f);  // 1.5 * 2^23: rounds to a whole number
+        const int k = __float_as_int(magic) - 0x4B400000;
+        const float g = __fmaf_rn(magic - 12582912.0f, -1.0f / kTable, yh);  // exact
+        const float zh = g * kLn2;
+        const float zl = __fmaf_rn(g, kLn2, -zh) + __fmaf_rn(g, kLn2Lo, yl * kLn2);
+        const float q = __fmaf_rn(zh, __fmaf_rn(zh, 1.0f / 24, 1.0f / 6), 0.5f);
+        const float el = zl + __fmaf_rn(zh * zh, q, zh * zl);  // 2^(g + yl) = 1 + zh + el
+        const float2 t = table[k & (kTable - 1)];
+        const float ph = t.x * zh, pl = __fmaf_rn(t.x, zh, -ph);
+        const float s = t.x + ph;
+        const float lo = (ph - (s - t.x)) + (pl + (t.y + __fmaf_rn(t.x, el, t.y * zh)));
+        const float scale = __int_as_float(((k >> 8) + 127) << 23);
+        return FF{s * scale, lo * scale};
+    }
+};
 struct SampleArgs {
     const void* logits;
     uint64_t ld;
@@ -86,9 +157,19 @@ struct SampleArgs {
     uint32_t share;  // vectors a CTA takes
 };
 
+// What the CTAs of a row tell each other: each writes its line of every CTA's
+// table, and the CTA that decides a step its results.
+struct Totals {
+    double mass;
+    uint32_t count, min_count;
+};
+enum { kMassK, kMassN, kProb, kDoubles };
+enum { kRankP, kBin, kPlace, kRank, kInts };
+
 struct Shared {
     uint32_t hist[kBins / 2];
     uint16_t units[kUnits];  // the row's non-empty units, in bin order
+    float2 table[kTable];
     double incl_m[kNT];
     uint32_t incl_c[kNT];
     uint32_t bits[kWords];
@@ -96,8 +177,10 @@ struct Shared {
     double warp_m[kWarps];
     uint32_t warp_c[kWarps];
     uint32_t seg[kVPT * kWarps];
-    double d[4];     // broadcast results of the walks
-    uint32_t u[8];
+    Totals totals[kMaxCluster];
+    double d[kDoubles];
+    uint32_t u[kInts];
+    uint32_t find[2];
 };
 
 template <typename T>
@@ -115,6 +198,7 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
     uint4* h4 = reinterpret_cast<uint4*>(s.hist);
 #pragma unroll
     for (int i = 0; i < static_cast<int>(kUnits / kNT); ++i) h4[i * kNT + tid] = make_uint4(0, 0, 0, 0);
+    if (tid < kTable) s.table[tid] = kExpTable.v[tid];
     pdl_wait();
 
     // The row as 16-byte vectors from the aligned address at or below its
@@ -232,19 +316,23 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
     // unmasked, a uniform or a parameter out of its range.
     bool bad = !(Tf >= 0.0f) || isinf(Tf) || !(pf > 0.0f && pf <= 1.0f) || !(mf >= 0.0f && mf < 1.0f) ||
                !(uf >= 0.0f && uf < 1.0f) || nu == 0;
-    double xmax = 0.0;
+    float xmax = 0.0f;
+    uint32_t first_bin = 0;
     if (!bad) {
         uint32_t c[kUnitBins];
         const uint32_t first = s.units[0], last = s.units[nu - 1];
         counts(first, c);
-        int f = 0;
-        while (c[f] == 0) ++f;  // a listed unit has a count
-        xmax = bin_value<T>(first * kUnitBins + f);
-        bad = first * kUnitBins + f <= kPosInf;
+        uint32_t f = kUnitBins, l = 0;
+#pragma unroll
+        for (uint32_t b = kUnitBins; b-- > 0;)
+            if (c[b]) f = b;
         counts(last, c);
-        int l = kUnitBins - 1;
-        while (l > 0 && c[l] == 0) --l;
-        bad = bad || last * kUnitBins + l > kNegInf;
+#pragma unroll
+        for (uint32_t b = 0; b < kUnitBins; ++b)
+            if (c[b]) l = b;
+        first_bin = first * kUnitBins + f;
+        xmax = bin_value<T>(first_bin);
+        bad = first_bin <= kPosInf || last * kUnitBins + l > kNegInf;
     }
     if (bad) {  // the same in every CTA of the cluster
         if (rank == 0 && tid == 0) {
@@ -255,29 +343,32 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
         return;
     }
     const bool greedy = Tf == 0.0f;
-    const double Td = greedy ? 1.0 : static_cast<double>(Tf);
-    const double minp = mf;
-    auto weight = [&](uint32_t bin) { return exp((bin_value<T>(bin) - xmax) / Td); };
+    const Weights weight(xmax, greedy ? 1.0f : Tf, s.table);
+
+    // This CTA's part of the list, and each thread's.
+    const uint32_t first = static_cast<uint32_t>(static_cast<uint64_t>(nu) * rank / C);
+    const uint32_t last = static_cast<uint32_t>(static_cast<uint64_t>(nu) * (rank + 1) / C);
+    const uint32_t per = (last - first + kNT - 1) / kNT;
+    const uint32_t i0 = min(last, first + tid * per), i1 = min(last, i0 + per);
 
     // Counts and masses up to each thread's units, in order.
-    const uint32_t per = (nu + kNT - 1) / kNT;
-    const uint32_t i0 = min(nu, tid * per), i1 = min(nu, i0 + per);
     uint32_t c_in = 0, n_min = 0;
-    double m_in = 0.0;
+    FF mass{0.0f, 0.0f};
     for (uint32_t i = i0; i < i1; ++i) {
         uint32_t c[kUnitBins];
         const uint32_t unit = s.units[i];
         counts(unit, c);
 #pragma unroll
         for (uint32_t b = 0; b < kUnitBins; ++b) {
+            const FF w = weight(bin_value<T>(unit * kUnitBins + b));
             if (c[b]) {
-                const double w = weight(unit * kUnitBins + b);
                 c_in += c[b];
-                m_in += c[b] * w;
-                if (w >= minp) n_min += c[b];
+                mass = ff_add(mass, ff_mul_f(w, static_cast<float>(c[b])));
+                if (w.hi > mf || (w.hi == mf && w.lo >= 0.0f)) n_min += c[b];
             }
         }
     }
+    double m_in = ff_to_double(mass);
     n_min = __reduce_add_sync(kFull, n_min);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -309,111 +400,150 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
         s.warp_c[lane] = wc;
         s.warp_m[lane] = wm;
         n_min = __reduce_add_sync(kFull, s.seg[lane]);
-        if (lane == 0) s.u[0] = n_min;
+        wc = __shfl_sync(kFull, wc, 31);
+        wm = __shfl_sync(kFull, wm, 31);
+        if (lane < C) cl.map_shared_rank(s.totals, lane)[rank] = Totals{wm, wc, n_min};
     }
-    __syncthreads();
+    cl.sync();
+    // sums before this CTA's units and over the row, in the same order everywhere
+    uint32_t c_base = 0, n_all = 0;
+    double m_base = 0.0, m_all = 0.0;
+    n_min = 0;
+    for (uint32_t r = 0; r < C; ++r) {
+        if (r == rank) {
+            c_base = n_all;
+            m_base = m_all;
+        }
+        n_all += s.totals[r].count;
+        m_all += s.totals[r].mass;
+        n_min += s.totals[r].min_count;
+    }
     if (warp > 0) {
         c_in += s.warp_c[warp - 1];
         m_in += s.warp_m[warp - 1];
     }
+    c_in += c_base;
+    m_in += m_base;
     s.incl_c[tid] = c_in;
     s.incl_m[tid] = m_in;
     __syncthreads();
-    n_min = s.u[0];
-    const uint32_t c_before = tid ? s.incl_c[tid - 1] : 0u;
-    const double m_before = tid ? s.incl_m[tid - 1] : 0.0;
-    const uint32_t n_all = s.incl_c[kNT - 1];
+    const uint32_t c_before = tid ? s.incl_c[tid - 1] : c_base, c_end = s.incl_c[kNT - 1];
+    const double m_before = tid ? s.incl_m[tid - 1] : m_base;
 
+    // A thread's bins in order: f(bin, count, weight, ids before, mass before)
+    // until it returns true.
+    auto walk = [&](auto f) {
+        uint32_t seen = c_before;
+        double m = m_before;
+        for (uint32_t i = i0; i < i1; ++i) {
+            uint32_t c[kUnitBins];
+            const uint32_t unit = s.units[i];
+            counts(unit, c);
+#pragma unroll
+            for (uint32_t b = 0; b < kUnitBins; ++b) {
+                if (c[b] == 0) continue;
+                const uint32_t bin = unit * kUnitBins + b;
+                const double w = ff_to_double(weight(bin_value<T>(bin)));
+                if (f(bin, c[b], w, seen, m)) return;
+                seen += c[b];
+                m += c[b] * w;
+            }
+        }
+    };
+    auto tell = [&](auto&& field, auto value) {  // the same word of every CTA
+        for (uint32_t r = 0; r < C; ++r) *cl.map_shared_rank(&field, r) = value;
+    };
     // Mass of the first n ids of the order.
     auto prefix_mass = [&](uint32_t n, int slot) {
-        const int t = __syncthreads_count(c_in < n);
-        if (static_cast<int>(tid) == t) {
-            uint32_t left = n - c_before;
-            double mass = m_before;
-            for (uint32_t i = i0; i < i1 && left; ++i) {
-                uint32_t c[kUnitBins];
-                const uint32_t unit = s.units[i];
-                counts(unit, c);
-                for (uint32_t b = 0; b < kUnitBins && left; ++b) {
-                    const uint32_t take = min(left, c[b]);
-                    if (take) mass += take * weight(unit * kUnitBins + b);
-                    left -= take;
-                }
+        if (n == n_all) return m_all;
+        if (c_base < n && n <= c_end) {
+            if (static_cast<int>(tid) == __syncthreads_count(c_in < n)) {
+                double mass = 0.0;
+                walk([&](uint32_t, uint32_t c, double w, uint32_t seen, double m) {
+                    mass = m + min(n - seen, c) * w;
+                    return seen + c >= n;
+                });
+                tell(s.d[slot], mass);
             }
-            s.d[slot] = mass;
         }
-        __syncthreads();
+        cl.sync();
         return s.d[slot];
     };
-    // 0-based rank of the first id whose cumulative mass is at least `goal`
-    // (kOver: exceeds it); n_all when rounding leaves none.
-    auto rank_of = [&](double goal, bool over, int slot) {
-        const int t = min(__syncthreads_count(over ? m_in <= goal : m_in < goal), kNT - 1);
-        if (static_cast<int>(tid) == t) {
-            uint32_t at = c_in;  // not found inside: the next thread's first id
-            uint32_t seen = c_before;
-            double mass = m_before;
-            bool found = false;
-            for (uint32_t i = i0; i < i1 && !found; ++i) {
-                uint32_t c[kUnitBins];
-                const uint32_t unit = s.units[i];
-                counts(unit, c);
-                for (uint32_t b = 0; b < kUnitBins && !found; ++b) {
-                    if (c[b] == 0) continue;
-                    const double w = weight(unit * kUnitBins + b);
-                    const double end = mass + c[b] * w;
-                    if (over ? end > goal : end >= goal) {
-                        // w > 0 here; the r-th id (from 0) ends at mass + (r + 1) w
-                        const double r = over ? floor((goal - mass) / w) : ceil((goal - mass) / w) - 1.0;
-                        at = seen + static_cast<uint32_t>(fmin(fmax(r, 0.0), c[b] - 1.0));
-                        found = true;
-                    }
-                    mass = end;
-                    seen += c[b];
-                }
-            }
-            s.u[slot] = at;
+    // Whether the first id whose cumulative mass reaches `goal` (over: exceeds
+    // it) is among this CTA's, its last one's when rounding leaves none.
+    auto reached = [&](double m, double goal, bool over) { return over ? m > goal : m >= goal; };
+    auto holds = [&](double goal, bool over) {
+        double m = 0.0;
+        uint32_t r = 0;
+        for (; r + 1 < C; ++r) {
+            m += s.totals[r].mass;
+            if (reached(m, goal, over)) break;
         }
-        __syncthreads();
-        return s.u[slot];
+        return r == rank;
+    };
+    // The thread that has it, and that id: its bin, its place among the bin's
+    // ids, its rank in the row.
+    auto find_mass = [&](double goal, bool over, auto f) {
+        if (!holds(goal, over)) return;
+        if (static_cast<int>(tid) != min(__syncthreads_count(!reached(m_in, goal, over)), kNT - 1)) return;
+        uint32_t bin = 0, place = 0, at = c_in;  // not found inside: the next thread's first id
+        double weight_of = 1.0;
+        walk([&](uint32_t b, uint32_t c, double w, uint32_t seen, double m) {
+            bin = b;
+            weight_of = w;
+            if (!reached(m + c * w, goal, over)) {
+                place = c - 1;
+                return false;
+            }
+            // w > 0 here; the r-th id (from 0) ends at m + (r + 1) w
+            const double r = over ? floor((goal - m) / w) : ceil((goal - m) / w) - 1.0;
+            place = static_cast<uint32_t>(fmin(fmax(r, 0.0), c - 1.0));
+            at = seen + place;
+            return true;
+        });
+        f(bin, place, at, weight_of);
     };
 
-    uint32_t at = 0;
-    double Zs = 1.0;
-    if (!greedy) {
-        const uint32_t n_k = kk == 0 ? n_all : min(kk, n_all);
-        const double Z = prefix_mass(n_k, 0);
-        uint32_t n = min(n_k, n_min);
-        if (pf < 1.0f) n = min(n, rank_of(static_cast<double>(pf) * Z, false, 1) + 1u);
-        Zs = n == n_k ? Z : prefix_mass(n, 1);
-        at = min(rank_of(static_cast<double>(uf) * Zs, true, 2), n - 1u);
-    }
-    {
-        // the drawn rank's bin, and its place among the bin's ids
-        const int t = __syncthreads_count(c_in <= at);
-        if (static_cast<int>(tid) == t) {
-            uint32_t r = at - c_before;
-            bool found = false;
-            for (uint32_t i = i0; i < i1 && !found; ++i) {
-                uint32_t c[kUnitBins];
-                const uint32_t unit = s.units[i];
-                counts(unit, c);
-                for (uint32_t b = 0; b < kUnitBins && !found; ++b) {
-                    if (r < c[b]) {
-                        const uint32_t bin = unit * kUnitBins + b;
-                        s.u[3] = bin;
-                        s.u[4] = r;
-                        s.d[2] = greedy ? 1.0 : weight(bin) / Zs;
-                        found = true;
-                    }
-                    r -= c[b];
-                }
-            }
+    if (greedy) {
+        if (tid == 0) {
+            s.u[kBin] = first_bin;
+            s.u[kPlace] = 0;
+            s.d[kProb] = 1.0;
         }
         __syncthreads();
+    } else {
+        const uint32_t n_k = kk == 0 ? n_all : min(kk, n_all);
+        const double Z = prefix_mass(n_k, kMassK);
+        uint32_t n = min(n_k, n_min);
+        if (pf < 1.0f) {
+            find_mass(static_cast<double>(pf) * Z, false,
+                      [&](uint32_t, uint32_t, uint32_t at, double) { tell(s.u[kRankP], at); });
+            cl.sync();
+            n = min(n, s.u[kRankP] + 1u);
+        }
+        const double Zs = n == n_k ? Z : prefix_mass(n, kMassN);
+        auto drawn = [&](uint32_t bin, uint32_t place, uint32_t at, double w) {
+            tell(s.u[kBin], bin);
+            tell(s.u[kPlace], place);
+            tell(s.u[kRank], at);
+            tell(s.d[kProb], w / Zs);
+        };
+        find_mass(static_cast<double>(uf) * Zs, true, drawn);
+        cl.sync();
+        if (s.u[kRank] >= n) {  // rounding left none: the last survivor
+            cl.sync();          // every CTA has read the rank
+            if (c_base < n && n <= c_end && static_cast<int>(tid) == __syncthreads_count(c_in < n)) {
+                walk([&](uint32_t b, uint32_t c, double w, uint32_t seen, double) {
+                    if (seen + c < n) return false;
+                    drawn(b, n - 1 - seen, n - 1, w);
+                    return true;
+                });
+            }
+            cl.sync();
+        }
     }
-    const uint32_t bin = s.u[3];
-    uint32_t r = s.u[4];
+    const uint32_t bin = s.u[kBin];
+    uint32_t r = s.u[kPlace];
     uint32_t owner = C;
     for (uint32_t c = 0; c < C && owner == C; ++c) {
         const uint32_t n = (cl.map_shared_rank(s.hist, c)[bin >> 1] >> (16 * (bin & 1))) & 0xFFFFu;
@@ -453,13 +583,13 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
             if (before <= r && r < in) {
                 uint32_t i = lane * kVPT;
                 while (r - before >= s.seg[i]) before += s.seg[i++];
-                s.u[5] = i;
-                s.u[6] = r - before;
+                s.find[0] = i;
+                s.find[1] = r - before;
             }
         }
         __syncthreads();
-        const uint32_t seg = s.u[5];
-        r = s.u[6];
+        const uint32_t seg = s.find[0];
+        r = s.find[1];
         if (warp == seg % kWarps) {
 #pragma unroll
             for (int j = 0; j < kVPT; ++j) {
@@ -479,7 +609,7 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
                         if (hit(w[i >> 1], i & 1)) {
                             if (left == 0) {
                                 a.out_ids[row] = (lo + j * kNT + tid) * 8u + i - skew;
-                                a.out_probs[row] = static_cast<float>(s.d[2]);
+                                a.out_probs[row] = static_cast<float>(s.d[kProb]);
                             }
                             --left;
                         }

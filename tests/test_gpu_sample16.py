@@ -117,6 +117,18 @@ def test_every_finite_pattern(dtype):
     check(x, (T, k, None, None), np.array([0.3, 0.9, 0.7, 0.99], dtype=np.float32))
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("spread", [1e-38, 1e-7, 1.0, 1e4, 3e37])
+def test_temperatures_at_the_ends(dtype, spread):
+    """Temperatures from the smallest float to the largest on rows of any scale."""
+    if spread in (1e-38, 3e37) and dtype == "f16":
+        pytest.skip("outside f16")
+    rng = np.random.default_rng(8)
+    T = np.array([1e-45, 1e-42, 1.2e-38, 1e-30, 1e-5, 1.0, 1e5, 1e30, 3e38, spread, spread * 0.1, spread * 3], dtype=np.float32)
+    x = torch.from_numpy(rng.normal(0, spread, size=(len(T), 3000))).to(DT[dtype])
+    check(x, (T, None, np.full(len(T), 0.9, np.float32), None), rng.random(len(T), dtype=np.float32))
+
+
 def test_equal_weights_at_exact_borders():
     """Every weight is 1: uniforms and top-p cuts that fall on a border go by
     rational arithmetic."""
