@@ -14,10 +14,14 @@
 // into registers, and counts it into a histogram of 65,536 16-bit counters in
 // its shared memory (a share holds fewer than 65,536 ids, so no counter
 // overflows). After a cluster barrier the CTAs share the row's non-empty bins
-// between them, sum their counts through distributed shared memory, and
-// exchange the totals; each border (of top-k, top-p, the draw) is then found
-// by the CTA whose bins hold it. The CTA whose share holds the drawn id finds it
-// in its registers.
+// between them, a lane a bin, and sum counts (through distributed shared
+// memory) and masses of up to 2,048 entries in the first CTA. There one warp
+// finds every border (of top-k, top-p, the draw): ballots over the entries'
+// prefix sums, then the 32 bins of the entry. The CTA whose share holds the
+// drawn id finds it in its registers.
+//
+// FP64 runs at two results a clock and SM here, so only that one warp uses it:
+// a single FP64 addition by all 32 warps costs 460 clocks.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -106,19 +110,18 @@ struct Weights {
     float top;            // the row's largest logit, times `pre`
     float pre, post;      // powers of two, their product about 1 / T: r stays near 1
     FF r;                 // log2(e) / (T pre post)
-    const float2* table;  // in shared memory
 
-    __device__ __forceinline__ Weights(float row_max, float T, const float2* tab) : table(tab) {
+    // (by one thread, while the row is counted; `top` follows)
+    __device__ __forceinline__ void temperature(float T) {
         const int e = min(max(static_cast<int>(__float_as_uint(T) >> 23) - 127, -126), 126);  // T is about 2^e
         pre = exp2i(e > 0 ? -e : 0);
         post = exp2i(e > 0 ? 0 : -e);
-        top = row_max * pre;
         r = ff_from_double(1.4426950408889634 / (static_cast<double>(T) * pre * post));
     }
     static __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }
 
     // 0 below 2^-100, the whole tail of a row weighing less than 2^-80 then
-    __device__ __forceinline__ FF operator()(float logit) const {
+    __device__ __forceinline__ FF operator()(float logit, const float2* table) const {
         constexpr float kLn2 = 0.693147182464599609375f, kLn2Lo = -1.904654299957767e-9f;
         const float x = logit * pre;
         const float ds = x - top;  // and the subtraction's rounding error
@@ -157,29 +160,27 @@ struct SampleArgs {
     uint32_t share;  // vectors a CTA takes
 };
 
-// What the CTAs of a row tell each other: each writes its line of every CTA's
-// table, and the CTA that decides a step its results.
-struct Totals {
-    double mass;
-    uint32_t count, min_count;
-};
-enum { kMassK, kMassN, kProb, kDoubles };
-enum { kRankP, kBin, kPlace, kRank, kInts };
+constexpr uint32_t kEntries = 2048;             // at most; of up to four units, a lane a bin
+constexpr uint32_t kCoarse = kEntries / 32;     // entries a lane of the deciding warp looks at first
+static_assert(kUnits <= kEntries * 4 && kEntries == 2 * kNT);
 
 struct Shared {
     uint32_t hist[kBins / 2];
-    uint16_t units[kUnits];  // the row's non-empty units, in bin order
+    uint16_t units[kUnits];   // the row's non-empty units, in bin order
     float2 table[kTable];
-    double incl_m[kNT];
-    uint32_t incl_c[kNT];
-    uint32_t bits[kWords];
+    uint32_t entry_c[kEntries];  // in the row's first CTA: counts and masses of the entries,
+    FF entry_m[kEntries];        // then up to and with each entry
+    uint32_t bits[kWords];    // occupancy: bit l of word w is unit 32 w + l
     uint32_t off[kWords];
-    double warp_m[kWarps];
+    FF warp_m[kWarps];
     uint32_t warp_c[kWarps];
     uint32_t seg[kVPT * kWarps];
-    Totals totals[kMaxCluster];
-    double d[kDoubles];
-    uint32_t u[kInts];
+    Weights weights;
+    uint32_t n_min;           // ids that min-p leaves
+    uint32_t first_bin;       // the largest logit's
+    uint32_t bad;
+    uint32_t bin, owner, place;  // the drawn bin, the CTA of the drawn id, its place among that CTA's ids of the bin
+    float prob;
     uint32_t find[2];
 };
 
@@ -199,6 +200,7 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
 #pragma unroll
     for (int i = 0; i < static_cast<int>(kUnits / kNT); ++i) h4[i * kNT + tid] = make_uint4(0, 0, 0, 0);
     if (tid < kTable) s.table[tid] = kExpTable.v[tid];
+    if (tid == 0) s.n_min = 0;
     pdl_wait();
 
     // The row as 16-byte vectors from the aligned address at or below its
@@ -208,34 +210,39 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
     const uint32_t skew = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(x) & 15u) / 2u;
     const uint32_t vecs = (a.V + skew + 7u) / 8u;
     const uint32_t lo = rank * a.share, hi = min(vecs, lo + a.share);
+    const uint32_t full_lo = max(lo, skew ? 1u : 0u), full_hi = min(hi, (a.V + skew) / 8u);
     uint4 q[kVPT];
 #pragma unroll
     for (int j = 0; j < kVPT; ++j) {
         const uint32_t v = lo + j * kNT + tid;
         q[j] = make_uint4(kFill, kFill, kFill, kFill);
-        if (v < hi) {
-            const int64_t e0 = static_cast<int64_t>(v) * 8 - skew;
-            if (e0 >= 0 && e0 + 8 <= a.V) {
-                q[j] = ldg_stream16(x + e0);
-            } else {
-                uint32_t w[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int64_t e = e0 + 2 * i;
-                    const uint32_t b0 = e >= 0 && e < a.V ? x[e] : kNegInf;
-                    const uint32_t b1 = e + 1 >= 0 && e + 1 < a.V ? x[e + 1] : kNegInf;
-                    w[i] = b0 | (b1 << 16);
-                }
-                q[j] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        }
+        if (v >= full_lo && v < full_hi) q[j] = ldg_stream16(x - skew + static_cast<uint64_t>(v) * 8u);
     }
     const float Tf = a.temperature ? a.temperature[row] : 1.0f;
     const uint32_t kk = a.top_k ? a.top_k[row] : 0u;
     const float pf = a.top_p ? a.top_p[row] : 1.0f;
     const float mf = a.min_p ? a.min_p[row] : 0.0f;
     const float uf = a.uniforms[row];
+    auto edge = [&](uint32_t v) {  // the vector v, if it is this thread's
+        if (v < lo || v >= hi || (v - lo) % kNT != tid) return;
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = 0;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t e = static_cast<int64_t>(v) * 8 - skew + 2 * i + h;
+                w[i] |= (e >= 0 && e < a.V ? x[e] : kNegInf) << (16 * h);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kVPT; ++j)
+            if ((v - lo) / kNT == static_cast<uint32_t>(j)) q[j] = make_uint4(w[0], w[1], w[2], w[3]);
+    };
+    if (skew) edge(0);
+    if ((a.V + skew) % 8u && (vecs > 1 || !skew)) edge(vecs - 1);
     pdl_trigger();
+    if (tid == 32) s.weights.temperature(Tf > 0.0f ? Tf : 1.0f);
     __syncthreads();  // the histogram is clear
 
 #pragma unroll
@@ -259,82 +266,63 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
         s.hist[kZeroBin / 2] += neg << 16;
     }
     __syncthreads();
-    // occupancy: bit l of word w is unit 32 w + l
 #pragma unroll
     for (int i = 0; i < static_cast<int>(kUnits / kNT); ++i) {
-        const uint32_t unit = (warp * (kUnits / kNT) + i) * 32 + lane;
-        const uint4 v = h4[unit];
+        const uint32_t word = i * kWarps + warp;
+        const uint4 v = h4[word * 32 + lane];
         const uint32_t b = __ballot_sync(kFull, (v.x | v.y | v.z | v.w) != 0);
-        if (lane == 0) s.bits[warp * (kUnits / kNT) + i] = b;
+        if (lane == 0) s.bits[word] = b;
     }
     cl.sync();
 
     // The row's non-empty units, in order.
-    uint32_t word = 0, pc = 0;
+    uint32_t word = 0;
     if (tid < kWords) {
-        for (uint32_t c = 0; c < C; ++c) word |= cl.map_shared_rank(s.bits, c)[tid];
-        pc = __popc(word);
-        uint32_t in = pc;
+        for (uint32_t r = 0; r < C; ++r) word |= cl.map_shared_rank(s.bits, r)[tid];
+        uint32_t in = __popc(word);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t t = __shfl_up_sync(kFull, in, o);
-            if (lane >= static_cast<uint32_t>(o)) in += t;
+            const uint32_t n = __shfl_up_sync(kFull, in, o);
+            if (lane >= static_cast<uint32_t>(o)) in += n;
         }
-        s.off[tid] = in;
+        s.off[tid] = in;  // up to and with this word, in its 32
+        s.seg[tid] = word;
     }
     __syncthreads();
     uint32_t nu = 0;
 #pragma unroll
-    for (uint32_t w = 0; w < kWords / 32; ++w) nu += s.off[w * 32 + 31];
-    if (tid < kWords) {
-        uint32_t at = s.off[tid] - pc;
-        for (uint32_t w = 0; w < warp; ++w) at += s.off[w * 32 + 31];
-        while (word) {
-            const int b = __ffs(word) - 1;
-            word &= word - 1;
-            s.units[at++] = static_cast<uint16_t>(tid * 32 + b);
-        }
+    for (int i = 0; i < static_cast<int>(kUnits / kNT); ++i) {
+        const uint32_t w = i * kWarps + warp, m = s.seg[w], before = s.off[w] - __popc(m);
+        if (m >> lane & 1) s.units[nu + before + __popc(m & ((1u << lane) - 1u))] = static_cast<uint16_t>(w * 32 + lane);
+        nu += s.off[i * kWarps + 31];
     }
     __syncthreads();
 
-    // counts of one unit's bins over the cluster
-    auto counts = [&](uint32_t unit, uint32_t (&c)[kUnitBins]) {
-#pragma unroll
-        for (int i = 0; i < static_cast<int>(kUnitBins); ++i) c[i] = 0;
-        for (uint32_t r = 0; r < C; ++r) {
-            const uint4 v = reinterpret_cast<const uint4*>(cl.map_shared_rank(s.hist, r))[unit];
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                c[2 * i] += w[i] & 0xFFFFu;
-                c[2 * i + 1] += w[i] >> 16;
+    auto count = [&](uint32_t bin) {  // over the row
+        uint32_t n = 0;
+        for (uint32_t r = 0; r < C; ++r) n += reinterpret_cast<const uint16_t*>(cl.map_shared_rank(s.hist, r))[bin];
+        return n;
+    };
+    if (warp == 0) {
+        // The policy, and the row's validity: a NaN or +Inf logit, nothing
+        // unmasked, a uniform or a parameter out of its range.
+        bool bad = !(Tf >= 0.0f) || isinf(Tf) || !(pf > 0.0f && pf <= 1.0f) || !(mf >= 0.0f && mf < 1.0f) ||
+                   !(uf >= 0.0f && uf < 1.0f) || nu == 0;
+        if (!bad) {
+            const uint32_t unit = lane < 8 ? s.units[0] : s.units[nu - 1];
+            const uint32_t used = __ballot_sync(kFull, lane < 16 && count(unit * kUnitBins + lane % 8) > 0);
+            const uint32_t first = s.units[0] * kUnitBins + __ffs(used & 0xFFu) - 1;
+            const uint32_t last = s.units[nu - 1] * kUnitBins + (31 - __clz(used >> 8));
+            bad = first <= kPosInf || last > kNegInf;
+            if (lane == 0) {
+                s.first_bin = first;
+                s.weights.top = bin_value<T>(first) * s.weights.pre;
             }
         }
-    };
-
-    // The policy, and the row's validity: a NaN or +Inf logit, nothing
-    // unmasked, a uniform or a parameter out of its range.
-    bool bad = !(Tf >= 0.0f) || isinf(Tf) || !(pf > 0.0f && pf <= 1.0f) || !(mf >= 0.0f && mf < 1.0f) ||
-               !(uf >= 0.0f && uf < 1.0f) || nu == 0;
-    float xmax = 0.0f;
-    uint32_t first_bin = 0;
-    if (!bad) {
-        uint32_t c[kUnitBins];
-        const uint32_t first = s.units[0], last = s.units[nu - 1];
-        counts(first, c);
-        uint32_t f = kUnitBins, l = 0;
-#pragma unroll
-        for (uint32_t b = kUnitBins; b-- > 0;)
-            if (c[b]) f = b;
-        counts(last, c);
-#pragma unroll
-        for (uint32_t b = 0; b < kUnitBins; ++b)
-            if (c[b]) l = b;
-        first_bin = first * kUnitBins + f;
-        xmax = bin_value<T>(first_bin);
-        bad = first_bin <= kPosInf || last * kUnitBins + l > kNegInf;
+        if (lane == 0) s.bad = bad;
     }
-    if (bad) {  // the same in every CTA of the cluster
+    __syncthreads();
+    if (s.bad) {  // the same in every CTA of the cluster
         if (rank == 0 && tid == 0) {
             a.out_ids[row] = SEL_INVALID_ID;
             a.out_probs[row] = __uint_as_float(0x7FC00000u);
@@ -343,282 +331,269 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
         return;
     }
     const bool greedy = Tf == 0.0f;
-    const Weights weight(xmax, greedy ? 1.0f : Tf, s.table);
+    const Weights weights = s.weights;
 
-    // This CTA's part of the list, and each thread's.
-    const uint32_t first = static_cast<uint32_t>(static_cast<uint64_t>(nu) * rank / C);
-    const uint32_t last = static_cast<uint32_t>(static_cast<uint64_t>(nu) * (rank + 1) / C);
-    const uint32_t per = (last - first + kNT - 1) / kNT;
-    const uint32_t i0 = min(last, first + tid * per), i1 = min(last, i0 + per);
-
-    // Counts and masses up to each thread's units, in order.
-    uint32_t c_in = 0, n_min = 0;
-    FF mass{0.0f, 0.0f};
-    for (uint32_t i = i0; i < i1; ++i) {
-        uint32_t c[kUnitBins];
-        const uint32_t unit = s.units[i];
-        counts(unit, c);
-#pragma unroll
-        for (uint32_t b = 0; b < kUnitBins; ++b) {
-            const FF w = weight(bin_value<T>(unit * kUnitBins + b));
-            if (c[b]) {
-                c_in += c[b];
-                mass = ff_add(mass, ff_mul_f(w, static_cast<float>(c[b])));
-                if (w.hi > mf || (w.hi == mf && w.lo >= 0.0f)) n_min += c[b];
-            }
-        }
-    }
-    double m_in = ff_to_double(mass);
-    n_min = __reduce_add_sync(kFull, n_min);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t tc = __shfl_up_sync(kFull, c_in, o);
-        const double tm = __shfl_up_sync(kFull, m_in, o);
-        if (lane >= static_cast<uint32_t>(o)) {
-            c_in += tc;
-            m_in += tm;
-        }
-    }
-    if (lane == 31) {
-        s.warp_c[warp] = c_in;
-        s.warp_m[warp] = m_in;
-    }
-    if (lane == 0) s.seg[warp] = n_min;
-    __syncthreads();
-    if (warp == 0) {
-        uint32_t wc = s.warp_c[lane];
-        double wm = s.warp_m[lane];
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t tc = __shfl_up_sync(kFull, wc, o);
-            const double tm = __shfl_up_sync(kFull, wm, o);
-            if (lane >= static_cast<uint32_t>(o)) {
-                wc += tc;
-                wm += tm;
-            }
-        }
-        s.warp_c[lane] = wc;
-        s.warp_m[lane] = wm;
-        n_min = __reduce_add_sync(kFull, s.seg[lane]);
-        wc = __shfl_sync(kFull, wc, 31);
-        wm = __shfl_sync(kFull, wm, 31);
-        if (lane < C) cl.map_shared_rank(s.totals, lane)[rank] = Totals{wm, wc, n_min};
-    }
-    cl.sync();
-    // sums before this CTA's units and over the row, in the same order everywhere
-    uint32_t c_base = 0, n_all = 0;
-    double m_base = 0.0, m_all = 0.0;
-    n_min = 0;
-    for (uint32_t r = 0; r < C; ++r) {
-        if (r == rank) {
-            c_base = n_all;
-            m_base = m_all;
-        }
-        n_all += s.totals[r].count;
-        m_all += s.totals[r].mass;
-        n_min += s.totals[r].min_count;
-    }
-    if (warp > 0) {
-        c_in += s.warp_c[warp - 1];
-        m_in += s.warp_m[warp - 1];
-    }
-    c_in += c_base;
-    m_in += m_base;
-    s.incl_c[tid] = c_in;
-    s.incl_m[tid] = m_in;
-    __syncthreads();
-    const uint32_t c_before = tid ? s.incl_c[tid - 1] : c_base, c_end = s.incl_c[kNT - 1];
-    const double m_before = tid ? s.incl_m[tid - 1] : m_base;
-
-    // A thread's bins in order: f(bin, count, weight, ids before, mass before)
-    // until it returns true.
-    auto walk = [&](auto f) {
-        uint32_t seen = c_before;
-        double m = m_before;
-        for (uint32_t i = i0; i < i1; ++i) {
-            uint32_t c[kUnitBins];
-            const uint32_t unit = s.units[i];
-            counts(unit, c);
-#pragma unroll
-            for (uint32_t b = 0; b < kUnitBins; ++b) {
-                if (c[b] == 0) continue;
-                const uint32_t bin = unit * kUnitBins + b;
-                const double w = ff_to_double(weight(bin_value<T>(bin)));
-                if (f(bin, c[b], w, seen, m)) return;
-                seen += c[b];
-                m += c[b] * w;
-            }
-        }
-    };
-    auto tell = [&](auto&& field, auto value) {  // the same word of every CTA
-        for (uint32_t r = 0; r < C; ++r) *cl.map_shared_rank(&field, r) = value;
-    };
-    // Mass of the first n ids of the order.
-    auto prefix_mass = [&](uint32_t n, int slot) {
-        if (n == n_all) return m_all;
-        if (c_base < n && n <= c_end) {
-            if (static_cast<int>(tid) == __syncthreads_count(c_in < n)) {
-                double mass = 0.0;
-                walk([&](uint32_t, uint32_t c, double w, uint32_t seen, double m) {
-                    mass = m + min(n - seen, c) * w;
-                    return seen + c >= n;
-                });
-                tell(s.d[slot], mass);
-            }
-        }
-        cl.sync();
-        return s.d[slot];
-    };
-    // Whether the first id whose cumulative mass reaches `goal` (over: exceeds
-    // it) is among this CTA's, its last one's when rounding leaves none.
-    auto reached = [&](double m, double goal, bool over) { return over ? m > goal : m >= goal; };
-    auto holds = [&](double goal, bool over) {
-        double m = 0.0;
-        uint32_t r = 0;
-        for (; r + 1 < C; ++r) {
-            m += s.totals[r].mass;
-            if (reached(m, goal, over)) break;
-        }
-        return r == rank;
-    };
-    // The thread that has it, and that id: its bin, its place among the bin's
-    // ids, its rank in the row.
-    auto find_mass = [&](double goal, bool over, auto f) {
-        if (!holds(goal, over)) return;
-        if (static_cast<int>(tid) != min(__syncthreads_count(!reached(m_in, goal, over)), kNT - 1)) return;
-        uint32_t bin = 0, place = 0, at = c_in;  // not found inside: the next thread's first id
-        double weight_of = 1.0;
-        walk([&](uint32_t b, uint32_t c, double w, uint32_t seen, double m) {
-            bin = b;
-            weight_of = w;
-            if (!reached(m + c * w, goal, over)) {
-                place = c - 1;
-                return false;
-            }
-            // w > 0 here; the r-th id (from 0) ends at m + (r + 1) w
-            const double r = over ? floor((goal - m) / w) : ceil((goal - m) / w) - 1.0;
-            place = static_cast<uint32_t>(fmin(fmax(r, 0.0), c - 1.0));
-            at = seen + place;
-            return true;
-        });
-        f(bin, place, at, weight_of);
-    };
-
-    if (greedy) {
-        if (tid == 0) {
-            s.u[kBin] = first_bin;
-            s.u[kPlace] = 0;
-            s.d[kProb] = 1.0;
-        }
-        __syncthreads();
-    } else {
-        const uint32_t n_k = kk == 0 ? n_all : min(kk, n_all);
-        const double Z = prefix_mass(n_k, kMassK);
-        uint32_t n = min(n_k, n_min);
-        if (pf < 1.0f) {
-            find_mass(static_cast<double>(pf) * Z, false,
-                      [&](uint32_t, uint32_t, uint32_t at, double) { tell(s.u[kRankP], at); });
-            cl.sync();
-            n = min(n, s.u[kRankP] + 1u);
-        }
-        const double Zs = n == n_k ? Z : prefix_mass(n, kMassN);
-        auto drawn = [&](uint32_t bin, uint32_t place, uint32_t at, double w) {
-            tell(s.u[kBin], bin);
-            tell(s.u[kPlace], place);
-            tell(s.u[kRank], at);
-            tell(s.d[kProb], w / Zs);
-        };
-        find_mass(static_cast<double>(uf) * Zs, true, drawn);
-        cl.sync();
-        if (s.u[kRank] >= n) {  // rounding left none: the last survivor
-            cl.sync();          // every CTA has read the rank
-            if (c_base < n && n <= c_end && static_cast<int>(tid) == __syncthreads_count(c_in < n)) {
-                walk([&](uint32_t b, uint32_t c, double w, uint32_t seen, double) {
-                    if (seen + c < n) return false;
-                    drawn(b, n - 1 - seen, n - 1, w);
-                    return true;
-                });
-            }
-            cl.sync();
-        }
-    }
-    const uint32_t bin = s.u[kBin];
-    uint32_t r = s.u[kPlace];
-    uint32_t owner = C;
-    for (uint32_t c = 0; c < C && owner == C; ++c) {
-        const uint32_t n = (cl.map_shared_rank(s.hist, c)[bin >> 1] >> (16 * (bin & 1))) & 0xFFFFu;
-        if (r < n) owner = c;
-        else r -= n;
-    }
-    if (owner == rank) {
-        auto hit = [&](uint32_t w, int half) {
-            const uint32_t b = half ? w >> 16 : w & 0xFFFFu;
-            return b == bin || (bin == kZeroBin && b == kMinusZeroBin);
-        };
-        auto hits = [&](const uint4& v) {
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            uint32_t n = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) n += hit(w[i >> 1], i & 1);
-            return n;
-        };
-        // ids rise with j, then the warp, the lane and the element
-#pragma unroll
-        for (int j = 0; j < kVPT; ++j) {
-            const uint32_t n = __reduce_add_sync(kFull, hits(q[j]));
-            if (lane == 0) s.seg[j * kWarps + warp] = n;
-        }
-        __syncthreads();
-        if (warp == 0) {
-            uint32_t sum = 0;
-#pragma unroll
-            for (int i = 0; i < kVPT; ++i) sum += s.seg[lane * kVPT + i];
-            uint32_t in = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t t = __shfl_up_sync(kFull, in, o);
-                if (lane >= static_cast<uint32_t>(o)) in += t;
-            }
-            uint32_t before = in - sum;
-            if (before <= r && r < in) {
-                uint32_t i = lane * kVPT;
-                while (r - before >= s.seg[i]) before += s.seg[i++];
-                s.find[0] = i;
-                s.find[1] = r - before;
-            }
-        }
-        __syncthreads();
-        const uint32_t seg = s.find[0];
-        r = s.find[1];
-        if (warp == seg % kWarps) {
-#pragma unroll
-            for (int j = 0; j < kVPT; ++j) {
-                if (static_cast<uint32_t>(j) != seg / kWarps) continue;
-                const uint32_t n = hits(q[j]);
-                uint32_t in = n;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const uint32_t t = __shfl_up_sync(kFull, in, o);
-                    if (lane >= static_cast<uint32_t>(o)) in += t;
-                }
-                uint32_t left = r - (in - n);
-                if (in - n <= r && r < in) {
-                    const uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if (hit(w[i >> 1], i & 1)) {
-                            if (left == 0) {
-                                a.out_ids[row] = (lo + j * kNT + tid) * 8u + i - skew;
-                                a.out_probs[row] = static_cast<float>(s.d[kProb]);
-                            }
-                            --left;
-                        }
+    // Entries of up to four units, shared between the CTAs; a lane a bin.
+    const uint32_t per = (nu + kEntries - 1) / kEntries, entries = (nu + per - 1) / per;
+    if (!greedy) {
+        const uint32_t e0 = entries * rank / C, e1 = entries * (rank + 1) / C;
+        uint32_t n_min = 0;
+        for (uint32_t base = e0 + warp * 4; base < e1; base += kWarps * 4) {
+            const uint32_t e = base + lane / 8;
+            uint32_t c = 0;
+            FF m{0.0f, 0.0f};
+            for (uint32_t g = 0; g < per; ++g) {
+                const uint32_t i = e * per + g;
+                if (e < e1 && i < nu) {
+                    const uint32_t bin = s.units[i] * kUnitBins + lane % 8, n = count(bin);
+                    const FF w = weights(bin_value<T>(bin), s.table);
+                    if (n) {
+                        c += n;
+                        m = ff_add(m, ff_mul_f(w, static_cast<float>(n)));
+                        if (w.hi > mf || (w.hi == mf && w.lo >= 0.0f)) n_min += n;
                     }
                 }
             }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) {
+                c += __shfl_xor_sync(kFull, c, o);
+                const FF other = ff_shfl_xor(m, o);
+                m = lane & o ? ff_add(other, m) : ff_add(m, other);
+            }
+            if (lane % 8 == 0 && e < e1) {
+                cl.map_shared_rank(s.entry_c, 0)[e] = c;
+                cl.map_shared_rank(s.entry_m, 0)[e] = m;
+            }
+        }
+        n_min = __reduce_add_sync(kFull, n_min);
+        if (lane == 0 && n_min) atomicAdd(cl.map_shared_rank(&s.n_min, 0), n_min);
+    }
+    cl.sync();
+
+    if (rank == 0) {
+        if (!greedy) {
+            // the entries' prefix sums, two a thread
+            uint32_t c[2];
+            FF m[2];
+#pragma unroll
+            for (uint32_t i = 0; i < 2; ++i) {
+                const uint32_t e = 2 * tid + i;
+                c[i] = e < entries ? s.entry_c[e] : 0u;
+                m[i] = e < entries ? s.entry_m[e] : FF{0.0f, 0.0f};
+            }
+            uint32_t wc = c[0] + c[1];
+            const FF both = ff_add(m[0], m[1]);
+            FF wm = ff_warp_scan(both);
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t n = __shfl_up_sync(kFull, wc, o);
+                if (lane >= static_cast<uint32_t>(o)) wc += n;
+            }
+            if (lane == 31) {
+                s.warp_c[warp] = wc;
+                s.warp_m[warp] = wm;
+            }
+            __syncthreads();
+            if (warp == 0) {
+                uint32_t tc = s.warp_c[lane];
+                const FF tm = ff_warp_scan(s.warp_m[lane]);
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t n = __shfl_up_sync(kFull, tc, o);
+                    if (lane >= static_cast<uint32_t>(o)) tc += n;
+                }
+                s.warp_c[lane] = tc;
+                s.warp_m[lane] = tm;
+            }
+            __syncthreads();
+            // up to the first and the second entry: what lies before the pair, and on
+            uint32_t before_c = wc - (c[0] + c[1]);
+            FF before_m = ff_shfl_up(wm, 1);
+            if (lane == 0) before_m = FF{0.0f, 0.0f};
+            if (warp > 0) {
+                before_c += s.warp_c[warp - 1];
+                before_m = ff_add(s.warp_m[warp - 1], before_m);
+            }
+            s.entry_c[2 * tid] = before_c + c[0];
+            s.entry_c[2 * tid + 1] = before_c + c[0] + c[1];
+            s.entry_m[2 * tid] = ff_add(before_m, m[0]);
+            s.entry_m[2 * tid + 1] = ff_add(before_m, both);
+            __syncthreads();
+        }
+        if (warp == 0) {
+            // Lane l holds bin l of an entry's up to 32; sums up to and with it.
+            struct Bins {
+                uint32_t bin, c;      // the lane's bin and its count
+                uint32_t c_before, c_in;
+                double w, m_before, m_in;
+            };
+            auto open = [&](uint32_t e) {
+                Bins b{};
+                const uint32_t i = e * per + lane / 8;
+                FF m{0.0f, 0.0f};
+                if (lane / 8 < per && i < nu) {
+                    b.bin = s.units[i] * kUnitBins + lane % 8;
+                    b.c = count(b.bin);
+                    const FF w = weights(bin_value<T>(b.bin), s.table);
+                    b.w = ff_to_double(w);
+                    if (b.c) m = ff_mul_f(w, static_cast<float>(b.c));
+                }
+                b.c_in = b.c;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t n = __shfl_up_sync(kFull, b.c_in, o);
+                    if (lane >= static_cast<uint32_t>(o)) b.c_in += n;
+                }
+                const FF scan = ff_warp_scan(m);
+                if (e) b.c_in += s.entry_c[e - 1];
+                b.m_in = ff_to_double(e ? ff_add(s.entry_m[e - 1], scan) : scan);
+                b.c_before = b.c_in - b.c;
+                b.m_before = __shfl_up_sync(kFull, b.m_in, 1);
+                if (lane == 0) b.m_before = e ? ff_to_double(s.entry_m[e - 1]) : 0.0;
+                return b;
+            };
+            // The first entry for which `past` holds, the last one when none does.
+            auto first_entry = [&](auto past) {
+                const uint32_t coarse = __ballot_sync(kFull, past(lane * kCoarse + kCoarse - 1));
+                const uint32_t at = (coarse ? __ffs(coarse) - 1 : 31) * kCoarse;
+                uint32_t e = at + kCoarse - 1;
+#pragma unroll
+                for (uint32_t i = kCoarse / 32; i-- > 0;) {
+                    const uint32_t fine = __ballot_sync(kFull, past(at + i * 32 + lane));
+                    if (fine) e = at + i * 32 + __ffs(fine) - 1;
+                }
+                return min(e, entries - 1);
+            };
+            const uint32_t n_all = s.entry_c[kEntries - 1];
+            const double m_all = ff_to_double(s.entry_m[kEntries - 1]);
+            auto prefix_mass = [&](uint32_t n) {  // of the first n ids of the order
+                if (n == n_all) return m_all;
+                const Bins b = open(first_entry([&](uint32_t e) { return s.entry_c[e] >= n; }));
+                const int l = __ffs(__ballot_sync(kFull, b.c_in >= n)) - 1;
+                return __shfl_sync(kFull, b.m_before + (n - b.c_before) * b.w, l);
+            };
+            // The first id whose cumulative mass reaches `goal` (over: exceeds
+            // it): its lane, its place among the bin's ids; and its rank.
+            auto by_mass = [&](double goal, bool over, Bins& b, uint32_t& place, int& l) {
+                auto past = [&](double m) { return over ? m > goal : m >= goal; };
+                b = open(first_entry([&](uint32_t e) { return past(ff_to_double(s.entry_m[e])); }));
+                const uint32_t hit = __ballot_sync(kFull, b.c > 0 && past(b.m_in));
+                // (rounding may leave none: the entry's last id)
+                l = hit ? __ffs(hit) - 1 : 31 - __clz(__ballot_sync(kFull, b.c > 0));
+                // the r-th id of the bin (from 0) ends at m_before + (r + 1) w
+                const double r = over ? floor((goal - b.m_before) / b.w) : ceil((goal - b.m_before) / b.w) - 1.0;
+                place = hit ? static_cast<uint32_t>(fmin(fmax(r, 0.0), b.c - 1.0)) : b.c - 1u;
+                place = __shfl_sync(kFull, place, l);
+                return __shfl_sync(kFull, b.c_before, l) + place;
+            };
+
+            uint32_t bin = s.first_bin, place = 0;
+            double prob = 1.0;
+            if (!greedy) {
+                const uint32_t n_k = kk == 0 ? n_all : min(kk, n_all);
+                const double Z = prefix_mass(n_k);
+                uint32_t n = min(n_k, s.n_min);
+                Bins b;
+                int l;
+                if (pf < 1.0f) n = min(n, by_mass(static_cast<double>(pf) * Z, false, b, place, l) + 1u);
+                const double Zs = n == n_k ? Z : prefix_mass(n);
+                if (by_mass(static_cast<double>(uf) * Zs, true, b, place, l) >= n) {
+                    // rounding: the last survivor
+                    b = open(first_entry([&](uint32_t e) { return s.entry_c[e] >= n; }));
+                    l = __ffs(__ballot_sync(kFull, b.c_in >= n)) - 1;
+                    place = __shfl_sync(kFull, n - 1u - b.c_before, l);
+                }
+                bin = __shfl_sync(kFull, b.bin, l);
+                prob = __shfl_sync(kFull, b.w, l) / Zs;
+            }
+            // the CTA that holds it: ids rise with the CTAs
+            const uint32_t c = lane < C ? reinterpret_cast<const uint16_t*>(cl.map_shared_rank(s.hist, lane))[bin] : 0u;
+            uint32_t in = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t n = __shfl_up_sync(kFull, in, o);
+                if (lane >= static_cast<uint32_t>(o)) in += n;
+            }
+            const int owner = __ffs(__ballot_sync(kFull, place < in)) - 1;
+            place = __shfl_sync(kFull, place - (in - c), owner);
+            if (lane < C) {
+                Shared& o = *cl.map_shared_rank(&s, lane);
+                o.bin = bin;
+                o.owner = owner;
+                o.place = place;
+                o.prob = static_cast<float>(prob);
+            }
         }
     }
-    cl.sync();  // no CTA leaves while another reads its histogram
+    cl.sync();
+    if (rank != s.owner) return;
+
+    // The place-th id of the bin in this CTA's registers: ids rise with j, then
+    // the warp, the lane and the element.
+    const uint32_t bin = s.bin, pattern = bin * 0x00010001u;
+    uint32_t r = s.place;
+    auto flags = [&](uint32_t w) {  // bits 0 and 16: the halves that match
+        uint32_t f = __vcmpeq2(w, pattern);
+        if (bin == kZeroBin) f |= __vcmpeq2(w, kMinusZeroBin * 0x00010001u);
+        return f & 0x00010001u;
+    };
+    auto hits = [&](const uint4& v) {
+        const uint32_t f = flags(v.x) + flags(v.y) + flags(v.z) + flags(v.w);
+        return (f & 0xFFFFu) + (f >> 16);
+    };
+#pragma unroll
+    for (int j = 0; j < kVPT; ++j) {
+        const uint32_t n = __reduce_add_sync(kFull, hits(q[j]));
+        if (lane == 0) s.seg[j * kWarps + warp] = n;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        uint32_t sum = 0;
+#pragma unroll
+        for (int i = 0; i < kVPT; ++i) sum += s.seg[lane * kVPT + i];
+        uint32_t in = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t n = __shfl_up_sync(kFull, in, o);
+            if (lane >= static_cast<uint32_t>(o)) in += n;
+        }
+        uint32_t before = in - sum;
+        if (before <= r && r < in) {
+            uint32_t i = lane * kVPT;
+            while (r - before >= s.seg[i]) before += s.seg[i++];
+            s.find[0] = i;
+            s.find[1] = r - before;
+        }
+    }
+    __syncthreads();
+    const uint32_t seg = s.find[0];
+    r = s.find[1];
+    if (warp != seg % kWarps) return;
+#pragma unroll
+    for (int j = 0; j < kVPT; ++j) {
+        if (static_cast<uint32_t>(j) != seg / kWarps) continue;
+        const uint32_t n = hits(q[j]);
+        uint32_t in = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t m = __shfl_up_sync(kFull, in, o);
+            if (lane >= static_cast<uint32_t>(o)) in += m;
+        }
+        uint32_t left = r - (in - n);
+        if (in - n <= r && r < in) {
+            const uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (flags(w[i >> 1]) >> (16 * (i & 1)) & 1) {
+                    if (left == 0) {
+                        a.out_ids[row] = (lo + j * kNT + tid) * 8u + i - skew;
+                        a.out_probs[row] = s.prob;
+                    }
+                    --left;
+                }
+            }
+        }
+    }
 }
 
 template <typename T>
