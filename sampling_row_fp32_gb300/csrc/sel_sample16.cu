@@ -10,22 +10,25 @@
 // are sums of count * w in 64 bits, and the drawn id is the r-th id of one
 // pattern.
 //
-// One cluster of C CTAs per row. Each CTA reads its share of the row once,
-// into registers, and counts it into a histogram of 65,536 16-bit counters in
-// its shared memory (a share holds fewer than 65,536 ids, so no counter
-// overflows). After a cluster barrier the CTAs share the row's non-empty bins
-// between them, a lane a bin, and sum counts (through distributed shared
-// memory) and masses of up to 2,048 entries in the first CTA. There one warp
-// finds every border (of top-k, top-p, the draw): ballots over the entries'
-// prefix sums, then the 32 bins of the entry. The CTA whose share holds the
-// drawn id finds it in its registers.
+// One cluster of C CTAs per row. Each CTA counts its share of the row into a
+// histogram of 65,536 16-bit counters in its shared memory. After a cluster
+// barrier the CTAs share the row's non-empty bins between them, a lane a bin,
+// and sum counts (through distributed shared memory) and masses of up to
+// 2,048 entries in the first CTA. There one warp finds every border (of top-k,
+// top-p, the draw): ballots over the entries' prefix sums, then the 32 bins of
+// the entry. The CTA whose share holds the drawn id reads it again, up to it.
 //
-// FP64 runs at two results a clock and SM here, so only that one warp uses it:
-// a single FP64 addition by all 32 warps costs 460 clocks.
+// A counter that overflows (a value that more than 65,535 ids of a share have)
+// makes the counters' sum differ from the ids counted; the share is then
+// counted again in batches, and counters past half are taken down in between.
+//
+// Masses are pairs of floats: FP64 runs at two results a clock and SM here.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <cooperative_groups.h>
+
+#include <type_traits>
 
 #include "sel.h"
 #include "sel_common.cuh"
@@ -40,17 +43,18 @@ namespace {
 
 constexpr int kNT = 1024;
 constexpr int kWarps = kNT / 32;
-constexpr int kVPT = 8;                     // 16-byte vectors a thread holds
-constexpr uint32_t kShareVecs = 8191;       // vectors a CTA takes at most: 65,528 ids
+constexpr int kAhead = 4;                   // 16-byte vectors a thread loads ahead
 constexpr uint32_t kMaxCluster = 8;
+constexpr uint32_t kBatchVecs = 4095;       // vectors whose ids overflow no counter below half
+constexpr uint32_t kHalf = 32768;
+constexpr uint32_t kMaxHeavy = SEL_SAMPLE16_MAX_V / kHalf + 1;
 constexpr uint32_t kBins = 65536;
 constexpr uint32_t kUnitBins = 8;           // a 16-byte unit of the histogram
 constexpr uint32_t kUnits = kBins / kUnitBins;
 constexpr uint32_t kWords = kUnits / 32;    // occupancy bitmap
 constexpr uint32_t kZeroBin = 0x7FFF;       // +0
 constexpr uint32_t kMinusZeroBin = 0x8000;  // -0, counted as +0
-static_assert(kShareVecs * 8 < 65536 && kShareVecs <= kNT * kVPT);
-static_assert(static_cast<uint64_t>(kMaxCluster) * kShareVecs * 8 >= SEL_SAMPLE16_MAX_V + 7ull);
+static_assert(kBatchVecs * 8 + kHalf <= 65536);
 
 // Bin of a bit pattern: descending by value, so bin 0 side is the largest.
 // (For two patterns packed in a word.)
@@ -104,7 +108,8 @@ struct ExpTable {
         }
     }
 };
-__constant__ const ExpTable kExpTable;
+// (in global memory: constant memory serves one address a request)
+__device__ const ExpTable kExpTable;
 
 struct Weights {
     float top;            // the row's largest logit, times `pre`
@@ -157,24 +162,28 @@ struct SampleArgs {
     uint32_t* out_ids;
     float* out_probs;
     uint32_t V;
+    uint32_t ctas;   // of a row's cluster
     uint32_t share;  // vectors a CTA takes
 };
 
 constexpr uint32_t kEntries = 2048;             // at most; of up to four units, a lane a bin
-constexpr uint32_t kCoarse = kEntries / 32;     // entries a lane of the deciding warp looks at first
-static_assert(kUnits <= kEntries * 4 && kEntries == 2 * kNT);
+constexpr uint32_t kCoarse = kEntries / kWarps;  // entries of a warp's prefix sums
+static_assert(kUnits <= kEntries * 4 && kCoarse == 64);
 
 struct Shared {
     uint32_t hist[kBins / 2];
     uint16_t units[kUnits];   // the row's non-empty units, in bin order
     float2 table[kTable];
     uint32_t entry_c[kEntries];  // in the row's first CTA: counts and masses of the entries,
-    FF entry_m[kEntries];        // then up to and with each entry
+    FF entry_m[kEntries];        // then up to and with each entry within its 64
     uint32_t bits[kWords];    // occupancy: bit l of word w is unit 32 w + l
     uint32_t off[kWords];
-    FF warp_m[kWarps];
+    uint32_t row_bits[kWords];
+    FF warp_m[kWarps];        // of 64 entries
     uint32_t warp_c[kWarps];
-    uint32_t seg[kVPT * kWarps];
+    uint32_t seg[kAhead * kWarps];
+    uint32_t heavy[kMaxHeavy];  // bins with 32,768 ids more than their counter says, once for each
+    uint32_t heavies, counted, n_bits, any_heavy;
     Weights weights;
     uint32_t n_min;           // ids that min-p leaves
     uint32_t first_bin;       // the largest logit's
@@ -184,47 +193,31 @@ struct Shared {
     uint32_t find[2];
 };
 
+// A vector of 16 bytes where `on` holds, else four times `fill`: without a
+// branch, so that a thread's loads are all on their way together.
+__device__ __forceinline__ uint4 load_or(const void* p, bool on, uint32_t fill) {
+    uint4 v;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %5, 0;\n\t"
+        "mov.b32 %0, %6;\n\tmov.b32 %1, %6;\n\tmov.b32 %2, %6;\n\tmov.b32 %3, %6;\n\t"
+        "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+        : "l"(p), "r"(static_cast<uint32_t>(on)), "r"(fill));
+    return v;
+}
+
+// A CTA's share of a row, as 16-byte vectors from the aligned address at or
+// below the row's start; `skew` ids of the first vector are not the row's.
 template <typename T>
-__global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
-    extern __shared__ __align__(16) unsigned char smem_raw[];
-    Shared& s = *reinterpret_cast<Shared*>(smem_raw);
-    cg::cluster_group cl = cg::this_cluster();
-    const uint32_t C = cl.num_blocks(), rank = cl.block_rank();
-    const uint32_t row = blockIdx.x / C;
-    const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr uint32_t kPosInf = 0x7FFFu - Kind<T>::kInf;     // this bin and lower: +Inf, NaN
-    constexpr uint32_t kNegInf = 0x8000u | Kind<T>::kInf;     // masked; higher bins: NaN
-    constexpr uint32_t kFill = kNegInf | (kNegInf << 16);
+struct Share {
+    const uint16_t* x;
+    uint32_t V, skew, lo, hi;  // vectors [lo, hi)
 
-    uint4* h4 = reinterpret_cast<uint4*>(s.hist);
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(kUnits / kNT); ++i) h4[i * kNT + tid] = make_uint4(0, 0, 0, 0);
-    if (tid < kTable) s.table[tid] = kExpTable.v[tid];
-    if (tid == 0) s.n_min = 0;
-    pdl_wait();
-
-    // The row as 16-byte vectors from the aligned address at or below its
-    // start; `skew` ids of the first vector are not the row's. Vectors that
-    // reach over either end of the row are read by element.
-    const uint16_t* x = static_cast<const uint16_t*>(a.logits) + static_cast<uint64_t>(row) * a.ld;
-    const uint32_t skew = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(x) & 15u) / 2u;
-    const uint32_t vecs = (a.V + skew + 7u) / 8u;
-    const uint32_t lo = rank * a.share, hi = min(vecs, lo + a.share);
-    const uint32_t full_lo = max(lo, skew ? 1u : 0u), full_hi = min(hi, (a.V + skew) / 8u);
-    uint4 q[kVPT];
-#pragma unroll
-    for (int j = 0; j < kVPT; ++j) {
-        const uint32_t v = lo + j * kNT + tid;
-        q[j] = make_uint4(kFill, kFill, kFill, kFill);
-        if (v >= full_lo && v < full_hi) q[j] = ldg_stream16(x - skew + static_cast<uint64_t>(v) * 8u);
-    }
-    const float Tf = a.temperature ? a.temperature[row] : 1.0f;
-    const uint32_t kk = a.top_k ? a.top_k[row] : 0u;
-    const float pf = a.top_p ? a.top_p[row] : 1.0f;
-    const float mf = a.min_p ? a.min_p[row] : 0.0f;
-    const float uf = a.uniforms[row];
-    auto edge = [&](uint32_t v) {  // the vector v, if it is this thread's
-        if (v < lo || v >= hi || (v - lo) % kNT != tid) return;
+    // Bins of vector v, masked ids (and those outside the row) as -Inf's bin.
+    // Vectors that reach over an end of the row are read by element.
+    __device__ __forceinline__ uint4 edge(uint32_t v) const {
+        constexpr uint32_t kNegInf = 0x8000u | Kind<T>::kInf;
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -232,53 +225,176 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int64_t e = static_cast<int64_t>(v) * 8 - skew + 2 * i + h;
-                w[i] |= (e >= 0 && e < a.V ? x[e] : kNegInf) << (16 * h);
+                w[i] |= (e >= 0 && e < V ? x[e] : kNegInf) << (16 * h);
             }
         }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // f(v, bins) for vectors base + tid, + kNT, ... below end; kAhead at a time,
+    // the next ones on their way. f returns nothing.
+    template <typename F>
+    __device__ __forceinline__ void each(uint32_t base, uint32_t end, F f) const {
+        constexpr uint32_t kNegInf = 0x8000u | Kind<T>::kInf, kFill = kNegInf | (kNegInf << 16);
+        const uint32_t full_lo = skew ? 1u : 0u, full_hi = (V + skew) / 8u;
+        const uint16_t* origin = x - skew;
+        uint4 next[kAhead];
+        auto load = [&](uint32_t at) {
 #pragma unroll
-        for (int j = 0; j < kVPT; ++j)
-            if ((v - lo) / kNT == static_cast<uint32_t>(j)) q[j] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int j = 0; j < kAhead; ++j) {
+                const uint32_t v = at + j * kNT + threadIdx.x;
+                next[j] = load_or(origin + static_cast<uint64_t>(v) * 8u, v >= full_lo && v < full_hi && v < end, kFill);
+            }
+        };
+        load(base);
+        for (uint32_t at = base; at < end; at += kAhead * kNT) {
+            uint4 q[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) q[j] = next[j];
+            load(at + kAhead * kNT);
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const uint32_t v = at + j * kNT + threadIdx.x;
+                if (v < end && (v < full_lo || v >= full_hi)) q[j] = edge(v);
+                f(j, make_uint4(bins_of(q[j].x), bins_of(q[j].y), bins_of(q[j].z), bins_of(q[j].w)));
+            }
+        }
+    }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    Shared& s = *reinterpret_cast<Shared*>(smem_raw);
+    cg::cluster_group cl = cg::this_cluster();
+    const uint32_t C = a.ctas, rank = C > 1 ? cl.block_rank() : 0u;
+    const uint32_t row = blockIdx.x / C;
+    const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr uint32_t kPosInf = 0x7FFFu - Kind<T>::kInf;     // this bin and lower: +Inf, NaN
+    constexpr uint32_t kNegInf = 0x8000u | Kind<T>::kInf;     // masked; higher bins: NaN
+    auto cluster_sync = [&] {
+        if (C > 1) cl.sync();
+        else __syncthreads();
     };
-    if (skew) edge(0);
-    if ((a.V + skew) % 8u && (vecs > 1 || !skew)) edge(vecs - 1);
+    auto peer = [&](auto* p, uint32_t r) { return C > 1 ? cl.map_shared_rank(p, r) : p; };
+
+    uint4* h4 = reinterpret_cast<uint4*>(s.hist);
+    auto clear = [&] {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(kUnits / kNT); ++i) h4[i * kNT + tid] = make_uint4(0, 0, 0, 0);
+    };
+    clear();
+    if (tid < kTable) s.table[tid] = kExpTable.v[tid];
+    if (tid == 0) s.n_min = s.heavies = s.counted = s.n_bits = s.any_heavy = 0;
+    pdl_wait();
+
+    Share<T> share;
+    share.x = static_cast<const uint16_t*>(a.logits) + static_cast<uint64_t>(row) * a.ld;
+    share.V = a.V;
+    share.skew = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(share.x) & 15u) / 2u;
+    share.lo = rank * a.share;
+    share.hi = max(share.lo, min((a.V + share.skew + 7u) / 8u, share.lo + a.share));
+    const float Tf = a.temperature ? a.temperature[row] : 1.0f;
+    const uint32_t kk = a.top_k ? a.top_k[row] : 0u;
+    const float pf = a.top_p ? a.top_p[row] : 1.0f;
+    const float mf = a.min_p ? a.min_p[row] : 0.0f;
+    const float uf = a.uniforms[row];
     pdl_trigger();
-    if (tid == 32) s.weights.temperature(Tf > 0.0f ? Tf : 1.0f);
     __syncthreads();  // the histogram is clear
 
+    // Count; returns how many ids the thread counted (tally).
+    auto count_share = [&](uint32_t base, uint32_t end, auto tally) {
+        uint32_t n = 0;
+        share.each(base, end, [&](int, const uint4& q) {
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-    for (int j = 0; j < kVPT; ++j) {
-        uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t d = bins_of(w[i]);
-            const uint32_t d0 = d & 0xFFFFu, d1 = d >> 16;
-            if (d0 != kNegInf) atomicAdd(&s.hist[d0 >> 1], 1u << (16 * (d0 & 1)));
-            if (d1 != kNegInf) atomicAdd(&s.hist[d1 >> 1], 1u << (16 * (d1 & 1)));
-            w[i] = d;
-        }
-        q[j] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t d0 = w[i] & 0xFFFFu, d1 = w[i] >> 16;
+                if (d0 != kNegInf) {
+                    atomicAdd(&s.hist[d0 >> 1], 1u << (16 * (d0 & 1)));
+                    if (tally.value) ++n;
+                }
+                if (d1 != kNegInf) {
+                    atomicAdd(&s.hist[d1 >> 1], 1u << (16 * (d1 & 1)));
+                    if (tally.value) ++n;
+                }
+            }
+        });
+        return n;
+    };
+    // fewer than 65,536 ids: no counter can overflow
+    const bool small = share.hi - share.lo <= kBatchVecs * 2;
+    if (small) {
+        count_share(share.lo, share.hi, std::false_type{});
+    } else {
+        const uint32_t n = __reduce_add_sync(kFull, count_share(share.lo, share.hi, std::true_type{}));
+        if (lane == 0) atomicAdd(&s.counted, n);
     }
+    if (tid == 32) s.weights.temperature(Tf > 0.0f ? Tf : 1.0f);
     __syncthreads();
-    if (tid == 0) {
-        // -0 ties with +0: one bin (bins 0x7FFF and 0x8000)
+    auto merge_zeros = [&] {  // -0 ties with +0: one bin (bins 0x7FFF and 0x8000)
         const uint32_t neg = s.hist[kMinusZeroBin / 2] & 0xFFFFu;
-        s.hist[kMinusZeroBin / 2] -= neg;
-        s.hist[kZeroBin / 2] += neg << 16;
-    }
+        const uint32_t pos = s.hist[kZeroBin / 2] >> 16;
+        if (pos + neg < 65536u) {
+            s.hist[kMinusZeroBin / 2] -= neg;
+            s.hist[kZeroBin / 2] += neg << 16;
+        } else {
+            s.counted = 0;  // counted again below
+        }
+    };
+    if (tid == 0) merge_zeros();
     __syncthreads();
+    auto occupancy = [&] {
+        uint32_t sum = 0;
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(kUnits / kNT); ++i) {
-        const uint32_t word = i * kWarps + warp;
-        const uint4 v = h4[word * 32 + lane];
-        const uint32_t b = __ballot_sync(kFull, (v.x | v.y | v.z | v.w) != 0);
-        if (lane == 0) s.bits[word] = b;
+        for (int i = 0; i < static_cast<int>(kUnits / kNT); ++i) {
+            const uint32_t word = i * kWarps + warp;
+            const uint4 v = h4[word * 32 + lane];
+            const uint32_t b = __ballot_sync(kFull, (v.x | v.y | v.z | v.w) != 0);
+            if (lane == 0) s.bits[word] = b;
+            sum += (v.x & 0xFFFFu) + (v.x >> 16) + (v.y & 0xFFFFu) + (v.y >> 16) + (v.z & 0xFFFFu) + (v.z >> 16) +
+                   (v.w & 0xFFFFu) + (v.w >> 16);
+        }
+        return __reduce_add_sync(kFull, sum);
+    };
+    if (small) {
+        (void)occupancy();
+        __syncthreads();
+    } else {
+        const uint32_t sum = occupancy();
+        if (lane == 0) atomicAdd(&s.n_bits, sum);
+        __syncthreads();
+        if (s.n_bits != s.counted) {
+            // Some counter overflowed (each overflow takes 65,535 or 65,536 from the
+            // sum): again in batches, none of which overflows a counter below half.
+            __syncthreads();
+            clear();
+            __syncthreads();
+            for (uint32_t at = share.lo; at < share.hi; at += kBatchVecs) {
+                count_share(at, min(share.hi, at + kBatchVecs), std::false_type{});
+                __syncthreads();
+                if (tid == 0) merge_zeros();
+                __syncthreads();
+                for (uint32_t i = tid; i < kBins / 2; i += kNT) {
+                    const uint32_t w = s.hist[i], over = w & 0x80008000u;
+                    if (over) {
+                        s.hist[i] = w - over;
+                        if (over & 0x8000u) s.heavy[atomicAdd(&s.heavies, 1u)] = 2 * i;
+                        if (over >> 31) s.heavy[atomicAdd(&s.heavies, 1u)] = 2 * i + 1;
+                    }
+                }
+                __syncthreads();
+            }
+            (void)occupancy();
+            __syncthreads();
+            if (tid < s.heavies) atomicOr(&s.bits[s.heavy[tid] / (kUnitBins * 32)], 1u << (s.heavy[tid] / kUnitBins % 32));
+        }
     }
-    cl.sync();
+    cluster_sync();
 
     // The row's non-empty units, in order.
-    uint32_t word = 0;
     if (tid < kWords) {
-        for (uint32_t r = 0; r < C; ++r) word |= cl.map_shared_rank(s.bits, r)[tid];
+        uint32_t word = 0;
+        for (uint32_t r = 0; r < C; ++r) word |= peer(s.bits, r)[tid];
         uint32_t in = __popc(word);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -286,21 +402,32 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
             if (lane >= static_cast<uint32_t>(o)) in += n;
         }
         s.off[tid] = in;  // up to and with this word, in its 32
-        s.seg[tid] = word;
+        s.row_bits[tid] = word;
+    } else if (tid < kWords + C) {
+        if (*peer(&s.heavies, tid - kWords)) s.any_heavy = 1;
     }
     __syncthreads();
     uint32_t nu = 0;
 #pragma unroll
     for (int i = 0; i < static_cast<int>(kUnits / kNT); ++i) {
-        const uint32_t w = i * kWarps + warp, m = s.seg[w], before = s.off[w] - __popc(m);
+        const uint32_t w = i * kWarps + warp, m = s.row_bits[w], before = s.off[w] - __popc(m);
         if (m >> lane & 1) s.units[nu + before + __popc(m & ((1u << lane) - 1u))] = static_cast<uint16_t>(w * 32 + lane);
         nu += s.off[i * kWarps + 31];
     }
     __syncthreads();
 
+    const bool any_heavy = s.any_heavy != 0;
+    auto count_of = [&](uint32_t bin, uint32_t r) {  // in CTA r
+        uint32_t n = reinterpret_cast<const uint16_t*>(peer(s.hist, r))[bin];
+        if (any_heavy) {
+            const uint32_t* heavy = peer(s.heavy, r);
+            for (uint32_t i = 0; i < *peer(&s.heavies, r); ++i) n += heavy[i] == bin ? kHalf : 0u;
+        }
+        return n;
+    };
     auto count = [&](uint32_t bin) {  // over the row
         uint32_t n = 0;
-        for (uint32_t r = 0; r < C; ++r) n += reinterpret_cast<const uint16_t*>(cl.map_shared_rank(s.hist, r))[bin];
+        for (uint32_t r = 0; r < C; ++r) n += count_of(bin, r);
         return n;
     };
     if (warp == 0) {
@@ -327,7 +454,7 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
             a.out_ids[row] = SEL_INVALID_ID;
             a.out_probs[row] = __uint_as_float(0x7FC00000u);
         }
-        cl.sync();  // no CTA leaves while another reads its histogram
+        cluster_sync();  // no CTA leaves while another reads its histogram
         return;
     }
     const bool greedy = Tf == 0.0f;
@@ -361,82 +488,98 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
                 m = lane & o ? ff_add(other, m) : ff_add(m, other);
             }
             if (lane % 8 == 0 && e < e1) {
-                cl.map_shared_rank(s.entry_c, 0)[e] = c;
-                cl.map_shared_rank(s.entry_m, 0)[e] = m;
+                peer(s.entry_c, 0)[e] = c;
+                peer(s.entry_m, 0)[e] = m;
             }
         }
         n_min = __reduce_add_sync(kFull, n_min);
-        if (lane == 0 && n_min) atomicAdd(cl.map_shared_rank(&s.n_min, 0), n_min);
+        if (lane == 0 && n_min) atomicAdd(peer(&s.n_min, 0), n_min);
     }
-    cl.sync();
+    cluster_sync();
 
     if (rank == 0) {
         if (!greedy) {
-            // the entries' prefix sums, two a thread
-            uint32_t c[2];
-            FF m[2];
-#pragma unroll
-            for (uint32_t i = 0; i < 2; ++i) {
-                const uint32_t e = 2 * tid + i;
-                c[i] = e < entries ? s.entry_c[e] : 0u;
-                m[i] = e < entries ? s.entry_m[e] : FF{0.0f, 0.0f};
-            }
-            uint32_t wc = c[0] + c[1];
-            const FF both = ff_add(m[0], m[1]);
-            FF wm = ff_warp_scan(both);
+            // prefix sums of each 64 entries, two a lane
+            const uint32_t e = 2 * tid;
+            const uint32_t c0 = e < entries ? s.entry_c[e] : 0u, c1 = e + 1 < entries ? s.entry_c[e + 1] : 0u;
+            const FF m0 = e < entries ? s.entry_m[e] : FF{0.0f, 0.0f};
+            const FF m1 = e + 1 < entries ? s.entry_m[e + 1] : FF{0.0f, 0.0f};
+            uint32_t wc = c0 + c1;
+            const FF both = ff_add(m0, m1);
+            const FF wm = ff_warp_scan(both);
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const uint32_t n = __shfl_up_sync(kFull, wc, o);
                 if (lane >= static_cast<uint32_t>(o)) wc += n;
             }
+            FF before = ff_shfl_up(wm, 1);
+            if (lane == 0) before = FF{0.0f, 0.0f};
+            s.entry_c[e] = wc - c1;
+            s.entry_c[e + 1] = wc;
+            s.entry_m[e] = ff_add(before, m0);
+            s.entry_m[e + 1] = wm;
             if (lane == 31) {
                 s.warp_c[warp] = wc;
                 s.warp_m[warp] = wm;
             }
             __syncthreads();
-            if (warp == 0) {
-                uint32_t tc = s.warp_c[lane];
-                const FF tm = ff_warp_scan(s.warp_m[lane]);
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const uint32_t n = __shfl_up_sync(kFull, tc, o);
-                    if (lane >= static_cast<uint32_t>(o)) tc += n;
-                }
-                s.warp_c[lane] = tc;
-                s.warp_m[lane] = tm;
-            }
-            __syncthreads();
-            // up to the first and the second entry: what lies before the pair, and on
-            uint32_t before_c = wc - (c[0] + c[1]);
-            FF before_m = ff_shfl_up(wm, 1);
-            if (lane == 0) before_m = FF{0.0f, 0.0f};
-            if (warp > 0) {
-                before_c += s.warp_c[warp - 1];
-                before_m = ff_add(s.warp_m[warp - 1], before_m);
-            }
-            s.entry_c[2 * tid] = before_c + c[0];
-            s.entry_c[2 * tid + 1] = before_c + c[0] + c[1];
-            s.entry_m[2 * tid] = ff_add(before_m, m[0]);
-            s.entry_m[2 * tid + 1] = ff_add(before_m, both);
-            __syncthreads();
         }
         if (warp == 0) {
-            // Lane l holds bin l of an entry's up to 32; sums up to and with it.
+            // sums up to and with the lane's 64 entries, and before them
+            uint32_t seg_c = 0, seg_c0 = 0;
+            FF seg_m{0.0f, 0.0f}, seg_m0{0.0f, 0.0f};
+            if (!greedy) {
+                seg_c = s.warp_c[lane];
+                seg_m = ff_warp_scan(s.warp_m[lane]);
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t n = __shfl_up_sync(kFull, seg_c, o);
+                    if (lane >= static_cast<uint32_t>(o)) seg_c += n;
+                }
+                seg_c0 = __shfl_up_sync(kFull, seg_c, 1);
+                seg_m0 = ff_shfl_up(seg_m, 1);
+                if (lane == 0) {
+                    seg_c0 = 0;
+                    seg_m0 = FF{0.0f, 0.0f};
+                }
+            }
+            const uint32_t n_all = __shfl_sync(kFull, seg_c, 31);
+            const FF m_all = ff_shfl(seg_m, 31);
+            // Lane l holds bin l of an entry's up to 32; sums before and with it.
             struct Bins {
-                uint32_t bin, c;      // the lane's bin and its count
-                uint32_t c_before, c_in;
-                double w, m_before, m_in;
+                uint32_t bin, c, c_before, c_in;
+                FF w, m_before, m_in;
             };
-            auto open = [&](uint32_t e) {
+            // The bins of the first entry for which past(count, mass up to and with
+            // it) holds, of the last one when none does.
+            auto open = [&](auto past) {
+                const uint32_t coarse = __ballot_sync(kFull, past(seg_c, seg_m));
+                const int sg = coarse ? __ffs(coarse) - 1 : 31;
+                const uint32_t c0 = __shfl_sync(kFull, seg_c0, sg);
+                const FF m0 = ff_shfl(seg_m0, sg);
+                uint32_t e = sg * kCoarse + kCoarse - 1;
+#pragma unroll
+                for (int i = static_cast<int>(kCoarse / 32) - 1; i >= 0; --i) {
+                    const uint32_t at = sg * kCoarse + i * 32 + lane;
+                    const uint32_t fine = __ballot_sync(kFull, past(c0 + s.entry_c[at], ff_add(m0, s.entry_m[at])));
+                    if (fine) e = sg * kCoarse + i * 32 + __ffs(fine) - 1;
+                }
+                e = min(e, entries - 1);
+                const uint32_t first = e / kCoarse * kCoarse;  // (e may lie before the segment by that)
+                uint32_t c_base = __shfl_sync(kFull, seg_c0, e / kCoarse);
+                FF m_base = ff_shfl(seg_m0, e / kCoarse);
+                if (e > first) {
+                    c_base += s.entry_c[e - 1];
+                    m_base = ff_add(m_base, s.entry_m[e - 1]);
+                }
                 Bins b{};
                 const uint32_t i = e * per + lane / 8;
                 FF m{0.0f, 0.0f};
                 if (lane / 8 < per && i < nu) {
                     b.bin = s.units[i] * kUnitBins + lane % 8;
                     b.c = count(b.bin);
-                    const FF w = weights(bin_value<T>(b.bin), s.table);
-                    b.w = ff_to_double(w);
-                    if (b.c) m = ff_mul_f(w, static_cast<float>(b.c));
+                    b.w = weights(bin_value<T>(b.bin), s.table);
+                    if (b.c) m = ff_mul_f(b.w, static_cast<float>(b.c));
                 }
                 b.c_in = b.c;
 #pragma unroll
@@ -444,70 +587,63 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
                     const uint32_t n = __shfl_up_sync(kFull, b.c_in, o);
                     if (lane >= static_cast<uint32_t>(o)) b.c_in += n;
                 }
-                const FF scan = ff_warp_scan(m);
-                if (e) b.c_in += s.entry_c[e - 1];
-                b.m_in = ff_to_double(e ? ff_add(s.entry_m[e - 1], scan) : scan);
+                b.c_in += c_base;
                 b.c_before = b.c_in - b.c;
-                b.m_before = __shfl_up_sync(kFull, b.m_in, 1);
-                if (lane == 0) b.m_before = e ? ff_to_double(s.entry_m[e - 1]) : 0.0;
+                b.m_in = ff_add(m_base, ff_warp_scan(m));
+                b.m_before = ff_shfl_up(b.m_in, 1);
+                if (lane == 0) b.m_before = m_base;
                 return b;
             };
-            // The first entry for which `past` holds, the last one when none does.
-            auto first_entry = [&](auto past) {
-                const uint32_t coarse = __ballot_sync(kFull, past(lane * kCoarse + kCoarse - 1));
-                const uint32_t at = (coarse ? __ffs(coarse) - 1 : 31) * kCoarse;
-                uint32_t e = at + kCoarse - 1;
-#pragma unroll
-                for (uint32_t i = kCoarse / 32; i-- > 0;) {
-                    const uint32_t fine = __ballot_sync(kFull, past(at + i * 32 + lane));
-                    if (fine) e = at + i * 32 + __ffs(fine) - 1;
-                }
-                return min(e, entries - 1);
-            };
-            const uint32_t n_all = s.entry_c[kEntries - 1];
-            const double m_all = ff_to_double(s.entry_m[kEntries - 1]);
             auto prefix_mass = [&](uint32_t n) {  // of the first n ids of the order
                 if (n == n_all) return m_all;
-                const Bins b = open(first_entry([&](uint32_t e) { return s.entry_c[e] >= n; }));
+                const Bins b = open([&](uint32_t c, FF) { return c >= n; });
                 const int l = __ffs(__ballot_sync(kFull, b.c_in >= n)) - 1;
-                return __shfl_sync(kFull, b.m_before + (n - b.c_before) * b.w, l);
+                return ff_shfl(ff_add(b.m_before, ff_mul_f(b.w, static_cast<float>(n - b.c_before))), l);
             };
             // The first id whose cumulative mass reaches `goal` (over: exceeds
             // it): its lane, its place among the bin's ids; and its rank.
-            auto by_mass = [&](double goal, bool over, Bins& b, uint32_t& place, int& l) {
-                auto past = [&](double m) { return over ? m > goal : m >= goal; };
-                b = open(first_entry([&](uint32_t e) { return past(ff_to_double(s.entry_m[e])); }));
+            auto by_mass = [&](FF goal, bool over, Bins& b, uint32_t& place, int& l) {
+                auto past = [&](FF m) { return over ? ff_lt(goal, m) : !ff_lt(m, goal); };
+                b = open([&](uint32_t, FF m) { return past(m); });
                 const uint32_t hit = __ballot_sync(kFull, b.c > 0 && past(b.m_in));
                 // (rounding may leave none: the entry's last id)
                 l = hit ? __ffs(hit) - 1 : 31 - __clz(__ballot_sync(kFull, b.c > 0));
-                // the r-th id of the bin (from 0) ends at m_before + (r + 1) w
-                const double r = over ? floor((goal - b.m_before) / b.w) : ceil((goal - b.m_before) / b.w) - 1.0;
-                place = hit ? static_cast<uint32_t>(fmin(fmax(r, 0.0), b.c - 1.0)) : b.c - 1u;
-                place = __shfl_sync(kFull, place, l);
+                // The r-th id of the bin (from 0) ends at m_before + (r + 1) w: r to
+                // within one from the quotient of the leading floats, then the first
+                // of its neighbourhood that is past.
+                const FF gap = ff_add(goal, FF{-b.m_before.hi, -b.m_before.lo});
+                float r = fminf(fmaxf(floorf(gap.hi / b.w.hi) - 2.0f, 0.0f), static_cast<float>(b.c) - 1.0f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (r + 1.0f < static_cast<float>(b.c) && !past(ff_add(b.m_before, ff_mul_f(b.w, r + 1.0f)))) r += 1.0f;
+                place = __shfl_sync(kFull, hit ? static_cast<uint32_t>(fmaxf(r, 0.0f)) : b.c - 1u, l);
                 return __shfl_sync(kFull, b.c_before, l) + place;
             };
 
             uint32_t bin = s.first_bin, place = 0;
-            double prob = 1.0;
+            float prob = 1.0f;
             if (!greedy) {
                 const uint32_t n_k = kk == 0 ? n_all : min(kk, n_all);
-                const double Z = prefix_mass(n_k);
+                const FF Z = prefix_mass(n_k);
                 uint32_t n = min(n_k, s.n_min);
                 Bins b;
                 int l;
-                if (pf < 1.0f) n = min(n, by_mass(static_cast<double>(pf) * Z, false, b, place, l) + 1u);
-                const double Zs = n == n_k ? Z : prefix_mass(n);
-                if (by_mass(static_cast<double>(uf) * Zs, true, b, place, l) >= n) {
+                if (pf < 1.0f) n = min(n, by_mass(ff_mul_f(Z, pf), false, b, place, l) + 1u);
+                const FF Zs = n == n_k ? Z : prefix_mass(n);
+                if (by_mass(ff_mul_f(Zs, uf), true, b, place, l) >= n) {
                     // rounding: the last survivor
-                    b = open(first_entry([&](uint32_t e) { return s.entry_c[e] >= n; }));
+                    b = open([&](uint32_t c, FF) { return c >= n; });
                     l = __ffs(__ballot_sync(kFull, b.c_in >= n)) - 1;
                     place = __shfl_sync(kFull, n - 1u - b.c_before, l);
                 }
                 bin = __shfl_sync(kFull, b.bin, l);
-                prob = __shfl_sync(kFull, b.w, l) / Zs;
+                const FF w = ff_shfl(b.w, l);
+                // w / Zs, rounded once: the quotient of the leading floats and its remainder
+                const float q0 = w.hi / Zs.hi;
+                prob = q0 + (__fmaf_rn(-q0, Zs.hi, w.hi) + __fmaf_rn(-q0, Zs.lo, w.lo)) / Zs.hi;
             }
             // the CTA that holds it: ids rise with the CTAs
-            const uint32_t c = lane < C ? reinterpret_cast<const uint16_t*>(cl.map_shared_rank(s.hist, lane))[bin] : 0u;
+            const uint32_t c = lane < C ? count_of(bin, lane) : 0u;
             uint32_t in = c;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -517,101 +653,150 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
             const int owner = __ffs(__ballot_sync(kFull, place < in)) - 1;
             place = __shfl_sync(kFull, place - (in - c), owner);
             if (lane < C) {
-                Shared& o = *cl.map_shared_rank(&s, lane);
+                Shared& o = *peer(&s, lane);
                 o.bin = bin;
                 o.owner = owner;
                 o.place = place;
-                o.prob = static_cast<float>(prob);
+                o.prob = prob;
             }
         }
     }
-    cl.sync();
+    cluster_sync();
     if (rank != s.owner) return;
 
-    // The place-th id of the bin in this CTA's registers: ids rise with j, then
-    // the warp, the lane and the element.
+    // The place-th id of the bin in this CTA's share, kAhead vectors a thread at a
+    // time: ids rise with the vectors' number j, then the thread.
     const uint32_t bin = s.bin, pattern = bin * 0x00010001u;
-    uint32_t r = s.place;
     auto flags = [&](uint32_t w) {  // bits 0 and 16: the halves that match
         uint32_t f = __vcmpeq2(w, pattern);
         if (bin == kZeroBin) f |= __vcmpeq2(w, kMinusZeroBin * 0x00010001u);
         return f & 0x00010001u;
     };
-    auto hits = [&](const uint4& v) {
-        const uint32_t f = flags(v.x) + flags(v.y) + flags(v.z) + flags(v.w);
-        return (f & 0xFFFFu) + (f >> 16);
-    };
+    uint32_t r = s.place;
+    for (uint32_t at = share.lo; at < share.hi; at += kAhead * kNT) {
+        uint4 q[kAhead];
+        share.each(at, min(share.hi, at + kAhead * kNT), [&](int j, const uint4& v) {
 #pragma unroll
-    for (int j = 0; j < kVPT; ++j) {
-        const uint32_t n = __reduce_add_sync(kFull, hits(q[j]));
-        if (lane == 0) s.seg[j * kWarps + warp] = n;
-    }
-    __syncthreads();
-    if (warp == 0) {
-        uint32_t sum = 0;
+            for (int i = 0; i < kAhead; ++i)
+                if (i == j) q[i] = v;
+        });
+        uint32_t mine[kAhead];
 #pragma unroll
-        for (int i = 0; i < kVPT; ++i) sum += s.seg[lane * kVPT + i];
-        uint32_t in = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t n = __shfl_up_sync(kFull, in, o);
-            if (lane >= static_cast<uint32_t>(o)) in += n;
+        for (int j = 0; j < kAhead; ++j) {
+            const uint32_t f = flags(q[j].x) + flags(q[j].y) + flags(q[j].z) + flags(q[j].w);
+            mine[j] = (f & 0xFFFFu) + (f >> 16);
+            const uint32_t n = __reduce_add_sync(kFull, mine[j]);
+            if (lane == 0) s.seg[j * kWarps + warp] = n;
         }
-        uint32_t before = in - sum;
-        if (before <= r && r < in) {
-            uint32_t i = lane * kVPT;
-            while (r - before >= s.seg[i]) before += s.seg[i++];
-            s.find[0] = i;
-            s.find[1] = r - before;
+        __syncthreads();
+        if (warp == 0) {
+            uint32_t sum = 0;
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) sum += s.seg[lane * kAhead + i];
+            uint32_t in = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t n = __shfl_up_sync(kFull, in, o);
+                if (lane >= static_cast<uint32_t>(o)) in += n;
+            }
+            uint32_t before = in - sum;
+            if (lane == 31) s.find[0] = 0xFFFFFFFFu, s.find[1] = in;  // not here: past this many
+            __syncwarp();
+            if (before <= r && r < in) {
+                uint32_t i = lane * kAhead;
+                while (r - before >= s.seg[i]) before += s.seg[i++];
+                s.find[0] = i;
+                s.find[1] = r - before;
+            }
         }
-    }
-    __syncthreads();
-    const uint32_t seg = s.find[0];
-    r = s.find[1];
-    if (warp != seg % kWarps) return;
-#pragma unroll
-    for (int j = 0; j < kVPT; ++j) {
-        if (static_cast<uint32_t>(j) != seg / kWarps) continue;
-        const uint32_t n = hits(q[j]);
-        uint32_t in = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t m = __shfl_up_sync(kFull, in, o);
-            if (lane >= static_cast<uint32_t>(o)) in += m;
+        __syncthreads();
+        const uint32_t seg = s.find[0], left0 = s.find[1];
+        if (seg == 0xFFFFFFFFu) {
+            r -= left0;
+            __syncthreads();
+            continue;
         }
-        uint32_t left = r - (in - n);
-        if (in - n <= r && r < in) {
-            const uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
+        if (warp != seg % kWarps) return;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (flags(w[i >> 1]) >> (16 * (i & 1)) & 1) {
-                    if (left == 0) {
-                        a.out_ids[row] = (lo + j * kNT + tid) * 8u + i - skew;
-                        a.out_probs[row] = s.prob;
+        for (int j = 0; j < kAhead; ++j) {
+            if (static_cast<uint32_t>(j) != seg / kWarps) continue;
+            uint32_t in = mine[j];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t m = __shfl_up_sync(kFull, in, o);
+                if (lane >= static_cast<uint32_t>(o)) in += m;
+            }
+            uint32_t left = left0 - (in - mine[j]);
+            if (in - mine[j] <= left0 && left0 < in) {
+                const uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (flags(w[i >> 1]) >> (16 * (i & 1)) & 1) {
+                        if (left == 0) {
+                            a.out_ids[row] = (at + j * kNT + tid) * 8u + i - share.skew;
+                            a.out_probs[row] = s.prob;
+                        }
+                        --left;
                     }
-                    --left;
                 }
             }
         }
+        return;
     }
+}
+
+// CTAs a row for a batch: the cluster size whose rounds of resident clusters
+// take least. A CTA takes about 9 us beside its share, and 1 us for 14,000 ids.
+template <typename T>
+uint32_t ctas_for(uint32_t rows, uint32_t V) {
+    struct Table {
+        int resident[kMaxCluster + 1] = {};
+    };
+    static const Table t = [] {
+        Table r;
+        for (uint32_t c = 1; c <= kMaxCluster; ++c) {
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3(c, 1, 1);
+            cfg.blockDim = dim3(kNT, 1, 1);
+            cfg.dynamicSmemBytes = sizeof(Shared);
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = c;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, sample16_kernel<T>, &cfg) != cudaSuccess || n < 0) {
+                (void)cudaGetLastError();
+                n = 0;
+            }
+            r.resident[c] = n;
+        }
+        return r;
+    }();
+    uint32_t best = 1;
+    double least = 1e30;
+    for (uint32_t c = 1; c <= kMaxCluster; ++c) {
+        if (t.resident[c] == 0) continue;
+        const double rounds = ceil_div(rows, static_cast<uint64_t>(t.resident[c]));
+        const double us = rounds * (9.0 + static_cast<double>(V) / c / 14000.0);
+        if (us < least) {
+            least = us;
+            best = c;
+        }
+    }
+    return best;
 }
 
 template <typename T>
 sel_status launch(const SampleArgs& in, uint32_t rows, cudaStream_t stream) {
-    const int sms = device_sms();
-    if (sms <= 0) return SEL_ECUDA;
-    // the fewest CTAs whose shares hold the row; more while every CTA of the
-    // batch still has an SM of its own
-    const uint32_t vecs = ceil_div(static_cast<uint64_t>(in.V) + 7, 8);
-    uint32_t C = 1;
-    while (ceil_div(vecs, C) > kShareVecs) C *= 2;
-    while (C < kMaxCluster && vecs > C * static_cast<uint32_t>(kNT) &&
-           static_cast<uint64_t>(rows) * C * 2 <= static_cast<uint64_t>(sms))
-        C *= 2;
+    if (!set_dynamic_smem(sample16_kernel<T>, sizeof(Shared))) return SEL_ECUDA;
+    const uint32_t vecs = ceil_div(static_cast<uint64_t>(in.V) + 7, 8), C = ctas_for<T>(rows, in.V);
     if (static_cast<uint64_t>(rows) * C > 0x7fffffffull) return SEL_EUNSUPPORTED;
     SampleArgs a = in;
+    a.ctas = C;
     a.share = ceil_div(vecs, C);
-    if (!set_dynamic_smem(sample16_kernel<T>, sizeof(Shared))) return SEL_ECUDA;
     const cudaError_t e = launch_pdl_cluster(sample16_kernel<T>, dim3(rows * C), dim3(kNT), C, sizeof(Shared), stream, a);
     return e == cudaSuccess ? SEL_OK : SEL_ECUDA;
 }

@@ -90,12 +90,34 @@ def test_widths(V, rows, pad, off):
     check(rows_of(rng, "normal", rows, V, "bf16"), policies(rng, rows, V), rng.random(rows, dtype=np.float32), pad, off)
 
 
-@pytest.mark.parametrize("rows", [20, 49, 76, 77, 200])
+@pytest.mark.parametrize("rows", [2, 18, 20, 30, 49, 76, 77, 152, 153, 200])
 def test_batches(rows):
     """Batches on either side of where the number of CTAs per row changes."""
     rng = np.random.default_rng(rows)
     x = rows_of(rng, "normal", rows, 30_011, "bf16")
     check(x, policies(rng, rows, 30_011), rng.random(rows, dtype=np.float32))
+
+
+@pytest.mark.parametrize("rows", [1, 60, 160])
+@pytest.mark.parametrize("kind", ["equal", "half", "zeros", "spread"])
+def test_values_that_fill_a_counter(rows, kind):
+    """More than 65,535 ids of one value: in one CTA's share, where a batch
+    gives a row few CTAs, and in the row."""
+    V = 230_003
+    rng = np.random.default_rng(rows)
+    x = rng.normal(0, 3, size=(rows, V))
+    at = rng.permutation(V)
+    if kind == "equal":
+        x[:] = 1.25
+    elif kind == "half":
+        x[:, at[:131_072]] = 2.0
+        x[:, at[131_072:200_000]] = -1.5
+    elif kind == "zeros":
+        x[:, at[:80_000]] = 0.0
+        x[:, at[80_000:160_000]] = -0.0
+    else:
+        x[:, at[:65_536]] = 0.5
+    check(torch.from_numpy(x).to(torch.bfloat16), policies(rng, rows, V), rng.random(rows, dtype=np.float32), 3, 1)
 
 
 def test_widest_row():
