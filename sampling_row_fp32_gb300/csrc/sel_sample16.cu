@@ -16,7 +16,11 @@
 // and sum counts (through distributed shared memory) and masses of up to
 // 2,048 entries in the first CTA. There one warp finds every border (of top-k,
 // top-p, the draw): ballots over the entries' prefix sums, then the 32 bins of
-// the entry. The CTA whose share holds the drawn id reads it again, up to it.
+// the entry. The CTA whose share holds the drawn id reads its share again.
+//
+// Where top-k is on, the first batch of a share gives a bound that the top k
+// of the row are not under, and the rest of the share is only counted down to
+// it: what bounds the counting is the atomics, at about five a clock and SM.
 //
 // A counter that overflows (a value that more than 65,535 ids of a share have)
 // makes the counters' sum differ from the ids counted; the share is then
@@ -27,8 +31,6 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <cooperative_groups.h>
-
-#include <type_traits>
 
 #include "sel.h"
 #include "sel_common.cuh"
@@ -181,7 +183,7 @@ struct Shared {
     uint32_t row_bits[kWords];
     FF warp_m[kWarps];        // of 64 entries
     uint32_t warp_c[kWarps];
-    uint32_t seg[kAhead * kWarps];
+    uint32_t seg[kWarps];
     uint32_t heavy[kMaxHeavy];  // bins with 32,768 ids more than their counter says, once for each
     uint32_t heavies, counted, n_bits, any_heavy;
     Weights weights;
@@ -190,7 +192,6 @@ struct Shared {
     uint32_t bad;
     uint32_t bin, owner, place;  // the drawn bin, the CTA of the drawn id, its place among that CTA's ids of the bin
     float prob;
-    uint32_t find[2];
 };
 
 // A vector of 16 bytes where `on` holds, else four times `fill`: without a
@@ -230,10 +231,11 @@ struct Share {
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
-    // f(v, bins) for vectors base + tid, + kNT, ... below end; kAhead at a time,
-    // the next ones on their way. f returns nothing.
-    template <typename F>
-    __device__ __forceinline__ void each(uint32_t base, uint32_t end, F f) const {
+    // f(v, bins) for vectors base + me, + kStride, ... below end, kAhead at a time
+    // with the next ones on their way; every thread calls it for all kAhead,
+    // past the end with masked ids.
+    template <uint32_t kStride, typename F>
+    __device__ __forceinline__ void each(uint32_t base, uint32_t end, uint32_t me, F f) const {
         constexpr uint32_t kNegInf = 0x8000u | Kind<T>::kInf, kFill = kNegInf | (kNegInf << 16);
         const uint32_t full_lo = skew ? 1u : 0u, full_hi = (V + skew) / 8u;
         const uint16_t* origin = x - skew;
@@ -241,25 +243,41 @@ struct Share {
         auto load = [&](uint32_t at) {
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
-                const uint32_t v = at + j * kNT + threadIdx.x;
+                const uint32_t v = at + j * kStride + me;
                 next[j] = load_or(origin + static_cast<uint64_t>(v) * 8u, v >= full_lo && v < full_hi && v < end, kFill);
             }
         };
         load(base);
-        for (uint32_t at = base; at < end; at += kAhead * kNT) {
+        for (uint32_t at = base; at < end; at += kAhead * kStride) {
             uint4 q[kAhead];
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) q[j] = next[j];
-            load(at + kAhead * kNT);
+            load(at + kAhead * kStride);
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
-                const uint32_t v = at + j * kNT + threadIdx.x;
+                const uint32_t v = at + j * kStride + me;
                 if (v < end && (v < full_lo || v >= full_hi)) q[j] = edge(v);
-                f(j, make_uint4(bins_of(q[j].x), bins_of(q[j].y), bins_of(q[j].z), bins_of(q[j].w)));
+                f(v, make_uint4(bins_of(q[j].x), bins_of(q[j].y), bins_of(q[j].z), bins_of(q[j].w)));
             }
         }
     }
 };
+
+// Ids of a unit's eight counters.
+__device__ __forceinline__ uint32_t unit_sum(const uint4& v) {
+    return (v.x & 0xFFFFu) + (v.x >> 16) + (v.y & 0xFFFFu) + (v.y >> 16) + (v.z & 0xFFFFu) + (v.z >> 16) + (v.w & 0xFFFFu) +
+           (v.w >> 16);
+}
+// Inclusive sums over the warp's lanes.
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t n = __shfl_up_sync(kFull, v, o);
+        if ((threadIdx.x & 31) >= static_cast<uint32_t>(o)) v += n;
+    }
+    return v;
+}
+__device__ __forceinline__ uint32_t ceil_div32(uint32_t a, uint32_t b) { return (a + b - 1) / b; }
 
 template <typename T>
 __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
@@ -301,21 +319,22 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
     pdl_trigger();
     __syncthreads();  // the histogram is clear
 
-    // Count; returns how many ids the thread counted (tally).
-    auto count_share = [&](uint32_t base, uint32_t end, auto tally) {
+    // Count the ids of bins up to `most` (and NaNs past the masked bin); returns
+    // how many the thread counted.
+    auto count_share = [&](uint32_t base, uint32_t end, uint32_t most) {
         uint32_t n = 0;
-        share.each(base, end, [&](int, const uint4& q) {
+        share.template each<kNT>(base, end, tid, [&](uint32_t, const uint4& q) {
             const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t d0 = w[i] & 0xFFFFu, d1 = w[i] >> 16;
-                if (d0 != kNegInf) {
+                if (d0 <= most || d0 > kNegInf) {
                     atomicAdd(&s.hist[d0 >> 1], 1u << (16 * (d0 & 1)));
-                    if (tally.value) ++n;
+                    ++n;
                 }
-                if (d1 != kNegInf) {
+                if (d1 <= most || d1 > kNegInf) {
                     atomicAdd(&s.hist[d1 >> 1], 1u << (16 * (d1 & 1)));
-                    if (tally.value) ++n;
+                    ++n;
                 }
             }
         });
@@ -323,13 +342,45 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
     };
     // fewer than 65,536 ids: no counter can overflow
     const bool small = share.hi - share.lo <= kBatchVecs * 2;
+    const uint32_t want = Tf == 0.0f ? 1u : kk;  // ids of the row that can matter, from the largest; 0: all
+    uint32_t most = kNegInf - 1;
+    if (tid == 32) s.weights.temperature(Tf > 0.0f ? Tf : 1.0f);
     if (small) {
-        count_share(share.lo, share.hi, std::false_type{});
+        count_share(share.lo, share.hi, most);
     } else {
-        const uint32_t n = __reduce_add_sync(kFull, count_share(share.lo, share.hi, std::true_type{}));
+        uint32_t n = 0, at = share.lo;
+        if (want && want < kBatchVecs * 8) {
+            // The top `want` ids of the first batch bound those of the row from
+            // below: the rest of the share only counts what is not under them.
+            at += kBatchVecs;
+            n = count_share(share.lo, at, most);
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < static_cast<int>(kUnits / kNT); ++i) {
+                const uint32_t word = warp * (kUnits / kNT) + i;
+                const uint32_t sum = __reduce_add_sync(kFull, unit_sum(h4[word * 32 + lane]));
+                if (lane == 0) s.off[word] = sum;
+            }
+            __syncthreads();
+            // every warp finds the same: the 256 bins where the count gets there, then their unit
+            uint32_t sum = 0;
+#pragma unroll
+            for (uint32_t i = 0; i < kWords / 32; ++i) sum += s.off[lane * (kWords / 32) + i];
+            const uint32_t in = warp_scan(sum), hit = __ballot_sync(kFull, in >= want);
+            if (hit) {
+                const int l = __ffs(hit) - 1;
+                uint32_t before = __shfl_sync(kFull, in - sum, l), word = l * (kWords / 32);
+                while (before + s.off[word] < want) before += s.off[word++];
+                const uint32_t units = warp_scan(unit_sum(h4[word * 32 + lane]));
+                const uint32_t unit = word * 32 + __ffs(__ballot_sync(kFull, before + units >= want)) - 1;
+                most = min(most, unit * kUnitBins + kUnitBins - 1);
+                if (most == kZeroBin) most = kMinusZeroBin;
+            }
+            __syncthreads();
+        }
+        n = __reduce_add_sync(kFull, n + count_share(at, share.hi, most));
         if (lane == 0) atomicAdd(&s.counted, n);
     }
-    if (tid == 32) s.weights.temperature(Tf > 0.0f ? Tf : 1.0f);
     __syncthreads();
     auto merge_zeros = [&] {  // -0 ties with +0: one bin (bins 0x7FFF and 0x8000)
         const uint32_t neg = s.hist[kMinusZeroBin / 2] & 0xFFFFu;
@@ -351,8 +402,7 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
             const uint4 v = h4[word * 32 + lane];
             const uint32_t b = __ballot_sync(kFull, (v.x | v.y | v.z | v.w) != 0);
             if (lane == 0) s.bits[word] = b;
-            sum += (v.x & 0xFFFFu) + (v.x >> 16) + (v.y & 0xFFFFu) + (v.y >> 16) + (v.z & 0xFFFFu) + (v.z >> 16) +
-                   (v.w & 0xFFFFu) + (v.w >> 16);
+            sum += unit_sum(v);
         }
         return __reduce_add_sync(kFull, sum);
     };
@@ -370,7 +420,7 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
             clear();
             __syncthreads();
             for (uint32_t at = share.lo; at < share.hi; at += kBatchVecs) {
-                count_share(at, min(share.hi, at + kBatchVecs), std::false_type{});
+                count_share(at, min(share.hi, at + kBatchVecs), most);
                 __syncthreads();
                 if (tid == 0) merge_zeros();
                 __syncthreads();
@@ -395,12 +445,7 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
     if (tid < kWords) {
         uint32_t word = 0;
         for (uint32_t r = 0; r < C; ++r) word |= peer(s.bits, r)[tid];
-        uint32_t in = __popc(word);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t n = __shfl_up_sync(kFull, in, o);
-            if (lane >= static_cast<uint32_t>(o)) in += n;
-        }
+        const uint32_t in = warp_scan(__popc(word));
         s.off[tid] = in;  // up to and with this word, in its 32
         s.row_bits[tid] = word;
     } else if (tid < kWords + C) {
@@ -417,17 +462,26 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
     __syncthreads();
 
     const bool any_heavy = s.any_heavy != 0;
-    auto count_of = [&](uint32_t bin, uint32_t r) {  // in CTA r
-        uint32_t n = reinterpret_cast<const uint16_t*>(peer(s.hist, r))[bin];
-        if (any_heavy) {
-            const uint32_t* heavy = peer(s.heavy, r);
-            for (uint32_t i = 0; i < *peer(&s.heavies, r); ++i) n += heavy[i] == bin ? kHalf : 0u;
-        }
+    auto heavy_of = [&](uint32_t bin, uint32_t r) {  // ids of CTA r that its counter leaves out
+        uint32_t n = 0;
+        const uint32_t* heavy = peer(s.heavy, r);
+        for (uint32_t i = 0; i < *peer(&s.heavies, r); ++i) n += heavy[i] == bin ? kHalf : 0u;
         return n;
     };
-    auto count = [&](uint32_t bin) {  // over the row
-        uint32_t n = 0;
-        for (uint32_t r = 0; r < C; ++r) n += count_of(bin, r);
+    auto count_of = [&](uint32_t bin, uint32_t r) {  // in CTA r
+        const uint32_t n = reinterpret_cast<const uint16_t*>(peer(s.hist, r))[bin];
+        return any_heavy ? n + heavy_of(bin, r) : n;
+    };
+    auto count = [&](uint32_t bin) {  // over the row; the loads of all CTAs on their way together
+        if (C == 1) return count_of(bin, 0);
+        uint32_t v[kMaxCluster], n = 0;
+#pragma unroll
+        for (uint32_t r = 0; r < kMaxCluster; ++r)
+            v[r] = r < C ? reinterpret_cast<const uint16_t*>(cl.map_shared_rank(s.hist, r))[bin] : 0u;
+#pragma unroll
+        for (uint32_t r = 0; r < kMaxCluster; ++r) n += v[r];
+        if (any_heavy)
+            for (uint32_t r = 0; r < C; ++r) n += heavy_of(bin, r);
         return n;
     };
     if (warp == 0) {
@@ -504,14 +558,9 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
             const uint32_t c0 = e < entries ? s.entry_c[e] : 0u, c1 = e + 1 < entries ? s.entry_c[e + 1] : 0u;
             const FF m0 = e < entries ? s.entry_m[e] : FF{0.0f, 0.0f};
             const FF m1 = e + 1 < entries ? s.entry_m[e + 1] : FF{0.0f, 0.0f};
-            uint32_t wc = c0 + c1;
+            const uint32_t wc = warp_scan(c0 + c1);
             const FF both = ff_add(m0, m1);
             const FF wm = ff_warp_scan(both);
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t n = __shfl_up_sync(kFull, wc, o);
-                if (lane >= static_cast<uint32_t>(o)) wc += n;
-            }
             FF before = ff_shfl_up(wm, 1);
             if (lane == 0) before = FF{0.0f, 0.0f};
             s.entry_c[e] = wc - c1;
@@ -529,13 +578,8 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
             uint32_t seg_c = 0, seg_c0 = 0;
             FF seg_m{0.0f, 0.0f}, seg_m0{0.0f, 0.0f};
             if (!greedy) {
-                seg_c = s.warp_c[lane];
+                seg_c = warp_scan(s.warp_c[lane]);
                 seg_m = ff_warp_scan(s.warp_m[lane]);
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const uint32_t n = __shfl_up_sync(kFull, seg_c, o);
-                    if (lane >= static_cast<uint32_t>(o)) seg_c += n;
-                }
                 seg_c0 = __shfl_up_sync(kFull, seg_c, 1);
                 seg_m0 = ff_shfl_up(seg_m, 1);
                 if (lane == 0) {
@@ -581,13 +625,7 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
                     b.w = weights(bin_value<T>(b.bin), s.table);
                     if (b.c) m = ff_mul_f(b.w, static_cast<float>(b.c));
                 }
-                b.c_in = b.c;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const uint32_t n = __shfl_up_sync(kFull, b.c_in, o);
-                    if (lane >= static_cast<uint32_t>(o)) b.c_in += n;
-                }
-                b.c_in += c_base;
+                b.c_in = c_base + warp_scan(b.c);
                 b.c_before = b.c_in - b.c;
                 b.m_in = ff_add(m_base, ff_warp_scan(m));
                 b.m_before = ff_shfl_up(b.m_in, 1);
@@ -644,12 +682,7 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
             }
             // the CTA that holds it: ids rise with the CTAs
             const uint32_t c = lane < C ? count_of(bin, lane) : 0u;
-            uint32_t in = c;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t n = __shfl_up_sync(kFull, in, o);
-                if (lane >= static_cast<uint32_t>(o)) in += n;
-            }
+            const uint32_t in = warp_scan(c);
             const int owner = __ffs(__ballot_sync(kFull, place < in)) - 1;
             place = __shfl_sync(kFull, place - (in - c), owner);
             if (lane < C) {
@@ -664,85 +697,56 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
     cluster_sync();
     if (rank != s.owner) return;
 
-    // The place-th id of the bin in this CTA's share, kAhead vectors a thread at a
-    // time: ids rise with the vectors' number j, then the thread.
+    // The place-th id of the bin in this CTA's share: each warp counts the bin's
+    // ids in a run of vectors of its own, then the warp that has the id goes
+    // through its run again.
     const uint32_t bin = s.bin, pattern = bin * 0x00010001u;
     auto flags = [&](uint32_t w) {  // bits 0 and 16: the halves that match
         uint32_t f = __vcmpeq2(w, pattern);
         if (bin == kZeroBin) f |= __vcmpeq2(w, kMinusZeroBin * 0x00010001u);
         return f & 0x00010001u;
     };
-    uint32_t r = s.place;
-    for (uint32_t at = share.lo; at < share.hi; at += kAhead * kNT) {
-        uint4 q[kAhead];
-        share.each(at, min(share.hi, at + kAhead * kNT), [&](int j, const uint4& v) {
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i)
-                if (i == j) q[i] = v;
-        });
-        uint32_t mine[kAhead];
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            const uint32_t f = flags(q[j].x) + flags(q[j].y) + flags(q[j].z) + flags(q[j].w);
-            mine[j] = (f & 0xFFFFu) + (f >> 16);
-            const uint32_t n = __reduce_add_sync(kFull, mine[j]);
-            if (lane == 0) s.seg[j * kWarps + warp] = n;
+    auto hits = [&](const uint4& q) {
+        const uint32_t f = flags(q.x) + flags(q.y) + flags(q.z) + flags(q.w);
+        return (f & 0xFFFFu) + (f >> 16);
+    };
+    const uint32_t run = ceil_div32(share.hi - share.lo, kWarps);
+    const uint32_t run_lo = min(share.hi, share.lo + warp * run), run_hi = min(share.hi, run_lo + run);
+    uint32_t mine = 0;
+    share.template each<32>(run_lo, run_hi, lane, [&](uint32_t, const uint4& q) { mine += hits(q); });
+    mine = __reduce_add_sync(kFull, mine);
+    if (lane == 0) s.seg[warp] = mine;
+    __syncthreads();
+    const uint32_t in = warp_scan(s.seg[lane]);
+    const uint32_t place = s.place;
+    if (static_cast<int>(warp) != __ffs(__ballot_sync(kFull, place < in)) - 1) return;
+    uint32_t left = place - (__shfl_sync(kFull, in, warp) - mine);  // ids of the bin before it in the run
+    bool found = false;
+    share.template each<32>(run_lo, run_hi, lane, [&](uint32_t v, const uint4& q) {
+        if (found) return;
+        const uint32_t n = hits(q);
+        const uint32_t upto = warp_scan(n);
+        const uint32_t all = __shfl_sync(kFull, upto, 31);
+        if (left >= all) {
+            left -= all;
+            return;
         }
-        __syncthreads();
-        if (warp == 0) {
-            uint32_t sum = 0;
+        found = true;
+        uint32_t skip = left - (upto - n);
+        if (upto - n <= left && left < upto) {
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) sum += s.seg[lane * kAhead + i];
-            uint32_t in = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t n = __shfl_up_sync(kFull, in, o);
-                if (lane >= static_cast<uint32_t>(o)) in += n;
-            }
-            uint32_t before = in - sum;
-            if (lane == 31) s.find[0] = 0xFFFFFFFFu, s.find[1] = in;  // not here: past this many
-            __syncwarp();
-            if (before <= r && r < in) {
-                uint32_t i = lane * kAhead;
-                while (r - before >= s.seg[i]) before += s.seg[i++];
-                s.find[0] = i;
-                s.find[1] = r - before;
-            }
-        }
-        __syncthreads();
-        const uint32_t seg = s.find[0], left0 = s.find[1];
-        if (seg == 0xFFFFFFFFu) {
-            r -= left0;
-            __syncthreads();
-            continue;
-        }
-        if (warp != seg % kWarps) return;
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-            if (static_cast<uint32_t>(j) != seg / kWarps) continue;
-            uint32_t in = mine[j];
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t m = __shfl_up_sync(kFull, in, o);
-                if (lane >= static_cast<uint32_t>(o)) in += m;
-            }
-            uint32_t left = left0 - (in - mine[j]);
-            if (in - mine[j] <= left0 && left0 < in) {
-                const uint32_t w[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (flags(w[i >> 1]) >> (16 * (i & 1)) & 1) {
-                        if (left == 0) {
-                            a.out_ids[row] = (at + j * kNT + tid) * 8u + i - share.skew;
-                            a.out_probs[row] = s.prob;
-                        }
-                        --left;
+            for (int i = 0; i < 8; ++i) {
+                if (flags(w[i >> 1]) >> (16 * (i & 1)) & 1) {
+                    if (skip == 0) {
+                        a.out_ids[row] = v * 8u + i - share.skew;
+                        a.out_probs[row] = s.prob;
                     }
+                    --skip;
                 }
             }
         }
-        return;
-    }
+    });
 }
 
 // CTAs a row for a batch: the cluster size whose rounds of resident clusters

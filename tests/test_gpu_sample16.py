@@ -151,6 +151,30 @@ def test_temperatures_at_the_ends(dtype, spread):
     check(x, (T, None, np.full(len(T), 0.9, np.float32), None), rng.random(len(T), dtype=np.float32))
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("late", [False, True])
+def test_top_k_of_long_shares(dtype, late):
+    """Batches whose rows one CTA takes, top-k on: rows that rise towards their
+    end, rows whose first part is masked or has few ids, zeros of both signs as
+    the k-th value, NaNs past the bound."""
+    rows, V = 160, 140_003
+    rng = np.random.default_rng(12)
+    x = rng.normal(0, 3, size=(rows, V))
+    if late:
+        x += np.linspace(-30, 0, V)
+    x[0:20, :60_000] = -np.inf
+    x[20:30, :33_000] = -np.inf
+    x[20:30, 7] = 1.0
+    x[30:50] = np.where(rng.random((20, V)) < 0.5, 0.0, -0.0)
+    x[30:50, rng.integers(0, V, 30)] = 5.0
+    x[50, V - 1] = np.inf
+    x[51, V - 2] = np.nan
+    x[52, V - 3] = -np.nan
+    pol = list(policies(rng, rows, V))
+    pol[1] = rng.choice([1, 2, 29, 40, 1000, 30_000, 32_759, 32_760, 100_000], rows).astype(np.uint32)
+    check(torch.from_numpy(x).to(DT[dtype]), tuple(pol), rng.random(rows, dtype=np.float32), 1, 2)
+
+
 def test_equal_weights_at_exact_borders():
     """Every weight is 1: uniforms and top-p cuts that fall on a border go by
     rational arithmetic."""
