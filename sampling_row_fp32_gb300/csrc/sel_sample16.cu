@@ -45,7 +45,10 @@ namespace {
 
 constexpr int kNT = 1024;
 constexpr int kWarps = kNT / 32;
-constexpr int kAhead = 4;                   // 16-byte vectors a thread loads ahead
+// 16-byte vectors a thread loads ahead. Two: every further one lengthens the code
+// of a pass, which a small batch fetches for its first and only use (16.9 us a
+// row of 151,936 with two, 18.9 with four), and large ones gain nothing.
+constexpr int kAhead = 2;
 constexpr uint32_t kMaxCluster = 8;
 constexpr uint32_t kBatchVecs = 4095;       // vectors whose ids overflow no counter below half
 constexpr uint32_t kHalf = 32768;
@@ -54,32 +57,45 @@ constexpr uint32_t kBins = 65536;
 constexpr uint32_t kUnitBins = 8;           // a 16-byte unit of the histogram
 constexpr uint32_t kUnits = kBins / kUnitBins;
 constexpr uint32_t kWords = kUnits / 32;    // occupancy bitmap
-constexpr uint32_t kZeroBin = 0x7FFF;       // +0
-constexpr uint32_t kMinusZeroBin = 0x8000;  // -0, counted as +0
 static_assert(kBatchVecs * 8 + kHalf <= 65536);
 
-// Bin of a bit pattern: descending by value, so bin 0 side is the largest.
-// (For two patterns packed in a word.)
-__device__ __forceinline__ uint32_t bins_of(uint32_t w) {
-    const uint32_t pos = (~w >> 15) & 0x00010001u;  // 1 where the sign bit is clear
-    return w ^ (pos * 0x7FFFu);
-}
+// Counters are indexed by the logits' bit patterns. Bins number the patterns by
+// value, descending: bin 0 is the largest. (Its own inverse.)
+__device__ __forceinline__ uint32_t pattern_of(uint32_t bin) { return bin < 0x8000u ? 0x7FFFu - bin : bin; }
+// The unit of eight counters that holds the bins of unit u.
+__device__ __forceinline__ uint32_t stored_unit(uint32_t u) { return u < kUnits / 2 ? kUnits / 2 - 1 - u : u; }
 
+// Per type: the pattern of +Inf, and comparisons of two packed logits, done by
+// the half-precision pipe; the integer pipe is what bounds the passes over a row.
 template <typename T>
 struct Kind;
 template <>
 struct Kind<__nv_bfloat16> {
     static constexpr uint32_t kInf = 0x7F80;
+    using Pair = __nv_bfloat162;
 };
 template <>
 struct Kind<__half> {
     static constexpr uint32_t kInf = 0x7C00;
+    using Pair = __half2;
 };
+template <typename T>
+__device__ __forceinline__ typename Kind<T>::Pair as_pair(uint32_t w) {
+    typename Kind<T>::Pair p;
+    memcpy(&p, &w, 4);
+    return p;
+}
+// All ones in each half that equals (-0 equals +0); that is not below, NaNs included.
+template <typename T>
+__device__ __forceinline__ uint32_t equal2(uint32_t a, uint32_t b) { return __heq2_mask(as_pair<T>(a), as_pair<T>(b)); }
+template <typename T>
+__device__ __forceinline__ uint32_t not_below2(uint32_t a, uint32_t b) {
+    return __hgeu2_mask(as_pair<T>(a), as_pair<T>(b));
+}
 
 template <typename T>
 __device__ __forceinline__ float bin_value(uint32_t bin) {
-    const uint32_t u = bin < 0x8000u ? 0x7FFFu - bin : bin;
-    return bits_f32<T>(static_cast<uint16_t>(u));
+    return bits_f32<T>(static_cast<uint16_t>(pattern_of(bin)));
 }
 
 // ---------------------------------------------------------------------------
@@ -215,8 +231,8 @@ struct Share {
     const uint16_t* x;
     uint32_t V, skew, lo, hi;  // vectors [lo, hi)
 
-    // Bins of vector v, masked ids (and those outside the row) as -Inf's bin.
-    // Vectors that reach over an end of the row are read by element.
+    // Vector v where it reaches over an end of the row: by element, -Inf (a masked
+    // id) outside.
     __device__ __forceinline__ uint4 edge(uint32_t v) const {
         constexpr uint32_t kNegInf = 0x8000u | Kind<T>::kInf;
         uint32_t w[4];
@@ -231,33 +247,28 @@ struct Share {
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
-    // f(v, bins) for vectors base + me, + kStride, ... below end, kAhead at a time
-    // with the next ones on their way; every thread calls it for all kAhead,
+    // f(v, logits) for vectors base + me, + kStride, ... below end, kAhead at a time
+    // with the next ones on their way. kAll: every thread calls it for all kAhead,
     // past the end with masked ids.
-    template <uint32_t kStride, typename F>
+    template <uint32_t kStride, bool kAll, typename F>
     __device__ __forceinline__ void each(uint32_t base, uint32_t end, uint32_t me, F f) const {
         constexpr uint32_t kNegInf = 0x8000u | Kind<T>::kInf, kFill = kNegInf | (kNegInf << 16);
         const uint32_t full_lo = skew ? 1u : 0u, full_hi = (V + skew) / 8u;
         const uint16_t* origin = x - skew;
         uint4 next[kAhead];
-        auto load = [&](uint32_t at) {
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                const uint32_t v = at + j * kStride + me;
-                next[j] = load_or(origin + static_cast<uint64_t>(v) * 8u, v >= full_lo && v < full_hi && v < end, kFill);
-            }
+        auto load = [&](uint32_t v) {
+            return load_or(origin + static_cast<uint64_t>(v) * 8u, v >= full_lo && v < full_hi && v < end, kFill);
         };
-        load(base);
-        for (uint32_t at = base; at < end; at += kAhead * kStride) {
-            uint4 q[kAhead];
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) q[j] = next[j];
-            load(at + kAhead * kStride);
+        for (int j = 0; j < kAhead; ++j) next[j] = load(base + j * kStride + me);
+        for (uint32_t at = base + me; at - me < end; at += kAhead * kStride) {
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
-                const uint32_t v = at + j * kStride + me;
-                if (v < end && (v < full_lo || v >= full_hi)) q[j] = edge(v);
-                f(v, make_uint4(bins_of(q[j].x), bins_of(q[j].y), bins_of(q[j].z), bins_of(q[j].w)));
+                const uint32_t v = at + j * kStride;
+                uint4 q = next[j];
+                next[j] = load(v + kAhead * kStride);
+                if (v < end && (v < full_lo || v >= full_hi)) q = edge(v);
+                if (kAll || v < end) f(v, q);
             }
         }
     }
@@ -319,21 +330,53 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
     pdl_trigger();
     __syncthreads();  // the histogram is clear
 
-    // Count the ids of bins up to `most` (and NaNs past the masked bin); returns
-    // how many the thread counted.
-    auto count_share = [&](uint32_t base, uint32_t end, uint32_t most) {
+    // Counting. The counter of pattern u is half u & 1 of word u >> 1.
+    auto add_low = [&](uint32_t w) {
+        atomicAdd(reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(s.hist) + (w << 1 & 0x1FFFCu)), 1u + (w & 1u) * 0xFFFFu);
+    };
+    auto add_high = [&](uint32_t w) {
+        atomicAdd(reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(s.hist) + (w >> 15 & 0x1FFFCu)), max(w & 0x10000u, 1u));
+    };
+    // Counts the unmasked ids; returns how many the thread counted.
+    auto count_all = [&](uint32_t base, uint32_t end) {
         uint32_t n = 0;
-        share.template each<kNT>(base, end, tid, [&](uint32_t, const uint4& q) {
+        share.template each<kNT, false>(base, end, tid, [&](uint32_t, const uint4& q) {
             const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t d0 = w[i] & 0xFFFFu, d1 = w[i] >> 16;
-                if (d0 <= most || d0 > kNegInf) {
-                    atomicAdd(&s.hist[d0 >> 1], 1u << (16 * (d0 & 1)));
+                const uint32_t masked = equal2<T>(w[i], kNegInf * 0x00010001u);
+                if (!masked) {
+                    add_low(w[i]);
+                    add_high(w[i]);
+                    n += 2;
+                } else {
+                    if (!(masked & 1u)) {
+                        add_low(w[i]);
+                        ++n;
+                    }
+                    if (!(masked >> 31)) {
+                        add_high(w[i]);
+                        ++n;
+                    }
+                }
+            }
+        });
+        return n;
+    };
+    // The same of ids that are not below `bound` (a pair of the same pattern).
+    auto count_from = [&](uint32_t base, uint32_t end, uint32_t bound) {
+        uint32_t n = 0;
+        share.template each<kNT, false>(base, end, tid, [&](uint32_t, const uint4& q) {
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t in = not_below2<T>(w[i], bound);
+                if (in & 1u) {
+                    add_low(w[i]);
                     ++n;
                 }
-                if (d1 <= most || d1 > kNegInf) {
-                    atomicAdd(&s.hist[d1 >> 1], 1u << (16 * (d1 & 1)));
+                if (in >> 31) {
+                    add_high(w[i]);
                     ++n;
                 }
             }
@@ -343,22 +386,22 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
     // fewer than 65,536 ids: no counter can overflow
     const bool small = share.hi - share.lo <= kBatchVecs * 2;
     const uint32_t want = Tf == 0.0f ? 1u : kk;  // ids of the row that can matter, from the largest; 0: all
-    uint32_t most = kNegInf - 1;
+    uint32_t bound = 0;  // 0: none yet, else a pair of the least pattern that counts
     if (tid == 32) s.weights.temperature(Tf > 0.0f ? Tf : 1.0f);
     if (small) {
-        count_share(share.lo, share.hi, most);
+        count_all(share.lo, share.hi);
     } else {
         uint32_t n = 0, at = share.lo;
         if (want && want < kBatchVecs * 8) {
             // The top `want` ids of the first batch bound those of the row from
             // below: the rest of the share only counts what is not under them.
             at += kBatchVecs;
-            n = count_share(share.lo, at, most);
+            n = count_all(share.lo, at);
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < static_cast<int>(kUnits / kNT); ++i) {
                 const uint32_t word = warp * (kUnits / kNT) + i;
-                const uint32_t sum = __reduce_add_sync(kFull, unit_sum(h4[word * 32 + lane]));
+                const uint32_t sum = __reduce_add_sync(kFull, unit_sum(h4[stored_unit(word * 32 + lane)]));
                 if (lane == 0) s.off[word] = sum;
             }
             __syncthreads();
@@ -371,23 +414,23 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
                 const int l = __ffs(hit) - 1;
                 uint32_t before = __shfl_sync(kFull, in - sum, l), word = l * (kWords / 32);
                 while (before + s.off[word] < want) before += s.off[word++];
-                const uint32_t units = warp_scan(unit_sum(h4[word * 32 + lane]));
+                const uint32_t units = warp_scan(unit_sum(h4[stored_unit(word * 32 + lane)]));
                 const uint32_t unit = word * 32 + __ffs(__ballot_sync(kFull, before + units >= want)) - 1;
-                most = min(most, unit * kUnitBins + kUnitBins - 1);
-                if (most == kZeroBin) most = kMinusZeroBin;
+                // (the unit's least value; the least finite one where that is -Inf or a NaN)
+                bound = pattern_of(min(unit * kUnitBins + kUnitBins - 1, kNegInf - 1)) * 0x00010001u;
+                if (!bound) bound = 0x80008000u;  // 0 as -0, which compares the same
             }
             __syncthreads();
         }
-        n = __reduce_add_sync(kFull, n + count_share(at, share.hi, most));
+        n = __reduce_add_sync(kFull, n + (bound ? count_from(at, share.hi, bound) : count_all(at, share.hi)));
         if (lane == 0) atomicAdd(&s.counted, n);
     }
     __syncthreads();
-    auto merge_zeros = [&] {  // -0 ties with +0: one bin (bins 0x7FFF and 0x8000)
-        const uint32_t neg = s.hist[kMinusZeroBin / 2] & 0xFFFFu;
-        const uint32_t pos = s.hist[kZeroBin / 2] >> 16;
-        if (pos + neg < 65536u) {
-            s.hist[kMinusZeroBin / 2] -= neg;
-            s.hist[kZeroBin / 2] += neg << 16;
+    auto merge_zeros = [&] {  // -0 ties with +0: its pattern, 0x8000, is counted with 0
+        const uint32_t neg = s.hist[0x8000 / 2] & 0xFFFFu;
+        if ((s.hist[0] & 0xFFFFu) + neg < 65536u) {
+            s.hist[0x8000 / 2] -= neg;
+            s.hist[0] += neg;
         } else {
             s.counted = 0;  // counted again below
         }
@@ -399,7 +442,7 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
 #pragma unroll
         for (int i = 0; i < static_cast<int>(kUnits / kNT); ++i) {
             const uint32_t word = i * kWarps + warp;
-            const uint4 v = h4[word * 32 + lane];
+            const uint4 v = h4[stored_unit(word * 32 + lane)];
             const uint32_t b = __ballot_sync(kFull, (v.x | v.y | v.z | v.w) != 0);
             if (lane == 0) s.bits[word] = b;
             sum += unit_sum(v);
@@ -420,7 +463,8 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
             clear();
             __syncthreads();
             for (uint32_t at = share.lo; at < share.hi; at += kBatchVecs) {
-                count_share(at, min(share.hi, at + kBatchVecs), most);
+                if (bound) count_from(at, min(share.hi, at + kBatchVecs), bound);
+                else count_all(at, min(share.hi, at + kBatchVecs));
                 __syncthreads();
                 if (tid == 0) merge_zeros();
                 __syncthreads();
@@ -428,8 +472,8 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
                     const uint32_t w = s.hist[i], over = w & 0x80008000u;
                     if (over) {
                         s.hist[i] = w - over;
-                        if (over & 0x8000u) s.heavy[atomicAdd(&s.heavies, 1u)] = 2 * i;
-                        if (over >> 31) s.heavy[atomicAdd(&s.heavies, 1u)] = 2 * i + 1;
+                        if (over & 0x8000u) s.heavy[atomicAdd(&s.heavies, 1u)] = pattern_of(2 * i);
+                        if (over >> 31) s.heavy[atomicAdd(&s.heavies, 1u)] = pattern_of(2 * i + 1);
                     }
                 }
                 __syncthreads();
@@ -469,7 +513,7 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
         return n;
     };
     auto count_of = [&](uint32_t bin, uint32_t r) {  // in CTA r
-        const uint32_t n = reinterpret_cast<const uint16_t*>(peer(s.hist, r))[bin];
+        const uint32_t n = reinterpret_cast<const uint16_t*>(peer(s.hist, r))[pattern_of(bin)];
         return any_heavy ? n + heavy_of(bin, r) : n;
     };
     auto count = [&](uint32_t bin) {  // over the row; the loads of all CTAs on their way together
@@ -477,7 +521,7 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
         uint32_t v[kMaxCluster], n = 0;
 #pragma unroll
         for (uint32_t r = 0; r < kMaxCluster; ++r)
-            v[r] = r < C ? reinterpret_cast<const uint16_t*>(cl.map_shared_rank(s.hist, r))[bin] : 0u;
+            v[r] = r < C ? reinterpret_cast<const uint16_t*>(cl.map_shared_rank(s.hist, r))[pattern_of(bin)] : 0u;
 #pragma unroll
         for (uint32_t r = 0; r < kMaxCluster; ++r) n += v[r];
         if (any_heavy)
@@ -700,21 +744,21 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
     // The place-th id of the bin in this CTA's share: each warp counts the bin's
     // ids in a run of vectors of its own, then the warp that has the id goes
     // through its run again.
-    const uint32_t bin = s.bin, pattern = bin * 0x00010001u;
-    auto flags = [&](uint32_t w) {  // bits 0 and 16: the halves that match
-        uint32_t f = __vcmpeq2(w, pattern);
-        if (bin == kZeroBin) f |= __vcmpeq2(w, kMinusZeroBin * 0x00010001u);
-        return f & 0x00010001u;
-    };
-    auto hits = [&](const uint4& q) {
-        const uint32_t f = flags(q.x) + flags(q.y) + flags(q.z) + flags(q.w);
-        return (f & 0xFFFFu) + (f >> 16);
-    };
+    const uint32_t pattern = pattern_of(s.bin) * 0x00010001u;
     const uint32_t run = ceil_div32(share.hi - share.lo, kWarps);
     const uint32_t run_lo = min(share.hi, share.lo + warp * run), run_hi = min(share.hi, run_lo + run);
-    uint32_t mine = 0;
-    share.template each<32>(run_lo, run_hi, lane, [&](uint32_t, const uint4& q) { mine += hits(q); });
-    mine = __reduce_add_sync(kFull, mine);
+    uint32_t mine;
+    {
+        // (a lane sees at most 256 pairs, whose number either type holds exactly)
+        static_assert(SEL_SAMPLE16_MAX_V / (8 * 32 * kWarps) < 64);
+        auto sum = as_pair<T>(0);
+        const auto drawn = as_pair<T>(pattern);
+        share.template each<32, false>(run_lo, run_hi, lane, [&](uint32_t, const uint4& q) {
+            sum = __hadd2(sum, __hadd2(__hadd2(__heq2(as_pair<T>(q.x), drawn), __heq2(as_pair<T>(q.y), drawn)),
+                                       __hadd2(__heq2(as_pair<T>(q.z), drawn), __heq2(as_pair<T>(q.w), drawn))));
+        });
+        mine = __reduce_add_sync(kFull, static_cast<uint32_t>(to_f32(sum.x) + to_f32(sum.y)));
+    }
     if (lane == 0) s.seg[warp] = mine;
     __syncthreads();
     const uint32_t in = warp_scan(s.seg[lane]);
@@ -722,9 +766,16 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
     if (static_cast<int>(warp) != __ffs(__ballot_sync(kFull, place < in)) - 1) return;
     uint32_t left = place - (__shfl_sync(kFull, in, warp) - mine);  // ids of the bin before it in the run
     bool found = false;
-    share.template each<32>(run_lo, run_hi, lane, [&](uint32_t v, const uint4& q) {
+    share.template each<32, true>(run_lo, run_hi, lane, [&](uint32_t v, const uint4& q) {
         if (found) return;
-        const uint32_t n = hits(q);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+        uint32_t which = 0;  // bit i: id i of the vector
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t f = equal2<T>(w[i], pattern);
+            which |= (f & 1u) << (2 * i) | f >> 31 << (2 * i + 1);
+        }
+        const uint32_t n = __popc(which);
         const uint32_t upto = warp_scan(n);
         const uint32_t all = __shfl_sync(kFull, upto, 31);
         if (left >= all) {
@@ -734,17 +785,9 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
         found = true;
         uint32_t skip = left - (upto - n);
         if (upto - n <= left && left < upto) {
-            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (flags(w[i >> 1]) >> (16 * (i & 1)) & 1) {
-                    if (skip == 0) {
-                        a.out_ids[row] = v * 8u + i - share.skew;
-                        a.out_probs[row] = s.prob;
-                    }
-                    --skip;
-                }
-            }
+            for (; skip > 0; --skip) which &= which - 1;
+            a.out_ids[row] = v * 8u + __ffs(which) - 1 - share.skew;
+            a.out_probs[row] = s.prob;
         }
     });
 }
