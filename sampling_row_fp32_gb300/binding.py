@@ -444,14 +444,28 @@ _DTYPES = {torch.float32: SEL_F32, torch.float16: SEL_F16, torch.bfloat16: SEL_B
 _IDS = (torch.int32, torch.uint32)
 
 
-def _device(first, *others) -> None:
-    """Every tensor on the one current CUDA device (the stream's)."""
-    dev = first.device
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+# The fast forms of torch.cuda.current_device() and of the current stream's
+# handle, where this torch has them: at the smallest sizes a call costs less on
+# the GPU than the public ones do on the host.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _device(first, *others) -> int:
+    """The index of the current CUDA device, on which every tensor must be."""
+    dev = first.get_device()
+    if dev < 0 or dev != _current_device():
         raise ValueError("tensors passed to the selection library must be on the current CUDA device")
     for t in others:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != dev:
             raise ValueError("tensors of one call must be on one device")
+    return dev
+
+
+def _on_stream(stream, dev: int) -> int:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream(stream)
 
 
 def _rows_2d(t, name) -> tuple[int, int, int]:
@@ -494,7 +508,7 @@ def sel_head_w4(hidden, q, scales, zeros, group: int, logits, stream=None) -> No
     """hidden [rows, H] f16/bf16 through the 4-bit matrix (q [V, H / 2] uint8,
     scales [V, H / group] of hidden's type, zeros [V, H / group] uint8 or
     None) into logits [rows, V] (f32, f16 or bf16; its rows may be padded)."""
-    _device(hidden, q, scales, zeros, logits)
+    dev = _device(hidden, q, scales, zeros, logits)
     V, H = _w4(q, scales, zeros, group, hidden.dtype)
     rows, cols, ld = _rows_2d(logits, "logits")
     if tuple(hidden.shape) != (rows, H) or not hidden.is_contiguous():
@@ -503,14 +517,14 @@ def sel_head_w4(hidden, q, scales, zeros, group: int, logits, stream=None) -> No
         raise ValueError("logits must be [rows, V] of f32, f16 or bf16, hidden of f16 or bf16")
     _check(load().sel_head_w4(hidden.data_ptr(), rows, q.data_ptr(), scales.data_ptr(),
                               None if zeros is None else zeros.data_ptr(), group, _DTYPES[hidden.dtype], V, H,
-                              logits.data_ptr(), _DTYPES[logits.dtype], ld, _stream(stream)), "sel_head_w4")
+                              logits.data_ptr(), _DTYPES[logits.dtype], ld, _on_stream(stream, dev)), "sel_head_w4")
 
 
 def sel_sample16(logits, temperature, top_k, top_p, min_p, uniforms, out_ids, out_probs, stream=None) -> None:
     """logits [rows, V] f16/bf16 (rows may be padded); temperature, top_p,
     min_p f32 [rows] and top_k int32/uint32 [rows], each or None (1, off, off,
     off); uniforms, out_probs f32 [rows], out_ids int32/uint32 [rows]."""
-    _device(logits, temperature, top_k, top_p, min_p, uniforms, out_ids, out_probs)
+    dev = _device(logits, temperature, top_k, top_p, min_p, uniforms, out_ids, out_probs)
     rows, V, ld = _rows_2d(logits, "logits")
     if logits.dtype not in _DTYPES:
         raise ValueError("logits must be f16 or bf16")
@@ -519,7 +533,7 @@ def sel_sample16(logits, temperature, top_k, top_p, min_p, uniforms, out_ids, ou
                                _vector(temperature, rows, f32, "temperature"), _vector(top_k, rows, _IDS, "top_k"),
                                _vector(top_p, rows, f32, "top_p"), _vector(min_p, rows, f32, "min_p"),
                                _vector(uniforms, rows, f32, "uniforms"), _vector(out_ids, rows, _IDS, "out_ids"),
-                               _vector(out_probs, rows, f32, "out_probs"), _stream(stream)), "sel_sample16")
+                               _vector(out_probs, rows, f32, "out_probs"), _on_stream(stream, dev)), "sel_sample16")
 
 
 def _embed_out(ids, out, H: int, dtype) -> int:
@@ -534,26 +548,26 @@ def _embed_out(ids, out, H: int, dtype) -> int:
 def sel_embed(ids, table, scale: float, out, stream=None) -> None:
     """out[i] = scale * table[ids[i]] (zeros for ids >= V); table [V, H] f32,
     f16 or bf16, ids of any shape, out that shape plus [H]."""
-    _device(ids, table, out)
+    dev = _device(ids, table, out)
     if table.dtype not in _DTYPES or table.dim() != 2 or not table.is_contiguous():
         raise ValueError("table must be a contiguous matrix [V, H] of f32, f16 or bf16")
     V, H = table.shape
     n = _embed_out(ids, out, H, table.dtype)
     _check(load().sel_embed(ids.data_ptr(), n, table.data_ptr(), _DTYPES[table.dtype], V, H, scale, out.data_ptr(),
-                            _stream(stream)), "sel_embed")
+                            _on_stream(stream, dev)), "sel_embed")
 
 
 def sel_embed_w4(ids, q, scales, zeros, group: int, scale: float, out, stream=None) -> None:
     """sel_embed from a 4-bit matrix (as for sel_head_w4); out of the scales'
     type."""
-    _device(ids, q, scales, zeros, out)
+    dev = _device(ids, q, scales, zeros, out)
     if scales.dtype not in (torch.float16, torch.bfloat16):
         raise ValueError("scales must be f16 or bf16")
     V, H = _w4(q, scales, zeros, group, scales.dtype)
     n = _embed_out(ids, out, H, scales.dtype)
     _check(load().sel_embed_w4(ids.data_ptr(), n, q.data_ptr(), scales.data_ptr(),
                                None if zeros is None else zeros.data_ptr(), group, _DTYPES[scales.dtype], V, H, scale,
-                               out.data_ptr(), _stream(stream)), "sel_embed_w4")
+                               out.data_ptr(), _on_stream(stream, dev)), "sel_embed_w4")
 
 
 # ---------------------------------------------------------------------------

@@ -7,9 +7,10 @@
 // sequence's last emitted token) gives zeros, and reads nothing of the table.
 //
 // Bound by memory: each table row is read once and each output row written
-// once. A thread owns one 16-byte output vector, so loads and stores of a
-// warp are contiguous; the vectors of all rows form one index space, so that
-// a single long row spreads over several blocks and many short rows fill one.
+// once. A block takes up to 512 of a row's 16-byte output vectors, four a
+// thread whose loads are on their way together (a row alone is then spread
+// over several blocks); loads and stores of a warp are contiguous. 16,384 rows
+// of 5,120 bf16: 49 us, 6.8 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -23,7 +24,8 @@
 namespace sel {
 namespace {
 
-constexpr int kNT = 256;
+constexpr int kPer = 4;        // vectors (or elements) a thread
+constexpr uint32_t kMaxNT = 128;
 
 struct EmbedArgs {
     const uint32_t* ids;
@@ -31,68 +33,110 @@ struct EmbedArgs {
     const void* scales;  // 4-bit: [V][H / group]
     const uint8_t* zeros;  // 4-bit: [V][H / group] or null (8)
     void* out;           // [n][H]
-    uint64_t total;      // output vectors (or elements): n * per_row
     uint32_t per_row;    // vectors (or elements) a row
-    uint32_t V, H, group;
+    uint32_t chunks, chunk;  // blocks a row, vectors a block
+    uint32_t V, H, group_log2;
     float scale;
 };
 
-// One 16-byte vector (kVec) or one element of a table row.
+// The block's row, its id, and the vectors [c0, c1) of the row.
+struct Piece {
+    uint64_t row;
+    uint32_t id, c0, c1;
+};
+__device__ __forceinline__ Piece piece(const EmbedArgs& a) {
+    Piece p;
+    p.row = blockIdx.x / a.chunks;
+    p.c0 = (blockIdx.x % a.chunks) * a.chunk;
+    p.c1 = min(a.per_row, p.c0 + a.chunk);
+    p.id = a.ids[p.row];
+    return p;
+}
+
+// 16-byte vectors (kVec) or elements of a table row.
 template <typename T, bool kVec>
-__global__ void __launch_bounds__(kNT) embed_kernel(EmbedArgs a) {
+__global__ void __launch_bounds__(kMaxNT) embed_kernel(EmbedArgs a) {
     pdl_wait();
     pdl_trigger();
-    const uint64_t i = static_cast<uint64_t>(blockIdx.x) * kNT + threadIdx.x;
-    if (i >= a.total) return;
-    const uint64_t row = i / a.per_row;
-    const uint32_t c = static_cast<uint32_t>(i - row * a.per_row);
-    const uint32_t id = a.ids[row];
-    constexpr int kPer = 16 / sizeof(T);
-    if (kVec) {
+    const Piece p = piece(a);
+    if constexpr (kVec) {
+        const uint4* src = static_cast<const uint4*>(a.table) + static_cast<uint64_t>(p.id) * a.per_row;
+        uint4* dst = static_cast<uint4*>(a.out) + p.row * a.per_row;
+        uint4 v[kPer];
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const uint32_t c = p.c0 + j * blockDim.x + threadIdx.x;
+            v[j] = make_uint4(0, 0, 0, 0);
+            if (c < p.c1 && p.id < a.V) v[j] = ldg_stream16(src + c);
+        }
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const uint32_t c = p.c0 + j * blockDim.x + threadIdx.x;
+            T* e = reinterpret_cast<T*>(&v[j]);
+#pragma unroll
+            for (int k = 0; k < static_cast<int>(16 / sizeof(T)); ++k) e[k] = from_f32<T>(to_f32(e[k]) * a.scale);
+            if (p.id >= a.V) v[j] = make_uint4(0, 0, 0, 0);  // (0 * scale may be NaN)
+            if (c < p.c1) dst[c] = v[j];
+        }
+    } else {
+        const T* src = static_cast<const T*>(a.table) + static_cast<uint64_t>(p.id) * a.H;
+        T* dst = static_cast<T*>(a.out) + p.row * a.H;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const uint32_t c = p.c0 + j * blockDim.x + threadIdx.x;
+            if (c < p.c1) dst[c] = p.id < a.V ? from_f32<T>(to_f32(src[c]) * a.scale) : from_f32<T>(0.0f);
+        }
+    }
+}
+
+// Vectors of eight columns: one 32-bit word of nibbles each.
+template <typename T>
+__global__ void __launch_bounds__(kMaxNT) embed_w4_kernel(EmbedArgs a) {
+    pdl_wait();
+    pdl_trigger();
+    const Piece p = piece(a);
+    const uint32_t* src = static_cast<const uint32_t*>(a.table) + static_cast<uint64_t>(p.id) * a.per_row;
+    const uint64_t g0 = static_cast<uint64_t>(p.id) * (a.H >> a.group_log2);
+    uint4* dst = static_cast<uint4*>(a.out) + p.row * a.per_row;
+    uint32_t w[kPer];
+    float s[kPer];
+    int z[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const uint32_t c = p.c0 + j * blockDim.x + threadIdx.x;
+        w[j] = 0;
+        s[j] = 0.0f;
+        z[j] = 8;
+        if (c < p.c1 && p.id < a.V) {
+            const uint64_t g = g0 + (c * 8u >> a.group_log2);
+            w[j] = src[c];
+            s[j] = to_f32(static_cast<const T*>(a.scales)[g]);
+            if (a.zeros) z[j] = a.zeros[g] & 15;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const uint32_t c = p.c0 + j * blockDim.x + threadIdx.x;
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (id < a.V) {
-            v = ldg_stream16(static_cast<const T*>(a.table) + static_cast<size_t>(id) * a.H + static_cast<size_t>(c) * kPer);
+        if (p.id < a.V) {
             T* e = reinterpret_cast<T*>(&v);
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) e[j] = from_f32<T>(to_f32(e[j]) * a.scale);
+            for (int k = 0; k < 8; ++k)
+                e[k] = from_f32<T>(s[j] * static_cast<float>(static_cast<int>((w[j] >> (4 * k)) & 15u) - z[j]) * a.scale);
         }
-        reinterpret_cast<uint4*>(a.out)[i] = v;
-    } else {
-        float x = 0.0f;
-        if (id < a.V) x = to_f32(static_cast<const T*>(a.table)[static_cast<size_t>(id) * a.H + c]) * a.scale;
-        static_cast<T*>(a.out)[i] = from_f32<T>(x);
+        if (c < p.c1) dst[c] = v;
     }
 }
 
-// Eight columns (one 32-bit word of nibbles, one 16-byte output vector).
-template <typename T>
-__global__ void __launch_bounds__(kNT) embed_w4_kernel(EmbedArgs a) {
-    pdl_wait();
-    pdl_trigger();
-    const uint64_t i = static_cast<uint64_t>(blockIdx.x) * kNT + threadIdx.x;
-    if (i >= a.total) return;
-    const uint64_t row = i / a.per_row;
-    const uint32_t c = static_cast<uint32_t>(i - row * a.per_row);
-    const uint32_t id = a.ids[row];
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (id < a.V) {
-        const uint32_t w = static_cast<const uint32_t*>(a.table)[static_cast<size_t>(id) * a.per_row + c];
-        const size_t g = static_cast<size_t>(id) * (a.H / a.group) + (c * 8u) / a.group;
-        const float s = to_f32(static_cast<const T*>(a.scales)[g]);
-        const int z = a.zeros ? a.zeros[g] & 15 : 8;
-        T* e = reinterpret_cast<T*>(&v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            e[j] = from_f32<T>(s * static_cast<float>(static_cast<int>((w >> (4 * j)) & 15u) - z) * a.scale);
-    }
-    reinterpret_cast<uint4*>(a.out)[i] = v;
-}
-
+// per_row vectors a row, in equal pieces of at most kPer a thread.
 template <typename K>
-sel_status launch(K kernel, const EmbedArgs& a, cudaStream_t stream) {
-    const uint64_t blocks = (a.total + kNT - 1) / kNT;
+sel_status launch(K kernel, EmbedArgs a, uint32_t n, cudaStream_t stream) {
+    a.chunks = ceil_div(a.per_row, kPer * kMaxNT);
+    a.chunk = ceil_div(a.per_row, a.chunks);
+    const uint64_t blocks = static_cast<uint64_t>(n) * a.chunks;
     if (blocks > 0x7fffffffull) return SEL_EUNSUPPORTED;
-    const cudaError_t e = launch_pdl(kernel, dim3(static_cast<uint32_t>(blocks)), dim3(kNT), 0, stream, a);
+    const uint32_t nt = ceil_div(ceil_div(a.chunk, kPer), 32) * 32;
+    const cudaError_t e = launch_pdl(kernel, dim3(static_cast<uint32_t>(blocks)), dim3(nt), 0, stream, a);
     return e == cudaSuccess ? SEL_OK : SEL_ECUDA;
 }
 
@@ -101,8 +145,7 @@ sel_status embed(EmbedArgs a, uint32_t n, cudaStream_t stream) {
     const bool vec = reinterpret_cast<uintptr_t>(a.table) % 16 == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0 &&
                      (static_cast<uint64_t>(a.H) * sizeof(T)) % 16 == 0;
     a.per_row = vec ? static_cast<uint32_t>(a.H * sizeof(T) / 16) : a.H;
-    a.total = static_cast<uint64_t>(n) * a.per_row;
-    return vec ? launch(embed_kernel<T, true>, a, stream) : launch(embed_kernel<T, false>, a, stream);
+    return vec ? launch(embed_kernel<T, true>, a, n, stream) : launch(embed_kernel<T, false>, a, n, stream);
 }
 
 }  // namespace
@@ -146,10 +189,9 @@ extern "C" sel_status sel_embed_w4(const uint32_t* d_ids, uint32_t n, const uint
     a.out = d_out;
     a.V = V;
     a.H = H;
-    a.group = group;
+    a.group_log2 = group == 32 ? 5 : group == 64 ? 6 : 7;
     a.scale = scale;
     a.per_row = H / 8;
-    a.total = static_cast<uint64_t>(n) * a.per_row;
-    return dtype == SEL_F16 ? launch(embed_w4_kernel<__half>, a, stream)
-                            : launch(embed_w4_kernel<__nv_bfloat16>, a, stream);
+    return dtype == SEL_F16 ? launch(embed_w4_kernel<__half>, a, n, stream)
+                            : launch(embed_w4_kernel<__nv_bfloat16>, a, n, stream);
 }

@@ -592,7 +592,7 @@ sel_status launch(const HeadIn& in, const HeadArgs& args, cudaStream_t stream) {
         cudaFuncAttributes f{};
         return cudaFuncGetAttributes(&f, head_kernel<T, O, N>) == cudaSuccess && f.numRegs == kLaunchRegs;
     }();
-    if (!regs_ok || !set_dynamic_smem(head_kernel<T, O, N>, Config<N>::kSmem)) return SEL_ECUDA;
+    if (!regs_ok || !dynamic_smem_once<head_kernel<T, O, N>>(Config<N>::kSmem)) return SEL_ECUDA;
     const cudaError_t e = launch_pdl(head_kernel<T, O, N>, dim3(ceil_div(a.V, a.range)), dim3(kNT), Config<N>::kSmem,
                                      stream, mt, mb, mx, a);
     return e == cudaSuccess ? SEL_OK : SEL_ECUDA;

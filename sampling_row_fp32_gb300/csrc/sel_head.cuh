@@ -179,10 +179,12 @@ __device__ __forceinline__ void copy_words(unsigned char* dst, const unsigned ch
 template <uint32_t kBytes, uint32_t kBatch>
 __device__ __forceinline__ void copy_rows(unsigned char* dst, const unsigned char* src, uint32_t at, uint32_t row_bytes,
                                           uint32_t rows, uint32_t width) {
+    // (narrow words: twice as many on their way, 54 us against 41 for 5 rows of
+    // 2,880 x 93,001 with groups of 32, whose rows of scales are 180 bytes)
     if (width >= kBytes) copy_words<kBytes, kBytes, kBatch>(dst, src, at, row_bytes, rows);
-    else if (kBytes > 4 && width >= 4) copy_words<kBytes, kBytes < 4 ? kBytes : 4, kBatch>(dst, src, at, row_bytes, rows);
-    else if (kBytes > 2 && width >= 2) copy_words<kBytes, 2, kBatch>(dst, src, at, row_bytes, rows);
-    else copy_words<kBytes, 1, kBatch>(dst, src, at, row_bytes, rows);
+    else if (kBytes > 4 && width >= 4) copy_words<kBytes, kBytes < 4 ? kBytes : 4, 2 * kBatch>(dst, src, at, row_bytes, rows);
+    else if (kBytes > 2 && width >= 2) copy_words<kBytes, 2, 2 * kBatch>(dst, src, at, row_bytes, rows);
+    else copy_words<kBytes, 1, 2 * kBatch>(dst, src, at, row_bytes, rows);
 }
 template <uint32_t kBytes>
 __device__ __forceinline__ void read_entries(uint32_t src, uint32_t (&v)[(kBytes + 3) / 4]) {

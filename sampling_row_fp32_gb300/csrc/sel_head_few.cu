@@ -353,8 +353,8 @@ sel_status launch(const HeadIn& in, const HeadArgs& args, cudaStream_t stream) {
     if (f.stages > kMaxStages) f.stages = kMaxStages;
     CUtensorMap map;
     if (!make_weight_map(&map, in.q, args.V, args.H, f.tile / 2)) return SEL_ECUDA;
-    const auto kernel = head_few_kernel<T, O, kGroupLog2, kZeros>;
-    if (!set_dynamic_smem(kernel, kSmemBytes)) return SEL_ECUDA;
+    constexpr auto kernel = head_few_kernel<T, O, kGroupLog2, kZeros>;
+    if (!dynamic_smem_once<kernel>(kSmemBytes)) return SEL_ECUDA;
     const cudaError_t e = launch_pdl(kernel, dim3(ceil_div(args.V, f.a.range)), dim3(32 * (f.tile / 16 + 1 + kHelpers)),
                                      1024 + f.stages * f.tile * row_bytes + x_bytes, stream, map,
                                      static_cast<const T*>(in.x), f);

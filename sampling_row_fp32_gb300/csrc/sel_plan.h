@@ -2,6 +2,7 @@
 // workspace layout shared by the operations.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -19,6 +20,21 @@ inline uint32_t ceil_div(uint64_t a, uint64_t b) {
 
 // Multiprocessor count of the current device (0 if it cannot be queried).
 int device_sms();
+
+// Lets kernel K use `bytes` of dynamic shared memory: asked of the driver once
+// for each device.
+template <auto K>
+inline bool dynamic_smem_once(size_t bytes) {
+    static std::atomic<uint64_t> done{0};  // a bit a device
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return true;
+    if (cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) != cudaSuccess)
+        return false;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+}
 
 // Workspace bytes of each operation (0 when none is needed).
 size_t argmax_ws_bytes(uint32_t rows, uint32_t V);

@@ -838,7 +838,7 @@ uint32_t ctas_for(uint32_t rows, uint32_t V) {
 
 template <typename T>
 sel_status launch(const SampleArgs& in, uint32_t rows, cudaStream_t stream) {
-    if (!set_dynamic_smem(sample16_kernel<T>, sizeof(Shared))) return SEL_ECUDA;
+    if (!dynamic_smem_once<sample16_kernel<T>>(sizeof(Shared))) return SEL_ECUDA;
     const uint32_t vecs = ceil_div(static_cast<uint64_t>(in.V) + 7, 8), C = ctas_for<T>(rows, in.V);
     if (static_cast<uint64_t>(rows) * C > 0x7fffffffull) return SEL_EUNSUPPORTED;
     SampleArgs a = in;
