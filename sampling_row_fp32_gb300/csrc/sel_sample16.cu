@@ -395,7 +395,9 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
         if (want && want < kBatchVecs * 8) {
             // The top `want` ids of the first batch bound those of the row from
             // below: the rest of the share only counts what is not under them.
-            at += kBatchVecs;
+            // (A 64th of the batch, where it can be: the bound then lets about that
+            // much through.)
+            at += min(kBatchVecs, max(static_cast<uint32_t>(kNT), want * 8u));
             n = count_all(share.lo, at);
             __syncthreads();
 #pragma unroll
