@@ -33,6 +33,13 @@ __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2hal
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
+// Element i of an array of a type that is known at run time only.
+__device__ __forceinline__ void store_as(void* p, int dtype, uint64_t i, float x) {
+    if (dtype == SEL_F32) static_cast<float*>(p)[i] = x;
+    else if (dtype == SEL_F16) static_cast<__half*>(p)[i] = __float2half_rn(x);
+    else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x);
+}
+
 __device__ __forceinline__ uint4 ldg_stream16(const void* p) {
     uint4 v;
     asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"

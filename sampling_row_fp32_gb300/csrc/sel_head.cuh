@@ -31,6 +31,7 @@ struct HeadArgs {
     const uint8_t* zeros;
     void* out;
     uint64_t ld;
+    int out_dtype;
     uint32_t rows, V, H, group_log2;
     uint32_t range;  // matrix rows a CTA
 };
@@ -47,7 +48,11 @@ struct HeadIn {
 inline bool head_few_fits(uint32_t rows, uint32_t H) {
     return rows <= 8 && static_cast<uint64_t>(rows) * ceil_div(H, kStageK) * kStageK * 2 <= 128u * 1024u;
 }
-sel_status head_few(int dtype, int out_dtype, const HeadIn& in, const HeadArgs& a, cudaStream_t stream);
+sel_status head_few(int dtype, const HeadIn& in, const HeadArgs& a, cudaStream_t stream);
+
+// Any number of hidden rows; the matrix is read once for every 64.
+template <typename T>
+sel_status head_many(const HeadIn& in, const HeadArgs& a, cudaStream_t stream);
 
 __device__ __forceinline__ void tma_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
     asm volatile(
@@ -283,8 +288,15 @@ inline bool make_map(CUtensorMap* map, CUtensorMapDataType type, uint32_t elem, 
     if (!f) return false;
     const cuuint64_t dims[2] = {cols, rows}, strides[1] = {cols * elem};
     const cuuint32_t box[2] = {box_cols, box_rows}, step[2] = {1, 1};
-    return f(map, type, 2, const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    auto encode = [&] {
+        return f(map, type, 2, const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                 CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    if (encode()) return true;
+    // A host thread whose first CUDA call this is has no context yet, which the
+    // driver's function, unlike the runtime's, does not see to.
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode();
 }
 
 // Packed weights in copies of box_rows rows of a stage.

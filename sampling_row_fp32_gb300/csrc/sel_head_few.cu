@@ -1,7 +1,7 @@
 // sel_head_few.cu -- the 4-bit output head for at most 8 hidden rows (plain
 // decoding, a few sequences), where the weights' bytes are the whole cost.
 //
-// The same sums as sel_head.cu, with the products on warp-level matrix
+// The same sums as sel_head_many.cuh, with the products on warp-level matrix
 // instructions whose A operand (the weights) comes from registers: an
 // unpacked word needs no trip through tensor memory, and because this kernel
 // lays out the hidden rows, a pair of operand columns may be any two columns.
@@ -105,7 +105,7 @@ __device__ __forceinline__ int row_shift(uint32_t m) {
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
 // The consuming warps: operands of type E (T, or f16 for a bf16 T).
-template <typename T, typename E, typename O, int kGroupLog2, bool kZeros>
+template <typename T, typename E, int kGroupLog2, bool kZeros>
 __device__ __forceinline__ void consume(Ctx& c, uint32_t ring, uint32_t entries, uint32_t xs, const FewArgs& f, uint32_t v_begin,
                                         uint32_t v_end) {
     using B = EntryBytes<kGroupLog2>;
@@ -179,13 +179,13 @@ __device__ __forceinline__ void consume(Ctx& c, uint32_t ring, uint32_t entries,
             if (active && r < a.rows && v < v_end) {
                 float y = acc[e];
                 if constexpr (!std::is_same_v<T, E>) y *= exp2i(-row_shift(c.largest[r]));
-                static_cast<O*>(a.out)[r * a.ld + v] = from_f32<O>(y);
+                store_as(a.out, a.out_dtype, r * a.ld + v, y);
             }
         }
     }
 }
 
-template <typename T, typename O, int kGroupLog2, bool kZeros>
+template <typename T, int kGroupLog2, bool kZeros>
 __global__ void __launch_bounds__(kMaxNT, 1)
     head_few_kernel(const __grid_constant__ CUtensorMap map, const T* x, const __grid_constant__ FewArgs f) {
     const HeadArgs& a = f.a;
@@ -321,21 +321,21 @@ __global__ void __launch_bounds__(kMaxNT, 1)
         }
         const uint32_t rs = smem_u32(ring), es = smem_u32(entries), xa = smem_u32(xs);
         if constexpr (std::is_same_v<T, __nv_bfloat16>) {
-            if (as_f16) consume<T, __half, O, kGroupLog2, kZeros>(c, rs, es, xa, f, v_begin, v_end);
-            else consume<T, T, O, kGroupLog2, kZeros>(c, rs, es, xa, f, v_begin, v_end);
+            if (as_f16) consume<T, __half, kGroupLog2, kZeros>(c, rs, es, xa, f, v_begin, v_end);
+            else consume<T, T, kGroupLog2, kZeros>(c, rs, es, xa, f, v_begin, v_end);
         } else {
-            consume<T, T, O, kGroupLog2, kZeros>(c, rs, es, xa, f, v_begin, v_end);
+            consume<T, T, kGroupLog2, kZeros>(c, rs, es, xa, f, v_begin, v_end);
         }
     }
     __syncthreads();
     if (c.err) {  // a wait ran out: nothing this CTA wrote can be trusted
         for (uint32_t r = 0; r < a.rows; ++r)
             for (uint32_t v = v_begin + tid; v < v_end; v += blockDim.x)
-                static_cast<O*>(a.out)[r * a.ld + v] = from_f32<O>(__uint_as_float(0x7FC00000u));
+                store_as(a.out, a.out_dtype, r * a.ld + v, __uint_as_float(0x7FC00000u));
     }
 }
 
-template <typename T, typename O, int kGroupLog2, bool kZeros>
+template <typename T, int kGroupLog2, bool kZeros>
 sel_status launch(const HeadIn& in, const HeadArgs& args, cudaStream_t stream) {
     const int sms = device_sms();
     if (sms <= 0) return SEL_ECUDA;
@@ -353,7 +353,7 @@ sel_status launch(const HeadIn& in, const HeadArgs& args, cudaStream_t stream) {
     if (f.stages > kMaxStages) f.stages = kMaxStages;
     CUtensorMap map;
     if (!make_weight_map(&map, in.q, args.V, args.H, f.tile / 2)) return SEL_ECUDA;
-    constexpr auto kernel = head_few_kernel<T, O, kGroupLog2, kZeros>;
+    constexpr auto kernel = head_few_kernel<T, kGroupLog2, kZeros>;
     if (!dynamic_smem_once<kernel>(kSmemBytes)) return SEL_ECUDA;
     const cudaError_t e = launch_pdl(kernel, dim3(ceil_div(args.V, f.a.range)), dim3(32 * (f.tile / 16 + 1 + kHelpers)),
                                      1024 + f.stages * f.tile * row_bytes + x_bytes, stream, map,
@@ -361,32 +361,22 @@ sel_status launch(const HeadIn& in, const HeadArgs& args, cudaStream_t stream) {
     return e == cudaSuccess ? SEL_OK : SEL_ECUDA;
 }
 
-template <typename T, typename O, bool kZeros>
+template <typename T, bool kZeros>
 sel_status launch_group(const HeadIn& in, const HeadArgs& a, cudaStream_t stream) {
-    if (a.group_log2 == 7) return launch<T, O, 7, kZeros>(in, a, stream);
-    if (a.group_log2 == 6) return launch<T, O, 6, kZeros>(in, a, stream);
-    return launch<T, O, 5, kZeros>(in, a, stream);
-}
-
-template <typename T, typename O>
-sel_status launch_zeros(const HeadIn& in, const HeadArgs& a, cudaStream_t stream) {
-    return a.zeros ? launch_group<T, O, true>(in, a, stream) : launch_group<T, O, false>(in, a, stream);
+    if (a.group_log2 == 7) return launch<T, 7, kZeros>(in, a, stream);
+    if (a.group_log2 == 6) return launch<T, 6, kZeros>(in, a, stream);
+    return launch<T, 5, kZeros>(in, a, stream);
 }
 
 template <typename T>
-sel_status launch_out(int out_dtype, const HeadIn& in, const HeadArgs& a, cudaStream_t stream) {
-    switch (out_dtype) {
-        case SEL_F32: return launch_zeros<T, float>(in, a, stream);
-        case SEL_F16: return launch_zeros<T, __half>(in, a, stream);
-        default: return launch_zeros<T, __nv_bfloat16>(in, a, stream);
-    }
+sel_status launch_zeros(const HeadIn& in, const HeadArgs& a, cudaStream_t stream) {
+    return a.zeros ? launch_group<T, true>(in, a, stream) : launch_group<T, false>(in, a, stream);
 }
 
 }  // namespace
 
-sel_status head_few(int dtype, int out_dtype, const HeadIn& in, const HeadArgs& a, cudaStream_t stream) {
-    return dtype == SEL_F16 ? launch_out<__half>(out_dtype, in, a, stream)
-                            : launch_out<__nv_bfloat16>(out_dtype, in, a, stream);
+sel_status head_few(int dtype, const HeadIn& in, const HeadArgs& a, cudaStream_t stream) {
+    return dtype == SEL_F16 ? launch_zeros<__half>(in, a, stream) : launch_zeros<__nv_bfloat16>(in, a, stream);
 }
 
 }  // namespace sel

@@ -1,6 +1,11 @@
 """The operators around selection in the order a decode step runs them: hidden
 states through the 4-bit head, a token per row from the 16-bit logits (or an
 fp32 call), the tokens' vectors from the same 4-bit matrix."""
+import os
+import subprocess
+import sys
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -137,3 +142,86 @@ def test_a_failed_row_reaches_the_next_step_as_zeros():
     s.run()
     assert int(s.ids[2]) == -1 and torch.isnan(s.probs[2]) and not s.next[2].any()
     assert (s.ids[[0, 1, 3, 4, 5, 6]] >= 0).all()
+
+
+FIRST_CALL = """
+import torch
+from sampling_row_fp32_gb300 import binding as B
+rows, V, H = ROWS, 9001, 256
+q = torch.randint(0, 256, (V, H // 2), dtype=torch.uint8, device="cuda")
+s = torch.full((V, H // 64), 0.01, dtype=torch.bfloat16, device="cuda")
+x = torch.randn(rows, H, device="cuda").bfloat16()
+logits = torch.full((rows, V), 7.0, dtype=torch.bfloat16, device="cuda")
+ids = torch.full((rows,), -7, dtype=torch.int32, device="cuda")
+probs, u = torch.empty(rows, device="cuda"), torch.rand(rows, device="cuda")
+out = torch.empty(rows, H, dtype=torch.bfloat16, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    B.sel_head_w4(x, q, s, None, 64, logits)
+    B.sel_sample16(logits, None, None, None, None, u, ids, probs)
+    B.sel_embed_w4(ids, q, s, None, 64, 1.0, out)
+g.replay()
+torch.cuda.synchronize()
+assert ((ids >= 0) & (ids < V)).all() and (probs > 0).all()
+w = (torch.stack((q & 15, q >> 4), 2).view(V, H).float() - 8) * s.float().repeat_interleave(64, 1)
+assert torch.allclose(logits.float(), x.float() @ w.t(), rtol=2.0 ** -7, atol=1e-3)
+assert torch.equal(out.float(), w[ids.long()].bfloat16().float())
+print("captured")
+"""
+
+
+@pytest.mark.parametrize("rows", [3, 40])
+def test_first_call_of_a_process_inside_a_capture(rows):
+    """Whatever the library asks of the driver once is allowed in a capture."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL.replace("ROWS", str(rows))], cwd=root, capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_calls_from_two_threads():
+    """Two host threads, each on its own stream with its own buffers."""
+    steps = [Step(8), Step(9, rows=25)]
+    streams = [torch.cuda.Stream() for _ in steps]
+    torch.cuda.synchronize()
+
+    def work(i):
+        for _ in range(30):
+            steps[i].run(streams[i])
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for s in steps:
+        s.check()
+
+
+def test_binding_refuses_wrong_shapes():
+    s = Step(10)
+    with pytest.raises(ValueError):
+        B.sel_head_w4(s.hidden[:, ::2], s.q, s.s, s.z, GROUP, s.logits)
+    with pytest.raises(ValueError):
+        B.sel_head_w4(s.hidden, s.q, s.s[:, :-1].contiguous(), s.z, GROUP, s.logits)
+    with pytest.raises(ValueError):
+        B.sel_head_w4(s.hidden, s.q, s.s.half(), s.z, GROUP, s.logits)
+    with pytest.raises(ValueError):
+        B.sel_head_w4(s.hidden, s.q, s.s, s.z, GROUP, s.logits[:, :-1])
+    with pytest.raises(B.SelError):
+        B.sel_head_w4(s.hidden, s.q, torch.empty(V, H // 16, dtype=torch.bfloat16, device="cuda"), None, 16, s.logits)
+    with pytest.raises(ValueError):
+        B.sel_sample16(s.logits, s.T[:-1], s.k, s.p, s.m, s.u, s.ids, s.probs)
+    with pytest.raises(ValueError):
+        B.sel_sample16(s.logits, s.T, s.k.float(), s.p, s.m, s.u, s.ids, s.probs)
+    with pytest.raises(ValueError):
+        B.sel_sample16(s.logits.t(), s.T, s.k, s.p, s.m, s.u, s.ids, s.probs)
+    with pytest.raises(B.SelError):  # fp32 rows are sel_sample's
+        B.sel_sample16(s.logits.float().contiguous(), s.T, s.k, s.p, s.m, s.u, s.ids, s.probs)
+    with pytest.raises(ValueError):
+        B.sel_embed_w4(s.ids, s.q, s.s, s.z, GROUP, 1.0, s.next[:-1])
+    with pytest.raises(ValueError):
+        B.sel_embed(s.ids, s.s.float()[:, :4], 1.0, s.probs)
+    with pytest.raises(ValueError):
+        B.sel_embed(s.ids.long(), s.s, 1.0, torch.empty(ROWS, H // GROUP, dtype=torch.bfloat16, device="cuda"))

@@ -116,18 +116,50 @@ def test_no_rows():
     B.sel_head_w4(x.cuda(), q.cuda(), s.cuda(), None, 64, torch.empty(0, 10, device="cuda"))
 
 
-def test_nonfinite_inputs_fail_closed():
+@pytest.mark.parametrize("rows", [3, 20, 40])
+def test_nonfinite_inputs_fail_closed(rows):
     """A NaN hidden state or scale reaches its row's or column's logits and no others."""
-    x, q, s, z = make(1, 3, 200, 256, 64, None, "bf16")
+    x, q, s, z = make(1, rows, 200, 256, 64, None, "bf16")
     x[1, 130] = float("nan")
     s[77, 2] = float("inf")
-    logits = torch.empty(3, 200, device="cuda")
+    logits = torch.empty(rows, 200, device="cuda")
     B.sel_head_w4(x.cuda(), q.cuda(), s.cuda(), None, 64, logits)
     finite = torch.isfinite(logits).cpu()
-    want = torch.ones(3, 200, dtype=torch.bool)
+    want = torch.ones(rows, 200, dtype=torch.bool)
     want[1] = False
     want[:, 77] = False
     assert torch.equal(finite, want)
+
+
+@pytest.mark.parametrize("rows", [2, 30, 70])
+def test_results_do_not_depend_on_the_run(rows):
+    """The same bits in every run, and with other work on a second stream."""
+    x, q, s, z = (None if t is None else t.cuda() for t in make(5, rows, 5001, 1024, 32, "nibble", "f16"))
+    outs = [torch.empty(rows, 5001, device="cuda") for _ in range(6)]
+    other = torch.empty(rows, 5001, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for o in outs:
+        with torch.cuda.stream(side):
+            B.sel_head_w4(x, q, s, None, 32, other, side)
+        B.sel_head_w4(x, q, s, z, 32, o)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, outs[0]) for o in outs)
+
+
+@pytest.mark.parametrize("rows", [4, 33])
+@pytest.mark.parametrize("off", [2, 4, 6])
+def test_entries_at_any_alignment(rows, off):
+    """Scales `off` bytes and zero points off / 2 bytes past a 16-byte boundary."""
+    x, q, s, z = make(6, rows, 999, 1024, 64, "nibble", "bf16")
+    fs = torch.empty(s.numel() + 8, dtype=s.dtype, device="cuda")[off // 2:off // 2 + s.numel()].view(s.shape)
+    fz = torch.empty(z.numel() + 16, dtype=z.dtype, device="cuda")[off // 2:off // 2 + z.numel()].view(z.shape)
+    fs.copy_(s)
+    fz.copy_(z)
+    out, want = (torch.empty(rows, 999, device="cuda") for _ in range(2))
+    B.sel_head_w4(x.cuda(), q.cuda(), fs, fz, 64, out)
+    B.sel_head_w4(x.cuda(), q.cuda(), s.cuda(), z.cuda(), 64, want)
+    assert torch.equal(out, want)
 
 
 def test_offsets_past_32_bits():

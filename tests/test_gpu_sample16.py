@@ -120,6 +120,13 @@ def test_values_that_fill_a_counter(rows, kind):
     check(torch.from_numpy(x).to(torch.bfloat16), policies(rng, rows, V), rng.random(rows, dtype=np.float32), 3, 1)
 
 
+def test_widest_rows_in_one_cta_each():
+    V, rows = B.SEL_SAMPLE16_MAX_V, 130
+    rng = np.random.default_rng(10)
+    x = rows_of(rng, "normal", 10, V, "f16").repeat(13, 1)
+    check(x, policies(rng, rows, V), rng.random(rows, dtype=np.float32))
+
+
 def test_widest_row():
     V = B.SEL_SAMPLE16_MAX_V
     rng = np.random.default_rng(9)
