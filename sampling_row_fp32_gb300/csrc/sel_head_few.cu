@@ -208,11 +208,17 @@ __global__ void __launch_bounds__(kMaxNT, 1)
         c.err = 0;
     }
     if (tid < 8) c.largest[tid] = 0;
+    const uint32_t v_begin = blockIdx.x * a.range, v_end = min(a.V, v_begin + a.range);
+    if (warp == workers && elect_one()) {  // the first stages, while the launch before ends
+        const uint32_t n = min(f.stages, (a.H + kStageK - 1) / kStageK);
+        for (uint32_t i = 0; i < n; ++i) {
+            tma_prefetch_2d(&map, i * kRowBytes, v_begin);
+            if (v_begin + f.tile / 2 < v_end) tma_prefetch_2d(&map, i * kRowBytes, v_begin + f.tile / 2);
+        }
+    }
     __syncthreads();
     pdl_wait();
     pdl_trigger();
-
-    const uint32_t v_begin = blockIdx.x * a.range, v_end = min(a.V, v_begin + a.range);
     if (warp == workers) {
         const uint32_t stages = (a.H + kStageK - 1) / kStageK;
         const bool leader = elect_one();

@@ -485,14 +485,17 @@ __global__ void __launch_bounds__(kNT, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
+    const uint32_t v_begin = blockIdx.x * a.range, v_end = min(a.V, v_begin + a.range);
+    if (warp == 0 && elect_one() && v_end - v_begin >= kTileV) {  // the first stages, while the launch before ends
+        const uint32_t n = min(C::kStages, (a.H + kStageK - 1) / kStageK);
+        for (uint32_t i = 0; i < n; ++i) tma_prefetch_2d(&map_tile, i * (kStageK / 2), v_begin);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(kFull, c.tmem, 0);
     pdl_wait();
     pdl_trigger();
-
-    const uint32_t v_begin = blockIdx.x * a.range, v_end = min(a.V, v_begin + a.range);
     const uint32_t blocks = (a.rows + N - 1) / N;  // blocks of hidden rows
     const uint32_t quarter = warp & 3;
 
