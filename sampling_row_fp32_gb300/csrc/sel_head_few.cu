@@ -106,6 +106,15 @@ __device__ __forceinline__ int row_shift(uint32_t m) {
 }
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
+__device__ __forceinline__ void mul2(float& a, float& b, const float (&f)[2]) {
+    asm("{\n\t.reg .b64 x, y;\n\t"
+        "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+        "mul.rn.f32x2 x, x, y;\n\t"
+        "mov.b64 {%0, %1}, x;\n\t}"
+        : "+f"(a), "+f"(b)
+        : "f"(f[0]), "f"(f[1]));
+}
+
 // The consuming warps: operands of type E (T, or f16 for a bf16 T).
 template <typename T, typename E, int kGroupLog2, bool kZeros>
 __device__ __forceinline__ void consume(Ctx& c, uint32_t ring, uint32_t entries, uint32_t xs, const FewArgs& f, uint32_t v_begin,
@@ -124,6 +133,19 @@ __device__ __forceinline__ void consume(Ctx& c, uint32_t ring, uint32_t entries,
     const uint32_t entry_bytes = f.tile * (B::kScales + (kZeros ? B::kZeros : 0));  // a slot's
     const uint32_t e0 = entries + row * B::kScales, ez = entries + f.tile * B::kScales + row * B::kZeros;
     const uint32_t x_block = a.rows * 64, slot_bytes = f.tile * kRowBytes;
+    // Rows that were scaled up go back before the group's scale meets their sums,
+    // rows that were scaled down at the end: nothing in between overflows that
+    // unscaled sums would not.
+    constexpr bool kScaled = !std::is_same_v<T, E>;
+    float down[2], up[2];
+    if constexpr (kScaled) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int sh = row_shift(c.largest[min(2 * t + e, a.rows - 1)]);
+            down[e] = exp2i(min(-sh, 0));
+            up[e] = exp2i(max(-sh, 0));
+        }
+    }
     uint32_t slot = 0, phase = 0;
     for (uint32_t vt = v_begin; vt < v_end; vt += f.tile) {
         const bool active = warp * 16 < v_end - vt;
@@ -160,6 +182,10 @@ __device__ __forceinline__ void consume(Ctx& c, uint32_t ring, uint32_t entries,
                     mma<E>(d, a23, xv[2], xv[3]);
                     if (b % kBlocks == kBlocks - 1) {
                         const float sa = bits_f32<T>(entry16(sc[0], grp)), sb = bits_f32<T>(entry16(sc[1], grp));
+                        if constexpr (kScaled) {
+                            mul2(d[0], d[1], down);
+                            mul2(d[2], d[3], down);
+                        }
                         acc[0] = fmaf(sa, d[0], acc[0]);
                         acc[1] = fmaf(sa, d[1], acc[1]);
                         acc[2] = fmaf(sb, d[2], acc[2]);
@@ -178,11 +204,8 @@ __device__ __forceinline__ void consume(Ctx& c, uint32_t ring, uint32_t entries,
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const uint32_t r = 2 * t + (e & 1), v = vt + row + 8 * (e >> 1);
-            if (active && r < a.rows && v < v_end) {
-                float y = acc[e];
-                if constexpr (!std::is_same_v<T, E>) y *= exp2i(-row_shift(c.largest[r]));
-                store_as(a.out, a.out_dtype, r * a.ld + v, y);
-            }
+            if constexpr (kScaled) acc[e] *= up[e & 1];
+            if (active && r < a.rows && v < v_end) store_as(a.out, a.out_dtype, r * a.ld + v, acc[e]);
         }
     }
 }

@@ -111,6 +111,14 @@ def test_hidden_states_at_the_ends_of_bf16(scale):
     check((x.double() * scale).bfloat16(), q, s, z, 128)
 
 
+@pytest.mark.parametrize("rows", [1, 6, 20])
+@pytest.mark.parametrize("hidden,scale", [(2.0 ** -110, 2.0 ** 120), (2.0 ** 100, 2.0 ** -122), (2.0 ** 100, 2.0 ** -40)])
+def test_small_hidden_states_meet_large_scales(rows, hidden, scale):
+    """Only their products need to be in range, not a row's scaled sums."""
+    x, q, s, z = make(11, rows, 300, 512, 64, "nibble", "bf16")
+    check(x * hidden, q, s * scale, z, 64)
+
+
 def test_no_rows():
     x, q, s, z = make(0, 0, 10, 64, 64, None, "bf16")
     B.sel_head_w4(x.cuda(), q.cuda(), s.cuda(), None, 64, torch.empty(0, 10, device="cuda"))
