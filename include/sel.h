@@ -714,7 +714,8 @@ sel_status sel_head_w4(const void *d_hidden, uint32_t rows, const uint8_t *d_q,
  * survivor in that order whose cumulative mass exceeds u times the
  * survivors' mass. This is sel_sample's order for top_k > 0; a row with
  * top_k == 0 is walked in the same order here (sel_sample walks it by
- * ascending id). Ranks are counted exactly; masses are sums in 64 bits.
+ * ascending id). Ranks are counted
+ * exactly; masses are sums of float pairs, to about 45 bits.
  * A logit of -Inf is a masked id: it is never drawn and does not count.
  *
  *   d_logits       rows of V of `dtype` (SEL_F16 or SEL_BF16), row r at

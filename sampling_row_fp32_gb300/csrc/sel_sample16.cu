@@ -7,8 +7,8 @@
 // surviving prefix whose cumulative mass exceeds u times the prefix's mass.
 // A 16-bit row holds at most 65,536 distinct logits, so a histogram of the
 // 16-bit patterns holds all of it: ranks are integer sums of counts, masses
-// are sums of count * w in 64 bits, and the drawn id is the r-th id of one
-// pattern.
+// are sums of count * w to about 45 bits, and the drawn id is the r-th id of
+// one pattern.
 //
 // One cluster of C CTAs per row. Each CTA counts its share of the row into a
 // histogram of 65,536 16-bit counters in its shared memory. After a cluster
@@ -100,6 +100,14 @@ __device__ __forceinline__ uint32_t not_below2(uint32_t a, uint32_t b) {
 template <typename T>
 __device__ __forceinline__ float bin_value(uint32_t bin) {
     return bits_f32<T>(static_cast<uint16_t>(pattern_of(bin)));
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t bin_of(float x) {  // of a logit (an f16 or bf16 value; +0 for -0)
+    const T h = from_f32<T>(x + 0.0f);
+    uint16_t u;
+    memcpy(&u, &h, 2);
+    return pattern_of(u);
 }
 
 // ---------------------------------------------------------------------------
@@ -208,8 +216,7 @@ struct Shared {
     uint32_t heavies, counted, n_bits, any_heavy;
     Weights weights;
     uint32_t n_min;           // ids that min-p leaves
-    uint32_t first_bin;       // the largest logit's
-    uint32_t bad;
+    uint32_t top, row_top;    // the share's and the row's largest logit, by f2key; all ones for a NaN
     uint32_t bin, owner, place;  // the drawn bin, the CTA of the drawn id, its place among that CTA's ids of the bin
     float prob;
 };
@@ -302,7 +309,6 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
     const uint32_t C = a.ctas, rank = C > 1 ? cl.block_rank() : 0u;
     const uint32_t row = blockIdx.x / C;
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr uint32_t kPosInf = 0x7FFFu - Kind<T>::kInf;     // this bin and lower: +Inf, NaN
     constexpr uint32_t kNegInf = 0x8000u | Kind<T>::kInf;     // masked; higher bins: NaN
     auto cluster_sync = [&] {
         if (C > 1) cl.sync();
@@ -317,7 +323,7 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
     };
     clear();
     if (tid < kTable) s.table[tid] = kExpTable.v[tid];
-    if (tid == 0) s.n_min = s.heavies = s.counted = s.n_bits = s.any_heavy = 0;
+    if (tid == 0) s.n_min = s.heavies = s.counted = s.n_bits = s.any_heavy = s.top = s.row_top = 0;
     pdl_wait();
 
     Share<T> share;
@@ -334,6 +340,9 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
     pdl_trigger();
     __syncthreads();  // the histogram is clear
 
+    // The thread's largest logits, NaN once it has seen one: all that a row's
+    // validity needs. (Masked ids and those outside the row are -Inf.)
+    typename Kind<T>::Pair top = as_pair<T>(kNegInf * 0x00010001u);
     // Counting. The counter of pattern u is half u & 1 of word u >> 1.
     auto add_low = [&](uint32_t w) {
         atomicAdd(reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(s.hist) + (w << 1 & 0x1FFFCu)), 1u + (w & 1u) * 0xFFFFu);
@@ -348,6 +357,7 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
             const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+                top = __hmax2_nan(top, as_pair<T>(w[i]));
                 const uint32_t masked = equal2<T>(w[i], kNegInf * 0x00010001u);
                 if (!masked) {
                     add_low(w[i]);
@@ -374,6 +384,7 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
             const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+                top = __hmax2_nan(top, as_pair<T>(w[i]));
                 const uint32_t in = not_below2<T>(w[i], bound);
                 if (in & 1u) {
                     add_low(w[i]);
@@ -430,6 +441,13 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
         }
         n = __reduce_add_sync(kFull, n + (bound ? count_from(at, share.hi, bound) : count_all(at, share.hi)));
         if (lane == 0) atomicAdd(&s.counted, n);
+    }
+    {
+        // as a whole number in the order of the values, NaN above all
+        const float x0 = to_f32(top.x), x1 = to_f32(top.y);
+        const uint32_t key = isnan(x0) || isnan(x1) ? 0xFFFFFFFFu : f2key(fmaxf(x0, x1));
+        const uint32_t most = __reduce_max_sync(kFull, key);
+        if (lane == 0) atomicMax(&s.top, most);
     }
     __syncthreads();
     auto merge_zeros = [&] {  // -0 ties with +0: its pattern, 0x8000, is counted with 0
@@ -500,6 +518,7 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
         s.row_bits[tid] = word;
     } else if (tid < kWords + C) {
         if (*peer(&s.heavies, tid - kWords)) s.any_heavy = 1;
+        atomicMax(&s.row_top, *peer(&s.top, tid - kWords));
     }
     __syncthreads();
     uint32_t nu = 0;
@@ -534,35 +553,22 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
             for (uint32_t r = 0; r < C; ++r) n += heavy_of(bin, r);
         return n;
     };
-    if (warp == 0) {
-        // The policy, and the row's validity: a NaN or +Inf logit, nothing
-        // unmasked, a uniform or a parameter out of its range.
-        bool bad = !(Tf >= 0.0f) || isinf(Tf) || !(pf > 0.0f && pf <= 1.0f) || !(mf >= 0.0f && mf < 1.0f) ||
-                   !(uf >= 0.0f && uf < 1.0f) || nu == 0;
-        if (!bad) {
-            const uint32_t unit = lane < 8 ? s.units[0] : s.units[nu - 1];
-            const uint32_t used = __ballot_sync(kFull, lane < 16 && count(unit * kUnitBins + lane % 8) > 0);
-            const uint32_t first = s.units[0] * kUnitBins + __ffs(used & 0xFFu) - 1;
-            const uint32_t last = s.units[nu - 1] * kUnitBins + (31 - __clz(used >> 8));
-            bad = first <= kPosInf || last > kNegInf;
-            if (lane == 0) {
-                s.first_bin = first;
-                s.weights.top = bin_value<T>(first) * s.weights.pre;
-            }
-        }
-        if (lane == 0) s.bad = bad;
-    }
-    __syncthreads();
-    if (s.bad) {  // the same in every CTA of the cluster
+    // The policy, and the row's validity: a NaN or +Inf logit, nothing unmasked, a
+    // uniform or a parameter out of its range; the same in every CTA of the cluster.
+    const bool bad = !(Tf >= 0.0f) || isinf(Tf) || !(pf > 0.0f && pf <= 1.0f) || !(mf >= 0.0f && mf < 1.0f) ||
+                     !(uf >= 0.0f && uf < 1.0f) || nu == 0 || s.row_top > kKeyMaxFinite;
+    if (bad) {
         if (rank == 0 && tid == 0) {
             a.out_ids[row] = SEL_INVALID_ID;
             a.out_probs[row] = __uint_as_float(0x7FC00000u);
         }
-        cluster_sync();  // no CTA leaves while another reads its histogram
+        cluster_sync();  // no CTA leaves while another reads its tables
         return;
     }
+    const float row_top = key2f(s.row_top);
     const bool greedy = Tf == 0.0f;
-    const Weights weights = s.weights;
+    Weights weights = s.weights;
+    weights.top = row_top * weights.pre;
 
     // Entries of up to four units, shared between the CTAs; a lane a bin.
     const uint32_t per = (nu + kEntries - 1) / kEntries, entries = (nu + per - 1) / per;
@@ -708,7 +714,7 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
                 return __shfl_sync(kFull, b.c_before, l) + place;
             };
 
-            uint32_t bin = s.first_bin, place = 0;
+            uint32_t bin = bin_of<T>(row_top), place = 0;  // greedy: the largest logit's first id
             float prob = 1.0f;
             if (!greedy) {
                 const uint32_t n_k = kk == 0 ? n_all : min(kk, n_all);

@@ -1,5 +1,5 @@
 """sel_sample16 on the GPU against sorting each row in 64 bits. Ids must be
-equal: masses are 64-bit sums, so a draw could differ only for a uniform
+equal: masses are kept to about 45 bits, so a draw could differ only for a uniform
 within about 1e-13 of a border, and equal weights add up exactly."""
 import numpy as np
 import pytest
@@ -40,7 +40,7 @@ def check(x, pol, u, pad=0, off=0):
                         np.ones(rows) if p is None else p, np.zeros(rows) if m is None else m, u)
     gi, gp = call(x, pol, u, pad, off)
     assert np.array_equal(gi, wi), np.flatnonzero(gi != wi)[:8]
-    # one rounding to fp32, and 64-bit sums on both sides
+    # one rounding to fp32 (2^-24), and masses to about 2^-45
     assert np.array_equal(np.isnan(gp), np.isnan(wp))
     ok = ~np.isnan(wp)
     assert (np.abs(gp[ok] - wp[ok]) <= 2.0 ** -24 * 1.001 * wp[ok] + 2.0 ** -150).all()
