@@ -497,7 +497,7 @@ def _w4(q, scales, zeros, group: int, dtype) -> tuple[int, int]:
     V, H = q.shape[0], 2 * q.shape[1]
     if group <= 0 or H % group:
         raise ValueError("H must be a multiple of group")
-    if scales.dtype != dtype or tuple(scales.shape) != (V, H // group) or not scales.is_contiguous():
+    if scales.dtype != dtype or scales.shape != (V, H // group) or not scales.is_contiguous():
         raise ValueError(f"scales must be contiguous [V, H / group] of {dtype}")
     if zeros is not None and (zeros.dtype != torch.uint8 or zeros.shape != scales.shape or not zeros.is_contiguous()):
         raise ValueError("zeros must be contiguous uint8 [V, H / group]")
@@ -511,13 +511,14 @@ def sel_head_w4(hidden, q, scales, zeros, group: int, logits, stream=None) -> No
     dev = _device(hidden, q, scales, zeros, logits)
     V, H = _w4(q, scales, zeros, group, hidden.dtype)
     rows, cols, ld = _rows_2d(logits, "logits")
-    if tuple(hidden.shape) != (rows, H) or not hidden.is_contiguous():
+    if hidden.shape != (rows, H) or not hidden.is_contiguous():
         raise ValueError("hidden must be contiguous [rows, H]")
     if cols != V or logits.dtype not in _DTYPES or hidden.dtype not in (torch.float16, torch.bfloat16):
         raise ValueError("logits must be [rows, V] of f32, f16 or bf16, hidden of f16 or bf16")
-    _check(load().sel_head_w4(hidden.data_ptr(), rows, q.data_ptr(), scales.data_ptr(),
-                              None if zeros is None else zeros.data_ptr(), group, _DTYPES[hidden.dtype], V, H,
-                              logits.data_ptr(), _DTYPES[logits.dtype], ld, _on_stream(stream, dev)), "sel_head_w4")
+    _check((_lib or load()).sel_head_w4(hidden.data_ptr(), rows, q.data_ptr(), scales.data_ptr(),
+                                        None if zeros is None else zeros.data_ptr(), group, _DTYPES[hidden.dtype],
+                                        V, H, logits.data_ptr(), _DTYPES[logits.dtype], ld,
+                                        _on_stream(stream, dev)), "sel_head_w4")
 
 
 def sel_sample16(logits, temperature, top_k, top_p, min_p, uniforms, out_ids, out_probs, stream=None) -> None:
@@ -529,11 +530,13 @@ def sel_sample16(logits, temperature, top_k, top_p, min_p, uniforms, out_ids, ou
     if logits.dtype not in _DTYPES:
         raise ValueError("logits must be f16 or bf16")
     f32 = (torch.float32,)
-    _check(load().sel_sample16(logits.data_ptr(), _DTYPES[logits.dtype], rows, V, ld,
-                               _vector(temperature, rows, f32, "temperature"), _vector(top_k, rows, _IDS, "top_k"),
-                               _vector(top_p, rows, f32, "top_p"), _vector(min_p, rows, f32, "min_p"),
-                               _vector(uniforms, rows, f32, "uniforms"), _vector(out_ids, rows, _IDS, "out_ids"),
-                               _vector(out_probs, rows, f32, "out_probs"), _on_stream(stream, dev)), "sel_sample16")
+    _check((_lib or load()).sel_sample16(logits.data_ptr(), _DTYPES[logits.dtype], rows, V, ld,
+                                         _vector(temperature, rows, f32, "temperature"),
+                                         _vector(top_k, rows, _IDS, "top_k"), _vector(top_p, rows, f32, "top_p"),
+                                         _vector(min_p, rows, f32, "min_p"), _vector(uniforms, rows, f32, "uniforms"),
+                                         _vector(out_ids, rows, _IDS, "out_ids"),
+                                         _vector(out_probs, rows, f32, "out_probs"),
+                                         _on_stream(stream, dev)), "sel_sample16")
 
 
 def _embed_out(ids, out, H: int, dtype) -> int:
@@ -553,8 +556,8 @@ def sel_embed(ids, table, scale: float, out, stream=None) -> None:
         raise ValueError("table must be a contiguous matrix [V, H] of f32, f16 or bf16")
     V, H = table.shape
     n = _embed_out(ids, out, H, table.dtype)
-    _check(load().sel_embed(ids.data_ptr(), n, table.data_ptr(), _DTYPES[table.dtype], V, H, scale, out.data_ptr(),
-                            _on_stream(stream, dev)), "sel_embed")
+    _check((_lib or load()).sel_embed(ids.data_ptr(), n, table.data_ptr(), _DTYPES[table.dtype], V, H, scale,
+                                      out.data_ptr(), _on_stream(stream, dev)), "sel_embed")
 
 
 def sel_embed_w4(ids, q, scales, zeros, group: int, scale: float, out, stream=None) -> None:
@@ -565,9 +568,9 @@ def sel_embed_w4(ids, q, scales, zeros, group: int, scale: float, out, stream=No
         raise ValueError("scales must be f16 or bf16")
     V, H = _w4(q, scales, zeros, group, scales.dtype)
     n = _embed_out(ids, out, H, scales.dtype)
-    _check(load().sel_embed_w4(ids.data_ptr(), n, q.data_ptr(), scales.data_ptr(),
-                               None if zeros is None else zeros.data_ptr(), group, _DTYPES[scales.dtype], V, H, scale,
-                               out.data_ptr(), _on_stream(stream, dev)), "sel_embed_w4")
+    _check((_lib or load()).sel_embed_w4(ids.data_ptr(), n, q.data_ptr(), scales.data_ptr(),
+                                         None if zeros is None else zeros.data_ptr(), group, _DTYPES[scales.dtype],
+                                         V, H, scale, out.data_ptr(), _on_stream(stream, dev)), "sel_embed_w4")
 
 
 # ---------------------------------------------------------------------------
