@@ -227,6 +227,35 @@ def test_invalid_rows_fail_closed_alone():
     assert gi[0] < V and gi[15] < V
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("rows", [12, 156])
+def test_one_bad_logit_anywhere_in_a_long_row(dtype, rows):
+    """Also where a row with top-k or a greedy one only counts down to a bound."""
+    V = 200_009
+    rng = np.random.default_rng(rows)
+    x = rows_of(rng, "normal", 12, V, dtype).repeat(rows // 12, 1)
+    T, k = np.ones(rows, np.float32), np.full(rows, 40, np.uint32)
+    T[1::4], k[2::4] = 0.0, 0
+    bad = np.zeros(rows, bool)
+    for i, at in enumerate([0, 1, 4096, 40_000, 131_071, 180_002, V - 2, V - 1]):
+        r = i + 2 if rows == 12 else 15 * i + i % 4
+        x[r, at] = [np.nan, np.inf, -np.nan][i % 3]
+        bad[r] = True
+    gi, gp = check(x, (T, k, None, None), rng.random(rows, dtype=np.float32), 3, 1)
+    assert np.array_equal(gi == 0xFFFFFFFF, bad) and np.array_equal(np.isnan(gp), bad)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("largest", [-0.0, 1e-40, 5.9e-8, -5.9e-8, -1e-40, -30000.0])
+def test_largest_logits_of_either_sign_and_subnormal(dtype, largest):
+    """The row's maximum, to which every weight is taken."""
+    rng = np.random.default_rng(21)
+    x = torch.from_numpy(largest - np.abs(rng.normal(0, 1, size=(6, 3001))) * max(abs(largest), 1e-3)).to(DT[dtype])
+    x[:, 1000] = largest
+    T = np.array([0.0, 1.0, 0.5, 1.0, 2.0, 1e-3], np.float32)
+    check(x, (T, None, None, None), rng.random(6, dtype=np.float32))
+
+
 def test_absent_policies_are_off():
     rng = np.random.default_rng(6)
     x = rows_of(rng, "normal", 5, 2000, "f16")
