@@ -52,7 +52,7 @@ constexpr int kWarps = kNT / 32;
 // 16-byte vectors a thread loads ahead. Two: every further one lengthens the code
 // of a pass, which a small batch fetches for its first and only use (16.9 us a
 // row of 151,936 with two, 18.9 with four), and large ones gain nothing.
-constexpr int kAhead = 2;
+constexpr uint32_t kAhead = 2, kAheadFrom = 4;
 constexpr uint32_t kMaxCluster = 8;
 constexpr uint32_t kBatchVecs = 4095;       // vectors whose ids overflow no counter below half
 constexpr uint32_t kHalf = 32768;
@@ -89,13 +89,14 @@ __device__ __forceinline__ typename Kind<T>::Pair as_pair(uint32_t w) {
     memcpy(&p, &w, 4);
     return p;
 }
-// All ones in each half that equals (-0 equals +0); that is not below, NaNs included.
+// All ones in each half that equals (-0 equals +0); that differs, that is not
+// below, NaNs included.
 template <typename T>
 __device__ __forceinline__ uint32_t equal2(uint32_t a, uint32_t b) { return __heq2_mask(as_pair<T>(a), as_pair<T>(b)); }
 template <typename T>
-__device__ __forceinline__ uint32_t not_below2(uint32_t a, uint32_t b) {
-    return __hgeu2_mask(as_pair<T>(a), as_pair<T>(b));
-}
+__device__ __forceinline__ uint32_t differ2(uint32_t a, uint32_t b) { return __hneu2_mask(as_pair<T>(a), as_pair<T>(b)); }
+template <typename T>
+__device__ __forceinline__ uint32_t not_below2(typename Kind<T>::Pair a, typename Kind<T>::Pair b) { return __hgeu2_mask(a, b); }
 
 template <typename T>
 __device__ __forceinline__ float bin_value(uint32_t bin) {
@@ -283,6 +284,37 @@ struct Share {
             }
         }
     }
+    // f(logits) for the vectors of [base, end) in any order, thread `me` of kStride
+    // taking every kStride-th, kDepth ahead. f gets vectors of masked ids too; a
+    // share's end vectors, which reach over the row's, come in a step of their own.
+    template <uint32_t kStride, uint32_t kDepth, typename F>
+    __device__ __forceinline__ void sweep(uint32_t base, uint32_t end, uint32_t me, F f) const {
+        constexpr uint32_t kNegInf = 0x8000u | Kind<T>::kInf, kFill = kNegInf | (kNegInf << 16);
+        const uint32_t full_lo = skew ? 1u : 0u, full_hi = (V + skew) / 8u;
+        const uint32_t lo = max(base, full_lo), hi = max(lo, min(end, full_hi));
+        const bool edges = base < full_lo || end > full_hi;
+        int left = static_cast<int>(hi - lo) - static_cast<int>(me) + (edges ? static_cast<int>(kStride) : 0);
+        const char* p = reinterpret_cast<const char*>(x - skew) + (static_cast<int64_t>(lo) + me) * 16 -
+                        (edges ? static_cast<int64_t>(kStride) * 16 : 0);
+        uint4 next[kDepth];
+#pragma unroll
+        for (uint32_t j = 0; j < kDepth; ++j)
+            next[j] = load_or(p + j * kStride * 16u, left > static_cast<int>(j * kStride) && !(edges && j == 0), kFill);
+        if (edges && me < 2) {
+            const uint32_t v = me ? full_hi : 0u;
+            if (v >= base && v < end && (me ? full_hi >= full_lo : skew != 0)) next[0] = edge(v);
+        }
+        while (left > 0) {
+#pragma unroll
+            for (uint32_t j = 0; j < kDepth; ++j) {
+                const uint4 q = next[j];
+                next[j] = load_or(p + (kDepth + j) * kStride * 16u, left > static_cast<int>((kDepth + j) * kStride), kFill);
+                f(q);
+            }
+            p += kDepth * kStride * 16u;
+            left -= static_cast<int>(kDepth * kStride);
+        }
+    }
 };
 
 // Ids of a unit's eight counters.
@@ -309,6 +341,7 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
     const uint32_t C = a.ctas, rank = C > 1 ? cl.block_rank() : 0u;
     const uint32_t row = blockIdx.x / C;
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr uint32_t kPosInf = 0x7FFFu - Kind<T>::kInf;     // lower bins: NaN
     constexpr uint32_t kNegInf = 0x8000u | Kind<T>::kInf;     // masked; higher bins: NaN
     auto cluster_sync = [&] {
         if (C > 1) cl.sync();
@@ -343,103 +376,100 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
     // The thread's largest logits, NaN once it has seen one: all that a row's
     // validity needs. (Masked ids and those outside the row are -Inf.)
     typename Kind<T>::Pair top = as_pair<T>(kNegInf * 0x00010001u);
-    // Counting. The counter of pattern u is half u & 1 of word u >> 1.
-    auto add_low = [&](uint32_t w) {
-        atomicAdd(reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(s.hist) + (w << 1 & 0x1FFFCu)), 1u + (w & 1u) * 0xFFFFu);
+    // Counting. The counter of pattern u is half u & 1 of word u >> 1. Ids are added
+    // under a predicate: branches took twice the instructions of all the rest.
+    const uint32_t hist = smem_u32(s.hist);
+    auto add = [&](uint32_t w, uint32_t in) {  // the halves of w whose half of `in` is all ones
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t.reg .b32 t;\n\t"
+            "and.b32 t, %4, 1;\n\tsetp.ne.u32 p, t, 0;\n\tsetp.lt.s32 q, %4, 0;\n\t"
+            "@p red.shared.add.u32 [%0], %1;\n\t"
+            "@q red.shared.add.u32 [%2], %3;\n\t}" ::"r"(hist + ((w & 0xFFFEu) << 1)),
+            "r"(1u + (w & 1u) * 0xFFFFu), "r"(hist + ((w >> 17) << 2)), "r"(max(w & 0x10000u, 1u)), "r"(in)
+            : "memory");
     };
-    auto add_high = [&](uint32_t w) {
-        atomicAdd(reinterpret_cast<uint32_t*>(reinterpret_cast<char*>(s.hist) + (w >> 15 & 0x1FFFCu)), max(w & 0x10000u, 1u));
+    // Halves that are all ones in the masks that `sum` adds up (fewer than 65,536 each).
+    auto halves = [](uint32_t sum) {
+        const uint32_t low = -sum & 0xFFFFu;  // sum = 65535 low - 65536 high
+        return low + ((65535u * low - sum) >> 16);
+    };
+    auto largest = [&](const uint4& q) {
+        return __hmax2_nan(__hmax2_nan(as_pair<T>(q.x), as_pair<T>(q.y)), __hmax2_nan(as_pair<T>(q.z), as_pair<T>(q.w)));
     };
     // Counts the unmasked ids; returns how many the thread counted.
     auto count_all = [&](uint32_t base, uint32_t end) {
-        uint32_t n = 0;
-        share.template each<kNT, false>(base, end, tid, [&](uint32_t, const uint4& q) {
+        uint32_t sum = 0;
+        share.template sweep<kNT, kAhead>(base, end, tid, [&](const uint4& q) {
+            top = __hmax2_nan(top, largest(q));
             const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                top = __hmax2_nan(top, as_pair<T>(w[i]));
-                const uint32_t masked = equal2<T>(w[i], kNegInf * 0x00010001u);
-                if (!masked) {
-                    add_low(w[i]);
-                    add_high(w[i]);
-                    n += 2;
-                } else {
-                    if (!(masked & 1u)) {
-                        add_low(w[i]);
-                        ++n;
-                    }
-                    if (!(masked >> 31)) {
-                        add_high(w[i]);
-                        ++n;
-                    }
-                }
+                const uint32_t in = differ2<T>(w[i], kNegInf * 0x00010001u);
+                sum += in;
+                add(w[i], in);
             }
         });
-        return n;
+        return halves(sum);
     };
     // The same of ids that are not below `bound` (a pair of the same pattern).
     auto count_from = [&](uint32_t base, uint32_t end, uint32_t bound) {
-        uint32_t n = 0;
-        share.template each<kNT, false>(base, end, tid, [&](uint32_t, const uint4& q) {
+        uint32_t sum = 0;
+        const auto low = as_pair<T>(bound);
+        share.template sweep<kNT, kAheadFrom>(base, end, tid, [&](const uint4& q) {
+            const auto most = largest(q);
+            top = __hmax2_nan(top, most);
+            if (!not_below2<T>(most, low)) return;
             const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                top = __hmax2_nan(top, as_pair<T>(w[i]));
-                const uint32_t in = not_below2<T>(w[i], bound);
-                if (in & 1u) {
-                    add_low(w[i]);
-                    ++n;
-                }
-                if (in >> 31) {
-                    add_high(w[i]);
-                    ++n;
-                }
+                const uint32_t in = not_below2<T>(as_pair<T>(w[i]), low);
+                sum += in;
+                add(w[i], in);
             }
         });
-        return n;
+        return halves(sum);
     };
     // fewer than 65,536 ids: no counter can overflow
     const bool small = share.hi - share.lo <= kBatchVecs * 2;
-    const uint32_t want = Tf == 0.0f ? 1u : kk;  // ids of the row that can matter, from the largest; 0: all
-    uint32_t bound = 0;  // 0: none yet, else a pair of the least pattern that counts
+    // ids of the row that can matter, from the largest
+    const uint32_t want = Tf == 0.0f ? 1u : kk && kk < kBatchVecs * 8 ? kk : a.V;
+    uint32_t bound = (kNegInf - 1) * 0x00010001u;  // a pair of the least pattern that counts: the least finite one
     if (tid == 32) s.weights.temperature(Tf > 0.0f ? Tf : 1.0f);
-    if (small) {
-        count_all(share.lo, share.hi);
-    } else {
-        uint32_t n = 0, at = share.lo;
-        if (want && want < kBatchVecs * 8) {
-            // The top `want` ids of the first batch bound those of the row from
-            // below: the rest of the share only counts what is not under them.
-            // (A 64th of the batch, where it can be: the bound then lets about that
-            // much through.)
-            at += min(kBatchVecs, max(static_cast<uint32_t>(kNT), want * 8u));
-            n = count_all(share.lo, at);
-            __syncthreads();
+    // The top `want` ids of a first batch bound those of the row from below: the
+    // rest of the share only counts what is not under them. (A 64th of the batch,
+    // where it can be: the bound then lets about that much through.)
+    uint32_t at = share.hi;
+    if (!small && want < kBatchVecs * 8) at = share.lo + min(kBatchVecs, max(static_cast<uint32_t>(kNT), want * 8u));
+    uint32_t n = count_all(share.lo, at);
+    if (at < share.hi) {
+        __syncthreads();
 #pragma unroll
-            for (int i = 0; i < static_cast<int>(kUnits / kNT); ++i) {
-                const uint32_t word = warp * (kUnits / kNT) + i;
-                const uint32_t sum = __reduce_add_sync(kFull, unit_sum(h4[stored_unit(word * 32 + lane)]));
-                if (lane == 0) s.off[word] = sum;
-            }
-            __syncthreads();
-            // every warp finds the same: the 256 bins where the count gets there, then their unit
-            uint32_t sum = 0;
-#pragma unroll
-            for (uint32_t i = 0; i < kWords / 32; ++i) sum += s.off[lane * (kWords / 32) + i];
-            const uint32_t in = warp_scan(sum), hit = __ballot_sync(kFull, in >= want);
-            if (hit) {
-                const int l = __ffs(hit) - 1;
-                uint32_t before = __shfl_sync(kFull, in - sum, l), word = l * (kWords / 32);
-                while (before + s.off[word] < want) before += s.off[word++];
-                const uint32_t units = warp_scan(unit_sum(h4[stored_unit(word * 32 + lane)]));
-                const uint32_t unit = word * 32 + __ffs(__ballot_sync(kFull, before + units >= want)) - 1;
-                // (the unit's least value; the least finite one where that is -Inf or a NaN)
-                bound = pattern_of(min(unit * kUnitBins + kUnitBins - 1, kNegInf - 1)) * 0x00010001u;
-                if (!bound) bound = 0x80008000u;  // 0 as -0, which compares the same
-            }
-            __syncthreads();
+        for (int i = 0; i < static_cast<int>(kUnits / kNT); ++i) {
+            const uint32_t word = warp * (kUnits / kNT) + i;
+            const uint32_t sum = __reduce_add_sync(kFull, unit_sum(h4[stored_unit(word * 32 + lane)]));
+            if (lane == 0) s.off[word] = sum;
         }
-        n = __reduce_add_sync(kFull, n + (bound ? count_from(at, share.hi, bound) : count_all(at, share.hi)));
+        __syncthreads();
+        // every warp finds the same: the 256 bins where the count gets there, then their unit
+        uint32_t sum = 0;
+#pragma unroll
+        for (uint32_t i = 0; i < kWords / 32; ++i) sum += s.off[lane * (kWords / 32) + i];
+        const uint32_t in = warp_scan(sum), hit = __ballot_sync(kFull, in >= want);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            uint32_t before = __shfl_sync(kFull, in - sum, l), word = l * (kWords / 32);
+            while (before + s.off[word] < want) before += s.off[word++];
+            const uint32_t units = warp_scan(unit_sum(h4[stored_unit(word * 32 + lane)]));
+            const uint32_t unit = word * 32 + __ffs(__ballot_sync(kFull, before + units >= want)) - 1;
+            // (the unit's least value, from +Inf to the least finite one: no NaN, with
+            // which every comparison would let -Inf through)
+            bound = pattern_of(max(kPosInf, min(unit * kUnitBins + kUnitBins - 1, kNegInf - 1))) * 0x00010001u;
+        }
+        __syncthreads();
+        n += count_from(at, share.hi, bound);
+    }
+    if (!small) {
+        n = __reduce_add_sync(kFull, n);
         if (lane == 0) atomicAdd(&s.counted, n);
     }
     {
@@ -487,8 +517,7 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
             clear();
             __syncthreads();
             for (uint32_t at = share.lo; at < share.hi; at += kBatchVecs) {
-                if (bound) count_from(at, min(share.hi, at + kBatchVecs), bound);
-                else count_all(at, min(share.hi, at + kBatchVecs));
+                count_from(at, min(share.hi, at + kBatchVecs), bound);
                 __syncthreads();
                 if (tid == 0) merge_zeros();
                 __syncthreads();
@@ -765,7 +794,7 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
         static_assert(SEL_SAMPLE16_MAX_V / (8 * 32 * kWarps) < 64);
         auto sum = as_pair<T>(0);
         const auto drawn = as_pair<T>(pattern);
-        share.template each<32, false>(run_lo, run_hi, lane, [&](uint32_t, const uint4& q) {
+        share.template sweep<32, kAheadFrom>(run_lo, run_hi, lane, [&](const uint4& q) {
             sum = __hadd2(sum, __hadd2(__hadd2(__heq2(as_pair<T>(q.x), drawn), __heq2(as_pair<T>(q.y), drawn)),
                                        __hadd2(__heq2(as_pair<T>(q.z), drawn), __heq2(as_pair<T>(q.w), drawn))));
         });
