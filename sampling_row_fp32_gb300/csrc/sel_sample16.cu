@@ -20,7 +20,9 @@
 //
 // Where top-k is on, the first batch of a share gives a bound that the top k
 // of the row are not under, and the rest of the share is only counted down to
-// it: what bounds the counting is the atomics, at about five a clock and SM.
+// it: what bounds counting every id is the atomics, at about five a clock and SM.
+// Ids past the first batch that are not under the bound are listed as well, where
+// they are few, and the drawn id is looked for there.
 //
 // A counter that overflows (a value that more than 65,535 ids of a share have)
 // makes the counters' sum differ from the ids counted; the share is then
@@ -199,6 +201,9 @@ struct SampleArgs {
 
 constexpr uint32_t kEntries = 2048;             // at most; of up to four units, a lane a bin
 constexpr uint32_t kCoarse = kEntries / kWarps;  // entries of a warp's prefix sums
+// Entries of a share's list. Twice as many cost the L1 cache 12 KB more, and rows
+// that list nothing 7 % (152 of 202,048 without top-k: 41.5 -> 44.7 us).
+constexpr uint32_t kList = 2048;
 static_assert(kUnits <= kEntries * 4 && kCoarse == 64);
 
 struct Shared {
@@ -215,8 +220,11 @@ struct Shared {
     uint32_t seg[kWarps];
     uint32_t heavy[kMaxHeavy];  // bins with 32,768 ids more than their counter says, once for each
     uint32_t heavies, counted, n_bits, any_heavy;
+    uint32_t list_at[kList];  // ids past the first batch that the bound lets through: 8 times the vector and the place,
+    uint16_t list_pattern[kList];  // and logits (0 for -0)
     Weights weights;
     uint32_t n_min;           // ids that min-p leaves
+    uint32_t listed, matches;  // (listed: kList and more when some found no place)
     uint32_t top, row_top;    // the share's and the row's largest logit, by f2key; all ones for a NaN
     uint32_t bin, owner, place;  // the drawn bin, the CTA of the drawn id, its place among that CTA's ids of the bin
     float prob;
@@ -284,9 +292,9 @@ struct Share {
             }
         }
     }
-    // f(logits) for the vectors of [base, end) in any order, thread `me` of kStride
-    // taking every kStride-th, kDepth ahead. f gets vectors of masked ids too; a
-    // share's end vectors, which reach over the row's, come in a step of their own.
+    // f(v, logits) for the vectors of [base, end) in any order, thread `me` of
+    // kStride taking every kStride-th, kDepth ahead. f gets vectors of masked ids
+    // too; a row's end vectors, which reach over it, come in a step of their own.
     template <uint32_t kStride, uint32_t kDepth, typename F>
     __device__ __forceinline__ void sweep(uint32_t base, uint32_t end, uint32_t me, F f) const {
         constexpr uint32_t kNegInf = 0x8000u | Kind<T>::kInf, kFill = kNegInf | (kNegInf << 16);
@@ -309,7 +317,8 @@ struct Share {
             for (uint32_t j = 0; j < kDepth; ++j) {
                 const uint4 q = next[j];
                 next[j] = load_or(p + (kDepth + j) * kStride * 16u, left > static_cast<int>((kDepth + j) * kStride), kFill);
-                f(q);
+                const int v = static_cast<int>(hi) - left + static_cast<int>(j * kStride);
+                f(v >= static_cast<int>(lo) ? static_cast<uint32_t>(v) : me ? full_hi : 0u, q);
             }
             p += kDepth * kStride * 16u;
             left -= static_cast<int>(kDepth * kStride);
@@ -356,7 +365,7 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
     };
     clear();
     if (tid < kTable) s.table[tid] = kExpTable.v[tid];
-    if (tid == 0) s.n_min = s.heavies = s.counted = s.n_bits = s.any_heavy = s.top = s.row_top = 0;
+    if (tid == 0) s.n_min = s.heavies = s.counted = s.n_bits = s.any_heavy = s.top = s.row_top = s.listed = s.matches = 0;
     pdl_wait();
 
     Share<T> share;
@@ -399,7 +408,7 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
     // Counts the unmasked ids; returns how many the thread counted.
     auto count_all = [&](uint32_t base, uint32_t end) {
         uint32_t sum = 0;
-        share.template sweep<kNT, kAhead>(base, end, tid, [&](const uint4& q) {
+        share.template sweep<kNT, kAhead>(base, end, tid, [&](uint32_t, const uint4& q) {
             top = __hmax2_nan(top, largest(q));
             const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -412,19 +421,34 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
         return halves(sum);
     };
     // The same of ids that are not below `bound` (a pair of the same pattern).
-    auto count_from = [&](uint32_t base, uint32_t end, uint32_t bound) {
+    // note: they go into the list.
+    auto count_from = [&](uint32_t base, uint32_t end, uint32_t bound, bool note) {
         uint32_t sum = 0;
         const auto low = as_pair<T>(bound);
-        share.template sweep<kNT, kAheadFrom>(base, end, tid, [&](const uint4& q) {
+        share.template sweep<kNT, kAheadFrom>(base, end, tid, [&](uint32_t v, const uint4& q) {
             const auto most = largest(q);
             top = __hmax2_nan(top, most);
             if (!not_below2<T>(most, low)) return;
+            uint32_t which = 0;
             const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t in = not_below2<T>(as_pair<T>(w[i]), low);
                 sum += in;
                 add(w[i], in);
+            }
+            if (!note) return;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) which |= (not_below2<T>(as_pair<T>(w[i]), low) & 0x10001u) << i;
+            while (which && *const_cast<volatile uint32_t*>(&s.listed) < kList) {  // bit i + 16 h: half h of word i
+                const uint32_t b = __ffs(which) - 1, k = b & 3;
+                which &= which - 1;
+                const uint32_t u = (k & 2 ? (k & 1 ? q.w : q.z) : (k & 1 ? q.y : q.x)) >> (b & 16) & 0xFFFFu;
+                const uint32_t i = atomicAdd(&s.listed, 1u);
+                if (i < kList) {
+                    s.list_at[i] = v * 8 + 2 * k + (b >> 4);
+                    s.list_pattern[i] = static_cast<uint16_t>(u == 0x8000u ? 0u : u);
+                }
             }
         });
         return halves(sum);
@@ -434,12 +458,17 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
     // ids of the row that can matter, from the largest
     const uint32_t want = Tf == 0.0f ? 1u : kk && kk < kBatchVecs * 8 ? kk : a.V;
     uint32_t bound = (kNegInf - 1) * 0x00010001u;  // a pair of the least pattern that counts: the least finite one
+    uint32_t last_unit = kUnits - 1;  // that holds one: later units' masses are not needed
     if (tid == 32) s.weights.temperature(Tf > 0.0f ? Tf : 1.0f);
     // The top `want` ids of a first batch bound those of the row from below: the
     // rest of the share only counts what is not under them. (A 64th of the batch,
     // where it can be: the bound then lets about that much through.)
-    uint32_t at = share.hi;
-    if (!small && want < kBatchVecs * 8) at = share.lo + min(kBatchVecs, max(static_cast<uint32_t>(kNT), want * 8u));
+    uint32_t at = share.hi;  // the first batch's end
+    if (!small && want < kBatchVecs * 8) at = share.lo + min(kBatchVecs, max(2 * static_cast<uint32_t>(kNT), want * 8u));
+    // Where the bound lets few through, they are listed, so that the drawn id need
+    // not be looked for in the rest of the share (152 rows of 202,048, top 40: 36.7
+    // -> 32.5 us, greedy 29 -> 19).
+    const bool listing = at < share.hi && want * static_cast<uint64_t>(share.hi - at) <= kList / 2 * (at - share.lo);
     uint32_t n = count_all(share.lo, at);
     if (at < share.hi) {
         __syncthreads();
@@ -461,12 +490,13 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
             while (before + s.off[word] < want) before += s.off[word++];
             const uint32_t units = warp_scan(unit_sum(h4[stored_unit(word * 32 + lane)]));
             const uint32_t unit = word * 32 + __ffs(__ballot_sync(kFull, before + units >= want)) - 1;
+            last_unit = unit;
             // (the unit's least value, from +Inf to the least finite one: no NaN, with
             // which every comparison would let -Inf through)
             bound = pattern_of(max(kPosInf, min(unit * kUnitBins + kUnitBins - 1, kNegInf - 1))) * 0x00010001u;
         }
         __syncthreads();
-        n += count_from(at, share.hi, bound);
+        n += count_from(at, share.hi, bound, listing);
     }
     if (!small) {
         n = __reduce_add_sync(kFull, n);
@@ -497,7 +527,7 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
         for (int i = 0; i < static_cast<int>(kUnits / kNT); ++i) {
             const uint32_t word = i * kWarps + warp;
             const uint4 v = h4[stored_unit(word * 32 + lane)];
-            const uint32_t b = __ballot_sync(kFull, (v.x | v.y | v.z | v.w) != 0);
+            const uint32_t b = __ballot_sync(kFull, (v.x | v.y | v.z | v.w) != 0 && word * 32 + lane <= last_unit);
             if (lane == 0) s.bits[word] = b;
             sum += unit_sum(v);
         }
@@ -516,8 +546,8 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
             __syncthreads();
             clear();
             __syncthreads();
-            for (uint32_t at = share.lo; at < share.hi; at += kBatchVecs) {
-                count_from(at, min(share.hi, at + kBatchVecs), bound);
+            for (uint32_t b = share.lo; b < share.hi; b += kBatchVecs) {
+                count_from(b, min(share.hi, b + kBatchVecs), bound, false);
                 __syncthreads();
                 if (tid == 0) merge_zeros();
                 __syncthreads();
@@ -784,17 +814,20 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
 
     // The place-th id of the bin in this CTA's share: each warp counts the bin's
     // ids in a run of vectors of its own, then the warp that has the id goes
-    // through its run again.
+    // through its run again. Where the ids past the first batch are listed, in that
+    // batch only, and then in the list.
+    const bool in_list = listing && s.listed < kList;
+    const uint32_t find_hi = in_list ? at : share.hi;
     const uint32_t pattern = pattern_of(s.bin) * 0x00010001u;
-    const uint32_t run = ceil_div32(share.hi - share.lo, kWarps);
-    const uint32_t run_lo = min(share.hi, share.lo + warp * run), run_hi = min(share.hi, run_lo + run);
+    const uint32_t run = ceil_div32(find_hi - share.lo, kWarps);
+    const uint32_t run_lo = min(find_hi, share.lo + warp * run), run_hi = min(find_hi, run_lo + run);
     uint32_t mine;
     {
         // (a lane sees at most 256 pairs, whose number either type holds exactly)
         static_assert(SEL_SAMPLE16_MAX_V / (8 * 32 * kWarps) < 64);
         auto sum = as_pair<T>(0);
         const auto drawn = as_pair<T>(pattern);
-        share.template sweep<32, kAheadFrom>(run_lo, run_hi, lane, [&](const uint4& q) {
+        share.template sweep<32, kAheadFrom>(run_lo, run_hi, lane, [&](uint32_t, const uint4& q) {
             sum = __hadd2(sum, __hadd2(__hadd2(__heq2(as_pair<T>(q.x), drawn), __heq2(as_pair<T>(q.y), drawn)),
                                        __hadd2(__heq2(as_pair<T>(q.z), drawn), __heq2(as_pair<T>(q.w), drawn))));
         });
@@ -804,7 +837,26 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
     __syncthreads();
     const uint32_t in = warp_scan(s.seg[lane]);
     const uint32_t place = s.place;
-    if (static_cast<int>(warp) != __ffs(__ballot_sync(kFull, place < in)) - 1) return;
+    const uint32_t has = __ballot_sync(kFull, place < in);
+    if (!has) {  // (the same in every warp; with a list only)
+        uint32_t* match = s.hist;  // which nothing reads any more
+        const uint32_t rank_in_list = place - __shfl_sync(kFull, in, 31);
+        const uint32_t wanted = pattern & 0xFFFFu;
+        for (uint32_t i = tid; i < s.listed; i += kNT)
+            if (s.list_pattern[i] == wanted) match[atomicAdd(&s.matches, 1u)] = s.list_at[i];
+        __syncthreads();
+        const uint32_t n = s.matches;
+        for (uint32_t i = tid; i < n; i += kNT) {
+            uint32_t before = 0;
+            for (uint32_t j = 0; j < n; ++j) before += match[j] < match[i];
+            if (before == rank_in_list) {
+                a.out_ids[row] = match[i] - share.skew;
+                a.out_probs[row] = s.prob;
+            }
+        }
+        return;
+    }
+    if (static_cast<int>(warp) != __ffs(has) - 1) return;
     uint32_t left = place - (__shfl_sync(kFull, in, warp) - mine);  // ids of the bin before it in the run
     bool found = false;
     share.template each<32, true>(run_lo, run_hi, lane, [&](uint32_t v, const uint4& q) {
@@ -876,6 +928,8 @@ uint32_t ctas_for(uint32_t rows, uint32_t V) {
     }
     return best;
 }
+
+static_assert(sizeof(Shared) <= 227 * 1024);
 
 template <typename T>
 sel_status launch(const SampleArgs& in, uint32_t rows, cudaStream_t stream) {

@@ -182,6 +182,32 @@ def test_top_k_of_long_shares(dtype, late):
     check(torch.from_numpy(x).to(DT[dtype]), tuple(pol), rng.random(rows, dtype=np.float32), 1, 2)
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("kind", ["ties", "rising", "falling", "late ties", "zeros"])
+@pytest.mark.parametrize("rows", [60, 150])
+def test_draws_past_the_first_batch(dtype, kind, rows):
+    """Long shares, whose top ids lie behind the batch that bounds them: few or
+    many ids over the bound, one value many times."""
+    V = 200_009
+    rng = np.random.default_rng(rows)
+    x = rng.normal(0, 2, size=V)
+    if kind == "ties":
+        x = np.round(x)
+    elif kind in ("rising", "falling"):
+        x = np.sort(x)[:: 1 if kind == "rising" else -1]
+    elif kind == "late ties":
+        x[rng.choice(np.arange(60_000, V), 70, replace=False)] = 9.0
+    else:
+        x = -np.abs(x) - 1.0
+        x[rng.choice(V, 300, replace=False)] = 0.0
+        x[rng.choice(V, 300, replace=False)] = -0.0
+    x = torch.from_numpy(np.ascontiguousarray(x)).to(DT[dtype]).expand(rows, V)
+    T = rng.uniform(0.5, 1.5, size=rows).astype(np.float32)
+    T[::10] = 0.0
+    k = rng.choice([1, 2, 20, 40, 84, 90, 91, 92, 93, 400, 5000], size=rows).astype(np.uint32)
+    check(x, (T, k, None, None), rng.random(rows, dtype=np.float32), 5, 3)
+
+
 def test_equal_weights_at_exact_borders():
     """Every weight is 1: uniforms and top-p cuts that fall on a border go by
     rational arithmetic."""
