@@ -30,9 +30,11 @@
 //
 // Masses are pairs of floats: FP64 runs at two results a clock and SM here.
 //
-// One row of 151,936 takes 17 us, a chain of about a dozen dependent steps; 49
-// rows of 248,320 33 us and 256 of 202,048 77 us, most of it counting (the rows'
-// bytes alone would take 3.6 and 15).
+// One row of 151,936 takes 13-18 us, a chain of about a dozen dependent steps; 49
+// rows of 248,320 32 us and 256 of 202,048 74 us (the rows' bytes alone would take
+// 3.6 and 15). Of the 41 us of 152 rows of 202,048 without top-k, counting takes
+// 15, the second look at the share 10 and the chain most of the rest; with a small
+// top-k counting runs at 5.9 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -53,7 +55,8 @@ constexpr int kNT = 1024;
 constexpr int kWarps = kNT / 32;
 // 16-byte vectors a thread loads ahead. Two: every further one lengthens the code
 // of a pass, which a small batch fetches for its first and only use (16.9 us a
-// row of 151,936 with two, 18.9 with four), and large ones gain nothing.
+// row of 151,936 with two, 18.9 with four), and large ones gain nothing. Four where
+// most vectors need a comparison only.
 constexpr uint32_t kAhead = 2, kAheadFrom = 4;
 constexpr uint32_t kMaxCluster = 8;
 constexpr uint32_t kBatchVecs = 4095;       // vectors whose ids overflow no counter below half
@@ -886,7 +889,8 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
 }
 
 // CTAs a row for a batch: the cluster size whose rounds of resident clusters
-// take least. A CTA takes about 9 us beside its share, and 1 us for 14,000 ids.
+// take least. A CTA takes about 15 us beside its share, and 1 us for 8,000 ids (12,000
+// where the rows' top-k is small).
 template <typename T>
 uint32_t ctas_for(uint32_t rows, uint32_t V) {
     struct Table {
@@ -920,7 +924,7 @@ uint32_t ctas_for(uint32_t rows, uint32_t V) {
     for (uint32_t c = 1; c <= kMaxCluster; ++c) {
         if (t.resident[c] == 0) continue;
         const double rounds = ceil_div(rows, static_cast<uint64_t>(t.resident[c]));
-        const double us = rounds * (9.0 + static_cast<double>(V) / c / 14000.0);
+        const double us = rounds * (14.5 + static_cast<double>(V) / c / 10000.0);
         if (us < least) {
             least = us;
             best = c;
