@@ -21,7 +21,7 @@
 // matrix rows in tiles of equal height (up to 352) through a ring of stages of
 // 256 columns that one warp fills (TMA); warp w of the others owns rows 16 w ..
 // 16 w + 15 of a tile over all columns, so nothing is exchanged between warps.
-// One row of 4,096 x 248,320 takes 93 us with groups of 128 and 100 with 64, 5.7
+// One row of 4,096 x 248,320 takes 93 us with groups of 128 and 99 with 64, 5.6
 // and 5.4 TB/s; the matrix's bytes alone would take 77 and 80.
 #include <type_traits>
 

@@ -26,11 +26,11 @@
 // Every wait is bounded; one that runs out makes the CTA's logits NaN.
 //
 // What bounds it: not the copies (the matrix alone would take 77 us at 4,096 x
-// 248,320) but instruction issue, 64 to 70 percent busy: 13 instructions a word
-// of eight weights to unpack, a multiply-add for each D entry of a group, and
-// the hand-overs between the roles. 4,096 x 248,320, groups of 64: 16 rows 119
-// us, 32 rows 138, 49 rows 193 (3.0 TB/s, 520 TFLOP/s); 64 rows of 8,192 x
-// 202,048, groups of 128: 240. Folding the scales into the operand would take
+// 248,320) but instruction issue, 59 percent busy: 13 instructions a word of
+// eight weights to unpack, a multiply-add for each D entry of a group, and the
+// hand-overs between the roles. 4,096 x 248,320, groups of 64: 16 rows 117 us, 32
+// rows 137, 49 rows 192 (3.0 TB/s, 520 TFLOP/s); 64 rows of 8,192 x 202,048, groups
+// of 128: 252, with zero points 262. Folding the scales into the operand would take
 // the epilogue out, and round every weight.
 #pragma once
 
