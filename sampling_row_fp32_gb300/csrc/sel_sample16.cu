@@ -184,7 +184,8 @@ struct Weights {
         const float s = t.x + ph;
         const float lo = (ph - (s - t.x)) + (pl + (t.y + __fmaf_rn(t.x, el, t.y * zh)));
         const float scale = __int_as_float(((k >> 8) + 127) << 23);
-        return FF{s * scale, lo * scale};
+        const float hi = s + lo;  // normalised, as comparisons with it need: lo reaches 2^-16 of s
+        return FF{hi * scale, (lo - (hi - s)) * scale};
     }
 };
 struct SampleArgs {
