@@ -50,3 +50,26 @@ def test_min_p_next_to_a_weight(dtype, T):
         assert (ids == last).all(), (int((ids != last).sum()), n)
         want = w / (1 + w) if last else np.ones(n)
         assert (np.abs(probs - want) <= 2.0 ** -24 * 1.001 * want).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_min_p_at_weights_far_down(dtype):
+    """One id above 16,384 equal ones of a weight w from 2^-33 to 2^-20 that lies
+    2^-42 to 2^-38.5 of itself from a float, which is min-p. The kernel's y =
+    log2 w is good to 2^-43: its second float, up to 2^-20, rounds twice, and
+    1 / T is held to 2^-49 of y; everything after y adds 2^-45."""
+    rng = np.random.default_rng(5)
+    n, ids = 1 << 22, 16_384
+    gap = torch.from_numpy(rng.uniform(6.0, 22.0, size=n)).to(DT[dtype]).double().numpy()
+    T = (gap / rng.uniform(20 * np.log(2), 33 * np.log(2), size=n)).astype(np.float32)
+    w = np.exp(-gap.astype(np.longdouble) / T.astype(np.longdouble))
+    m = w.astype(np.float32)
+    off = ((m.astype(np.longdouble) - w) / w).astype(np.float64)
+    at = np.flatnonzero((np.abs(off) > 2.0 ** -42) & (np.abs(off) < 2.0 ** -38.5))[:300]
+    assert at.size > 150
+    x = torch.zeros(at.size, 1 + ids, dtype=DT[dtype])
+    x[:, 1:] = torch.from_numpy(-gap[at])[:, None]
+    u = np.full(at.size, 1 - 2.0 ** -24, np.float32)  # the last survivors, as 16,384 w > 2^-20
+    got, _ = call(x.cuda(), T[at], None, None, m[at], u)
+    kept = off[at] <= 0
+    assert np.array_equal(got > 0, kept), (int(((got > 0) != kept).sum()), at.size)
