@@ -140,16 +140,18 @@ __device__ __forceinline__ float ex2_approx(float x) {
 // Unevaluated sum hi + lo of two floats (about 44 significant bits),
 // accumulated with Knuth's TwoSum and renormalised with Dekker's Fast2Sum;
 // sums of many small fp32 terms keep ~1e-13 relative error without FP64.
+// Every step is rounded by itself (__fadd_rn and the like): an addition fused
+// with the product it takes would count that product's rounding error twice.
 struct FF {
     float hi, lo;
 };
 __device__ __forceinline__ FF ff_add(FF a, FF b) {
-    const float s = a.hi + b.hi;
-    const float v = s - a.hi;
-    float e = (a.hi - (s - v)) + (b.hi - v);
-    e += a.lo + b.lo;
-    const float h = s + e;
-    return FF{h, e - (h - s)};
+    const float s = __fadd_rn(a.hi, b.hi);
+    const float v = __fsub_rn(s, a.hi);
+    float e = __fadd_rn(__fsub_rn(a.hi, __fsub_rn(s, v)), __fsub_rn(b.hi, v));
+    e = __fadd_rn(e, __fadd_rn(a.lo, b.lo));
+    const float h = __fadd_rn(s, e);
+    return FF{h, __fsub_rn(e, __fsub_rn(h, s))};
 }
 __device__ __forceinline__ FF ff_shfl_xor(FF a, int m) {
     return FF{__shfl_xor_sync(kFull, a.hi, m), __shfl_xor_sync(kFull, a.lo, m)};
@@ -182,10 +184,10 @@ __device__ __forceinline__ FF ff_warp_scan(FF a) {
 }
 // a * b for a float b (Dekker's product through fmaf, then Fast2Sum).
 __device__ __forceinline__ FF ff_mul_f(FF a, float b) {
-    const float p = a.hi * b;
-    const float e = __fmaf_rn(a.hi, b, -p) + a.lo * b;
-    const float h = p + e;
-    return FF{h, e - (h - p)};
+    const float p = __fmul_rn(a.hi, b);
+    const float e = __fmaf_rn(a.lo, b, __fmaf_rn(a.hi, b, -p));
+    const float h = __fadd_rn(p, e);
+    return FF{h, __fsub_rn(e, __fsub_rn(h, p))};
 }
 __device__ __forceinline__ FF ff_from_double(double d) {
     const float hi = static_cast<float>(d);

@@ -168,31 +168,32 @@ struct Weights {
     // 0 below 2^-100, the whole tail of a row weighing less than 2^-80 then
     __device__ __forceinline__ FF operator()(float logit, const float2* table) const {
         constexpr float kLn2 = 0.693147182464599609375f, kLn2Lo = -1.904654299957767e-9f;
-        const float x = logit * pre;
-        const float ds = x - top;  // and the subtraction's rounding error
-        const float v = ds - x;
-        const float dl = ((x - (ds - v)) - (top + v)) * post;
-        const float dh = ds * post;
-        const float yh = dh * r.hi;
+        // (every step rounded by itself, as for float pairs at large)
+        const float x = __fmul_rn(logit, pre);
+        const float ds = __fsub_rn(x, top);  // and the subtraction's rounding error
+        const float v = __fsub_rn(ds, x);
+        const float dl = __fmul_rn(__fsub_rn(__fsub_rn(x, __fsub_rn(ds, v)), __fadd_rn(top, v)), post);
+        const float dh = __fmul_rn(ds, post);
+        const float yh = __fmul_rn(dh, r.hi);
         if (!(yh > -100.0f)) return FF{0.0f, 0.0f};
-        const float yl = __fmaf_rn(dh, r.hi, -yh) + __fmaf_rn(dl, r.hi, dh * r.lo);
+        const float yl = __fadd_rn(__fmaf_rn(dh, r.hi, -yh), __fmaf_rn(dl, r.hi, __fmul_rn(dh, r.lo)));
         const float magic = __fmaf_rn(yh, static_cast<float>(kTable), 12582912.0f);  // 1.5 * 2^23: rounds to a whole number
         const int k = __float_as_int(magic) - 0x4B400000;
-        const float g0 = __fmaf_rn(magic - 12582912.0f, -1.0f / kTable, yh);  // exact
-        const float g = g0 + yl, gl = yl - (g - g0);
-        const float zh = g * kLn2;
-        const float zl = __fmaf_rn(g, kLn2, -zh) + __fmaf_rn(g, kLn2Lo, gl * kLn2);
-        const float sq = zh * zh, half = 0.5f * sq, sql = __fmaf_rn(zh, zh, -sq);
+        const float g0 = __fmaf_rn(__fsub_rn(magic, 12582912.0f), -1.0f / kTable, yh);  // exact
+        const float g = __fadd_rn(g0, yl), gl = __fsub_rn(yl, __fsub_rn(g, g0));
+        const float zh = __fmul_rn(g, kLn2);
+        const float zl = __fadd_rn(__fmaf_rn(g, kLn2, -zh), __fmaf_rn(g, kLn2Lo, __fmul_rn(gl, kLn2)));
+        const float sq = __fmul_rn(zh, zh), half = __fmul_rn(0.5f, sq), sql = __fmaf_rn(zh, zh, -sq);
         const float rest = sq * zh * __fmaf_rn(zh, 1.0f / 24, 1.0f / 6);  // of the series, beyond the square
-        const float u = zh + half;  // 2^(g + gl) = 1 + u + ul
-        const float ul = (half - (u - zh)) + (rest + (zl + __fmaf_rn(zh, zl, 0.5f * sql)));
+        const float u = __fadd_rn(zh, half);  // 2^(g + gl) = 1 + u + ul
+        const float ul = __fsub_rn(half, __fsub_rn(u, zh)) + (rest + (zl + __fmaf_rn(zh, zl, 0.5f * sql)));
         const float2 t = table[k & (kTable - 1)];
-        const float ph = t.x * u, pl = __fmaf_rn(t.x, u, -ph);
-        const float s = t.x + ph;
-        const float lo = (ph - (s - t.x)) + (pl + (t.y + __fmaf_rn(t.x, ul, t.y * u)));
+        const float ph = __fmul_rn(t.x, u), pl = __fmaf_rn(t.x, u, -ph);
+        const float s = __fadd_rn(t.x, ph);
+        const float lo = __fsub_rn(ph, __fsub_rn(s, t.x)) + (pl + (t.y + __fmaf_rn(t.x, ul, t.y * u)));
         const float scale = __int_as_float(((k >> 8) + 127) << 23);
-        const float hi = s + lo;  // normalised, as comparisons with it need
-        return FF{hi * scale, (lo - (hi - s)) * scale};
+        const float hi = __fadd_rn(s, lo);  // normalised, as comparisons with it need
+        return FF{__fmul_rn(hi, scale), __fmul_rn(__fsub_rn(lo, __fsub_rn(hi, s)), scale)};
     }
 };
 struct SampleArgs {

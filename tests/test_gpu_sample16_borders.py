@@ -1,4 +1,5 @@
-"""sel_sample16 on the GPU at borders next to a float: min-p at an id's weight."""
+"""sel_sample16 on the GPU at borders next to a float: min-p at an id's weight, and
+draws at a cumulative mass."""
 import numpy as np
 import pytest
 import torch
@@ -73,3 +74,48 @@ def test_min_p_at_weights_far_down(dtype):
     got, _ = call(x.cuda(), T[at], None, None, m[at], u)
     kept = off[at] <= 0
     assert np.array_equal(got > 0, kept), (int(((got > 0) != kept).sum()), at.size)
+
+
+def near_borders(x, T, least, most, many):
+    """(uniform, id) pairs of a row: floats between `least` and `most` off an
+    id's cumulative mass relative to the whole, and the id that they draw."""
+    order = np.lexsort((np.arange(x.size), -x))
+    z = x[order].astype(np.longdouble)
+    w = np.exp((z - z[0]) / np.longdouble(np.float32(T)))
+    cum = np.cumsum(w)
+    b = cum[:-1] / cum[-1]
+    u = b.astype(np.float32)
+    off = np.abs(b - u.astype(np.longdouble)).astype(np.float64)
+    hit = (off >= least) & (off <= most) & (u < 1)
+    # both ids at the border weigh far more than the distance to it
+    share = (w / cum[-1]).astype(np.float64)
+    hit &= (share[:-1] > 8 * most) & (share[1:] > 8 * most)
+    at = np.flatnonzero(hit)[:many]
+    past = u[at].astype(np.longdouble) >= b[at]
+    return u[at], order[np.where(past, at + 1, at)]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("kind,T", [("few values", 1.0), ("few values", 0.7), ("many values", 0.9)])
+def test_draws_next_to_a_cumulative_mass(dtype, kind, T):
+    """Rows whose borders lie 2^-39 to 2^-35 from a float. Weights are good to
+    2^-44 where they count, a sum of two float pairs to 2^-46, and about 30 of
+    those lie between an id's weight and its cumulative mass, a product with
+    the uniform after them: at most 2^-40 in all. A product of a float pair whose
+    steps were fused would be good to 2^-24 only."""
+    rng = np.random.default_rng(17)
+    V = 40_000 if kind == "few values" else 9_000
+    rows, us, want = [], [], []
+    for _ in range(24):
+        x = rng.normal(0, 1.5, size=V)
+        if kind == "few values":
+            x = np.round(x * 3) / 3
+        x = torch.from_numpy(x).to(DT[dtype])
+        u, ids = near_borders(x.double().numpy(), T, 2.0 ** -39, 2.0 ** -35, 24)
+        rows += [x] * len(u)
+        us.append(u)
+        want.append(ids)
+    us, want = np.concatenate(us), np.concatenate(want)
+    assert us.size > 60
+    got, _ = call(torch.stack(rows).cuda(), np.full(us.size, T, np.float32), None, None, None, us)
+    assert np.array_equal(got, want), (int((got != want).sum()), us.size)
