@@ -133,17 +133,20 @@ __device__ __forceinline__ void consume(Ctx& c, uint32_t ring, uint32_t entries,
     const uint32_t entry_bytes = f.tile * (B::kScales + (kZeros ? B::kZeros : 0));  // a slot's
     const uint32_t e0 = entries + row * B::kScales, ez = entries + f.tile * B::kScales + row * B::kZeros;
     const uint32_t x_block = a.rows * 64, slot_bytes = f.tile * kRowBytes;
-    // Rows that were scaled up go back before the group's scale meets their sums,
-    // rows that were scaled down at the end: nothing in between overflows that
-    // unscaled sums would not.
+    // Sums go back to scale before the group's scale meets them, as far as they
+    // stay in range: a group's is below 2^26, so by up to 2^100. What is left, for
+    // rows that were scaled down by more, follows at the end. Nothing in between
+    // overflows that unscaled sums would not, and nothing gets lost below fp32's
+    // smallest normal (a group's least nonzero sum is 2^-24, and it back by 2^100
+    // meets scales of 2^-133 at the least).
     constexpr bool kScaled = !std::is_same_v<T, E>;
-    float down[2], up[2];
+    float before[2], after[2];
     if constexpr (kScaled) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int sh = row_shift(c.largest[min(2 * t + e, a.rows - 1)]);
-            down[e] = exp2i(min(-sh, 0));
-            up[e] = exp2i(max(-sh, 0));
+            before[e] = exp2i(min(-sh, 100));
+            after[e] = exp2i(max(-sh - 100, 0));
         }
     }
     uint32_t slot = 0, phase = 0;
@@ -183,8 +186,8 @@ __device__ __forceinline__ void consume(Ctx& c, uint32_t ring, uint32_t entries,
                     if (b % kBlocks == kBlocks - 1) {
                         const float sa = bits_f32<T>(entry16(sc[0], grp)), sb = bits_f32<T>(entry16(sc[1], grp));
                         if constexpr (kScaled) {
-                            mul2(d[0], d[1], down);
-                            mul2(d[2], d[3], down);
+                            mul2(d[0], d[1], before);
+                            mul2(d[2], d[3], before);
                         }
                         acc[0] = fmaf(sa, d[0], acc[0]);
                         acc[1] = fmaf(sa, d[1], acc[1]);
@@ -204,7 +207,7 @@ __device__ __forceinline__ void consume(Ctx& c, uint32_t ring, uint32_t entries,
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const uint32_t r = 2 * t + (e & 1), v = vt + row + 8 * (e >> 1);
-            if constexpr (kScaled) acc[e] *= up[e & 1];
+            if constexpr (kScaled) acc[e] *= after[e & 1];
             if (active && r < a.rows && v < v_end) store_as(a.out, a.out_dtype, r * a.ld + v, acc[e]);
         }
     }
