@@ -37,6 +37,7 @@
 #include <type_traits>
 
 #include "sel_head.cuh"
+#include "sel_per_device.h"
 
 namespace sel {
 namespace {
@@ -608,11 +609,16 @@ sel_status launch(const HeadIn& in, const HeadArgs& args, cudaStream_t stream) {
         !make_map(&mx, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, in.x, a.H, a.rows, kAtomK, N, CU_TENSOR_MAP_SWIZZLE_128B))
         return SEL_ECUDA;
     // the split of the registers counts on what the launch has
-    static const bool regs_ok = [] {
-        cudaFuncAttributes f{};
-        return cudaFuncGetAttributes(&f, head_kernel<T, N>) == cudaSuccess && f.numRegs == kLaunchRegs;
-    }();
-    if (!regs_ok || !dynamic_smem_once<head_kernel<T, N>>(Config<N>::kSmem)) return SEL_ECUDA;
+    static PerDevice<int> registers;
+    int dev = -1, regs = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || !registers.get(dev, regs, [](int& n) {
+            cudaFuncAttributes f{};
+            if (cudaFuncGetAttributes(&f, head_kernel<T, N>) != cudaSuccess) return false;
+            n = f.numRegs;
+            return true;
+        }))
+        return SEL_ECUDA;
+    if (regs != kLaunchRegs || !dynamic_smem_once<head_kernel<T, N>>(Config<N>::kSmem)) return SEL_ECUDA;
     const cudaError_t e = launch_pdl(head_kernel<T, N>, dim3(ceil_div(a.V, a.range)), dim3(kNT), Config<N>::kSmem,
                                      stream, mt, mb, mx, a);
     return e == cudaSuccess ? SEL_OK : SEL_ECUDA;

@@ -43,6 +43,7 @@
 #include "sel.h"
 #include "sel_common.cuh"
 #include "sel_dtype.cuh"
+#include "sel_per_device.h"
 #include "sel_plan.h"
 #include "sel_units.cuh"
 
@@ -901,15 +902,20 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
 }
 
 // CTAs a row for a batch: the cluster size whose rounds of resident clusters
-// take least. A CTA takes about 15 us beside its share, and 1 us for 8,000 ids (12,000
-// where the rows' top-k is small).
+// take least. A CTA takes 14.5 us beside its share, and 1 us for 10,000 ids (8,000
+// without top-k, 12,000 where the rows' top-k is small).
 template <typename T>
 uint32_t ctas_for(uint32_t rows, uint32_t V) {
     struct Table {
-        int resident[kMaxCluster + 1] = {};
+        int resident[kMaxCluster + 1];  // clusters of that size on the device at a time
     };
-    static const Table t = [] {
-        Table r;
+    static PerDevice<Table> tables;
+    Table t{};
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
+    // (where a query fails, this call goes by the ones that did not)
+    (void)tables.get(dev, t, [](Table& r) {
+        bool ok = true;
         for (uint32_t c = 1; c <= kMaxCluster; ++c) {
             cudaLaunchConfig_t cfg{};
             cfg.gridDim = dim3(c, 1, 1);
@@ -925,12 +931,13 @@ uint32_t ctas_for(uint32_t rows, uint32_t V) {
             int n = 0;
             if (cudaOccupancyMaxActiveClusters(&n, sample16_kernel<T>, &cfg) != cudaSuccess || n < 0) {
                 (void)cudaGetLastError();
+                ok = false;
                 n = 0;
             }
             r.resident[c] = n;
         }
-        return r;
-    }();
+        return ok;
+    });
     uint32_t best = 1;
     double least = 1e30;
     for (uint32_t c = 1; c <= kMaxCluster; ++c) {
