@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -34,6 +35,34 @@ def nvcc() -> str:
 
 def sources() -> list[str]:
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
+
+
+def launch_registers() -> int:
+    """The registers a thread that the wide head's split between its warps
+    counts on (csrc/sel_head_many.cuh)."""
+    text = open(os.path.join(CSRC, "sel_head_many.cuh")).read()
+    return int(re.search(r"kLaunchRegs = (\d+)", text).group(1))
+
+
+def check_registers(src: str, report: str, want: int) -> None:
+    """Raise unless every head_kernel in the assembler's report (-Xptxas -v)
+    takes `want` registers a thread: with another number, which another compiler
+    may choose, the library refuses every call of it."""
+    found = {}
+    name = None
+    for line in report.splitlines():
+        if m := re.search(r"Compiling entry function '([^']+)'", line):
+            name = m.group(1)
+        elif name and (m := re.search(r"Used (\d+) registers", line)):
+            found[name] = int(m.group(1))
+            name = None
+    heads = {n: r for n, r in found.items() if "head_kernel" in n}
+    if not heads:
+        raise RuntimeError(f"{os.path.basename(src)}: the assembler reported no head_kernel")
+    wrong = {n: r for n, r in heads.items() if r != want}
+    if wrong:
+        raise RuntimeError(f"{os.path.basename(src)}: kernels of other than {want} registers a thread, on which the "
+                           f"split between their warps (kLaunchRegs) counts: {wrong}")
 
 
 def _inputs() -> list[str]:
@@ -65,10 +94,13 @@ def build(force: bool = False, verbose: bool = False, extra_flags: tuple[str, ..
 
     def compile_one(src: str) -> str:
         obj = os.path.join(objdir, os.path.basename(src)[:-3] + ".o")
-        cmd = [cc, *ARCH, *NVCC_FLAGS, *extra_flags, "-c", src, "-o", obj]
+        counted = os.path.basename(src).startswith("sel_head_many")
+        cmd = [cc, *ARCH, *NVCC_FLAGS, *(["-Xptxas", "-v"] if counted else []), *extra_flags, "-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
+        if counted:
+            check_registers(src, r.stdout + r.stderr, launch_registers())
         if verbose:
             sys.stdout.write(r.stdout + r.stderr)
         return obj
