@@ -468,11 +468,16 @@ def _on_stream(stream, dev: int) -> int:
     return _stream(stream)
 
 
+_U32_MAX = 0xFFFFFFFF  # the library's sizes; ctypes would pass larger ones on without their upper bits
+
+
 def _rows_2d(t, name) -> tuple[int, int, int]:
     """(rows, columns, row stride) of a matrix whose rows are contiguous."""
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions")
     rows, cols = t.shape
+    if rows > _U32_MAX or cols > _U32_MAX:
+        raise ValueError(f"{name} must have fewer than 2^32 rows and columns")
     if cols > 1 and t.stride(1) != 1:
         raise ValueError(f"the rows of {name} must be contiguous")
     ld = t.stride(0) if rows > 1 else cols
@@ -495,7 +500,9 @@ def _w4(q, scales, zeros, group: int, dtype) -> tuple[int, int]:
     if q.dtype != torch.uint8 or q.dim() != 2 or not q.is_contiguous():
         raise ValueError("q must be a contiguous uint8 matrix [V, H / 2]")
     V, H = q.shape[0], 2 * q.shape[1]
-    if group <= 0 or H % group:
+    if V > _U32_MAX or H > _U32_MAX:
+        raise ValueError("q must have fewer than 2^32 rows and columns")
+    if group <= 0 or group > _U32_MAX or H % group:
         raise ValueError("H must be a multiple of group")
     if scales.dtype != dtype or scales.shape != (V, H // group) or not scales.is_contiguous():
         raise ValueError(f"scales must be contiguous [V, H / group] of {dtype}")
@@ -543,6 +550,8 @@ def _embed_out(ids, out, H: int, dtype) -> int:
     if ids.dtype not in _IDS or not ids.is_contiguous():
         raise ValueError("ids must be contiguous int32 or uint32")
     n = ids.numel()
+    if n > _U32_MAX:
+        raise ValueError("a call takes fewer than 2^32 ids")
     if out.dtype != dtype or out.numel() != n * H or out.shape[-1] != H or not out.is_contiguous():
         raise ValueError(f"out must be contiguous [ids, H] of {dtype}")
     return n
@@ -555,6 +564,8 @@ def sel_embed(ids, table, scale: float, out, stream=None) -> None:
     if table.dtype not in _DTYPES or table.dim() != 2 or not table.is_contiguous():
         raise ValueError("table must be a contiguous matrix [V, H] of f32, f16 or bf16")
     V, H = table.shape
+    if V > _U32_MAX or H > _U32_MAX:
+        raise ValueError("table must have fewer than 2^32 rows and columns")
     n = _embed_out(ids, out, H, table.dtype)
     _check((_lib or load()).sel_embed(ids.data_ptr(), n, table.data_ptr(), _DTYPES[table.dtype], V, H, scale,
                                       out.data_ptr(), _on_stream(stream, dev)), "sel_embed")
