@@ -685,8 +685,11 @@ typedef enum sel_dtype { SEL_F32 = 0, SEL_F16 = 1, SEL_BF16 = 2 } sel_dtype;
  * hidden[r][k] * s[v][k / group] * (q[v][k] - z[v][k / group]).
  * Products are exact, a group is summed in fp32, its scale is applied in
  * fp32 and each logit is rounded once to its type (f32 for the fp32 calls of
- * this library, f16 or bf16 for sel_sample16). A nonfinite hidden state or
- * scale gives nonfinite logits, which the selection calls fail closed.
+ * this library, f16 or bf16 for sel_sample16). A nonfinite hidden state makes
+ * every logit of its row nonfinite, and each selection call fails the row
+ * closed. A nonfinite scale makes its matrix row's logits nonfinite: the fp32
+ * calls fail rows with one closed, sel_sample16 those with a NaN or a +Inf (a
+ * -Inf logit, here or by overflow of an f16 one, is a masked id to it).
  *
  *   d_hidden     [rows][H] of `dtype`, 16-byte aligned
  *   d_q          [V][H / 2] bytes, 16-byte aligned
