@@ -234,7 +234,7 @@ inline uint32_t entry_row_bytes(uint32_t group_log2, bool zeros) { return (kStag
 // `wait_empty(slot, phase)` waits for a slot, `done(slot)` reports it filled.
 template <int kGroupLog2, bool kZeros, uint32_t kBatch, typename Wait, typename Done>
 __device__ __forceinline__ void copy_entries(const HeadArgs& a, unsigned char* entries, uint32_t slot_bytes, uint32_t tile,
-                                             uint32_t slots, uint32_t repeats, uint32_t first, uint32_t step,
+                                             uint32_t slots, uint32_t first, uint32_t step,
                                              uint32_t v_begin, uint32_t v_end, Wait wait_empty, Done done) {
     using B = EntryBytes<kGroupLog2>;
     const uint32_t groups = a.H >> kGroupLog2, stages = (a.H + kStageK - 1) / kStageK;
@@ -243,24 +243,22 @@ __device__ __forceinline__ void copy_entries(const HeadArgs& a, unsigned char* e
     uint32_t slot = 0, phase = 0, turn = first;  // stages until this warp's next one
     for (uint32_t vt = v_begin; vt < v_end; vt += tile) {
         const uint32_t rows = min(tile, v_end - vt);
-        for (uint32_t rep = 0; rep < repeats; ++rep) {
-            for (uint32_t i = 0; i < stages; ++i) {
-                if (turn == 0) {
-                    turn = step;
-                    wait_empty(slot, phase);
-                    unsigned char* dst = entries + slot * slot_bytes;
-                    const uint64_t row = static_cast<uint64_t>(vt) * groups;
-                    copy_rows<B::kScales, kBatch>(dst, scales + 2 * row, i * B::kScales, 2 * groups, rows, ws);
-                    if (kZeros)
-                        copy_rows<B::kZeros, kBatch>(dst + tile * B::kScales, a.zeros + row, i * B::kZeros, groups, rows, wz);
-                    __syncwarp();
-                    done(slot);
-                }
-                --turn;
-                if (++slot == slots) {
-                    slot = 0;
-                    phase ^= 1;
-                }
+        for (uint32_t i = 0; i < stages; ++i) {
+            if (turn == 0) {
+                turn = step;
+                wait_empty(slot, phase);
+                unsigned char* dst = entries + slot * slot_bytes;
+                const uint64_t row = static_cast<uint64_t>(vt) * groups;
+                copy_rows<B::kScales, kBatch>(dst, scales + 2 * row, i * B::kScales, 2 * groups, rows, ws);
+                if (kZeros)
+                    copy_rows<B::kZeros, kBatch>(dst + tile * B::kScales, a.zeros + row, i * B::kZeros, groups, rows, wz);
+                __syncwarp();
+                done(slot);
+            }
+            --turn;
+            if (++slot == slots) {
+                slot = 0;
+                phase ^= 1;
             }
         }
     }

@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kMaxNT, 1)
         // round ahead would take a slot's phase before last for its last.
         const uint32_t lane = tid & 31, helper = warp - workers - 1, helpers = min(kHelpers, f.stages);
         if (helper < helpers) copy_entries<kGroupLog2, kZeros, kMaxTile / 32>(
-            a, entries, entry_bytes, f.tile, f.stages, 1, helper, helpers, v_begin, v_end,
+            a, entries, entry_bytes, f.tile, f.stages, helper, helpers, v_begin, v_end,
             [&](uint32_t slot, uint32_t phase) { wait(&c.empty[slot], phase ^ 1, &c.err); },
             [&](uint32_t slot) {
                 if (lane == 0) arrive(&c.full[slot]);

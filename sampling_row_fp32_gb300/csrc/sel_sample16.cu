@@ -281,9 +281,9 @@ struct Share {
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
     // f(v, logits) for vectors base + me, + kStride, ... below end, kAhead at a time
-    // with the next ones on their way. kAll: every thread calls it for all kAhead,
-    // past the end with masked ids.
-    template <uint32_t kStride, bool kAll, typename F>
+    // with the next ones on their way. Every thread calls it for all kAhead, past
+    // the end with masked ids.
+    template <uint32_t kStride, typename F>
     __device__ __forceinline__ void each(uint32_t base, uint32_t end, uint32_t me, F f) const {
         constexpr uint32_t kNegInf = 0x8000u | Kind<T>::kInf, kFill = kNegInf | (kNegInf << 16);
         const uint32_t full_lo = skew ? 1u : 0u, full_hi = (V + skew) / 8u;
@@ -301,7 +301,7 @@ struct Share {
                 uint4 q = next[j];
                 next[j] = load(v + kAhead * kStride);
                 if (v < end && (v < full_lo || v >= full_hi)) q = edge(v);
-                if (kAll || v < end) f(v, q);
+                f(v, q);
             }
         }
     }
@@ -875,7 +875,7 @@ __global__ void __launch_bounds__(kNT, 1) sample16_kernel(SampleArgs a) {
     if (static_cast<int>(warp) != __ffs(has) - 1) return;
     uint32_t left = place - (__shfl_sync(kFull, in, warp) - mine);  // ids of the bin before it in the run
     bool found = false;
-    share.template each<32, true>(run_lo, run_hi, lane, [&](uint32_t v, const uint4& q) {
+    share.template each<32>(run_lo, run_hi, lane, [&](uint32_t v, const uint4& q) {
         if (found) return;
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
         uint32_t which = 0;  // bit i: id i of the vector
