@@ -42,9 +42,15 @@ struct HeadIn {
 };
 
 // At most 8 hidden rows (the columns of one warp-level product) that fit shared
-// memory next to a ring of at least three stages. 4,096 x 248,320, groups of 64:
-// one row takes 100 us with head_few and 118 with the tcgen05 kernel; 16 rows,
-// two products a pair of words, took 155 against 121.
+// memory next to a ring of at least three stages. Times of 1 / 2 / 4 / 8 rows in
+// us, head_few against the tcgen05 kernel:
+//   4,096 x 248,320, groups of 64     99 / 107 / 110 / 114    115 / 116 / 116 / 116
+//   4,096 x 248,320, groups of 128    94 / 95 / 98 / 104      110 / 110 / 110 / 111
+//   8,192 x 202,048, 128, zeros      168 / 173 / 180 / 199    199 / 199 / 199 / 199
+//   2,880 x 93,001, 32, zeros (f16)   47 / 48 / 48 / 52       128 / 128 / 128 / 128
+//   1,024 x 151,936, groups of 64     20 / 20 / 20 / 22        22 / 22 / 22 / 23
+// 16 rows, two products a pair of words, took head_few 155 at the first size
+// against 117.
 inline bool head_few_fits(uint32_t rows, uint32_t H) {
     return rows <= 8 && static_cast<uint64_t>(rows) * ceil_div(H, kStageK) * kStageK * 2 <= 128u * 1024u;
 }

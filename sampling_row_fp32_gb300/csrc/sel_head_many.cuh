@@ -29,9 +29,10 @@
 // 248,320) but instruction issue, 59 percent busy: 13 instructions a word of
 // eight weights to unpack, a multiply-add for each D entry of a group, and the
 // hand-overs between the roles. 4,096 x 248,320, groups of 64: 16 rows 117 us, 32
-// rows 137, 49 rows 192 (3.0 TB/s, 520 TFLOP/s); 64 rows of 8,192 x 202,048, groups
-// of 128: 252, with zero points 262. Folding the scales into the operand would take
-// the epilogue out, and round every weight.
+// rows 137, 49 rows 192-193 (3.0 TB/s, 520 TFLOP/s), 64 rows 195 (33 to 64 rows are
+// one form, N = 64); 64 rows of 8,192 x 202,048, groups of 128: 253, with zero points
+// 262-275. Folding the scales into the operand would take the epilogue out, and
+// round every weight.
 #pragma once
 
 #include <type_traits>

@@ -30,9 +30,10 @@
 //
 // Masses are pairs of floats: FP64 runs at two results a clock and SM here.
 //
-// One row of 151,936 takes 13-18 us, a chain of about a dozen dependent steps; 49
-// rows of 248,320 32 us and 256 of 202,048 74 us (the rows' bytes alone would take
-// 3.6 and 15). Of the 41 us of 152 rows of 202,048 without top-k, counting takes
+// One row of 151,936 takes 14-18 us, 9 when it is greedy, a chain of about a dozen
+// dependent steps; 49 rows of 248,320 32 us and 256 of 202,048 72-74 us (the rows'
+// bytes alone would take 3.6 and 15). Of the 40 us of 152 rows of 202,048 without
+// top-k, counting takes
 // 15, the second look at the share 10 and the chain most of the rest; with a small
 // top-k counting runs at 5.9 TB/s.
 #include <cuda_bf16.h>
