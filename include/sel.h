@@ -67,7 +67,7 @@ typedef enum sel_status {
 /* Operation codes for sel_workspace_bytes. */
 enum { SEL_OP_ARGMAX = 0, SEL_OP_TOPK = 1, SEL_OP_SAMPLE = 2, SEL_OP_SPEC = 3,
        SEL_OP_SPEC_SAMPLER = 4, SEL_OP_SPEC_DIAG = 5, SEL_OP_SHARD_DRAW = 6,
-       SEL_OP_SPEC_SHARD_DRAW = 7 };
+       SEL_OP_SPEC_SHARD_DRAW = 7, SEL_OP_HEAD_LOSS = 9, SEL_OP_HEAD_LOSS_GRAD = 10 };
 
 /* Order of temperature and filters in sel_sample. */
 enum {
@@ -96,6 +96,7 @@ enum {
  *   op SEL_OP_SPEC_DIAG: rows = S, V, k = K
  *   op SEL_OP_SHARD_DRAW: rows, V = the shard's slice width (k ignored)
  *   op SEL_OP_SPEC_SHARD_DRAW: rows = S, V = the shard's slice width
+ *   op SEL_OP_HEAD_LOSS, SEL_OP_HEAD_LOSS_GRAD: rows, V, k = H
  * The size depends only on these arguments, not on the device. Returns 0
  * when the arguments are invalid (the entry point would refuse them anyway).
  */
@@ -761,6 +762,61 @@ sel_status sel_embed_w4(const uint32_t *d_ids, uint32_t n, const uint8_t *d_q,
                         const void *d_scales, const uint8_t *d_zeros,
                         uint32_t group, int dtype, uint32_t V, uint32_t H,
                         float scale, void *d_out, cudaStream_t stream);
+
+/*
+ * Learning: what a drafter is trained with on the rows that selection works on.
+ *
+ * sel_head_loss -- cross entropy of hidden states through a 16-bit output head,
+ * the logits z[r][v] = sum over k of hidden[r][k] * weight[v][k] never stored:
+ * lse[r] = ln sum over v of exp z[r][v], loss[r] = lse[r] - z[r][targets[r]]
+ * (the negative log-probability of the target). A target >= V
+ * (SEL_INVALID_ID: a prompt's or padding's position) makes the row ignored:
+ * its loss is 0. Products are exact, their sums and the statistics are in fp32 or
+ * more, and a loss near 0 keeps its relative precision. A row with a NaN or
+ * +Inf logit gets NaN; -Inf is a probability of 0.
+ *
+ *   d_hidden     [rows][H] of `dtype`, 16-byte aligned
+ *   d_weight     [V][H] of `dtype`, 16-byte aligned
+ *   dtype        SEL_F16 or SEL_BF16; H a multiple of 8 (SEL_EUNSUPPORTED
+ *                otherwise)
+ *   d_targets    [rows] u32
+ *   d_loss       [rows] f32
+ *   d_lse        [rows] f32, or NULL
+ *   d_ws         workspace of sel_workspace_bytes(SEL_OP_HEAD_LOSS, rows, V, H)
+ */
+sel_status sel_head_loss(const void *d_hidden, uint32_t rows,
+                         const void *d_weight, int dtype, uint32_t V,
+                         uint32_t H, const uint32_t *d_targets, float *d_loss,
+                         float *d_lse, void *d_ws, size_t ws_bytes,
+                         cudaStream_t stream);
+
+/*
+ * sel_head_loss_grad -- the gradients of sum over r of grad[r] * loss[r]: with
+ * P[r][v] = exp(z[r][v] - lse[r]) - (v == targets[r]),
+ *   hidden_grad[r] = grad[r] * sum over v of P[r][v] * weight[v]
+ *   weight_grad[v] = sum over r of grad[r] * P[r][v] * hidden[r].
+ * Ignored rows and rows whose grad is 0 count for nothing, whatever they hold:
+ * their hidden_grad is zeros. P is rounded to `dtype` for the products, as is
+ * hidden times grad over the largest grad (exactly hidden where all grads
+ * are equal); sums are in fp32 and each gradient is rounded once. z is
+ * computed again, in pieces of the vocabulary.
+ *
+ *   d_hidden, rows, d_weight, dtype, V, H, d_targets  as for sel_head_loss
+ *   d_lse          [rows] f32, from sel_head_loss
+ *   d_grad         [rows] f32
+ *   d_hidden_grad  [rows][H] of `dtype`, 16-byte aligned, or NULL
+ *   d_weight_grad  [V][H] of `dtype`, 16-byte aligned, or NULL (not both)
+ *   d_ws           workspace of sel_workspace_bytes(SEL_OP_HEAD_LOSS_GRAD,
+ *                  rows, V, H)
+ * With rows == 0 weight_grad becomes zeros.
+ */
+sel_status sel_head_loss_grad(const void *d_hidden, uint32_t rows,
+                              const void *d_weight, int dtype, uint32_t V,
+                              uint32_t H, const uint32_t *d_targets,
+                              const float *d_lse, const float *d_grad,
+                              void *d_hidden_grad, void *d_weight_grad,
+                              void *d_ws, size_t ws_bytes,
+                              cudaStream_t stream);
 
 /* Static description of a status code. */
 const char *sel_status_string(sel_status status);

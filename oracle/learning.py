@@ -1,0 +1,46 @@
+"""Plain 64-bit forms of the operators that a drafter learns with
+(``include/sel.h``): cross entropy through an output head with its gradient, and
+the divergence from a teacher's top logits with its gradient. Inputs are torch
+tensors of any device whose values are taken as they are; written from the
+definitions, with no code of the kernels."""
+from __future__ import annotations
+
+import torch
+
+INF = float("inf")
+
+
+def _in_vocabulary(ids, V):
+    """ids as int64, -1 for those that name no column."""
+    ids = ids.to(torch.int64)
+    return torch.where((ids >= 0) & (ids < V), ids, -1)
+
+
+def head_loss(x, w, targets):
+    """(loss, lse) of hidden rows x [n, H] through w [V, H]. The loss of a row is
+    ln(1 + sum over the other ids of exp(z - z_target)), 0 where the target names
+    no id."""
+    z = x.double() @ w.double().T
+    t = _in_vocabulary(targets, w.shape[0])
+    lse = torch.logsumexp(z, dim=1)
+    rows = torch.arange(len(t), device=z.device)
+    at = z[rows, t.clamp(min=0)]
+    others = z.clone()
+    others[rows, t.clamp(min=0)] = -INF
+    d = torch.logsumexp(others, dim=1) - at
+    loss = torch.where(d > 30, d + torch.exp(-d), torch.log1p(torch.exp(d)))
+    return torch.where(t >= 0, loss, 0.0), lse
+
+
+def head_loss_grad(x, w, targets, lse, grad):
+    """(hidden gradient, weight gradient) of sum of grad * loss; rows whose target
+    names no id or whose grad is 0 count for nothing."""
+    x64, w64 = x.double(), w.double()
+    t = _in_vocabulary(targets, w.shape[0])
+    live = torch.nonzero((t >= 0) & (grad != 0))[:, 0]
+    p = torch.exp(x64[live] @ w64.T - lse[live].double()[:, None])
+    p[torch.arange(len(live), device=p.device), t[live]] -= 1.0
+    p = p * grad[live].double()[:, None]
+    dx = torch.zeros_like(x64)
+    dx[live] = p @ w64
+    return dx, p.T @ x64[live]

@@ -23,6 +23,7 @@ SEL_INVALID_ID = 0xFFFFFFFF
 SEL_MAX_K = 1024
 (SEL_OP_ARGMAX, SEL_OP_TOPK, SEL_OP_SAMPLE, SEL_OP_SPEC, SEL_OP_SPEC_SAMPLER, SEL_OP_SPEC_DIAG,
  SEL_OP_SHARD_DRAW, SEL_OP_SPEC_SHARD_DRAW) = range(8)
+SEL_OP_HEAD_LOSS, SEL_OP_HEAD_LOSS_GRAD = 9, 10
 SEL_ORDER_TEMP_FIRST, SEL_ORDER_TEMP_LAST = 0, 1
 SPEC_MODE_REJECTION, SPEC_MODE_ARGMAX = 0, 1
 
@@ -31,7 +32,8 @@ EXPORTED = ("sel_workspace_bytes", "sel_workspace_init", "sel_argmax", "sel_topk
             "sel_merge_shards", "sel_sample_shards", "sel_argmax_excluding",
             "spec_accept_sampler", "spec_diagnostics", "sel_topk_stats", "sel_shard_draw_mass",
             "sel_shard_draw", "spec_shard_stats", "spec_accept_shards", "spec_shard_draw_mass",
-            "spec_shard_draw", "sel_head_w4", "sel_sample16", "sel_embed", "sel_embed_w4")
+            "spec_shard_draw", "sel_head_w4", "sel_sample16", "sel_embed", "sel_embed_w4",
+            "sel_head_loss", "sel_head_loss_grad")
 SEL_F32, SEL_F16, SEL_BF16 = range(3)
 SEL_MAX_H = 1 << 20
 SEL_SAMPLE16_MAX_V = 524_208
@@ -141,6 +143,10 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.sel_embed.restype = _i
     lib.sel_embed_w4.argtypes = [_vp, _u32, _vp, _vp, _vp, _u32, _i, _u32, _u32, _f, _vp, _vp]
     lib.sel_embed_w4.restype = _i
+    lib.sel_head_loss.argtypes = [_vp, _u32, _vp, _i, _u32, _u32, _vp, _vp, _vp, _vp, _sz, _vp]
+    lib.sel_head_loss.restype = _i
+    lib.sel_head_loss_grad.argtypes = [_vp, _u32, _vp, _i, _u32, _u32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+    lib.sel_head_loss_grad.restype = _i
     lib.sel_status_string.argtypes = [ctypes.c_int]
     lib.sel_status_string.restype = ctypes.c_char_p
     if path is None:
@@ -582,6 +588,65 @@ def sel_embed_w4(ids, q, scales, zeros, group: int, scale: float, out, stream=No
     _check((_lib or load()).sel_embed_w4(ids.data_ptr(), n, q.data_ptr(), scales.data_ptr(),
                                          None if zeros is None else zeros.data_ptr(), group, _DTYPES[scales.dtype],
                                          V, H, scale, out.data_ptr(), _on_stream(stream, dev)), "sel_embed_w4")
+
+
+# ---------------------------------------------------------------------------
+# learning: cross entropy through the head, distillation
+# ---------------------------------------------------------------------------
+
+def _head16(hidden, weight, targets) -> tuple[int, int, int]:
+    """(rows, V, H) of hidden [rows, H], weight [V, H] and targets [rows]."""
+    if hidden.dtype not in (torch.float16, torch.bfloat16) or weight.dtype != hidden.dtype:
+        raise ValueError("hidden and weight must be f16 or bf16, both the same")
+    if hidden.dim() != 2 or not hidden.is_contiguous() or weight.dim() != 2 or not weight.is_contiguous():
+        raise ValueError("hidden and weight must be contiguous [rows, H] and [V, H]")
+    rows, H = hidden.shape
+    V = weight.shape[0]
+    if weight.shape[1] != H:
+        raise ValueError("hidden and weight must have rows of one width")
+    if rows > _U32_MAX or V > _U32_MAX or H > _U32_MAX:
+        raise ValueError("hidden and weight must have fewer than 2^32 rows and columns")
+    return rows, V, H
+
+
+def _workspace(ws) -> int | None:
+    if ws is None:
+        return None
+    if not ws.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    return ws.data_ptr()
+
+
+def sel_head_loss(hidden, weight, targets, loss, lse=None, ws=None, stream=None) -> None:
+    """hidden [rows, H] and weight [V, H] f16/bf16, targets int32/uint32 [rows]
+    (an id >= V ignores its row) -> loss and lse (or None) f32 [rows]; ws of
+    workspace(SEL_OP_HEAD_LOSS, rows, V, H)."""
+    dev = _device(hidden, weight, targets, loss, lse, ws)
+    rows, V, H = _head16(hidden, weight, targets)
+    f32 = (torch.float32,)
+    _check((_lib or load()).sel_head_loss(hidden.data_ptr(), rows, weight.data_ptr(), _DTYPES[hidden.dtype], V, H,
+                                          _vector(targets, rows, _IDS, "targets"), _vector(loss, rows, f32, "loss"),
+                                          _vector(lse, rows, f32, "lse"), _workspace(ws), _nbytes(ws),
+                                          _on_stream(stream, dev)), "sel_head_loss")
+
+
+def sel_head_loss_grad(hidden, weight, targets, lse, grad, hidden_grad, weight_grad, ws=None, stream=None) -> None:
+    """lse from sel_head_loss and grad, f32 [rows] -> hidden_grad [rows, H] and
+    weight_grad [V, H] (either may be None) of hidden's type; ws of
+    workspace(SEL_OP_HEAD_LOSS_GRAD, rows, V, H)."""
+    dev = _device(hidden, weight, targets, lse, grad, hidden_grad, weight_grad, ws)
+    rows, V, H = _head16(hidden, weight, targets)
+    for t, like, name in ((hidden_grad, hidden, "hidden_grad"), (weight_grad, weight, "weight_grad")):
+        if t is not None and (t.dtype != like.dtype or t.shape != like.shape or not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous, of the shape and type of {name[:-5]}")
+    f32 = (torch.float32,)
+    _check((_lib or load()).sel_head_loss_grad(hidden.data_ptr(), rows, weight.data_ptr(), _DTYPES[hidden.dtype], V, H,
+                                               _vector(targets, rows, _IDS, "targets"),
+                                               _vector(lse, rows, f32, "lse"), _vector(grad, rows, f32, "grad"),
+                                               None if hidden_grad is None else hidden_grad.data_ptr(),
+                                               None if weight_grad is None else weight_grad.data_ptr(),
+                                               _workspace(ws), _nbytes(ws), _on_stream(stream, dev)),
+           "sel_head_loss_grad")
 
 
 # ---------------------------------------------------------------------------

@@ -47,6 +47,10 @@ extern "C" size_t sel_workspace_bytes(int op, uint32_t rows, uint32_t V, uint32_
             return shard_draw_ws_bytes(rows, V);
         case SEL_OP_SPEC_SHARD_DRAW:
             return spec_shard_draw_ws_bytes(rows, V);
+        case SEL_OP_HEAD_LOSS:
+            return head_loss_ws_bytes(rows, V, k);
+        case SEL_OP_HEAD_LOSS_GRAD:
+            return head_loss_grad_ws_bytes(rows, V, k);
         default:
             return 0;
     }

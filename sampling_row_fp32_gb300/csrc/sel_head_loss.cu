@@ -1,0 +1,647 @@
+// sel_head_loss.cu -- cross entropy through a 16-bit output head without its
+// logits rows, and the gradient of that.
+//
+//   z = X W^T;  lse_r = ln sum_v exp z_rv;  loss_r = lse_r - z_r,t
+//   P_rv = exp(z_rv - lse_r) - [v == t_r]
+//   dX_r = g_r sum_v P_rv W_v;  dW_v = sum_r g_r P_rv X_r
+//
+// The loss is one product (sel_gemm.cuh) whose epilogue keeps two numbers of each
+// row and 128 columns, a reference exponent and the sum of the others' weights
+// over it; a small launch joins them. The target's logit is kept apart, so that
+// loss = ln(1 + sum_others / e^z_t) holds its bits where it is near zero.
+//
+// The gradient goes over the vocabulary in pieces. For each, one launch computes
+// z again and leaves P in the workspace, rounded to the operands' type; a second
+// one computes the piece's rows of dW (K = rows) and adds the piece's share of
+// dX (K = the piece) to fp32 sums.
+#include <algorithm>
+
+#include <cuda_runtime.h>
+
+#include "sel_gemm.cuh"
+
+using namespace sel;
+
+namespace sel {
+namespace {
+
+constexpr float kLog2E = 1.4426950408889634f;
+
+// Row tiles run fastest over up to 32 of them, then columns: the rows' operand
+// stays in L2 while the matrix passes once.
+struct Raster {
+    uint32_t mt, nt;
+    __device__ __forceinline__ void at(uint32_t i, uint32_t& m, uint32_t& n) const {
+        constexpr uint32_t kGroup = 32;
+        const uint32_t g = i / (kGroup * nt), r = i - g * kGroup * nt, gm = min(kGroup, mt - g * kGroup);
+        n = r / gm;
+        m = g * kGroup + r - n * gm;
+    }
+    __device__ __forceinline__ uint32_t share(uint32_t worker, uint32_t workers) const {
+        const uint32_t n = mt * nt;
+        return worker < n ? (n - worker - 1) / workers + 1 : 0;
+    }
+};
+
+// 2^n for a whole n <= 0, 0 below the normal numbers (and for -Inf).
+__device__ __forceinline__ float pow2(float n) {
+    return n >= -126.0f ? __uint_as_float(static_cast<uint32_t>(static_cast<int>(n) + 127) << 23) : 0.0f;
+}
+
+__device__ __forceinline__ bool any_target(uint32_t t, uint32_t col) { return t - col < 32u; }
+
+// A row of z in logarithms to base 2: sum over its ids but the target of 2^(y - m),
+// m a whole number, so that sums of different tiles meet by exact shifts.
+struct Part {
+    float m, s;
+};
+
+template <typename T, bool kPair>
+struct LossProblem {
+    using Type = T;
+    CUtensorMap x, w;
+    const uint32_t* targets;
+    Part* parts;  // [2 nt][rows]
+    float* at;    // [rows]: the target's logit
+    uint32_t* error;
+    uint32_t rows, V, steps;
+    Raster raster;
+
+    __device__ __forceinline__ uint32_t count(uint32_t worker, uint32_t workers) const { return raster.share(worker, workers); }
+    __device__ __forceinline__ GemmTile tile(uint32_t worker, uint32_t workers, uint32_t j) const {
+        uint32_t m, n;
+        raster.at(worker + j * workers, m, n);
+        return {&x, &w, m * GemmConfig<kPair>::kTileM, n * kTileN, 0, 0, steps, false, false};
+    }
+    template <typename Load>
+    __device__ __forceinline__ void epilogue(const GemmTile& t, const EpiWarp& w, Load load) const {
+        const uint32_t row = t.am + w.row, col = t.bn + w.col;
+        const uint32_t target = row < rows ? targets[row] : SEL_INVALID_ID;
+        Part p{-INFINITY, 0.0f};
+#pragma unroll 1
+        for (uint32_t c = 0; c < 4; ++c) {
+            float v[32];
+            load(c, v);
+            const uint32_t c0 = col + 32 * c;
+            if (any_target(target, c0)) {
+#pragma unroll
+                for (uint32_t i = 0; i < 32; ++i) {
+                    if (target == c0 + i) {
+                        if (target < V) at[row] = v[i];
+                        v[i] = -INFINITY;
+                    }
+                }
+            }
+            if (c0 + 32 > V) {
+#pragma unroll
+                for (uint32_t i = 0; i < 32; ++i)
+                    if (c0 + i >= V) v[i] = -INFINITY;
+            }
+            float top = v[0];
+#pragma unroll
+            for (uint32_t i = 1; i < 31; i += 2) top = max3f(top, v[i], v[i + 1]);
+            top = fmaxf(top, v[31]);
+            const float m = fmaxf(p.m, ceilf(top * kLog2E));
+            const float ref = m == -INFINITY ? 0.0f : m;
+            float s[4] = {p.s * pow2(p.m - ref), 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (uint32_t i = 0; i < 32; ++i) s[i % 4] += ex2_approx(fmaf(v[i], kLog2E, -ref));
+            p.m = m;
+            p.s = (s[0] + s[1]) + (s[2] + s[3]);
+        }
+        if (row < rows) parts[static_cast<uint64_t>(col / 128) * rows + row] = p;
+    }
+};
+
+struct Joined {
+    float m;
+    FF s;
+};
+__device__ __forceinline__ Joined join(const Joined& a, const Joined& b) {
+    const float m = fmaxf(a.m, b.m), ref = m == -INFINITY ? 0.0f : m;
+    const float fa = pow2(a.m - ref), fb = pow2(b.m - ref);
+    return {m, ff_add(FF{a.s.hi * fa, a.s.lo * fa}, FF{b.s.hi * fb, b.s.lo * fb})};
+}
+
+struct LossFinishArgs {
+    const Part* parts;
+    const float* at;
+    const uint32_t* targets;
+    const uint32_t* error;
+    float* loss;
+    float* lse;
+    uint32_t rows, V, slots;
+};
+
+// The loss and lse of a row from the joined weights of its other ids.
+__device__ __forceinline__ void finish_row(const LossFinishArgs& a, uint32_t row, const Joined& j) {
+    const uint32_t t = a.targets[row];
+    // (one row's last steps: in 64 bits they cost nothing next to its launch)
+    const double c = static_cast<double>(kLog2E);
+    const double sum = ff_to_double(j.s);
+    const double others = sum == 0.0 ? -INFINITY : (static_cast<double>(j.m) + log2(sum)) / c;
+    double loss = 0.0, lse = others;
+    if (t < a.V) {
+        const double z = static_cast<double>(a.at[row]), d = others - z;
+        loss = d > 40.0 ? d + exp(-d) : log1p(exp(d));
+        lse = z + loss;
+        if (z == -INFINITY) lse = others;
+        if (z == INFINITY) loss = lse = NAN;
+    }
+    if (*a.error) loss = lse = NAN;
+    a.loss[row] = static_cast<float>(loss);
+    if (a.lse) a.lse[row] = static_cast<float>(lse);
+}
+
+constexpr uint32_t kFinishThreads = 256;
+
+// kWide: 32 rows a block, a lane each, the slots spread over the warps; else a
+// row a block.
+template <bool kWide>
+__global__ void __launch_bounds__(kFinishThreads) loss_finish_kernel(LossFinishArgs a) {
+    __shared__ Joined sh[8][32];
+    pdl_wait();
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t row = kWide ? blockIdx.x * 32 + lane : blockIdx.x;
+    Joined j{-INFINITY, FF{0.0f, 0.0f}};
+    if (row < a.rows) {
+        const uint32_t step = kWide ? 8 : kFinishThreads;
+#pragma unroll 4
+        for (uint32_t i = kWide ? warp : threadIdx.x; i < a.slots; i += step) {
+            const Part p = a.parts[static_cast<uint64_t>(i) * a.rows + row];
+            j = join(j, Joined{p.m, FF{p.s, 0.0f}});
+        }
+    }
+    if (!kWide) {
+#pragma unroll
+        for (uint32_t m = 16; m > 0; m >>= 1)
+            j = join(j, Joined{__shfl_xor_sync(kFull, j.m, m), ff_shfl_xor(j.s, m)});
+    }
+    sh[warp][lane] = j;
+    __syncthreads();
+    if (warp != 0 || row >= a.rows) return;
+    for (uint32_t i = 1; i < 8; ++i) j = join(j, sh[i][lane]);
+    if (kWide || lane == 0) finish_row(a, row, j);
+}
+
+// ---------------------------------------------------------------------------
+// gradient
+// ---------------------------------------------------------------------------
+
+// f16 holds P times 2^14: entries down to 2^-28 stay normal numbers, and the
+// target's, no smaller than -1, does not overflow.
+template <typename T>
+constexpr float kProbShift = 0.0f;
+template <>
+constexpr float kProbShift<__half> = 14.0f;
+
+template <typename T, bool kPair>
+struct ProbProblem {
+    using Type = T;
+    CUtensorMap x, w, p;
+    const uint32_t* targets;
+    const float* lse;
+    const float* grad;
+    uint32_t* error;
+    uint32_t rows, V, v0, width, steps;
+    Raster raster;
+
+    __device__ __forceinline__ uint32_t count(uint32_t worker, uint32_t workers) const { return raster.share(worker, workers); }
+    __device__ __forceinline__ GemmTile tile(uint32_t worker, uint32_t workers, uint32_t j) const {
+        uint32_t m, n;
+        raster.at(worker + j * workers, m, n);
+        return {&x, &w, m * GemmConfig<kPair>::kTileM, v0 + n * kTileN, 0, 0, steps, false, false};
+    }
+    template <typename Load>
+    __device__ __forceinline__ void epilogue(const GemmTile& t, const EpiWarp& w, Load load) const {
+        const uint32_t row = t.am + w.row, col = t.bn + w.col;
+        uint32_t target = SEL_INVALID_ID;
+        float ref = 0.0f, g = 0.0f;
+        if (row < rows) {
+            target = targets[row];
+            ref = lse[row];
+            g = grad[row];
+        }
+        const bool live = target < V && g != 0.0f;
+        const float up = kProbShift<T>;
+        const uint32_t first = t.am + w.row - w.lane;
+#pragma unroll 1
+        for (uint32_t c = 0; c < 4; ++c) {
+            float v[32];
+            load(c, v);
+            const uint32_t c0 = col + 32 * c;
+            const bool mine = any_target(target, c0);
+            float z = 0.0f;
+#pragma unroll
+            for (uint32_t i = 0; i < 32; ++i) {
+                const float d = v[i] - ref;
+                if (mine && target == c0 + i) z = d;
+                v[i] = live ? ex2_approx(fmaf(d, kLog2E, up)) : 0.0f;
+            }
+            if (mine && live) {
+                z = expm1f(z) * exp2f(up);
+#pragma unroll
+                for (uint32_t i = 0; i < 32; ++i)
+                    if (target == c0 + i) v[i] = z;
+            }
+            const uint32_t x = t.bn - v0 + w.col + (c / 2) * 64;
+            store_chunk<T>(w, &p, x, first, c, x < width && first < rows, v);
+        }
+    }
+};
+
+// Items of a worker: its tiles of dX first, each a long sum, then its tiles of dW.
+template <typename T, bool kPair>
+struct GradsProblem {
+    using Type = T;
+    CUtensorMap p_mn, x_mn, dw, p_k, w_mn;
+    const float* scale;  // of dW: the largest gradient, less P's shift
+    float* acc;          // [slices][rows][H]
+    uint32_t* error;
+    uint32_t rows, V, H, v0, width;
+    uint32_t ht;                       // column tiles of both
+    uint32_t dx_tiles, dx_items, k_slice;  // k_slice: columns of P a slice sums
+    uint32_t dw_items, dw_steps, extra;    // extra: dW tiles ahead for workers with one dX tile less
+    bool add;
+
+    __device__ __forceinline__ uint32_t dx_count(uint32_t worker, uint32_t workers) const {
+        return worker < dx_items ? (dx_items - worker - 1) / workers + 1 : 0;
+    }
+    __device__ __forceinline__ uint32_t count(uint32_t worker, uint32_t workers) const {
+        const uint32_t more = dx_items % workers, light = workers - more;
+        const uint32_t rest = dw_items - extra * light;
+        const uint32_t dw = worker < rest ? (rest - worker - 1) / workers + 1 : 0;
+        return dx_count(worker, workers) + dw + (worker >= more ? extra : 0);
+    }
+    __device__ __forceinline__ GemmTile tile(uint32_t worker, uint32_t workers, uint32_t j) const {
+        constexpr uint32_t kTileM = GemmConfig<kPair>::kTileM;
+        const uint32_t n_dx = dx_count(worker, workers);
+        if (j < n_dx) {
+            const uint32_t i = worker + j * workers, slice = i / dx_tiles, at = i - slice * dx_tiles;
+            const uint32_t k0 = slice * k_slice, k1 = min(width, k0 + k_slice);
+            // (an empty slice sums one step of zeros past the piece's end)
+            const uint32_t steps = k1 > k0 ? (k1 - k0 + kStepK - 1) / kStepK : 1;
+            return {&p_k, &w_mn, at / ht * kTileM, at % ht * kTileN, k0, v0 + k0, steps, false, true};
+        }
+        const uint32_t more = dx_items % workers, light = workers - more, e = worker >= more ? extra : 0;
+        j -= n_dx;
+        const uint32_t i = j < e ? worker - more + j * light : extra * light + worker + (j - e) * workers;
+        return {&p_mn, &x_mn, i / ht * kTileM, i % ht * kTileN, 0, 0, dw_steps, true, true};
+    }
+    template <typename Load>
+    __device__ __forceinline__ void epilogue(const GemmTile& t, const EpiWarp& w, Load load) const {
+        if (t.a_mn) {
+            const float s = *scale;
+            const uint32_t first = v0 + t.am + w.row - w.lane;
+#pragma unroll 1
+            for (uint32_t c = 0; c < 4; ++c) {
+                float v[32];
+                load(c, v);
+#pragma unroll
+                for (uint32_t i = 0; i < 32; ++i) v[i] *= s;
+                const uint32_t x = t.bn + w.col + (c / 2) * 64;
+                store_chunk<T>(w, &dw, x, first, c, x < H && first < V, v);
+            }
+        } else {
+            const uint32_t row = t.am + w.row, slice = t.ak / k_slice;
+            float* o = acc + (static_cast<uint64_t>(slice) * rows + row) * H;
+#pragma unroll 1
+            for (uint32_t c = 0; c < 4; ++c) {
+                float v[32];
+                load(c, v);
+                const uint32_t x = t.bn + w.col + c * 32;
+                if (row < rows) {
+#pragma unroll
+                    for (uint32_t i = 0; i < 32; i += 4) {
+                        if (x + i >= H) break;
+                        float4* q = reinterpret_cast<float4*>(o + x + i);
+                        float4 r = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                        if (add) {
+                            const float4 b = *q;
+                            r = make_float4(r.x + b.x, r.y + b.y, r.z + b.z, r.w + b.w);
+                        }
+                        *q = r;
+                    }
+                }
+            }
+        }
+    }
+};
+
+struct PrepArgs {
+    const uint4* x;
+    uint4* scaled;  // x times grad over the largest, NULL: not wanted
+    const uint32_t* targets;
+    const float* grad;
+    float* scale;
+    uint32_t rows, V, vecs;  // vecs: of 8 entries a row
+    float down;
+};
+
+constexpr uint32_t kPrepThreads = 256;
+
+template <typename T>
+__device__ __forceinline__ void unpack2(uint32_t w, float& lo, float& hi) {
+    lo = bits_f32<T>(static_cast<uint16_t>(w));
+    hi = bits_f32<T>(static_cast<uint16_t>(w >> 16));
+}
+
+// dW's second operand: hidden rows times their gradients over the largest one, so
+// that equal gradients (a mean's) round nothing; others round each entry once
+// more. Rows that do not count are zeros, whatever they hold.
+template <typename T>
+__global__ void __launch_bounds__(kPrepThreads) grad_prep_kernel(PrepArgs a) {
+    __shared__ float sh[kPrepThreads / 32];
+    pdl_wait();
+    pdl_trigger();
+    float top = 0.0f;
+    for (uint32_t r = threadIdx.x; r < a.rows; r += kPrepThreads)
+        if (a.targets[r] < a.V) top = fmaxf(top, fabsf(a.grad[r]));
+#pragma unroll
+    for (uint32_t m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, m));
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (uint32_t i = 0; i < kPrepThreads / 32; ++i) top = fmaxf(top, sh[i]);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.scale = top * a.down;
+    const uint64_t n = static_cast<uint64_t>(a.rows) * a.vecs;
+    for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * kPrepThreads + threadIdx.x; i < n;
+         i += static_cast<uint64_t>(gridDim.x) * kPrepThreads) {
+        const uint32_t r = static_cast<uint32_t>(i / a.vecs);
+        const float g = a.grad[r];
+        uint4 q = make_uint4(0, 0, 0, 0);
+        if (a.targets[r] < a.V && g != 0.0f) {
+            q = a.x[i];
+            const float f = g / top;
+            uint32_t* p = &q.x;
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k) {
+                float lo, hi;
+                unpack2<T>(p[k], lo, hi);
+                p[k] = pack2<T>(lo * f, hi * f);
+            }
+        }
+        a.scaled[i] = q;
+    }
+}
+
+struct GradFinishArgs {
+    const float* acc;
+    const uint32_t* targets;
+    const float* grad;
+    const uint32_t* error;
+    uint4* dx;  // NULL: not wanted
+    uint4* dw;
+    uint32_t rows, V, vecs, slices;
+    float down;
+};
+
+// dX from its sums, rounded once. With the error word raised both gradients
+// become NaN.
+template <typename T>
+__global__ void __launch_bounds__(kPrepThreads) grad_finish_kernel(GradFinishArgs a) {
+    pdl_wait();
+    pdl_trigger();
+    const uint64_t n = static_cast<uint64_t>(a.rows) * a.vecs;
+    const uint64_t first = static_cast<uint64_t>(blockIdx.x) * kPrepThreads + threadIdx.x;
+    const uint64_t step = static_cast<uint64_t>(gridDim.x) * kPrepThreads;
+    const bool bad = *a.error != 0;
+    const uint32_t nan2 = pack2<T>(NAN, NAN);
+    for (uint64_t i = first; a.dx && i < n; i += step) {
+        const uint32_t r = static_cast<uint32_t>(i / a.vecs);
+        const float g = a.grad[r];
+        uint4 q = make_uint4(0, 0, 0, 0);
+        if (a.targets[r] < a.V && g != 0.0f) {
+            float s[8] = {};
+            for (uint32_t k = 0; k < a.slices; ++k) {
+                const float4* p = reinterpret_cast<const float4*>(a.acc) + 2 * (k * n + i);
+                const float4 u = p[0], v = p[1];
+                s[0] += u.x, s[1] += u.y, s[2] += u.z, s[3] += u.w;
+                s[4] += v.x, s[5] += v.y, s[6] += v.z, s[7] += v.w;
+            }
+            const float f = a.down;
+#pragma unroll
+            for (uint32_t k = 0; k < 8; ++k) s[k] = s[k] * f * g;
+            q = make_uint4(pack2<T>(s[0], s[1]), pack2<T>(s[2], s[3]), pack2<T>(s[4], s[5]), pack2<T>(s[6], s[7]));
+        }
+        if (bad) q = make_uint4(nan2, nan2, nan2, nan2);
+        a.dx[i] = q;
+    }
+    if (bad && a.dw) {
+        for (uint64_t i = first; i < static_cast<uint64_t>(a.V) * a.vecs; i += step)
+            a.dw[i] = make_uint4(nan2, nan2, nan2, nan2);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+// Up to 128 rows fill one CTA's tile; a pair's second CTA would compute nothing.
+inline bool use_pair(uint32_t rows) { return rows > kCtaM; }
+inline uint32_t tile_m(uint32_t rows) { return use_pair(rows) ? 2 * kCtaM : kCtaM; }
+
+inline bool sizes_fit(uint32_t rows, uint32_t V, uint32_t H) {
+    const uint64_t m = ceil_div(rows, kCtaM), n = ceil_div(V, kCtaM), h = ceil_div(H, kTileN);
+    return rows <= 0x7fffffffu && m * n < (1ull << 31) && n * h < (1ull << 31) && m * h * 64 < (1ull << 31);
+}
+
+struct LossPlan {
+    uint32_t nt;
+    size_t at, parts, bytes;
+};
+inline LossPlan loss_plan(uint32_t rows, uint32_t V) {
+    LossPlan p;
+    p.nt = ceil_div(V, kTileN);
+    p.at = kWsHeaderBytes;
+    p.parts = p.at + align_up(static_cast<size_t>(rows) * sizeof(float), 256);
+    p.bytes = p.parts + align_up(static_cast<size_t>(2 * p.nt) * rows * sizeof(Part), 256);
+    return p;
+}
+
+// The vocabulary in pieces: as few as keep P within 2^28 entries, but none below
+// 16,384 columns, and all alike.
+struct GradPlan {
+    uint32_t piece, pieces, slices;
+    size_t scaled, acc, p, bytes;
+};
+inline GradPlan grad_plan(uint32_t rows, uint32_t V, uint32_t H) {
+    GradPlan g;
+    const uint32_t cap = static_cast<uint32_t>(std::max<uint64_t>(16384, (1ull << 28) / rows));
+    g.piece = ceil_div(ceil_div(V, ceil_div(V, cap)), kTileN) * kTileN;
+    g.pieces = ceil_div(V, g.piece);
+    // few tiles of dX: the sum over the piece is split
+    const uint64_t tiles = static_cast<uint64_t>(ceil_div(rows, tile_m(rows))) * ceil_div(H, kTileN);
+    const uint32_t workers = use_pair(rows) ? 76 : 152;
+    g.slices = std::min(std::max(1u, g.piece / 1024), tiles >= workers ? 1u : ceil_div(workers, tiles));
+    g.scaled = kWsHeaderBytes;
+    g.acc = g.scaled + align_up(static_cast<size_t>(rows) * H * 2, 256);
+    g.p = g.acc + align_up(static_cast<size_t>(g.slices) * rows * H * sizeof(float), 256);
+    g.bytes = g.p + static_cast<size_t>(rows) * g.piece * 2;
+    return g;
+}
+
+inline bool map16(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t box_cols, uint32_t box_rows,
+                  uint64_t pitch = 0) {
+    return make_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, base, cols, rows, box_cols, box_rows, CU_TENSOR_MAP_SWIZZLE_128B,
+                    pitch);
+}
+
+struct HeadLossCall {
+    const void *x, *w;
+    const uint32_t* targets;
+    uint32_t rows, V, H;
+    unsigned char* ws;
+    cudaStream_t stream;
+};
+
+template <typename T, bool kPair>
+sel_status run_loss(const HeadLossCall& c, float* loss, float* lse) {
+    using C = GemmConfig<kPair>;
+    const int sms = device_sms();
+    if (sms <= 0) return SEL_ECUDA;
+    const LossPlan plan = loss_plan(c.rows, c.V);
+    LossProblem<T, kPair> p{};
+    if (!map16(&p.x, c.x, c.H, c.rows, kStepK, kCtaM) || !map16(&p.w, c.w, c.H, c.V, kStepK, C::kCtaN)) return SEL_ECUDA;
+    p.targets = c.targets;
+    p.at = reinterpret_cast<float*>(c.ws + plan.at);
+    p.parts = reinterpret_cast<Part*>(c.ws + plan.parts);
+    p.error = reinterpret_cast<uint32_t*>(c.ws);
+    p.rows = c.rows;
+    p.V = c.V;
+    p.steps = ceil_div(c.H, kStepK);
+    p.raster = {ceil_div(c.rows, C::kTileM), plan.nt};
+    const uint32_t workers = std::min<uint32_t>(kPair ? sms / 2 : sms, p.raster.mt * p.raster.nt);
+    if (const sel_status s = launch_gemm<LossProblem<T, kPair>, kPair>(p, workers, c.stream); s != SEL_OK) return s;
+    const LossFinishArgs f{p.parts, p.at, c.targets, p.error, loss, lse, c.rows, c.V, 2 * plan.nt};
+    const cudaError_t e = c.rows >= 64
+                              ? launch_pdl(loss_finish_kernel<true>, dim3(ceil_div(c.rows, 32)), dim3(kFinishThreads), 0, c.stream, f)
+                              : launch_pdl(loss_finish_kernel<false>, dim3(c.rows), dim3(kFinishThreads), 0, c.stream, f);
+    return e == cudaSuccess ? SEL_OK : SEL_ECUDA;
+}
+
+template <typename T, bool kPair>
+sel_status run_grad(const HeadLossCall& c, const float* lse, const float* grad, void* dx, void* dw) {
+    using C = GemmConfig<kPair>;
+    const int sms = device_sms();
+    if (sms <= 0) return SEL_ECUDA;
+    const GradPlan plan = grad_plan(c.rows, c.V, c.H);
+    auto* error = reinterpret_cast<uint32_t*>(c.ws);
+    auto* scale = reinterpret_cast<float*>(c.ws + 16);
+    auto* acc = reinterpret_cast<float*>(c.ws + plan.acc);
+    void* prob = c.ws + plan.p;
+    void* scaled = c.ws + plan.scaled;
+    const float down = 1.0f / static_cast<float>(1u << static_cast<uint32_t>(kProbShift<T>));
+    const uint32_t vecs = c.H / 8, all = kPair ? sms / 2 : sms;
+    const uint32_t blocks = static_cast<uint32_t>(std::min<uint64_t>(2 * sms, ceil_div(static_cast<uint64_t>(c.rows) * vecs, kPrepThreads)));
+    if (dw) {
+        const PrepArgs a{static_cast<const uint4*>(c.x), static_cast<uint4*>(scaled), c.targets, grad, scale, c.rows, c.V, vecs, down};
+        if (launch_pdl(grad_prep_kernel<T>, dim3(blocks), dim3(kPrepThreads), 0, c.stream, a) != cudaSuccess) return SEL_ECUDA;
+    }
+    for (uint32_t i = 0; i < plan.pieces; ++i) {
+        const uint32_t v0 = i * plan.piece, width = std::min(plan.piece, c.V - v0);
+        const uint64_t pitch = static_cast<uint64_t>(plan.piece) * 2;
+        ProbProblem<T, kPair> p{};
+        if (!map16(&p.x, c.x, c.H, c.rows, kStepK, kCtaM) || !map16(&p.w, c.w, c.H, c.V, kStepK, C::kCtaN) ||
+            !map16(&p.p, prob, width, c.rows, 64, 32, pitch))
+            return SEL_ECUDA;
+        p.targets = c.targets;
+        p.lse = lse;
+        p.grad = grad;
+        p.error = error;
+        p.rows = c.rows;
+        p.V = c.V;
+        p.v0 = v0;
+        p.width = width;
+        p.steps = ceil_div(c.H, kStepK);
+        p.raster = {ceil_div(c.rows, C::kTileM), ceil_div(width, kTileN)};
+        if (const sel_status s = launch_gemm<ProbProblem<T, kPair>, kPair>(
+                p, std::min(all, p.raster.mt * p.raster.nt), c.stream);
+            s != SEL_OK)
+            return s;
+        GradsProblem<T, kPair> g{};
+        if (!map16(&g.p_mn, prob, width, c.rows, 64, kStepK, pitch) || !map16(&g.x_mn, scaled, c.H, c.rows, 64, kStepK) ||
+            (dw && !map16(&g.dw, dw, c.H, c.V, 64, 32)) || !map16(&g.p_k, prob, width, c.rows, kStepK, kCtaM, pitch) ||
+            !map16(&g.w_mn, c.w, c.H, c.V, 64, kStepK))
+            return SEL_ECUDA;
+        g.scale = scale;
+        g.acc = acc;
+        g.error = error;
+        g.rows = c.rows;
+        g.V = c.V;
+        g.H = c.H;
+        g.v0 = v0;
+        g.width = width;
+        g.ht = ceil_div(c.H, kTileN);
+        g.dx_tiles = p.raster.mt * g.ht;
+        g.dx_items = dx ? g.dx_tiles * plan.slices : 0;
+        g.k_slice = ceil_div(ceil_div(plan.piece, plan.slices), kStepK) * kStepK;
+        g.dw_items = dw ? ceil_div(width, C::kTileM) * g.ht : 0;
+        g.dw_steps = ceil_div(c.rows, kStepK);
+        g.add = i > 0;
+        const uint32_t workers = std::min(all, g.dx_items + g.dw_items);
+        const uint32_t light = workers - g.dx_items % workers;
+        g.extra = light == workers ? 0 : std::min(g.dw_items / light, (g.k_slice / kStepK) / (g.dw_steps + 2));
+        if (const sel_status s = launch_gemm<GradsProblem<T, kPair>, kPair>(g, workers, c.stream); s != SEL_OK) return s;
+    }
+    const GradFinishArgs f{acc, c.targets, grad, error, static_cast<uint4*>(dx), static_cast<uint4*>(dw), c.rows, c.V, vecs, plan.slices, down};
+    return launch_pdl(grad_finish_kernel<T>, dim3(blocks), dim3(kPrepThreads), 0, c.stream, f) == cudaSuccess ? SEL_OK : SEL_ECUDA;
+}
+
+sel_status check_head(const void* x, const void* w, const uint32_t* targets, int dtype, uint32_t rows, uint32_t V, uint32_t H) {
+    if (dtype != SEL_F16 && dtype != SEL_BF16) return SEL_EINVAL;
+    if (V == 0 || V > SEL_MAX_V || H == 0 || H > SEL_MAX_H) return SEL_EINVAL;
+    if (H % 8 != 0) return SEL_EUNSUPPORTED;
+    if (rows == 0) return SEL_OK;
+    if (!x || !w || !targets) return SEL_EINVAL;
+    if (misaligned(x, 16) || misaligned(w, 16) || misaligned(targets, 4)) return SEL_EINVAL;
+    return sizes_fit(rows, V, H) ? SEL_OK : SEL_EUNSUPPORTED;
+}
+
+}  // namespace
+
+size_t head_loss_ws_bytes(uint32_t rows, uint32_t V, uint32_t H) {
+    if (rows == 0 || H == 0 || H > SEL_MAX_H || H % 8 != 0 || !sizes_fit(rows, V, H)) return 0;
+    return loss_plan(rows, V).bytes;
+}
+size_t head_loss_grad_ws_bytes(uint32_t rows, uint32_t V, uint32_t H) {
+    if (rows == 0 || H == 0 || H > SEL_MAX_H || H % 8 != 0 || !sizes_fit(rows, V, H)) return 0;
+    return grad_plan(rows, V, H).bytes;
+}
+
+}  // namespace sel
+
+extern "C" sel_status sel_head_loss(const void* d_hidden, uint32_t rows, const void* d_weight, int dtype, uint32_t V,
+                                    uint32_t H, const uint32_t* d_targets, float* d_loss, float* d_lse, void* d_ws,
+                                    size_t ws_bytes, cudaStream_t stream) {
+    if (const sel_status s = check_head(d_hidden, d_weight, d_targets, dtype, rows, V, H); s != SEL_OK) return s;
+    if (rows == 0) return SEL_OK;
+    if (!d_loss || misaligned(d_loss, 4) || misaligned(d_lse, 4)) return SEL_EINVAL;
+    if (!d_ws || misaligned(d_ws, SEL_WS_ALIGN)) return SEL_EINVAL;
+    if (ws_bytes < head_loss_ws_bytes(rows, V, H)) return SEL_EWORKSPACE;
+    const HeadLossCall c{d_hidden, d_weight, d_targets, rows, V, H, static_cast<unsigned char*>(d_ws), stream};
+    if (dtype == SEL_F16) return use_pair(rows) ? run_loss<__half, true>(c, d_loss, d_lse) : run_loss<__half, false>(c, d_loss, d_lse);
+    return use_pair(rows) ? run_loss<__nv_bfloat16, true>(c, d_loss, d_lse) : run_loss<__nv_bfloat16, false>(c, d_loss, d_lse);
+}
+
+extern "C" sel_status sel_head_loss_grad(const void* d_hidden, uint32_t rows, const void* d_weight, int dtype, uint32_t V,
+                                         uint32_t H, const uint32_t* d_targets, const float* d_lse, const float* d_grad,
+                                         void* d_hidden_grad, void* d_weight_grad, void* d_ws, size_t ws_bytes,
+                                         cudaStream_t stream) {
+    if (const sel_status s = check_head(d_hidden, d_weight, d_targets, dtype, rows, V, H); s != SEL_OK) return s;
+    if (misaligned(d_hidden_grad, 16) || misaligned(d_weight_grad, 16)) return SEL_EINVAL;
+    if (!d_hidden_grad && !d_weight_grad) return SEL_EINVAL;
+    if (rows == 0) {
+        if (!d_weight_grad) return SEL_OK;
+        return cudaMemsetAsync(d_weight_grad, 0, static_cast<size_t>(V) * H * 2, stream) == cudaSuccess ? SEL_OK : SEL_ECUDA;
+    }
+    if (!d_lse || !d_grad || misaligned(d_lse, 4) || misaligned(d_grad, 4)) return SEL_EINVAL;
+    if (!d_ws || misaligned(d_ws, SEL_WS_ALIGN)) return SEL_EINVAL;
+    if (ws_bytes < head_loss_grad_ws_bytes(rows, V, H)) return SEL_EWORKSPACE;
+    const HeadLossCall c{d_hidden, d_weight, d_targets, rows, V, H, static_cast<unsigned char*>(d_ws), stream};
+    if (dtype == SEL_F16)
+        return use_pair(rows) ? run_grad<__half, true>(c, d_lse, d_grad, d_hidden_grad, d_weight_grad)
+                              : run_grad<__half, false>(c, d_lse, d_grad, d_hidden_grad, d_weight_grad);
+    return use_pair(rows) ? run_grad<__nv_bfloat16, true>(c, d_lse, d_grad, d_hidden_grad, d_weight_grad)
+                          : run_grad<__nv_bfloat16, false>(c, d_lse, d_grad, d_hidden_grad, d_weight_grad);
+}
