@@ -818,6 +818,54 @@ sel_status sel_head_loss_grad(const void *d_hidden, uint32_t rows,
                               void *d_ws, size_t ws_bytes,
                               cudaStream_t stream);
 
+/*
+ * sel_distill -- the divergence of logits rows from a teacher that is known by
+ * its top logits (sel_topk's lists). With q = softmax(x / T) over the row and
+ * the list's p_i = exp(v_i / T - L):
+ *   loss = sum over the list of p_i * (ln p_i - ln q[ids_i])      (>= 0)
+ * d_teacher_lse NULL: L is the list's own ln sum exp(v_i / T), so that p sums
+ * to 1. Given, L is the teacher's over its whole row, and what the list leaves
+ * out is one more class: with r = 1 - sum p (0 where rounding makes it
+ * negative, or where the list names every id) and s the sum of q over the ids
+ * that the list does not name, the loss has r * (ln r - ln s) added.
+ * Entries whose id is >= V (SEL_INVALID_ID) are left out; a row without an
+ * entry whose value is above -Inf is ignored, with a loss of 0. A logit of -Inf
+ * is a probability of 0. A row with a NaN or +Inf logit, value or lse, with
+ * every id at -Inf, or with an id listed twice gets NaN.
+ *
+ *   d_logits       rows of V of `dtype` (any sel_dtype), row r at r * ld, aligned
+ *                  to their elements. V at most SEL_DISTILL_MAX_V
+ *   d_vals, d_ids  [rows][k] f32 and u32, any order; 1 <= k <= min(V, SEL_MAX_K)
+ *   d_teacher_lse  [rows] f32 (ln sum exp(v / T) over the teacher's row), or NULL
+ *   temperature    > 0 and finite
+ *   d_loss         [rows] f32
+ *
+ * sel_distill_grad -- the gradient of sum over r of grad[r] * loss[r] as to the
+ * logits, and the losses, in one pass:
+ *   grad[r] / T * (m * q_j - p_j) for the list's ids, m = sum p + r,
+ *   grad[r] / T * (m - r / s) * q_j for the others;
+ * zeros for ignored rows and where grad is 0; NaN in rows whose loss is NaN.
+ *
+ *   d_grad         [rows] f32
+ *   d_loss         [rows] f32, or NULL
+ *   d_logits_grad  rows of V of `dtype`, row r at r * ld_grad; may be d_logits
+ *                  itself (with ld_grad == ld). What lies between its rows is
+ *                  left as it was
+ */
+#define SEL_DISTILL_MAX_V (1u << 23)
+sel_status sel_distill(const void *d_logits, int dtype, uint32_t rows,
+                       uint32_t V, uint64_t ld, const float *d_vals,
+                       const uint32_t *d_ids, uint32_t k,
+                       const float *d_teacher_lse, float temperature,
+                       float *d_loss, cudaStream_t stream);
+sel_status sel_distill_grad(const void *d_logits, int dtype, uint32_t rows,
+                            uint32_t V, uint64_t ld, const float *d_vals,
+                            const uint32_t *d_ids, uint32_t k,
+                            const float *d_teacher_lse, float temperature,
+                            const float *d_grad, float *d_loss,
+                            void *d_logits_grad, uint64_t ld_grad,
+                            cudaStream_t stream);
+
 /* Static description of a status code. */
 const char *sel_status_string(sel_status status);
 

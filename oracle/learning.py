@@ -44,3 +44,46 @@ def head_loss_grad(x, w, targets, lse, grad):
     dx = torch.zeros_like(x64)
     dx[live] = p @ w64
     return dx, p.T @ x64[live]
+
+
+def distill(x, vals, ids, teacher_lse, temperature, grad=None):
+    """loss [n] of logits rows x [n, V] against a teacher's lists, and with `grad`
+    [n] also the gradient of sum of grad * loss as to x."""
+    n, V = x.shape
+    T = torch.tensor(temperature, dtype=torch.float32).double().item()  # the value that a call hands over
+    lq = torch.log_softmax(x.double() / T, dim=1)
+    q = lq.exp()
+    at = _in_vocabulary(ids, V)
+    loss = torch.zeros(n, dtype=torch.float64, device=x.device)
+    out = torch.zeros((n, V), dtype=torch.float64, device=x.device)
+    for r in range(n):
+        e = torch.nonzero(at[r] >= 0)[:, 0]
+        i, v = at[r, e], vals[r, e].double() / T
+        if not len(i) or (v == -INF).all():
+            continue
+        g = 1.0 if grad is None else grad[r].double()
+        L = torch.logsumexp(v, dim=0) if teacher_lse is None else teacher_lse[r].double()
+        lp = v - L
+        p = lp.exp()
+        if len(i.unique()) < len(i) or not torch.isfinite(L) or (v == INF).any() or torch.isnan(lq[r]).any():
+            loss[r] = float("nan")
+            out[r] = float("nan")
+        else:
+            some = p > 0
+            loss[r] = (p[some] * (lp[some] - lq[r, i[some]])).sum()
+            listed = torch.zeros(V, dtype=torch.bool, device=x.device)
+            listed[i] = True
+            left = torch.zeros((), dtype=torch.float64, device=x.device)
+            if teacher_lse is not None and len(i) < V:
+                left = (1.0 - p.sum()).clamp(min=0.0)
+            m = p.sum() + left
+            d = m * q[r]
+            d[i] -= p
+            if left > 0:
+                s = q[r, ~listed].sum()
+                loss[r] += left * torch.log(left / s)
+                d[~listed] = (m - left / s) * q[r, ~listed] if s > 0 else 0.0
+            out[r] = g / T * d
+        if grad is not None and g == 0:
+            out[r] = 0.0
+    return loss if grad is None else (loss, out)

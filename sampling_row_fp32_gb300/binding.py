@@ -33,7 +33,7 @@ EXPORTED = ("sel_workspace_bytes", "sel_workspace_init", "sel_argmax", "sel_topk
             "spec_accept_sampler", "spec_diagnostics", "sel_topk_stats", "sel_shard_draw_mass",
             "sel_shard_draw", "spec_shard_stats", "spec_accept_shards", "spec_shard_draw_mass",
             "spec_shard_draw", "sel_head_w4", "sel_sample16", "sel_embed", "sel_embed_w4",
-            "sel_head_loss", "sel_head_loss_grad")
+            "sel_head_loss", "sel_head_loss_grad", "sel_distill", "sel_distill_grad")
 SEL_F32, SEL_F16, SEL_BF16 = range(3)
 SEL_MAX_H = 1 << 20
 SEL_SAMPLE16_MAX_V = 524_208
@@ -147,6 +147,10 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.sel_head_loss.restype = _i
     lib.sel_head_loss_grad.argtypes = [_vp, _u32, _vp, _i, _u32, _u32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
     lib.sel_head_loss_grad.restype = _i
+    lib.sel_distill.argtypes = [_vp, _i, _u32, _u32, _u64, _vp, _vp, _u32, _vp, _f, _vp, _vp]
+    lib.sel_distill.restype = _i
+    lib.sel_distill_grad.argtypes = [_vp, _i, _u32, _u32, _u64, _vp, _vp, _u32, _vp, _f, _vp, _vp, _vp, _u64, _vp]
+    lib.sel_distill_grad.restype = _i
     lib.sel_status_string.argtypes = [ctypes.c_int]
     lib.sel_status_string.restype = ctypes.c_char_p
     if path is None:
@@ -647,6 +651,52 @@ def sel_head_loss_grad(hidden, weight, targets, lse, grad, hidden_grad, weight_g
                                                None if weight_grad is None else weight_grad.data_ptr(),
                                                _workspace(ws), _nbytes(ws), _on_stream(stream, dev)),
            "sel_head_loss_grad")
+
+
+def _lists(vals, ids, rows: int) -> int:
+    """k of a teacher's lists: vals f32 and ids int32/uint32, both [rows, k]."""
+    if vals.dtype != torch.float32 or vals.dim() != 2 or vals.shape[0] != rows or not vals.is_contiguous():
+        raise ValueError("vals must be contiguous float32 [rows, k]")
+    if ids.dtype not in _IDS or ids.shape != vals.shape or not ids.is_contiguous():
+        raise ValueError("ids must be contiguous int32 or uint32 [rows, k]")
+    if vals.shape[1] > _U32_MAX:
+        raise ValueError("lists must have fewer than 2^32 entries")
+    return vals.shape[1]
+
+
+def sel_distill(logits, vals, ids, teacher_lse, temperature: float, loss, stream=None) -> None:
+    """logits [rows, V] f32/f16/bf16 (rows may be padded), a teacher's lists vals
+    f32 and ids int32/uint32 [rows, k], teacher_lse f32 [rows] or None -> loss
+    f32 [rows]."""
+    dev = _device(logits, vals, ids, teacher_lse, loss)
+    rows, V, ld = _rows_2d(logits, "logits")
+    if logits.dtype not in _DTYPES:
+        raise ValueError("logits must be f32, f16 or bf16")
+    k = _lists(vals, ids, rows)
+    f32 = (torch.float32,)
+    _check((_lib or load()).sel_distill(logits.data_ptr(), _DTYPES[logits.dtype], rows, V, ld, vals.data_ptr(),
+                                        ids.data_ptr(), k, _vector(teacher_lse, rows, f32, "teacher_lse"),
+                                        float(temperature), _vector(loss, rows, f32, "loss"),
+                                        _on_stream(stream, dev)), "sel_distill")
+
+
+def sel_distill_grad(logits, vals, ids, teacher_lse, temperature: float, grad, loss, logits_grad, stream=None) -> None:
+    """sel_distill's arguments, grad f32 [rows] -> loss f32 [rows] (or None) and
+    logits_grad [rows, V] of the logits' type (rows may be padded; may be logits)."""
+    dev = _device(logits, vals, ids, teacher_lse, grad, loss, logits_grad)
+    rows, V, ld = _rows_2d(logits, "logits")
+    if logits.dtype not in _DTYPES:
+        raise ValueError("logits must be f32, f16 or bf16")
+    out_rows, out_V, out_ld = _rows_2d(logits_grad, "logits_grad")
+    if logits_grad.dtype != logits.dtype or (out_rows, out_V) != (rows, V):
+        raise ValueError("logits_grad must have the shape and type of logits")
+    k = _lists(vals, ids, rows)
+    f32 = (torch.float32,)
+    _check((_lib or load()).sel_distill_grad(logits.data_ptr(), _DTYPES[logits.dtype], rows, V, ld, vals.data_ptr(),
+                                             ids.data_ptr(), k, _vector(teacher_lse, rows, f32, "teacher_lse"),
+                                             float(temperature), _vector(grad, rows, f32, "grad"),
+                                             _vector(loss, rows, f32, "loss"), logits_grad.data_ptr(), out_ld,
+                                             _on_stream(stream, dev)), "sel_distill_grad")
 
 
 # ---------------------------------------------------------------------------
