@@ -103,9 +103,14 @@ struct LossProblem {
             top = fmaxf(top, v[31]);
             const float m = fmaxf(p.m, ceilf(top * kLog2E));
             const float ref = m == -INFINITY ? 0.0f : m;
+            // The product z log2(e) is not rounded before the subtraction, but where
+            // its rounding is no longer small next to 1 it has to be: then the
+            // largest is m itself.
+            const bool big = fabsf(ref) >= 1048576.0f;
+            const float k0 = big ? kLog2E : 1.0f, k1 = big ? 1.0f : kLog2E;
             float s[4] = {p.s * pow2(p.m - ref), 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (uint32_t i = 0; i < 32; ++i) s[i % 4] += ex2_approx(fmaf(v[i], kLog2E, -ref));
+            for (uint32_t i = 0; i < 32; ++i) s[i % 4] += ex2_approx(fmaf(v[i] * k0, k1, -ref));
             p.m = m;
             p.s = (s[0] + s[1]) + (s[2] + s[3]);
         }
