@@ -852,7 +852,7 @@ sel_status sel_head_loss_grad(const void *d_hidden, uint32_t rows,
  *                  itself (with ld_grad == ld). What lies between its rows is
  *                  left as it was
  */
-#define SEL_DISTILL_MAX_V (1u << 23)
+#define SEL_DISTILL_MAX_V (1u << 20)
 sel_status sel_distill(const void *d_logits, int dtype, uint32_t rows,
                        uint32_t V, uint64_t ld, const float *d_vals,
                        const uint32_t *d_ids, uint32_t k,

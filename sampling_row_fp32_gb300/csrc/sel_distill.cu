@@ -8,13 +8,20 @@
 //   d loss / d x_j = (m q_j - p_j) / T listed, (m - r / s) q_j / T unlisted,
 //   m = sum p + r
 //
-// One cluster of C CTAs per row, each with a share of its vectors. A CTA marks the
-// list's ids that fall in its share in a bitmap (an id marked twice is a repeated
-// one), so that the unlisted sum leaves them out instead of subtracting them:
-// lists hold nearly all of a peaked row, and 1 - sum q_i would be rounding. The
-// shares' sums meet through distributed shared memory, joined in the shares'
-// order; then the gradient is written from a second read of the share, which L2
-// still holds, and the listed ids' entries after it.
+// Clusters of C CTAs walk the rows, each CTA with a share of a row's vectors. Warp
+// roles:
+//   warp 8     reads the list for the teacher's normaliser and mass, and copies the
+//              share into a ring of shared-memory chunks; it runs ahead, into the
+//              next row as its chunks become free
+//   warps 0-7  mark the list's ids that fall in the share in a bitmap (an id marked
+//              twice is a repeated one), sum the share's weights, exchange the sums
+//              with the row's other CTAs, and write the gradient from the same
+//              chunks, then the listed ids' entries
+// The bitmap leaves listed ids out of the unlisted sum instead of subtracting them:
+// lists hold nearly all of a peaked row, and 1 - sum q_i would be rounding. Sums
+// meet as messages between the warps of the cluster (st.async), joined in one
+// order; no barrier of the cluster stands between a row and the next. Every wait is
+// bounded; one that runs out makes the CTA's rows NaN.
 #include <algorithm>
 #include <type_traits>
 
@@ -22,7 +29,9 @@
 
 #include "sel_common.cuh"
 #include "sel_dtype.cuh"
+#include "sel_per_device.h"
 #include "sel_plan.h"
+#include "sel_tma.cuh"
 #include "sel_units.cuh"
 
 using namespace sel;
@@ -30,9 +39,10 @@ using namespace sel;
 namespace sel {
 namespace {
 
-constexpr uint32_t kNT = 256, kWarps = kNT / 32, kMaxC = 8;
+constexpr uint32_t kNT = 256, kWarps = kNT / 32, kThreads = kNT + 32, kMaxC = 8;
 constexpr uint32_t kEntries = SEL_MAX_K / kNT;  // of a list, a thread
 constexpr uint32_t kBatch = 4;                  // vectors a thread takes at a time
+constexpr uint32_t kChunkVecs = kBatch * kNT, kChunkBytes = 16 * kChunkVecs, kMaxSlots = 13;
 constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct DistillArgs {
@@ -44,7 +54,9 @@ struct DistillArgs {
     float* loss;
     void* out;
     uint64_t ld, ld_out;
-    uint32_t V, k, C, share;  // share: vectors a CTA
+    uint32_t rows, V, k;
+    uint32_t C, share, slots;  // CTAs a row, vectors and chunks a CTA
+    bool resident;             // a share's chunks stay until its gradient is written
     float kf, kl;             // log2(e) / T as a sum of two floats
     float inv_t;
 };
@@ -220,23 +232,22 @@ struct Share {
         if (threadIdx.x < heads) return head + threadIdx.x;
         return threadIdx.x < heads + tails ? tail + (threadIdx.x - heads) : -1;
     }
-    template <uint32_t kB>
-    __device__ __forceinline__ void load(uint32_t i0, Vec<T> (&q)[kB]) const {
-#pragma unroll
-        for (uint32_t u = 0; u < kB; ++u) {
-            const uint4 t = *reinterpret_cast<const uint4*>(vec + i0 + u * kNT);
-            q[u].w[0] = t.x, q[u].w[1] = t.y, q[u].w[2] = t.z, q[u].w[3] = t.w;
-        }
-    }
+};
+
+// What the teacher's list comes to. norm: log2 of its normaliser over its largest
+// value `top`; left: r; mass: the sum of p and r (NaN fails the row).
+struct Teacher {
+    float top, norm, left, mass;
+    uint32_t live;
 };
 
 struct Shared {
-    Sums warps[kWarps];
-    float losses[kWarps];
-    float teacher[3];        // the list's largest value, log2 of its normaliser, sum p
-    Sums table[kMaxC];       // every CTA's sums
-    float row_losses[kMaxC];
-    uint32_t twice;
+    alignas(16) float4 table[2][kMaxC * kWarps];  // sums of every warp of the cluster
+    float losses[2][kMaxC * kWarps];
+    Teacher teacher[2];
+    uint64_t full[kMaxSlots], empty[kMaxSlots];
+    uint64_t t_full[2], t_empty[2], sums[2], loss[2];
+    uint32_t err;
 };
 
 __device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
@@ -244,16 +255,41 @@ __device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
     return r;
 }
-__device__ __forceinline__ void st_peer(uint32_t a, uint32_t v) {
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+// Stores into a CTA of the cluster, counted on a barrier there.
+__device__ __forceinline__ void send(uint32_t to, uint32_t bar, float a, float b, float c) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
+                 "r"(__float_as_uint(a)), "r"(__float_as_uint(b)), "r"(__float_as_uint(c)), "r"(0u), "r"(bar)
+                 : "memory");
 }
-__device__ __forceinline__ void cluster_sync(uint32_t C) {
-    if (C > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-    else __syncthreads();
+__device__ __forceinline__ void send(uint32_t to, uint32_t bar, float a) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(to),
+                 "r"(__float_as_uint(a)), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(kSuspendNs)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ void wait_cluster(uint64_t* bar, uint32_t parity, volatile uint32_t* err) {
+    bool ok = try_wait_cluster(bar, parity);
+    for (uint32_t i = 0; !ok && i < kWaitPolls && !*err; ++i) ok = try_wait_cluster(bar, parity);
+    if (!ok) *err = 1;
+    __syncwarp();
+}
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kNT) : "memory"); }
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// log2 of a listed value's probability. `lh`: log2 of the list's normaliser over its
-// largest value `top`; or with the teacher's own lse, log2(e) of it as lh + ll.
+// log2 of a listed value's probability; with the teacher's own lse, log2(e) of that
+// is lh + ll.
 struct LogP {
     float kf, kl, top, lh, ll;
     bool given;
@@ -261,10 +297,61 @@ struct LogP {
         if (v == -INFINITY) return v;
         return given ? fmaf(v, kf, -lh) + fmaf(v, kl, -ll) : (v - top) * kf - lh;
     }
+    __device__ __forceinline__ LogP(const DistillArgs& a, uint32_t row) {
+        kf = a.kf;
+        kl = a.kl;
+        top = lh = ll = 0.0f;
+        given = a.teacher_lse != nullptr;
+        if (given) {
+            const float l = a.teacher_lse[row];
+            lh = l * kLog2E;
+            ll = fmaf(l, kLog2E, -lh) + l * 1.9259629911e-8f;  // (log2(e) less its float)
+            if (!(fabsf(l) < INFINITY)) lh = NAN;
+        }
+    }
 };
 
-// This thread's sums over whole vectors and over single entries. Vector i's bits
-// of the list are byte i (f32: half a byte).
+// By one warp.
+__device__ __forceinline__ Teacher read_teacher(const DistillArgs& a, uint32_t row) {
+    const uint32_t lane = threadIdx.x & 31;
+    const float* vals = a.vals + static_cast<uint64_t>(row) * a.k;
+    const uint32_t* ids = a.ids + static_cast<uint64_t>(row) * a.k;
+    const LogP log_p(a, row);
+    float top = -INFINITY;
+    uint32_t named = 0;
+    bool nan = false;
+#pragma unroll 4
+    for (uint32_t i = lane; i < a.k; i += 32) {
+        const uint32_t id = ids[i];
+        const float v = vals[i];
+        if (id >= a.V) continue;
+        ++named;
+        nan |= !(v < INFINITY);
+        top = fmaxf(top, v);
+    }
+    top = warp_max(top);
+    named = __reduce_add_sync(kFull, named);
+    nan = __any_sync(kFull, nan);
+    FF w{0.0f, 0.0f};
+#pragma unroll 4
+    for (uint32_t i = lane; i < a.k; i += 32) {
+        const uint32_t id = ids[i];
+        const float v = vals[i];
+        if (id < a.V) w = ff_add(w, FF{exp2f(log_p.given ? log_p(v) : (v - top) * a.kf), 0.0f});
+    }
+    w = ff_warp_sum(w);
+    Teacher t{top, 0.0f, 0.0f, 1.0f, nan || top > -INFINITY};
+    if (log_p.given) {
+        t.left = named == a.V ? 0.0f : fmaxf(0.0f, (1.0f - w.hi) - w.lo);
+        if (t.left == 0.0f) t.mass = w.hi + w.lo;
+    } else {
+        t.norm = log2f(w.hi + w.lo);
+    }
+    if (nan || isnan(w.hi)) t.mass = NAN;
+    return t;
+}
+
+// This thread's sums. Vector i's bits of the list are byte i (f32: half a byte).
 template <typename T>
 struct Summer {
     const uint32_t* bits;
@@ -310,56 +397,6 @@ struct Summer {
     }
 };
 
-// One number of every CTA of the row, in every CTA. (Its first barrier: the table
-// is no longer read.)
-__device__ __forceinline__ void exchange(Shared& s, uint32_t rank, uint32_t C, Sums v) {
-    cluster_sync(C);
-    if (threadIdx.x < C) {
-        const uint32_t p = peer_addr(&s.table[rank], threadIdx.x);
-        st_peer(p, __float_as_uint(v.m));
-        st_peer(p + 4, __float_as_uint(v.rest));
-        st_peer(p + 8, __float_as_uint(v.list));
-    }
-    __syncwarp();
-    cluster_sync(C);
-}
-
-// The row's largest logit and the sums of 2^((x - it) kf), for rows whose logits are
-// too large, or all too small, for whole-number references.
-template <typename T>
-__device__ __noinline__ Sums slow_sums(Shared& s, const uint32_t* bits, const Share<T>& x, uint32_t V, uint32_t rank,
-                                       uint32_t C, float kf) {
-    const uint32_t warp = threadIdx.x / 32;
-    const int64_t lo = max(x.base, static_cast<int64_t>(0)), hi = min(x.base + x.span, static_cast<int64_t>(V));
-    float m = -INFINITY;
-    for (int64_t i = lo + threadIdx.x; i < hi; i += kNT) m = fmaxf(m, to_f32(x.row[i]));
-    m = warp_max(m);
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) s.warps[warp].m = m;
-    __syncthreads();
-    for (uint32_t i = 0; i < kWarps; ++i) m = fmaxf(m, s.warps[i].m);
-    exchange(s, rank, C, Sums{m, 0.0f, 0.0f});
-    for (uint32_t i = 0; i < C; ++i) m = fmaxf(m, s.table[i].m);
-    float rest = 0.0f, list = 0.0f;
-    for (int64_t i = lo + threadIdx.x; i < hi; i += kNT) {
-        const uint32_t off = static_cast<uint32_t>(i - x.base);
-        const float e = ex2_approx((to_f32(x.row[i]) - m) * kf);  // (NaN where the row's largest is infinite)
-        if (bits[off >> 5] >> (off & 31) & 1) list += e;
-        else rest += e;
-    }
-    rest = warp_sum(rest);
-    list = warp_sum(list);
-    if (threadIdx.x % 32 == 0) s.warps[warp] = {m, rest, list};
-    __syncthreads();
-    rest = list = 0.0f;
-    for (uint32_t i = 0; i < kWarps; ++i) rest += s.warps[i].rest, list += s.warps[i].list;
-    if (s.twice) rest = NAN;
-    exchange(s, rank, C, Sums{m, rest, list});
-    rest = list = 0.0f;
-    for (uint32_t i = 0; i < C; ++i) rest += s.table[i].rest, list += s.table[i].list;
-    return {m, rest, list};
-}
-
 template <typename T, bool kAligned>
 __device__ __forceinline__ void store_vec(T* to, const Vec<T>& q) {
     if constexpr (kAligned) {
@@ -372,269 +409,442 @@ __device__ __forceinline__ void store_vec(T* to, const Vec<T>& q) {
     }
 }
 
-// The share's gradient but for the listed ids: factor * 2^(x kf - m), over the loads
-// that a first batch already has.
-template <typename T, bool kAligned>
-__device__ __forceinline__ void write_share(const Share<T>& x, T* out, float kf, float m, float factor) {
-    constexpr uint32_t kN = Vec<T>::kN;
-    const Pair k(kf, kf), r(-m, -m), f(factor, factor);
-    T* to = out + x.base;
-    auto write = [&](uint32_t i0, auto& q) {
+// factor * 2^(x kf - m) for some vectors, to where they go.
+template <typename T, bool kAligned, uint32_t kB>
+__device__ __forceinline__ void write_vecs(T* to, Vec<T> (&q)[kB], Pair k, Pair r, Pair f) {
 #pragma unroll
-        for (uint32_t u = 0; u < sizeof(q) / 16; ++u) {
+    for (uint32_t u = 0; u < kB; ++u) {
 #pragma unroll
-            for (uint32_t j = 0; j < Vec<T>::kPairs; ++j) {
-                float e0, e1;
-                fma2(q[u].pair(j), k, r).get(e0, e1);
-                q[u].set(j, mul2(Pair(ex2_approx(e0), ex2_approx(e1)), f));
-            }
-            store_vec<T, kAligned>(to + static_cast<uint64_t>(i0 + u * kNT) * kN, q[u]);
+        for (uint32_t j = 0; j < Vec<T>::kPairs; ++j) {
+            float e0, e1;
+            fma2(q[u].pair(j), k, r).get(e0, e1);
+            q[u].set(j, mul2(Pair(ex2_approx(e0), ex2_approx(e1)), f));
         }
-    };
-    uint32_t i = x.w0 + threadIdx.x;
-    for (; i + (kBatch - 1) * kNT < x.w1; i += kBatch * kNT) {
-        Vec<T> q[kBatch];
-        x.load(i, q);
-        write(i, q);
-    }
-    for (; i < x.w1; i += kNT) {
-        Vec<T> q[1];
-        x.load(i, q);
-        write(i, q);
+        store_vec<T, kAligned>(to + u * kNT * Vec<T>::kN, q[u]);
     }
 }
 
+// A place in the ring of chunks.
+struct Place {
+    uint32_t slot = 0, phase = 0;
+    __device__ __forceinline__ void next(uint32_t slots) {
+        if (++slot == slots) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+// The eight warps that work on the rows.
 template <typename T, bool kGrad>
-__global__ void __launch_bounds__(kNT, 4) distill_kernel(DistillArgs a) {
-    constexpr uint32_t kN = Vec<T>::kN;
-    extern __shared__ uint32_t bits[];
-    __shared__ Shared s;
-    const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, C = a.C;
-    const uint32_t row = blockIdx.x / C, rank = blockIdx.x - row * C;
-    const uint32_t words = (a.share * kN + 31) / 32;
-    for (uint32_t i = tid; i < words; i += kNT) bits[i] = 0;
-    if (tid == 0) s.twice = 0;
-    // (a peer's memory is written only once the peer runs)
-    if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-    pdl_wait();
-    pdl_trigger();
-    const Share<T> x(a.x, row * a.ld, a.V, rank, a.share);
-    const float* vals = a.vals + static_cast<uint64_t>(row) * a.k;
-    const uint32_t* ids = a.ids + static_cast<uint64_t>(row) * a.k;
-    T* out = kGrad ? static_cast<T*>(a.out) + row * a.ld_out : nullptr;
-    auto zeros = [&] {
+struct Worker {
+    const DistillArgs& a;
+    Shared& s;
+    const unsigned char* ring;
+    uint32_t* bitmaps;  // two, of `words` each
+    uint32_t words, rank, tid, lane, warp;
+    Place at;
+    uint32_t messages = 0;  // exchanges so far
+
+    // The sums of all of the row's warps.
+    __device__ __forceinline__ Sums exchange(Sums z) {
+        const uint32_t p = messages & 1;
+        if (tid == 0) expect_tx(&s.sums[p], a.C * kWarps * 16);
+        z = warp_join(z);
+        if (lane < a.C) send(peer_addr(&s.table[p][rank * kWarps + warp], lane), peer_addr(&s.sums[p], lane), z.m, z.rest, z.list);
+        wait_cluster(&s.sums[p], messages >> 1 & 1, &s.err);
+        ++messages;
+        z = {-INFINITY, 0.0f, 0.0f};
+        for (uint32_t i = lane; i < a.C * kWarps; i += 32) {
+            const float4 o = s.table[p][i];
+            const float m = fmaxf(z.m, o.x), f = pow2(z.m - m), g = pow2(o.x - m);
+            z = {m, z.rest * f + o.y * g, z.list * f + o.z * g};
+        }
+        return warp_join(z);
+    }
+    template <uint32_t kB>
+    __device__ __forceinline__ void read(uint32_t j, Vec<T> (&q)[kB]) const {
+        const auto* src = reinterpret_cast<const uint4*>(ring + at.slot * kChunkBytes) + j;
+#pragma unroll
+        for (uint32_t u = 0; u < kB; ++u) {
+            const uint4 t = src[u * kNT];
+            q[u].w[0] = t.x, q[u].w[1] = t.y, q[u].w[2] = t.z, q[u].w[3] = t.w;
+        }
+    }
+    __device__ __forceinline__ void release() {
+        __syncwarp();
+        if (lane == 0) arrive(&s.empty[at.slot]);
+        at.next(a.slots);
+    }
+    // Chunks that nobody reads.
+    __device__ __forceinline__ void skip(uint32_t chunks) {
+        for (uint32_t c = 0; c < chunks; ++c) {
+            wait(&s.full[at.slot], at.phase, &s.err);
+            release();
+        }
+    }
+    // f(j, q): vectors j + 256 u of the share's whole ones, all of a chunk's four or
+    // one at a time.
+    template <typename F>
+    __device__ __forceinline__ void chunk(uint32_t first, uint32_t vecs, F f) const {
+        if (first + kChunkVecs <= vecs) {
+            Vec<T> q[kBatch];
+            read(tid, q);
+            f(first + tid, q);
+        } else {
+            for (uint32_t j = tid; first + j < vecs; j += kNT) {
+                Vec<T> q[1];
+                read(j, q);
+                f(first + j, q);
+            }
+        }
+    }
+    __device__ __forceinline__ void zeros(const Share<T>& x, T* out) const {
         const int64_t lo = max(x.base, static_cast<int64_t>(0)), hi = min(x.base + x.span, static_cast<int64_t>(a.V));
         for (int64_t i = lo + tid; i < hi; i += kNT) out[i] = from_f32<T>(0.0f);
-    };
-    uint32_t i0 = x.w0 + tid;
-    const bool ahead = i0 + (kBatch - 1) * kNT < x.w1;
-    Vec<T> q[kBatch];
-    if (ahead) x.load(i0, q);  // on their way while the list is read
-    const int64_t single = x.single();
-    const float alone = single >= 0 ? to_f32(x.row[single]) : -INFINITY;
-    if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    else __syncthreads();
-
-    // The list: entries of this thread that this share holds, marked in the bitmap.
-    uint32_t id[kEntries];
-    float val[kEntries], at[kEntries];
-    bool some = false;
-#pragma unroll
-    for (uint32_t e = 0; e < kEntries; ++e) {
-        const uint32_t i = tid + e * kNT;
-        id[e] = SEL_INVALID_ID;
-        val[e] = -INFINITY;
-        at[e] = -INFINITY;
-        if (i >= a.k) continue;
-        const uint32_t n = ids[i];
-        if (n >= a.V) continue;
-        val[e] = vals[i];
-        some |= !(val[e] == -INFINITY);
-        const int64_t off = static_cast<int64_t>(n) - x.base;
-        if (off < 0 || off >= x.span) continue;
-        id[e] = n;
-        at[e] = to_f32(x.row[n]);
-        const uint32_t bit = 1u << (off & 31);
-        if (atomicOr(&bits[off >> 5], bit) & bit) s.twice = 1;
     }
-    // (the same in every CTA of the row)
-    if (!__syncthreads_or(some)) {
-        if (rank == 0 && tid == 0 && a.loss) a.loss[row] = 0.0f;
-        if constexpr (kGrad) zeros();
-        return;
+    template <bool kAligned>
+    __device__ __forceinline__ void write_share(const Share<T>& x, T* out, float m, float factor, uint32_t vecs) {
+        const Pair k(a.kf, a.kf), r(-m, -m), f(factor, factor);
+        T* to = out + (x.base + static_cast<int64_t>(x.w0) * Vec<T>::kN);
+        for (uint32_t first = 0; first < vecs; first += kChunkVecs) {
+            if (!a.resident) wait(&s.full[at.slot], at.phase, &s.err);
+            chunk(first, vecs, [&](uint32_t j, auto& q) { write_vecs<T, kAligned>(to + static_cast<uint64_t>(j) * Vec<T>::kN, q, k, r, f); });
+            release();
+        }
+    }
+    // The row's largest logit and the sums of 2^((x - it) kf), for rows whose logits
+    // are too large, or all too small, for whole-number references.
+    __device__ __forceinline__ Sums slow_sums(const Share<T>& x, const uint32_t* bits, bool twice) {
+        const int64_t lo = max(x.base, static_cast<int64_t>(0)), hi = min(x.base + x.span, static_cast<int64_t>(a.V));
+        float m = -INFINITY;
+        for (int64_t i = lo + tid; i < hi; i += kNT) m = fmaxf(m, to_f32(x.row[i]));
+        m = exchange(Sums{m, 0.0f, 0.0f}).m;
+        float rest = twice ? NAN : 0.0f, list = 0.0f;
+        for (int64_t i = lo + tid; i < hi; i += kNT) {
+            const uint32_t off = static_cast<uint32_t>(i - x.base);
+            const float e = ex2_approx((to_f32(x.row[i]) - m) * a.kf);  // (NaN where the row's largest is infinite)
+            if (bits[off >> 5] >> (off & 31) & 1) list += e;
+            else rest += e;
+        }
+        return exchange(Sums{m, rest, list});
     }
 
-    // The teacher's normaliser and mass, by one warp that has time for it.
-    const bool given = a.teacher_lse != nullptr;
-    LogP log_p{a.kf, a.kl, 0.0f, 0.0f, 0.0f, given};
-    if (given) {
-        const float l = a.teacher_lse[row];
-        log_p.lh = l * kLog2E;
-        log_p.ll = fmaf(l, kLog2E, -log_p.lh) + l * 1.9259629911e-8f;  // (log2(e) less its float)
-        if (!(fabsf(l) < INFINITY)) log_p.lh = NAN;
-    }
-    if (warp == kWarps - 1) {
-        float top = -INFINITY;
-        uint32_t named = 0;
-        bool nan = false;
-        for (uint32_t i = lane; i < a.k; i += 32) {
-            if (ids[i] >= a.V) continue;
-            ++named;
-            nan |= !(vals[i] < INFINITY);
-            top = fmaxf(top, vals[i]);
-        }
-        top = warp_max(top);
-        named = __reduce_add_sync(kFull, named);
-        nan = __any_sync(kFull, nan);
-        FF w{0.0f, 0.0f};
-        for (uint32_t i = lane; i < a.k; i += 32)
-            if (ids[i] < a.V) w = ff_add(w, FF{exp2f(given ? log_p(vals[i]) : (vals[i] - top) * a.kf), 0.0f});
-        w = ff_warp_sum(w);
-        float left = 0.0f, mass = 1.0f;  // r, and the sum of p and r
-        if (given) {
-            left = named == a.V ? 0.0f : fmaxf(0.0f, (1.0f - w.hi) - w.lo);
-            if (left == 0.0f) mass = w.hi + w.lo;
-        }
-        if (nan || isnan(w.hi)) mass = NAN;
-        if (lane == 0) {
-            s.teacher[0] = top;
-            s.teacher[1] = given ? left : log2f(w.hi + w.lo);
-            s.teacher[2] = mass;
-        }
-    }
-
-    // This share's sums.
-    Summer<T> mine{bits, a.kf, -kHuge, 0.0f};
-    if (ahead) {
-        while (true) {
-            mine.add(i0, q);
-            i0 += kBatch * kNT;
-            if (i0 + (kBatch - 1) * kNT >= x.w1) break;
-            x.load(i0, q);
-        }
-    }
-    for (; i0 < x.w1; i0 += kNT) {
-        Vec<T> one[1];
-        x.load(i0, one);
-        mine.add(i0, one);
-    }
-    if (single >= 0) {
-        const uint32_t off = static_cast<uint32_t>(single - x.base);
-        if (!(bits[off >> 5] >> (off & 31) & 1)) mine.add_one(alone);
-    }
-    Sums z{mine.m, mine.sum, 0.0f};
+    __device__ __forceinline__ void run(uint32_t first_row, uint32_t step) {
+        // of the row before: what its loss still needs, and listed entries to write
+        uint32_t pending = 0, pending_row = 0, lives = 0;
+        float p_left = 0.0f, p_rest = 0.0f, p_log_z = 0.0f, p_mass = 0.0f;
+        T* p_out = nullptr;
+        uint32_t id[kEntries];
+        float grads[kEntries];
 #pragma unroll
-    for (uint32_t e = 0; e < kEntries; ++e) {
-        if (id[e] == SEL_INVALID_ID) continue;
-        const float n = fmaxf(z.m, ceilf(at[e] * a.kf)), f = pow2(z.m - n);
-        z = {n, z.rest * f, z.list * f + ex2_approx(fmaf(at[e], a.kf, -n))};
-    }
-    z = warp_join(z);
-    if (lane == 0) s.warps[warp] = z;
-    __syncthreads();
-    if (warp == 0) {
-        z = warp_join(lane < kWarps ? s.warps[lane] : Sums{-kHuge, 0.0f, 0.0f});
-        if (s.twice) z.rest = NAN;
-        if (lane < C) {
-            const uint32_t p = peer_addr(&s.table[rank], lane);
-            st_peer(p, __float_as_uint(z.m));
-            st_peer(p + 4, __float_as_uint(z.rest));
-            st_peer(p + 8, __float_as_uint(z.list));
-        }
-    }
-    __syncwarp();
-    cluster_sync(C);
-    z = {-kHuge, 0.0f, 0.0f};
-    for (uint32_t i = 0; i < C; ++i) z.m = fmaxf(z.m, s.table[i].m);
-    for (uint32_t i = 0; i < C; ++i) {
-        const float f = pow2(s.table[i].m - z.m);
-        z.rest += s.table[i].rest * f;
-        z.list += s.table[i].list * f;
-    }
-    // (the same in every CTA of the row)
-    const bool slow = !(fabsf(z.m) < kHuge);
-    if (slow) z = slow_sums(s, bits, x, a.V, rank, C, a.kf);
-    const float total = z.rest + z.list, log_z = log2f(total);
-    auto exponent = [&](float v) { return slow ? (v - z.m) * a.kf : fmaf(v, a.kf, -z.m); };
-    float left = 0.0f;
-    const float mass = s.teacher[2];
-    log_p.top = s.teacher[0];
-    if (given) left = s.teacher[1];
-    else log_p.lh = s.teacher[1];
-
-    const float grad = kGrad ? a.grad[row] : 0.0f, g = grad * a.inv_t;
-    float part = 0.0f;
+        for (uint32_t e = 0; e < kEntries; ++e) id[e] = SEL_INVALID_ID;
+        auto finish = [&] {  // by the first warp of the row's first CTA
+            const uint32_t p = (pending - 1) & 1;
+            wait_cluster(&s.loss[p], (pending - 1) >> 1 & 1, &s.err);
+            float loss = 0.0f;
+            for (uint32_t i = lane; i < a.C * kWarps; i += 32) loss += s.losses[p][i];
+            loss = warp_sum(loss);
+            if (p_left != 0.0f) loss += p_left * (log2f(p_left) - (log2f(p_rest) - p_log_z));
+            if (lane == 0) a.loss[pending_row] = p_mass == p_mass && !s.err ? loss * kLn2 : NAN;
+        };
+        auto scatter = [&] {
+            if constexpr (kGrad) {
 #pragma unroll
-    for (uint32_t e = 0; e < kEntries; ++e) {
-        if (id[e] == SEL_INVALID_ID) continue;
-        const float lp = log_p(val[e]), y = exponent(at[e]), p = exp2f(lp);
-        if (p != 0.0f) part += p * (lp - (y - log_z));
-        if (kGrad) at[e] = g * (mass * (ex2_approx(y) / total) - p);
-    }
-    part = warp_sum(part);
-    if (lane == 0) s.losses[warp] = part;
-    __syncthreads();
-    if (a.loss && tid == 0) {
-        part = 0.0f;
-#pragma unroll
-        for (uint32_t i = 0; i < kWarps; ++i) part += s.losses[i];
-        st_peer(peer_addr(&s.row_losses[rank], 0), __float_as_uint(part));
-    }
-    if constexpr (kGrad) {
-        if (grad == 0.0f) {
-            zeros();
-        } else {
-            const float f = g / total * (left != 0.0f && z.rest != 0.0f ? mass - left * total / z.rest : mass);
-            if (slow) {
-                const int64_t lo = max(x.base, static_cast<int64_t>(0)), hi = min(x.base + x.span, static_cast<int64_t>(a.V));
-                for (int64_t i = lo + tid; i < hi; i += kNT) out[i] = from_f32<T>(ex2_approx(exponent(to_f32(x.row[i]))) * f);
-            } else {
-                if ((reinterpret_cast<uintptr_t>(out) - reinterpret_cast<uintptr_t>(x.row)) % 16 == 0)
-                    write_share<T, true>(x, out, a.kf, z.m, f);
-                else write_share<T, false>(x, out, a.kf, z.m, f);
-                if (single >= 0) out[single] = from_f32<T>(ex2_approx(exponent(alone)) * f);
+                for (uint32_t e = 0; e < kEntries; ++e) {
+                    if (id[e] != SEL_INVALID_ID) p_out[id[e]] = from_f32<T>(grads[e]);
+                    id[e] = SEL_INVALID_ID;
+                }
             }
-            __syncthreads();
+        };
+        uint32_t n = 0;
+        for (uint32_t row = first_row; row < a.rows; row += step, ++n) {
+            const Share<T> x(a.x, row * a.ld, a.V, rank, a.share);
+            const uint32_t vecs = x.w1 - x.w0, chunks = (vecs + kChunkVecs - 1) / kChunkVecs;
+            T* out = kGrad ? static_cast<T*>(a.out) + row * a.ld_out : nullptr;
+            const float* vals = a.vals + static_cast<uint64_t>(row) * a.k;
+            const uint32_t* ids = a.ids + static_cast<uint64_t>(row) * a.k;
+            uint32_t* bits = bitmaps + (n & 1) * words;
+            const int64_t single = x.single();
+            const float alone = single >= 0 ? to_f32(x.row[single]) : -INFINITY;
+
+            // The list: this thread's entries that the share holds, marked.
+            uint32_t new_id[kEntries];
+            float val[kEntries], logit[kEntries];
+            bool twice = false;
+#pragma unroll
+            for (uint32_t e = 0; e < kEntries; ++e) {
+                new_id[e] = SEL_INVALID_ID;
+                val[e] = logit[e] = -INFINITY;
+                if (e * kNT >= a.k) continue;
+                const uint32_t i = tid + e * kNT;
+                if (i >= a.k) continue;
+                const uint32_t at_id = ids[i];
+                const int64_t off = static_cast<int64_t>(at_id) - x.base;
+                if (at_id >= a.V || off < 0 || off >= x.span) continue;
+                new_id[e] = at_id;
+                val[e] = vals[i];
+                logit[e] = to_f32(x.row[at_id]);
+                const uint32_t bit = 1u << (off & 31);
+                twice |= (atomicOr(&bits[off >> 5], bit) & bit) != 0;
+            }
+            consumers_sync();
+            // (all of the row before is written, and this row's bitmap is whole)
+            scatter();
+            wait(&s.t_full[n & 1], n >> 1 & 1, &s.err);
+            const Teacher t = s.teacher[n & 1];
+            __syncwarp();
+            if (lane == 0) arrive(&s.t_empty[n & 1]);
+            if (!t.live) {
+                if (n == 0) skip(min(chunks, a.slots));  // (copied before the list was read)
+                if (rank == 0 && tid == 0 && a.loss) a.loss[row] = 0.0f;
+                if constexpr (kGrad) zeros(x, out);
+#pragma unroll
+                for (uint32_t e = 0; e < kEntries; ++e)
+                    if (new_id[e] != SEL_INVALID_ID) bits[(new_id[e] - x.base) >> 5] = 0;
+                continue;
+            }
+
+            Summer<T> mine{bits, a.kf, -kHuge, 0.0f};
+            const Place begin = at;
+            for (uint32_t first = 0; first < vecs; first += kChunkVecs) {
+                wait(&s.full[at.slot], at.phase, &s.err);
+                chunk(first, vecs, [&](uint32_t j, auto& q) { mine.add(x.w0 + j, q); });
+                if (a.resident) at.next(a.slots);
+                else release();
+            }
+            if (single >= 0) {
+                const uint32_t off = static_cast<uint32_t>(single - x.base);
+                if (!(bits[off >> 5] >> (off & 31) & 1)) mine.add_one(alone);
+            }
+            Sums z{mine.m, mine.sum, 0.0f};
+#pragma unroll
+            for (uint32_t e = 0; e < kEntries; ++e) {
+                if (new_id[e] == SEL_INVALID_ID) continue;
+                const float m = fmaxf(z.m, ceilf(logit[e] * a.kf)), f = pow2(z.m - m);
+                z = {m, z.rest * f, z.list * f + ex2_approx(fmaf(logit[e], a.kf, -m))};
+            }
+            if (twice) z.rest = NAN;
+            z = exchange(z);
+            // (the same in every warp of the cluster)
+            const bool slow = !(fabsf(z.m) < kHuge);
+            if (slow) z = slow_sums(x, bits, twice);
+            if (s.err) z.rest = NAN;
+            const float total = z.rest + z.list, log_z = log2f(total);
+            auto exponent = [&](float v) { return slow ? (v - z.m) * a.kf : fmaf(v, a.kf, -z.m); };
+            LogP log_p(a, row);
+            log_p.top = t.top;
+            if (!log_p.given) log_p.lh = t.norm;
+
+            // (every warp has read this bitmap; it is marked again two rows on)
 #pragma unroll
             for (uint32_t e = 0; e < kEntries; ++e)
-                if (id[e] != SEL_INVALID_ID) out[id[e]] = from_f32<T>(at[e]);
+                if (new_id[e] != SEL_INVALID_ID) bits[(new_id[e] - x.base) >> 5] = 0;
+            const float grad = kGrad ? a.grad[row] : 0.0f, g = grad * a.inv_t;
+            float part = 0.0f;
+#pragma unroll
+            for (uint32_t e = 0; e < kEntries; ++e) {
+                id[e] = new_id[e];
+                if (id[e] == SEL_INVALID_ID) continue;
+                const float lp = log_p(val[e]), y = exponent(logit[e]), p = exp2f(lp);
+                if (p != 0.0f) part += p * (lp - (y - log_z));
+                grads[e] = g * (t.mass * (ex2_approx(y) / total) - p);
+                if (kGrad && grad == 0.0f) id[e] = SEL_INVALID_ID;
+            }
+            if (a.loss) {
+                if (rank == 0 && tid == 0) expect_tx(&s.loss[lives & 1], a.C * kWarps * 4);
+                if (rank == 0 && warp == 0 && pending) finish();
+                part = warp_sum(part);
+                if (lane == 0) send(peer_addr(&s.losses[lives & 1][rank * kWarps + warp], 0), peer_addr(&s.loss[lives & 1], 0), part);
+            }
+            if constexpr (kGrad) {
+                p_out = out;
+                if (a.resident) at = begin;
+                if (grad == 0.0f || slow) {
+                    skip(chunks);
+                    if (slow && grad != 0.0f) {
+                        const float f = g / total * (t.left != 0.0f && z.rest != 0.0f ? t.mass - t.left * total / z.rest : t.mass);
+                        const int64_t lo = max(x.base, static_cast<int64_t>(0)), hi = min(x.base + x.span, static_cast<int64_t>(a.V));
+                        for (int64_t i = lo + tid; i < hi; i += kNT) out[i] = from_f32<T>(ex2_approx(exponent(to_f32(x.row[i]))) * f);
+                    } else {
+                        zeros(x, out);
+                    }
+                } else {
+                    const float f = g / total * (t.left != 0.0f && z.rest != 0.0f ? t.mass - t.left * total / z.rest : t.mass);
+                    if ((reinterpret_cast<uintptr_t>(out) - reinterpret_cast<uintptr_t>(x.row)) % 16 == 0)
+                        write_share<true>(x, out, z.m, f, vecs);
+                    else write_share<false>(x, out, z.m, f, vecs);
+                    if (single >= 0) out[single] = from_f32<T>(ex2_approx(exponent(alone)) * f);
+                }
+            }
+            p_left = t.left;
+            p_rest = z.rest;
+            p_log_z = log_z;
+            p_mass = t.mass;
+            pending_row = row;
+            ++lives;
+            pending = lives;
         }
+        consumers_sync();
+        scatter();
+        if (a.loss && rank == 0 && warp == 0 && pending) finish();
     }
-    if (!a.loss) return;
+};
+
+template <typename T, bool kGrad>
+__global__ void __launch_bounds__(kThreads, 2) distill_kernel(DistillArgs a) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ Shared s;
+    const uint32_t tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), C = a.C;
+    const uint32_t cluster = blockIdx.x / C, rank = blockIdx.x - cluster * C, clusters = gridDim.x / C;
+    unsigned char* ring = smem;
+    auto* bitmaps = reinterpret_cast<uint32_t*>(smem + a.slots * kChunkBytes);
+    const uint32_t words = (a.share * Vec<T>::kN + 31) / 32;
+    for (uint32_t i = tid; i < 2 * words; i += kThreads) bitmaps[i] = 0;
+    if (tid == 0) {
+        for (uint32_t i = 0; i < a.slots; ++i) {
+            mbar_init(&s.full[i], 1);
+            mbar_init(&s.empty[i], kWarps);
+        }
+        for (uint32_t i = 0; i < 2; ++i) {
+            mbar_init(&s.t_full[i], 1);
+            mbar_init(&s.t_empty[i], kWarps);
+            mbar_init(&s.sums[i], 1);
+            mbar_init(&s.loss[i], 1);
+        }
+        s.err = 0;
+    }
+    cluster_sync_all();
+    pdl_wait();
+    pdl_trigger();
+    if (warp == kWarps) {
+        Place at;
+        uint32_t issued = 0, n = 0;
+        bool ok = true;
+        for (uint32_t row = cluster; row < a.rows && ok; row += clusters, ++n) {
+            const Share<T> x(a.x, row * a.ld, a.V, rank, a.share);
+            const uint32_t vecs = x.w1 - x.w0;
+            const auto* src = reinterpret_cast<const unsigned char*>(x.vec + x.w0);
+            const uint32_t early = min(vecs, a.slots * kChunkVecs);
+            auto copy = [&](uint32_t from, uint32_t to) {
+                for (uint32_t first = from; first < to && ok; first += kChunkVecs) {
+                    ok = __all_sync(kFull, mbar_wait(&s.empty[at.slot], at.phase ^ 1));
+                    if (!ok) break;
+                    if ((tid & 31) == 0)
+                        bulk_load(ring + at.slot * kChunkBytes, src + static_cast<uint64_t>(first) * 16,
+                                  min(kChunkVecs, vecs - first) * 16, &s.full[at.slot]);
+                    ++issued;
+                    at.next(a.slots);
+                }
+            };
+            if (n == 0) copy(0, early);  // (before it is known whether the row counts)
+            if (n >= 2) ok = ok && __all_sync(kFull, mbar_wait(&s.t_empty[n & 1], (n >> 1) + 1 & 1));
+            const Teacher t = read_teacher(a, row);
+            if ((tid & 31) == 0) {
+                s.teacher[n & 1] = t;
+                arrive(&s.t_full[n & 1]);
+            }
+            __syncwarp();
+            if (t.live) copy(n == 0 ? early : 0, vecs);
+            if (kGrad && !a.resident && t.live) copy(0, vecs);  // for the gradient
+        }
+        // every copy has landed before the CTA may end
+        if (!ok) s.err = 1;
+        Place last = at;
+        for (uint32_t i = 0; i < min(issued, a.slots); ++i) {
+            last.phase ^= last.slot == 0;
+            last.slot = (last.slot == 0 ? a.slots : last.slot) - 1;
+            if (!mbar_wait(&s.full[last.slot], last.phase)) s.err = 1;
+        }
+        __syncwarp();
+    } else {
+        Worker<T, kGrad> w{a, s, ring, bitmaps, words, rank, tid, tid & 31, warp};
+        w.run(cluster, clusters);
+    }
+    // (nothing is on its way to this CTA, or from it to one that has ended)
     __syncwarp();
-    cluster_sync(C);
-    if (rank == 0 && tid == 0) {
-        float loss = 0.0f;
-        for (uint32_t i = 0; i < C; ++i) loss += s.row_losses[i];
-        if (left != 0.0f) loss += left * (log2f(left) - (log2f(z.rest) - log_z));
-        a.loss[row] = mass == mass ? loss * kLn2 : NAN;
-    }
+    cluster_sync_all();
 }
 
-// CTAs a row: enough that the device is full with few rows, and that the rows that
-// are on the device at a time stay in L2 until their second read.
-template <typename T>
-uint32_t ctas_for(uint32_t rows, uint32_t V, int sms) {
-    const uint64_t row_bytes = static_cast<uint64_t>(V) * sizeof(T), at_a_time = 3ull * sms;
-    uint32_t C = 1;
-    while (C < kMaxC && V / C > 4096 && (rows * static_cast<uint64_t>(C) < at_a_time || at_a_time / C * row_bytes > (48ull << 20)))
-        C *= 2;
-    return C;
+constexpr size_t kSmemMax = 220 * 1024;
+
+// How a call is laid out: chunks that fit two CTAs an SM, or one.
+struct Layout {
+    uint32_t C, slots, clusters;
+    bool resident;
+};
+
+template <typename T, bool kGrad>
+bool layout_for(uint32_t rows, uint32_t V, Layout& best) {
+    struct Table {
+        int clusters[2][kMaxC + 1];  // resident at a time, with half of an SM's memory for a CTA or all of it
+    };
+    static PerDevice<Table> tables;
+    Table t{};
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (!tables.get(dev, t, [](Table& r) {
+            for (uint32_t h = 0; h < 2; ++h) {
+                for (uint32_t c = 1; c <= kMaxC; ++c) {
+                    cudaLaunchConfig_t cfg{};
+                    cfg.gridDim = dim3(c);
+                    cfg.blockDim = dim3(kThreads);
+                    cfg.dynamicSmemBytes = h == 0 ? kSmemMax / 2 : kSmemMax;
+                    cudaLaunchAttribute attr[1];
+                    attr[0].id = cudaLaunchAttributeClusterDimension;
+                    attr[0].val.clusterDim.x = c;
+                    attr[0].val.clusterDim.y = 1;
+                    attr[0].val.clusterDim.z = 1;
+                    cfg.attrs = attr;
+                    cfg.numAttrs = 1;
+                    int n = 0;
+                    if (cudaOccupancyMaxActiveClusters(&n, distill_kernel<T, kGrad>, &cfg) != cudaSuccess) {
+                        (void)cudaGetLastError();
+                        return false;
+                    }
+                    r.clusters[h][c] = n;
+                }
+            }
+            return true;
+        }))
+        return false;
+    double least = 1e30;
+    for (uint32_t h = 0; h < 2; ++h) {
+        for (uint32_t c = 1; c <= kMaxC; ++c) {
+            if (t.clusters[h][c] <= 0) continue;
+            const uint64_t vecs = ceil_div(ceil_div(static_cast<uint64_t>(V) + Vec<T>::kN - 1, Vec<T>::kN), c);
+            const uint64_t bits = 2 * (vecs * Vec<T>::kN / 8 + 8);
+            const uint64_t room = (h == 0 ? kSmemMax / 2 : kSmemMax);
+            if (bits + 3 * kChunkBytes > room) continue;
+            const uint32_t slots = std::min<uint32_t>(kMaxSlots, static_cast<uint32_t>((room - bits) / kChunkBytes));
+            const bool resident = kGrad && ceil_div(vecs, kChunkVecs) <= slots;
+            const double rounds = ceil_div(rows, static_cast<uint64_t>(t.clusters[h][c]));
+            // us: a row's fixed cost and its bytes at a CTA's share of the rate
+            const double bytes = static_cast<double>(vecs) * 16 * (kGrad ? (resident ? 2 : 3) : 1);
+            const double us = rounds * (4.0 + bytes / (h == 0 ? 20e3 : 30e3));
+            if (us < least) {
+                least = us;
+                best = {c, slots, static_cast<uint32_t>(t.clusters[h][c]), resident};
+            }
+        }
+    }
+    return least < 1e30;
 }
 
 template <typename T, bool kGrad>
 sel_status launch(const DistillArgs& in, uint32_t rows, cudaStream_t stream) {
-    const int sms = device_sms();
-    if (sms <= 0) return SEL_ECUDA;
     DistillArgs a = in;
-    a.C = ctas_for<T>(rows, a.V, sms);
+    if (!dynamic_smem_once<distill_kernel<T, kGrad>>(kSmemMax)) return SEL_ECUDA;
+    Layout l{};
+    if (!layout_for<T, kGrad>(rows, a.V, l)) return SEL_ECUDA;
+    a.rows = rows;
+    a.C = l.C;
+    a.slots = l.slots;
+    a.resident = l.resident;
     a.share = ceil_div(ceil_div(static_cast<uint64_t>(a.V) + Vec<T>::kN - 1, Vec<T>::kN), a.C);
-    // a CTA's bitmap starts on a whole word of its own
-    const size_t smem = align_up(static_cast<size_t>(a.share) * Vec<T>::kN / 8 + 4, 16);
-    if (static_cast<uint64_t>(rows) * a.C > 0x7fffffffull) return SEL_EUNSUPPORTED;
-    if (smem > 160 * 1024) return SEL_EUNSUPPORTED;
-    if (smem > 32 * 1024 && !dynamic_smem_once<distill_kernel<T, kGrad>>(160 * 1024)) return SEL_ECUDA;
-    return launch_pdl_cluster(distill_kernel<T, kGrad>, dim3(rows * a.C), dim3(kNT), a.C, smem, stream, a) == cudaSuccess
+    const size_t smem = a.slots * static_cast<size_t>(kChunkBytes) + 2 * ((static_cast<size_t>(a.share) * Vec<T>::kN + 31) / 32 * 4);
+    return launch_pdl_cluster(distill_kernel<T, kGrad>, dim3(std::min(rows, l.clusters) * a.C), dim3(kThreads), a.C, smem,
+                              stream, a) == cudaSuccess
                ? SEL_OK
                : SEL_ECUDA;
 }
