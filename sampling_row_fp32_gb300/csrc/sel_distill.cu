@@ -42,7 +42,7 @@ namespace {
 constexpr uint32_t kNT = 256, kWarps = kNT / 32, kThreads = kNT + 32, kMaxC = 8;
 constexpr uint32_t kEntries = SEL_MAX_K / kNT;  // of a list, a thread
 constexpr uint32_t kBatch = 4;                  // vectors a thread takes at a time
-constexpr uint32_t kChunkVecs = kBatch * kNT, kChunkBytes = 16 * kChunkVecs, kMaxSlots = 13;
+constexpr uint32_t kChunkVecs = kBatch * kNT, kChunkBytes = 16 * kChunkVecs, kMaxSlots = 6;
 constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct DistillArgs {
@@ -558,13 +558,24 @@ struct Worker {
             }
         };
         uint32_t n = 0;
+        uint32_t list[kEntries];  // the row's ids, on their way since the row before
+        auto read_list = [&](uint32_t row) {
+#pragma unroll
+            for (uint32_t e = 0; e < kEntries; ++e) {
+                list[e] = SEL_INVALID_ID;
+                if (e * kNT < a.k && tid + e * kNT < a.k && row < a.rows)
+                    list[e] = a.ids[static_cast<uint64_t>(row) * a.k + tid + e * kNT];
+            }
+        };
+        read_list(first_row);
         for (uint32_t row = first_row; row < a.rows; row += step, ++n) {
             const Share<T> x(a.x, row * a.ld, a.V, rank, a.share);
             const uint32_t vecs = x.w1 - x.w0, chunks = (vecs + kChunkVecs - 1) / kChunkVecs;
             T* out = kGrad ? static_cast<T*>(a.out) + row * a.ld_out : nullptr;
             const float* vals = a.vals + static_cast<uint64_t>(row) * a.k;
-            const uint32_t* ids = a.ids + static_cast<uint64_t>(row) * a.k;
             uint32_t* bits = bitmaps + (n & 1) * words;
+            const float grad = kGrad ? a.grad[row] : 0.0f, g = grad * a.inv_t;
+            LogP log_p(a, row);
             const int64_t single = x.single();
             const float alone = single >= 0 ? to_f32(x.row[single]) : -INFINITY;
 
@@ -577,17 +588,16 @@ struct Worker {
                 new_id[e] = SEL_INVALID_ID;
                 val[e] = logit[e] = -INFINITY;
                 if (e * kNT >= a.k) continue;
-                const uint32_t i = tid + e * kNT;
-                if (i >= a.k) continue;
-                const uint32_t at_id = ids[i];
+                const uint32_t at_id = list[e];
                 const int64_t off = static_cast<int64_t>(at_id) - x.base;
                 if (at_id >= a.V || off < 0 || off >= x.span) continue;
                 new_id[e] = at_id;
-                val[e] = vals[i];
+                val[e] = vals[tid + e * kNT];
                 logit[e] = to_f32(x.row[at_id]);
                 const uint32_t bit = 1u << (off & 31);
                 twice |= (atomicOr(&bits[off >> 5], bit) & bit) != 0;
             }
+            read_list(row + step);
             consumers_sync();
             // (all of the row before is written, and this row's bitmap is whole)
             scatter();
@@ -632,7 +642,6 @@ struct Worker {
             if (s.err) z.rest = NAN;
             const float total = z.rest + z.list, log_z = log2f(total);
             auto exponent = [&](float v) { return slow ? (v - z.m) * a.kf : fmaf(v, a.kf, -z.m); };
-            LogP log_p(a, row);
             log_p.top = t.top;
             if (!log_p.given) log_p.lh = t.norm;
 
@@ -640,7 +649,6 @@ struct Worker {
 #pragma unroll
             for (uint32_t e = 0; e < kEntries; ++e)
                 if (new_id[e] != SEL_INVALID_ID) bits[(new_id[e] - x.base) >> 5] = 0;
-            const float grad = kGrad ? a.grad[row] : 0.0f, g = grad * a.inv_t;
             float part = 0.0f;
 #pragma unroll
             for (uint32_t e = 0; e < kEntries; ++e) {
@@ -766,66 +774,66 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(DistillArgs a) {
     cluster_sync_all();
 }
 
-constexpr size_t kSmemMax = 220 * 1024;
+constexpr size_t kSmem = 110 * 1024;  // a CTA's ring and bitmaps: two CTAs an SM
+constexpr uint32_t kMinSlots = 3;
+constexpr size_t bitmap_bytes(uint64_t ids) { return 2 * ((ids + 31) / 32 * 4); }
+static_assert(bitmap_bytes(SEL_DISTILL_MAX_V / kMaxC + 16) + kMinSlots * kChunkBytes <= kSmem);
 
-// How a call is laid out: chunks that fit two CTAs an SM, or one.
 struct Layout {
-    uint32_t C, slots, clusters;
+    uint32_t C, share, slots, clusters;
     bool resident;
 };
 
+// CTAs a row: what takes least by a model of the rounds of resident clusters. A CTA
+// takes 2.1 us a row and 1 us for 23 KB; shares that do not fit the ring cross it
+// twice, the second time out of L2 (as 0.2 of a read from memory), unless the rows
+// on the device at a time are too many for it. 4,096 rows of 151,936 bf16, CTAs a
+// row 1 / 2 / 3 / 4 (with 4 a share fits): 526 / 446 / 505 / 484 us; one and three
+// CTAs an SM instead of two were slower at each.
 template <typename T, bool kGrad>
 bool layout_for(uint32_t rows, uint32_t V, Layout& best) {
     struct Table {
-        int clusters[2][kMaxC + 1];  // resident at a time, with half of an SM's memory for a CTA or all of it
+        int clusters[kMaxC + 1];  // resident at a time
     };
     static PerDevice<Table> tables;
     Table t{};
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    if (!tables.get(dev, t, [](Table& r) {
-            for (uint32_t h = 0; h < 2; ++h) {
-                for (uint32_t c = 1; c <= kMaxC; ++c) {
-                    cudaLaunchConfig_t cfg{};
-                    cfg.gridDim = dim3(c);
-                    cfg.blockDim = dim3(kThreads);
-                    cfg.dynamicSmemBytes = h == 0 ? kSmemMax / 2 : kSmemMax;
-                    cudaLaunchAttribute attr[1];
-                    attr[0].id = cudaLaunchAttributeClusterDimension;
-                    attr[0].val.clusterDim.x = c;
-                    attr[0].val.clusterDim.y = 1;
-                    attr[0].val.clusterDim.z = 1;
-                    cfg.attrs = attr;
-                    cfg.numAttrs = 1;
-                    int n = 0;
-                    if (cudaOccupancyMaxActiveClusters(&n, distill_kernel<T, kGrad>, &cfg) != cudaSuccess) {
-                        (void)cudaGetLastError();
-                        return false;
-                    }
-                    r.clusters[h][c] = n;
-                }
-            }
-            return true;
-        }))
-        return false;
-    double least = 1e30;
-    for (uint32_t h = 0; h < 2; ++h) {
+    const bool known = tables.get(dev, t, [](Table& r) {
         for (uint32_t c = 1; c <= kMaxC; ++c) {
-            if (t.clusters[h][c] <= 0) continue;
-            const uint64_t vecs = ceil_div(ceil_div(static_cast<uint64_t>(V) + Vec<T>::kN - 1, Vec<T>::kN), c);
-            const uint64_t bits = 2 * (vecs * Vec<T>::kN / 8 + 8);
-            const uint64_t room = (h == 0 ? kSmemMax / 2 : kSmemMax);
-            if (bits + 3 * kChunkBytes > room) continue;
-            const uint32_t slots = std::min<uint32_t>(kMaxSlots, static_cast<uint32_t>((room - bits) / kChunkBytes));
-            const bool resident = kGrad && ceil_div(vecs, kChunkVecs) <= slots;
-            const double rounds = ceil_div(rows, static_cast<uint64_t>(t.clusters[h][c]));
-            // us: a row's fixed cost and its bytes at a CTA's share of the rate
-            const double bytes = static_cast<double>(vecs) * 16 * (kGrad ? (resident ? 2 : 3) : 1);
-            const double us = rounds * (4.0 + bytes / (h == 0 ? 20e3 : 30e3));
-            if (us < least) {
-                least = us;
-                best = {c, slots, static_cast<uint32_t>(t.clusters[h][c]), resident};
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3(c);
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = kSmem;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = c;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&r.clusters[c], distill_kernel<T, kGrad>, &cfg) != cudaSuccess) {
+                (void)cudaGetLastError();
+                return false;
             }
+        }
+        return true;
+    });
+    if (!known) return false;
+    double least = 1e30;
+    for (uint32_t c = 1; c <= kMaxC; ++c) {
+        if (t.clusters[c] <= 0) continue;
+        const uint32_t share = ceil_div(ceil_div(static_cast<uint64_t>(V) + Vec<T>::kN - 1, Vec<T>::kN), c);
+        const size_t bits = bitmap_bytes(static_cast<uint64_t>(share) * Vec<T>::kN);
+        if (bits + kMinSlots * kChunkBytes > kSmem) continue;
+        const uint32_t slots = std::min(kMaxSlots, static_cast<uint32_t>((kSmem - bits) / kChunkBytes));
+        const bool resident = kGrad && ceil_div(share, kChunkVecs) <= slots;
+        const bool in_l2 = static_cast<double>(t.clusters[c]) * V * sizeof(T) <= 64e6;
+        const double moved = share * 16.0 * (!kGrad ? 1.0 : resident ? 2.0 : in_l2 ? 2.2 : 3.0);
+        const double us = ceil_div(rows, static_cast<uint64_t>(t.clusters[c])) * (2.1 + moved / 23.1e3);
+        if (us < least) {
+            least = us;
+            best = {c, share, slots, static_cast<uint32_t>(t.clusters[c]), resident};
         }
     }
     return least < 1e30;
@@ -834,15 +842,15 @@ bool layout_for(uint32_t rows, uint32_t V, Layout& best) {
 template <typename T, bool kGrad>
 sel_status launch(const DistillArgs& in, uint32_t rows, cudaStream_t stream) {
     DistillArgs a = in;
-    if (!dynamic_smem_once<distill_kernel<T, kGrad>>(kSmemMax)) return SEL_ECUDA;
+    if (!dynamic_smem_once<distill_kernel<T, kGrad>>(kSmem)) return SEL_ECUDA;
     Layout l{};
     if (!layout_for<T, kGrad>(rows, a.V, l)) return SEL_ECUDA;
     a.rows = rows;
     a.C = l.C;
+    a.share = l.share;
     a.slots = l.slots;
     a.resident = l.resident;
-    a.share = ceil_div(ceil_div(static_cast<uint64_t>(a.V) + Vec<T>::kN - 1, Vec<T>::kN), a.C);
-    const size_t smem = a.slots * static_cast<size_t>(kChunkBytes) + 2 * ((static_cast<size_t>(a.share) * Vec<T>::kN + 31) / 32 * 4);
+    const size_t smem = a.slots * static_cast<size_t>(kChunkBytes) + bitmap_bytes(static_cast<uint64_t>(a.share) * Vec<T>::kN);
     return launch_pdl_cluster(distill_kernel<T, kGrad>, dim3(std::min(rows, l.clusters) * a.C), dim3(kThreads), a.C, smem,
                               stream, a) == cudaSuccess
                ? SEL_OK
