@@ -4,17 +4,17 @@
 //   D[m][n] = sum_k A[m][k] * B[n][k]
 //
 // Each operand may lie with k or with its own index (m or n) in the rows of its
-// matrix: tensor memory's products take both, so nothing is transposed. A
-// worker (a CTA, or a pair of CTAs whose products run as one) walks a list of
-// tiles that the problem P gives it: 256 columns, 128 rows a CTA. Warp roles:
+// matrix: the tensor cores take both, so nothing is transposed. A worker, a
+// pair of CTAs whose products run as one, walks a list of tiles that the problem P
+// gives it: 256 rows (128 a CTA) and up to 256 columns. Warp roles:
 //   warp 0      copies both operands, 64 k a stage, into a ring (TMA, swizzled)
 //   warp 1      issues the products (the pair's first CTA for both)
-//   warps 4-11  read a tile's D from tensor memory, 32 rows x 128 columns a
-//               warp, and run P's epilogue; D is double-buffered, so that
-//               the products of the next tile run meanwhile
-// A pair shares the tile's 256 columns of B: each CTA holds half of them and both
-// halves feed both, which halves what a product reads through L2 and shared
-// memory: 32 KB a CTA and stage instead of 48.
+//   warps 4-11  read a tile's D from tensor memory, 32 rows and about half of the
+//               columns a warp, and run P's epilogue; D is double-buffered, so that the
+//               products of the next tile run meanwhile
+// Each CTA of a pair holds half of the tile's columns of B and both halves feed
+// both, which halves what a product reads through L2 and shared memory: 32 KB a CTA
+// and stage for 256 x 256, where a CTA on its own takes 48 for its 128 x 256.
 // Every wait is bounded; one that runs out raises the workspace's error word.
 #pragma once
 
@@ -29,44 +29,38 @@
 
 namespace sel {
 
-constexpr uint32_t kTileN = 256, kCtaM = 128, kStepK = 64;
+constexpr uint32_t kTileM = 256, kTileN = 256, kCtaM = 128, kStepK = 64;
 constexpr int kGemmThreads = 384;
-constexpr uint32_t kEpiWarps = 8;
-constexpr uint32_t kStageABytes = kCtaM * kStepK * 2;
-constexpr uint32_t kStoreBytes = 32 * 128;  // a warp's 32 rows x 64 columns on their way out
+constexpr uint32_t kEpiWarps = 8, kGemmStages = 6;
+constexpr uint32_t kStageABytes = kCtaM * kStepK * 2, kStageBytes = kStageABytes + kTileN / 2 * kStepK * 2;
+constexpr uint32_t kWarpBytes = 32 * 128;  // shared memory of an epilogue warp: 32 rows x 64 columns on their way out
+constexpr uint32_t kGemmSmem = 1024 + kGemmStages * kStageBytes + kEpiWarps * kWarpBytes;
+static_assert(kGemmSmem + 1024 <= 227 * 1024);
 
-template <bool kPair>
-struct GemmConfig {
-    static constexpr uint32_t kTileM = kPair ? 2 * kCtaM : kCtaM;
-    static constexpr uint32_t kCtaN = kPair ? kTileN / 2 : kTileN;  // rows of B a CTA holds
-    static constexpr uint32_t kStageBytes = kStageABytes + kCtaN * kStepK * 2;
-    static constexpr uint32_t kStages = kPair ? 6 : 4;
-    static constexpr uint32_t kSmem = 1024 + kStages * kStageBytes + kEpiWarps * kStoreBytes;
-    static_assert(kSmem + 1024 <= 227 * 1024);
-};
-
-// A tile of a product: its first row, column and k, its steps of 64 k, and the
-// operands' maps; *_mn: the operand's own index lies in the rows of its matrix.
-// Maps of operands with k in the rows have boxes of 64 k x the rows a CTA holds,
-// the others boxes of 64 x 64 k.
+// A tile of a product: its columns n (a multiple of 16, at most 256), its steps of
+// 64 k, and the operands' maps; *_mn: the operand's own index lies in the rows of its
+// matrix. Maps of operands with k in the rows have boxes of 64 k x the rows a CTA
+// holds (128 of A, n / 2 of B), the others boxes of 64 x 64 k.
 struct GemmTile {
     const CUtensorMap *a, *b;
     uint32_t am, bn;  // where the operands' own indices begin
     uint32_t ak, bk;  // where their k begin
-    uint32_t steps;
+    uint32_t steps, n;
     bool a_mn, b_mn;
 };
 
 struct GemmShared {
-    uint64_t full[6], empty[6], d_full[2], d_empty[2], drain;
+    uint64_t full[kGemmStages], empty[kGemmStages], d_full[2], d_empty[2], drain;
     uint32_t tmem, err;
 };
 
-// A warp's place in a tile, and what it writes through.
+// A warp's place in a tile: this lane's row, the warp's first column and how many it
+// has, in pieces of 32 (the last may be short: what it reads beyond is meaningless).
 struct EpiWarp {
-    uint32_t row, col;  // of the tile's first row and column: this lane's row, the warp's first of 128 columns
-    uint32_t lane;
-    unsigned char* store;  // kStoreBytes of shared memory
+    uint32_t row, col, cols, chunks, lane;
+    uint32_t worker, workers;
+    bool first, last;     // of the worker's tiles
+    unsigned char* smem;  // kWarpBytes of its own
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -104,43 +98,26 @@ __device__ __forceinline__ void store_read_wait() { asm volatile("cp.async.bulk.
 __device__ __forceinline__ void store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-template <bool kPair>
 __device__ __forceinline__ void gemm_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-    if constexpr (kPair)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
-            : "memory");
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+        : "memory");
 }
-// The barrier, of both CTAs of a pair, completes once every product issued before
-// by this thread has.
-template <bool kPair>
+// The barrier, of both CTAs, completes once every product issued before by this
+// thread has.
 __device__ __forceinline__ void gemm_commit(uint64_t* bar) {
-    if constexpr (kPair)
-        asm volatile(
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-                smem_u32(bar)),
-            "h"(static_cast<uint16_t>(3))
-            : "memory");
-    else
-        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                     : "memory");
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
 }
-
 // The same for a barrier of this CTA alone.
-template <bool kPair>
 __device__ __forceinline__ void gemm_commit_here(uint64_t* bar) {
-    if constexpr (kPair)
-        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                     : "memory");
-    else gemm_commit<false>(bar);
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
 }
 
 // Descriptor of an operand tile whose own index lies in its 128-byte rows (64
@@ -184,12 +161,12 @@ __device__ __forceinline__ void store_chunk(const EpiWarp& w, const CUtensorMap*
         q.z = pack2<T>(v[8 * j + 4], v[8 * j + 5]);
         q.w = pack2<T>(v[8 * j + 6], v[8 * j + 7]);
         const uint32_t ch = (c % 2) * 4 + j;
-        *reinterpret_cast<uint4*>(w.store + w.lane * 128 + ((ch ^ (w.lane & 7)) << 4)) = q;
+        *reinterpret_cast<uint4*>(w.smem + w.lane * 128 + ((ch ^ (w.lane & 7)) << 4)) = q;
     }
     if (c % 2 == 1) {
         proxy_fence();
         __syncwarp();
-        if (w.lane == 0 && inside) tma_store_2d(map, x, y, w.store);
+        if (w.lane == 0 && inside) tma_store_2d(map, x, y, w.smem);
     }
 }
 
@@ -198,45 +175,35 @@ __device__ __forceinline__ void store_chunk(const EpiWarp& w, const CUtensorMap*
 //   uint32_t* error                    the workspace's error word
 //   count(worker, workers)             how many tiles a worker has
 //   tile(worker, workers, j)           the j-th of them
-//   epilogue(tile, w, load)            load(c, v): columns 32 c .. of the warp's rows,
-//                                      c = 0, 1, 2, 3 in order, each once
-template <typename P, bool kPair>
+//   epilogue(tile, w, load)            load(c, v): the warp's columns 32 c .., for
+//                                      c = 0 .. chunks - 1 in order, each once
+template <typename P>
 __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_constant__ P p) {
-    using C = GemmConfig<kPair>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    unsigned char* store = ring + C::kStages * C::kStageBytes;
     __shared__ GemmShared c;
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(kFull, tid >> 5, 0);
-    const uint32_t rank = kPair ? cluster_rank() : 0;
-    const uint32_t worker = kPair ? blockIdx.x / 2 : blockIdx.x, workers = kPair ? gridDim.x / 2 : gridDim.x;
+    const uint32_t rank = cluster_rank(), worker = blockIdx.x / 2, workers = gridDim.x / 2;
 
     if (tid == 0) {
-        for (uint32_t i = 0; i < C::kStages; ++i) {
+        for (uint32_t i = 0; i < kGemmStages; ++i) {
             mbar_init(&c.full[i], 1);
             mbar_init(&c.empty[i], 1);
         }
         for (uint32_t i = 0; i < 2; ++i) {
             mbar_init(&c.d_full[i], 1);
-            mbar_init(&c.d_empty[i], kPair ? 2 * kEpiWarps : kEpiWarps);
+            mbar_init(&c.d_empty[i], 2 * kEpiWarps);
         }
         mbar_init(&c.drain, 1);
         c.err = 0;
     }
     if (warp == 2) {
-        if constexpr (kPair) {
-            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&c.tmem))
-                         : "memory");
-            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-        } else {
-            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&c.tmem))
-                         : "memory");
-            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-        }
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&c.tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
     }
     tc_fence_before();
-    if constexpr (kPair) cluster_sync_all();
-    else __syncthreads();
+    cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(kFull, c.tmem, 0);
     pdl_wait();
@@ -245,34 +212,32 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
 
     if (warp == 0) {
         const bool leader = elect_one();
-        Ring<C::kStages> st;
+        Ring<kGemmStages> st;
         uint32_t issued = 0;
         bool ok = true;
         for (uint32_t j = 0; j < count && ok; ++j) {
             const GemmTile t = p.tile(worker, workers, j);
-            const uint32_t am = t.am + rank * kCtaM, bn = t.bn + rank * C::kCtaN;
+            const uint32_t am = t.am + rank * kCtaM, bn = t.bn + rank * (t.n / 2);
+            const uint32_t b_boxes = (t.n + 127) / 128;  // of 64
+            const uint32_t bytes = 2 * (kStageABytes + (t.b_mn ? b_boxes * 8192 : t.n * 64));
             for (uint32_t s = 0; s < t.steps; ++s) {
                 ok = __all_sync(kFull, mbar_wait(&c.empty[st.i], st.phase ^ 1));
                 if (!ok) break;
                 if (leader) {
-                    unsigned char* da = ring + st.i * C::kStageBytes;
+                    unsigned char* da = ring + st.i * kStageBytes;
                     unsigned char* db = da + kStageABytes;
                     const uint32_t ak = t.ak + s * kStepK, bk = t.bk + s * kStepK;
-                    if (rank == 0) expect_tx(&c.full[st.i], (kPair ? 2 : 1) * C::kStageBytes);
-                    const uint32_t bar = kPair ? first_cta(&c.full[st.i]) : 0;
-                    auto copy = [&](unsigned char* dst, const CUtensorMap* map, uint32_t x, uint32_t y) {
-                        if constexpr (kPair) tma_2d_pair(dst, map, x, y, bar);
-                        else tma_2d(dst, map, x, y, &c.full[st.i]);
-                    };
+                    if (rank == 0) expect_tx(&c.full[st.i], bytes);
+                    const uint32_t bar = first_cta(&c.full[st.i]);
                     if (t.a_mn) {
-                        for (uint32_t i = 0; i < kCtaM / 64; ++i) copy(da + i * 8192, t.a, am + i * 64, ak);
+                        for (uint32_t i = 0; i < kCtaM / 64; ++i) tma_2d_pair(da + i * 8192, t.a, am + i * 64, ak, bar);
                     } else {
-                        copy(da, t.a, ak, am);
+                        tma_2d_pair(da, t.a, ak, am, bar);
                     }
                     if (t.b_mn) {
-                        for (uint32_t i = 0; i < C::kCtaN / 64; ++i) copy(db + i * 8192, t.b, bn + i * 64, bk);
+                        for (uint32_t i = 0; i < b_boxes; ++i) tma_2d_pair(db + i * 8192, t.b, bn + i * 64, bk, bar);
                     } else {
-                        copy(db, t.b, bk, bn);
+                        tma_2d_pair(db, t.b, bk, bn, bar);
                     }
                 }
                 ++issued;
@@ -281,20 +246,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
         }
         // every copy has landed before the CTAs may end
         if (leader && rank == 0) {
-            for (uint32_t i = issued > C::kStages ? issued - C::kStages : 0; i < issued; ++i)
-                if (!mbar_wait(&c.full[i % C::kStages], (i / C::kStages) & 1)) ok = false;
+            for (uint32_t i = issued > kGemmStages ? issued - kGemmStages : 0; i < issued; ++i)
+                if (!mbar_wait(&c.full[i % kGemmStages], (i / kGemmStages) & 1)) ok = false;
         }
         if (!ok) c.err = 1;
         __syncwarp();
     } else if (warp == 1 && rank == 0) {
         const bool leader = elect_one();
         constexpr uint32_t kType = std::is_same_v<typename P::Type, __nv_bfloat16> ? 1 : 0;
-        constexpr uint32_t kIdesc = (1u << 4) | (kType << 7) | (kType << 10) | ((kTileN >> 3) << 17) | ((C::kTileM >> 4) << 24);
-        Ring<C::kStages> st;
+        constexpr uint32_t kIdesc = (1u << 4) | (kType << 7) | (kType << 10) | ((kTileM >> 4) << 24);
+        Ring<kGemmStages> st;
         Ring<2> dr;
         for (uint32_t j = 0; j < count; ++j) {
             const GemmTile t = p.tile(worker, workers, j);
-            const uint32_t idesc = kIdesc | (t.a_mn ? 1u << 15 : 0) | (t.b_mn ? 1u << 16 : 0);
+            const uint32_t idesc = kIdesc | (t.a_mn ? 1u << 15 : 0) | (t.b_mn ? 1u << 16 : 0) | ((t.n >> 3) << 17);
             const uint32_t step_a = t.a_mn ? 2048 >> 4 : 32 >> 4, step_b = t.b_mn ? 2048 >> 4 : 32 >> 4;
             wait(&c.d_empty[dr.i], dr.phase ^ 1, &c.err);
             tc_fence_after();
@@ -303,50 +268,57 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
                 wait(&c.full[st.i], st.phase, &c.err);
                 tc_fence_after();
                 if (leader) {
-                    const uint32_t sa = smem_u32(ring + st.i * C::kStageBytes), sb = sa + kStageABytes;
+                    const uint32_t sa = smem_u32(ring + st.i * kStageBytes), sb = sa + kStageABytes;
                     const uint64_t a = t.a_mn ? smem_desc_mn(sa) : smem_desc(sa);
                     const uint64_t b = t.b_mn ? smem_desc_mn(sb) : smem_desc(sb);
 #pragma unroll
                     for (uint32_t k = 0; k < kStepK / 16; ++k)
-                        gemm_mma<kPair>(d, a + k * step_a, b + k * step_b, idesc, s > 0 || k > 0);
-                    gemm_commit<kPair>(&c.empty[st.i]);
+                        gemm_mma(d, a + k * step_a, b + k * step_b, idesc, s > 0 || k > 0);
+                    gemm_commit(&c.empty[st.i]);
                 }
                 __syncwarp();
                 st.next();
             }
-            if (leader) gemm_commit<kPair>(&c.d_full[dr.i]);
+            if (leader) gemm_commit(&c.d_full[dr.i]);
             __syncwarp();
             dr.next();
         }
         // no product is in flight when the tensor memory is given back
-        if (leader) gemm_commit_here<kPair>(&c.drain);
+        if (leader) gemm_commit_here(&c.drain);
         if (!mbar_wait(&c.drain, 0)) c.err = 1;
         __syncwarp();
     } else if (warp >= 4) {
         const uint32_t quarter = warp & 3, half = (warp - 4) >> 2;
         EpiWarp w;
         w.row = rank * kCtaM + quarter * 32 + lane;
-        w.col = half * 128;
         w.lane = lane;
-        w.store = store + (warp - 4) * kStoreBytes;
+        w.worker = worker;
+        w.workers = workers;
+        w.smem = ring + kGemmStages * kStageBytes + (warp - 4) * kWarpBytes;
         Ring<2> dr;
         for (uint32_t j = 0; j < count; ++j) {
             const GemmTile t = p.tile(worker, workers, j);
+            const uint32_t low = (t.n / 2 + 15) / 16 * 16;  // (whole 32 bytes of 16-bit results)
+            w.cols = half ? t.n - low : low;
+            w.col = half * low;
+            w.chunks = (w.cols + 31) / 32;
+            w.first = j == 0;
+            w.last = j == count - 1;
             wait(&c.d_full[dr.i], dr.phase, &c.err);
             tc_fence_after();
-            const uint32_t d = tmem + (quarter << 21) + dr.i * kTileN + half * 128;
+            // (a short last piece reads on, at most to the end of the tensor memory)
+            const uint32_t d = tmem + (quarter << 21) + dr.i * kTileN + w.col;
+            auto release = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_cluster(first_cta(&c.d_empty[dr.i]));
+            };
+            if (w.chunks == 0) release();  // (16 columns: all of them the other half's)
             p.epilogue(t, w, [&](uint32_t i, float(&v)[32]) {
                 uint32_t r[32];
                 __syncwarp();
                 tmem_ld(d + i * 32, r);
-                if (i == 3) {  // the buffer is read
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if constexpr (kPair) arrive_cluster(first_cta(&c.d_empty[dr.i]));
-                        else arrive(&c.d_empty[dr.i]);
-                    }
-                }
+                if (i == w.chunks - 1) release();  // the buffer is read
 #pragma unroll
                 for (uint32_t k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k]);
             });
@@ -356,25 +328,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
         __syncwarp();
     }
     tc_fence_before();
-    if constexpr (kPair) cluster_sync_all();
-    else __syncthreads();
+    cluster_sync_all();
     tc_fence_after();
-    if (warp == 2) {
-        if constexpr (kPair) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
-        else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
-    }
+    if (warp == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     if (tid == 0 && c.err) atomicOr(p.error, kErrTimeout);
 }
 
-template <typename P, bool kPair>
+template <typename P>
 inline sel_status launch_gemm(const P& p, uint32_t workers, cudaStream_t stream) {
-    using C = GemmConfig<kPair>;
-    if (!dynamic_smem_once<gemm_kernel<P, kPair>>(C::kSmem)) return SEL_ECUDA;
-    cudaError_t e;
-    if constexpr (kPair)
-        e = launch_pdl_cluster(gemm_kernel<P, kPair>, dim3(2 * workers), dim3(kGemmThreads), 2, C::kSmem, stream, p);
-    else
-        e = launch_pdl(gemm_kernel<P, kPair>, dim3(workers), dim3(kGemmThreads), C::kSmem, stream, p);
+    if (!dynamic_smem_once<gemm_kernel<P>>(kGemmSmem)) return SEL_ECUDA;
+    const cudaError_t e =
+        launch_pdl_cluster(gemm_kernel<P>, dim3(2 * workers), dim3(kGemmThreads), 2, kGemmSmem, stream, p);
     return e == cudaSuccess ? SEL_OK : SEL_ECUDA;
 }
 

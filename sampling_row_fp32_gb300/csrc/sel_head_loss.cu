@@ -6,8 +6,8 @@
 //   dX_r = g_r sum_v P_rv W_v;  dW_v = sum_r g_r P_rv X_r
 //
 // The loss is one product (sel_gemm.cuh) whose epilogue keeps two numbers of each
-// row and 128 columns, a reference exponent and the sum of the others' weights
-// over it; a small launch joins them. The target's logit is kept apart, so that
+// row and 128 ids (32 where the rows lie on the columns), a reference exponent and
+// the sum of the others' weights over it; a small launch joins them. The target's logit is kept apart, so that
 // loss = ln(1 + sum_others / e^z_t) holds its bits where it is near zero.
 //
 // The gradient goes over the vocabulary in pieces. For each, one launch computes
@@ -56,12 +56,29 @@ struct Part {
     float m, s;
 };
 
-template <typename T, bool kPair>
+// The reference for a largest logit `top`, and the weights under it.
+struct Weights {
+    float ref, k0, k1;
+    __device__ __forceinline__ explicit Weights(float m) {
+        ref = m == -INFINITY ? 0.0f : m;
+        // The product z log2(e) is not rounded before the subtraction, but where
+        // its rounding is no longer small next to 1 it has to be: then the largest
+        // is m itself.
+        const bool big = fabsf(ref) >= 1048576.0f;
+        k0 = big ? kLog2E : 1.0f;
+        k1 = big ? 1.0f : kLog2E;
+    }
+    __device__ __forceinline__ float operator()(float z) const { return ex2_approx(fmaf(z * k0, k1, -ref)); }
+};
+
+// Hidden rows on the product's rows: a lane has one of them, and half a tile's
+// columns of z.
+template <typename T>
 struct LossProblem {
     using Type = T;
     CUtensorMap x, w;
     const uint32_t* targets;
-    Part* parts;  // [2 nt][rows]
+    Part* parts;  // [2 column tiles][rows]
     float* at;    // [rows]: the target's logit
     uint32_t* error;
     uint32_t rows, V, steps;
@@ -71,7 +88,7 @@ struct LossProblem {
     __device__ __forceinline__ GemmTile tile(uint32_t worker, uint32_t workers, uint32_t j) const {
         uint32_t m, n;
         raster.at(worker + j * workers, m, n);
-        return {&x, &w, m * GemmConfig<kPair>::kTileM, n * kTileN, 0, 0, steps, false, false};
+        return {&x, &w, m * kTileM, n * kTileN, 0, 0, steps, kTileN, false, false};
     }
     template <typename Load>
     __device__ __forceinline__ void epilogue(const GemmTile& t, const EpiWarp& w, Load load) const {
@@ -79,7 +96,7 @@ struct LossProblem {
         const uint32_t target = row < rows ? targets[row] : SEL_INVALID_ID;
         Part p{-INFINITY, 0.0f};
 #pragma unroll 1
-        for (uint32_t c = 0; c < 4; ++c) {
+        for (uint32_t c = 0; c < w.chunks; ++c) {
             float v[32];
             load(c, v);
             const uint32_t c0 = col + 32 * c;
@@ -102,19 +119,108 @@ struct LossProblem {
             for (uint32_t i = 1; i < 31; i += 2) top = max3f(top, v[i], v[i + 1]);
             top = fmaxf(top, v[31]);
             const float m = fmaxf(p.m, ceilf(top * kLog2E));
-            const float ref = m == -INFINITY ? 0.0f : m;
-            // The product z log2(e) is not rounded before the subtraction, but where
-            // its rounding is no longer small next to 1 it has to be: then the
-            // largest is m itself.
-            const bool big = fabsf(ref) >= 1048576.0f;
-            const float k0 = big ? kLog2E : 1.0f, k1 = big ? 1.0f : kLog2E;
-            float s[4] = {p.s * pow2(p.m - ref), 0.0f, 0.0f, 0.0f};
+            const Weights e(m);
+            float s[4] = {p.s * pow2(p.m - e.ref), 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (uint32_t i = 0; i < 32; ++i) s[i % 4] += ex2_approx(fmaf(v[i] * k0, k1, -ref));
+            for (uint32_t i = 0; i < 32; ++i) s[i % 4] += e(v[i]);
             p.m = m;
             p.s = (s[0] + s[1]) + (s[2] + s[3]);
         }
         if (row < rows) parts[static_cast<uint64_t>(col / 128) * rows + row] = p;
+    }
+};
+
+// Hidden rows on the product's columns, so that a tile has as few as 16 of them: a
+// lane has one id, and the logits of half a tile's rows for it.
+
+// Of 32 rows' values in each lane, the sums over the lanes: lane i gets row i's.
+__device__ __forceinline__ float sum_across(float (&v)[32]) {
+    const uint32_t lane = threadIdx.x & 31;
+#pragma unroll
+    for (uint32_t n = 16; n > 0; n >>= 1) {
+        const bool up = lane & n;
+#pragma unroll
+        for (uint32_t i = 0; i < n; ++i) {
+            const float keep = up ? v[i + n] : v[i], give = up ? v[i] : v[i + n];
+            v[i] = keep + __shfl_xor_sync(kFull, give, n);
+        }
+    }
+    return v[0];
+}
+__device__ __forceinline__ float max_across(float v) {
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(v));  // (a NaN shows in the sums, not here)
+    return r;
+}
+
+template <typename T>
+struct LossColumnsProblem {
+    using Type = T;
+    CUtensorMap x, w;
+    const uint32_t* targets;
+    Part* parts;  // [8 workers of a row tile][rows]
+    float* at;
+    uint32_t* error;
+    uint32_t rows, V, steps, n, row_tiles, v_tiles;
+
+    // A worker stays with its row tile and keeps that one's sums from tile to tile;
+    // neighbours take the same ids with the other row tiles.
+    __device__ __forceinline__ uint32_t count(uint32_t worker, uint32_t workers) const {
+        const uint32_t v = worker / row_tiles, step = workers / row_tiles;
+        return v < v_tiles ? (v_tiles - v - 1) / step + 1 : 0;
+    }
+    __device__ __forceinline__ GemmTile tile(uint32_t worker, uint32_t workers, uint32_t j) const {
+        const uint32_t v = worker / row_tiles + j * (workers / row_tiles);
+        return {&w, &x, v * kTileM, worker % row_tiles * n, 0, 0, steps, n, false, false};
+    }
+    template <typename Load>
+    __device__ __forceinline__ void epilogue(const GemmTile& t, const EpiWarp& w, Load load) const {
+        const uint32_t id = t.am + w.row, first = t.bn + w.col;
+        auto* sums = reinterpret_cast<Part*>(w.smem) + w.lane;
+#pragma unroll 1
+        for (uint32_t c = 0; c < w.chunks; ++c) {
+            const uint32_t row = first + 32 * c + w.lane;  // whose result this lane will have
+            const bool mine = 32 * c + w.lane < w.cols && row < rows;
+            const uint32_t target = mine ? targets[row] : SEL_INVALID_ID;
+            float v[32];
+            load(c, v);
+            if (id >= V) {
+#pragma unroll
+                for (uint32_t i = 0; i < 32; ++i) v[i] = -INFINITY;
+            }
+            // targets among this warp's 32 ids
+            uint32_t hits = __ballot_sync(kFull, target < V && target - (id - w.lane) < 32u);
+            while (hits) {
+                const uint32_t i = __ffs(hits) - 1;
+                hits &= hits - 1;
+                const uint32_t its = __shfl_sync(kFull, target, i);
+                if (its == id) {
+#pragma unroll
+                    for (uint32_t k = 0; k < 32; ++k) {
+                        if (k == i) {
+                            at[first + 32 * c + i] = v[k];
+                            v[k] = -INFINITY;
+                        }
+                    }
+                }
+            }
+            float m = -INFINITY;
+#pragma unroll
+            for (uint32_t i = 0; i < 32; ++i) {
+                const float top = ceilf(max_across(v[i]) * kLog2E);
+                v[i] = Weights(top)(v[i]);
+                if (w.lane == i) m = top;
+            }
+            Part p{m, sum_across(v)};
+            if (!w.first) {
+                const Part before = sums[32 * c];
+                const float top = fmaxf(p.m, before.m), ref = top == -INFINITY ? 0.0f : top;
+                p = {top, p.s * pow2(p.m - ref) + before.s * pow2(before.m - ref)};
+            }
+            sums[32 * c] = p;
+            if (w.last && mine)
+                parts[static_cast<uint64_t>(w.worker / row_tiles * 8 + w.row / 32) * rows + row] = p;
+        }
     }
 };
 
@@ -158,35 +264,45 @@ __device__ __forceinline__ void finish_row(const LossFinishArgs& a, uint32_t row
     if (a.lse) a.lse[row] = static_cast<float>(lse);
 }
 
-constexpr uint32_t kFinishThreads = 256;
+constexpr uint32_t kFinishThreads = 1024, kFinishWarps = kFinishThreads / 32;
 
 // kWide: 32 rows a block, a lane each, the slots spread over the warps; else a
 // row a block.
 template <bool kWide>
 __global__ void __launch_bounds__(kFinishThreads) loss_finish_kernel(LossFinishArgs a) {
-    __shared__ Joined sh[8][32];
+    __shared__ Joined sh[kFinishWarps][32];
     pdl_wait();
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t row = kWide ? blockIdx.x * 32 + lane : blockIdx.x;
     Joined j{-INFINITY, FF{0.0f, 0.0f}};
     if (row < a.rows) {
-        const uint32_t step = kWide ? 8 : kFinishThreads;
-#pragma unroll 4
+        const uint32_t step = kWide ? kFinishWarps : kFinishThreads;
+#pragma unroll 8
         for (uint32_t i = kWide ? warp : threadIdx.x; i < a.slots; i += step) {
             const Part p = a.parts[static_cast<uint64_t>(i) * a.rows + row];
             j = join(j, Joined{p.m, FF{p.s, 0.0f}});
         }
     }
-    if (!kWide) {
+    auto across = [](Joined v) {
 #pragma unroll
-        for (uint32_t m = 16; m > 0; m >>= 1)
-            j = join(j, Joined{__shfl_xor_sync(kFull, j.m, m), ff_shfl_xor(j.s, m)});
-    }
+        for (uint32_t m = 16; m > 0; m >>= 1) v = join(v, Joined{__shfl_xor_sync(kFull, v.m, m), ff_shfl_xor(v.s, m)});
+        return v;
+    };
+    if (!kWide) j = across(j);
     sh[warp][lane] = j;
     __syncthreads();
-    if (warp != 0 || row >= a.rows) return;
-    for (uint32_t i = 1; i < 8; ++i) j = join(j, sh[i][lane]);
-    if (kWide || lane == 0) finish_row(a, row, j);
+    if (kWide) {
+        // a warp takes a row, a lane another warp's share of it; the last steps, in 64
+        // bits, by the lanes of one warp
+        j = across(sh[lane][warp]);
+        __syncthreads();
+        if (lane == 0) sh[0][warp] = j;
+        __syncthreads();
+        if (warp == 0 && row < a.rows) finish_row(a, row, sh[0][lane]);
+    } else if (warp == 0) {
+        j = across(sh[lane][0]);
+        if (lane == 0) finish_row(a, row, j);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -200,72 +316,110 @@ constexpr float kProbShift = 0.0f;
 template <>
 constexpr float kProbShift<__half> = 14.0f;
 
-template <typename T, bool kPair>
+// 16 entries, rounded to T, as one 32-byte store: a whole sector a lane.
+template <typename T>
+__device__ __forceinline__ void store16(T* to, const float (&v)[32], uint32_t i) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(pack2<T>(v[i], v[i + 1])),
+                 "r"(pack2<T>(v[i + 2], v[i + 3])), "r"(pack2<T>(v[i + 4], v[i + 5])), "r"(pack2<T>(v[i + 6], v[i + 7])),
+                 "r"(pack2<T>(v[i + 8], v[i + 9])), "r"(pack2<T>(v[i + 10], v[i + 11])),
+                 "r"(pack2<T>(v[i + 12], v[i + 13])), "r"(pack2<T>(v[i + 14], v[i + 15]))
+                 : "memory");
+}
+
+// P of a piece: [its ids][hidden rows]. Hidden rows lie on the product's columns, so
+// that a tile has no more of them than it needs.
+template <typename T>
 struct ProbProblem {
     using Type = T;
-    CUtensorMap x, w, p;
+    CUtensorMap x, w;
+    T* p;
     const uint32_t* targets;
     const float* lse;
     const float* grad;
     uint32_t* error;
-    uint32_t rows, V, v0, width, steps;
+    uint32_t rows, V, v0, width, steps, n, pitch;
     Raster raster;
 
     __device__ __forceinline__ uint32_t count(uint32_t worker, uint32_t workers) const { return raster.share(worker, workers); }
     __device__ __forceinline__ GemmTile tile(uint32_t worker, uint32_t workers, uint32_t j) const {
-        uint32_t m, n;
-        raster.at(worker + j * workers, m, n);
-        return {&x, &w, m * GemmConfig<kPair>::kTileM, v0 + n * kTileN, 0, 0, steps, false, false};
+        uint32_t r, v;
+        raster.at(worker + j * workers, r, v);
+        return {&w, &x, v0 + v * kTileM, r * n, 0, 0, steps, n, false, false};
     }
     template <typename Load>
     __device__ __forceinline__ void epilogue(const GemmTile& t, const EpiWarp& w, Load load) const {
-        const uint32_t row = t.am + w.row, col = t.bn + w.col;
-        uint32_t target = SEL_INVALID_ID;
-        float ref = 0.0f, g = 0.0f;
-        if (row < rows) {
-            target = targets[row];
-            ref = lse[row];
-            g = grad[row];
+        const uint32_t id = t.am + w.row, first = t.bn + w.col;
+        // the warp's rows: lse, and of 32 a bit for those that do not count, and one for
+        // those whose target is among the warp's ids
+        auto* refs = reinterpret_cast<float*>(w.smem);
+        auto* bits = reinterpret_cast<uint2*>(w.smem + 512);
+        auto* ids = reinterpret_cast<uint32_t*>(w.smem + 544);
+        __syncwarp();
+        for (uint32_t c = 0; c < w.chunks; ++c) {
+            const uint32_t i = 32 * c + w.lane, row = first + i;
+            const uint32_t target = i < w.cols && row < rows ? targets[row] : SEL_INVALID_ID;
+            const bool live = target < V && grad[row] != 0.0f;
+            refs[i] = live ? lse[row] : 0.0f;
+            ids[i] = target;
+            const uint32_t dead = __ballot_sync(kFull, !live);
+            const uint32_t hits = __ballot_sync(kFull, live && target - (id - w.lane) < 32u);
+            if (w.lane == 0) bits[c] = make_uint2(dead, hits);
         }
-        const bool live = target < V && g != 0.0f;
+        __syncwarp();
         const float up = kProbShift<T>;
-        const uint32_t first = t.am + w.row - w.lane;
+        T* out = p + static_cast<uint64_t>(id - v0) * pitch + first;
+        const uint32_t cols = min(w.cols, first < pitch ? pitch - first : 0);
 #pragma unroll 1
-        for (uint32_t c = 0; c < 4; ++c) {
+        for (uint32_t c = 0; c < w.chunks; ++c) {
             float v[32];
             load(c, v);
-            const uint32_t c0 = col + 32 * c;
-            const bool mine = any_target(target, c0);
-            float z = 0.0f;
-#pragma unroll
-            for (uint32_t i = 0; i < 32; ++i) {
-                const float d = v[i] - ref;
-                if (mine && target == c0 + i) z = d;
-                v[i] = live ? ex2_approx(fmaf(d, kLog2E, up)) : 0.0f;
-            }
-            if (mine && live) {
-                z = expm1f(z) * exp2f(up);
+            const uint2 of = bits[c];
+            // targets' entries, rare, through shared memory: a lane may have several
+            auto* kept = reinterpret_cast<float*>(w.smem + 1056);
+            if (of.y) {
 #pragma unroll
                 for (uint32_t i = 0; i < 32; ++i)
-                    if (target == c0 + i) v[i] = z;
+                    if ((of.y >> i & 1) && ids[32 * c + i] == id) kept[i] = expm1f(v[i] - refs[32 * c + i]) * exp2f(up);
             }
-            const uint32_t x = t.bn - v0 + w.col + (c / 2) * 64;
-            store_chunk<T>(w, &p, x, first, c, x < width && first < rows, v);
+#pragma unroll
+            for (uint32_t i = 0; i < 32; i += 4) {
+                const float4 r = *reinterpret_cast<const float4*>(refs + 32 * c + i);
+                v[i] = ex2_approx(fmaf(v[i] - r.x, kLog2E, up));
+                v[i + 1] = ex2_approx(fmaf(v[i + 1] - r.y, kLog2E, up));
+                v[i + 2] = ex2_approx(fmaf(v[i + 2] - r.z, kLog2E, up));
+                v[i + 3] = ex2_approx(fmaf(v[i + 3] - r.w, kLog2E, up));
+            }
+            if (of.y) {
+#pragma unroll
+                for (uint32_t i = 0; i < 32; ++i)
+                    if ((of.y >> i & 1) && ids[32 * c + i] == id) v[i] = kept[i];
+            }
+            if (of.x) {
+#pragma unroll
+                for (uint32_t i = 0; i < 32; ++i)
+                    if (of.x >> i & 1) v[i] = 0.0f;
+            }
+            if (id - v0 < width) {
+#pragma unroll
+                for (uint32_t i = 0; i < 32; i += 16)
+                    if (32 * c + i < cols) store16<T>(out + 32 * c + i, v, i);
+            }
         }
     }
 };
 
 // Items of a worker: its tiles of dX first, each a long sum, then its tiles of dW.
-template <typename T, bool kPair>
+template <typename T>
 struct GradsProblem {
     using Type = T;
-    CUtensorMap p_mn, x_mn, dw, p_k, w_mn;
+    CUtensorMap p_k, x_mn, dw, p_mn, w_mn;
     const float* scale;  // of dW: the largest gradient, less P's shift
     float* acc;          // [slices][rows][H]
     uint32_t* error;
     uint32_t rows, V, H, v0, width;
-    uint32_t ht;                       // column tiles of both
-    uint32_t dx_tiles, dx_items, k_slice;  // k_slice: columns of P a slice sums
+    uint32_t n_rows, row_tiles;            // dX: columns a tile
+    uint32_t dx_tiles, dx_items, k_slice;  // k_slice: ids of the piece a slice sums
+    uint32_t h_tiles;                      // dW: column tiles, the last of 128 where that is enough
     uint32_t dw_items, dw_steps, extra;    // extra: dW tiles ahead for workers with one dX tile less
     bool add;
 
@@ -279,53 +433,49 @@ struct GradsProblem {
         return dx_count(worker, workers) + dw + (worker >= more ? extra : 0);
     }
     __device__ __forceinline__ GemmTile tile(uint32_t worker, uint32_t workers, uint32_t j) const {
-        constexpr uint32_t kTileM = GemmConfig<kPair>::kTileM;
-        const uint32_t n_dx = dx_count(worker, workers);
-        if (j < n_dx) {
+        const uint32_t dx = dx_count(worker, workers);
+        if (j < dx) {
             const uint32_t i = worker + j * workers, slice = i / dx_tiles, at = i - slice * dx_tiles;
             const uint32_t k0 = slice * k_slice, k1 = min(width, k0 + k_slice);
             // (an empty slice sums one step of zeros past the piece's end)
             const uint32_t steps = k1 > k0 ? (k1 - k0 + kStepK - 1) / kStepK : 1;
-            return {&p_k, &w_mn, at / ht * kTileM, at % ht * kTileN, k0, v0 + k0, steps, false, true};
+            return {&w_mn, &p_mn, at / row_tiles * kTileM, at % row_tiles * n_rows, v0 + k0, k0, steps, n_rows, true, true};
         }
         const uint32_t more = dx_items % workers, light = workers - more, e = worker >= more ? extra : 0;
-        j -= n_dx;
+        j -= dx;
         const uint32_t i = j < e ? worker - more + j * light : extra * light + worker + (j - e) * workers;
-        return {&p_mn, &x_mn, i / ht * kTileM, i % ht * kTileN, 0, 0, dw_steps, true, true};
+        const uint32_t h = i % h_tiles * kTileN;
+        return {&p_k, &x_mn, i / h_tiles * kTileM, h, 0, 0, dw_steps, H - h <= kTileN / 2 ? kTileN / 2 : kTileN, false, true};
     }
     template <typename Load>
     __device__ __forceinline__ void epilogue(const GemmTile& t, const EpiWarp& w, Load load) const {
-        if (t.a_mn) {
+        if (!t.a_mn) {
             const float s = *scale;
-            const uint32_t first = v0 + t.am + w.row - w.lane;
+            const uint32_t id = v0 + t.am + w.row - w.lane;
 #pragma unroll 1
-            for (uint32_t c = 0; c < 4; ++c) {
+            for (uint32_t c = 0; c < w.chunks; ++c) {
                 float v[32];
                 load(c, v);
 #pragma unroll
                 for (uint32_t i = 0; i < 32; ++i) v[i] *= s;
-                const uint32_t x = t.bn + w.col + (c / 2) * 64;
-                store_chunk<T>(w, &dw, x, first, c, x < H && first < V, v);
+                const uint32_t x = t.bn + w.col + c / 2 * 64;
+                store_chunk<T>(w, &dw, x, id, c, x < H && id < V, v);
             }
         } else {
-            const uint32_t row = t.am + w.row, slice = t.ak / k_slice;
-            float* o = acc + (static_cast<uint64_t>(slice) * rows + row) * H;
+            const uint32_t h = t.am + w.row, slice = t.bk / k_slice, first = t.bn + w.col;
+            float* o = acc + (static_cast<uint64_t>(slice) * rows + first) * H + h;
 #pragma unroll 1
-            for (uint32_t c = 0; c < 4; ++c) {
+            for (uint32_t c = 0; c < w.chunks; ++c) {
                 float v[32];
                 load(c, v);
-                const uint32_t x = t.bn + w.col + c * 32;
-                if (row < rows) {
+                const uint32_t n = min(w.cols, first < rows ? rows - first : 0);
+                if (h < H) {
 #pragma unroll
-                    for (uint32_t i = 0; i < 32; i += 4) {
-                        if (x + i >= H) break;
-                        float4* q = reinterpret_cast<float4*>(o + x + i);
-                        float4 r = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-                        if (add) {
-                            const float4 b = *q;
-                            r = make_float4(r.x + b.x, r.y + b.y, r.z + b.z, r.w + b.w);
+                    for (uint32_t i = 0; i < 32; ++i) {
+                        if (32 * c + i < n) {
+                            float* q = o + static_cast<uint64_t>(32 * c + i) * H;
+                            *q = add ? *q + v[i] : v[i];
                         }
-                        *q = r;
                     }
                 }
             }
@@ -442,47 +592,63 @@ __global__ void __launch_bounds__(kPrepThreads) grad_finish_kernel(GradFinishArg
 // host side
 // ---------------------------------------------------------------------------
 
-// Up to 128 rows fill one CTA's tile; a pair's second CTA would compute nothing.
-inline bool use_pair(uint32_t rows) { return rows > kCtaM; }
-inline uint32_t tile_m(uint32_t rows) { return use_pair(rows) ? 2 * kCtaM : kCtaM; }
+// Hidden rows on a product's columns: tiles of up to 256, all alike, a multiple of 16.
+struct Columns {
+    uint32_t n, tiles;
+    explicit Columns(uint32_t rows) {
+        n = ceil_div(ceil_div(rows, ceil_div(rows, kTileN)), 16) * 16;
+        tiles = ceil_div(rows, n);
+    }
+    uint32_t padded() const { return n * tiles; }
+};
 
 inline bool sizes_fit(uint32_t rows, uint32_t V, uint32_t H) {
-    const uint64_t m = ceil_div(rows, kCtaM), n = ceil_div(V, kCtaM), h = ceil_div(H, kTileN);
+    const uint64_t m = ceil_div(rows, 128), n = ceil_div(V, 128), h = ceil_div(H, 128);
     return rows <= 0x7fffffffu && m * n < (1ull << 31) && n * h < (1ull << 31) && m * h * 64 < (1ull << 31);
 }
 
+constexpr uint32_t kMaxWorkers = 96;  // (the workspace's size goes by no device)
+
 struct LossPlan {
-    uint32_t nt;
+    bool columns;  // hidden rows on the products' columns
+    uint32_t slots;
     size_t at, parts, bytes;
 };
+// Rows on the columns pad less, but their workers are a multiple of the row tiles
+// (of some 76).
 inline LossPlan loss_plan(uint32_t rows, uint32_t V) {
     LossPlan p;
-    p.nt = ceil_div(V, kTileN);
+    const Columns c(rows);
+    p.columns = c.tiles <= 76 && static_cast<uint64_t>(ceil_div(rows, kTileM)) * kTileM * (76 / c.tiles * c.tiles) >
+                                     static_cast<uint64_t>(c.padded()) * 76;
+    p.slots = 2 * ceil_div(V, kTileN);
+    if (p.columns) p.slots = std::max(p.slots, 8 * kMaxWorkers);
     p.at = kWsHeaderBytes;
     p.parts = p.at + align_up(static_cast<size_t>(rows) * sizeof(float), 256);
-    p.bytes = p.parts + align_up(static_cast<size_t>(2 * p.nt) * rows * sizeof(Part), 256);
+    p.bytes = p.parts + align_up(static_cast<size_t>(p.slots) * rows * sizeof(Part), 256);
     return p;
 }
 
 // The vocabulary in pieces: as few as keep P within 2^28 entries, but none below
-// 16,384 columns, and all alike.
+// 16,384 ids, and all alike.
 struct GradPlan {
-    uint32_t piece, pieces, slices;
+    uint32_t piece, pieces, slices, pitch, dx_n;
     size_t scaled, acc, p, bytes;
 };
 inline GradPlan grad_plan(uint32_t rows, uint32_t V, uint32_t H) {
     GradPlan g;
-    const uint32_t cap = static_cast<uint32_t>(std::max<uint64_t>(16384, (1ull << 28) / rows));
-    g.piece = ceil_div(ceil_div(V, ceil_div(V, cap)), kTileN) * kTileN;
+    const uint64_t cap = std::max<uint64_t>(16384, (1ull << 28) / rows);
+    g.piece = ceil_div(ceil_div(V, ceil_div(V, cap)), kTileM) * kTileM;
     g.pieces = ceil_div(V, g.piece);
+    g.pitch = ceil_div(rows, 16) * 16;
     // few tiles of dX: the sum over the piece is split
-    const uint64_t tiles = static_cast<uint64_t>(ceil_div(rows, tile_m(rows))) * ceil_div(H, kTileN);
-    const uint32_t workers = use_pair(rows) ? 76 : 152;
-    g.slices = std::min(std::max(1u, g.piece / 1024), tiles >= workers ? 1u : ceil_div(workers, tiles));
+    g.dx_n = rows <= kTileN ? ceil_div(rows, 16) * 16 : kTileN;
+    const uint64_t tiles = static_cast<uint64_t>(ceil_div(H, kTileM)) * ceil_div(rows, g.dx_n);
+    g.slices = std::min(std::max(1u, g.piece / 1024), tiles >= 76 ? 1u : ceil_div(76, tiles));
     g.scaled = kWsHeaderBytes;
     g.acc = g.scaled + align_up(static_cast<size_t>(rows) * H * 2, 256);
     g.p = g.acc + align_up(static_cast<size_t>(g.slices) * rows * H * sizeof(float), 256);
-    g.bytes = g.p + static_cast<size_t>(rows) * g.piece * 2;
+    g.bytes = g.p + static_cast<size_t>(g.pitch) * g.piece * 2;
     return g;
 }
 
@@ -500,44 +666,66 @@ struct HeadLossCall {
     cudaStream_t stream;
 };
 
-template <typename T, bool kPair>
+template <typename T>
 sel_status run_loss(const HeadLossCall& c, float* loss, float* lse) {
-    using C = GemmConfig<kPair>;
     const int sms = device_sms();
-    if (sms <= 0) return SEL_ECUDA;
+    if (sms < 2) return SEL_ECUDA;
     const LossPlan plan = loss_plan(c.rows, c.V);
-    LossProblem<T, kPair> p{};
-    if (!map16(&p.x, c.x, c.H, c.rows, kStepK, kCtaM) || !map16(&p.w, c.w, c.H, c.V, kStepK, C::kCtaN)) return SEL_ECUDA;
-    p.targets = c.targets;
-    p.at = reinterpret_cast<float*>(c.ws + plan.at);
-    p.parts = reinterpret_cast<Part*>(c.ws + plan.parts);
-    p.error = reinterpret_cast<uint32_t*>(c.ws);
-    p.rows = c.rows;
-    p.V = c.V;
-    p.steps = ceil_div(c.H, kStepK);
-    p.raster = {ceil_div(c.rows, C::kTileM), plan.nt};
-    const uint32_t workers = std::min<uint32_t>(kPair ? sms / 2 : sms, p.raster.mt * p.raster.nt);
-    if (const sel_status s = launch_gemm<LossProblem<T, kPair>, kPair>(p, workers, c.stream); s != SEL_OK) return s;
-    const LossFinishArgs f{p.parts, p.at, c.targets, p.error, loss, lse, c.rows, c.V, 2 * plan.nt};
+    auto* at = reinterpret_cast<float*>(c.ws + plan.at);
+    auto* parts = reinterpret_cast<Part*>(c.ws + plan.parts);
+    auto* error = reinterpret_cast<uint32_t*>(c.ws);
+    const uint32_t v_tiles = ceil_div(c.V, kTileM);
+    uint32_t workers = std::min<uint32_t>(sms / 2, kMaxWorkers), slots;
+    auto launch = [&](auto& p, uint32_t x_box) {
+        if (!map16(&p.x, c.x, c.H, c.rows, kStepK, x_box) || !map16(&p.w, c.w, c.H, c.V, kStepK, kCtaM)) return SEL_ECUDA;
+        p.targets = c.targets;
+        p.at = at;
+        p.parts = parts;
+        p.error = error;
+        p.rows = c.rows;
+        p.V = c.V;
+        p.steps = ceil_div(c.H, kStepK);
+        return launch_gemm(p, workers, c.stream);
+    };
+    sel_status st;
+    const Columns cols(c.rows);
+    if (plan.columns && cols.tiles <= workers) {
+        const uint32_t each = std::min(workers / cols.tiles, v_tiles);  // workers of a row tile
+        workers = each * cols.tiles;
+        slots = 8 * each;
+        LossColumnsProblem<T> p{};
+        p.n = cols.n;
+        p.row_tiles = cols.tiles;
+        p.v_tiles = v_tiles;
+        st = launch(p, cols.n / 2);
+    } else {
+        LossProblem<T> p{};
+        p.raster = {ceil_div(c.rows, kTileM), v_tiles};
+        slots = 2 * v_tiles;
+        workers = std::min(workers, p.raster.mt * p.raster.nt);
+        st = launch(p, kCtaM);
+    }
+    if (st != SEL_OK) return st;
+    const LossFinishArgs f{parts, at, c.targets, error, loss, lse, c.rows, c.V, slots};
     const cudaError_t e = c.rows >= 64
                               ? launch_pdl(loss_finish_kernel<true>, dim3(ceil_div(c.rows, 32)), dim3(kFinishThreads), 0, c.stream, f)
                               : launch_pdl(loss_finish_kernel<false>, dim3(c.rows), dim3(kFinishThreads), 0, c.stream, f);
     return e == cudaSuccess ? SEL_OK : SEL_ECUDA;
 }
 
-template <typename T, bool kPair>
+template <typename T>
 sel_status run_grad(const HeadLossCall& c, const float* lse, const float* grad, void* dx, void* dw) {
-    using C = GemmConfig<kPair>;
     const int sms = device_sms();
-    if (sms <= 0) return SEL_ECUDA;
+    if (sms < 2) return SEL_ECUDA;
     const GradPlan plan = grad_plan(c.rows, c.V, c.H);
+    const Columns rows(c.rows);
     auto* error = reinterpret_cast<uint32_t*>(c.ws);
     auto* scale = reinterpret_cast<float*>(c.ws + 16);
     auto* acc = reinterpret_cast<float*>(c.ws + plan.acc);
     void* prob = c.ws + plan.p;
     void* scaled = c.ws + plan.scaled;
     const float down = 1.0f / static_cast<float>(1u << static_cast<uint32_t>(kProbShift<T>));
-    const uint32_t vecs = c.H / 8, all = kPair ? sms / 2 : sms;
+    const uint32_t vecs = c.H / 8, all = sms / 2;
     const uint32_t blocks = static_cast<uint32_t>(std::min<uint64_t>(2 * sms, ceil_div(static_cast<uint64_t>(c.rows) * vecs, kPrepThreads)));
     if (dw) {
         const PrepArgs a{static_cast<const uint4*>(c.x), static_cast<uint4*>(scaled), c.targets, grad, scale, c.rows, c.V, vecs, down};
@@ -545,11 +733,10 @@ sel_status run_grad(const HeadLossCall& c, const float* lse, const float* grad, 
     }
     for (uint32_t i = 0; i < plan.pieces; ++i) {
         const uint32_t v0 = i * plan.piece, width = std::min(plan.piece, c.V - v0);
-        const uint64_t pitch = static_cast<uint64_t>(plan.piece) * 2;
-        ProbProblem<T, kPair> p{};
-        if (!map16(&p.x, c.x, c.H, c.rows, kStepK, kCtaM) || !map16(&p.w, c.w, c.H, c.V, kStepK, C::kCtaN) ||
-            !map16(&p.p, prob, width, c.rows, 64, 32, pitch))
-            return SEL_ECUDA;
+        const uint64_t pitch = static_cast<uint64_t>(plan.pitch) * 2;
+        ProbProblem<T> p{};
+        if (!map16(&p.x, c.x, c.H, c.rows, kStepK, rows.n / 2) || !map16(&p.w, c.w, c.H, c.V, kStepK, kCtaM)) return SEL_ECUDA;
+        p.p = static_cast<T*>(prob);
         p.targets = c.targets;
         p.lse = lse;
         p.grad = grad;
@@ -559,14 +746,13 @@ sel_status run_grad(const HeadLossCall& c, const float* lse, const float* grad, 
         p.v0 = v0;
         p.width = width;
         p.steps = ceil_div(c.H, kStepK);
-        p.raster = {ceil_div(c.rows, C::kTileM), ceil_div(width, kTileN)};
-        if (const sel_status s = launch_gemm<ProbProblem<T, kPair>, kPair>(
-                p, std::min(all, p.raster.mt * p.raster.nt), c.stream);
-            s != SEL_OK)
-            return s;
-        GradsProblem<T, kPair> g{};
-        if (!map16(&g.p_mn, prob, width, c.rows, 64, kStepK, pitch) || !map16(&g.x_mn, scaled, c.H, c.rows, 64, kStepK) ||
-            (dw && !map16(&g.dw, dw, c.H, c.V, 64, 32)) || !map16(&g.p_k, prob, width, c.rows, kStepK, kCtaM, pitch) ||
+        p.n = rows.n;
+        p.pitch = plan.pitch;
+        p.raster = {rows.tiles, ceil_div(width, kTileM)};
+        if (const sel_status s = launch_gemm(p, std::min(all, p.raster.mt * p.raster.nt), c.stream); s != SEL_OK) return s;
+        GradsProblem<T> g{};
+        if (!map16(&g.p_k, prob, c.rows, width, kStepK, kCtaM, pitch) || !map16(&g.x_mn, scaled, c.H, c.rows, 64, kStepK) ||
+            (dw && !map16(&g.dw, dw, c.H, c.V, 64, 32)) || !map16(&g.p_mn, prob, c.rows, width, 64, kStepK, pitch) ||
             !map16(&g.w_mn, c.w, c.H, c.V, 64, kStepK))
             return SEL_ECUDA;
         g.scale = scale;
@@ -577,17 +763,19 @@ sel_status run_grad(const HeadLossCall& c, const float* lse, const float* grad, 
         g.H = c.H;
         g.v0 = v0;
         g.width = width;
-        g.ht = ceil_div(c.H, kTileN);
-        g.dx_tiles = p.raster.mt * g.ht;
+        g.n_rows = plan.dx_n;
+        g.row_tiles = ceil_div(c.rows, plan.dx_n);
+        g.dx_tiles = ceil_div(c.H, kTileM) * g.row_tiles;
         g.dx_items = dx ? g.dx_tiles * plan.slices : 0;
         g.k_slice = ceil_div(ceil_div(plan.piece, plan.slices), kStepK) * kStepK;
-        g.dw_items = dw ? ceil_div(width, C::kTileM) * g.ht : 0;
+        g.h_tiles = ceil_div(c.H, kTileN);
+        g.dw_items = dw ? ceil_div(width, kTileM) * g.h_tiles : 0;
         g.dw_steps = ceil_div(c.rows, kStepK);
         g.add = i > 0;
         const uint32_t workers = std::min(all, g.dx_items + g.dw_items);
         const uint32_t light = workers - g.dx_items % workers;
         g.extra = light == workers ? 0 : std::min(g.dw_items / light, (g.k_slice / kStepK) / (g.dw_steps + 2));
-        if (const sel_status s = launch_gemm<GradsProblem<T, kPair>, kPair>(g, workers, c.stream); s != SEL_OK) return s;
+        if (const sel_status s = launch_gemm(g, workers, c.stream); s != SEL_OK) return s;
     }
     const GradFinishArgs f{acc, c.targets, grad, error, static_cast<uint4*>(dx), static_cast<uint4*>(dw), c.rows, c.V, vecs, plan.slices, down};
     return launch_pdl(grad_finish_kernel<T>, dim3(blocks), dim3(kPrepThreads), 0, c.stream, f) == cudaSuccess ? SEL_OK : SEL_ECUDA;
@@ -625,8 +813,7 @@ extern "C" sel_status sel_head_loss(const void* d_hidden, uint32_t rows, const v
     if (!d_ws || misaligned(d_ws, SEL_WS_ALIGN)) return SEL_EINVAL;
     if (ws_bytes < head_loss_ws_bytes(rows, V, H)) return SEL_EWORKSPACE;
     const HeadLossCall c{d_hidden, d_weight, d_targets, rows, V, H, static_cast<unsigned char*>(d_ws), stream};
-    if (dtype == SEL_F16) return use_pair(rows) ? run_loss<__half, true>(c, d_loss, d_lse) : run_loss<__half, false>(c, d_loss, d_lse);
-    return use_pair(rows) ? run_loss<__nv_bfloat16, true>(c, d_loss, d_lse) : run_loss<__nv_bfloat16, false>(c, d_loss, d_lse);
+    return dtype == SEL_F16 ? run_loss<__half>(c, d_loss, d_lse) : run_loss<__nv_bfloat16>(c, d_loss, d_lse);
 }
 
 extern "C" sel_status sel_head_loss_grad(const void* d_hidden, uint32_t rows, const void* d_weight, int dtype, uint32_t V,
@@ -644,9 +831,6 @@ extern "C" sel_status sel_head_loss_grad(const void* d_hidden, uint32_t rows, co
     if (!d_ws || misaligned(d_ws, SEL_WS_ALIGN)) return SEL_EINVAL;
     if (ws_bytes < head_loss_grad_ws_bytes(rows, V, H)) return SEL_EWORKSPACE;
     const HeadLossCall c{d_hidden, d_weight, d_targets, rows, V, H, static_cast<unsigned char*>(d_ws), stream};
-    if (dtype == SEL_F16)
-        return use_pair(rows) ? run_grad<__half, true>(c, d_lse, d_grad, d_hidden_grad, d_weight_grad)
-                              : run_grad<__half, false>(c, d_lse, d_grad, d_hidden_grad, d_weight_grad);
-    return use_pair(rows) ? run_grad<__nv_bfloat16, true>(c, d_lse, d_grad, d_hidden_grad, d_weight_grad)
-                          : run_grad<__nv_bfloat16, false>(c, d_lse, d_grad, d_hidden_grad, d_weight_grad);
+    return dtype == SEL_F16 ? run_grad<__half>(c, d_lse, d_grad, d_hidden_grad, d_weight_grad)
+                            : run_grad<__nv_bfloat16>(c, d_lse, d_grad, d_hidden_grad, d_weight_grad);
 }
