@@ -622,8 +622,7 @@ inline LossPlan loss_plan(uint32_t rows, uint32_t V) {
     const Columns c(rows);
     p.columns = c.tiles <= 76 && static_cast<uint64_t>(ceil_div(rows, kTileM)) * kTileM * (76 / c.tiles * c.tiles) >
                                      static_cast<uint64_t>(c.padded()) * 76;
-    p.slots = 2 * ceil_div(V, kTileN);
-    if (p.columns) p.slots = std::max(p.slots, 8 * kMaxWorkers);
+    p.slots = std::max(2 * ceil_div(V, kTileN), 8 * kMaxWorkers);  // (of either form, so that more rows take no less)
     p.at = kWsHeaderBytes;
     p.parts = p.at + align_up(static_cast<size_t>(rows) * sizeof(float), 256);
     p.bytes = p.parts + align_up(static_cast<size_t>(p.slots) * rows * sizeof(Part), 256);
@@ -638,10 +637,10 @@ struct GradPlan {
 };
 inline GradPlan grad_plan(uint32_t rows, uint32_t V, uint32_t H) {
     GradPlan g;
-    const uint64_t cap = std::max<uint64_t>(16384, (1ull << 28) / rows);
+    g.pitch = ceil_div(rows, 16) * 16;
+    const uint64_t cap = std::max<uint64_t>(16384, (1ull << 28) / g.pitch);
     g.piece = ceil_div(ceil_div(V, ceil_div(V, cap)), kTileM) * kTileM;
     g.pieces = ceil_div(V, g.piece);
-    g.pitch = ceil_div(rows, 16) * 16;
     // few tiles of dX: the sum over the piece is split
     // dX's columns a tile: equal tiles pad less, but their halves begin anywhere in a
     // line of P and are copied 64 rows at a time: 777 rows (4 x 208 or 4 x 256) 578 us
@@ -652,8 +651,13 @@ inline GradPlan grad_plan(uint32_t rows, uint32_t V, uint32_t H) {
     g.slices = std::min(std::max(1u, g.piece / 1024), tiles >= 76 ? 1u : ceil_div(76, tiles));
     g.scaled = kWsHeaderBytes;
     g.acc = g.scaled + align_up(static_cast<size_t>(rows) * H * 2, 256);
-    g.p = g.acc + align_up(static_cast<size_t>(g.slices) * rows * H * sizeof(float), 256);
-    g.bytes = g.p + static_cast<size_t>(g.pitch) * g.piece * 2;
+    // What the sums and P take at most: slices * tiles < 76 + tiles, and P as above;
+    // these bounds grow with each size, so that a workspace serves smaller calls too.
+    const size_t sums = static_cast<size_t>(std::min(rows, kTileN)) * std::min(H, kTileM) * 76 + static_cast<size_t>(rows) * H;
+    const size_t whole = static_cast<size_t>(g.pitch) * (ceil_div(V, kTileM) * static_cast<size_t>(kTileM));
+    const size_t most = std::max<size_t>(g.pitch * 16384ull, 1ull << 28) + g.pitch * static_cast<size_t>(kTileM);
+    g.p = g.acc + align_up(sums * sizeof(float), 256);
+    g.bytes = g.p + std::min(whole, most) * 2;
     return g;
 }
 

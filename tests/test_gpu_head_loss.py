@@ -8,6 +8,7 @@ from sampling_row_fp32_gb300 import binding as B
 
 pytestmark = pytest.mark.gpu
 
+NAN = float("nan")
 DT = {"f16": torch.float16, "bf16": torch.bfloat16}
 
 
@@ -133,3 +134,228 @@ def test_grad(rows, V, H, dtype):
     x, w, t, grad = make(rows + V, rows, V, H, dtype)
     _, lse = run_loss(x, w, t)
     check_grad(x, w, t, lse, grad)
+
+
+@pytest.mark.parametrize("rows,V,H", [(16_400, 17_000, 64), (1, 151_936, 256), (20, 60_001, 512), (300, 40_000, 72)])
+def test_pieces_and_long_vocabularies(rows, V, H):
+    x, w, t, grad = make(rows, rows, V, H, "bf16")
+    _, lse = check_loss(x, w, t)
+    check_grad(x, w, t, lse, grad)
+
+
+def test_equal_gradients_round_hidden_rows_once():
+    """A mean's gradients: hidden rows enter dW unrounded, and check_grad allows nothing for them."""
+    x, w, t, _ = make(3, 200, 500, 64, "bf16")
+    _, lse = run_loss(x, w, t)
+    check_grad(x, w, t, lse, torch.full((200,), 1 / 160, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_gradients_of_both_signs_and_very_different_sizes(dtype):
+    x, w, t, grad = make(4, 140, 300, 128, dtype)
+    grad = grad * torch.where(torch.arange(140, device="cuda") % 3 == 0, -1.0, 1.0)
+    grad = grad * 2.0 ** -(torch.arange(140, device="cuda") % 9)
+    _, lse = run_loss(x, w, t)
+    check_grad(x, w, t, lse, grad)
+
+
+@pytest.mark.parametrize("rows", [5, 260])
+def test_one_output_alone_is_the_same(rows):
+    x, w, t, grad = make(5, rows, 700, 200, "bf16")
+    _, lse = run_loss(x, w, t)
+    dx, dw = run_grad(x, w, t, lse, grad)
+    ws = B.workspace(B.SEL_OP_HEAD_LOSS_GRAD, rows, 700, 200)
+    a, b = torch.full_like(x, 9.0), torch.full_like(w, 9.0)
+    B.sel_head_loss_grad(x, w, t, lse, grad, a, None, ws)
+    B.sel_head_loss_grad(x, w, t, lse, grad, None, b, ws)
+    assert torch.equal(b, dw)
+    # (dX's sums are split alike whether dW is there or not)
+    assert torch.equal(a, dx)
+
+
+@pytest.mark.parametrize("rows", [3, 200])
+def test_rows_that_do_not_count_hold_anything(rows):
+    x, w, t, grad = make(6, rows, 400, 96, "bf16", ignored=0.0)
+    t[0], t[2] = -1, 400  # (the first id past the vocabulary)
+    if rows > 100:
+        t[100] = 0x7FFFFFFF
+        grad[150] = 0.0
+    x[0], grad[2] = NAN, NAN
+    loss, lse = run_loss(x, w, t)
+    assert not loss[[0, 2]].any() and torch.isfinite(loss).all() and torch.isnan(lse[0])
+    dx, dw = run_grad(x, w, t, lse, grad)
+    assert torch.isfinite(dx).all() and torch.isfinite(dw).all() and not dx[[0, 2]].any()
+    clean = x.clone()
+    clean[0] = 0
+    g = torch.nan_to_num(grad)
+    same = run_grad(clean, w, t, run_loss(clean, w, t)[1], g)
+    assert torch.equal(dx, same[0]) and torch.equal(dw, same[1])
+
+
+@pytest.mark.parametrize("rows", [2, 300])
+def test_no_row_counts(rows):
+    x, w, t, grad = make(7, rows, 300, 64, "f16")
+    t.fill_(-1)
+    loss, lse = run_loss(x, w, t)
+    assert not loss.any() and torch.allclose(lse.double(), L.head_loss(x, w, t)[1], atol=1e-4)
+    dx, dw = run_grad(x, w, t, lse, grad)
+    assert not dx.any() and not dw.any()
+
+
+@pytest.mark.parametrize("rows", [4, 260])
+def test_nonfinite_values_reach_what_they_are_part_of(rows):
+    x, w, t, grad = make(8, rows, 500, 64, "bf16", ignored=0.0)
+    x[1, 3] = NAN
+    x[2] = 0
+    x[2, 5] = float("inf")  # infinities of both signs among its logits
+    loss, lse = run_loss(x, w, t)
+    bad = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    bad[1:3] = True
+    assert torch.equal(torch.isnan(loss), bad) and torch.equal(torch.isnan(lse), bad)
+    dx, dw = run_grad(x, w, t, lse, grad)
+    assert torch.isnan(dx[1:3]).all() and torch.isfinite(dx[~bad]).all() and torch.isnan(dw).all()
+    # a weight of -Inf where the hidden row is positive: a logit of -Inf, a probability of 0
+    x, w, t, grad = make(9, rows, 500, 64, "bf16", ignored=0.0)
+    x[:, 7] = x[:, 7].abs() + 0.5
+    w[77, 7] = -float("inf")
+    t[0] = 77
+    loss, lse = run_loss(x, w, t)
+    assert loss[0] == float("inf") and torch.isfinite(loss[1:][t[1:] != 77]).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("rows", [1, 40, 256])
+@pytest.mark.parametrize("scale", [2.0 ** 8, 2.0 ** 30, 2.0 ** 60])
+def test_logits_of_any_size(rows, scale):
+    """Logits so far apart that one id has all the weight: the loss is their difference."""
+    x, w, t, _ = make(10, rows, 300, 64, "bf16", ignored=0.0)
+    loss, lse = run_loss((x.double() * scale).to(x.dtype), w, t)
+    z = x.double() @ w.double().T * scale
+    want = torch.logsumexp(z, 1)
+    tol = 2 * logit_error(x, w).max(dim=1).values * scale + 2.0 ** -19 + 2.0 ** -22 * want.abs()
+    assert ((lse.double() - want).abs() <= tol).all()
+    assert ((loss.double() - (want - z[torch.arange(rows), t.long()])).abs() <= 2 * tol).all()
+
+
+def test_confident_rows_keep_the_bits_of_their_losses():
+    """Losses down to 1e-30: relative precision, as the definition has it."""
+    H, V = 64, 300
+    w = torch.zeros(V, H, device="cuda", dtype=torch.bfloat16)
+    w[:, 0] = torch.arange(V, device="cuda") % 2 * 0.125
+    w[5, 0], w[5, 1] = 0, 1.0
+    x = torch.zeros(70, H, device="cuda", dtype=torch.bfloat16)
+    x[:, 0] = 1.0
+    x[:, 1] = torch.arange(70, device="cuda").bfloat16()  # the target's logit: whole numbers, exact
+    t = torch.full((70,), 5, dtype=torch.int32, device="cuda")
+    loss, _ = run_loss(x, w, t)
+    want, _ = L.head_loss(x, w, t)
+    assert want.min() < 1e-27
+    assert ((loss.double() / want - 1).abs() < 2.0 ** -18).all()
+
+
+@pytest.mark.parametrize("rows", [5, 90, 300])
+def test_results_do_not_depend_on_the_run_or_the_workspace(rows):
+    """The same bits from a workspace full of anything but its error word, and with
+    other work on a second stream."""
+    x, w, t, grad = make(11, rows, 5000, 264, "f16")
+    loss, lse = run_loss(x, w, t)
+    dx, dw = run_grad(x, w, t, lse, grad)
+    side = torch.cuda.Stream()
+    ws = [B.workspace(op, 400, 6000, 512) for op in (B.SEL_OP_HEAD_LOSS, B.SEL_OP_HEAD_LOSS_GRAD)]
+    other = B.workspace(B.SEL_OP_HEAD_LOSS, rows, 5000, 264), torch.empty(rows, device="cuda")
+    torch.cuda.synchronize()
+    for fill in (0, 255, 127):
+        for b in ws:
+            b[4:].fill_(fill)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            B.sel_head_loss(x, w, t, other[1], None, other[0], side)
+        again = run_loss(x, w, t, ws=ws[0])
+        assert torch.equal(loss, again[0]) and torch.equal(lse, again[1])
+        again = run_grad(x, w, t, lse, grad, ws=ws[1])
+        assert torch.equal(dx, again[0]) and torch.equal(dw, again[1])
+    assert torch.equal(other[1], loss)
+
+
+def test_no_rows():
+    x, w, t, grad = make(0, 0, 10, 64, "bf16")
+    e = torch.empty(0, device="cuda")
+    B.sel_head_loss(x, w, t, e, e, None)
+    dw = torch.full_like(w, 5.0)
+    B.sel_head_loss_grad(x, w, t, e, e, x, dw, None)
+    assert not dw.any()
+
+
+def test_uint32_targets_and_no_lse():
+    x, w, t, _ = make(12, 33, 200, 64, "bf16")
+    loss, _ = run_loss(x, w, t)
+    got = torch.empty_like(loss)
+    B.sel_head_loss(x, w, t.view(torch.uint32), got, None, B.workspace(B.SEL_OP_HEAD_LOSS, 33, 200, 64))
+    assert torch.equal(got, loss)
+
+
+def test_a_raised_error_word_fails_every_row():
+    """What a wait that runs out does: here the word is raised by the host."""
+    x, w, t, grad = make(13, 20, 300, 64, "bf16")
+    lse = run_loss(x, w, t)[1]
+    ws = B.workspace(B.SEL_OP_HEAD_LOSS_GRAD, 20, 300, 64)
+    ws[0] = 1
+    assert all(torch.isnan(o).all() for o in run_loss(x, w, t, ws=ws))
+    dx, dw = torch.zeros_like(x), torch.zeros_like(w)
+    B.sel_head_loss_grad(x, w, t, lse, grad, dx, dw, ws)
+    assert torch.isnan(dx).all() and torch.isnan(dw).all()
+
+
+def test_gradient_is_the_losses_differences():
+    """Central differences of the losses the kernel gives. Hidden states are whole
+    multiples of 2^-5 below 4 and the step is 2^-4: exact in f16."""
+    rows, V, H = 40, 200, 64
+    _, w, t, grad = make(14, rows, V, H, "f16")
+    grad = grad / 256
+    x = (torch.randint(-100, 100, (rows, H), generator=torch.Generator().manual_seed(1)) / 32).half().cuda()
+    _, lse = run_loss(x, w, t)
+    dx, _ = check_grad(x, w, t, lse, grad)
+    h = 2.0 ** -4
+    for k in range(0, H, 9):
+        e = torch.zeros(H, device="cuda", dtype=torch.float16)
+        e[k] = h
+        up, down = run_loss(x + e, w, t)[0].double(), run_loss(x - e, w, t)[0].double()
+        # (a row's difference moves none of the others)
+        diff = grad.double() * (up - down) / (2 * h)
+        # the third derivative is w[:, k]'s third cumulant: below 0.1 of its range cubed;
+        # the losses' own errors as in check_loss, the gradient's as in check_grad (2^-11 of
+        # it and of P's terms, whose magnitudes sum to at most 2 max |w|)
+        r = (w[:, k].double().max() - w[:, k].double().min()).item()
+        dz = logit_error(x + e, w).max(dim=1).values
+        tol = 0.1 * r ** 3 * h ** 2 / 6 + (2 * dz + 2.0 ** -19 + 2.0 ** -23 * up.abs().max()) / h
+        tol = grad.double() * (tol + 2.0 ** -10 * 3 * w[:, k].double().abs().max())
+        assert ((diff - dx[:, k].double()).abs() <= tol).all()
+
+
+def test_offsets_past_32_bits():
+    """A matrix of more than 2^32 entries: its last rows are its own."""
+    V, H, rows = 1_050_000, 4104, 3
+    g = torch.Generator(device="cuda").manual_seed(3)
+    w = torch.zeros(V, H, dtype=torch.bfloat16, device="cuda")
+    tail = (torch.randn(300, H, generator=g, device="cuda") * 0.1).bfloat16()
+    w[-300:] = tail
+    x = torch.randn(rows, H, generator=g, device="cuda").bfloat16()
+    t = torch.tensor([V - 1, V - 299, 5], dtype=torch.int32, device="cuda")
+    loss, lse = run_loss(x, w, t)
+    z = x.double() @ tail.double().T
+    want = torch.logsumexp(torch.cat([z, torch.full((rows, 1), float(V - 300), device="cuda").double().log()], 1), 1)
+    dz = (H + 2) * 2.0 ** -23 * (x.double().abs() @ tail.double().abs().T).max(dim=1).values
+    assert ((lse.double() - want).abs() <= dz + 2.0 ** -18).all()
+    at = torch.stack([z[0, 299], z[1, 1], torch.zeros((), device="cuda").double()])
+    assert ((loss.double() - (want - at)).abs() <= 2 * dz + 2.0 ** -18).all()
+    grad = torch.ones(rows, device="cuda")
+    dx, dw = run_grad(x, w, t, lse, grad)
+    p = torch.exp(z - lse.double()[:, None])
+    p[0, 299] -= 1
+    p[1, 1] -= 1
+    want_w = p.T @ x.double()
+    tol = 2.0 ** -7 * (p.abs().T @ x.double().abs()) + 1e-6  # P's rounding, the result's and dz, 2^-9 each at most
+    assert ((dw[-300:].double() - want_w).abs() <= tol).all()
+    u = torch.exp(-lse.double())  # every other id's
+    want_0 = (u[:, None] * x.double()).sum(0)
+    assert ((dw[:5].double() - want_0).abs() <= 2.0 ** -7 * (u[:, None] * x.double().abs()).sum(0) + 1e-6).all()
+    assert ((dx.double() - p @ tail.double()).abs() <= 2.0 ** -7 * (p.abs() @ tail.double().abs()) + 1e-6).all()
