@@ -234,12 +234,35 @@ struct Share {
     }
 };
 
+// log2 of a sum as a whole number, which goes with others, and the logarithm of what
+// is between 0.7 and 1.5: that one is rounded to 2^-25, log2(sum) of a flat row would
+// be to 2^-20, for every entry alike.
+struct Log2 {
+    float whole, part;
+    Log2() = default;
+    __device__ __forceinline__ explicit Log2(float v) {
+        int e = static_cast<int>(__float_as_uint(v) >> 23) - 127;
+        const bool normal = v >= 1.17549435e-38f && v < INFINITY;
+        e = normal ? e : 0;
+        const float f = normal ? __uint_as_float((__float_as_uint(v) & 0x007FFFFFu) | 0x3F800000u) : v;  // [1, 2)
+        const bool high = f >= 1.41421356f;
+        whole = static_cast<float>(e + (normal && high));
+        part = log2f(normal && high ? 0.5f * f : f);
+    }
+};
+
 // What the teacher's list comes to. norm: log2 of its normaliser over its largest
-// value `top`; left: r; mass: the sum of p and r (NaN fails the row).
+// value `top`; left: r, and `log_left` its logarithm; mass: the sum
+// of p and r (NaN fails the row).
 struct Teacher {
-    float top, norm, left, mass;
+    float top;
+    Log2 norm;
+    float left, log_left, mass;
     uint32_t live;
 };
+
+// ln of 1 - p, p and 1 - p both at hand.
+__device__ __forceinline__ float log_rest(float p, float rest) { return rest > 0.5f ? log1pf(-p) : logf(rest); }
 
 struct Shared {
     alignas(16) float4 table[2][kMaxC * kWarps];  // sums of every warp of the cluster
@@ -295,7 +318,7 @@ struct LogP {
     bool given;
     __device__ __forceinline__ float operator()(float v) const {
         if (v == -INFINITY) return v;
-        return given ? fmaf(v, kf, -lh) + fmaf(v, kl, -ll) : (v - top) * kf - lh;
+        return given ? fmaf(v, kf, -lh) + fmaf(v, kl, -ll) : fmaf(v - top, kf, -lh) - ll;
     }
     __device__ __forceinline__ LogP(const DistillArgs& a, uint32_t row) {
         kf = a.kf;
@@ -340,12 +363,13 @@ __device__ __forceinline__ Teacher read_teacher(const DistillArgs& a, uint32_t r
         if (id < a.V) w = ff_add(w, FF{exp2f(log_p.given ? log_p(v) : (v - top) * a.kf), 0.0f});
     }
     w = ff_warp_sum(w);
-    Teacher t{top, 0.0f, 0.0f, 1.0f, nan || top > -INFINITY};
+    Teacher t{top, Log2{}, 0.0f, 0.0f, 1.0f, nan || top > -INFINITY};
     if (log_p.given) {
         t.left = named == a.V ? 0.0f : fmaxf(0.0f, (1.0f - w.hi) - w.lo);
+        t.log_left = log_rest(w.hi + w.lo, t.left);
         if (t.left == 0.0f) t.mass = w.hi + w.lo;
     } else {
-        t.norm = log2f(w.hi + w.lo);
+        t.norm = Log2(w.hi + w.lo);
     }
     if (nan || isnan(w.hi)) t.mass = NAN;
     return t;
@@ -533,7 +557,7 @@ struct Worker {
     __device__ __forceinline__ void run(uint32_t first_row, uint32_t step) {
         // of the row before: what its loss still needs, and listed entries to write
         uint32_t pending = 0, pending_row = 0, lives = 0;
-        float p_left = 0.0f, p_rest = 0.0f, p_log_z = 0.0f, p_mass = 0.0f;
+        float p_left = 0.0f, p_logs = 0.0f, p_mass = 0.0f;
         T* p_out = nullptr;
         uint32_t id[kEntries];
         float grads[kEntries];
@@ -545,8 +569,9 @@ struct Worker {
             float loss = 0.0f;
             for (uint32_t i = lane; i < a.C * kWarps; i += 32) loss += s.losses[p][i];
             loss = warp_sum(loss);
-            if (p_left != 0.0f) loss += p_left * (log2f(p_left) - (log2f(p_rest) - p_log_z));
-            if (lane == 0) a.loss[pending_row] = p_mass == p_mass && !s.err ? loss * kLn2 : NAN;
+            loss *= kLn2;
+            if (p_left != 0.0f) loss += p_left * p_logs;
+            if (lane == 0) a.loss[pending_row] = p_mass == p_mass && !s.err ? loss : NAN;
         };
         auto scatter = [&] {
             if constexpr (kGrad) {
@@ -640,10 +665,17 @@ struct Worker {
             const bool slow = !(fabsf(z.m) < kHuge);
             if (slow) z = slow_sums(x, bits, twice);
             if (s.err) z.rest = NAN;
-            const float total = z.rest + z.list, log_z = log2f(total);
+            const float total = z.rest + z.list;
+            const Log2 log_z(total);
             auto exponent = [&](float v) { return slow ? (v - z.m) * a.kf : fmaf(v, a.kf, -z.m); };
+            auto log_q = [&](float v) {
+                return (slow ? fmaf(v - z.m, a.kf, -log_z.whole) : fmaf(v, a.kf, -(z.m + log_z.whole))) - log_z.part;
+            };
             log_p.top = t.top;
-            if (!log_p.given) log_p.lh = t.norm;
+            if (!log_p.given) {
+                log_p.lh = t.norm.whole;
+                log_p.ll = t.norm.part;
+            }
 
             // (every warp has read this bitmap; it is marked again two rows on)
 #pragma unroll
@@ -654,9 +686,9 @@ struct Worker {
             for (uint32_t e = 0; e < kEntries; ++e) {
                 id[e] = new_id[e];
                 if (id[e] == SEL_INVALID_ID) continue;
-                const float lp = log_p(val[e]), y = exponent(logit[e]), p = exp2f(lp);
-                if (p != 0.0f) part += p * (lp - (y - log_z));
-                grads[e] = g * (t.mass * (ex2_approx(y) / total) - p);
+                const float lp = log_p(val[e]), p = exp2f(lp);
+                if (p != 0.0f) part += p * (lp - log_q(logit[e]));
+                grads[e] = g * (t.mass * (ex2_approx(exponent(logit[e])) / total) - p);
                 if (kGrad && grad == 0.0f) id[e] = SEL_INVALID_ID;
             }
             if (a.loss) {
@@ -686,8 +718,7 @@ struct Worker {
                 }
             }
             p_left = t.left;
-            p_rest = z.rest;
-            p_log_z = log_z;
+            p_logs = t.log_left - log_rest(z.list / total, z.rest / total);  // ln (r / s)
             p_mass = t.mass;
             pending_row = row;
             ++lives;

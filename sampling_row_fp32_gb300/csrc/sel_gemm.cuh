@@ -172,6 +172,9 @@ __device__ __forceinline__ void store_chunk(const EpiWarp& w, const CUtensorMap*
 
 // P: a trivially copyable problem with its maps, and
 //   using Type                         the operands' type
+//   kPart                              steps that are summed in tensor memory: the sums
+//                                      of a tile's parts meet in the epilogue's
+//                                      registers (0: all of them in tensor memory)
 //   uint32_t* error                    the workspace's error word
 //   count(worker, workers)             how many tiles a worker has
 //   tile(worker, workers, j)           the j-th of them
@@ -263,8 +266,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
             const uint32_t step_a = t.a_mn ? 2048 >> 4 : 32 >> 4, step_b = t.b_mn ? 2048 >> 4 : 32 >> 4;
             wait(&c.d_empty[dr.i], dr.phase ^ 1, &c.err);
             tc_fence_after();
-            const uint32_t d = tmem + dr.i * kTileN;
+            uint32_t d = tmem + dr.i * kTileN;
+            uint32_t left = P::kPart;  // of a part
             for (uint32_t s = 0; s < t.steps; ++s) {
+                if (P::kPart != 0 && left == 0) {
+                    if (leader) gemm_commit(&c.d_full[dr.i]);
+                    __syncwarp();
+                    dr.next();
+                    wait(&c.d_empty[dr.i], dr.phase ^ 1, &c.err);
+                    tc_fence_after();
+                    d = tmem + dr.i * kTileN;
+                    left = P::kPart;
+                }
+                const bool fresh = P::kPart != 0 ? left == P::kPart : s == 0;
+                --left;
                 wait(&c.full[st.i], st.phase, &c.err);
                 tc_fence_after();
                 if (leader) {
@@ -273,7 +288,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
                     const uint64_t b = t.b_mn ? smem_desc_mn(sb) : smem_desc(sb);
 #pragma unroll
                     for (uint32_t k = 0; k < kStepK / 16; ++k)
-                        gemm_mma(d, a + k * step_a, b + k * step_b, idesc, s > 0 || k > 0);
+                        gemm_mma(d, a + k * step_a, b + k * step_b, idesc, !fresh || k > 0);
                     gemm_commit(&c.empty[st.i]);
                 }
                 __syncwarp();
@@ -304,23 +319,48 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
             w.chunks = (w.cols + 31) / 32;
             w.first = j == 0;
             w.last = j == count - 1;
-            wait(&c.d_full[dr.i], dr.phase, &c.err);
-            tc_fence_after();
             // (a short last piece reads on, at most to the end of the tensor memory)
-            const uint32_t d = tmem + (quarter << 21) + dr.i * kTileN + w.col;
+            const uint32_t d = tmem + (quarter << 21) + w.col;
+            auto piece = [&](uint32_t i, uint32_t (&r)[32]) {
+                __syncwarp();
+                tmem_ld(d + dr.i * kTileN + i * 32, r);
+            };
             auto release = [&] {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) arrive_cluster(first_cta(&c.d_empty[dr.i]));
             };
+            float sums[P::kPart != 0 ? 128 : 1];  // of the parts before the last
+            if constexpr (P::kPart != 0) {
+#pragma unroll
+                for (uint32_t i = 0; i < 128; ++i) sums[i] = 0.0f;
+                for (uint32_t s = P::kPart; s < t.steps; s += P::kPart) {
+                    wait(&c.d_full[dr.i], dr.phase, &c.err);
+                    tc_fence_after();
+#pragma unroll
+                    for (uint32_t i = 0; i < 4; ++i) {
+                        if (i >= w.chunks) break;
+                        uint32_t r[32];
+                        piece(i, r);
+#pragma unroll
+                        for (uint32_t k = 0; k < 32; ++k) sums[32 * i + k] += __uint_as_float(r[k]);
+                    }
+                    release();
+                    dr.next();
+                }
+            }
+            wait(&c.d_full[dr.i], dr.phase, &c.err);
+            tc_fence_after();
             if (w.chunks == 0) release();  // (16 columns: all of them the other half's)
             p.epilogue(t, w, [&](uint32_t i, float(&v)[32]) {
                 uint32_t r[32];
-                __syncwarp();
-                tmem_ld(d + i * 32, r);
+                piece(i, r);
                 if (i == w.chunks - 1) release();  // the buffer is read
 #pragma unroll
-                for (uint32_t k = 0; k < 32; ++k) v[k] = __uint_as_float(r[k]);
+                for (uint32_t k = 0; k < 32; ++k) {
+                    v[k] = __uint_as_float(r[k]);
+                    if constexpr (P::kPart != 0) v[k] += sums[32 * i + k];
+                }
             });
             dr.next();
         }

@@ -48,6 +48,16 @@ __device__ __forceinline__ float pow2(float n) {
     return n >= -126.0f ? __uint_as_float(static_cast<uint32_t>(static_cast<int>(n) + 127) << 23) : 0.0f;
 }
 
+// v 2^e for any e that floats and P's shift give.
+struct Shift {
+    float a, b;
+    __device__ __forceinline__ explicit Shift(int e) {
+        a = __int_as_float((e / 2 + 127) << 23);
+        b = __int_as_float((e - e / 2 + 127) << 23);
+    }
+    __device__ __forceinline__ float operator()(float v) const { return v * a * b; }
+};
+
 __device__ __forceinline__ bool any_target(uint32_t t, uint32_t col) { return t - col < 32u; }
 
 // A row of z in logarithms to base 2: sum over its ids but the target of 2^(y - m),
@@ -71,11 +81,18 @@ struct Weights {
     __device__ __forceinline__ float operator()(float z) const { return ex2_approx(fmaf(z * k0, k1, -ref)); }
 };
 
+// The tensor cores round their sums towards zero, 16 products at a time: a logit of
+// 4,096 products comes out 1.6e-6 too small, which a loss shows. So a logit is summed in
+// parts of 1,024, joined in the epilogue's registers. (P and the gradients are rounded
+// to 16 bits: they need no such care.)
+constexpr uint32_t kLossPart = 1024 / kStepK;
+
 // Hidden rows on the product's rows: a lane has one of them, and half a tile's
 // columns of z.
 template <typename T>
 struct LossProblem {
     using Type = T;
+    static constexpr uint32_t kPart = kLossPart;
     CUtensorMap x, w;
     const uint32_t* targets;
     Part* parts;  // [2 column tiles][rows]
@@ -95,8 +112,9 @@ struct LossProblem {
         const uint32_t row = t.am + w.row, col = t.bn + w.col;
         const uint32_t target = row < rows ? targets[row] : SEL_INVALID_ID;
         Part p{-INFINITY, 0.0f};
-#pragma unroll 1
-        for (uint32_t c = 0; c < w.chunks; ++c) {
+#pragma unroll
+        for (uint32_t c = 0; c < 4; ++c) {
+            if (c >= w.chunks) break;
             float v[32];
             load(c, v);
             const uint32_t c0 = col + 32 * c;
@@ -156,6 +174,7 @@ __device__ __forceinline__ float max_across(float v) {
 template <typename T>
 struct LossColumnsProblem {
     using Type = T;
+    static constexpr uint32_t kPart = kLossPart;
     CUtensorMap x, w;
     const uint32_t* targets;
     Part* parts;  // [8 workers of a row tile][rows]
@@ -177,8 +196,9 @@ struct LossColumnsProblem {
     __device__ __forceinline__ void epilogue(const GemmTile& t, const EpiWarp& w, Load load) const {
         const uint32_t id = t.am + w.row, first = t.bn + w.col;
         auto* sums = reinterpret_cast<Part*>(w.smem) + w.lane;
-#pragma unroll 1
-        for (uint32_t c = 0; c < w.chunks; ++c) {
+#pragma unroll
+        for (uint32_t c = 0; c < 4; ++c) {
+            if (c >= w.chunks) break;
             const uint32_t row = first + 32 * c + w.lane;  // whose result this lane will have
             const bool mine = 32 * c + w.lane < w.cols && row < rows;
             const uint32_t target = mine ? targets[row] : SEL_INVALID_ID;
@@ -309,6 +329,21 @@ __global__ void __launch_bounds__(kFinishThreads) loss_finish_kernel(LossFinishA
 // gradient
 // ---------------------------------------------------------------------------
 
+// A row's gradient g = m 2^e, m in (1/2, 1): m goes into P before P is rounded, 2^e, of
+// which nothing is rounded, into the hidden rows for dW and into dX's sums. So P's
+// rounding and the results' are all there is.
+struct GradParts {
+    float m;
+    int e;
+    __device__ __forceinline__ explicit GradParts(float g) {
+        m = frexpf(g, &e);
+        if (!(fabsf(g) < INFINITY)) {
+            m = NAN;
+            e = 0;
+        }
+    }
+};
+
 // f16 holds P times 2^14: entries down to 2^-28 stay normal numbers, and the
 // target's, no smaller than -1, does not overflow.
 template <typename T>
@@ -331,6 +366,7 @@ __device__ __forceinline__ void store16(T* to, const float (&v)[32], uint32_t i)
 template <typename T>
 struct ProbProblem {
     using Type = T;
+    static constexpr uint32_t kPart = 0;
     CUtensorMap x, w;
     T* p;
     const uint32_t* targets;
@@ -349,21 +385,22 @@ struct ProbProblem {
     template <typename Load>
     __device__ __forceinline__ void epilogue(const GemmTile& t, const EpiWarp& w, Load load) const {
         const uint32_t id = t.am + w.row, first = t.bn + w.col;
-        // the warp's rows: lse, and of 32 a bit for those that do not count, and one for
-        // those whose target is among the warp's ids
+        // the warp's rows: lse less ln |m|, and of 32 a bit for those that do not count,
+        // one for a negative m, one for a target among the warp's ids
         auto* refs = reinterpret_cast<float*>(w.smem);
-        auto* bits = reinterpret_cast<uint2*>(w.smem + 512);
-        auto* ids = reinterpret_cast<uint32_t*>(w.smem + 544);
+        auto* bits = reinterpret_cast<uint4*>(w.smem + 512);
+        auto* ids = reinterpret_cast<uint32_t*>(w.smem + 576);
         __syncwarp();
         for (uint32_t c = 0; c < w.chunks; ++c) {
             const uint32_t i = 32 * c + w.lane, row = first + i;
             const uint32_t target = i < w.cols && row < rows ? targets[row] : SEL_INVALID_ID;
-            const bool live = target < V && grad[row] != 0.0f;
-            refs[i] = live ? lse[row] : 0.0f;
+            const float m = target < V ? GradParts(grad[row]).m : 0.0f;
+            const bool live = m != 0.0f;
+            refs[i] = live ? lse[row] - logf(fabsf(m)) : 0.0f;
             ids[i] = target;
-            const uint32_t dead = __ballot_sync(kFull, !live);
+            const uint32_t dead = __ballot_sync(kFull, !live), negative = __ballot_sync(kFull, m < 0.0f);
             const uint32_t hits = __ballot_sync(kFull, live && target - (id - w.lane) < 32u);
-            if (w.lane == 0) bits[c] = make_uint2(dead, hits);
+            if (w.lane == 0) bits[c] = make_uint4(dead, hits, negative, 0);
         }
         __syncwarp();
         const float up = kProbShift<T>;
@@ -373,13 +410,17 @@ struct ProbProblem {
         for (uint32_t c = 0; c < w.chunks; ++c) {
             float v[32];
             load(c, v);
-            const uint2 of = bits[c];
+            const uint4 of = bits[c];
             // targets' entries, rare, through shared memory: a lane may have several
-            auto* kept = reinterpret_cast<float*>(w.smem + 1056);
+            auto* kept = reinterpret_cast<float*>(w.smem + 1088);
             if (of.y) {
 #pragma unroll
-                for (uint32_t i = 0; i < 32; ++i)
-                    if ((of.y >> i & 1) && ids[32 * c + i] == id) kept[i] = expm1f(v[i] - refs[32 * c + i]) * exp2f(up);
+                for (uint32_t i = 0; i < 32; ++i) {
+                    if ((of.y >> i & 1) && ids[32 * c + i] == id) {
+                        const uint32_t row = first + 32 * c + i;
+                        kept[i] = expm1f(v[i] - lse[row]) * fabsf(GradParts(grad[row]).m) * static_cast<float>(1 << static_cast<int>(kProbShift<T>));
+                    }
+                }
             }
 #pragma unroll
             for (uint32_t i = 0; i < 32; i += 4) {
@@ -393,6 +434,11 @@ struct ProbProblem {
 #pragma unroll
                 for (uint32_t i = 0; i < 32; ++i)
                     if ((of.y >> i & 1) && ids[32 * c + i] == id) v[i] = kept[i];
+            }
+            if (of.z) {
+#pragma unroll
+                for (uint32_t i = 0; i < 32; ++i)
+                    if (of.z >> i & 1) v[i] = -v[i];
             }
             if (of.x) {
 #pragma unroll
@@ -412,8 +458,9 @@ struct ProbProblem {
 template <typename T>
 struct GradsProblem {
     using Type = T;
+    static constexpr uint32_t kPart = 0;
     CUtensorMap p_k, x_mn, dw, p_mn, w_mn;
-    const float* scale;  // of dW: the largest gradient, less P's shift
+    const int* exponent;  // of dW's sums
     float* acc;          // [slices][rows][H]
     uint32_t* error;
     uint32_t rows, V, H, v0, width;
@@ -450,14 +497,14 @@ struct GradsProblem {
     template <typename Load>
     __device__ __forceinline__ void epilogue(const GemmTile& t, const EpiWarp& w, Load load) const {
         if (!t.a_mn) {
-            const float s = *scale;
+            const Shift shift(*exponent);
             const uint32_t id = v0 + t.am + w.row - w.lane;
 #pragma unroll 1
             for (uint32_t c = 0; c < w.chunks; ++c) {
                 float v[32];
                 load(c, v);
 #pragma unroll
-                for (uint32_t i = 0; i < 32; ++i) v[i] *= s;
+                for (uint32_t i = 0; i < 32; ++i) v[i] = shift(v[i]);
                 const uint32_t x = t.bn + w.col + c / 2 * 64;
                 store_chunk<T>(w, &dw, x, id, c, x < H && id < V, v);
             }
@@ -485,12 +532,12 @@ struct GradsProblem {
 
 struct PrepArgs {
     const uint4* x;
-    uint4* scaled;  // x times grad over the largest, NULL: not wanted
+    uint4* scaled;  // x times 2^e over the largest gradient's
     const uint32_t* targets;
     const float* grad;
-    float* scale;
+    int* exponent;           // of dW's sums
     uint32_t rows, V, vecs;  // vecs: of 8 entries a row
-    float down;
+    int shift;  // P's
 };
 
 constexpr uint32_t kPrepThreads = 128;
@@ -501,24 +548,23 @@ __device__ __forceinline__ void unpack2(uint32_t w, float& lo, float& hi) {
     hi = bits_f32<T>(static_cast<uint16_t>(w >> 16));
 }
 
-// dW's second operand: hidden rows times their gradients over the largest one, so
-// that equal gradients (a mean's) round nothing; others round each entry once
-// more. Rows that do not count are zeros, whatever they hold.
+// dW's second operand: hidden rows times the power of two of their gradient over the
+// largest one's: exact, but for entries that become subnormal. Rows that do not count
+// are zeros, whatever they hold.
 template <typename T>
 __global__ void __launch_bounds__(kPrepThreads) grad_prep_kernel(PrepArgs a) {
-    __shared__ float sh[kPrepThreads / 32];
+    __shared__ int sh[kPrepThreads / 32];
     pdl_wait();
     pdl_trigger();
-    float top = 0.0f;
+    int top = -1000;
     for (uint32_t r = threadIdx.x; r < a.rows; r += kPrepThreads)
-        if (a.targets[r] < a.V) top = fmaxf(top, fabsf(a.grad[r]));
-#pragma unroll
-    for (uint32_t m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, m));
+        if (a.targets[r] < a.V && a.grad[r] != 0.0f) top = max(top, GradParts(a.grad[r]).e);
+    top = __reduce_max_sync(kFull, top);
     if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = top;
     __syncthreads();
 #pragma unroll
-    for (uint32_t i = 0; i < kPrepThreads / 32; ++i) top = fmaxf(top, sh[i]);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.scale = top * a.down;
+    for (uint32_t i = 0; i < kPrepThreads / 32; ++i) top = max(top, sh[i]);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.exponent = max(top, -200) - a.shift;
     const uint64_t n = static_cast<uint64_t>(a.rows) * a.vecs;
     for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * kPrepThreads + threadIdx.x; i < n;
          i += static_cast<uint64_t>(gridDim.x) * kPrepThreads) {
@@ -527,7 +573,7 @@ __global__ void __launch_bounds__(kPrepThreads) grad_prep_kernel(PrepArgs a) {
         uint4 q = make_uint4(0, 0, 0, 0);
         if (a.targets[r] < a.V && g != 0.0f) {
             q = a.x[i];
-            const float f = g / top;
+            const float f = pow2(static_cast<float>(GradParts(g).e - top));
             uint32_t* p = &q.x;
 #pragma unroll
             for (uint32_t k = 0; k < 4; ++k) {
@@ -548,7 +594,7 @@ struct GradFinishArgs {
     uint4* dx;  // NULL: not wanted
     uint4* dw;
     uint32_t rows, V, vecs, slices;
-    float down;
+    int shift;  // P's
 };
 
 // dX from its sums, rounded once. With the error word raised both gradients
@@ -575,9 +621,9 @@ __global__ void __launch_bounds__(kPrepThreads) grad_finish_kernel(GradFinishArg
                 s[0] += u.x, s[1] += u.y, s[2] += u.z, s[3] += u.w;
                 s[4] += v.x, s[5] += v.y, s[6] += v.z, s[7] += v.w;
             }
-            const float f = a.down;
+            const Shift shift(GradParts(g).e - a.shift);
 #pragma unroll
-            for (uint32_t k = 0; k < 8; ++k) s[k] = s[k] * f * g;
+            for (uint32_t k = 0; k < 8; ++k) s[k] = shift(s[k]);
             q = make_uint4(pack2<T>(s[0], s[1]), pack2<T>(s[2], s[3]), pack2<T>(s[4], s[5]), pack2<T>(s[6], s[7]));
         }
         if (bad) q = make_uint4(nan2, nan2, nan2, nan2);
@@ -729,15 +775,15 @@ sel_status run_grad(const HeadLossCall& c, const float* lse, const float* grad, 
     const GradPlan plan = grad_plan(c.rows, c.V, c.H);
     const Columns rows(c.rows);
     auto* error = reinterpret_cast<uint32_t*>(c.ws);
-    auto* scale = reinterpret_cast<float*>(c.ws + 16);
+    auto* exponent = reinterpret_cast<int*>(c.ws + 16);
     auto* acc = reinterpret_cast<float*>(c.ws + plan.acc);
     void* prob = c.ws + plan.p;
     void* scaled = c.ws + plan.scaled;
-    const float down = 1.0f / static_cast<float>(1u << static_cast<uint32_t>(kProbShift<T>));
+    const int shift = static_cast<int>(kProbShift<T>);
     const uint32_t vecs = c.H / 8, all = sms / 2;
     const uint32_t blocks = static_cast<uint32_t>(std::min<uint64_t>(8 * sms, ceil_div(static_cast<uint64_t>(c.rows) * vecs, kPrepThreads)));
     if (dw) {
-        const PrepArgs a{static_cast<const uint4*>(c.x), static_cast<uint4*>(scaled), c.targets, grad, scale, c.rows, c.V, vecs, down};
+        const PrepArgs a{static_cast<const uint4*>(c.x), static_cast<uint4*>(scaled), c.targets, grad, exponent, c.rows, c.V, vecs, shift};
         if (launch_pdl(grad_prep_kernel<T>, dim3(blocks), dim3(kPrepThreads), 0, c.stream, a) != cudaSuccess) return SEL_ECUDA;
     }
     for (uint32_t i = 0; i < plan.pieces; ++i) {
@@ -764,7 +810,7 @@ sel_status run_grad(const HeadLossCall& c, const float* lse, const float* grad, 
             (dw && !map16(&g.dw, dw, c.H, c.V, 64, 32)) || !map16(&g.p_mn, prob, c.rows, width, 64, kStepK, pitch) ||
             !map16(&g.w_mn, c.w, c.H, c.V, 64, kStepK))
             return SEL_ECUDA;
-        g.scale = scale;
+        g.exponent = exponent;
         g.acc = acc;
         g.error = error;
         g.rows = c.rows;
@@ -786,7 +832,7 @@ sel_status run_grad(const HeadLossCall& c, const float* lse, const float* grad, 
         g.extra = light == workers ? 0 : std::min(g.dw_items / light, (g.k_slice / kStepK) / (g.dw_steps + 2));
         if (const sel_status s = launch_gemm(g, workers, c.stream); s != SEL_OK) return s;
     }
-    const GradFinishArgs f{acc, c.targets, grad, error, static_cast<uint4*>(dx), static_cast<uint4*>(dw), c.rows, c.V, vecs, plan.slices, down};
+    const GradFinishArgs f{acc, c.targets, grad, error, static_cast<uint4*>(dx), static_cast<uint4*>(dw), c.rows, c.V, vecs, plan.slices, shift};
     return launch_pdl(grad_finish_kernel<T>, dim3(blocks), dim3(kPrepThreads), 0, c.stream, f) == cudaSuccess ? SEL_OK : SEL_ECUDA;
 }
 

@@ -86,14 +86,14 @@ def check_grad(x, w, t, lse, grad):
     # An entry of P: its logit's error and that of the exponential (its exponent, z -
     # lse rounded, moves it by 2^-23 |z - lse|, and |d| e^d <= 1 below), the same on
     # the target's e^d - 1, whose own rounding and that to T come on top; f16 holds it
-    # 2^14 up, where 2^-25 is half its smallest step.
+    # 2^14 up times at least 1/2, where 2^-25 is half its smallest step.
     dz = logit_error(x, w) + 2.0 ** -20
     depth = 1 + (x64 @ w64.T - l64[:, None]).abs()
     dp = p * (dz + 2.0 ** -23 * depth) * (1 + 2.0 ** -8)
     hot = torch.zeros_like(p)
     hot[live, tl[live]] = 1.0
     a = (p - hot).abs()
-    dp = dp + a * (eps + 2.0 ** -22) + (2.0 ** -39 if T == torch.float16 else 2.0 ** -134) * live[:, None]
+    dp = dp + a * (eps + 2.0 ** -22) + (2.0 ** -38 if T == torch.float16 else 2.0 ** -134) * live[:, None]
     g = grad.double().abs() * live
     # sums: a rounding of a whole fp32 step for each term, as above
     mag = (a + dp) @ w64.abs()
