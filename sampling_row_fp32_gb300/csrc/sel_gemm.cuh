@@ -178,8 +178,9 @@ __device__ __forceinline__ void store_chunk(const EpiWarp& w, const CUtensorMap*
 //   uint32_t* error                    the workspace's error word
 //   count(worker, workers)             how many tiles a worker has
 //   tile(worker, workers, j)           the j-th of them
-//   epilogue(tile, w, load)            load(c, v): the warp's columns 32 c .., for
-//                                      c = 0 .. chunks - 1 in order, each once
+//   epilogue(tile, w, arrive, load)    arrive(): waits for the sums; then load(c, v): the
+//                                      warp's columns 32 c .., for c = 0 .. chunks - 1 in
+//                                      order, each once
 template <typename P>
 __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_constant__ P p) {
     extern __shared__ unsigned char smem_raw[];
@@ -349,10 +350,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
                     dr.next();
                 }
             }
-            wait(&c.d_full[dr.i], dr.phase, &c.err);
-            tc_fence_after();
-            if (w.chunks == 0) release();  // (16 columns: all of them the other half's)
-            p.epilogue(t, w, [&](uint32_t i, float(&v)[32]) {
+            auto arrived = [&] {
+                wait(&c.d_full[dr.i], dr.phase, &c.err);
+                tc_fence_after();
+                if (w.chunks == 0) release();  // (16 columns: all of them the other half's)
+            };
+            p.epilogue(t, w, arrived, [&](uint32_t i, float(&v)[32]) {
                 uint32_t r[32];
                 piece(i, r);
                 if (i == w.chunks - 1) release();  // the buffer is read

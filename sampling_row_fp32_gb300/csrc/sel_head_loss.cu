@@ -107,11 +107,12 @@ struct LossProblem {
         raster.at(worker + j * workers, m, n);
         return {&x, &w, m * kTileM, n * kTileN, 0, 0, steps, kTileN, false, false};
     }
-    template <typename Load>
-    __device__ __forceinline__ void epilogue(const GemmTile& t, const EpiWarp& w, Load load) const {
+    template <typename Arrive, typename Load>
+    __device__ __forceinline__ void epilogue(const GemmTile& t, const EpiWarp& w, Arrive arrived, Load load) const {
         const uint32_t row = t.am + w.row, col = t.bn + w.col;
         const uint32_t target = row < rows ? targets[row] : SEL_INVALID_ID;
         Part p{-INFINITY, 0.0f};
+        arrived();
 #pragma unroll
         for (uint32_t c = 0; c < 4; ++c) {
             if (c >= w.chunks) break;
@@ -192,10 +193,11 @@ struct LossColumnsProblem {
         const uint32_t v = worker / row_tiles + j * (workers / row_tiles);
         return {&w, &x, v * kTileM, worker % row_tiles * n, 0, 0, steps, n, false, false};
     }
-    template <typename Load>
-    __device__ __forceinline__ void epilogue(const GemmTile& t, const EpiWarp& w, Load load) const {
+    template <typename Arrive, typename Load>
+    __device__ __forceinline__ void epilogue(const GemmTile& t, const EpiWarp& w, Arrive arrived, Load load) const {
         const uint32_t id = t.am + w.row, first = t.bn + w.col;
         auto* sums = reinterpret_cast<Part*>(w.smem) + w.lane;
+        arrived();
 #pragma unroll
         for (uint32_t c = 0; c < 4; ++c) {
             if (c >= w.chunks) break;
@@ -344,6 +346,12 @@ struct GradParts {
     }
 };
 
+// The target's entry, e^(z - lse) - 1, carries most of a row's gradient, so that its
+// rounding would show in all of it. What it lost is kept, one number a row, and added
+// back in fp32: to dX by the last launch, to dW's rows in the epilogue, for the first
+// few hidden rows with a target among a warp's ids (of many the roundings average).
+constexpr uint32_t kKeptRows = 8;
+
 // f16 holds P times 2^14: entries down to 2^-28 stay normal numbers, and the
 // target's, no smaller than -1, does not overflow.
 template <typename T>
@@ -369,6 +377,7 @@ struct ProbProblem {
     static constexpr uint32_t kPart = 0;
     CUtensorMap x, w;
     T* p;
+    float* lost;  // [rows]: of the targets' entries, by their rounding
     const uint32_t* targets;
     const float* lse;
     const float* grad;
@@ -382,8 +391,8 @@ struct ProbProblem {
         raster.at(worker + j * workers, r, v);
         return {&w, &x, v0 + v * kTileM, r * n, 0, 0, steps, n, false, false};
     }
-    template <typename Load>
-    __device__ __forceinline__ void epilogue(const GemmTile& t, const EpiWarp& w, Load load) const {
+    template <typename Arrive, typename Load>
+    __device__ __forceinline__ void epilogue(const GemmTile& t, const EpiWarp& w, Arrive arrived, Load load) const {
         const uint32_t id = t.am + w.row, first = t.bn + w.col;
         // the warp's rows: lse less ln |m|, and of 32 a bit for those that do not count,
         // one for a negative m, one for a target among the warp's ids
@@ -402,7 +411,7 @@ struct ProbProblem {
             const uint32_t hits = __ballot_sync(kFull, live && target - (id - w.lane) < 32u);
             if (w.lane == 0) bits[c] = make_uint4(dead, hits, negative, 0);
         }
-        __syncwarp();
+        arrived();  // (and the warp's lanes are together again)
         const float up = kProbShift<T>;
         T* out = p + static_cast<uint64_t>(id - v0) * pitch + first;
         const uint32_t cols = min(w.cols, first < pitch ? pitch - first : 0);
@@ -418,7 +427,11 @@ struct ProbProblem {
                 for (uint32_t i = 0; i < 32; ++i) {
                     if ((of.y >> i & 1) && ids[32 * c + i] == id) {
                         const uint32_t row = first + 32 * c + i;
-                        kept[i] = expm1f(v[i] - lse[row]) * fabsf(GradParts(grad[row]).m) * static_cast<float>(1 << static_cast<int>(kProbShift<T>));
+                        const float m = GradParts(grad[row]).m;
+                        const float e = expm1f(v[i] - lse[row]) * fabsf(m) * static_cast<float>(1 << static_cast<int>(kProbShift<T>));
+                        const float less = e - to_f32(from_f32<T>(e));
+                        kept[i] = e;
+                        lost[row] = m < 0.0f ? -less : less;
                     }
                 }
             }
@@ -461,7 +474,12 @@ struct GradsProblem {
     static constexpr uint32_t kPart = 0;
     CUtensorMap p_k, x_mn, dw, p_mn, w_mn;
     const int* exponent;  // of dW's sums
-    float* acc;          // [slices][rows][H]
+    const T* scaled;      // [rows][H]: the hidden rows of dW
+    const float* lost;
+    const uint32_t* hits;  // [V / 32][1 + kKeptRows]: rows with a target among 32 ids
+    const uint32_t* targets;
+    const float* grad;
+    float* acc;  // [slices][rows][H]
     uint32_t* error;
     uint32_t rows, V, H, v0, width;
     uint32_t n_rows, row_tiles;            // dX: columns a tile
@@ -494,15 +512,36 @@ struct GradsProblem {
         const uint32_t h = i % h_tiles * kTileN;
         return {&p_k, &x_mn, i / h_tiles * kTileM, h, 0, 0, dw_steps, H - h <= kTileN / 2 ? kTileN / 2 : kTileN, false, true};
     }
-    template <typename Load>
-    __device__ __forceinline__ void epilogue(const GemmTile& t, const EpiWarp& w, Load load) const {
+    // What row r's target entry lost, if its target is this lane's id, to columns x ..
+    __device__ __forceinline__ void add_lost(uint32_t r, uint32_t id, uint32_t x, float (&v)[32]) const {
+        if (targets[r] != id || id >= V || grad[r] == 0.0f) return;
+        const float f = lost[r];
+        const T* row = scaled + static_cast<uint64_t>(r) * H;
+#pragma unroll
+        for (uint32_t i = 0; i < 32; i += 8) {
+            if (x + i >= H) break;
+            const uint4 q = *reinterpret_cast<const uint4*>(row + x + i);
+            const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k) {
+                v[i + 2 * k] = fmaf(f, bits_f32<T>(static_cast<uint16_t>(u[k])), v[i + 2 * k]);
+                v[i + 2 * k + 1] = fmaf(f, bits_f32<T>(static_cast<uint16_t>(u[k] >> 16)), v[i + 2 * k + 1]);
+            }
+        }
+    }
+    template <typename Arrive, typename Load>
+    __device__ __forceinline__ void epilogue(const GemmTile& t, const EpiWarp& w, Arrive arrived, Load load) const {
         if (!t.a_mn) {
             const Shift shift(*exponent);
             const uint32_t id = v0 + t.am + w.row - w.lane;
+            const uint32_t* kept = hits + static_cast<uint64_t>(id / 32) * (kKeptRows + 1);
+            const uint32_t n = id < V ? kept[0] : 0;
+            arrived();
 #pragma unroll 1
             for (uint32_t c = 0; c < w.chunks; ++c) {
                 float v[32];
                 load(c, v);
+                for (uint32_t k = 0; k < n; ++k) add_lost(kept[1 + k], id + w.lane, t.bn + w.col + 32 * c, v);
 #pragma unroll
                 for (uint32_t i = 0; i < 32; ++i) v[i] = shift(v[i]);
                 const uint32_t x = t.bn + w.col + c / 2 * 64;
@@ -511,6 +550,7 @@ struct GradsProblem {
         } else {
             const uint32_t h = t.am + w.row, slice = t.bk / k_slice, first = t.bn + w.col;
             float* o = acc + (static_cast<uint64_t>(slice) * rows + first) * H + h;
+            arrived();
 #pragma unroll 1
             for (uint32_t c = 0; c < w.chunks; ++c) {
                 float v[32];
@@ -536,6 +576,7 @@ struct PrepArgs {
     const uint32_t* targets;
     const float* grad;
     int* exponent;           // of dW's sums
+    uint32_t* hits;
     uint32_t rows, V, vecs;  // vecs: of 8 entries a row
     int shift;  // P's
 };
@@ -550,7 +591,8 @@ __device__ __forceinline__ void unpack2(uint32_t w, float& lo, float& hi) {
 
 // dW's second operand: hidden rows times the power of two of their gradient over the
 // largest one's: exact, but for entries that become subnormal. Rows that do not count
-// are zeros, whatever they hold.
+// are zeros, whatever they hold. And of each 32 ids the first rows that have one of
+// them for a target.
 template <typename T>
 __global__ void __launch_bounds__(kPrepThreads) grad_prep_kernel(PrepArgs a) {
     __shared__ int sh[kPrepThreads / 32];
@@ -584,10 +626,25 @@ __global__ void __launch_bounds__(kPrepThreads) grad_prep_kernel(PrepArgs a) {
         }
         a.scaled[i] = q;
     }
+    const uint32_t lane = threadIdx.x & 31, warps = gridDim.x * (kPrepThreads / 32);
+    for (uint32_t v = blockIdx.x * (kPrepThreads / 32) + threadIdx.x / 32; v < (a.V + 31) / 32; v += warps) {
+        uint32_t* to = a.hits + static_cast<uint64_t>(v) * (kKeptRows + 1);
+        uint32_t found = 0;
+        for (uint32_t r0 = 0; r0 < a.rows && found < kKeptRows; r0 += 32) {
+            const uint32_t r = r0 + lane, t = r < a.rows ? a.targets[r] : SEL_INVALID_ID;
+            const uint32_t mine = __ballot_sync(kFull, t / 32 == v);
+            const uint32_t at = found + __popc(mine & ((1u << lane) - 1));
+            if ((mine >> lane & 1) && at < kKeptRows) to[1 + at] = r;
+            found += __popc(mine);
+        }
+        if (lane == 0) to[0] = min(found, kKeptRows);
+    }
 }
 
 struct GradFinishArgs {
     const float* acc;
+    const float* lost;
+    const uint4* w;
     const uint32_t* targets;
     const float* grad;
     const uint32_t* error;
@@ -620,6 +677,16 @@ __global__ void __launch_bounds__(kPrepThreads) grad_finish_kernel(GradFinishArg
                 const float4 u = p[0], v = p[1];
                 s[0] += u.x, s[1] += u.y, s[2] += u.z, s[3] += u.w;
                 s[4] += v.x, s[5] += v.y, s[6] += v.z, s[7] += v.w;
+            }
+            const float f = a.lost[r];
+            const uint4 of = a.w[static_cast<uint64_t>(a.targets[r]) * a.vecs + i % a.vecs];
+            const uint32_t u[4] = {of.x, of.y, of.z, of.w};
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k) {
+                float lo, hi;
+                unpack2<T>(u[k], lo, hi);
+                s[2 * k] = fmaf(f, lo, s[2 * k]);
+                s[2 * k + 1] = fmaf(f, hi, s[2 * k + 1]);
             }
             const Shift shift(GradParts(g).e - a.shift);
 #pragma unroll
@@ -679,7 +746,7 @@ inline LossPlan loss_plan(uint32_t rows, uint32_t V) {
 // 16,384 ids, and all alike.
 struct GradPlan {
     uint32_t piece, pieces, slices, pitch, dx_n;
-    size_t scaled, acc, p, bytes;
+    size_t lost, hits, scaled, acc, p, bytes;
 };
 inline GradPlan grad_plan(uint32_t rows, uint32_t V, uint32_t H) {
     GradPlan g;
@@ -695,7 +762,9 @@ inline GradPlan grad_plan(uint32_t rows, uint32_t V, uint32_t H) {
     g.dx_n = rows <= kTileN || c.padded() * 1.38 < static_cast<double>(ceil_div(rows, kTileN)) * kTileN ? c.n : kTileN;
     const uint64_t tiles = static_cast<uint64_t>(ceil_div(H, kTileM)) * ceil_div(rows, g.dx_n);
     g.slices = std::min(std::max(1u, g.piece / 1024), tiles >= 76 ? 1u : ceil_div(76, tiles));
-    g.scaled = kWsHeaderBytes;
+    g.lost = kWsHeaderBytes;
+    g.hits = g.lost + align_up(static_cast<size_t>(rows) * sizeof(float), 256);
+    g.scaled = g.hits + align_up(ceil_div(V, 32) * (kKeptRows + 1) * sizeof(uint32_t), 256);
     g.acc = g.scaled + align_up(static_cast<size_t>(rows) * H * 2, 256);
     // What the sums and P take at most: slices * tiles < 76 + tiles, and P as above;
     // these bounds grow with each size, so that a workspace serves smaller calls too.
@@ -779,12 +848,15 @@ sel_status run_grad(const HeadLossCall& c, const float* lse, const float* grad, 
     auto* acc = reinterpret_cast<float*>(c.ws + plan.acc);
     void* prob = c.ws + plan.p;
     void* scaled = c.ws + plan.scaled;
+    auto* lost = reinterpret_cast<float*>(c.ws + plan.lost);
+    auto* hits = reinterpret_cast<uint32_t*>(c.ws + plan.hits);
     const int shift = static_cast<int>(kProbShift<T>);
     const uint32_t vecs = c.H / 8, all = sms / 2;
     const uint32_t blocks = static_cast<uint32_t>(std::min<uint64_t>(8 * sms, ceil_div(static_cast<uint64_t>(c.rows) * vecs, kPrepThreads)));
     if (dw) {
-        const PrepArgs a{static_cast<const uint4*>(c.x), static_cast<uint4*>(scaled), c.targets, grad, exponent, c.rows, c.V, vecs, shift};
-        if (launch_pdl(grad_prep_kernel<T>, dim3(blocks), dim3(kPrepThreads), 0, c.stream, a) != cudaSuccess) return SEL_ECUDA;
+        const PrepArgs a{static_cast<const uint4*>(c.x), static_cast<uint4*>(scaled), c.targets, grad, exponent, hits, c.rows, c.V, vecs, shift};
+        const uint32_t prep = std::max(blocks, std::min(8u * sms, ceil_div(c.V, 32 * (kPrepThreads / 32))));
+        if (launch_pdl(grad_prep_kernel<T>, dim3(prep), dim3(kPrepThreads), 0, c.stream, a) != cudaSuccess) return SEL_ECUDA;
     }
     for (uint32_t i = 0; i < plan.pieces; ++i) {
         const uint32_t v0 = i * plan.piece, width = std::min(plan.piece, c.V - v0);
@@ -792,6 +864,7 @@ sel_status run_grad(const HeadLossCall& c, const float* lse, const float* grad, 
         ProbProblem<T> p{};
         if (!map16(&p.x, c.x, c.H, c.rows, kStepK, rows.n / 2) || !map16(&p.w, c.w, c.H, c.V, kStepK, kCtaM)) return SEL_ECUDA;
         p.p = static_cast<T*>(prob);
+        p.lost = lost;
         p.targets = c.targets;
         p.lse = lse;
         p.grad = grad;
@@ -811,6 +884,11 @@ sel_status run_grad(const HeadLossCall& c, const float* lse, const float* grad, 
             !map16(&g.w_mn, c.w, c.H, c.V, 64, kStepK))
             return SEL_ECUDA;
         g.exponent = exponent;
+        g.scaled = static_cast<const T*>(scaled);
+        g.lost = lost;
+        g.hits = hits;
+        g.targets = c.targets;
+        g.grad = grad;
         g.acc = acc;
         g.error = error;
         g.rows = c.rows;
@@ -832,7 +910,7 @@ sel_status run_grad(const HeadLossCall& c, const float* lse, const float* grad, 
         g.extra = light == workers ? 0 : std::min(g.dw_items / light, (g.k_slice / kStepK) / (g.dw_steps + 2));
         if (const sel_status s = launch_gemm(g, workers, c.stream); s != SEL_OK) return s;
     }
-    const GradFinishArgs f{acc, c.targets, grad, error, static_cast<uint4*>(dx), static_cast<uint4*>(dw), c.rows, c.V, vecs, plan.slices, shift};
+    const GradFinishArgs f{acc, lost, static_cast<const uint4*>(c.w), c.targets, grad, error, static_cast<uint4*>(dx), static_cast<uint4*>(dw), c.rows, c.V, vecs, plan.slices, shift};
     return launch_pdl(grad_finish_kernel<T>, dim3(blocks), dim3(kPrepThreads), 0, c.stream, f) == cudaSuccess ? SEL_OK : SEL_ECUDA;
 }
 
