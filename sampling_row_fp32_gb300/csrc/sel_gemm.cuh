@@ -54,12 +54,23 @@ struct GemmShared {
     uint32_t tmem, err;
 };
 
+// Division by a number that the host knows, of numbers below 2^31.
+struct Div {
+    uint32_t d, mul, shift;
+    Div() = default;
+    explicit Div(uint32_t by) : d(by), shift(0) {
+        while ((1ull << shift) < by) ++shift;
+        mul = static_cast<uint32_t>(((1ull << 32) * ((1ull << shift) - by)) / by + 1);
+    }
+    __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+};
+
 // A warp's place in a tile: this lane's row, the warp's first column and how many it
 // has, in pieces of 32 (the last may be short: what it reads beyond is meaningless).
 struct EpiWarp {
     uint32_t row, col, cols, chunks, lane;
-    uint32_t worker, workers;
-    bool first, last;     // of the worker's tiles
+    uint32_t j;           // the tile's number among the worker's
+    uint32_t kept;        // P's, from a tile to the next
     unsigned char* smem;  // kWarpBytes of its own
 };
 
@@ -176,9 +187,8 @@ __device__ __forceinline__ void store_chunk(const EpiWarp& w, const CUtensorMap*
 //                                      of a tile's parts meet in the epilogue's
 //                                      registers (0: all of them in tensor memory)
 //   uint32_t* error                    the workspace's error word
-//   count(worker, workers)             how many tiles a worker has
-//   tile(worker, workers, j)           the j-th of them
-//   epilogue(tile, w, arrive, load)    arrive(): waits for the sums; then load(c, v): the
+//   Cursor(p, worker, workers)         a worker's tiles: `count` of them, tile(j)
+//   epilogue(cursor, tile, w, arrive, load)  arrive(): waits for the sums; then load(c, v): the
 //                                      warp's columns 32 c .., for c = 0 .. chunks - 1 in
 //                                      order, each once
 template <typename P>
@@ -212,7 +222,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
     const uint32_t tmem = __shfl_sync(kFull, c.tmem, 0);
     pdl_wait();
     pdl_trigger();
-    const uint32_t count = p.count(worker, workers);
+    const typename P::Cursor cursor(p, worker, workers);
+    const uint32_t count = cursor.count;
 
     if (warp == 0) {
         const bool leader = elect_one();
@@ -220,7 +231,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
         uint32_t issued = 0;
         bool ok = true;
         for (uint32_t j = 0; j < count && ok; ++j) {
-            const GemmTile t = p.tile(worker, workers, j);
+            const GemmTile t = cursor.tile(j);
             const uint32_t am = t.am + rank * kCtaM, bn = t.bn + rank * (t.n / 2);
             const uint32_t b_boxes = (t.n + 127) / 128;  // of 64
             const uint32_t bytes = 2 * (kStageABytes + (t.b_mn ? b_boxes * 8192 : t.n * 64));
@@ -262,7 +273,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
         Ring<kGemmStages> st;
         Ring<2> dr;
         for (uint32_t j = 0; j < count; ++j) {
-            const GemmTile t = p.tile(worker, workers, j);
+            const GemmTile t = cursor.tile(j);
             const uint32_t idesc = kIdesc | (t.a_mn ? 1u << 15 : 0) | (t.b_mn ? 1u << 16 : 0) | ((t.n >> 3) << 17);
             const uint32_t step_a = t.a_mn ? 2048 >> 4 : 32 >> 4, step_b = t.b_mn ? 2048 >> 4 : 32 >> 4;
             wait(&c.d_empty[dr.i], dr.phase ^ 1, &c.err);
@@ -308,18 +319,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
         EpiWarp w;
         w.row = rank * kCtaM + quarter * 32 + lane;
         w.lane = lane;
-        w.worker = worker;
-        w.workers = workers;
+        w.kept = 0;
         w.smem = ring + kGemmStages * kStageBytes + (warp - 4) * kWarpBytes;
         Ring<2> dr;
         for (uint32_t j = 0; j < count; ++j) {
-            const GemmTile t = p.tile(worker, workers, j);
+            const GemmTile t = cursor.tile(j);
             const uint32_t low = (t.n / 2 + 15) / 16 * 16;  // (whole 32 bytes of 16-bit results)
             w.cols = half ? t.n - low : low;
             w.col = half * low;
             w.chunks = (w.cols + 31) / 32;
-            w.first = j == 0;
-            w.last = j == count - 1;
+            w.j = j;
             // (a short last piece reads on, at most to the end of the tensor memory)
             const uint32_t d = tmem + (quarter << 21) + w.col;
             auto piece = [&](uint32_t i, uint32_t (&r)[32]) {
@@ -355,7 +364,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
                 tc_fence_after();
                 if (w.chunks == 0) release();  // (16 columns: all of them the other half's)
             };
-            p.epilogue(t, w, arrived, [&](uint32_t i, float(&v)[32]) {
+            p.epilogue(cursor, t, w, arrived, [&](uint32_t i, float(&v)[32]) {
                 uint32_t r[32];
                 piece(i, r);
                 if (i == w.chunks - 1) release();  // the buffer is read

@@ -43,6 +43,20 @@ struct Raster {
     }
 };
 
+// Every workers-th tile of a raster.
+template <typename P>
+struct RasterCursor {
+    const P& p;
+    uint32_t worker, workers, count;
+    __device__ __forceinline__ RasterCursor(const P& of, uint32_t w, uint32_t n)
+        : p(of), worker(w), workers(n), count(of.raster.share(w, n)) {}
+    __device__ __forceinline__ GemmTile tile(uint32_t j) const {
+        uint32_t m, n;
+        p.raster.at(worker + j * workers, m, n);
+        return p.tile(m, n);
+    }
+};
+
 // 2^n for a whole n <= 0, 0 below the normal numbers (and for -Inf).
 __device__ __forceinline__ float pow2(float n) {
     return n >= -126.0f ? __uint_as_float(static_cast<uint32_t>(static_cast<int>(n) + 127) << 23) : 0.0f;
@@ -101,14 +115,12 @@ struct LossProblem {
     uint32_t rows, V, steps;
     Raster raster;
 
-    __device__ __forceinline__ uint32_t count(uint32_t worker, uint32_t workers) const { return raster.share(worker, workers); }
-    __device__ __forceinline__ GemmTile tile(uint32_t worker, uint32_t workers, uint32_t j) const {
-        uint32_t m, n;
-        raster.at(worker + j * workers, m, n);
+    using Cursor = RasterCursor<LossProblem>;
+    __device__ __forceinline__ GemmTile tile(uint32_t m, uint32_t n) const {
         return {&x, &w, m * kTileM, n * kTileN, 0, 0, steps, kTileN, false, false};
     }
     template <typename Arrive, typename Load>
-    __device__ __forceinline__ void epilogue(const GemmTile& t, const EpiWarp& w, Arrive arrived, Load load) const {
+    __device__ __forceinline__ void epilogue(const Cursor& cursor, const GemmTile& t, EpiWarp& w, Arrive arrived, Load load) const {
         const uint32_t row = t.am + w.row, col = t.bn + w.col;
         const uint32_t target = row < rows ? targets[row] : SEL_INVALID_ID;
         Part p{-INFINITY, 0.0f};
@@ -185,16 +197,21 @@ struct LossColumnsProblem {
 
     // A worker stays with its row tile and keeps that one's sums from tile to tile;
     // neighbours take the same ids with the other row tiles.
-    __device__ __forceinline__ uint32_t count(uint32_t worker, uint32_t workers) const {
-        const uint32_t v = worker / row_tiles, step = workers / row_tiles;
-        return v < v_tiles ? (v_tiles - v - 1) / step + 1 : 0;
-    }
-    __device__ __forceinline__ GemmTile tile(uint32_t worker, uint32_t workers, uint32_t j) const {
-        const uint32_t v = worker / row_tiles + j * (workers / row_tiles);
-        return {&w, &x, v * kTileM, worker % row_tiles * n, 0, 0, steps, n, false, false};
-    }
+    struct Cursor {
+        const LossColumnsProblem& p;
+        uint32_t row, v, step, count;
+        __device__ __forceinline__ Cursor(const LossColumnsProblem& of, uint32_t worker, uint32_t workers) : p(of) {
+            v = worker / p.row_tiles;
+            row = worker - v * p.row_tiles;
+            step = workers / p.row_tiles;
+            count = v < p.v_tiles ? (p.v_tiles - v - 1) / step + 1 : 0;
+        }
+        __device__ __forceinline__ GemmTile tile(uint32_t j) const {
+            return {&p.w, &p.x, (v + j * step) * kTileM, row * p.n, 0, 0, p.steps, p.n, false, false};
+        }
+    };
     template <typename Arrive, typename Load>
-    __device__ __forceinline__ void epilogue(const GemmTile& t, const EpiWarp& w, Arrive arrived, Load load) const {
+    __device__ __forceinline__ void epilogue(const Cursor& cursor, const GemmTile& t, EpiWarp& w, Arrive arrived, Load load) const {
         const uint32_t id = t.am + w.row, first = t.bn + w.col;
         auto* sums = reinterpret_cast<Part*>(w.smem) + w.lane;
         arrived();
@@ -234,14 +251,14 @@ struct LossColumnsProblem {
                 if (w.lane == i) m = top;
             }
             Part p{m, sum_across(v)};
-            if (!w.first) {
+            if (w.j > 0) {
                 const Part before = sums[32 * c];
                 const float top = fmaxf(p.m, before.m), ref = top == -INFINITY ? 0.0f : top;
                 p = {top, p.s * pow2(p.m - ref) + before.s * pow2(before.m - ref)};
             }
             sums[32 * c] = p;
-            if (w.last && mine)
-                parts[static_cast<uint64_t>(w.worker / row_tiles * 8 + w.row / 32) * rows + row] = p;
+            if (w.j == cursor.count - 1 && mine)
+                parts[static_cast<uint64_t>(cursor.v * 8 + w.row / 32) * rows + row] = p;
         }
     }
 };
@@ -385,14 +402,12 @@ struct ProbProblem {
     uint32_t rows, V, v0, width, steps, n, pitch;
     Raster raster;
 
-    __device__ __forceinline__ uint32_t count(uint32_t worker, uint32_t workers) const { return raster.share(worker, workers); }
-    __device__ __forceinline__ GemmTile tile(uint32_t worker, uint32_t workers, uint32_t j) const {
-        uint32_t r, v;
-        raster.at(worker + j * workers, r, v);
+    using Cursor = RasterCursor<ProbProblem>;
+    __device__ __forceinline__ GemmTile tile(uint32_t r, uint32_t v) const {
         return {&w, &x, v0 + v * kTileM, r * n, 0, 0, steps, n, false, false};
     }
     template <typename Arrive, typename Load>
-    __device__ __forceinline__ void epilogue(const GemmTile& t, const EpiWarp& w, Arrive arrived, Load load) const {
+    __device__ __forceinline__ void epilogue(const Cursor& cursor, const GemmTile& t, EpiWarp& w, Arrive arrived, Load load) const {
         const uint32_t id = t.am + w.row, first = t.bn + w.col;
         // the warp's rows: lse less ln |m|, and of 32 a bit for those that do not count,
         // one for a negative m, one for a target among the warp's ids
@@ -482,36 +497,38 @@ struct GradsProblem {
     float* acc;  // [slices][rows][H]
     uint32_t* error;
     uint32_t rows, V, H, v0, width;
-    uint32_t n_rows, row_tiles;            // dX: columns a tile
-    uint32_t dx_tiles, dx_items, k_slice;  // k_slice: ids of the piece a slice sums
-    uint32_t h_tiles;                      // dW: column tiles, the last of 128 where that is enough
+    uint32_t n_rows;             // dX: columns a tile
+    Div by_row_tiles, by_dx_tiles, by_h_tiles;  // (dW's last column tile: 128 where that is enough)
+    uint32_t dx_items, k_slice;  // k_slice: ids of the piece a slice sums
     uint32_t dw_items, dw_steps, extra;    // extra: dW tiles ahead for workers with one dX tile less
     bool add;
 
-    __device__ __forceinline__ uint32_t dx_count(uint32_t worker, uint32_t workers) const {
-        return worker < dx_items ? (dx_items - worker - 1) / workers + 1 : 0;
-    }
-    __device__ __forceinline__ uint32_t count(uint32_t worker, uint32_t workers) const {
-        const uint32_t more = dx_items % workers, light = workers - more;
-        const uint32_t rest = dw_items - extra * light;
-        const uint32_t dw = worker < rest ? (rest - worker - 1) / workers + 1 : 0;
-        return dx_count(worker, workers) + dw + (worker >= more ? extra : 0);
-    }
-    __device__ __forceinline__ GemmTile tile(uint32_t worker, uint32_t workers, uint32_t j) const {
-        const uint32_t dx = dx_count(worker, workers);
-        if (j < dx) {
-            const uint32_t i = worker + j * workers, slice = i / dx_tiles, at = i - slice * dx_tiles;
-            const uint32_t k0 = slice * k_slice, k1 = min(width, k0 + k_slice);
-            // (an empty slice sums one step of zeros past the piece's end)
-            const uint32_t steps = k1 > k0 ? (k1 - k0 + kStepK - 1) / kStepK : 1;
-            return {&w_mn, &p_mn, at / row_tiles * kTileM, at % row_tiles * n_rows, v0 + k0, k0, steps, n_rows, true, true};
+    struct Cursor {
+        const GradsProblem& p;
+        uint32_t worker, workers, dx, more, light, ahead, count;
+        __device__ __forceinline__ Cursor(const GradsProblem& of, uint32_t w, uint32_t n) : p(of), worker(w), workers(n) {
+            dx = w < p.dx_items ? (p.dx_items - w - 1) / n + 1 : 0;
+            more = p.dx_items % n;
+            light = n - more;
+            ahead = w >= more ? p.extra : 0;
+            const uint32_t rest = p.dw_items - p.extra * light;
+            count = dx + ahead + (w < rest ? (rest - w - 1) / n + 1 : 0);
         }
-        const uint32_t more = dx_items % workers, light = workers - more, e = worker >= more ? extra : 0;
-        j -= dx;
-        const uint32_t i = j < e ? worker - more + j * light : extra * light + worker + (j - e) * workers;
-        const uint32_t h = i % h_tiles * kTileN;
-        return {&p_k, &x_mn, i / h_tiles * kTileM, h, 0, 0, dw_steps, H - h <= kTileN / 2 ? kTileN / 2 : kTileN, false, true};
-    }
+        __device__ __forceinline__ GemmTile tile(uint32_t j) const {
+            if (j < dx) {
+                const uint32_t i = worker + j * workers, slice = p.by_dx_tiles(i), at = i - slice * p.by_dx_tiles.d;
+                const uint32_t h = p.by_row_tiles(at), r = at - h * p.by_row_tiles.d;
+                const uint32_t k0 = slice * p.k_slice, k1 = min(p.width, k0 + p.k_slice);
+                // (an empty slice sums one step of zeros past the piece's end)
+                const uint32_t steps = k1 > k0 ? (k1 - k0 + kStepK - 1) / kStepK : 1;
+                return {&p.w_mn, &p.p_mn, h * kTileM, r * p.n_rows, p.v0 + k0, k0, steps, p.n_rows, true, true};
+            }
+            j -= dx;
+            const uint32_t i = j < ahead ? worker - more + j * light : p.extra * light + worker + (j - ahead) * workers;
+            const uint32_t v = p.by_h_tiles(i), h = (i - v * p.by_h_tiles.d) * kTileN;
+            return {&p.p_k, &p.x_mn, v * kTileM, h, 0, 0, p.dw_steps, p.H - h <= kTileN / 2 ? kTileN / 2 : kTileN, false, true};
+        }
+    };
     // What row r's target entry lost, if its target is this lane's id, to columns x ..
     __device__ __forceinline__ void add_lost(uint32_t r, uint32_t id, uint32_t x, float (&v)[32]) const {
         if (targets[r] != id || id >= V || grad[r] == 0.0f) return;
@@ -530,12 +547,18 @@ struct GradsProblem {
         }
     }
     template <typename Arrive, typename Load>
-    __device__ __forceinline__ void epilogue(const GemmTile& t, const EpiWarp& w, Arrive arrived, Load load) const {
+    __device__ __forceinline__ void epilogue(const Cursor& cursor, const GemmTile& t, EpiWarp& w, Arrive arrived, Load load) const {
         if (!t.a_mn) {
             const Shift shift(*exponent);
             const uint32_t id = v0 + t.am + w.row - w.lane;
-            const uint32_t* kept = hits + static_cast<uint64_t>(id / 32) * (kKeptRows + 1);
-            const uint32_t n = id < V ? kept[0] : 0;
+            auto entry = [&](uint32_t of) { return hits + static_cast<uint64_t>(of / 32) * (kKeptRows + 1); };
+            const uint32_t* kept = entry(id);
+            // (how many rows the next tile's ids have is asked for a tile ahead)
+            const uint32_t n = w.j > cursor.dx ? w.kept : id < V ? kept[0] : 0;
+            if (w.j + 1 < cursor.count) {
+                const uint32_t next = id - t.am + cursor.tile(w.j + 1).am;
+                w.kept = next < V ? entry(next)[0] : 0;
+            }
             arrived();
 #pragma unroll 1
             for (uint32_t c = 0; c < w.chunks; ++c) {
@@ -548,7 +571,7 @@ struct GradsProblem {
                 store_chunk<T>(w, &dw, x, id, c, x < H && id < V, v);
             }
         } else {
-            const uint32_t h = t.am + w.row, slice = t.bk / k_slice, first = t.bn + w.col;
+            const uint32_t h = t.am + w.row, slice = by_dx_tiles(cursor.worker + w.j * cursor.workers), first = t.bn + w.col;
             float* o = acc + (static_cast<uint64_t>(slice) * rows + first) * H + h;
             arrived();
 #pragma unroll 1
@@ -630,7 +653,8 @@ __global__ void __launch_bounds__(kPrepThreads) grad_prep_kernel(PrepArgs a) {
     for (uint32_t v = blockIdx.x * (kPrepThreads / 32) + threadIdx.x / 32; v < (a.V + 31) / 32; v += warps) {
         uint32_t* to = a.hits + static_cast<uint64_t>(v) * (kKeptRows + 1);
         uint32_t found = 0;
-        for (uint32_t r0 = 0; r0 < a.rows && found < kKeptRows; r0 += 32) {
+#pragma unroll 8
+        for (uint32_t r0 = 0; r0 < a.rows; r0 += 32) {
             const uint32_t r = r0 + lane, t = r < a.rows ? a.targets[r] : SEL_INVALID_ID;
             const uint32_t mine = __ballot_sync(kFull, t / 32 == v);
             const uint32_t at = found + __popc(mine & ((1u << lane) - 1));
@@ -897,12 +921,12 @@ sel_status run_grad(const HeadLossCall& c, const float* lse, const float* grad, 
         g.v0 = v0;
         g.width = width;
         g.n_rows = plan.dx_n;
-        g.row_tiles = ceil_div(c.rows, plan.dx_n);
-        g.dx_tiles = ceil_div(c.H, kTileM) * g.row_tiles;
-        g.dx_items = dx ? g.dx_tiles * plan.slices : 0;
+        g.by_row_tiles = Div(ceil_div(c.rows, plan.dx_n));
+        g.by_dx_tiles = Div(ceil_div(c.H, kTileM) * g.by_row_tiles.d);
+        g.dx_items = dx ? g.by_dx_tiles.d * plan.slices : 0;
         g.k_slice = ceil_div(ceil_div(plan.piece, plan.slices), kStepK) * kStepK;
-        g.h_tiles = ceil_div(c.H, kTileN);
-        g.dw_items = dw ? ceil_div(width, kTileM) * g.h_tiles : 0;
+        g.by_h_tiles = Div(ceil_div(c.H, kTileN));
+        g.dw_items = dw ? ceil_div(width, kTileM) * g.by_h_tiles.d : 0;
         g.dw_steps = ceil_div(c.rows, kStepK);
         g.add = i > 0;
         const uint32_t workers = std::min(all, g.dx_items + g.dw_items);

@@ -359,3 +359,30 @@ def test_offsets_past_32_bits():
     want_0 = (u[:, None] * x.double()).sum(0)
     assert ((dw[:5].double() - want_0).abs() <= 2.0 ** -7 * (u[:, None] * x.double().abs()).sum(0) + 1e-6).all()
     assert ((dx.double() - p @ tail.double()).abs() <= 2.0 ** -7 * (p.abs() @ tail.double().abs()) + 1e-6).all()
+
+
+@pytest.mark.parametrize("same", [1, 8, 40])
+@pytest.mark.parametrize("rows", [40, 300])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_target_entries_are_not_rounded(dtype, rows, same):
+    """Gradients whose mantissa lies half way between two values of the type: rounded, a
+    target's entry (nearly -1 here) would put 2^-8 (f16: 2^-11) of itself on all of its
+    row's gradient. The results' own rounding has no such lean: over N entries it leaves
+    about 0.6 / sqrt(N) of that, below 0.05."""
+    V, H = 4000, 512
+    half = torch.finfo(DT[dtype]).eps / 2
+    x, w, t, _ = make(15, rows, V, H, dtype, spread=0.5, ignored=0.0)
+    x = x * 0.1
+    # up to eight rows a run of 32 ids (at most 299 * 13 + 5 = 3,892)
+    t = torch.arange(rows, device="cuda").int() // same * (13 if same == 1 else 33) + 5
+    grad = torch.full((rows,), 1 + half, device="cuda") * torch.where(torch.arange(rows, device="cuda") % 2 == 0, -4.0, 4.0)
+    if same > 1:
+        grad = grad.abs()
+    _, lse = run_loss(x, w, t)
+    dx, dw = check_grad(x, w, t, lse, grad)
+    want_x, want_w = L.head_loss_grad(x, w, t, lse, grad)
+    # (runs of 32 ids with more than eight rows keep the roundings of the rest)
+    pairs = [(dx, want_x)] + ([(dw[t.long().unique()], want_w[t.long().unique()])] if same <= 8 else [])
+    for got, want in pairs:
+        lean = ((got.double() - want) * want).sum() / want.square().sum()
+        assert abs(lean.item()) < 0.25 * half, lean.item() / half
