@@ -368,6 +368,7 @@ struct GradParts {
 // back in fp32: to dX by the last launch, to dW's rows in the epilogue, for the first
 // few hidden rows with a target among a warp's ids (of many the roundings average).
 constexpr uint32_t kKeptRows = 8;
+constexpr uint32_t kHitWords = 1 + 2 * kKeptRows;  // of 32 ids: how many rows, the rows, their targets
 
 // f16 holds P times 2^14: entries down to 2^-28 stay normal numbers, and the
 // target's, no smaller than -1, does not overflow.
@@ -491,9 +492,7 @@ struct GradsProblem {
     const int* exponent;  // of dW's sums
     const T* scaled;      // [rows][H]: the hidden rows of dW
     const float* lost;
-    const uint32_t* hits;  // [V / 32][1 + kKeptRows]: rows with a target among 32 ids
-    const uint32_t* targets;
-    const float* grad;
+    const uint32_t* hits;  // [V / 32][kHitWords]
     float* acc;  // [slices][rows][H]
     uint32_t* error;
     uint32_t rows, V, H, v0, width;
@@ -529,42 +528,47 @@ struct GradsProblem {
             return {&p.p_k, &p.x_mn, v * kTileM, h, 0, 0, p.dw_steps, p.H - h <= kTileN / 2 ? kTileN / 2 : kTileN, false, true};
         }
     };
-    // What row r's target entry lost, if its target is this lane's id, to columns x ..
-    __device__ __forceinline__ void add_lost(uint32_t r, uint32_t id, uint32_t x, float (&v)[32]) const {
-        if (targets[r] != id || id >= V || grad[r] == 0.0f) return;
-        const float f = lost[r];
-        const T* row = scaled + static_cast<uint64_t>(r) * H;
-#pragma unroll
-        for (uint32_t i = 0; i < 32; i += 8) {
-            if (x + i >= H) break;
-            const uint4 q = *reinterpret_cast<const uint4*>(row + x + i);
-            const uint32_t u[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-            for (uint32_t k = 0; k < 4; ++k) {
-                v[i + 2 * k] = fmaf(f, bits_f32<T>(static_cast<uint16_t>(u[k])), v[i + 2 * k]);
-                v[i + 2 * k + 1] = fmaf(f, bits_f32<T>(static_cast<uint16_t>(u[k] >> 16)), v[i + 2 * k + 1]);
-            }
-        }
-    }
     template <typename Arrive, typename Load>
     __device__ __forceinline__ void epilogue(const Cursor& cursor, const GemmTile& t, EpiWarp& w, Arrive arrived, Load load) const {
         if (!t.a_mn) {
             const Shift shift(*exponent);
             const uint32_t id = v0 + t.am + w.row - w.lane;
-            auto entry = [&](uint32_t of) { return hits + static_cast<uint64_t>(of / 32) * (kKeptRows + 1); };
-            const uint32_t* kept = entry(id);
-            // (how many rows the next tile's ids have is asked for a tile ahead)
-            const uint32_t n = w.j > cursor.dx ? w.kept : id < V ? kept[0] : 0;
-            if (w.j + 1 < cursor.count) {
-                const uint32_t next = id - t.am + cursor.tile(w.j + 1).am;
-                w.kept = next < V ? entry(next)[0] : 0;
+            // (lane k has word k of the ids' hits; the next tile's are asked for a tile ahead)
+            auto entry = [&](uint32_t of) {
+                return of < V && w.lane < kHitWords ? hits[static_cast<uint64_t>(of / 32) * kHitWords + w.lane] : 0u;
+            };
+            const uint32_t kept = w.j > cursor.dx ? w.kept : entry(id);
+            if (w.j + 1 < cursor.count) w.kept = entry(id - t.am + cursor.tile(w.j + 1).am);
+            const uint32_t n = __shfl_sync(kFull, kept, 0);
+            // lane k: what the k-th row's entry lost; x0: the first row's columns of all
+            // pieces, so that nothing is waited for below
+            float less = 0.0f;
+            T x0[4] = {};
+            const uint32_t col = t.bn + w.col + w.lane;
+            auto hidden = [&](uint32_t r, uint32_t x) { return x < H ? scaled[static_cast<uint64_t>(r) * H + x] : T{}; };
+            if (n > 0) {
+                const uint32_t r = __shfl_sync(kFull, kept, 1), mine = __shfl_sync(kFull, kept, 1 + w.lane);
+                if (w.lane < n) less = lost[mine];
+#pragma unroll
+                for (uint32_t c = 0; c < 4; ++c) x0[c] = hidden(r, col + 32 * c);
             }
             arrived();
 #pragma unroll 1
             for (uint32_t c = 0; c < w.chunks; ++c) {
                 float v[32];
                 load(c, v);
-                for (uint32_t k = 0; k < n; ++k) add_lost(kept[1 + k], id + w.lane, t.bn + w.col + 32 * c, v);
+                for (uint32_t k = 0; k < n; ++k) {
+                    const float f = __shfl_sync(kFull, less, k);
+                    const bool mine = __shfl_sync(kFull, kept, 1 + kKeptRows + k) == id + w.lane;
+                    const uint32_t r = __shfl_sync(kFull, kept, 1 + k);
+                    const T x = k > 0 ? hidden(r, col + 32 * c) : c == 0 ? x0[0] : c == 1 ? x0[1] : c == 2 ? x0[2] : x0[3];
+                    const float xf = to_f32(x);
+#pragma unroll
+                    for (uint32_t i = 0; i < 32; ++i) {
+                        const float xi = __shfl_sync(kFull, xf, i);
+                        if (mine) v[i] = fmaf(f, xi, v[i]);
+                    }
+                }
 #pragma unroll
                 for (uint32_t i = 0; i < 32; ++i) v[i] = shift(v[i]);
                 const uint32_t x = t.bn + w.col + c / 2 * 64;
@@ -651,14 +655,17 @@ __global__ void __launch_bounds__(kPrepThreads) grad_prep_kernel(PrepArgs a) {
     }
     const uint32_t lane = threadIdx.x & 31, warps = gridDim.x * (kPrepThreads / 32);
     for (uint32_t v = blockIdx.x * (kPrepThreads / 32) + threadIdx.x / 32; v < (a.V + 31) / 32; v += warps) {
-        uint32_t* to = a.hits + static_cast<uint64_t>(v) * (kKeptRows + 1);
+        uint32_t* to = a.hits + static_cast<uint64_t>(v) * kHitWords;
         uint32_t found = 0;
 #pragma unroll 8
         for (uint32_t r0 = 0; r0 < a.rows; r0 += 32) {
             const uint32_t r = r0 + lane, t = r < a.rows ? a.targets[r] : SEL_INVALID_ID;
-            const uint32_t mine = __ballot_sync(kFull, t / 32 == v);
+            const uint32_t mine = __ballot_sync(kFull, t / 32 == v && t < a.V && a.grad[r] != 0.0f);
             const uint32_t at = found + __popc(mine & ((1u << lane) - 1));
-            if ((mine >> lane & 1) && at < kKeptRows) to[1 + at] = r;
+            if ((mine >> lane & 1) && at < kKeptRows) {
+                to[1 + at] = r;
+                to[1 + kKeptRows + at] = t;
+            }
             found += __popc(mine);
         }
         if (lane == 0) to[0] = min(found, kKeptRows);
@@ -788,7 +795,7 @@ inline GradPlan grad_plan(uint32_t rows, uint32_t V, uint32_t H) {
     g.slices = std::min(std::max(1u, g.piece / 1024), tiles >= 76 ? 1u : ceil_div(76, tiles));
     g.lost = kWsHeaderBytes;
     g.hits = g.lost + align_up(static_cast<size_t>(rows) * sizeof(float), 256);
-    g.scaled = g.hits + align_up(ceil_div(V, 32) * (kKeptRows + 1) * sizeof(uint32_t), 256);
+    g.scaled = g.hits + align_up(static_cast<size_t>(ceil_div(V, 32)) * kHitWords * sizeof(uint32_t), 256);
     g.acc = g.scaled + align_up(static_cast<size_t>(rows) * H * 2, 256);
     // What the sums and P take at most: slices * tiles < 76 + tiles, and P as above;
     // these bounds grow with each size, so that a workspace serves smaller calls too.
@@ -911,8 +918,6 @@ sel_status run_grad(const HeadLossCall& c, const float* lse, const float* grad, 
         g.scaled = static_cast<const T*>(scaled);
         g.lost = lost;
         g.hits = hits;
-        g.targets = c.targets;
-        g.grad = grad;
         g.acc = acc;
         g.error = error;
         g.rows = c.rows;
