@@ -283,24 +283,36 @@ struct LossFinishArgs {
     uint32_t rows, V, slots;
 };
 
-// The loss and lse of a row from the joined weights of its other ids.
+// The loss and lse of a row from the joined weights of its other ids. The difference
+// of ln sum others and the target's logit is a float pair, so that a loss near zero,
+// its exponential, keeps its bits. (In 64 bits these few steps took 5 us more, of a
+// row's 54.)
 __device__ __forceinline__ void finish_row(const LossFinishArgs& a, uint32_t row, const Joined& j) {
     const uint32_t t = a.targets[row];
-    // (one row's last steps: in 64 bits they cost nothing next to its launch)
-    const double c = static_cast<double>(kLog2E);
-    const double sum = ff_to_double(j.s);
-    const double others = sum == 0.0 ? -INFINITY : (static_cast<double>(j.m) + log2(sum)) / c;
-    double loss = 0.0, lse = others;
+    // ln of the sum: its power of two over log2(e) as the weights have it, and the rest
+    constexpr double kOver = 1.0 / static_cast<double>(kLog2E);
+    constexpr float kHi = static_cast<float>(kOver), kLo = static_cast<float>(kOver - static_cast<double>(kHi));
+    const float sum = j.s.hi + j.s.lo;
+    const bool some = sum > 0.0f && sum < INFINITY;
+    int e = 0;
+    const float f = some ? frexpf(sum, &e) : sum;  // in [1/2, 1); the sum is at least 2^-1 or nothing
+    const float n = j.m + static_cast<float>(e);
+    const float p = __fmul_rn(n, kHi);
+    FF others{p, __fmaf_rn(n, kLo, __fmaf_rn(n, kHi, -p))};
+    others = ff_add(others, FF{logf(f), 0.0f});
+    if (!some) others = FF{sum == 0.0f ? -INFINITY : NAN, 0.0f};
+    float loss = 0.0f, lse = others.hi;
     if (t < a.V) {
-        const double z = static_cast<double>(a.at[row]), d = others - z;
-        loss = d > 40.0 ? d + exp(-d) : log1p(exp(d));
-        lse = z + loss;
-        if (z == -INFINITY) lse = others;
+        const float z = a.at[row];
+        FF d = ff_add(others, FF{-z, 0.0f});
+        if (!(fabsf(d.hi) < INFINITY)) d = FF{others.hi - z, 0.0f};
+        loss = d.hi > 20.0f ? d.hi + (d.lo + expf(-d.hi)) : log1pf(expf(d.hi) * (1.0f + d.lo));
+        lse = z == -INFINITY ? others.hi : z + loss;
         if (z == INFINITY) loss = lse = NAN;
     }
     if (*a.error) loss = lse = NAN;
-    a.loss[row] = static_cast<float>(loss);
-    if (a.lse) a.lse[row] = static_cast<float>(lse);
+    a.loss[row] = loss;
+    if (a.lse) a.lse[row] = lse;
 }
 
 constexpr uint32_t kFinishThreads = 1024, kFinishWarps = kFinishThreads / 32;
@@ -331,8 +343,8 @@ __global__ void __launch_bounds__(kFinishThreads) loss_finish_kernel(LossFinishA
     sh[warp][lane] = j;
     __syncthreads();
     if (kWide) {
-        // a warp takes a row, a lane another warp's share of it; the last steps, in 64
-        // bits, by the lanes of one warp
+        // a warp takes a row, a lane another warp's share of it; the last steps by the
+        // lanes of one warp
         j = across(sh[lane][warp]);
         __syncthreads();
         if (lane == 0) sh[0][warp] = j;
@@ -604,11 +616,17 @@ struct PrepArgs {
     const float* grad;
     int* exponent;           // of dW's sums
     uint32_t* hits;
-    uint32_t rows, V, vecs;  // vecs: of 8 entries a row
+    uint32_t rows, V;
+    Div by_vecs;             // vectors of 8 entries a row
     int shift;  // P's
 };
 
 constexpr uint32_t kPrepThreads = 128;
+
+// The row of the i-th vector of all rows.
+__device__ __forceinline__ uint32_t row_of(uint64_t i, const Div& by) {
+    return i < (1ull << 31) ? by(static_cast<uint32_t>(i)) : static_cast<uint32_t>(i / by.d);
+}
 
 template <typename T>
 __device__ __forceinline__ void unpack2(uint32_t w, float& lo, float& hi) {
@@ -634,10 +652,10 @@ __global__ void __launch_bounds__(kPrepThreads) grad_prep_kernel(PrepArgs a) {
 #pragma unroll
     for (uint32_t i = 0; i < kPrepThreads / 32; ++i) top = max(top, sh[i]);
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.exponent = max(top, -200) - a.shift;
-    const uint64_t n = static_cast<uint64_t>(a.rows) * a.vecs;
+    const uint64_t n = static_cast<uint64_t>(a.rows) * a.by_vecs.d;
     for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * kPrepThreads + threadIdx.x; i < n;
          i += static_cast<uint64_t>(gridDim.x) * kPrepThreads) {
-        const uint32_t r = static_cast<uint32_t>(i / a.vecs);
+        const uint32_t r = row_of(i, a.by_vecs);
         const float g = a.grad[r];
         uint4 q = make_uint4(0, 0, 0, 0);
         if (a.targets[r] < a.V && g != 0.0f) {
@@ -681,7 +699,8 @@ struct GradFinishArgs {
     const uint32_t* error;
     uint4* dx;  // NULL: not wanted
     uint4* dw;
-    uint32_t rows, V, vecs, slices;
+    uint32_t rows, V, slices;
+    Div by_vecs;
     int shift;  // P's
 };
 
@@ -691,18 +710,18 @@ template <typename T>
 __global__ void __launch_bounds__(kPrepThreads) grad_finish_kernel(GradFinishArgs a) {
     pdl_wait();
     pdl_trigger();
-    const uint64_t n = static_cast<uint64_t>(a.rows) * a.vecs;
+    const uint64_t n = static_cast<uint64_t>(a.rows) * a.by_vecs.d;
     const uint64_t first = static_cast<uint64_t>(blockIdx.x) * kPrepThreads + threadIdx.x;
     const uint64_t step = static_cast<uint64_t>(gridDim.x) * kPrepThreads;
     const bool bad = *a.error != 0;
     const uint32_t nan2 = pack2<T>(NAN, NAN);
     for (uint64_t i = first; a.dx && i < n; i += step) {
-        const uint32_t r = static_cast<uint32_t>(i / a.vecs);
+        const uint32_t r = row_of(i, a.by_vecs);
         const float g = a.grad[r];
         uint4 q = make_uint4(0, 0, 0, 0);
         if (a.targets[r] < a.V && g != 0.0f) {
             float s[8] = {};
-#pragma unroll 4
+#pragma unroll 10
             for (uint32_t k = 0; k < a.slices; ++k) {
                 const float4* p = reinterpret_cast<const float4*>(a.acc) + 2 * (k * n + i);
                 const float4 u = p[0], v = p[1];
@@ -710,7 +729,7 @@ __global__ void __launch_bounds__(kPrepThreads) grad_finish_kernel(GradFinishArg
                 s[4] += v.x, s[5] += v.y, s[6] += v.z, s[7] += v.w;
             }
             const float f = a.lost[r];
-            const uint4 of = a.w[static_cast<uint64_t>(a.targets[r]) * a.vecs + i % a.vecs];
+            const uint4 of = a.w[static_cast<uint64_t>(a.targets[r]) * a.by_vecs.d + (i - static_cast<uint64_t>(r) * a.by_vecs.d)];
             const uint32_t u[4] = {of.x, of.y, of.z, of.w};
 #pragma unroll
             for (uint32_t k = 0; k < 4; ++k) {
@@ -728,7 +747,7 @@ __global__ void __launch_bounds__(kPrepThreads) grad_finish_kernel(GradFinishArg
         a.dx[i] = q;
     }
     if (bad && a.dw) {
-        for (uint64_t i = first; i < static_cast<uint64_t>(a.V) * a.vecs; i += step)
+        for (uint64_t i = first; i < static_cast<uint64_t>(a.V) * a.by_vecs.d; i += step)
             a.dw[i] = make_uint4(nan2, nan2, nan2, nan2);
     }
 }
@@ -885,7 +904,7 @@ sel_status run_grad(const HeadLossCall& c, const float* lse, const float* grad, 
     const uint32_t vecs = c.H / 8, all = sms / 2;
     const uint32_t blocks = static_cast<uint32_t>(std::min<uint64_t>(8 * sms, ceil_div(static_cast<uint64_t>(c.rows) * vecs, kPrepThreads)));
     if (dw) {
-        const PrepArgs a{static_cast<const uint4*>(c.x), static_cast<uint4*>(scaled), c.targets, grad, exponent, hits, c.rows, c.V, vecs, shift};
+        const PrepArgs a{static_cast<const uint4*>(c.x), static_cast<uint4*>(scaled), c.targets, grad, exponent, hits, c.rows, c.V, Div(vecs), shift};
         const uint32_t prep = std::max(blocks, std::min(8u * sms, ceil_div(c.V, 32 * (kPrepThreads / 32))));
         if (launch_pdl(grad_prep_kernel<T>, dim3(prep), dim3(kPrepThreads), 0, c.stream, a) != cudaSuccess) return SEL_ECUDA;
     }
@@ -939,7 +958,7 @@ sel_status run_grad(const HeadLossCall& c, const float* lse, const float* grad, 
         g.extra = light == workers ? 0 : std::min(g.dw_items / light, (g.k_slice / kStepK) / (g.dw_steps + 2));
         if (const sel_status s = launch_gemm(g, workers, c.stream); s != SEL_OK) return s;
     }
-    const GradFinishArgs f{acc, lost, static_cast<const uint4*>(c.w), c.targets, grad, error, static_cast<uint4*>(dx), static_cast<uint4*>(dw), c.rows, c.V, vecs, plan.slices, shift};
+    const GradFinishArgs f{acc, lost, static_cast<const uint4*>(c.w), c.targets, grad, error, static_cast<uint4*>(dx), static_cast<uint4*>(dw), c.rows, c.V, plan.slices, Div(vecs), shift};
     return launch_pdl(grad_finish_kernel<T>, dim3(blocks), dim3(kPrepThreads), 0, c.stream, f) == cudaSuccess ? SEL_OK : SEL_ECUDA;
 }
 
