@@ -2,9 +2,11 @@
  * sel.h -- C ABI of the GB300 (sm_103a) decode-step token-selection library.
  *
  * Four operations over batched fp32 logits rows of a vocabulary of V entries:
- * argmax, exact top-k, filtered sampling and speculative acceptance; and the
+ * argmax, exact top-k, filtered sampling and speculative acceptance; the
  * operators around them (4-bit output head, sampling of 16-bit rows with a
- * policy per row, embedding of the drawn ids), declared at the end. Every
+ * policy per row, embedding of the drawn ids); and those a drafter learns with
+ * (cross entropy through a 16-bit head, divergence from a teacher's top
+ * logits, and their gradients), declared at the end. Every
  * entry point takes device pointers, sizes, the policy parameters, a
  * caller-owned workspace and a cudaStream_t, validates its arguments on the
  * host, enqueues its kernels on that stream and returns. It never allocates,
@@ -765,6 +767,7 @@ sel_status sel_embed_w4(const uint32_t *d_ids, uint32_t n, const uint8_t *d_q,
 
 /*
  * Learning: what a drafter is trained with on the rows that selection works on.
+ * Inputs and outputs must not overlap, but where it is said that they may.
  *
  * sel_head_loss -- cross entropy of hidden states through a 16-bit output head,
  * the logits z[r][v] = sum over k of hidden[r][k] * weight[v][k] never stored:
@@ -783,6 +786,8 @@ sel_status sel_embed_w4(const uint32_t *d_ids, uint32_t n, const uint8_t *d_q,
  *   d_loss       [rows] f32
  *   d_lse        [rows] f32, or NULL
  *   d_ws         workspace of sel_workspace_bytes(SEL_OP_HEAD_LOSS, rows, V, H)
+ * A wait on the GPU that runs out raises the workspace's first word; with it
+ * raised this call and the next give NaN until sel_workspace_init clears it.
  */
 sel_status sel_head_loss(const void *d_hidden, uint32_t rows,
                          const void *d_weight, int dtype, uint32_t V,
@@ -796,10 +801,12 @@ sel_status sel_head_loss(const void *d_hidden, uint32_t rows,
  *   hidden_grad[r] = grad[r] * sum over v of P[r][v] * weight[v]
  *   weight_grad[v] = sum over r of grad[r] * P[r][v] * hidden[r].
  * Ignored rows and rows whose grad is 0 count for nothing, whatever they hold:
- * their hidden_grad is zeros. P is rounded to `dtype` for the products, as is
- * hidden times grad over the largest grad (exactly hidden where all grads
- * are equal); sums are in fp32 and each gradient is rounded once. z is
- * computed again, in pieces of the vocabulary.
+ * their hidden_grad is zeros. A row with a nonfinite logit, lse or grad makes its
+ * own hidden_grad and all of weight_grad nonfinite. P times the mantissa of
+ * the row's grad is rounded to `dtype` for the products (what that takes from the
+ * targets' entries is added back); sums are in fp32 and each gradient is
+ * rounded once. z is computed again, in pieces of the vocabulary, so the
+ * workspace holds at most 2^28 entries of P, or 16,384 columns of it.
  *
  *   d_hidden, rows, d_weight, dtype, V, H, d_targets  as for sel_head_loss
  *   d_lse          [rows] f32, from sel_head_loss
