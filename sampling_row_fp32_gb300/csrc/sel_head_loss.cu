@@ -5,15 +5,23 @@
 //   P_rv = exp(z_rv - lse_r) - [v == t_r]
 //   dX_r = g_r sum_v P_rv W_v;  dW_v = sum_r g_r P_rv X_r
 //
-// The loss is one product (sel_gemm.cuh) whose epilogue keeps two numbers of each
-// row and 128 ids (32 where the rows lie on the columns), a reference exponent and
-// the sum of the others' weights over it; a small launch joins them. The target's logit is kept apart, so that
-// loss = ln(1 + sum_others / e^z_t) holds its bits where it is near zero.
+// The loss is one product (sel_gemm.cuh) whose epilogue keeps two numbers of each row
+// and 128 ids, or of each row and all ids of a worker: a reference exponent and the
+// sum of the others' weights over it. A small launch joins them. The target's logit is
+// kept apart, so that loss = ln(1 + sum_others / e^z_t) holds its bits near zero.
 //
 // The gradient goes over the vocabulary in pieces. For each, one launch computes
 // z again and leaves P in the workspace, rounded to the operands' type; a second
 // one computes the piece's rows of dW (K = rows) and adds the piece's share of
 // dX (K = the piece) to fp32 sums.
+//
+// What bounds them: the matrix's bytes for few rows (49 of 4,096 x 248,320: 297-308 us,
+// 6.7 TB/s; one of 1,024 x 151,936: 51), the tensor cores for many (4,096 rows: 98.6, 96.5
+// and 96.5 percent of their cycles in the three products; 4,096 x 151,936 in 2.43 ms
+// alone and 2.79 back to back, where the card's power limits it; the gradient of 2,048 x
+// 151,936 in 3.9 and 4.5). Between them padding counts: 777 rows of 2,880 x 93,001 take
+// 282 us (1.48 PFLOP/s) and 840. The gradient of 64 rows of 1,024 x 151,936 takes 208, 52
+// for P and 130 for the rest: the matrix is read twice.
 #include <algorithm>
 
 #include <cuda_runtime.h>
@@ -102,7 +110,7 @@ struct Weights {
 constexpr uint32_t kLossPart = 1024 / kStepK;
 
 // Hidden rows on the product's rows: a lane has one of them, and half a tile's
-// columns of z.
+// columns of z, so that its sum crosses no lanes. For rows that fill their tiles.
 template <typename T>
 struct LossProblem {
     using Type = T;
@@ -161,8 +169,10 @@ struct LossProblem {
     }
 };
 
-// Hidden rows on the product's columns, so that a tile has as few as 16 of them: a
-// lane has one id, and the logits of half a tile's rows for it.
+// Hidden rows on the product's columns, so that a tile has as few as 16 of them (one row
+// of 1,024 x 151,936: 71 us on rows, 54 here; 777: 335 and 272): a lane has one id, and
+// the logits of half a tile's rows for it. About 8 more instructions a logit for the
+// sums across the lanes, which the product of one more row tile outweighs.
 
 // Of 32 rows' values in each lane, the sums over the lanes: lane i gets row i's.
 __device__ __forceinline__ float sum_across(float (&v)[32]) {
@@ -400,7 +410,8 @@ __device__ __forceinline__ void store16(T* to, const float (&v)[32], uint32_t i)
 }
 
 // P of a piece: [its ids][hidden rows]. Hidden rows lie on the product's columns, so
-// that a tile has no more of them than it needs.
+// that a tile has no more of them than it needs. (Stores of 16 bytes: 474 us instead of
+// 430 for a piece of 4,096 rows.)
 template <typename T>
 struct ProbProblem {
     using Type = T;
@@ -495,7 +506,8 @@ struct ProbProblem {
     }
 };
 
-// Items of a worker: its tiles of dX first, each a long sum, then its tiles of dW.
+// Items of a worker: its tiles of dX first, each a long sum, then its tiles of dW, one
+// launch for both so that those even out what these leave.
 template <typename T>
 struct GradsProblem {
     using Type = T;
@@ -505,13 +517,13 @@ struct GradsProblem {
     const T* scaled;      // [rows][H]: the hidden rows of dW
     const float* lost;
     const uint32_t* hits;  // [V / 32][kHitWords]
-    float* acc;  // [slices][rows][H]
+    float* acc;            // [slices][rows][H]
     uint32_t* error;
     uint32_t rows, V, H, v0, width;
-    uint32_t n_rows;             // dX: columns a tile
+    uint32_t n_rows;                            // dX: columns a tile
     Div by_row_tiles, by_dx_tiles, by_h_tiles;  // (dW's last column tile: 128 where that is enough)
-    uint32_t dx_items, k_slice;  // k_slice: ids of the piece a slice sums
-    uint32_t dw_items, dw_steps, extra;    // extra: dW tiles ahead for workers with one dX tile less
+    uint32_t dx_items, k_slice;                 // k_slice: ids of the piece a slice sums
+    uint32_t dw_items, dw_steps, extra;         // extra: dW tiles ahead for workers with one dX tile less
     bool add;
 
     struct Cursor {
@@ -614,11 +626,11 @@ struct PrepArgs {
     uint4* scaled;  // x times 2^e over the largest gradient's
     const uint32_t* targets;
     const float* grad;
-    int* exponent;           // of dW's sums
+    int* exponent;  // of dW's sums
     uint32_t* hits;
     uint32_t rows, V;
-    Div by_vecs;             // vectors of 8 entries a row
-    int shift;  // P's
+    Div by_vecs;    // vectors of 8 entries a row
+    int shift;      // P's
 };
 
 constexpr uint32_t kPrepThreads = 128;
@@ -804,12 +816,12 @@ inline GradPlan grad_plan(uint32_t rows, uint32_t V, uint32_t H) {
     const uint64_t cap = std::max<uint64_t>(16384, (1ull << 28) / g.pitch);
     g.piece = ceil_div(ceil_div(V, ceil_div(V, cap)), kTileM) * kTileM;
     g.pieces = ceil_div(V, g.piece);
-    // few tiles of dX: the sum over the piece is split
     // dX's columns a tile: equal tiles pad less, but their halves begin anywhere in a
     // line of P and are copied 64 rows at a time: 777 rows (4 x 208 or 4 x 256) 578 us
     // against 541 for a piece's gradients
     const Columns c(rows);
     g.dx_n = rows <= kTileN || c.padded() * 1.38 < static_cast<double>(ceil_div(rows, kTileN)) * kTileN ? c.n : kTileN;
+    // few tiles of dX: the sum over the piece is split
     const uint64_t tiles = static_cast<uint64_t>(ceil_div(H, kTileM)) * ceil_div(rows, g.dx_n);
     g.slices = std::min(std::max(1u, g.piece / 1024), tiles >= 76 ? 1u : ceil_div(76, tiles));
     g.lost = kWsHeaderBytes;

@@ -223,6 +223,7 @@ def test_distill_validation(lib):
         assert f(V=5000, ld=5000, k=1025, **({"ld_out": 5000} if f is grad else {})) == B.SEL_EUNSUPPORTED
         V = (1 << 20) + 1
         assert f(V=V, ld=V, **({"ld_out": V} if f is grad else {})) == B.SEL_EUNSUPPORTED
+        assert f(rows=0x80000000) == B.SEL_EUNSUPPORTED
     assert distill(loss=None) == B.SEL_EINVAL
     for kw in (dict(g=None), dict(out=None), dict(g=F + 2), dict(out=F + 2), dict(ld_out=9), dict(out=F, ld=12, ld_out=10)):
         assert grad(**kw) == B.SEL_EINVAL, kw
