@@ -10,9 +10,11 @@
 //
 // Clusters of C CTAs walk the rows, each CTA with a share of a row's vectors. Warp
 // roles:
-//   warp 8     reads the list for the teacher's normaliser and mass, and copies the
-//              share into a ring of shared-memory chunks; it runs ahead, into the
-//              next row as its chunks become free
+//   warp 8     copies the share into a ring of shared-memory chunks; it runs ahead,
+//              into the next row as its chunks become free
+//   warp 9     reads the lists for the teacher's normaliser and mass, up to two rows
+//              ahead (by the copying warp, lists of 200 held up its copies: 777 rows
+//              of 93,001 in 77 us)
 //   warps 0-7  mark the list's ids that fall in the share in a bitmap (an id marked
 //              twice is a repeated one), sum the share's weights, exchange the sums
 //              with the row's other CTAs, and write the gradient from the same
@@ -46,7 +48,7 @@ using namespace sel;
 namespace sel {
 namespace {
 
-constexpr uint32_t kNT = 256, kWarps = kNT / 32, kThreads = kNT + 32, kMaxC = 8;
+constexpr uint32_t kNT = 256, kWarps = kNT / 32, kThreads = kNT + 64, kMaxC = 8;
 constexpr uint32_t kEntries = SEL_MAX_K / kNT;  // of a list, a thread
 constexpr uint32_t kBatch = 4;                  // vectors a thread takes at a time
 constexpr uint32_t kChunkVecs = kBatch * kNT, kChunkBytes = 16 * kChunkVecs, kMaxSlots = 6;
@@ -754,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(DistillArgs a) {
         }
         for (uint32_t i = 0; i < 2; ++i) {
             mbar_init(&s.t_full[i], 1);
-            mbar_init(&s.t_empty[i], kWarps);
+            mbar_init(&s.t_empty[i], kWarps + 1);
             mbar_init(&s.sums[i], 1);
             mbar_init(&s.loss[i], 1);
         }
@@ -786,15 +788,12 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(DistillArgs a) {
                 }
             };
             if (n == 0) copy(0, early);  // (before it is known whether the row counts)
-            if (n >= 2) ok = ok && __all_sync(kFull, mbar_wait(&s.t_empty[n & 1], (n >> 1) + 1 & 1));
-            const Teacher t = read_teacher(a, row);
-            if ((tid & 31) == 0) {
-                s.teacher[n & 1] = t;
-                arrive(&s.t_full[n & 1]);
-            }
+            ok = ok && __all_sync(kFull, mbar_wait(&s.t_full[n & 1], n >> 1 & 1));
+            const bool live = s.teacher[n & 1].live;
             __syncwarp();
-            if (t.live) copy(n == 0 ? early : 0, vecs);
-            if (kGrad && !a.resident && t.live) copy(0, vecs);  // for the gradient
+            if ((tid & 31) == 0) arrive(&s.t_empty[n & 1]);
+            if (live) copy(n == 0 ? early : 0, vecs);
+            if (kGrad && !a.resident && live) copy(0, vecs);  // for the gradient
         }
         // every copy has landed before the CTA may end
         if (!ok) s.err = 1;
@@ -805,6 +804,17 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(DistillArgs a) {
             if (!mbar_wait(&s.full[last.slot], last.phase)) s.err = 1;
         }
         __syncwarp();
+    } else if (warp == kWarps + 1) {
+        uint32_t n = 0;
+        for (uint32_t row = cluster; row < a.rows; row += clusters, ++n) {
+            if (n >= 2) wait(&s.t_empty[n & 1], (n >> 1) + 1 & 1, &s.err);
+            const Teacher t = read_teacher(a, row);
+            if ((tid & 31) == 0) {
+                s.teacher[n & 1] = t;
+                arrive(&s.t_full[n & 1]);
+            }
+            __syncwarp();
+        }
     } else {
         Worker<T, kGrad> w{a, s, ring, bitmaps, words, rank, tid, tid & 31, warp};
         w.run(cluster, clusters);
