@@ -169,10 +169,13 @@ __device__ __forceinline__ void Vec<T>::set(uint32_t j, Pair p) {
 template <typename T>
 __device__ __forceinline__ void Vec<T>::mask(uint32_t bits) {
 #pragma unroll
-    for (uint32_t j = 0; j < kN; ++j) {
-        if (bits >> j & 1) {
-            if constexpr (kN == 4) w[j] = NegInf<T>::kWord;
-            else w[j / 2] = j % 2 ? (w[j / 2] & 0xFFFFu) | (NegInf<T>::kWord & 0xFFFF0000u) : (w[j / 2] & 0xFFFF0000u) | (NegInf<T>::kWord & 0xFFFFu);
+    for (uint32_t j = 0; j < 4; ++j) {
+        if constexpr (kN == 4) {
+            if (bits >> j & 1) w[j] = NegInf<T>::kWord;
+        } else {
+            // bits 2 j and 2 j + 1 to the halves of a mask
+            const uint32_t m = (bits >> (2 * j) & 1) * 0xFFFFu | (bits >> (2 * j + 1) & 1) * 0xFFFF0000u;
+            w[j] = (w[j] & ~m) | (NegInf<T>::kWord & m);
         }
     }
 }
@@ -402,7 +405,8 @@ struct Summer {
         }
         if (any) {
 #pragma unroll
-            for (uint32_t u = 0; u < kB; ++u) q[u].mask(listed[u]);
+            for (uint32_t u = 0; u < kB; ++u)
+                if (listed[u]) q[u].mask(listed[u]);
         }
         const float n = fmaxf(m, ceilf(batch_top(q) * kf));
         sum *= pow2(m - n);
