@@ -839,11 +839,12 @@ struct Layout {
 };
 
 // CTAs a row: what takes least by a model of the rounds of resident clusters. A CTA
-// takes 2.1 us a row and 1 us for 23 KB; shares that do not fit the ring cross it
+// takes 4 us a row and 1 us for 28 KB; shares that do not fit the ring cross it
 // twice, the second time out of L2 (as 0.2 of a read from memory), unless the rows
-// on the device at a time are too many for it. 4,096 rows of 151,936 bf16, CTAs a
-// row 1 / 2 / 3 / 4 (with 4 a share fits): 526 / 446 / 505 / 484 us; one and three
-// CTAs an SM instead of two were slower at each.
+// on the device at a time are too many for it; over several rounds clusters of odd sizes
+// take about 1.3 times as long. Measured, 1 / 2 / 3 / 4 / 6 CTAs a row: 4,096 rows of
+// 151,936 bf16 (with 4 a share fits) 544 / 430 / 583 / 492 / 622 us; 777 of 93,001 f16
+// 71 / 77 / 98 / 95 / 115; 49 of 248,320 f32 52 / 35 / 29 / 26 / 30, and 23.4 with 5.
 template <typename T, bool kGrad>
 bool layout_for(uint32_t rows, uint32_t V, Layout& best) {
     struct Table {
@@ -884,7 +885,8 @@ bool layout_for(uint32_t rows, uint32_t V, Layout& best) {
         const bool resident = kGrad && ceil_div(share, kChunkVecs) <= slots;
         const bool in_l2 = static_cast<double>(t.clusters[c]) * V * sizeof(T) <= 64e6;
         const double moved = share * 16.0 * (!kGrad ? 1.0 : resident ? 2.0 : in_l2 ? 2.2 : 3.0);
-        const double us = ceil_div(rows, static_cast<uint64_t>(t.clusters[c])) * (2.1 + moved / 23.1e3);
+        const uint32_t rounds = ceil_div(rows, static_cast<uint64_t>(t.clusters[c]));
+        const double us = rounds * (4.0 + moved / 28e3) * (rounds > 1 && c > 1 && c % 2 == 1 ? 1.3 : 1.0);
         if (us < least) {
             least = us;
             best = {c, share, slots, static_cast<uint32_t>(t.clusters[c]), resident};
