@@ -26,11 +26,10 @@
 // bounded; one that runs out makes the CTA's rows NaN.
 //
 // What bounds it: large batches the row's bytes, and the second copy through L2 (4,096
-// x 151,936 bf16, lists of 64: 442-447 us, 5.6 TB/s, issue slots 51 percent busy with about
-// 11 instructions an entry and pass pair); a few hundred rows the last round of clusters
-// (512 x 202,048 bf16, loss alone: 44; 777 x 93,001 f16, lists of 200: 77); few rows the
-// chain from the list to the last store (49 x 248,320 f32: 21 on the GPU, 7 x 151,936, loss
-// alone: 7).
+// x 151,936 bf16, lists of 64: 430 us, 5.8 TB/s, 51 percent of the issue slots); a few
+// hundred rows the last round of clusters (512 x 202,048 bf16, loss alone: 42; 777 x
+// 93,001 f16, lists of 200: 71); few rows the chain from the list to the last store (49 x
+// 248,320 f32: 23; 7 x 151,936, loss alone: 7 on the GPU, 12 with the host's call).
 #include <algorithm>
 #include <type_traits>
 
