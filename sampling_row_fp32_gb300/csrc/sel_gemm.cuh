@@ -9,6 +9,7 @@
 // gives it: 256 rows (128 a CTA) and up to 256 columns. Warp roles:
 //   warp 0      copies both operands, 64 k a stage, into a ring (TMA, swizzled)
 //   warp 1      issues the products (the pair's first CTA for both)
+//   warps 2, 3  what else P has to do
 //   warps 4-11  read a tile's D from tensor memory, 32 rows and about half of the
 //               columns a warp, and run P's epilogue; D is double-buffered, so that the
 //               products of the next tile run meanwhile
@@ -192,6 +193,7 @@ __device__ __forceinline__ void store_chunk(const EpiWarp& w, const CUtensorMap*
 //                                      registers (0: all of them in tensor memory)
 //   uint32_t* error                    the workspace's error word
 //   Cursor(p, worker, workers)         a worker's tiles: `count` of them, tile(j)
+//   aside(warp, warps)                 what two warps a CTA do meanwhile
 //   epilogue(cursor, tile, w, arrive, load)  arrive(): waits for the sums; then load(c, v): the
 //                                      warp's columns 32 c .., for c = 0 .. chunks - 1 in
 //                                      order, each once
@@ -319,6 +321,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
         // no product is in flight when the tensor memory is given back
         if (leader) gemm_commit_here(&c.drain);
         if (!mbar_wait(&c.drain, 0)) c.err = 1;
+        __syncwarp();
+    } else if (warp == 2 || warp == 3) {
+        p.aside(2 * blockIdx.x + warp - 2, 2 * gridDim.x);
         __syncwarp();
     } else if (warp >= 4) {
         const uint32_t quarter = warp & 3, half = (warp - 4) >> 2;

@@ -124,6 +124,7 @@ struct LossProblem {
     Raster raster;
 
     using Cursor = RasterCursor<LossProblem>;
+    __device__ __forceinline__ void aside(uint32_t, uint32_t) const {}
     __device__ __forceinline__ GemmTile tile(uint32_t m, uint32_t n) const {
         return {&x, &w, m * kTileM, n * kTileN, 0, 0, steps, kTileN, false, false};
     }
@@ -205,6 +206,7 @@ struct LossColumnsProblem {
     uint32_t* error;
     uint32_t rows, V, steps, n, row_tiles, v_tiles;
 
+    __device__ __forceinline__ void aside(uint32_t, uint32_t) const {}
     // A worker stays with its row tile and keeps that one's sums from tile to tile;
     // neighbours take the same ids with the other row tiles.
     struct Cursor {
@@ -399,6 +401,85 @@ constexpr float kProbShift = 0.0f;
 template <>
 constexpr float kProbShift<__half> = 14.0f;
 
+// The row of the i-th vector of all rows.
+__device__ __forceinline__ uint32_t row_of(uint64_t i, const Div& by) {
+    return i < (1ull << 31) ? by(static_cast<uint32_t>(i)) : static_cast<uint32_t>(i / by.d);
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack2(uint32_t w, float& lo, float& hi) {
+    lo = bits_f32<T>(static_cast<uint16_t>(w));
+    hi = bits_f32<T>(static_cast<uint16_t>(w >> 16));
+}
+
+// What dW needs beside P, done by warps that the launch of P has to spare: hidden rows
+// times the power of two of their gradient over the largest one's (exact, but for
+// entries that become subnormal; rows that do not count are zeros, whatever they
+// hold), the exponent of its sums, and of each 32 ids the first rows that have one of
+// them for a target. (As a launch of its own: 4 us for 64 rows, 36 for 4,096.)
+template <typename T>
+struct Prep {
+    const uint4* x;  // NULL: nothing to do
+    uint4* scaled;
+    const uint32_t* targets;
+    const float* grad;
+    int* exponent;
+    uint32_t* hits;
+    uint32_t rows, V;
+    Div by_vecs;  // vectors of 8 entries a row
+    int shift;    // P's
+
+    __device__ __forceinline__ void run(uint32_t warp, uint32_t warps) const {
+        const uint32_t lane = threadIdx.x & 31;
+        int top = -1000;
+#pragma unroll 4
+        for (uint32_t r = lane; r < rows; r += 32)
+            if (targets[r] < V && grad[r] != 0.0f) top = max(top, GradParts(grad[r]).e);
+        top = __reduce_max_sync(kFull, top);
+        if (warp == 0 && lane == 0) *exponent = max(top, -200) - shift;
+        const uint64_t n = static_cast<uint64_t>(rows) * by_vecs.d;
+        for (uint64_t i = static_cast<uint64_t>(warp) * 32 + lane; i < n; i += static_cast<uint64_t>(warps) * 32) {
+            const uint32_t r = row_of(i, by_vecs);
+            const float g = grad[r];
+            uint4 q = make_uint4(0, 0, 0, 0);
+            if (targets[r] < V && g != 0.0f) {
+                q = x[i];
+                const float f = pow2(static_cast<float>(GradParts(g).e - top));
+                uint32_t* p = &q.x;
+#pragma unroll
+                for (uint32_t k = 0; k < 4; ++k) {
+                    float lo, hi;
+                    unpack2<T>(p[k], lo, hi);
+                    p[k] = pack2<T>(lo * f, hi * f);
+                }
+            }
+            scaled[i] = q;
+        }
+        // a run of groups of 32 ids a warp, one pass over the rows
+        const uint32_t groups = (V + 31) / 32, per = (groups + warps - 1) / warps;
+        const uint32_t v0 = min(groups, warp * per), v1 = min(groups, v0 + per);
+        for (uint32_t v = v0 + lane; v < v1; v += 32) hits[static_cast<uint64_t>(v) * kHitWords] = 0;
+        __syncwarp();
+#pragma unroll 4
+        for (uint32_t r0 = 0; r0 < rows && v0 < v1; r0 += 32) {
+            const uint32_t r = r0 + lane, t = r < rows ? targets[r] : SEL_INVALID_ID;
+            uint32_t mine = __ballot_sync(kFull, t < V && t / 32 >= v0 && t / 32 < v1 && grad[r] != 0.0f);
+            for (; mine; mine &= mine - 1) {  // (few)
+                const uint32_t i = __ffs(mine) - 1, its = __shfl_sync(kFull, t, i);
+                if (lane == 0) {
+                    uint32_t* to = hits + static_cast<uint64_t>(its / 32) * kHitWords;
+                    const uint32_t at = to[0];
+                    if (at < kKeptRows) {
+                        to[0] = at + 1;
+                        to[1 + at] = r0 + i;
+                        to[1 + kKeptRows + at] = its;
+                    }
+                }
+            }
+        }
+    }
+};
+
 // 16 entries, rounded to T, as one 32-byte store: a whole sector a lane.
 template <typename T>
 __device__ __forceinline__ void store16(T* to, const float (&v)[32], uint32_t i) {
@@ -417,6 +498,7 @@ struct ProbProblem {
     using Type = T;
     static constexpr uint32_t kPart = 0;
     CUtensorMap x, w;
+    Prep<T> prep;
     T* p;
     float* lost;  // [rows]: of the targets' entries, by their rounding
     const uint32_t* targets;
@@ -427,6 +509,9 @@ struct ProbProblem {
     Raster raster;
 
     using Cursor = RasterCursor<ProbProblem>;
+    __device__ __forceinline__ void aside(uint32_t warp, uint32_t warps) const {
+        if (prep.x) prep.run(warp, warps);
+    }
     __device__ __forceinline__ GemmTile tile(uint32_t r, uint32_t v) const {
         return {&w, &x, v0 + v * kTileM, r * n, 0, 0, steps, n, false, false};
     }
@@ -526,6 +611,7 @@ struct GradsProblem {
     uint32_t dw_items, dw_steps, extra;         // extra: dW tiles ahead for workers with one dX tile less
     bool add;
 
+    __device__ __forceinline__ void aside(uint32_t, uint32_t) const {}
     struct Cursor {
         const GradsProblem& p;
         uint32_t worker, workers, dx, more, light, ahead, count;
@@ -621,86 +707,7 @@ struct GradsProblem {
     }
 };
 
-struct PrepArgs {
-    const uint4* x;
-    uint4* scaled;  // x times 2^e over the largest gradient's
-    const uint32_t* targets;
-    const float* grad;
-    int* exponent;  // of dW's sums
-    uint32_t* hits;
-    uint32_t rows, V;
-    Div by_vecs;    // vectors of 8 entries a row
-    int shift;      // P's
-};
-
-constexpr uint32_t kPrepThreads = 128;
-
-// The row of the i-th vector of all rows.
-__device__ __forceinline__ uint32_t row_of(uint64_t i, const Div& by) {
-    return i < (1ull << 31) ? by(static_cast<uint32_t>(i)) : static_cast<uint32_t>(i / by.d);
-}
-
-template <typename T>
-__device__ __forceinline__ void unpack2(uint32_t w, float& lo, float& hi) {
-    lo = bits_f32<T>(static_cast<uint16_t>(w));
-    hi = bits_f32<T>(static_cast<uint16_t>(w >> 16));
-}
-
-// dW's second operand: hidden rows times the power of two of their gradient over the
-// largest one's: exact, but for entries that become subnormal. Rows that do not count
-// are zeros, whatever they hold. And of each 32 ids the first rows that have one of
-// them for a target.
-template <typename T>
-__global__ void __launch_bounds__(kPrepThreads) grad_prep_kernel(PrepArgs a) {
-    __shared__ int sh[kPrepThreads / 32];
-    pdl_wait();
-    pdl_trigger();
-    int top = -1000;
-    for (uint32_t r = threadIdx.x; r < a.rows; r += kPrepThreads)
-        if (a.targets[r] < a.V && a.grad[r] != 0.0f) top = max(top, GradParts(a.grad[r]).e);
-    top = __reduce_max_sync(kFull, top);
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = top;
-    __syncthreads();
-#pragma unroll
-    for (uint32_t i = 0; i < kPrepThreads / 32; ++i) top = max(top, sh[i]);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.exponent = max(top, -200) - a.shift;
-    const uint64_t n = static_cast<uint64_t>(a.rows) * a.by_vecs.d;
-    for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * kPrepThreads + threadIdx.x; i < n;
-         i += static_cast<uint64_t>(gridDim.x) * kPrepThreads) {
-        const uint32_t r = row_of(i, a.by_vecs);
-        const float g = a.grad[r];
-        uint4 q = make_uint4(0, 0, 0, 0);
-        if (a.targets[r] < a.V && g != 0.0f) {
-            q = a.x[i];
-            const float f = pow2(static_cast<float>(GradParts(g).e - top));
-            uint32_t* p = &q.x;
-#pragma unroll
-            for (uint32_t k = 0; k < 4; ++k) {
-                float lo, hi;
-                unpack2<T>(p[k], lo, hi);
-                p[k] = pack2<T>(lo * f, hi * f);
-            }
-        }
-        a.scaled[i] = q;
-    }
-    const uint32_t lane = threadIdx.x & 31, warps = gridDim.x * (kPrepThreads / 32);
-    for (uint32_t v = blockIdx.x * (kPrepThreads / 32) + threadIdx.x / 32; v < (a.V + 31) / 32; v += warps) {
-        uint32_t* to = a.hits + static_cast<uint64_t>(v) * kHitWords;
-        uint32_t found = 0;
-#pragma unroll 8
-        for (uint32_t r0 = 0; r0 < a.rows; r0 += 32) {
-            const uint32_t r = r0 + lane, t = r < a.rows ? a.targets[r] : SEL_INVALID_ID;
-            const uint32_t mine = __ballot_sync(kFull, t / 32 == v && t < a.V && a.grad[r] != 0.0f);
-            const uint32_t at = found + __popc(mine & ((1u << lane) - 1));
-            if ((mine >> lane & 1) && at < kKeptRows) {
-                to[1 + at] = r;
-                to[1 + kKeptRows + at] = t;
-            }
-            found += __popc(mine);
-        }
-        if (lane == 0) to[0] = min(found, kKeptRows);
-    }
-}
+constexpr uint32_t kGradThreads = 128;
 
 struct GradFinishArgs {
     const float* acc;
@@ -719,12 +726,12 @@ struct GradFinishArgs {
 // dX from its sums, rounded once. With the error word raised both gradients
 // become NaN.
 template <typename T>
-__global__ void __launch_bounds__(kPrepThreads) grad_finish_kernel(GradFinishArgs a) {
+__global__ void __launch_bounds__(kGradThreads) grad_finish_kernel(GradFinishArgs a) {
     pdl_wait();
     pdl_trigger();
     const uint64_t n = static_cast<uint64_t>(a.rows) * a.by_vecs.d;
-    const uint64_t first = static_cast<uint64_t>(blockIdx.x) * kPrepThreads + threadIdx.x;
-    const uint64_t step = static_cast<uint64_t>(gridDim.x) * kPrepThreads;
+    const uint64_t first = static_cast<uint64_t>(blockIdx.x) * kGradThreads + threadIdx.x;
+    const uint64_t step = static_cast<uint64_t>(gridDim.x) * kGradThreads;
     const bool bad = *a.error != 0;
     const uint32_t nan2 = pack2<T>(NAN, NAN);
     for (uint64_t i = first; a.dx && i < n; i += step) {
@@ -914,17 +921,15 @@ sel_status run_grad(const HeadLossCall& c, const float* lse, const float* grad, 
     auto* hits = reinterpret_cast<uint32_t*>(c.ws + plan.hits);
     const int shift = static_cast<int>(kProbShift<T>);
     const uint32_t vecs = c.H / 8, all = sms / 2;
-    const uint32_t blocks = static_cast<uint32_t>(std::min<uint64_t>(8 * sms, ceil_div(static_cast<uint64_t>(c.rows) * vecs, kPrepThreads)));
-    if (dw) {
-        const PrepArgs a{static_cast<const uint4*>(c.x), static_cast<uint4*>(scaled), c.targets, grad, exponent, hits, c.rows, c.V, Div(vecs), shift};
-        const uint32_t prep = std::max(blocks, std::min(8u * sms, ceil_div(c.V, 32 * (kPrepThreads / 32))));
-        if (launch_pdl(grad_prep_kernel<T>, dim3(prep), dim3(kPrepThreads), 0, c.stream, a) != cudaSuccess) return SEL_ECUDA;
-    }
+    const uint32_t blocks = static_cast<uint32_t>(std::min<uint64_t>(8 * sms, ceil_div(static_cast<uint64_t>(c.rows) * vecs, kGradThreads)));
     for (uint32_t i = 0; i < plan.pieces; ++i) {
         const uint32_t v0 = i * plan.piece, width = std::min(plan.piece, c.V - v0);
         const uint64_t pitch = static_cast<uint64_t>(plan.pitch) * 2;
         ProbProblem<T> p{};
         if (!map16(&p.x, c.x, c.H, c.rows, kStepK, rows.n / 2) || !map16(&p.w, c.w, c.H, c.V, kStepK, kCtaM)) return SEL_ECUDA;
+        if (dw && i == 0)
+            p.prep = {static_cast<const uint4*>(c.x), static_cast<uint4*>(scaled), c.targets, grad, exponent, hits, c.rows,
+                      c.V, Div(vecs), shift};
         p.p = static_cast<T*>(prob);
         p.lost = lost;
         p.targets = c.targets;
@@ -971,7 +976,7 @@ sel_status run_grad(const HeadLossCall& c, const float* lse, const float* grad, 
         if (const sel_status s = launch_gemm(g, workers, c.stream); s != SEL_OK) return s;
     }
     const GradFinishArgs f{acc, lost, static_cast<const uint4*>(c.w), c.targets, grad, error, static_cast<uint4*>(dx), static_cast<uint4*>(dw), c.rows, c.V, plan.slices, Div(vecs), shift};
-    return launch_pdl(grad_finish_kernel<T>, dim3(blocks), dim3(kPrepThreads), 0, c.stream, f) == cudaSuccess ? SEL_OK : SEL_ECUDA;
+    return launch_pdl(grad_finish_kernel<T>, dim3(blocks), dim3(kGradThreads), 0, c.stream, f) == cudaSuccess ? SEL_OK : SEL_ECUDA;
 }
 
 sel_status check_head(const void* x, const void* w, const uint32_t* targets, int dtype, uint32_t rows, uint32_t V, uint32_t H) {

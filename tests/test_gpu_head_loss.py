@@ -103,11 +103,11 @@ def check_grad(x, w, t, lse, grad):
     err = (dx.double() - want_x).abs()
     assert (err <= tol).all(), (err / tol).max()
     assert not dx[~live].any()
-    # hidden rows times grad / max grad, rounded to T once more, unless the ratio is 1
+    # hidden rows times a power of two: exact but for what becomes subnormal
     top = g.max()
-    ratio = torch.where(g == top, 0.0, eps + 2.0 ** -23)
-    u = x64.abs() * (1 + ratio[:, None])
-    du = x64.abs() * ratio[:, None] + torch.where(g == top, 0.0, tiny * (1 + top / g.clamp(min=1e-300)))[:, None] * live[:, None]
+    u = x64.abs()
+    small = torch.where(live & (g < top), tiny * (1 + top / torch.where(live, g, 1.0)), 0.0)  # (dead rows: no 0 * inf)
+    du = small[:, None].expand_as(u)
     ga, gd = a * g[:, None], dp * g[:, None]
     tol = gd.T @ u + ga.T @ du + gd.T @ du
     tol = tol + (rows + 4) * 2.0 ** -23 * ((ga + gd).T @ u)
@@ -386,3 +386,69 @@ def test_target_entries_are_not_rounded(dtype, rows, same):
     for got, want in pairs:
         lean = ((got.double() - want) * want).sum() / want.square().sum()
         assert abs(lean.item()) < 0.25 * half, lean.item() / half
+
+
+@pytest.mark.parametrize("rows", [15, 16, 17, 32, 33, 48, 240, 241, 255, 272, 273, 512, 513, 1024, 1281])
+def test_row_tiles(rows):
+    """Tiles of 16 to 256 hidden rows, and one more than fill them."""
+    x, w, t, grad = make(16, rows, 300, 72, "f16" if rows % 2 else "bf16")
+    _, lse = check_loss(x, w, t)
+    check_grad(x, w, t, lse, grad)
+
+
+@pytest.mark.parametrize("H", [8, 120, 128, 136, 248, 256, 264, 392, 1024, 1032, 2048])
+def test_widths(H):
+    x, w, t, grad = make(17, 70, 600, H, "bf16")
+    _, lse = check_loss(x, w, t)
+    check_grad(x, w, t, lse, grad)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -120, 2.0 ** -60, 2.0 ** 60, 2.0 ** 110])
+def test_gradients_at_the_ends_of_fp32(scale):
+    x, w, t, grad = make(18, 40, 300, 64, "bf16")
+    _, lse = run_loss(x, w, t)
+    check_grad(x, w, t, lse, grad * scale)
+
+
+def test_nonfinite_gradients_reach_what_they_are_part_of():
+    x, w, t, grad = make(19, 40, 300, 64, "bf16", ignored=0.0)
+    _, lse = run_loss(x, w, t)
+    grad[3], grad[30] = NAN, float("inf")
+    dx, dw = run_grad(x, w, t, lse, grad)
+    bad = ~torch.isfinite(dx).all(dim=1)
+    assert bad.nonzero()[:, 0].tolist() == [3, 30] and not torch.isfinite(dw).any()
+    t[3] = t[30] = -1  # ignored, they are nobody's
+    dx, dw = run_grad(x, w, t, lse, grad)
+    assert torch.isfinite(dx).all() and torch.isfinite(dw).all()
+
+
+def test_many_pieces_and_a_narrow_last_one():
+    """62 pieces of the vocabulary, the last of 576 ids, where dX's sums are split in two
+    and the second part has nothing of it."""
+    rows, V, H = 16_400, 1_000_000, 64
+    g = torch.Generator(device="cuda").manual_seed(20)
+    w = (torch.randn(V, H, generator=g, device="cuda") / 4).bfloat16()
+    x = torch.randn(rows, H, generator=g, device="cuda").bfloat16()
+    t = torch.randint(0, V, (rows,), generator=g, device="cuda").int()
+    t[::5] = V - 1 - t[::5] % 500  # some in the last piece
+    grad = torch.full((rows,), 0.5, device="cuda")
+    loss, lse = run_loss(x, w, t)
+    dx, dw = run_grad(x, w, t, lse, grad)
+    x64, want_x, total = x.double(), torch.zeros(rows, H, device="cuda", dtype=torch.float64), None
+    for lo in range(0, V, 50_000):
+        part = w[lo:lo + 50_000].double()
+        z = x64 @ part.T
+        total = torch.logsumexp(z, 1) if total is None else torch.logaddexp(total, torch.logsumexp(z, 1))
+        p = torch.exp(z - lse.double()[:, None])
+        here = ((t >= lo) & (t < lo + 50_000)).nonzero()[:, 0]
+        p[here, t[here].long() - lo] -= 1.0
+        p *= 0.5
+        want_x += p @ part
+        want = p.T @ x64
+        got = dw[lo:lo + 50_000].double()
+        # two roundings of 2^-9 in the mean square at most, the sums' far below
+        assert (got - want).norm() < 2.0 ** -8 * want.norm(), lo
+        if lo + 50_000 >= V:
+            assert (got[-576:] - want[-576:]).norm() < 2.0 ** -8 * want[-576:].norm()
+    assert (lse.double() - total).abs().max() < 1e-4
+    assert (dx.double() - want_x).norm() < 2.0 ** -8 * want_x.norm()
