@@ -20,7 +20,7 @@
 // and 96.5 percent of their cycles in the three products; 4,096 x 151,936 in 2.43 ms
 // alone and 2.79 back to back, where the card's power limits it; the gradient of 2,048 x
 // 151,936 in 3.9 and 4.5). Between them padding counts: 777 rows of 2,880 x 93,001 take
-// 282 us (1.48 PFLOP/s) and 840. The gradient of 64 rows of 1,024 x 151,936 takes 208, 52
+// 264 us (1.58 PFLOP/s) and 820. The gradient of 64 rows of 1,024 x 151,936 takes 206, 54
 // for P and 130 for the rest: the matrix is read twice.
 #include <algorithm>
 
@@ -171,8 +171,8 @@ struct LossProblem {
 };
 
 // Hidden rows on the product's columns, so that a tile has as few as 16 of them (one row
-// of 1,024 x 151,936: 71 us on rows, 54 here; 777: 335 and 272): a lane has one id, and
-// the logits of half a tile's rows for it. About 8 more instructions a logit for the
+// of 1,024 x 151,936: 71 us on rows, 50 here; 777: 335 and 264): a lane has one id, and
+// the logits of half a tile's rows for it. About 4 more instructions a logit for the
 // sums across the lanes, which the product of one more row tile outweighs.
 
 // Of 32 rows' values in each lane, the sums over the lanes: lane i gets row i's.
@@ -226,15 +226,27 @@ struct LossColumnsProblem {
     __device__ __forceinline__ void epilogue(const Cursor& cursor, const GemmTile& t, EpiWarp& w, Arrive arrived, Load load) const {
         const uint32_t id = t.am + w.row, first = t.bn + w.col;
         auto* sums = reinterpret_cast<Part*>(w.smem) + w.lane;
+        auto* wanted = reinterpret_cast<uint32_t*>(w.smem + 1024) + w.lane;  // targets of the rows, which stay
+        if (w.j == 0) {
+            for (uint32_t c = 0; c < w.chunks; ++c) {
+                const uint32_t row = first + 32 * c + w.lane;
+                wanted[32 * c] = 32 * c + w.lane < w.cols && row < rows ? targets[row] : SEL_INVALID_ID;
+            }
+        }
         arrived();
 #pragma unroll
         for (uint32_t c = 0; c < 4; ++c) {
             if (c >= w.chunks) break;
             const uint32_t row = first + 32 * c + w.lane;  // whose result this lane will have
             const bool mine = 32 * c + w.lane < w.cols && row < rows;
-            const uint32_t target = mine ? targets[row] : SEL_INVALID_ID;
+            const uint32_t target = wanted[32 * c];
             float v[32];
             load(c, v);
+            if (32 * c + 32 > w.cols) {  // (what lies beyond the tile)
+#pragma unroll
+                for (uint32_t i = 1; i < 32; ++i)
+                    if (32 * c + i >= w.cols) v[i] = v[0];
+            }
             if (id >= V) {
 #pragma unroll
                 for (uint32_t i = 0; i < 32; ++i) v[i] = -INFINITY;
@@ -255,12 +267,29 @@ struct LossColumnsProblem {
                     }
                 }
             }
-            float m = -INFINITY;
+            // One reference for all 32 rows, if no row's largest can lie far below it: the
+            // smallest of a lane's logits bounds every row's largest from below, and the
+            // largest such bound of all lanes is near where the rows are alike. Else a
+            // reference a row (777 rows: 282 us, 265 with one for all).
+            float m = v[0], least = v[0];
 #pragma unroll
-            for (uint32_t i = 0; i < 32; ++i) {
-                const float top = ceilf(max_across(v[i]) * kLog2E);
-                v[i] = Weights(top)(v[i]);
-                if (w.lane == i) m = top;
+            for (uint32_t i = 1; i < 31; i += 2) {
+                m = max3f(m, v[i], v[i + 1]);
+                least = fminf(least, fminf(v[i], v[i + 1]));
+            }
+            m = ceilf(max_across(fmaxf(m, v[31])) * kLog2E);
+            least = max_across(fminf(least, v[31])) * kLog2E;
+            if (m - least < 60.0f) {
+                const Weights e(m);
+#pragma unroll
+                for (uint32_t i = 0; i < 32; ++i) v[i] = e(v[i]);
+            } else {
+#pragma unroll
+                for (uint32_t i = 0; i < 32; ++i) {
+                    const float top = ceilf(max_across(v[i]) * kLog2E);
+                    v[i] = Weights(top)(v[i]);
+                    if (w.lane == i) m = top;
+                }
             }
             Part p{m, sum_across(v)};
             if (w.j > 0) {

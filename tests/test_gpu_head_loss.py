@@ -452,3 +452,15 @@ def test_many_pieces_and_a_narrow_last_one():
             assert (got[-576:] - want[-576:]).norm() < 2.0 ** -8 * want[-576:].norm()
     assert (lse.double() - total).abs().max() < 1e-4
     assert (dx.double() - want_x).norm() < 2.0 ** -8 * want_x.norm()
+
+
+@pytest.mark.parametrize("rows", [7, 40, 300])
+@pytest.mark.parametrize("apart", [20.0, 100.0, 1000.0])
+def test_rows_far_apart(rows, apart):
+    """Logits of neighbouring rows that lie far above and below each other: a row's sum
+    does not vanish under another's reference."""
+    x, w, t, grad = make(21, rows, 700, 64, "bf16")
+    w[:, 0] = 1.0
+    x[:, 0] = (torch.arange(rows, device="cuda") % 5 - 2).to(x.dtype) * apart
+    _, lse = check_loss(x, w, t)
+    check_grad(x, w, t, lse, grad)
