@@ -20,7 +20,7 @@
 // and 96.5 percent of their cycles in the three products; 4,096 x 151,936 in 2.43 ms
 // alone and 2.79 back to back, where the card's power limits it; the gradient of 2,048 x
 // 151,936 in 3.9 and 4.5). Between them padding counts: 777 rows of 2,880 x 93,001 take
-// 264 us (1.58 PFLOP/s) and 820. The gradient of 64 rows of 1,024 x 151,936 takes 206, 54
+// 264 us (1.58 PFLOP/s) and 820. The gradient of 64 rows of 1,024 x 151,936 takes 204, 54
 // for P and 130 for the rest: the matrix is read twice.
 #include <algorithm>
 
@@ -753,29 +753,50 @@ struct GradFinishArgs {
 };
 
 // dX from its sums, rounded once. With the error word raised both gradients
-// become NaN.
-template <typename T>
+// become NaN. kSplit: a block takes 32 vectors, each of its warps every fourth of their
+// slices (one thread for all 19 slices of 64 rows took 9 us, of 206).
+template <typename T, bool kSplit>
 __global__ void __launch_bounds__(kGradThreads) grad_finish_kernel(GradFinishArgs a) {
+    constexpr uint32_t kParts = kSplit ? kGradThreads / 32 : 1, kVecs = kGradThreads / kParts;
+    __shared__ float4 sh[kSplit ? kGradThreads : 1][2];
     pdl_wait();
     pdl_trigger();
     const uint64_t n = static_cast<uint64_t>(a.rows) * a.by_vecs.d;
-    const uint64_t first = static_cast<uint64_t>(blockIdx.x) * kGradThreads + threadIdx.x;
-    const uint64_t step = static_cast<uint64_t>(gridDim.x) * kGradThreads;
+    const uint32_t part = threadIdx.x / kVecs, at = threadIdx.x % kVecs;
     const bool bad = *a.error != 0;
     const uint32_t nan2 = pack2<T>(NAN, NAN);
-    for (uint64_t i = first; a.dx && i < n; i += step) {
-        const uint32_t r = row_of(i, a.by_vecs);
-        const float g = a.grad[r];
-        uint4 q = make_uint4(0, 0, 0, 0);
-        if (a.targets[r] < a.V && g != 0.0f) {
-            float s[8] = {};
-#pragma unroll 10
-            for (uint32_t k = 0; k < a.slices; ++k) {
+    for (uint64_t i0 = static_cast<uint64_t>(blockIdx.x) * kVecs; a.dx && i0 < n; i0 += static_cast<uint64_t>(gridDim.x) * kVecs) {
+        const uint64_t i = i0 + at;
+        const uint32_t r = i < n ? row_of(i, a.by_vecs) : 0;
+        const float g = i < n ? a.grad[r] : 0.0f;
+        const bool live = i < n && a.targets[r] < a.V && g != 0.0f;
+        float s[8] = {};
+        if (live) {
+#pragma unroll 5
+            for (uint32_t k = part; k < a.slices; k += kParts) {
                 const float4* p = reinterpret_cast<const float4*>(a.acc) + 2 * (k * n + i);
                 const float4 u = p[0], v = p[1];
                 s[0] += u.x, s[1] += u.y, s[2] += u.z, s[3] += u.w;
                 s[4] += v.x, s[5] += v.y, s[6] += v.z, s[7] += v.w;
             }
+        }
+        if constexpr (kSplit) {
+            sh[threadIdx.x][0] = make_float4(s[0], s[1], s[2], s[3]);
+            sh[threadIdx.x][1] = make_float4(s[4], s[5], s[6], s[7]);
+            __syncthreads();
+            if (part == 0) {
+#pragma unroll
+                for (uint32_t k = 1; k < kParts; ++k) {
+                    const float4 u = sh[k * kVecs + at][0], v = sh[k * kVecs + at][1];
+                    s[0] += u.x, s[1] += u.y, s[2] += u.z, s[3] += u.w;
+                    s[4] += v.x, s[5] += v.y, s[6] += v.z, s[7] += v.w;
+                }
+            }
+            __syncthreads();
+        }
+        if (part > 0 || i >= n) continue;
+        uint4 q = make_uint4(0, 0, 0, 0);
+        if (live) {
             const float f = a.lost[r];
             const uint4 of = a.w[static_cast<uint64_t>(a.targets[r]) * a.by_vecs.d + (i - static_cast<uint64_t>(r) * a.by_vecs.d)];
             const uint32_t u[4] = {of.x, of.y, of.z, of.w};
@@ -795,7 +816,8 @@ __global__ void __launch_bounds__(kGradThreads) grad_finish_kernel(GradFinishArg
         a.dx[i] = q;
     }
     if (bad && a.dw) {
-        for (uint64_t i = first; i < static_cast<uint64_t>(a.V) * a.by_vecs.d; i += step)
+        for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * kGradThreads + threadIdx.x;
+             i < static_cast<uint64_t>(a.V) * a.by_vecs.d; i += static_cast<uint64_t>(gridDim.x) * kGradThreads)
             a.dw[i] = make_uint4(nan2, nan2, nan2, nan2);
     }
 }
@@ -950,7 +972,6 @@ sel_status run_grad(const HeadLossCall& c, const float* lse, const float* grad, 
     auto* hits = reinterpret_cast<uint32_t*>(c.ws + plan.hits);
     const int shift = static_cast<int>(kProbShift<T>);
     const uint32_t vecs = c.H / 8, all = sms / 2;
-    const uint32_t blocks = static_cast<uint32_t>(std::min<uint64_t>(8 * sms, ceil_div(static_cast<uint64_t>(c.rows) * vecs, kGradThreads)));
     for (uint32_t i = 0; i < plan.pieces; ++i) {
         const uint32_t v0 = i * plan.piece, width = std::min(plan.piece, c.V - v0);
         const uint64_t pitch = static_cast<uint64_t>(plan.pitch) * 2;
@@ -1005,7 +1026,12 @@ sel_status run_grad(const HeadLossCall& c, const float* lse, const float* grad, 
         if (const sel_status s = launch_gemm(g, workers, c.stream); s != SEL_OK) return s;
     }
     const GradFinishArgs f{acc, lost, static_cast<const uint4*>(c.w), c.targets, grad, error, static_cast<uint4*>(dx), static_cast<uint4*>(dw), c.rows, c.V, plan.slices, Div(vecs), shift};
-    return launch_pdl(grad_finish_kernel<T>, dim3(blocks), dim3(kGradThreads), 0, c.stream, f) == cudaSuccess ? SEL_OK : SEL_ECUDA;
+    const bool split = plan.slices >= 4;
+    const uint64_t vectors = static_cast<uint64_t>(c.rows) * vecs;
+    const dim3 blocks(static_cast<uint32_t>(std::min<uint64_t>(8 * sms, ceil_div(vectors, split ? 32 : kGradThreads))));
+    const cudaError_t e = split ? launch_pdl(grad_finish_kernel<T, true>, blocks, dim3(kGradThreads), 0, c.stream, f)
+                                : launch_pdl(grad_finish_kernel<T, false>, blocks, dim3(kGradThreads), 0, c.stream, f);
+    return e == cudaSuccess ? SEL_OK : SEL_ECUDA;
 }
 
 sel_status check_head(const void* x, const void* w, const uint32_t* targets, int dtype, uint32_t rows, uint32_t V, uint32_t H) {
