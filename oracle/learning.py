@@ -80,9 +80,12 @@ def distill(x, vals, ids, teacher_lse, temperature, grad=None):
             d = m * q[r]
             d[i] -= p
             if left > 0:
-                s = q[r, ~listed].sum()
-                loss[r] += left * torch.log(left / s)
-                d[~listed] = (m - left / s) * q[r, ~listed] if s > 0 else 0.0
+                # in logarithms, and each id's share of s from the logits: s may lie below
+                # every 64-bit number
+                ln_s = torch.logsumexp(lq[r, ~listed], dim=0)
+                loss[r] += left * (torch.log(left) - ln_s)
+                share = torch.softmax(x[r, ~listed].double() / T, dim=0)
+                d[~listed] = d[~listed] - left * share if ln_s > -INF else 0.0
             out[r] = g / T * d
         if grad is not None and g == 0:
             out[r] = 0.0

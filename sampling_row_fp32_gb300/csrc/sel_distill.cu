@@ -20,10 +20,12 @@
 //              with the row's other CTAs, and write the gradient from the same
 //              chunks, then the listed ids' entries
 // The bitmap leaves listed ids out of the unlisted sum instead of subtracting them:
-// lists hold nearly all of a peaked row, and 1 - sum q_i would be rounding. Sums
-// meet as messages between the warps of the cluster (st.async), joined in one
-// order; no barrier of the cluster stands between a row and the next. Every wait is
-// bounded; one that runs out makes the CTA's rows NaN.
+// lists hold nearly all of a peaked row, and 1 - sum q_i would be rounding. The two
+// sums have a reference each: under one for both, s was 0 where the unlisted ids lie
+// 87 nats below the listed ones, though ln s and their shares of s are ordinary
+// numbers. Sums meet as messages between the warps of the cluster (st.async), joined
+// in one order; no barrier of the cluster stands between a row and the next. Every
+// wait is bounded; one that runs out makes the CTA's rows NaN.
 //
 // What bounds it: large batches the row's bytes, and the second copy through L2 (4,096
 // x 151,936 bf16, lists of 64: 430 us, 5.8 TB/s, 51 percent of the issue slots); a few
@@ -69,11 +71,11 @@ struct DistillArgs {
     float inv_t;
 };
 
-// Sums of 2^(x kf - m), m a whole number of at least -kHuge, so that sums meet by
-// exact shifts; apart for unlisted and listed ids. (x kf is not rounded before m
-// is subtracted.)
+// Sums of 2^(x kf - m) for unlisted and for listed ids, each under an m of its own, a
+// whole number of at least -kHuge, so that sums meet by exact shifts. (x kf is not
+// rounded before m is subtracted.)
 struct Sums {
-    float m, rest, list;
+    float rest_m, rest, list_m, list;
 };
 
 // 2^n for a whole n <= 0; 0 below the normal numbers (and for NaN).
@@ -98,8 +100,8 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 __device__ __forceinline__ Sums warp_join(const Sums& s) {
-    const float m = warp_max(s.m), f = pow2(s.m - m);
-    return {m, warp_sum(s.rest * f), warp_sum(s.list * f)};
+    const float m = warp_max(s.rest_m), n = warp_max(s.list_m);
+    return {m, warp_sum(s.rest * pow2(s.rest_m - m)), n, warp_sum(s.list * pow2(s.list_m - n))};
 }
 
 // Two floats side by side, for the instructions that take pairs.
@@ -124,6 +126,9 @@ __device__ __forceinline__ Pair mul2(Pair a, Pair b) {
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
     return r;
 }
+
+// What logits are taken relative to, under a largest of `m`: 0 where all are -Inf.
+__device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.0f : m; }
 
 // 16 bytes of a row: kN logits, taken as four pairs of two (f32: two pairs).
 template <typename T>
@@ -290,9 +295,10 @@ __device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
     return r;
 }
 // Stores into a CTA of the cluster, counted on a barrier there.
-__device__ __forceinline__ void send(uint32_t to, uint32_t bar, float a, float b, float c) {
+__device__ __forceinline__ void send(uint32_t to, uint32_t bar, const Sums& s) {
     asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
-                 "r"(__float_as_uint(a)), "r"(__float_as_uint(b)), "r"(__float_as_uint(c)), "r"(0u), "r"(bar)
+                 "r"(__float_as_uint(s.rest_m)), "r"(__float_as_uint(s.rest)), "r"(__float_as_uint(s.list_m)),
+                 "r"(__float_as_uint(s.list)), "r"(bar)
                  : "memory");
 }
 __device__ __forceinline__ void send(uint32_t to, uint32_t bar, float a) {
@@ -487,14 +493,14 @@ struct Worker {
         const uint32_t p = messages & 1;
         if (tid == 0) expect_tx(&s.sums[p], a.C * kWarps * 16);
         z = warp_join(z);
-        if (lane < a.C) send(peer_addr(&s.table[p][rank * kWarps + warp], lane), peer_addr(&s.sums[p], lane), z.m, z.rest, z.list);
+        if (lane < a.C) send(peer_addr(&s.table[p][rank * kWarps + warp], lane), peer_addr(&s.sums[p], lane), z);
         wait_cluster(&s.sums[p], messages >> 1 & 1, &s.err);
         ++messages;
-        z = {-INFINITY, 0.0f, 0.0f};
+        z = {-INFINITY, 0.0f, -INFINITY, 0.0f};
         for (uint32_t i = lane; i < a.C * kWarps; i += 32) {
             const float4 o = s.table[p][i];
-            const float m = fmaxf(z.m, o.x), f = pow2(z.m - m), g = pow2(o.x - m);
-            z = {m, z.rest * f + o.y * g, z.list * f + o.z * g};
+            const float m = fmaxf(z.rest_m, o.x), n = fmaxf(z.list_m, o.z);
+            z = {m, z.rest * pow2(z.rest_m - m) + o.y * pow2(o.x - m), n, z.list * pow2(z.list_m - n) + o.w * pow2(o.z - n)};
         }
         return warp_join(z);
     }
@@ -549,27 +555,35 @@ struct Worker {
             release();
         }
     }
-    // The row's largest logit and the sums of 2^((x - it) kf), for rows whose logits
-    // are too large, or all too small, for whole-number references.
+    // The largest unlisted and listed logits and the sums of 2^((x - it) kf), for rows
+    // whose logits are too large, or too small, for whole-number references.
     __device__ __forceinline__ Sums slow_sums(const Share<T>& x, const uint32_t* bits, bool twice) {
         const int64_t lo = max(x.base, static_cast<int64_t>(0)), hi = min(x.base + x.span, static_cast<int64_t>(a.V));
-        float m = -INFINITY;
-        for (int64_t i = lo + tid; i < hi; i += kNT) m = fmaxf(m, to_f32(x.row[i]));
-        m = exchange(Sums{m, 0.0f, 0.0f}).m;
-        float rest = twice ? NAN : 0.0f, list = 0.0f;
-        for (int64_t i = lo + tid; i < hi; i += kNT) {
+        auto listed = [&](int64_t i) {
             const uint32_t off = static_cast<uint32_t>(i - x.base);
-            const float e = ex2_approx((to_f32(x.row[i]) - m) * a.kf);  // (NaN where the row's largest is infinite)
-            if (bits[off >> 5] >> (off & 31) & 1) list += e;
-            else rest += e;
+            return (bits[off >> 5] >> (off & 31) & 1) != 0;
+        };
+        Sums z{-INFINITY, 0.0f, -INFINITY, 0.0f};
+        for (int64_t i = lo + tid; i < hi; i += kNT) {
+            float& m = listed(i) ? z.list_m : z.rest_m;
+            m = fmaxf(m, to_f32(x.row[i]));
         }
-        return exchange(Sums{m, rest, list});
+        z = exchange(z);
+        const float rest_ref = reference(z.rest_m), list_ref = reference(z.list_m);
+        z.rest = twice ? NAN : 0.0f;
+        z.list = 0.0f;
+        for (int64_t i = lo + tid; i < hi; i += kNT) {
+            const bool of = listed(i);
+            const float e = ex2_approx((to_f32(x.row[i]) - (of ? list_ref : rest_ref)) * a.kf);  // (NaN where a largest is +Inf)
+            (of ? z.list : z.rest) += e;
+        }
+        return exchange(z);
     }
 
     __device__ __forceinline__ void run(uint32_t first_row, uint32_t step) {
         // of the row before: what its loss still needs, and listed entries to write
         uint32_t pending = 0, pending_row = 0, lives = 0;
-        float p_left = 0.0f, p_logs = 0.0f, p_mass = 0.0f;
+        float p_rest = 0.0f, p_mass = 0.0f;
         T* p_out = nullptr;
         uint32_t id[kEntries];
         float grads[kEntries];
@@ -581,8 +595,7 @@ struct Worker {
             float loss = 0.0f;
             for (uint32_t i = lane; i < a.C * kWarps; i += 32) loss += s.losses[p][i];
             loss = warp_sum(loss);
-            loss *= kLn2;
-            if (p_left != 0.0f) loss += p_left * p_logs;
+            loss = fmaf(loss, kLn2, p_rest);
             if (lane == 0) a.loss[pending_row] = p_mass == p_mass && !s.err ? loss : NAN;
         };
         auto scatter = [&] {
@@ -664,24 +677,30 @@ struct Worker {
                 const uint32_t off = static_cast<uint32_t>(single - x.base);
                 if (!(bits[off >> 5] >> (off & 31) & 1)) mine.add_one(alone);
             }
-            Sums z{mine.m, mine.sum, 0.0f};
+            Sums z{mine.m, mine.sum, -kHuge, 0.0f};
 #pragma unroll
             for (uint32_t e = 0; e < kEntries; ++e) {
                 if (new_id[e] == SEL_INVALID_ID) continue;
-                const float m = fmaxf(z.m, ceilf(logit[e] * a.kf)), f = pow2(z.m - m);
-                z = {m, z.rest * f, z.list * f + ex2_approx(fmaf(logit[e], a.kf, -m))};
+                const float m = fmaxf(z.list_m, ceilf(logit[e] * a.kf));
+                z.list = z.list * pow2(z.list_m - m) + ex2_approx(fmaf(logit[e], a.kf, -m));
+                z.list_m = m;
             }
             if (twice) z.rest = NAN;
             z = exchange(z);
             // (the same in every warp of the cluster)
-            const bool slow = !(fabsf(z.m) < kHuge);
+            // (slow too where r > 0 is shared out among unlisted ids that lie below -kHuge)
+            const bool slow = !(fabsf(fmaxf(z.rest_m, z.list_m)) < kHuge) || (t.left != 0.0f && z.rest == 0.0f);
             if (slow) z = slow_sums(x, bits, twice);
             if (s.err) z.rest = NAN;
-            const float total = z.rest + z.list;
+            const float top = fmaxf(z.rest_m, z.list_m), rest_ref = reference(z.rest_m);
+            auto under = [&](float m) { return slow ? ex2_approx((m - top) * a.kf) : pow2(m - top); };
+            const float rest_up = under(z.rest_m);  // a unit of the unlisted sum in the row's
+            float total = z.rest * rest_up + z.list * under(z.list_m);
+            if (!(total > 0.0f)) total = NAN;  // (every id at -Inf)
             const Log2 log_z(total);
-            auto exponent = [&](float v) { return slow ? (v - z.m) * a.kf : fmaf(v, a.kf, -z.m); };
+            auto exponent = [&](float v, float ref) { return slow ? (v - ref) * a.kf : fmaf(v, a.kf, -ref); };
             auto log_q = [&](float v) {
-                return (slow ? fmaf(v - z.m, a.kf, -log_z.whole) : fmaf(v, a.kf, -(z.m + log_z.whole))) - log_z.part;
+                return (slow ? fmaf(v - top, a.kf, -log_z.whole) : fmaf(v, a.kf, -(top + log_z.whole))) - log_z.part;
             };
             log_p.top = t.top;
             if (!log_p.given) {
@@ -700,7 +719,7 @@ struct Worker {
                 if (id[e] == SEL_INVALID_ID) continue;
                 const float lp = log_p(val[e]), p = exp2f(lp);
                 if (p != 0.0f) part += p * (lp - log_q(logit[e]));
-                grads[e] = g * (t.mass * (ex2_approx(exponent(logit[e])) / total) - p);
+                grads[e] = g * (t.mass * (ex2_approx(exponent(logit[e], top)) / total) - p);
                 if (kGrad && grad == 0.0f) id[e] = SEL_INVALID_ID;
             }
             if (a.loss) {
@@ -712,25 +731,35 @@ struct Worker {
             if constexpr (kGrad) {
                 p_out = out;
                 if (a.resident) at = begin;
+                // Unlisted ids: m q_j - r q_j / s is their weight in the unlisted sum times this
+                // (left without r, q_j's own factor, one rounding less)
+                float f = g * t.mass * (rest_up / total);
+                if (t.left != 0.0f) f = z.rest != 0.0f ? g * (t.mass * (z.rest * rest_up / total) - t.left) / z.rest : 0.0f * total;
                 if (grad == 0.0f || slow) {
                     skip(chunks);
                     if (slow && grad != 0.0f) {
-                        const float f = g / total * (t.left != 0.0f && z.rest != 0.0f ? t.mass - t.left * total / z.rest : t.mass);
                         const int64_t lo = max(x.base, static_cast<int64_t>(0)), hi = min(x.base + x.span, static_cast<int64_t>(a.V));
-                        for (int64_t i = lo + tid; i < hi; i += kNT) out[i] = from_f32<T>(ex2_approx(exponent(to_f32(x.row[i]))) * f);
+                        for (int64_t i = lo + tid; i < hi; i += kNT) out[i] = from_f32<T>(ex2_approx(exponent(to_f32(x.row[i]), rest_ref)) * f);
                     } else {
                         zeros(x, out);
                     }
                 } else {
-                    const float f = g / total * (t.left != 0.0f && z.rest != 0.0f ? t.mass - t.left * total / z.rest : t.mass);
                     if ((reinterpret_cast<uintptr_t>(out) - reinterpret_cast<uintptr_t>(x.row)) % 16 == 0)
-                        write_share<true>(x, out, z.m, f, vecs);
-                    else write_share<false>(x, out, z.m, f, vecs);
-                    if (single >= 0) out[single] = from_f32<T>(ex2_approx(exponent(alone)) * f);
+                        write_share<true>(x, out, z.rest_m, f, vecs);
+                    else write_share<false>(x, out, z.rest_m, f, vecs);
+                    if (single >= 0) out[single] = from_f32<T>(ex2_approx(exponent(alone, z.rest_m)) * f);
                 }
             }
-            p_left = t.left;
-            p_logs = t.log_left - log_rest(z.list / total, z.rest / total);  // ln (r / s)
+            // r (ln r - ln s); ln s where it is small: the references' distance, and the sums
+            p_rest = 0.0f;
+            if (t.left != 0.0f) {
+                const float share = z.rest * rest_up / total;
+                const bool most = share > 0.5f;
+                const float ln_s = most ? log1pf(-(z.list * under(z.list_m)) / total)
+                                        : ((log2f(z.rest) - log_z.part) - log_z.whole) * kLn2;
+                p_rest = t.left * (t.log_left - ln_s);
+                if (!most) p_rest = fmaf(-(t.left * (slow ? a.inv_t : kLn2)), z.rest_m - top, p_rest);
+            }
             p_mass = t.mass;
             pending_row = row;
             ++lives;

@@ -1,0 +1,123 @@
+"""sel_distill and sel_distill_grad where a sum, a reference or a rounding of theirs
+could leave fp32, against the 64-bit formulas."""
+import math
+
+import pytest
+import torch
+
+from oracle import learning as L
+from sampling_row_fp32_gb300 import binding as B
+from tests.test_gpu_distill import DT, INF, make, run
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+def named_ids(ids, V):
+    named = torch.zeros(len(ids), V, dtype=torch.bool, device=ids.device)
+    for r in range(len(ids)):
+        at = ids[r].long()
+        named[r, at[(at >= 0) & (at < V)]] = True
+    return named
+
+
+def bounds(x, vals, ids, lse, T, grad, want, want_x):
+    """What fp32 steps may be off for rows whose listed ids hold the largest logits, with
+    the teacher's lse given.
+
+    As in test_gpu_distill.tolerances: log2(e) / T rounded stretches the logits by 2^-24,
+    which moves ln q by that much of a logit's distance from the mean one, which lies
+    among the listed; so ln q of a listed id is off by dq with the listed logits' width.
+    ln s is the distance from the largest logit to the largest unlisted one, through two
+    rounded factors and two products, and the rest as before: 2^-22 of itself and dq.
+    r = 1 - sum p is off by dp, which moves r (ln r - ln s) by dp (|ln r| + |ln s| + 1),
+    |ln r| below 20. A share of s is the softmax of the unlisted logits alone: off by dq
+    with their own width."""
+    y = x.double() / T
+    V = x.shape[1]
+    named = named_ids(ids, V)
+    lq = torch.log_softmax(y, dim=1)
+    far = lq.masked_fill(named, -INF)
+    ln_s = torch.logsumexp(far, dim=1)
+
+    def spread(keep):
+        n = torch.where(keep & torch.isfinite(y), y, float("nan"))
+        hi = torch.nan_to_num(n, nan=-INF).max(dim=1).values
+        lo = torch.nan_to_num(n, nan=INF).min(dim=1).values
+        return torch.where(hi >= lo, hi - lo, 0.0), torch.where(hi >= lo, torch.maximum(hi.abs(), lo.abs()), 0.0)
+    width = spread(named)[1] + 1
+    own = spread(~named & (far > ln_s[:, None] - 100))[0] + 1
+
+    def off(w):
+        depth = math.log(V) + 2 * w
+        return 2.0 ** -24 * (2 * w + 2 * depth + 80) + 2.0 ** -21 + 2.0 ** -22 * depth, depth
+    dq, depth = off(width)
+    ds, _ = off(own)
+    v = vals.double().abs().nan_to_num(posinf=0.0).max(dim=1).values / T + 1
+    dp = 2.0 ** -24 * (4 * v + 40) + 2.0 ** -21 + 2.0 ** -22 * (2 * v + 8) + 2.0 ** -22 * torch.maximum(v, lse.abs().double())
+    at = L._in_vocabulary(ids, V)
+    p = torch.where(at >= 0, torch.exp(vals.double() / T - lse.double()[:, None]), 0.0)
+    r = (1 - p.sum(dim=1)).clamp(min=0)
+    size = torch.where(torch.isfinite(ln_s), ln_s.abs(), 0.0)
+    loss = 3 * (dp + dq) * (2 + depth + 2 * v) + 2.0 ** -20 * (want.abs() + 1)
+    loss = loss + dp * (size + 21) + r * 2.0 ** -22 * size
+    T_eps = torch.finfo(x.dtype).eps / 2
+    q = torch.exp(lq)
+    share = torch.softmax(y.masked_fill(named, -INF), dim=1).nan_to_num(nan=0.0)
+    d = q * (dq + dp)[:, None] + share * (dp + r * (2 * ds + dq + 2.0 ** -21))[:, None]
+    d.scatter_add_(1, at.clamp(min=0), p * (dq + dp)[:, None] * (at >= 0))
+    d = d * (grad.double().abs() / T)[:, None]
+    tiny = torch.finfo(x.dtype).smallest_normal * T_eps
+    # (weights below 2^-126 of a class's largest are nothing)
+    return loss, d + (T_eps + 2.0 ** -22) * want_x.abs() + tiny + 2.0 ** -124 * grad.double().abs()[:, None] / T
+
+
+def compare(x, vals, ids, lse, T, grad):
+    want, want_x = L.distill(x, vals, ids, lse, T, grad)
+    tol, tol_x = bounds(x, vals, ids, lse, T, grad, want, want_x)
+    for loss, out in ((run(x, vals, ids, lse, T), None), run(x, vals, ids, lse, T, grad)):
+        inf = torch.isinf(want)
+        assert torch.equal(loss[inf].double(), want[inf])
+        err = (loss.double() - want).abs()[~inf]
+        assert (err <= tol[~inf]).all(), ((err / tol[~inf]).max(), loss, want)
+        if out is not None:
+            err = (out.double() - want_x).abs()
+            assert (err <= tol_x).all(), (err / tol_x).max()
+    return loss, out
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows,V,k", [(6, 300, 9), (5, 40_001, 60), (3, 300_000, 20)])
+@pytest.mark.parametrize("T,gap", [(1.0, 60.0), (1.0, 80.0), (1.0, 86.0), (1.0, 88.0), (1.0, 100.0), (0.25, 26.0), (1.0, 1e4),
+                                   (4.0, 3e4)])
+def test_unlisted_ids_far_below_the_list(T, gap, rows, V, k, dtype):
+    """The student gives the unlisted ids next to nothing, the teacher does not: the rest's
+    term is r (ln r - ln s) with s far below the smallest fp32 number, and a share of
+    r of the gradient still goes to each of them."""
+    x, vals, ids, lse, grad = make(int(gap), rows, V, k, dtype, T, rest=True)
+    named = named_ids(ids, V)
+    x -= torch.where(named, 0.0, gap).to(x.dtype)
+    x[0].masked_fill_(~named[0] & (torch.arange(V, device="cuda") % 3 == 0), -INF)
+    x[1].masked_fill_(~named[1], -gap)
+    x[2].masked_fill_(~named[2] & (torch.arange(V, device="cuda") % 50 != 7), -INF)
+    compare(x, vals, ids, lse, T, grad * (1024.0 if dtype == "f32" else 1.0))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [300, 150_000])
+def test_unlisted_ids_at_the_types_lowest_value(V, dtype):
+    """A mask of finfo.min on every unlisted id: ln s is that value, and their shares are even."""
+    x, vals, ids, lse, grad = make(3, 5, V, 8, dtype, 2.0, rest=True)
+    named = named_ids(ids, V)
+    x[::2] = torch.where(named, x, torch.finfo(x.dtype).min)[::2]
+    x[4] = torch.where(named[4], torch.finfo(x.dtype).min, x[4])  # and on every listed one
+    want, want_x = L.distill(x, vals, ids, lse, 2.0, grad)
+    loss, out = run(x, vals, ids, lse, 2.0, grad)
+    # (r and the p of the listed ids are off by about 1e-5, which the distance magnifies)
+    assert ((loss.double() - want).abs() <= 1e-4 * want.abs() + 1e-4).all(), (loss, want)
+    assert ((out.double() - want_x).abs() <= 1e-4 * grad.double()[:, None] + 2.0 ** -8 * want_x.abs()).all()

@@ -1,0 +1,24 @@
+"""The operators that a drafter learns with, without a GPU, at the borders of their
+contracts: the 64-bit forms there, and what the library's checks let through."""
+import math
+
+import torch
+
+from oracle import learning as L
+
+INF = float("inf")
+
+
+def test_distill_of_unlisted_ids_far_below_the_list():
+    """One id listed with p = 1/4, three others that lie 10^4 below it: s = 3 e^-10000, and
+    each of them gets a third of -r."""
+    x = torch.tensor([[0.0, -1e4, -1e4, -1e4]], dtype=torch.float64)
+    lse = torch.tensor([math.log(4.0)], dtype=torch.float64)
+    one = torch.ones(1, dtype=torch.float64)
+    loss, d = L.distill(x, torch.zeros(1, 1), torch.tensor([[0]]), lse, 1.0, one)
+    want = 0.25 * math.log(0.25) + 0.75 * (math.log(0.75) - (math.log(3.0) - 1e4))
+    assert abs(loss.item() / want - 1) < 1e-12
+    assert torch.allclose(d, torch.tensor([[0.75, -0.25, -0.25, -0.25]], dtype=torch.float64), rtol=1e-12)
+    x[0, 2:] = -INF
+    _, d = L.distill(x, torch.zeros(1, 1), torch.tensor([[0]]), lse, 1.0, one)
+    assert torch.allclose(d, torch.tensor([[0.75, -0.75, 0, 0]], dtype=torch.float64), rtol=1e-12)
