@@ -834,7 +834,10 @@ sel_status sel_head_loss_grad(const void *d_hidden, uint32_t rows,
  * to 1. Given, L is the teacher's over its whole row, and what the list leaves
  * out is one more class: with r = 1 - sum p (0 where rounding makes it
  * negative, or where the list names every id) and s the sum of q over the ids
- * that the list does not name, the loss has r * (ln r - ln s) added.
+ * that the list does not name, the loss has r * (ln r - ln s) added. An r of at
+ * most 2^-21 * max(1, |L|), which rounding of L makes, counts as 0 too where
+ * nothing is left for it: where an entry of the list has a probability below
+ * 2^-126 (a value of -Inf: a top-k list's others have no more), or s is below 2^-126.
  * Entries whose id is >= V (SEL_INVALID_ID) are left out; a row without an
  * entry whose value is above -Inf is ignored, with a loss of 0. A logit of -Inf
  * is a probability of 0. A row with a NaN or +Inf logit, value or lse, with

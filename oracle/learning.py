@@ -5,6 +5,8 @@ tensors of any device whose values are taken as they are; written from the
 definitions, with no code of the kernels."""
 from __future__ import annotations
 
+import math
+
 import torch
 
 INF = float("inf")
@@ -76,6 +78,11 @@ def distill(x, vals, ids, teacher_lse, temperature, grad=None):
             left = torch.zeros((), dtype=torch.float64, device=x.device)
             if teacher_lse is not None and len(i) < V:
                 left = (1.0 - p.sum()).clamp(min=0.0)
+                # an r no larger than the rounding of a 32-bit lse, with nothing left for it
+                nothing = -126 * math.log(2.0)
+                if left <= 2.0 ** -21 * max(1.0, abs(L.item())):
+                    if (lp < nothing).any() or torch.logsumexp(lq[r, ~listed], dim=0) < nothing:
+                        left = torch.zeros_like(left)
             m = p.sum() + left
             d = m * q[r]
             d[i] -= p

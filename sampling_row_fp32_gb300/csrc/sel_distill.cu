@@ -268,14 +268,20 @@ struct Log2 {
 };
 
 // What the teacher's list comes to. norm: log2 of its normaliser over its largest
-// value `top`; left: r, and `log_left` its logarithm; mass: the sum
-// of p and r (NaN fails the row).
+// value `top`; left: r, and `log_left` its logarithm; sum: of p; mass: of p and r (NaN fails
+// the row). noise: r is no more than the rounding of the given lse, and is nothing
+// where s is too.
 struct Teacher {
     float top;
     Log2 norm;
-    float left, log_left, mass;
-    uint32_t live;
+    float left, log_left, sum, mass;
+    uint32_t noise, live;
 };
+
+// What is taken for nothing, of p as of s; and what an fp32 lse may be off, itself and
+// in the sums that gave it, in units of max(1, |lse|): a list that names every id with
+// a probability leaves an r of that size, half of the time above 0.
+constexpr float kNothing = 1.17549435e-38f, kNothingLog2 = -126.0f, kLseNoise = 4.76837158e-7f;
 
 // ln of 1 - p, p and 1 - p both at hand.
 __device__ __forceinline__ float log_rest(float p, float rest) { return rest > 0.5f ? log1pf(-p) : logf(rest); }
@@ -373,18 +379,25 @@ __device__ __forceinline__ Teacher read_teacher(const DistillArgs& a, uint32_t r
     named = __reduce_add_sync(kFull, named);
     nan = __any_sync(kFull, nan);
     FF w{0.0f, 0.0f};
+    bool end = false;  // (of a top-k list: nothing follows)
 #pragma unroll 4
     for (uint32_t i = lane; i < a.k; i += 32) {
         const uint32_t id = ids[i];
         const float v = vals[i];
-        if (id < a.V) w = ff_add(w, FF{exp2f(log_p.given ? log_p(v) : (v - top) * a.kf), 0.0f});
+        if (id >= a.V) continue;
+        const float lp = log_p.given ? log_p(v) : (v - top) * a.kf;
+        end |= lp < kNothingLog2;
+        w = ff_add(w, FF{exp2f(lp), 0.0f});
     }
     w = ff_warp_sum(w);
-    Teacher t{top, Log2{}, 0.0f, 0.0f, 1.0f, nan || top > -INFINITY};
+    end = __any_sync(kFull, end);
+    Teacher t{top, Log2{}, 0.0f, 0.0f, w.hi + w.lo, 1.0f, 0, nan || top > -INFINITY};
     if (log_p.given) {
         t.left = named == a.V ? 0.0f : fmaxf(0.0f, (1.0f - w.hi) - w.lo);
-        t.log_left = log_rest(w.hi + w.lo, t.left);
-        if (t.left == 0.0f) t.mass = w.hi + w.lo;
+        t.noise = t.left <= kLseNoise * fmaxf(1.0f, fabsf(a.teacher_lse[row]));
+        if (t.noise && end) t.left = 0.0f;
+        t.log_left = log_rest(t.sum, t.left);
+        if (t.left == 0.0f) t.mass = t.sum;
     } else {
         t.norm = Log2(w.hi + w.lo);
     }
@@ -652,7 +665,7 @@ struct Worker {
             // (all of the row before is written, and this row's bitmap is whole)
             scatter();
             wait(&s.t_full[n & 1], n >> 1 & 1, &s.err);
-            const Teacher t = s.teacher[n & 1];
+            Teacher t = s.teacher[n & 1];
             __syncwarp();
             if (lane == 0) arrive(&s.t_empty[n & 1]);
             if (!t.live) {
@@ -697,6 +710,10 @@ struct Worker {
             const float rest_up = under(z.rest_m);  // a unit of the unlisted sum in the row's
             float total = z.rest * rest_up + z.list * under(z.list_m);
             if (!(total > 0.0f)) total = NAN;  // (every id at -Inf)
+            if (t.noise && z.rest * rest_up < kNothing * total) {
+                t.left = 0.0f;
+                t.mass = t.sum;
+            }
             const Log2 log_z(total);
             auto exponent = [&](float v, float ref) { return slow ? (v - ref) * a.kf : fmaf(v, a.kf, -ref); };
             auto log_q = [&](float v) {

@@ -121,3 +121,59 @@ def test_unlisted_ids_at_the_types_lowest_value(V, dtype):
     # (r and the p of the listed ids are off by about 1e-5, which the distance magnifies)
     assert ((loss.double() - want).abs() <= 1e-4 * want.abs() + 1e-4).all(), (loss, want)
     assert ((out.double() - want_x).abs() <= 1e-4 * grad.double()[:, None] + 2.0 ** -8 * want_x.abs()).all()
+
+
+def exhausted(seed, rows, V, some, k, T, mask):
+    """Rows of which `some` ids count; the others are -Inf to the teacher and `mask` to the student."""
+    g = torch.Generator().manual_seed(seed)
+    teacher = torch.full((rows, V), -INF)
+    x = torch.full((rows, V), mask)
+    for r in range(rows):
+        at = torch.randperm(V, generator=g)[:some]
+        teacher[r, at] = 3 * torch.randn(some, generator=g)
+        x[r, at] = 0.7 * teacher[r, at] + torch.randn(some, generator=g)
+    vals, ids = torch.topk(teacher, k, dim=1)
+    lse = torch.logsumexp(teacher.double() / T, dim=1).float()
+    grad = 0.5 + torch.rand(rows, generator=g)
+    return x.cuda(), vals.cuda(), ids.int().cuda(), lse.cuda(), grad.cuda()
+
+
+@pytest.mark.parametrize("mask", [-INF, torch.finfo(torch.float32).min, -1e4])
+@pytest.mark.parametrize("T", [1.0, 3.0])
+@pytest.mark.parametrize("rows,V,some,k", [(200, 400, 30, 30), (200, 400, 30, 50), (64, 70_000, 300, 300), (64, 70_000, 300, 310)])
+def test_lists_that_leave_nothing_out(rows, V, some, k, T, mask):
+    """Constrained decoding: the list names every id that can come. 1 - sum p is then the
+    rounding of the lse, above 0 in half of the rows, and what is left is masked in the
+    student as well: the loss is the divergence over the list, not that rounding times
+    the mask."""
+    x, vals, ids, lse, grad = exhausted(some + k, rows, V, some, k, T, mask)
+    p = torch.softmax(vals.double() / T, dim=1)
+    lq = torch.log_softmax(x.double() / T, dim=1).gather(1, ids.long())
+    want = torch.where(p > 0, p * (p.log() - lq), 0.0).sum(dim=1)
+    loss, out = run(x, vals, ids, lse, T, grad)
+    assert torch.equal(loss, run(x, vals, ids, lse, T))
+    # The lse's rounding (2^-24 of it, below 8 here) scales p; fp32 logarithms of up to 40
+    # in base 2 are off by 2^-18, and the exponentials of p by 2^-21.
+    assert ((loss.double() - want).abs() <= (2.0 ** -20 + 2.0 ** -17) * (1 + want)).all(), (loss, want)
+    w = torch.softmax(x.double() / T, dim=1)
+    w.scatter_add_(1, ids.long(), -p)
+    w = w * grad.double()[:, None] / T
+    assert ((out.double() - w).abs() <= 2.0 ** -17 * grad.double()[:, None] / T).all()
+
+
+def test_mass_outside_the_list_that_the_student_has_masked():
+    """r is no rounding here: no student's probability left for it is an infinite divergence."""
+    x, vals, ids, lse, grad = exhausted(9, 20, 500, 40, 20, 1.0, -INF)
+    x[::2].masked_fill_(~named_ids(ids, 500)[::2], -INF)
+    loss, out = run(x, vals, ids, lse, 1.0, grad)
+    want, want_x = L.distill(x, vals, ids, lse, 1.0, grad)
+    assert (loss[::2] == INF).all() and torch.isfinite(loss[1::2]).all() and torch.isfinite(out).all()
+    assert ((loss.double() - want).abs() <= 2.0 ** -16 * want)[1::2].all()
+    assert ((out.double() - want_x).abs() <= 2.0 ** -16 * grad.double()[:, None]).all()
+
+
+def test_an_entry_without_probability_leaves_real_mass_alone():
+    """A list that is no top-k list: one id of probability 0, and most of the row unnamed."""
+    x, vals, ids, lse, grad = make(12, 30, 4000, 7, "f32", 1.0, rest=True)
+    vals[:, 3] = -INF
+    compare(x, vals, ids, lse, 1.0, grad)

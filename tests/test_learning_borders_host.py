@@ -22,3 +22,18 @@ def test_distill_of_unlisted_ids_far_below_the_list():
     x[0, 2:] = -INF
     _, d = L.distill(x, torch.zeros(1, 1), torch.tensor([[0]]), lse, 1.0, one)
     assert torch.allclose(d, torch.tensor([[0.75, -0.75, 0, 0]], dtype=torch.float64), rtol=1e-12)
+
+
+def test_distill_of_lists_that_leave_nothing_out():
+    """The rounding of a 32-bit lse is no probability, where nothing is left for it."""
+    v = torch.tensor([[1.0, 0.5, -INF]])
+    exact = torch.logsumexp(v.double(), 1)
+    x = torch.tensor([[0.3, 0.1, -INF, -INF, -INF]], dtype=torch.float64)
+    want = L.distill(x[:, :3], v, torch.tensor([[0, 1, 2]]), None, 1.0)
+    for lse in (exact + 3e-7, exact - 3e-7):
+        for k in (2, 3):
+            assert abs((L.distill(x, v[:, :k], torch.tensor([[0, 1, 2]])[:, :k], lse, 1.0) - want).item()) < 1e-6
+    assert L.distill(x, v[:, :2], torch.tensor([[0, 1]]), exact + 0.1, 1.0).item() == INF
+    x[0, 3] = 0.0  # (and where something is, it counts)
+    _, d = L.distill(x, v[:, :2], torch.tensor([[0, 1]]), exact + 3e-7, 1.0, torch.ones(1))
+    assert abs(d.sum().item()) < 1e-12
