@@ -847,7 +847,7 @@ sel_status sel_head_loss_grad(const void *d_hidden, uint32_t rows,
  *                  to their elements. V at most SEL_DISTILL_MAX_V
  *   d_vals, d_ids  [rows][k] f32 and u32, any order; 1 <= k <= min(V, SEL_MAX_K)
  *   d_teacher_lse  [rows] f32 (ln sum exp(v / T) over the teacher's row), or NULL
- *   temperature    > 0 and finite
+ *   temperature    a normal number (at least 2^-126), finite
  *   d_loss         [rows] f32
  *
  * sel_distill_grad -- the gradient of sum over r of grad[r] * loss[r] as to the

@@ -608,7 +608,7 @@ struct Worker {
             float loss = 0.0f;
             for (uint32_t i = lane; i < a.C * kWarps; i += 32) loss += s.losses[p][i];
             loss = warp_sum(loss);
-            loss = fmaf(loss, kLn2, p_rest);
+            loss += p_rest;
             if (lane == 0) a.loss[pending_row] = p_mass == p_mass && !s.err ? loss : NAN;
         };
         auto scatter = [&] {
@@ -729,20 +729,22 @@ struct Worker {
 #pragma unroll
             for (uint32_t e = 0; e < kEntries; ++e)
                 if (new_id[e] != SEL_INVALID_ID) bits[(new_id[e] - x.base) >> 5] = 0;
-            float part = 0.0f;
+            float part = 0.0f, far = 0.0f;  // far: of logits that log2(e) / T takes past fp32 (a mask's lowest value)
 #pragma unroll
             for (uint32_t e = 0; e < kEntries; ++e) {
                 id[e] = new_id[e];
                 if (id[e] == SEL_INVALID_ID) continue;
                 const float lp = log_p(val[e]), p = exp2f(lp);
-                if (p != 0.0f) part += p * (lp - log_q(logit[e]));
+                const float lq = log_q(logit[e]);
+                if (lq == -INFINITY && logit[e] > -INFINITY) far += (p * a.inv_t) * ((slow ? top : 0.0f) - logit[e]);
+                else if (p != 0.0f) part += p * (lp - lq);
                 grads[e] = g * (t.mass * (ex2_approx(exponent(logit[e], top)) / total) - p);
                 if (kGrad && grad == 0.0f) id[e] = SEL_INVALID_ID;
             }
             if (a.loss) {
                 if (rank == 0 && tid == 0) expect_tx(&s.loss[lives & 1], a.C * kWarps * 4);
                 if (rank == 0 && warp == 0 && pending) finish();
-                part = warp_sum(part);
+                part = warp_sum(fmaf(part, kLn2, far));
                 if (lane == 0) send(peer_addr(&s.losses[lives & 1][rank * kWarps + warp], 0), peer_addr(&s.loss[lives & 1], 0), part);
             }
             if constexpr (kGrad) {
@@ -962,7 +964,8 @@ sel_status check(const void* x, int dtype, uint32_t rows, uint32_t V, uint64_t l
                  uint32_t k, const float* teacher_lse, float T) {
     const uint32_t size = dtype_bytes(dtype);
     if (size == 0 || V == 0 || V > SEL_MAX_V || ld < V || ld > SEL_MAX_LD) return SEL_EINVAL;
-    if (!(T > 0.0f) || !(T < INFINITY) || k == 0 || k > V) return SEL_EINVAL;
+    // (below the normal numbers log2(e) / T would be infinite)
+    if (!(T >= 1.17549435e-38f) || !(T < INFINITY) || k == 0 || k > V) return SEL_EINVAL;
     if (k > SEL_MAX_K || V > SEL_DISTILL_MAX_V || rows > 0x7fffffffu) return SEL_EUNSUPPORTED;
     if (rows == 0) return SEL_OK;
     if (!x || !vals || !ids) return SEL_EINVAL;

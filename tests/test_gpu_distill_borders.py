@@ -177,3 +177,46 @@ def test_an_entry_without_probability_leaves_real_mass_alone():
     x, vals, ids, lse, grad = make(12, 30, 4000, 7, "f32", 1.0, rest=True)
     vals[:, 3] = -INF
     compare(x, vals, ids, lse, 1.0, grad)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [300, 150_000])
+@pytest.mark.parametrize("T", [0.8, 1.0, 1.5])
+@pytest.mark.parametrize("high", [False, True])
+def test_listed_ids_at_the_types_lowest_value(high, T, V, dtype):
+    """The student masks what the teacher lists: the loss is that id's p times a distance
+    that fp32 holds in nats, but not in base 2."""
+    x, vals, ids, _, grad = make(4, 6, V, 8, dtype, T)
+    x[:, int(ids[5, 1])] = 0.0
+    if high:
+        x *= 1e7  # (references that are no whole numbers)
+    for r, e in ((0, 3), (1, 0), (2, 7), (4, 5)):
+        x[r, int(ids[r, e])] = torch.finfo(x.dtype).min
+    vals[2, 7] = vals[2].min() - 30.0 * T  # p about 1e-13
+    T = torch.tensor(T).item()
+    want, want_x = L.distill(x, vals, ids, None, T, grad)
+    loss, out = run(x, vals, ids, None, T, grad)
+    assert torch.equal(loss, run(x, vals, ids, None, T))
+    ok = want < torch.finfo(torch.float32).max  # (T below 1)
+    assert ok[[2, 3, 5]].all() and (loss[~ok] == INF).all()
+    # p is off by 2^-20 of itself (its logarithm, of up to 80 in base 2, by 2^-18)
+    assert ((loss.double() - want).abs() <= 2.0 ** -17 * want.abs() + 1e-4)[ok].all(), (loss, want)
+    # (ln q by 2^-20 of the logits' distances, which e^-distance takes back, and the type's rounding)
+    assert ((out.double() - want_x).abs() <= 2.0 ** -16 * grad.double()[:, None] / T + 2.0 ** -8 * want_x.abs()).all()
+
+
+@pytest.mark.parametrize("T", [2.0 ** -126, 1e-20, 1e30, 3e38])
+def test_temperatures_at_the_ends_of_fp32(T):
+    """Next to nothing and next to infinite: one id has all the weight, or all have the same."""
+    x, vals, ids, _, grad = make(6, 4, 900, 6, "f32")
+    x[0] = x[0].abs() + 1
+    T = torch.tensor(T).item()
+    want, want_x = L.distill(x, vals, ids, None, T, grad)
+    loss, out = run(x, vals, ids, None, T, grad)
+    fits = want < torch.finfo(torch.float32).max
+    assert ((loss.double() - want).abs() <= 2.0 ** -18 * want.abs() + 2.0 ** -20)[fits].all() and (loss[~fits] == INF).all()
+    # (of a gradient of g / T (q - p) each of the two to 2^-18, past fp32's largest infinite)
+    g = grad.double()[:, None] / T
+    err = torch.where(want_x.abs() < 3.4e38, (out.double() - want_x).abs(), 0.0)
+    assert (err <= 2.0 ** -18 * g + 2.0 ** -23 * want_x.abs() + 2.0 ** -148).all()
+    assert (out.abs()[want_x.abs() > 3.41e38] == INF).all()

@@ -1,10 +1,13 @@
 """The operators that a drafter learns with, without a GPU, at the borders of their
 contracts: the 64-bit forms there, and what the library's checks let through."""
+import ctypes
 import math
 
 import torch
 
 from oracle import learning as L
+from sampling_row_fp32_gb300 import binding as B
+from tests.test_learning_host import lib, needs_nvcc  # noqa: F401
 
 INF = float("inf")
 
@@ -37,3 +40,14 @@ def test_distill_of_lists_that_leave_nothing_out():
     x[0, 3] = 0.0  # (and where something is, it counts)
     _, d = L.distill(x, v[:, :2], torch.tensor([[0, 1]]), exact + 3e-7, 1.0, torch.ones(1))
     assert abs(d.sum().item()) < 1e-12
+
+
+@needs_nvcc
+def test_temperatures_that_are_no_normal_numbers_are_refused(lib):
+    F, vp = 0x10000, ctypes.c_void_p
+    for T in (1e-45, 2e-39, 1.1754942e-38):
+        assert lib.sel_distill(vp(F), B.SEL_F32, 3, 10, 10, vp(F), vp(F), 4, None, T, vp(F), None) == B.SEL_EINVAL
+        assert lib.sel_distill_grad(vp(F), B.SEL_F32, 3, 10, 10, vp(F), vp(F), 4, None, T, vp(F), vp(F), vp(2 * F), 10,
+                                    None) == B.SEL_EINVAL
+    # (the smallest that is: no rows, so that nothing is launched)
+    assert lib.sel_distill(vp(F), B.SEL_F32, 0, 10, 10, vp(F), vp(F), 4, None, 2.0 ** -126, vp(F), None) == B.SEL_OK
