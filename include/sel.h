@@ -829,7 +829,9 @@ sel_status sel_head_loss_grad(const void *d_hidden, uint32_t rows,
  * sel_distill -- the divergence of logits rows from a teacher that is known by
  * its top logits (sel_topk's lists). With q = softmax(x / T) over the row and
  * the list's p_i = exp(v_i / T - L):
- *   loss = sum over the list of p_i * (ln p_i - ln q[ids_i])      (>= 0)
+ *   loss = sum over the list of p_i * (ln p_i - ln q[ids_i])
+ * (>= 0: what rounding takes below is 0. ln p and ln q come from fp32, so a loss is
+ * off by about 2^-20 of their size, not of its own).
  * d_teacher_lse NULL: L is the list's own ln sum exp(v_i / T), so that p sums
  * to 1. Given, L is the teacher's over its whole row, and what the list leaves
  * out is one more class: with r = 1 - sum p (0 where rounding makes it

@@ -609,6 +609,7 @@ struct Worker {
             for (uint32_t i = lane; i < a.C * kWarps; i += 32) loss += s.losses[p][i];
             loss = warp_sum(loss);
             loss += p_rest;
+            if (loss < 0.0f) loss = 0.0f;  // (ln p and ln q are rounded apart; a NaN stays)
             if (lane == 0) a.loss[pending_row] = p_mass == p_mass && !s.err ? loss : NAN;
         };
         auto scatter = [&] {

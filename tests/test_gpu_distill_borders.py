@@ -220,3 +220,24 @@ def test_temperatures_at_the_ends_of_fp32(T):
     err = torch.where(want_x.abs() < 3.4e38, (out.double() - want_x).abs(), 0.0)
     assert (err <= 2.0 ** -18 * g + 2.0 ** -23 * want_x.abs() + 2.0 ** -148).all()
     assert (out.abs()[want_x.abs() > 3.41e38] == INF).all()
+
+
+@pytest.mark.parametrize("rest", [False, True])
+@pytest.mark.parametrize("rows,V,k", [(300, 64, 64), (300, 1000, 1000), (40, 30_000, 900)])
+def test_no_divergence_is_below_zero(rows, V, k, rest):
+    """A student equal to its teacher: rounding puts the sum on both sides of 0."""
+    x, vals, ids, lse, grad = make(rows + k, rows, V, k, "f32", 1.0, rest=rest)
+    x.scatter_(1, ids.long(), vals)
+    if rest:  # the unlisted ids with the mass that the teacher gives them, spread evenly
+        named = named_ids(ids, V)
+        left = (1 - torch.exp(vals.double() - lse.double()[:, None]).sum(dim=1)).clamp(min=1e-30)
+        even = lse.double() + torch.log(left / max(1, V - k))
+        x.copy_(torch.where(named, x, even[:, None].float()))
+    elif k < V:
+        x.masked_fill_(~named_ids(ids, V), -INF)
+    loss, _ = run(x, vals, ids, lse, 1.0, grad)
+    assert torch.equal(loss, run(x, vals, ids, lse, 1.0))
+    # (logarithms of up to 30 in base 2, and r's of its rounding over itself)
+    assert (loss >= 0).all() and (loss <= 2.0 ** -16).all(), (loss.min(), loss.max())
+    x[0, 5] = float("nan")
+    assert torch.isnan(run(x, vals, ids, lse, 1.0)[0])
