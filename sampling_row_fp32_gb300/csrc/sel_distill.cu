@@ -25,7 +25,9 @@
 // 87 nats below the listed ones, though ln s and their shares of s are ordinary
 // numbers. Sums meet as messages between the warps of the cluster (st.async), joined
 // in one order; no barrier of the cluster stands between a row and the next. Every
-// wait is bounded; one that runs out makes the CTA's rows NaN.
+// wait is bounded. One that runs out ends its CTA's roles before the next row (the
+// others' waits then run out too), and whatever was written till then, the cluster's
+// CTAs make all of its rows NaN at the end.
 //
 // What bounds it: large batches the row's bytes, and the second copy through L2 (4,096
 // x 151,936 bf16, lists of 64: 430 us, 5.8 TB/s, 51 percent of the issue slots); a few
@@ -286,13 +288,25 @@ constexpr float kNothing = 1.17549435e-38f, kNothingLog2 = -126.0f, kLseNoise = 
 // ln of 1 - p, p and 1 - p both at hand.
 __device__ __forceinline__ float log_rest(float p, float rest) { return rest > 0.5f ? log1pf(-p) : logf(rest); }
 
+// A build of the tests names a row and a CTA of its cluster whose list's result is not
+// handed on, so that waits run out.
+#ifdef SEL_TEST_DROP_ROW
+__device__ __forceinline__ bool dropped(uint32_t row, uint32_t rank) {
+    return row == SEL_TEST_DROP_ROW && rank == SEL_TEST_DROP_RANK;
+}
+#else
+__device__ __forceinline__ bool dropped(uint32_t, uint32_t) { return false; }
+#endif
+
 struct Shared {
     alignas(16) float4 table[2][kMaxC * kWarps];  // sums of every warp of the cluster
     float losses[2][kMaxC * kWarps];
     Teacher teacher[2];
     uint64_t full[kMaxSlots], empty[kMaxSlots];
     uint64_t t_full[2], t_empty[2], sums[2], loss[2];
-    uint32_t err;
+    uint32_t err;      // a wait ran out
+    uint32_t stop[2];  // that as one thread saw it before a row's barrier: the same for all
+    __device__ __forceinline__ bool failed() const { return *static_cast<const volatile uint32_t*>(&err) != 0; }
 };
 
 __device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
@@ -323,10 +337,27 @@ __device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity)
         : "memory");
     return ok != 0;
 }
-__device__ __forceinline__ void wait_cluster(uint64_t* bar, uint32_t parity, volatile uint32_t* err) {
-    bool ok = try_wait_cluster(bar, parity);
-    for (uint32_t i = 0; !ok && i < kWaitPolls && !*err; ++i) ok = try_wait_cluster(bar, parity);
-    if (!ok) *err = 1;
+// Waits of which this thread keeps whether it saw the phase end.
+__device__ __forceinline__ void wait_cluster(uint64_t* bar, uint32_t parity, volatile uint32_t* err, bool& missed) {
+    if (!try_wait_cluster(bar, parity)) {
+        bool ok = false;
+        for (uint32_t i = 0; !ok && i < kWaitPolls && !*err; ++i) ok = try_wait_cluster(bar, parity);
+        if (!ok) {
+            *err = 1;
+            missed = true;
+        }
+    }
+    __syncwarp();
+}
+__device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, volatile uint32_t* err, bool& missed) {
+    if (!mbar_try_wait(bar, parity)) {
+        bool ok = false;
+        for (uint32_t i = 0; !ok && i < kWaitPolls && !*err; ++i) ok = mbar_try_wait(bar, parity);
+        if (!ok) {
+            *err = 1;
+            missed = true;
+        }
+    }
     __syncwarp();
 }
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kNT) : "memory"); }
@@ -500,14 +531,15 @@ struct Worker {
     uint32_t words, rank, tid, lane, warp;
     Place at;
     uint32_t messages = 0;  // exchanges so far
+    bool missed = false;    // a wait of this thread's ran out: it arms no barrier and hands nothing on
 
     // The sums of all of the row's warps.
     __device__ __forceinline__ Sums exchange(Sums z) {
         const uint32_t p = messages & 1;
-        if (tid == 0) expect_tx(&s.sums[p], a.C * kWarps * 16);
+        if (tid == 0 && !missed) expect_tx(&s.sums[p], a.C * kWarps * 16);  // (never twice in a phase)
         z = warp_join(z);
         if (lane < a.C) send(peer_addr(&s.table[p][rank * kWarps + warp], lane), peer_addr(&s.sums[p], lane), z);
-        wait_cluster(&s.sums[p], messages >> 1 & 1, &s.err);
+        wait_cluster(&s.sums[p], messages >> 1 & 1, &s.err, missed);
         ++messages;
         z = {-INFINITY, 0.0f, -INFINITY, 0.0f};
         for (uint32_t i = lane; i < a.C * kWarps; i += 32) {
@@ -528,13 +560,14 @@ struct Worker {
     }
     __device__ __forceinline__ void release() {
         __syncwarp();
-        if (lane == 0) arrive(&s.empty[at.slot]);
+        if (lane == 0 && !missed) arrive(&s.empty[at.slot]);
         at.next(a.slots);
     }
+    __device__ __forceinline__ void await_chunk() { wait(&s.full[at.slot], at.phase, &s.err, missed); }
     // Chunks that nobody reads.
     __device__ __forceinline__ void skip(uint32_t chunks) {
         for (uint32_t c = 0; c < chunks; ++c) {
-            wait(&s.full[at.slot], at.phase, &s.err);
+            await_chunk();
             release();
         }
     }
@@ -563,7 +596,7 @@ struct Worker {
         const Pair k(a.kf, a.kf), r(-m, -m), f(factor, factor);
         T* to = out + (x.base + static_cast<int64_t>(x.w0) * Vec<T>::kN);
         for (uint32_t first = 0; first < vecs; first += kChunkVecs) {
-            if (!a.resident) wait(&s.full[at.slot], at.phase, &s.err);
+            if (!a.resident) await_chunk();
             chunk(first, vecs, [&](uint32_t j, auto& q) { write_vecs<T, kAligned>(to + static_cast<uint64_t>(j) * Vec<T>::kN, q, k, r, f); });
             release();
         }
@@ -604,13 +637,13 @@ struct Worker {
         for (uint32_t e = 0; e < kEntries; ++e) id[e] = SEL_INVALID_ID;
         auto finish = [&] {  // by the first warp of the row's first CTA
             const uint32_t p = (pending - 1) & 1;
-            wait_cluster(&s.loss[p], (pending - 1) >> 1 & 1, &s.err);
+            wait_cluster(&s.loss[p], (pending - 1) >> 1 & 1, &s.err, missed);
             float loss = 0.0f;
             for (uint32_t i = lane; i < a.C * kWarps; i += 32) loss += s.losses[p][i];
             loss = warp_sum(loss);
             loss += p_rest;
             if (loss < 0.0f) loss = 0.0f;  // (ln p and ln q are rounded apart; a NaN stays)
-            if (lane == 0) a.loss[pending_row] = p_mass == p_mass && !s.err ? loss : NAN;
+            if (lane == 0) a.loss[pending_row] = p_mass == p_mass ? loss : NAN;
         };
         auto scatter = [&] {
             if constexpr (kGrad) {
@@ -622,6 +655,7 @@ struct Worker {
             }
         };
         uint32_t n = 0;
+        bool stop = false;
         uint32_t list[kEntries];  // the row's ids, on their way since the row before
         auto read_list = [&](uint32_t row) {
 #pragma unroll
@@ -662,13 +696,16 @@ struct Worker {
                 twice |= (atomicOr(&bits[off >> 5], bit) & bit) != 0;
             }
             read_list(row + step);
+            if (stop) return;
+            if (tid == 0) *static_cast<volatile uint32_t*>(&s.stop[n & 1]) = s.failed();
             consumers_sync();
+            stop = *static_cast<volatile uint32_t*>(&s.stop[n & 1]);  // (looked at before the next barrier)
             // (all of the row before is written, and this row's bitmap is whole)
             scatter();
-            wait(&s.t_full[n & 1], n >> 1 & 1, &s.err);
+            wait(&s.t_full[n & 1], n >> 1 & 1, &s.err, missed);
             Teacher t = s.teacher[n & 1];
             __syncwarp();
-            if (lane == 0) arrive(&s.t_empty[n & 1]);
+            if (lane == 0 && !missed) arrive(&s.t_empty[n & 1]);
             if (!t.live) {
                 if (n == 0) skip(min(chunks, a.slots));  // (copied before the list was read)
                 if (rank == 0 && tid == 0 && a.loss) a.loss[row] = 0.0f;
@@ -682,7 +719,7 @@ struct Worker {
             Summer<T> mine{bits, a.kf, -kHuge, 0.0f};
             const Place begin = at;
             for (uint32_t first = 0; first < vecs; first += kChunkVecs) {
-                wait(&s.full[at.slot], at.phase, &s.err);
+                await_chunk();
                 chunk(first, vecs, [&](uint32_t j, auto& q) { mine.add(x.w0 + j, q); });
                 if (a.resident) at.next(a.slots);
                 else release();
@@ -705,7 +742,6 @@ struct Worker {
             // (slow too where r > 0 is shared out among unlisted ids that lie below -kHuge)
             const bool slow = !(fabsf(fmaxf(z.rest_m, z.list_m)) < kHuge) || (t.left != 0.0f && z.rest == 0.0f);
             if (slow) z = slow_sums(x, bits, twice);
-            if (s.err) z.rest = NAN;
             const float top = fmaxf(z.rest_m, z.list_m), rest_ref = reference(z.rest_m);
             auto under = [&](float m) { return slow ? ex2_approx((m - top) * a.kf) : pow2(m - top); };
             const float rest_up = under(z.rest_m);  // a unit of the unlisted sum in the row's
@@ -743,7 +779,7 @@ struct Worker {
                 if (kGrad && grad == 0.0f) id[e] = SEL_INVALID_ID;
             }
             if (a.loss) {
-                if (rank == 0 && tid == 0) expect_tx(&s.loss[lives & 1], a.C * kWarps * 4);
+                if (rank == 0 && tid == 0 && !missed) expect_tx(&s.loss[lives & 1], a.C * kWarps * 4);
                 if (rank == 0 && warp == 0 && pending) finish();
                 part = warp_sum(fmaf(part, kLn2, far));
                 if (lane == 0) send(peer_addr(&s.losses[lives & 1][rank * kWarps + warp], 0), peer_addr(&s.loss[lives & 1], 0), part);
@@ -785,6 +821,7 @@ struct Worker {
             ++lives;
             pending = lives;
         }
+        if (stop) return;
         consumers_sync();
         scatter();
         if (a.loss && rank == 0 && warp == 0 && pending) finish();
@@ -822,16 +859,17 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(DistillArgs a) {
         asm volatile("fence.proxy.async.global;" ::: "memory");
         Place at;
         uint32_t issued = 0, n = 0;
-        bool ok = true;
-        for (uint32_t row = cluster; row < a.rows && ok; row += clusters, ++n) {
+        bool missed = false;
+        for (uint32_t row = cluster; row < a.rows && !missed; row += clusters, ++n) {
             const Share<T> x(a.x, row * a.ld, a.V, rank, a.share);
             const uint32_t vecs = x.w1 - x.w0;
             const auto* src = reinterpret_cast<const unsigned char*>(x.vec + x.w0);
             const uint32_t early = min(vecs, a.slots * kChunkVecs);
             auto copy = [&](uint32_t from, uint32_t to) {
-                for (uint32_t first = from; first < to && ok; first += kChunkVecs) {
-                    ok = __all_sync(kFull, mbar_wait(&s.empty[at.slot], at.phase ^ 1));
-                    if (!ok) break;
+                for (uint32_t first = from; first < to && !missed; first += kChunkVecs) {
+                    wait(&s.empty[at.slot], at.phase ^ 1, &s.err, missed);
+                    missed = __any_sync(kFull, missed);
+                    if (missed) break;
                     if ((tid & 31) == 0)
                         bulk_load(ring + at.slot * kChunkBytes, src + static_cast<uint64_t>(first) * 16,
                                   min(kChunkVecs, vecs - first) * 16, &s.full[at.slot]);
@@ -840,7 +878,9 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(DistillArgs a) {
                 }
             };
             if (n == 0) copy(0, early);  // (before it is known whether the row counts)
-            ok = ok && __all_sync(kFull, mbar_wait(&s.t_full[n & 1], n >> 1 & 1));
+            wait(&s.t_full[n & 1], n >> 1 & 1, &s.err, missed);
+            missed = __any_sync(kFull, missed);
+            if (missed) break;
             const bool live = s.teacher[n & 1].live;
             __syncwarp();
             if ((tid & 31) == 0) arrive(&s.t_empty[n & 1]);
@@ -848,7 +888,6 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(DistillArgs a) {
             if (kGrad && !a.resident && live) copy(0, vecs);  // for the gradient
         }
         // every copy has landed before the CTA may end
-        if (!ok) s.err = 1;
         Place last = at;
         for (uint32_t i = 0; i < min(issued, a.slots); ++i) {
             last.phase ^= last.slot == 0;
@@ -858,10 +897,12 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(DistillArgs a) {
         __syncwarp();
     } else if (warp == kWarps + 1) {
         uint32_t n = 0;
+        bool missed = false;
         for (uint32_t row = cluster; row < a.rows; row += clusters, ++n) {
-            if (n >= 2) wait(&s.t_empty[n & 1], (n >> 1) + 1 & 1, &s.err);
+            if (n >= 2) wait(&s.t_empty[n & 1], (n >> 1) + 1 & 1, &s.err, missed);
+            if (__any_sync(kFull, missed)) break;
             const Teacher t = read_teacher(a, row);
-            if ((tid & 31) == 0) {
+            if ((tid & 31) == 0 && !dropped(row, rank)) {
                 s.teacher[n & 1] = t;
                 arrive(&s.t_full[n & 1]);
             }
@@ -871,9 +912,23 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(DistillArgs a) {
         Worker<T, kGrad> w{a, s, ring, bitmaps, words, rank, tid, tid & 31, warp};
         w.run(cluster, clusters);
     }
-    // (nothing is on its way to this CTA, or from it to one that has ended)
     __syncwarp();
+    if (s.failed() && (tid & 31) < C)
+        asm volatile("st.shared::cluster.u32 [%0], 1;" ::"r"(peer_addr(&s.err, tid & 31)) : "memory");
+    __syncwarp();
+    // (nothing is on its way to this CTA, or from it to one that has ended)
     cluster_sync_all();
+    if (s.failed()) {
+        for (uint32_t row = cluster; row < a.rows; row += clusters) {
+            if (a.loss && rank == 0 && tid == 0) a.loss[row] = NAN;
+            if constexpr (kGrad) {
+                const Share<T> x(a.x, row * a.ld, a.V, rank, a.share);
+                T* out = static_cast<T*>(a.out) + row * a.ld_out;
+                const int64_t lo = max(x.base, static_cast<int64_t>(0)), hi = min(x.base + x.span, static_cast<int64_t>(a.V));
+                for (int64_t i = lo + tid; i < hi; i += kThreads) out[i] = from_f32<T>(NAN);
+            }
+        }
+    }
 }
 
 constexpr size_t kSmem = 110 * 1024;  // a CTA's ring and bitmaps: two CTAs an SM

@@ -118,7 +118,10 @@ __device__ __forceinline__ void red_max_u64(unsigned long long* p, unsigned long
 // counted in bytes on an mbarrier). Every wait is bounded: after kWaitPolls
 // suspended polls (about two seconds) the caller records kErrTimeout.
 // ---------------------------------------------------------------------------
-constexpr uint32_t kWaitPolls = 10000;
+#ifndef SEL_WAIT_POLLS  // (a build of the tests gives up sooner)
+#define SEL_WAIT_POLLS 10000
+#endif
+constexpr uint32_t kWaitPolls = SEL_WAIT_POLLS;
 constexpr uint32_t kSuspendNs = 200000;  // 0.2 ms per poll at most
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

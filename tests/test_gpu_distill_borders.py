@@ -1,6 +1,8 @@
 """sel_distill and sel_distill_grad where a sum, a reference or a rounding of theirs
 could leave fp32, against the 64-bit formulas."""
+import ctypes
 import math
+import subprocess
 
 import pytest
 import torch
@@ -241,3 +243,52 @@ def test_no_divergence_is_below_zero(rows, V, k, rest):
     assert (loss >= 0).all() and (loss <= 2.0 ** -16).all(), (loss.min(), loss.max())
     x[0, 5] = float("nan")
     assert torch.isnan(run(x, vals, ids, lse, 1.0)[0])
+
+
+DROPPED = 7
+
+
+@pytest.fixture(scope="module", params=[0, 1])
+def dropping(request, tmp_path_factory):
+    """The divergence as a library whose waits give up after some 10 ms, and in which one
+    CTA never learns what row 7's list comes to: (rank of the CTA, the call)."""
+    from sampling_row_fp32_gb300 import build
+    out = str(tmp_path_factory.mktemp("drop") / "drop.so")
+    subprocess.run([build.nvcc(), *build.ARCH, *build.NVCC_FLAGS, "-DSEL_WAIT_POLLS=50", f"-DSEL_TEST_DROP_ROW={DROPPED}",
+                    f"-DSEL_TEST_DROP_RANK={request.param}", "-shared", build.CSRC + "/sel_distill.cu", "-o", out], check=True)
+    lib = ctypes.CDLL(out)
+    lib.sel_distill_grad.argtypes = B.load().sel_distill_grad.argtypes
+    lib.sel_distill_grad.restype = ctypes.c_int
+
+    def call(x, vals, ids, grad, loss, d):
+        return lib.sel_distill_grad(x.data_ptr(), {v: i for i, v in enumerate(DT.values())}[x.dtype], x.shape[0], x.shape[1],
+                                    x.stride(0), vals.data_ptr(), ids.data_ptr(), vals.shape[1], None, 1.0,
+                                    grad.data_ptr(), loss.data_ptr(), d.data_ptr(), d.stride(0),
+                                    torch.cuda.current_stream().cuda_stream)
+    return request.param, call
+
+
+@pytest.mark.parametrize("rows,V,dtype,apart", [(20, 150_001, "f32", True), (700, 151_936, "bf16", False)])
+def test_a_wait_that_runs_out_fails_its_rows(dropping, rows, V, dtype, apart):
+    """Losses and whole gradients of every row that its cluster works on, and no other's."""
+    rank, call = dropping
+    x, vals, ids, _, grad = make(13, rows, V, 30, dtype, pad=5)
+    want, want_x = run(x, vals, ids, None, 1.0, grad)
+    for n in (rows, DROPPED, rows):  # (the first seven rows alone: nothing is dropped)
+        loss = torch.full((n,), -77.0, device="cuda")
+        d = torch.full((n, V + 5), 44.0, dtype=x.dtype, device="cuda")
+        assert call(x[:n], vals[:n], ids[:n], grad[:n], loss, d) == B.SEL_OK
+        torch.cuda.synchronize()
+        bad = torch.isnan(loss)
+        at = bad.nonzero()[:, 0].tolist()
+        if n == DROPPED or (rank == 1 and not at and not apart):  # (many rows may have one CTA each)
+            assert not at
+        elif apart:
+            assert at == [DROPPED]
+        else:  # every row of the cluster, which takes each so-manieth
+            step = at[1] - at[0]
+            assert DROPPED in at and at == list(range(DROPPED % step, rows, step)) and step > 1
+        assert torch.isnan(d[bad, :V]).all() and (d[:, V:] == 44.0).all()
+        ok = ~bad
+        if n == rows:
+            assert torch.equal(loss[ok], want[ok]) and torch.equal(d[ok, :V], want_x[ok])
