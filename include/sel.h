@@ -805,7 +805,8 @@ sel_status sel_head_loss(const void *d_hidden, uint32_t rows,
  * own hidden_grad and all of weight_grad nonfinite. P times the mantissa of
  * the row's grad is rounded to `dtype` for the products (what that takes from the
  * targets' entries is added back); sums are in fp32 and each gradient is
- * rounded once. z is computed again, in pieces of the vocabulary, so the
+ * rounded once. With SEL_F16, entries of grad[r] * hidden[r] keep all of their bits in
+ * weight_grad down to 2^-28 of the largest, fewer down to 2^-40, none below. z is computed again, in pieces of the vocabulary, so the
  * workspace holds at most 2^28 entries of P, or 16,384 columns of it.
  *
  *   d_hidden, rows, d_weight, dtype, V, H, d_targets  as for sel_head_loss

@@ -65,7 +65,7 @@ struct RasterCursor {
     }
 };
 
-// 2^n for a whole n <= 0, 0 below the normal numbers (and for -Inf).
+// 2^n for a whole n <= 127, 0 below the normal numbers (and for -Inf).
 __device__ __forceinline__ float pow2(float n) {
     return n >= -126.0f ? __uint_as_float(static_cast<uint32_t>(static_cast<int>(n) + 127) << 23) : 0.0f;
 }
@@ -401,9 +401,9 @@ __global__ void __launch_bounds__(kFinishThreads) loss_finish_kernel(LossFinishA
 // gradient
 // ---------------------------------------------------------------------------
 
-// A row's gradient g = m 2^e, m in (1/2, 1): m goes into P before P is rounded, 2^e, of
-// which nothing is rounded, into the hidden rows for dW and into dX's sums. So P's
-// rounding and the results' are all there is.
+// A row's gradient g = m 2^e, m in (1/2, 1): m goes into P before P is rounded, 2^e into
+// the hidden rows for dW (unrounded within their type's exponents, see Prep) and into
+// dX's sums. So P's rounding and the results' are all there is.
 struct GradParts {
     float m;
     int e;
@@ -441,17 +441,74 @@ __device__ __forceinline__ void unpack2(uint32_t w, float& lo, float& hi) {
     hi = bits_f32<T>(static_cast<uint16_t>(w >> 16));
 }
 
+// Hidden rows enter dW times the power of two of their gradient, over one for all rows.
+// bf16 has the exponents for that: over the largest gradient's. f16 has 30, of
+// which the hidden rows take some: over that of the largest product of an entry and its
+// row's gradient, which then lies at 2^14 or above, so that a row keeps its bits down to
+// 2^-28 of it. (Over the largest gradient's, rows 2^14 below it were 2.6e-4 off, 2^20
+// below 2 percent, 2^25 below nothing.) That largest product takes a launch of its own
+// ahead of P's, a few of whose microseconds P's copies of the hidden rows get back.
+template <typename T>
+constexpr int kTopExponent = 0;  // of the largest scaled entry
+template <>
+constexpr int kTopExponent<__half> = 15;
+constexpr int kNoTop = -1000;
+constexpr uint32_t kTopBlocks = 256, kTopThreads = 256;
+
+struct TopArgs {
+    const uint4* x;
+    const uint32_t* targets;
+    const float* grad;
+    int* tops;  // [kTopBlocks]
+    uint32_t rows, V;
+    Div by_vecs;
+};
+
+// The exponent e, entries below 2^e, of f16 hidden rows times their gradients, of each
+// block's share of them.
+__global__ void __launch_bounds__(kTopThreads) row_tops_kernel(TopArgs a) {
+    __shared__ int sh[kTopThreads / 32];
+    pdl_wait();
+    pdl_trigger();
+    int top = kNoTop;
+    const uint64_t n = static_cast<uint64_t>(a.rows) * a.by_vecs.d, step = static_cast<uint64_t>(gridDim.x) * kTopThreads;
+#pragma unroll 4
+    for (uint64_t i = static_cast<uint64_t>(blockIdx.x) * kTopThreads + threadIdx.x; i < n; i += step) {
+        const uint32_t r = row_of(i, a.by_vecs);
+        const uint4 q = a.x[i];
+        const float g = a.grad[r];
+        if (!(a.targets[r] < a.V && g != 0.0f)) continue;
+        uint32_t bits = 0;
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k) bits = max(bits, max(w[k] & 0x7FFFu, w[k] >> 16 & 0x7FFFu));
+        if (bits == 0) continue;
+        int e;
+        frexpf(bits_f32<__half>(static_cast<uint16_t>(min(bits, 0x7BFFu))), &e);  // (what is not finite fails its row anyway)
+        top = max(top, e + GradParts(g).e);
+    }
+    top = __reduce_max_sync(kFull, top);
+    if (threadIdx.x % 32 == 0) sh[threadIdx.x / 32] = top;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        top = __reduce_max_sync(kFull, threadIdx.x < kTopThreads / 32 ? sh[threadIdx.x] : kNoTop);
+        if (threadIdx.x == 0) a.tops[blockIdx.x] = top;
+    }
+}
+
 // What dW needs beside P, done by warps that the launch of P has to spare: hidden rows
-// times the power of two of their gradient over the largest one's (exact, but for
-// entries that become subnormal; rows that do not count are zeros, whatever they
-// hold), the exponent of its sums, and of each 32 ids the first rows that have one of
-// them for a target. (As a launch of its own: 4 us for 64 rows, 36 for 4,096.)
+// times their powers of two (exact, but for entries that become subnormal; rows that
+// do not count are zeros, whatever they hold), the exponent of its sums, and of each
+// 32 ids the first rows that have one of them for a target. (As a launch of its own:
+// 4 us for 64 rows, 36 for 4,096.)
 template <typename T>
 struct Prep {
     const uint4* x;  // NULL: nothing to do
     uint4* scaled;
     const uint32_t* targets;
     const float* grad;
+    const int* tops;  // f16: from the launch before
+    uint32_t top_blocks;
     int* exponent;
     uint32_t* hits;
     uint32_t rows, V;
@@ -460,12 +517,16 @@ struct Prep {
 
     __device__ __forceinline__ void run(uint32_t warp, uint32_t warps) const {
         const uint32_t lane = threadIdx.x & 31;
-        int top = -1000;
+        int top = kNoTop;
+        if constexpr (kTopExponent<T> != 0) {
+            for (uint32_t i = lane; i < top_blocks; i += 32) top = max(top, tops[i]);
+        } else {
 #pragma unroll 4
-        for (uint32_t r = lane; r < rows; r += 32)
-            if (targets[r] < V && grad[r] != 0.0f) top = max(top, GradParts(grad[r]).e);
-        top = __reduce_max_sync(kFull, top);
-        if (warp == 0 && lane == 0) *exponent = max(top, -200) - shift;
+            for (uint32_t r = lane; r < rows; r += 32)
+                if (targets[r] < V && grad[r] != 0.0f) top = max(top, GradParts(grad[r]).e);
+        }
+        top = max(__reduce_max_sync(kFull, top), -200) - kTopExponent<T>;
+        if (warp == 0 && lane == 0) *exponent = top - shift;
         const uint64_t n = static_cast<uint64_t>(rows) * by_vecs.d;
         for (uint64_t i = static_cast<uint64_t>(warp) * 32 + lane; i < n; i += static_cast<uint64_t>(warps) * 32) {
             const uint32_t r = row_of(i, by_vecs);
@@ -880,7 +941,7 @@ inline LossPlan loss_plan(uint32_t rows, uint32_t V) {
 // 16,384 ids, and all alike.
 struct GradPlan {
     uint32_t piece, pieces, slices, pitch, dx_n;
-    size_t lost, hits, scaled, acc, p, bytes;
+    size_t lost, tops, hits, scaled, acc, p, bytes;
 };
 inline GradPlan grad_plan(uint32_t rows, uint32_t V, uint32_t H) {
     GradPlan g;
@@ -897,7 +958,8 @@ inline GradPlan grad_plan(uint32_t rows, uint32_t V, uint32_t H) {
     const uint64_t tiles = static_cast<uint64_t>(ceil_div(H, kTileM)) * ceil_div(rows, g.dx_n);
     g.slices = std::min(std::max(1u, g.piece / 1024), tiles >= 76 ? 1u : ceil_div(76, tiles));
     g.lost = kWsHeaderBytes;
-    g.hits = g.lost + align_up(static_cast<size_t>(rows) * sizeof(float), 256);
+    g.tops = g.lost + align_up(static_cast<size_t>(rows) * sizeof(float), 256);
+    g.hits = g.tops + kTopBlocks * sizeof(int);
     g.scaled = g.hits + align_up(static_cast<size_t>(ceil_div(V, 32)) * kHitWords * sizeof(uint32_t), 256);
     g.acc = g.scaled + align_up(static_cast<size_t>(rows) * H * 2, 256);
     // What the sums and P take at most: slices * tiles < 76 + tiles, and P as above;
@@ -986,14 +1048,19 @@ sel_status run_grad(const HeadLossCall& c, const float* lse, const float* grad, 
     auto* hits = reinterpret_cast<uint32_t*>(c.ws + plan.hits);
     const int shift = static_cast<int>(kProbShift<T>);
     const uint32_t vecs = c.H / 8, all = sms / 2;
+    const TopArgs tops{static_cast<const uint4*>(c.x), c.targets, grad, reinterpret_cast<int*>(c.ws + plan.tops), c.rows, c.V, Div(vecs)};
+    const uint32_t top_blocks = std::min<uint64_t>(kTopBlocks, ceil_div(static_cast<uint64_t>(c.rows) * vecs, kTopThreads));
+    if (dw && kTopExponent<T> != 0 &&
+        launch_pdl(row_tops_kernel, dim3(top_blocks), dim3(kTopThreads), 0, c.stream, tops) != cudaSuccess)
+        return SEL_ECUDA;
     for (uint32_t i = 0; i < plan.pieces; ++i) {
         const uint32_t v0 = i * plan.piece, width = std::min(plan.piece, c.V - v0);
         const uint64_t pitch = static_cast<uint64_t>(plan.pitch) * 2;
         ProbProblem<T> p{};
         if (!map16(&p.x, c.x, c.H, c.rows, kStepK, rows.n / 2) || !map16(&p.w, c.w, c.H, c.V, kStepK, kCtaM)) return SEL_ECUDA;
         if (dw && i == 0)
-            p.prep = {static_cast<const uint4*>(c.x), static_cast<uint4*>(scaled), c.targets, grad, exponent, hits, c.rows,
-                      c.V, Div(vecs), shift};
+            p.prep = {static_cast<const uint4*>(c.x), static_cast<uint4*>(scaled), c.targets, grad, tops.tops, top_blocks,
+                      exponent, hits, c.rows, c.V, Div(vecs), shift};
         p.p = static_cast<T*>(prob);
         p.lost = lost;
         p.targets = c.targets;
