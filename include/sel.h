@@ -801,8 +801,9 @@ sel_status sel_head_loss(const void *d_hidden, uint32_t rows,
  *   hidden_grad[r] = grad[r] * sum over v of P[r][v] * weight[v]
  *   weight_grad[v] = sum over r of grad[r] * P[r][v] * hidden[r].
  * Ignored rows and rows whose grad is 0 count for nothing, whatever they hold:
- * their hidden_grad is zeros. A row with a nonfinite logit, lse or grad makes its
- * own hidden_grad and all of weight_grad nonfinite. P times the mantissa of
+ * their hidden_grad is zeros. A row with a NaN or +Inf logit (its lse is NaN), a
+ * nonfinite lse or a nonfinite grad makes its own hidden_grad and all of weight_grad
+ * nonfinite; a logit of -Inf is a probability of 0. P times the mantissa of
  * the row's grad is rounded to `dtype` for the products (what that takes from the
  * targets' entries is added back); sums are in fp32 and each gradient is
  * rounded once. With SEL_F16, entries of grad[r] * hidden[r] keep all of their bits in

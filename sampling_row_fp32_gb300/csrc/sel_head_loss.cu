@@ -336,7 +336,7 @@ __device__ __forceinline__ void finish_row(const LossFinishArgs& a, uint32_t row
     const float sum = j.s.hi + j.s.lo;
     const bool some = sum > 0.0f && sum < INFINITY;
     int e = 0;
-    const float f = some ? frexpf(sum, &e) : sum;  // in [1/2, 1); the sum is at least 2^-1 or nothing
+    const float f = some ? frexpf(sum, &e) : sum;  // in [1/2, 1); the sum is at least 2^-61 or nothing
     const float n = j.m + static_cast<float>(e);
     const float p = __fmul_rn(n, kHi);
     FF others{p, __fmaf_rn(n, kLo, __fmaf_rn(n, kHi, -p))};
@@ -633,7 +633,8 @@ struct ProbProblem {
             const uint32_t i = 32 * c + w.lane, target = wanted[c];
             const float m = target < V ? GradParts(gs[c]).m : 0.0f;
             const bool live = m != 0.0f;
-            refs[i] = live ? ls[c] - logf(fabsf(m)) : 0.0f;
+            // (an lse of +Inf would make every probability 0, and the row's gradient a finite one)
+            refs[i] = !live ? 0.0f : fabsf(ls[c]) < INFINITY ? ls[c] - logf(fabsf(m)) : NAN;
             ids[i] = target;
             const uint32_t dead = __ballot_sync(kFull, !live), negative = __ballot_sync(kFull, m < 0.0f);
             const uint32_t hits = __ballot_sync(kFull, live && target - (id - w.lane) < 32u);
@@ -658,7 +659,7 @@ struct ProbProblem {
                         const float m = GradParts(grad[row]).m;
                         const float e = expm1f(v[i] - lse[row]) * fabsf(m) * static_cast<float>(1 << static_cast<int>(kProbShift<T>));
                         const float less = e - to_f32(from_f32<T>(e));
-                        kept[i] = e;
+                        kept[i] = isnan(refs[32 * c + i]) ? NAN : e;
                         lost[row] = m < 0.0f ? -less : less;
                     }
                 }

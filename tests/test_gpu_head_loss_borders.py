@@ -75,3 +75,31 @@ def test_small_hidden_states_of_f16_keep_their_bits():
     _, dw = run_grad(x, w, t, lse, grad)
     _, want = L.head_loss_grad(x, w, t, lse, grad)
     assert (dw.double() - want).norm() <= 2.0 ** -11 * want.norm()  # (P's rounding and the result's, each 2^-12 at most in the mean square)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("rows", [4, 260])
+@pytest.mark.parametrize("lse_of", [float("inf"), -float("inf"), NAN])
+def test_a_nonfinite_lse_fails_its_row(lse_of, rows, dtype):
+    x, w, t, grad = make(7, rows, 500, 64, dtype, ignored=0.0)
+    _, lse = run_loss(x, w, t)
+    grad[2] *= -1
+    bad = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    bad[1:3] = True
+    lse[bad] = lse_of
+    dx, dw = run_grad(x, w, t, lse, grad)
+    assert not torch.isfinite(dx[bad]).any() and torch.isfinite(dx[~bad]).all() and not torch.isfinite(dw).any()
+    t[1], grad[2] = -1, 0.0  # rows that do not count may have any
+    dx, dw = run_grad(x, w, t, lse, grad)
+    assert torch.isfinite(dx).all() and torch.isfinite(dw).all() and not dx[bad].any()
+
+
+def test_a_logit_of_minus_infinity_is_a_probability_of_zero():
+    x, w, t, grad = make(8, 30, 400, 64, "bf16", ignored=0.0)
+    x[:, 0] = 2.0 ** 120
+    w[:, 0] = 0.0
+    w[9, 0] = -2.0 ** 120  # (finite operands, a product past fp32)
+    t[t == 9] = 10
+    _, lse = run_loss(x, w, t)
+    dx, dw = run_grad(x, w, t, lse, grad)
+    assert torch.isfinite(dx).all() and torch.isfinite(dw).all() and not dw[9].any()
