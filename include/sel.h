@@ -814,7 +814,8 @@ sel_status sel_head_loss(const void *d_hidden, uint32_t rows,
  *   d_lse          [rows] f32, from sel_head_loss
  *   d_grad         [rows] f32
  *   d_hidden_grad  [rows][H] of `dtype`, 16-byte aligned, or NULL
- *   d_weight_grad  [V][H] of `dtype`, 16-byte aligned, or NULL (not both)
+ *   d_weight_grad  [V][H] of `dtype`, 16-byte aligned, or NULL (not both, but
+ *                  where rows == 0)
  *   d_ws           workspace of sel_workspace_bytes(SEL_OP_HEAD_LOSS_GRAD,
  *                  rows, V, H)
  * With rows == 0 weight_grad becomes zeros.

@@ -1157,8 +1157,8 @@ extern "C" sel_status sel_head_loss_grad(const void* d_hidden, uint32_t rows, co
                                          cudaStream_t stream) {
     if (const sel_status s = check_head(d_hidden, d_weight, d_targets, dtype, rows, V, H); s != SEL_OK) return s;
     if (misaligned(d_hidden_grad, 16) || misaligned(d_weight_grad, 16)) return SEL_EINVAL;
-    if (!d_hidden_grad && !d_weight_grad) return SEL_EINVAL;
-    if (rows == 0) {
+    if (rows > 0 && !d_hidden_grad && !d_weight_grad) return SEL_EINVAL;
+    if (rows == 0) {  // (an empty hidden_grad may have no address)
         if (!d_weight_grad) return SEL_OK;
         return cudaMemsetAsync(d_weight_grad, 0, static_cast<size_t>(V) * H * 2, stream) == cudaSuccess ? SEL_OK : SEL_ECUDA;
     }

@@ -51,3 +51,12 @@ def test_temperatures_that_are_no_normal_numbers_are_refused(lib):
                                     None) == B.SEL_EINVAL
     # (the smallest that is: no rows, so that nothing is launched)
     assert lib.sel_distill(vp(F), B.SEL_F32, 0, 10, 10, vp(F), vp(F), 4, None, 2.0 ** -126, vp(F), None) == B.SEL_OK
+
+
+@needs_nvcc
+def test_hidden_grad_alone_of_no_rows(lib):
+    """An empty tensor has no address, so the call gets NULL for both gradients."""
+    F, vp = 0x10000, ctypes.c_void_p
+    assert lib.sel_head_loss_grad(None, 0, vp(F), B.SEL_BF16, 10, 16, None, None, None, None, None, None, 0, None) == B.SEL_OK
+    assert lib.sel_head_loss_grad(vp(F), 1, vp(F), B.SEL_BF16, 10, 16, vp(F), vp(F), vp(F), None, None, vp(F), 1 << 40,
+                                  None) == B.SEL_EINVAL
