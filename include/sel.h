@@ -21,10 +21,15 @@
  *  - Workspace. d_ws holds per-row partial results, and the slots that the
  *    finishing launches combine and clear again. Size it with
  *    sel_workspace_bytes() for the largest call it will serve, zero it once
- *    with sel_workspace_init() after allocating it, then reuse it: every call
- *    leaves its counters at zero again. Calls that may run concurrently (on
- *    different streams) need separate workspaces. d_ws must be 256-byte
- *    aligned.
+ *    with sel_workspace_init() after allocating it, then reuse it for calls of
+ *    the same operation code, of any size up to that: every call leaves the
+ *    counters that the next one counts on at zero again. What else it holds then
+ *    is not zero (partial results; sums, an exponent and probabilities of the
+ *    head's loss), and other operations count on other parts of it: initialise
+ *    it again before a call of another code, or give each its own. (The two of
+ *    the head's loss count on their error word alone and may share one.) Calls
+ *    that may run concurrently (on different streams) need separate workspaces.
+ *    d_ws must be 256-byte aligned.
  *  - Errors. The return value reports what the host can see: bad arguments
  *    (SEL_EINVAL), a workspace too small (SEL_EWORKSPACE), an unsupported
  *    size (SEL_EUNSUPPORTED) or a launch failure (SEL_ECUDA). rows == 0 (or
@@ -106,7 +111,8 @@ size_t sel_workspace_bytes(int op, uint32_t rows, uint32_t V, uint32_t k);
 
 /*
  * Zero a freshly allocated workspace: one cudaMemsetAsync on `stream`.
- * Needed once per allocation; the entry points keep it zeroed afterwards.
+ * Needed once per allocation, and again before another operation uses it; the
+ * calls of one operation keep what they count on zeroed.
  */
 sel_status sel_workspace_init(void *d_ws, size_t ws_bytes, cudaStream_t stream);
 

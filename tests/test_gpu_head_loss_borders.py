@@ -103,3 +103,16 @@ def test_a_logit_of_minus_infinity_is_a_probability_of_zero():
     _, lse = run_loss(x, w, t)
     dx, dw = run_grad(x, w, t, lse, grad)
     assert torch.isfinite(dx).all() and torch.isfinite(dw).all() and not dw[9].any()
+
+
+@pytest.mark.parametrize("rows", [5, 260])
+def test_one_output_alone_is_the_same_in_f16(rows):
+    """weight_grad alone has the launch for its hidden rows' exponent, hidden_grad alone has not."""
+    x, w, t, grad = make(6, rows, 700, 200, "f16")
+    _, lse = run_loss(x, w, t)
+    dx, dw = run_grad(x, w, t, lse, grad)
+    ws = B.workspace(B.SEL_OP_HEAD_LOSS_GRAD, rows, 700, 200)
+    a, b = torch.full_like(x, 9.0), torch.full_like(w, 9.0)
+    B.sel_head_loss_grad(x, w, t, lse, grad, a, None, ws)
+    B.sel_head_loss_grad(x, w, t, lse, grad, None, b, ws)
+    assert torch.equal(a, dx) and torch.equal(b, dw)
