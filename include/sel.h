@@ -74,7 +74,8 @@ typedef enum sel_status {
 /* Operation codes for sel_workspace_bytes. */
 enum { SEL_OP_ARGMAX = 0, SEL_OP_TOPK = 1, SEL_OP_SAMPLE = 2, SEL_OP_SPEC = 3,
        SEL_OP_SPEC_SAMPLER = 4, SEL_OP_SPEC_DIAG = 5, SEL_OP_SHARD_DRAW = 6,
-       SEL_OP_SPEC_SHARD_DRAW = 7, SEL_OP_HEAD_LOSS = 9, SEL_OP_HEAD_LOSS_GRAD = 10 };
+       SEL_OP_SPEC_SHARD_DRAW = 7, /* 8: none */
+       SEL_OP_HEAD_LOSS = 9, SEL_OP_HEAD_LOSS_GRAD = 10 };
 
 /* Order of temperature and filters in sel_sample. */
 enum {
@@ -780,7 +781,9 @@ sel_status sel_embed_w4(const uint32_t *d_ids, uint32_t n, const uint8_t *d_q,
  * lse[r] = ln sum over v of exp z[r][v], loss[r] = lse[r] - z[r][targets[r]]
  * (the negative log-probability of the target). A target >= V
  * (SEL_INVALID_ID: a prompt's or padding's position) makes the row ignored:
- * its loss is 0. Products are exact, their sums and the statistics are in fp32 or
+ * its loss is 0. (So the weight is a whole head: with a slice of its ids, a row whose
+ * target lies in another slice would be taken for an ignored one, and its gradient
+ * would miss that slice's probabilities.) Products are exact, their sums and the statistics are in fp32 or
  * more, and a loss near 0 keeps its relative precision. A row with a NaN or
  * +Inf logit gets NaN; -Inf is a probability of 0.
  *
