@@ -137,6 +137,11 @@ __device__ __forceinline__ float ex2_approx(float x) {
     return y;
 }
 
+// 2^n for a whole n <= 127; 0 below the normal numbers (and for -Inf and NaN).
+__device__ __forceinline__ float pow2(float n) {
+    return n >= -126.0f ? __uint_as_float(static_cast<uint32_t>(static_cast<int>(n) + 127) << 23) : 0.0f;
+}
+
 // Unevaluated sum hi + lo of two floats (about 44 significant bits),
 // accumulated with Knuth's TwoSum and renormalised with Dekker's Fast2Sum;
 // sums of many small fp32 terms keep ~1e-13 relative error without FP64.

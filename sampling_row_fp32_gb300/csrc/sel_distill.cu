@@ -80,11 +80,6 @@ struct Sums {
     float rest_m, rest, list_m, list;
 };
 
-// 2^n for a whole n <= 0; 0 below the normal numbers (and for NaN).
-__device__ __forceinline__ float pow2(float n) {
-    return n >= -126.0f ? __uint_as_float(static_cast<uint32_t>(static_cast<int>(n) + 127) << 23) : 0.0f;
-}
-
 // References from here to kHuge: beyond, the rounding of x kf is no longer small
 // next to 1, and a row goes by x - its largest logit instead (slow_sums). Smaller
 // ones count as -kHuge: what lies that far below a row's largest weighs nothing.

@@ -65,11 +65,6 @@ struct RasterCursor {
     }
 };
 
-// 2^n for a whole n <= 127, 0 below the normal numbers (and for -Inf).
-__device__ __forceinline__ float pow2(float n) {
-    return n >= -126.0f ? __uint_as_float(static_cast<uint32_t>(static_cast<int>(n) + 127) << 23) : 0.0f;
-}
-
 // v 2^e for any e that floats and P's shift give.
 struct Shift {
     float a, b;
