@@ -946,10 +946,12 @@ inline GradPlan grad_plan(uint32_t rows, uint32_t V, uint32_t H) {
     g.piece = ceil_div(ceil_div(V, ceil_div(V, cap)), kTileM) * kTileM;
     g.pieces = ceil_div(V, g.piece);
     // dX's columns a tile: equal tiles pad less, but their halves begin anywhere in a
-    // line of P and are copied 64 rows at a time: 777 rows (4 x 208 or 4 x 256) 578 us
-    // against 541 for a piece's gradients
+    // sector of P and are copied 64 rows at a time, so they have to pad a good deal less
+    // (equal / whole tiles, 2,048 x 60,000, the whole call: 777 rows, 1.23 times as many
+    // columns, 408-421 / 384-404 us; 400, 1.23 times, 247 / 245; 550, 1.33 times, 308 / 314;
+    // 290, 1.6 times, 223 / 227)
     const Columns c(rows);
-    g.dx_n = rows <= kTileN || c.padded() * 1.38 < static_cast<double>(ceil_div(rows, kTileN)) * kTileN ? c.n : kTileN;
+    g.dx_n = rows <= kTileN || c.padded() * 1.28 < static_cast<double>(ceil_div(rows, kTileN)) * kTileN ? c.n : kTileN;
     // few tiles of dX: the sum over the piece is split
     const uint64_t tiles = static_cast<uint64_t>(ceil_div(H, kTileM)) * ceil_div(rows, g.dx_n);
     g.slices = std::min(std::max(1u, g.piece / 1024), tiles >= 76 ? 1u : ceil_div(76, tiles));
@@ -1023,7 +1025,10 @@ sel_status run_loss(const HeadLossCall& c, float* loss, float* lse) {
     }
     if (st != SEL_OK) return st;
     const LossFinishArgs f{parts, at, c.targets, error, loss, lse, c.rows, c.V, slots};
-    const cudaError_t e = c.rows >= 64
+    // A block a row until those outnumber what runs at a time (the whole call, a row a
+    // block / 32 rows a block, 1,024 x 151,936: 64 rows 54 / 62 us, 256 61 / 74, 512 102 /
+    // 108, 777 180 / 177, 1,024 198 / 190, 4,096 733 / 682)
+    const cudaError_t e = c.rows >= 640
                               ? launch_pdl(loss_finish_kernel<true>, dim3(ceil_div(c.rows, 32)), dim3(kFinishThreads), 0, c.stream, f)
                               : launch_pdl(loss_finish_kernel<false>, dim3(c.rows), dim3(kFinishThreads), 0, c.stream, f);
     return e == cudaSuccess ? SEL_OK : SEL_ECUDA;
@@ -1103,7 +1108,10 @@ sel_status run_grad(const HeadLossCall& c, const float* lse, const float* grad, 
         if (const sel_status s = launch_gemm(g, workers, c.stream); s != SEL_OK) return s;
     }
     const GradFinishArgs f{acc, lost, static_cast<const uint4*>(c.w), c.targets, grad, error, static_cast<uint4*>(dx), static_cast<uint4*>(dw), c.rows, c.V, plan.slices, Div(vecs), shift};
-    const bool split = plan.slices >= 4;
+    // (one thread for all slices / a warp for every fourth, the whole call: 1,024 rows of
+    // 2,560 x 30,000, 2 slices, 282 / 290 us; of 1,280, 4 slices, 171 / 175; of 768, 7
+    // slices, 125 / 124; 64 rows of 1,024 x 151,936, 19 slices, 207 / 205)
+    const bool split = plan.slices >= 6;
     const uint64_t vectors = static_cast<uint64_t>(c.rows) * vecs;
     const dim3 blocks(static_cast<uint32_t>(std::min<uint64_t>(8 * sms, ceil_div(vectors, split ? 32 : kGradThreads))));
     const cudaError_t e = split ? launch_pdl(grad_finish_kernel<T, true>, blocks, dim3(kGradThreads), 0, c.stream, f)
