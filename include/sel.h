@@ -854,9 +854,11 @@ sel_status sel_head_loss_grad(const void *d_hidden, uint32_t rows,
  * 2^-126 (a value of -Inf: a top-k list's others have no more), or s is below 2^-126.
  * Entries whose id is >= V (SEL_INVALID_ID) are left out; a row without an
  * entry whose value is above -Inf is ignored, with a loss of 0. A logit of -Inf
- * is a probability of 0. A row with a NaN or +Inf logit, value or lse, with
- * every id at -Inf, or with an id listed twice gets NaN. So do, with their whole
- * gradients, all rows that ran together with one where a wait on the GPU ran out.
+ * is a probability of 0. A row with a NaN or +Inf logit or value, with an lse that is
+ * NaN or 2^40 or more in magnitude, with every id at -Inf, or with an id listed twice
+ * gets NaN. So do, with their whole gradients, all rows that ran together with one
+ * where a wait on the GPU ran out. Logits, and values, whose differences fp32 does not
+ * hold may count as infinitely far apart.
  *
  *   d_logits       rows of V of `dtype` (any sel_dtype), row r at r * ld, aligned
  *                  to their elements. V at most SEL_DISTILL_MAX_V

@@ -275,6 +275,9 @@ struct Teacher {
     uint32_t noise, live;
 };
 
+// A given lse from here on is a NaN: its own rounding is far more than 1, and the pair
+// lh, ll holds log2(e) times it no better.
+constexpr float kMaxLse = 1.09951163e12f;  // 2^40
 // What is taken for nothing, of p as of s; and what an fp32 lse may be off, itself and
 // in the sums that gave it, in units of max(1, |lse|): a list that names every id with
 // a probability leaves an r of that size, half of the time above 0.
@@ -378,7 +381,7 @@ struct LogP {
             const float l = a.teacher_lse[row];
             lh = l * kLog2E;
             ll = fmaf(l, kLog2E, -lh) + l * 1.9259629911e-8f;  // (log2(e) less its float)
-            if (!(fabsf(l) < INFINITY)) lh = NAN;
+            if (!(fabsf(l) < kMaxLse)) lh = NAN;
         }
     }
 };
@@ -768,8 +771,10 @@ struct Worker {
                 if (id[e] == SEL_INVALID_ID) continue;
                 const float lp = log_p(val[e]), p = exp2f(lp);
                 const float lq = log_q(logit[e]);
-                if (lq == -INFINITY && logit[e] > -INFINITY) far += (p * a.inv_t) * ((slow ? top : 0.0f) - logit[e]);
-                else if (p != 0.0f) part += p * (lp - lq);
+                if (p != 0.0f) {  // (halves: their difference stays in fp32)
+                    if (lq == -INFINITY && logit[e] > -INFINITY) far += (2.0f * (p * a.inv_t)) * ((slow ? 0.5f * top : 0.0f) - 0.5f * logit[e]);
+                    else part += p * (lp - lq);
+                }
                 grads[e] = g * (t.mass * (ex2_approx(exponent(logit[e], top)) / total) - p);
                 if (kGrad && grad == 0.0f) id[e] = SEL_INVALID_ID;
             }

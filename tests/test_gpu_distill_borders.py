@@ -292,3 +292,24 @@ def test_a_wait_that_runs_out_fails_its_rows(dropping, rows, V, dtype, apart):
         ok = ~bad
         if n == rows:
             assert torch.equal(loss[ok], want[ok]) and torch.equal(d[ok, :V], want_x[ok])
+
+
+@pytest.mark.parametrize("lse_of", [2.0 ** 40, -2.0 ** 41, 3e38])
+def test_an_lse_past_its_rounding_fails_its_row(lse_of):
+    x, vals, ids, lse, grad = make(16, 5, 300, 5, "f32", rest=True)
+    lse[1] = lse_of
+    loss, out = run(x, vals, ids, lse, 1.0, grad)
+    bad = torch.arange(5, device="cuda") == 1
+    assert torch.equal(torch.isnan(loss), bad) and torch.isnan(out[1]).all() and torch.isfinite(out[~bad]).all()
+
+
+def test_an_id_without_probability_far_below_the_students_largest():
+    """p of 0 next to a distance past fp32 is nothing."""
+    x, vals, ids, _, grad = make(15, 4, 300, 5, "f32")
+    x[:, int(ids[0, 0])] = 3e38
+    for r in range(4):
+        x[r, int(ids[r, 4])] = torch.finfo(torch.float32).min
+        vals[r, 4] = vals[r].max() - 500
+    want, _ = L.distill(x, vals, ids, None, 1.0, grad)
+    loss, out = run(x, vals, ids, None, 1.0, grad)
+    assert torch.isfinite(out).all() and ((loss.double() - want).abs() <= 2.0 ** -18 * want).all()
