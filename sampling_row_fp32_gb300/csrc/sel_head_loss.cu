@@ -529,7 +529,8 @@ struct Prep {
             uint4 q = make_uint4(0, 0, 0, 0);
             if (targets[r] < V && g != 0.0f) {
                 q = x[i];
-                const float f = pow2(static_cast<float>(GradParts(g).e - top));
+                // (an f16 entry may be 2^-24, so 2^38 at most; more where no row has an entry but 0)
+                const float f = pow2(static_cast<float>(min(GradParts(g).e - top, 38)));
                 uint32_t* p = &q.x;
 #pragma unroll
                 for (uint32_t k = 0; k < 4; ++k) {

@@ -116,3 +116,19 @@ def test_one_output_alone_is_the_same_in_f16(rows):
     B.sel_head_loss_grad(x, w, t, lse, grad, a, None, ws)
     B.sel_head_loss_grad(x, w, t, lse, grad, None, b, ws)
     assert torch.equal(a, dx) and torch.equal(b, dw)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("size", [2.0 ** -88, 1.0, 2.0 ** 120])
+def test_hidden_states_of_zeros(size, dtype):
+    """Nothing to take an exponent of: weight_grad is zeros, hidden_grad the usual."""
+    x, w, t, grad = make(9, 20, 300, 64, dtype)
+    x.zero_()
+    grad = torch.full_like(grad, size)
+    _, lse = run_loss(x, w, t)
+    dx, dw = run_grad(x, w, t, lse, grad)
+    assert not dw.any()
+    want, _ = L.head_loss_grad(x, w, t, lse, grad)
+    fits = want.abs() < torch.finfo(DT[dtype]).max / 2
+    # (P's entries and the results to 2^-8, over all of which the errors lie on both sides)
+    assert (dx.double() - want)[fits].norm() <= 2.0 ** -8 * want[fits].norm() + torch.finfo(DT[dtype]).smallest_normal
