@@ -25,15 +25,15 @@
 // 87 nats below the listed ones, though ln s and their shares of s are ordinary
 // numbers. Sums meet as messages between the warps of the cluster (st.async), joined
 // in one order; no barrier of the cluster stands between a row and the next. Every
-// wait is bounded. One that runs out ends its CTA's roles before the next row (the
-// others' waits then run out too), and whatever was written till then, the cluster's
-// CTAs make all of its rows NaN at the end.
+// wait is bounded. One that runs out ends its CTA's roles before the next row but
+// one (the others' waits then run out too), and whatever was written till then, the
+// cluster's CTAs make all of its rows NaN at the end.
 //
 // What bounds it: large batches the row's bytes, and the second copy through L2 (4,096
-// x 151,936 bf16, lists of 64: 430 us, 5.8 TB/s, 51 percent of the issue slots); a few
+// x 151,936 bf16, lists of 64: 435 us, 5.7 TB/s, 51 percent of the issue slots); a few
 // hundred rows the last round of clusters (512 x 202,048 bf16, loss alone: 42; 777 x
-// 93,001 f16, lists of 200: 71); few rows the chain from the list to the last store (49 x
-// 248,320 f32: 23; 7 x 151,936, loss alone: 7 on the GPU, 12 with the host's call).
+// 93,001 f16, lists of 200: 72); few rows the chain from the list to the last store (49 x
+// 248,320 f32: 23; 7 x 151,936, loss alone: 6.4 on the GPU, 12 with the host's call).
 #include <algorithm>
 #include <type_traits>
 
@@ -945,9 +945,9 @@ struct Layout {
 // takes 4 us a row and 1 us for 28 KB; shares that do not fit the ring cross it
 // twice, the second time out of L2 (as 0.2 of a read from memory), unless the rows
 // on the device at a time are too many for it; over several rounds clusters of odd sizes
-// take about 1.3 times as long. Measured, 1 / 2 / 3 / 4 / 6 CTAs a row: 4,096 rows of
-// 151,936 bf16 (with 4 a share fits) 544 / 430 / 583 / 492 / 622 us; 777 of 93,001 f16
-// 71 / 77 / 98 / 95 / 115; 49 of 248,320 f32 52 / 35 / 29 / 26 / 30, and 23.4 with 5.
+// take about 1.3 times as long. Measured, 1 / 2 / 3 / 4 / 5 / 6 CTAs a row: 4,096 rows of
+// 151,936 bf16 (with 4 a share fits) 541 / 434 / 608 / 502 / 730 / 631 us; 777 of 93,001
+// f16 72 / 80 / 104 / 99 / 150 / 120; 49 of 248,320 f32 52 / 34 / 29 / 25 / 23 / 30.
 template <typename T, bool kGrad>
 bool layout_for(uint32_t rows, uint32_t V, Layout& best) {
     struct Table {

@@ -15,13 +15,15 @@
 // one computes the piece's rows of dW (K = rows) and adds the piece's share of
 // dX (K = the piece) to fp32 sums.
 //
-// What bounds them: the matrix's bytes for few rows (49 of 4,096 x 248,320: 297-308 us,
-// 6.7 TB/s; one of 1,024 x 151,936: 51), the tensor cores for many (4,096 rows: 98.6, 96.5
-// and 96.5 percent of their cycles in the three products; 4,096 x 151,936 in 2.43 ms
-// alone and 2.79 back to back, where the card's power limits it; the gradient of 2,048 x
-// 151,936 in 3.9 and 4.5). Between them padding counts: 777 rows of 2,880 x 93,001 take
-// 264 us (1.58 PFLOP/s) and 820. The gradient of 64 rows of 1,024 x 151,936 takes 204, 54
-// for P and 130 for the rest: the matrix is read twice.
+// What bounds them: the matrix's bytes for few rows (49 of 4,096 x 248,320: 307 us,
+// 6.6 TB/s; one of 1,024 x 151,936: 51.5), the tensor cores for many (4,096 rows: 98.5,
+// 96.4 and 96.6 percent of their cycles in the three products; 4,096 x 151,936 in 2.70 ms
+// in a short run and 2.79 in a long one, where the card's power limits it; the gradient of
+// 2,048 x 151,936 in 4.34 and 4.49). Between them padding counts: 777 rows of 2,880 x
+// 93,001 take 269 us and 313 (1.55 and 1.33 PFLOP/s), their gradient 899 and 951. The
+// gradient of 64 rows of 1,024 x 151,936 takes 205, 55 for P and 130 for the rest: the
+// matrix is read twice. Small calls are their chain of launches (256 rows of 128 x 8,000:
+// 10 us on the GPU for two, the gradient 24 for three; the host needs 10 and 13).
 #include <algorithm>
 
 #include <cuda_runtime.h>
@@ -101,7 +103,8 @@ struct Weights {
 // The tensor cores round their sums towards zero, 16 products at a time: a logit of
 // 4,096 products comes out 1.6e-6 too small, which a loss shows. So a logit is summed in
 // parts of 1,024, joined in the epilogue's registers. (P and the gradients are rounded
-// to 16 bits: they need no such care.)
+// to 16 bits and take it as it comes: dX's sums over a piece's ids leave f16 gradients
+// 2.2e-4 from the definition, where a product summed in fp32 leaves 2.1e-4.)
 constexpr uint32_t kLossPart = 1024 / kStepK;
 
 // Hidden rows on the product's rows: a lane has one of them, and half a tile's
@@ -442,7 +445,7 @@ __device__ __forceinline__ void unpack2(uint32_t w, float& lo, float& hi) {
 // row's gradient, which then lies at 2^14 or above, so that a row keeps its bits down to
 // 2^-28 of it. (Over the largest gradient's, rows 2^14 below it were 2.6e-4 off, 2^20
 // below 2 percent, 2^25 below nothing.) That largest product takes a launch of its own
-// ahead of P's, a few of whose microseconds P's copies of the hidden rows get back.
+// ahead of P's (777 rows of 2,880 x 93,001: 952 -> 957 us).
 template <typename T>
 constexpr int kTopExponent = 0;  // of the largest scaled entry
 template <>
