@@ -818,8 +818,9 @@ sel_status sel_head_loss(const void *d_hidden, uint32_t rows,
  * rounded once. With SEL_F16, entries of grad[r] * hidden[r] keep all of their bits in
  * weight_grad down to 2^-28 of the largest, fewer down to 2^-40, none below. The
  * rounding of the logits and of lse puts up to some 2^-23 of their size on P, so the
- * gradient of a row whose loss is smaller than that is of that size too. z is computed again, in pieces of the vocabulary, so the
- * workspace holds at most 2^28 entries of P, or 16,384 columns of it.
+ * gradient of a row whose loss is smaller than that is of that size too. z is
+ * computed again, in pieces of the vocabulary, so the workspace holds at most 2^28
+ * entries of P, or 16,384 columns of it.
  *
  *   d_hidden, rows, d_weight, dtype, V, H, d_targets  as for sel_head_loss
  *   d_lse          [rows] f32, from sel_head_loss
