@@ -781,10 +781,11 @@ sel_status sel_embed_w4(const uint32_t *d_ids, uint32_t n, const uint8_t *d_q,
  * lse[r] = ln sum over v of exp z[r][v], loss[r] = lse[r] - z[r][targets[r]]
  * (the negative log-probability of the target). A target >= V
  * (SEL_INVALID_ID: a prompt's or padding's position) makes the row ignored:
- * its loss is 0. (So the weight is a whole head: with a slice of its ids, a row whose
- * target lies in another slice would be taken for an ignored one, and its gradient
- * would miss that slice's probabilities.) Products are exact, their sums and the statistics are in fp32 or
- * more, and a loss near 0 keeps its relative precision. A row with a NaN or
+ * its loss is 0. (So the weight is a whole head: with a slice of its ids, a row
+ * whose target lies in another slice would be taken for an ignored one, and its
+ * gradient would miss that slice's probabilities.) Products are exact, their sums
+ * and the statistics are in fp32 or more, and a loss near 0 keeps its relative
+ * precision. A row with a NaN or
  * +Inf logit gets NaN; -Inf is a probability of 0.
  *
  *   d_hidden     [rows][H] of `dtype`, 16-byte aligned
